@@ -296,6 +296,72 @@ mk_status_t mk_moe_dispatch_gemm_noalloc(const void* x, const float* logits, int
 /* Bytes of workspace a call with these sizes needs (0 on invalid sizes). */
 size_t mk_workspace_size(int T, int H, int F, int E, int k, const mk_config_t* cfg);
 
+/* ------------------------------------------------------------------------
+ * Operators of a decode step around the expert layer.  All of them: device
+ * pointers, caller-owned; work is enqueued on `stream` and the call returns
+ * without synchronising; arguments are checked first and nothing is launched
+ * on a failure (MK_ERR_INVALID_ARG, MK_ERR_UNSUPPORTED); a device of compute
+ * capability 10.3.  Sums, norms and softmax statistics are held in fp32 and
+ * each output is rounded once.  Equal inputs give equal bits. */
+
+/* The residual's addition and the root-mean-square norm, in bf16 and / or in
+ * 8 bits.  With z = x + residual (x alone when residual is NULL):
+ *   residual_out[t,:] = bf16(z),
+ *   y = z * rsqrt(mean(z^2) + eps) * weight,
+ *   out[t,:] = bf16(y),
+ *   for each group of 128 columns (the last may be shorter): a = max |y|,
+ *   scale[t,g] = a / 448 (1 when a < 2^-100), out8[t,:] = e4m3(y / scale).
+ * y comes from the unrounded z.  A NaN in a row makes the row's y and scales
+ * NaN.
+ *   x[T,H] bf16 with x_stride elements between rows, residual[T,H] bf16 with
+ *   residual_stride (may be NULL), weight[H] bf16                 -- read only
+ *   out[T,H] bf16, out8[T,H] e4m3 with scale[T, ceil(H/128)] f32 (either of
+ *   the two outputs may be NULL; out8 and scale come together),
+ *   residual_out[T,H] bf16 (may be NULL; needs residual)          -- written
+ * residual_out may be residual itself when residual_stride is H; other
+ * overlaps of inputs and outputs are not allowed.  1 <= H <= 32768 (odd
+ * widths too), T >= 0, eps >= 0 and finite, strides of at least H when
+ * T > 1.  Rows that are 16-byte aligned (H, strides and pointers) are read
+ * 16 bytes at a time. */
+mk_status_t mk_add_rmsnorm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                           const void* weight, int T, int H, float eps, void* out, void* out8, float* scale,
+                           void* residual_out, void* stream);
+
+/* Attention of one new token per sequence over a paged key-value cache.  For
+ * sequence b with n = seq_lens[b] cached keys (the new token's own among
+ * them), query head h and its key-value head c = h / (Hq/Hkv):
+ *   s_j = scale * q[b,h,:] . k(j,c,:)  for j < n,   m = max_j s_j,
+ *   out[b,h,:] = sum_j e^(s_j - m) v(j,c,:) / sum_j e^(s_j - m),
+ *   lse[b,h] = log sum_j e^(s_j);
+ * without keys (n = 0, or every score -inf) out is 0 and lse -inf.  Key j of
+ * sequence b lies in page block_table[b, j / page_size] at token
+ * j % page_size: element page*page_stride + token*token_stride +
+ * c*head_stride of k_cache and of v_cache, D elements in a row.  Nothing past
+ * the n-th key is read, whatever the pages hold there.
+ *   q[B,Hq,D] bf16 with q_stride elements between sequences (heads
+ *   contiguous), caches bf16, block_table[B,max_pages] i32 (entries past a
+ *   sequence's pages are not read), seq_lens[B] i32 (device)      -- read only
+ *   out[B,Hq,D] bf16, lse[B,Hq] f32 (may be NULL)                 -- written
+ * Limits: D = 64, 128 or 256; Hq a multiple of Hkv; any page_size >= 1;
+ * B <= 4096; max_pages*page_size <= 2^31 - 16, and fewer than 2^31 tiles of
+ * 16 keys and 16 query heads in all; strides non-negative multiples of 8
+ * elements, caches 16-byte aligned, out 8, q 4 (q_stride even).  Keys and
+ * values that are read are finite.  The lengths and pages are checked on the
+ * device: a length outside [0, max_pages*page_size] is clamped, a page
+ * outside [0, num_pages) is not read (its keys count as zeros), and either is
+ * reported by mk_get_status() as MK_ERR_DEVICE_FAULT.
+ * workspace: NULL (library cache) or mk_paged_attention_workspace_size()
+ * bytes, 256-byte aligned, zero-filled before its first use and used by this
+ * entry point only; one stream at a time. */
+mk_status_t mk_paged_attention(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                               int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                               const int32_t* block_table, const int32_t* seq_lens, int B, int Hq, int Hkv, int D,
+                               int page_size, int max_pages, int num_pages, float scale, void* out, float* lse,
+                               void* stream, void* workspace, size_t ws_bytes);
+
+/* Workspace bytes mk_paged_attention needs (0 for invalid sizes). */
+size_t mk_paged_attention_workspace_size(int B, int Hq, int Hkv);
+
 /* Synchronise `stream`, then return and clear the device error word
  * (MK_ERR_TIMEOUT / MK_ERR_DEVICE_FAULT), or MK_ERR_CUDA if the stream holds
  * a CUDA error.  MK_OK when nothing was recorded. */

@@ -52,6 +52,9 @@ ABI_FUNCTIONS = (
     "mk_moe_ep_sim",
     "mk_moe_ep_sim_gated",
     "mk_ep_workspace_size",
+    "mk_add_rmsnorm",
+    "mk_paged_attention",
+    "mk_paged_attention_workspace_size",
     "mk_workspace_size",
     "mk_get_status",
     "mk_last_error_detail",
@@ -107,6 +110,7 @@ class mk_launch_info_t(ctypes.Structure):
 _lib_handle = None
 _p = ctypes.c_void_p
 _i = ctypes.c_int
+_i64 = ctypes.c_int64
 
 
 def lib(path: str | None = None) -> ctypes.CDLL:
@@ -145,6 +149,13 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     h.mk_ep_workspace_size.restype = ctypes.c_size_t
     h.mk_workspace_size.argtypes = [_i, _i, _i, _i, _i, ctypes.POINTER(mk_config_t)]
     h.mk_workspace_size.restype = ctypes.c_size_t
+    h.mk_add_rmsnorm.argtypes = [_p, _i64, _p, _i64, _p, _i, _i, ctypes.c_float, _p, _p, _p, _p, _p]
+    h.mk_add_rmsnorm.restype = _i
+    h.mk_paged_attention.argtypes = [_p, _i64, _p, _p, _i64, _i64, _i64, _p, _p, _i, _i, _i, _i, _i, _i, _i,
+                                     ctypes.c_float, _p, _p, _p, _p, ctypes.c_size_t]
+    h.mk_paged_attention.restype = _i
+    h.mk_paged_attention_workspace_size.argtypes = [_i, _i, _i]
+    h.mk_paged_attention_workspace_size.restype = ctypes.c_size_t
     h.mk_get_status.argtypes = [_p]
     h.mk_get_status.restype = _i
     h.mk_last_error_detail.argtypes = [ctypes.POINTER(ctypes.c_int32)] * 3
@@ -413,3 +424,120 @@ def moe_dispatch_gemm(x, logits, W, k, cfg: mk_config_t | None = None, out=None,
     if check:
         _check(mk_get_status(stream), "device status")
     return out
+
+
+# ------------------------------------------- operators of a decode step --
+
+def mk_add_rmsnorm(x, x_stride, residual, residual_stride, weight, T, H, eps, out, out8, scale, residual_out,
+                   stream=None) -> int:
+    return int(lib().mk_add_rmsnorm(_ptr(x), x_stride, _ptr(residual), residual_stride, _ptr(weight), T, H, eps,
+                                    _ptr(out), _ptr(out8), _ptr(scale), _ptr(residual_out), _stream(stream)))
+
+
+def _need(ok, what: str):
+    if not ok:
+        raise ValueError(what)
+
+
+def _used_on(stream, *tensors):
+    """Tell torch's allocator that a torch stream other than the current one
+    uses tensors allocated here, so that their memory is not handed out while
+    it still does."""
+    if hasattr(stream, "cuda_stream"):
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+
+
+def add_rmsnorm(x, weight, residual=None, eps=1e-6, bf16=True, e4m3=False, residual_out=None, stream=None, check=True):
+    """Residual addition + RMS norm on torch tensors x[T,H] bf16 (rows may be
+    strided), weight[H] bf16, residual[T,H] bf16.
+
+    Returns a dict: ``out`` (bf16) unless ``bf16`` is false, ``out8``
+    (float8_e4m3fn) and ``scale`` (one f32 per 128 columns) with ``e4m3``,
+    and with a residual the new stream ``residual`` (in ``residual_out`` when
+    given, which may be the residual itself).
+    """
+    import torch
+
+    b16, dev = torch.bfloat16, x.device
+    _need(x.dim() == 2 and x.dtype == b16 and x.is_cuda and (x.stride(1) == 1 or x.shape[1] == 1),
+          "x must be a CUDA bf16 [T,H] tensor with contiguous rows")
+    T, H = x.shape
+    _need(weight.shape == (H,) and weight.dtype == b16 and weight.device == dev and weight.is_contiguous(),
+          "weight must be bf16 [H] on x's device")
+    _need(bf16 or e4m3, "no output asked for")
+    o = {}
+    if bf16:
+        o["out"] = torch.empty((T, H), dtype=b16, device=dev)
+    if e4m3:
+        o["out8"] = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=dev)
+        o["scale"] = torch.empty((T, -(-H // 128)), dtype=torch.float32, device=dev)
+    if residual is not None:
+        _need(residual.shape == (T, H) and residual.dtype == b16 and residual.device == dev
+              and (residual.stride(1) == 1 or H == 1), "residual must be bf16 [T,H] with contiguous rows on x's device")
+        if residual_out is None:
+            residual_out = torch.empty((T, H), dtype=b16, device=dev)
+        _need(residual_out.shape == (T, H) and residual_out.dtype == b16 and residual_out.device == dev
+              and residual_out.is_contiguous(), "residual_out must be contiguous bf16 [T,H] on x's device")
+        o["residual"] = residual_out
+    else:
+        _need(residual_out is None, "residual_out needs a residual")
+    st = mk_add_rmsnorm(x, x.stride(0), residual, residual.stride(0) if residual is not None else 0, weight, T, H, eps,
+                        o.get("out"), o.get("out8"), o.get("scale"), o.get("residual"), stream)
+    _used_on(stream, *o.values())
+    _check(st, "mk_add_rmsnorm")
+    if check:
+        _check(mk_get_status(stream), "device status")
+    return o
+
+
+def mk_paged_attention(q, q_stride, k_cache, v_cache, page_stride, token_stride, head_stride, block_table, seq_lens, B,
+                       Hq, Hkv, D, page_size, max_pages, num_pages, scale, out, lse=None, stream=None, workspace=None,
+                       ws_bytes: int = 0) -> int:
+    return int(lib().mk_paged_attention(_ptr(q), q_stride, _ptr(k_cache), _ptr(v_cache), page_stride, token_stride,
+                                        head_stride, _ptr(block_table), _ptr(seq_lens), B, Hq, Hkv, D, page_size,
+                                        max_pages, num_pages, scale, _ptr(out), _ptr(lse), _stream(stream),
+                                        _ptr(workspace), int(ws_bytes)))
+
+
+def mk_paged_attention_workspace_size(B, Hq, Hkv) -> int:
+    return int(lib().mk_paged_attention_workspace_size(B, Hq, Hkv))
+
+
+def paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale=None, stream=None, workspace=None, ws_bytes=0,
+                    check=True):
+    """Attention of one new token per sequence, on torch tensors: q[B,Hq,D]
+    bf16, k_cache and v_cache [pages, page_size, Hkv, D] bf16 (views with equal
+    strides, the last dimension contiguous), block_table[B,max_pages] i32,
+    seq_lens[B] i32 (cached keys, the new token's among them).
+
+    ``scale`` defaults to D ** -0.5.  Returns ``out`` [B,Hq,D] bf16 and
+    ``lse`` [B,Hq] f32.
+    """
+    import torch
+
+    b16, i32, dev = torch.bfloat16, torch.int32, q.device
+    _need(q.dim() == 3 and q.dtype == b16 and q.is_cuda, "q must be a CUDA bf16 [B,Hq,D] tensor")
+    B, Hq, D = q.shape
+    _need(q.stride(2) == 1 and (Hq == 1 or q.stride(1) == D), "the heads of a sequence's q must be contiguous")
+    for t in (k_cache, v_cache):
+        _need(t.dim() == 4 and t.dtype == b16 and t.device == dev and t.shape[3] == D and t.stride(3) == 1,
+              "caches must be bf16 [pages, page_size, Hkv, D] on q's device, D contiguous")
+    _need(k_cache.shape == v_cache.shape and k_cache.stride() == v_cache.stride(),
+          "k_cache and v_cache must agree in shape and strides")
+    pages, page_size, Hkv, _ = k_cache.shape
+    _need(block_table.dim() == 2 and block_table.shape[0] == B and block_table.dtype == i32
+          and block_table.device == dev and block_table.is_contiguous(), "block_table must be i32 [B,max_pages]")
+    _need(seq_lens.shape == (B,) and seq_lens.dtype == i32 and seq_lens.device == dev and seq_lens.is_contiguous(),
+          "seq_lens must be i32 [B]")
+    out = torch.empty((B, Hq, D), dtype=b16, device=dev)
+    lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
+    st = mk_paged_attention(q, q.stride(0), k_cache, v_cache, *k_cache.stride()[:3], block_table, seq_lens, B, Hq, Hkv,
+                            D, page_size, block_table.shape[1], pages, D ** -0.5 if scale is None else scale, out, lse,
+                            stream, workspace, ws_bytes)
+    _used_on(stream, out, lse)
+    _check(st, "mk_paged_attention")
+    if check:
+        _check(mk_get_status(stream), "device status")
+    return dict(out=out, lse=lse)

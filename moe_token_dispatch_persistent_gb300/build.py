@@ -1,8 +1,8 @@
 """Build the CUDA library ``_build/libmk.so`` for sm_103a with nvcc.
 
-Two translation units (device code, host API) compile in parallel, then link
-into one shared library with the CUDA runtime linked statically.  The
-library's ABI is ``include/mk.h``.
+The translation units compile in parallel, then link into one shared library
+with the CUDA runtime linked statically.  The library's ABI is
+``include/mk.h``.
 """
 from __future__ import annotations
 
@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libmk.so")
-UNITS = ["mk_kernels.cu", "mk_api.cu", "mk_noalloc.cu"]
+UNITS = ["mk_kernels.cu", "mk_api.cu", "mk_noalloc.cu", "mk_norm.cu", "mk_attn.cu"]
 
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

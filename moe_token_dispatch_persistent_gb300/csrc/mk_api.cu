@@ -22,6 +22,7 @@
 
 #include "mk.h"
 #include "mk_common.h"
+#include "mk_host.h"
 
 namespace mk {
 cudaError_t launch_fused(const Params& p, const CUtensorMap& a, const CUtensorMap& b, const CUtensorMap& b3,
@@ -61,8 +62,8 @@ struct WsEntry {
     void* ptr = nullptr;
     size_t bytes = 0;
 };
-std::map<std::pair<int, cudaStream_t>, WsEntry> g_ws;
-std::map<std::pair<int, cudaStream_t>, WsEntry> g_ws_ep;  // expert-parallel layout (zeroed whole)
+// One cache per layout of the control block (all but WS_DISPATCH are zeroed whole).
+std::map<std::pair<int, cudaStream_t>, WsEntry> g_ws[WS_KINDS];
 
 struct HostStage {
     void* ptr = nullptr;
@@ -239,20 +240,30 @@ int n_group_for(int H, int F, int nb, int sharers = 1) {
 
 CUresult encode_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t outer, uint64_t row_bytes,
                    uint32_t box_inner, uint32_t box_outer) {
-    cuuint64_t dims[2] = {inner, outer};
-    cuuint64_t strides[1] = {row_bytes};
-    cuuint32_t box[2] = {box_inner, box_outer};
-    cuuint32_t estr[2] = {1, 1};
-    return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return host_encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, inner, outer, row_bytes, box_inner, box_outer);
 }
 
-// The library's workspace for (device, stream), grown on demand.  The new
-// buffer's bookkeeping part (everything before the staging rows) is zeroed.
+// The library's dispatch (or expert-parallel) workspace for (device, stream).
+// A new dispatch buffer's bookkeeping part (everything before the staging
+// rows) is zeroed; expert-parallel buffers whole.
 mk_status_t cached_workspace(int dev, cudaStream_t st, size_t need, size_t zero_bytes, void** out, bool ep = false) {
+    return host_workspace(ep ? WS_EP : WS_DISPATCH, dev, st, need, zero_bytes, out);
+}
+
+}  // namespace
+
+namespace mk {
+
+mk_status_t host_device(int* dev, int* sms) {
+    DevInfo* d = nullptr;
+    const mk_status_t s = device_info(dev, &d);
+    if (s == MK_OK) *sms = d->sms;
+    return s;
+}
+
+mk_status_t host_workspace(WsKind kind, int dev, cudaStream_t st, size_t need, size_t zero_bytes, void** out) {
     std::lock_guard<std::mutex> lock(g_mu);
-    WsEntry& w = ep ? g_ws_ep[{dev, st}] : g_ws[{dev, st}];
+    WsEntry& w = g_ws[kind][{dev, st}];
     if (w.bytes < need) {
         if (w.ptr && cudaFreeAsync(w.ptr, st) != cudaSuccess) return MK_ERR_CUDA;
         w.ptr = nullptr;
@@ -262,14 +273,24 @@ mk_status_t cached_workspace(int dev, cudaStream_t st, size_t need, size_t zero_
             w.ptr = nullptr;
             return MK_ERR_CUDA;
         }
-        if (cudaMemsetAsync(w.ptr, 0, ep ? grow : zero_bytes, st) != cudaSuccess) return MK_ERR_CUDA;
+        if (cudaMemsetAsync(w.ptr, 0, kind == WS_DISPATCH ? zero_bytes : grow, st) != cudaSuccess) return MK_ERR_CUDA;
         w.bytes = grow;
     }
     *out = w.ptr;
     return MK_OK;
 }
 
-}  // namespace
+CUresult host_encode_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t outer,
+                        uint64_t row_bytes, uint32_t box_inner, uint32_t box_outer) {
+    cuuint64_t dims[2] = {inner, outer};
+    cuuint64_t strides[1] = {row_bytes};
+    cuuint32_t box[2] = {box_inner, box_outer};
+    cuuint32_t estr[2] = {1, 1};
+    return g_encode(m, type, 2, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+}  // namespace mk
 
 extern "C" {
 
@@ -896,8 +917,8 @@ mk_status_t mk_read_trace(void* stream, const void* workspace, int T, int H, int
     const uint8_t* ws = static_cast<const uint8_t*>(workspace);
     if (!ws) {
         std::lock_guard<std::mutex> lock(g_mu);
-        auto it = g_ws.find({dev, st});
-        if (it == g_ws.end()) return MK_ERR_INVALID_ARG;
+        auto it = g_ws[WS_DISPATCH].find({dev, st});
+        if (it == g_ws[WS_DISPATCH].end()) return MK_ERR_INVALID_ARG;
         ws = static_cast<const uint8_t*>(it->second.ptr);
     }
     const WsLayout L = ws_layout(T, H, E, k);
@@ -913,20 +934,15 @@ void mk_release_workspace(void) {
     int cur = 0;
     cudaGetDevice(&cur);
     // streams may be gone by now: synchronise the device, then free
-    for (auto& kv : g_ws) {
-        if (!kv.second.ptr) continue;
-        cudaSetDevice(kv.first.first);
-        cudaDeviceSynchronize();
-        cudaFree(kv.second.ptr);
+    for (auto& cache : g_ws) {
+        for (auto& kv : cache) {
+            if (!kv.second.ptr) continue;
+            cudaSetDevice(kv.first.first);
+            cudaDeviceSynchronize();
+            cudaFree(kv.second.ptr);
+        }
+        cache.clear();
     }
-    g_ws.clear();
-    for (auto& kv : g_ws_ep) {
-        if (!kv.second.ptr) continue;
-        cudaSetDevice(kv.first.first);
-        cudaDeviceSynchronize();
-        cudaFree(kv.second.ptr);
-    }
-    g_ws_ep.clear();
     for (auto& kv : g_host_stage) {
         cudaSetDevice(kv.first.first);
         cudaDeviceSynchronize();

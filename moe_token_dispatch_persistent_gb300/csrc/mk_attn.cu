@@ -1,0 +1,653 @@
+// mk_attn.cu -- mk_paged_attention: attention of one new token per sequence
+// over a paged key-value cache, split over the caches' lengths and joined.
+//
+//   s_j = scale * q . k_j,   out = sum_j e^(s_j - m) v_j / l,
+//   m = max_j s_j,  l = sum_j e^(s_j - m),  lse = m + log l
+//
+// Every key and value is read once for all the query heads that share it, so
+// the cache's bytes bound it: 4*D bytes per token and key-value head against
+// 4*D operations per query head.
+//
+// Work.  A tile is 16 keys of one (sequence, group of up to 16 query heads
+// of one key-value head).  The tiles of all of them in a row are cut into one
+// equal range per CTA, whatever the lengths, so every SM streams the same
+// number of bytes; a range that covers a part of a (sequence, group) leaves
+// an unnormalised partial result, and the CTA that finishes last of those
+// sharing it joins them, in the order of the keys.  The caller's lengths stay
+// on the device: every CTA builds the table of tiles itself.
+//
+// Inside a CTA the warps take every WARPS-th tile of a range and never wait
+// for one another: each has its own ring of tiles in shared memory, filled by
+// its own 16-byte asynchronous copies (any page size, any stride, keys past
+// the end filled with zeros), which run ahead across the ends of ranges.  The
+// heads are the rows of m16n8k16 products (a decode step has at most 16 rows
+// to offer, where tcgen05 wants 64 or 128, and the products take a small part
+// of the time that the bytes do), so scores and weights stay in registers.
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "mk.h"
+#include "mk_common.h"
+#include "mk_host.h"
+#include "mk_ptx.cuh"
+
+namespace mk {
+namespace {
+
+constexpr int KEYS = 16;          // keys per tile
+constexpr int ROWS = 16;          // query heads per group (rows of the product)
+constexpr int ATTN_MAX_B = 4096;  // sequences (their tile counts sit in shared memory)
+constexpr int ATTN_MAX_CTAS = 256;
+constexpr float LOG2E = 1.4426950408889634f;
+constexpr float LN2 = 0.6931471805599453f;
+
+template <int D>
+struct Geo {
+    static constexpr int WARPS = D == 256 ? 4 : 8;
+    static constexpr int STAGES = D == 64 ? 4 : 2;
+    static constexpr int THREADS = WARPS * 32;
+    static constexpr int CHUNKS = D / 8;              // 16-byte pieces of a row
+    static constexpr int HALF = KEYS * D * 2;         // one tile's keys (or values)
+    static constexpr int RING = STAGES * 2 * HALF;    // per warp
+    static constexpr int OSTRIDE = D + 8;             // floats between rows of the join buffer: no bank conflicts
+    static constexpr int SM_O = WARPS * RING;
+    static constexpr int SM_ML = SM_O + WARPS * ROWS * OSTRIDE * 4;
+    static constexpr int SM_PREFIX = SM_ML + 2 * WARPS * ROWS * 4;
+    static constexpr int SM_SMALL = SM_PREFIX + (ATTN_MAX_B + 1) * 4;
+    static constexpr int SMEM = SM_SMALL + 256;
+    static constexpr int SLOT = 2 * ROWS + ROWS * D;  // floats of a partial result: m, l, O
+    static_assert(SMEM <= 232448, "dynamic shared memory of one CTA on sm_103");
+};
+
+constexpr size_t ATTN_SLOT_BYTES = size_t(Geo<256>::SLOT) * 4;
+constexpr size_t ATTN_SLOTS_BYTES = 2 * ATTN_MAX_CTAS * ATTN_SLOT_BYTES;  // fixed, so the counters never move
+
+struct AttnParams {
+    const __nv_bfloat16* q;
+    const __nv_bfloat16* k;
+    const __nv_bfloat16* v;
+    const int32_t* table;
+    const int32_t* lens;
+    __nv_bfloat16* out;
+    float* lse;                                   // or null
+    float* slots;                                 // two partial results per CTA
+    uint32_t* arrived;                            // per (sequence, group); zero between calls
+    DevError* err;
+    int64_t q_stride, page_stride, token_stride, head_stride;
+    int B, Hq, Hkv, page_size, max_pages, num_pages;
+    int per_kv;                                   // query heads per key-value head
+    int chunks;                                   // groups per key-value head
+    int groups;                                   // groups per sequence
+    float scale2;                                 // scale * log2(e)
+};
+
+__device__ __forceinline__ void attn_error(DevError* e, uint32_t site, uint32_t info) {
+    if (atomicCAS(&e->code, 0u, uint32_t(ERR_FAULT)) == 0u) {
+        e->site = site;
+        e->cta = blockIdx.x;
+        e->info = info;
+    }
+}
+
+// 16 bytes global -> shared; zeros when !ok (the source is then not read).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&b);
+}
+__device__ __forceinline__ float exp2_of(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+
+// Tiles [t0, t1) of group g of sequence b.
+struct Range {
+    int b, g;
+    uint32_t t0, t1;
+    uint32_t begin;  // position of the group's first tile in the whole order
+    uint32_t tiles;  // tiles of the group
+};
+
+// The range that starts at position `pos`, up to the group's or the CTA's end; advances pos.
+__device__ __forceinline__ bool next_range(uint32_t& pos, uint32_t end, const uint32_t* prefix, int B, uint32_t groups,
+                                           Range& r) {
+    if (pos >= end) return false;
+    const uint32_t want = pos / groups;  // tiles of one group before it
+    int lo = 0, hi = B;                  // the last b with prefix[b] <= want that has tiles
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (prefix[mid] <= want) lo = mid;
+        else hi = mid;
+    }
+    const uint32_t n = prefix[lo + 1] - prefix[lo];
+    const uint32_t in = pos - prefix[lo] * groups;
+    r.b = lo;
+    r.g = int(in / n);
+    r.tiles = n;
+    r.t0 = in - uint32_t(r.g) * n;
+    r.t1 = min(n, r.t0 + (end - pos));
+    r.begin = pos - r.t0;
+    pos += r.t1 - r.t0;
+    return true;
+}
+
+__device__ __forceinline__ uint32_t range_start(uint32_t total, uint32_t c, uint32_t n) {
+    return uint32_t(uint64_t(total) * c / n);
+}
+// The CTA whose range holds position p.
+__device__ __forceinline__ uint32_t range_owner(uint32_t total, uint32_t p, uint32_t n) {
+    return uint32_t((uint64_t(p + 1) * n - 1) / total);
+}
+
+// Element offset of one key's row of a tile (row = lane for lanes 0-15), or
+// -1 when the key lies past the sequence.
+__device__ __forceinline__ int64_t key_offset(const AttnParams& p, int b, int kv, uint32_t tile, int lane, int len) {
+    const int key = int(tile) * KEYS + (lane & (KEYS - 1));
+    if (key >= len) return -1;
+    const int slot = key / p.page_size;
+    const int page = __ldg(p.table + int64_t(b) * p.max_pages + slot);
+    if (page < 0 || page >= p.num_pages) {
+        attn_error(p.err, SITE_PAGE_RANGE, uint32_t(page));
+        return -1;
+    }
+    return page * p.page_stride + (key - slot * p.page_size) * p.token_stride + kv * p.head_stride;
+}
+
+template <int D>
+__global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(const AttnParams p) {
+    using G = Geo<D>;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + G::SM_PREFIX);
+    uint32_t* small = reinterpret_cast<uint32_t*>(smem + G::SM_SMALL);
+    float* sO = reinterpret_cast<float*>(smem + G::SM_O);
+    float* sM = reinterpret_cast<float*>(smem + G::SM_ML);
+    float* sL = sM + G::WARPS * ROWS;
+    const uint32_t groups = uint32_t(p.groups);
+    const int64_t cap = int64_t(p.max_pages) * p.page_size;
+
+    // ---- tiles per sequence, summed over the sequences before it
+    auto length = [&](int b) -> int {
+        const int n = __ldg(p.lens + b);
+        return n < 0 ? 0 : n > cap ? int(cap) : n;
+    };
+    {
+        const int per = (p.B + G::THREADS - 1) / G::THREADS;
+        const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
+        uint32_t mine = 0;
+        for (int b = b0; b < b1; ++b) {
+            const int n = __ldg(p.lens + b);
+            if ((n < 0 || n > cap) && blockIdx.x == 0) attn_error(p.err, SITE_SEQ_LEN, uint32_t(n));
+            mine += uint32_t((length(b) + KEYS - 1) / KEYS);
+        }
+        uint32_t run = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xffffffffu, run, d);
+            if (lane >= d) run += o;
+        }
+        if (lane == 31) small[warp] = run;
+        __syncthreads();
+        uint32_t base = run - mine;
+        for (int w = 0; w < warp; ++w) base += small[w];
+        for (int b = b0; b < b1; ++b) {
+            prefix[b] = base;
+            base += uint32_t((length(b) + KEYS - 1) / KEYS);
+        }
+        if (b1 == p.B && b0 < b1) prefix[p.B] = base;
+        __syncthreads();
+    }
+
+    // sequences without keys: zeros and -inf
+    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
+        if (prefix[b + 1] != prefix[b]) continue;
+        uint2* o = reinterpret_cast<uint2*>(p.out + int64_t(b) * p.Hq * D);
+        for (int i = tid; i < p.Hq * D / 4; i += G::THREADS) o[i] = make_uint2(0u, 0u);
+        if (p.lse)
+            for (int i = tid; i < p.Hq; i += G::THREADS) p.lse[int64_t(b) * p.Hq + i] = -INFINITY;
+    }
+
+    const uint32_t total = prefix[p.B] * groups;
+    // at least one tile per warp: a shorter range would only add partial results to join
+    const uint32_t nctas = min(gridDim.x, (total + G::WARPS - 1) / G::WARPS);
+    if (blockIdx.x >= nctas) return;
+    const uint32_t start = range_start(total, blockIdx.x, nctas), end = range_start(total, blockIdx.x + 1, nctas);
+
+    // ---- this warp's ring: loads run STAGES tiles ahead, across ranges
+    const uint32_t ring = smem_u32(smem) + uint32_t(warp) * G::RING;
+    uint32_t load_pos = start, load_tile = 0;
+    Range lr;
+    int load_len = 0;
+    bool loading = true;
+    lr.t1 = 0;
+    int64_t ahead = -1;  // row offset of the next tile to load
+    auto seek = [&](uint32_t t) {
+        load_tile = t;
+        while (load_tile >= lr.t1) {
+            if (!next_range(load_pos, end, prefix, p.B, groups, lr)) {
+                loading = false;
+                return;
+            }
+            load_len = length(lr.b);
+            load_tile = lr.t0 + uint32_t(warp);
+        }
+        // the page is looked up one tile before its rows are copied
+        ahead = key_offset(p, lr.b, lr.g / p.chunks, load_tile, lane, load_len);
+    };
+    seek(0);
+    uint32_t load_slot = 0;
+    auto issue = [&]() {
+        if (loading) {
+            const uint32_t dst = ring + load_slot * (2 * G::HALF);
+            const int64_t off = ahead;
+#pragma unroll
+            for (int i = 0; i < KEYS * G::CHUNKS / 32; ++i) {
+                const int piece = i * 32 + lane, row = piece / G::CHUNKS, c = piece % G::CHUNKS;
+                const int64_t ro = __shfl_sync(0xffffffffu, off, row);
+                const bool ok = ro >= 0;
+                const int64_t at = (ok ? ro : 0) + c * 8;
+                const uint32_t d = dst + uint32_t(row * D * 2 + ((c ^ (row & 7)) << 4));
+                copy16(d, p.k + at, ok);
+                copy16(d + G::HALF, p.v + at, ok);
+            }
+            seek(load_tile + G::WARPS);
+        }
+        copy_commit();
+        if (++load_slot == G::STAGES) load_slot = 0;
+    };
+#pragma unroll
+    for (int i = 0; i < G::STAGES; ++i) issue();
+
+    const int r0 = lane >> 2, r1 = r0 + 8;  // this lane's rows (heads) of the products
+    uint32_t slot = 0, pos = start;
+    Range r;
+    bool first = true;
+    while (next_range(pos, end, prefix, p.B, groups, r)) {
+        const int kv = r.g / p.chunks, head0 = kv * p.per_kv + (r.g % p.chunks) * ROWS;
+        const int heads = min(ROWS, (kv + 1) * p.per_kv - head0);
+        const int len = length(r.b);
+        // query rows as A fragments
+        uint32_t qa[D / 16][4];
+        {
+            const __nv_bfloat16* qb = p.q + int64_t(r.b) * p.q_stride + int64_t(head0) * D + (lane & 3) * 2;
+            const uint32_t* q0 = reinterpret_cast<const uint32_t*>(qb + int64_t(r0 < heads ? r0 : 0) * D);
+            const uint32_t* q1 = reinterpret_cast<const uint32_t*>(qb + int64_t(r1 < heads ? r1 : 0) * D);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                qa[kk][0] = r0 < heads ? q0[kk * 8] : 0u;
+                qa[kk][1] = r1 < heads ? q1[kk * 8] : 0u;
+                qa[kk][2] = r0 < heads ? q0[kk * 8 + 4] : 0u;
+                qa[kk][3] = r1 < heads ? q1[kk * 8 + 4] : 0u;
+            }
+        }
+        float o[D / 8][4];
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
+        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+
+        for (uint32_t t = r.t0 + warp; t < r.t1; t += G::WARPS) {
+            copy_wait<G::STAGES - 1>();
+            __syncwarp();
+            const uint32_t ks = ring + slot * (2 * G::HALF), vs = ks + G::HALF;
+            // scores: two tiles of 8 keys
+            float s[2][4] = {};
+            {
+                const int row = ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
+                const uint32_t rb = ks + uint32_t(row * D * 2);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    uint32_t kb[4];
+                    ldsm4(rb + (uint32_t((kk * 2 + half) ^ (row & 7)) << 4), kb);
+                    mma16816(s[0], qa[kk], kb[0], kb[1]);
+                    mma16816(s[1], qa[kk], kb[2], kb[3]);
+                }
+            }
+            const int key = int(t) * KEYS + (lane & 3) * 2;
+            const bool cut = int(t + 1) * KEYS > len;
+            float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s[n][i] *= p.scale2;
+                    if (cut && key + n * 8 + (i & 1) >= len) s[n][i] = -INFINITY;
+                }
+                x0 = fmaxf(x0, fmaxf(s[n][0], s[n][1]));
+                x1 = fmaxf(x1, fmaxf(s[n][2], s[n][3]));
+            }
+            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 1));
+            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 1));
+            x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, 2));
+            x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, 2));
+            if (__any_sync(0xffffffffu, x0 > m0 || x1 > m1)) {
+                // a new maximum: what was summed so far shrinks (from nothing: stays 0)
+                const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+                const float f0 = m0 == -INFINITY ? 0.f : exp2_of(m0 - n0);
+                const float f1 = m1 == -INFINITY ? 0.f : exp2_of(m1 - n1);
+                m0 = n0;
+                m1 = n1;
+                l0 *= f0;
+                l1 *= f1;
+#pragma unroll
+                for (int n = 0; n < D / 8; ++n) {
+                    o[n][0] *= f0;
+                    o[n][1] *= f0;
+                    o[n][2] *= f1;
+                    o[n][3] *= f1;
+                }
+            }
+            // a row whose scores are all -inf has weights 0, not e^(-inf + inf)
+            const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+            uint32_t hi[4], lo[4];
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {
+                const float p0 = exp2_of(s[n][0] - b0), p1 = exp2_of(s[n][1] - b0);
+                const float p2 = exp2_of(s[n][2] - b1), p3 = exp2_of(s[n][3] - b1);
+                l0 += p0 + p1;
+                l1 += p2 + p3;
+                // each weight as the sum of two bf16 values: 16 significant bits reach the products
+                hi[2 * n] = pack_bf16(p0, p1);
+                hi[2 * n + 1] = pack_bf16(p2, p3);
+                lo[2 * n] = pack_bf16(p0 - __uint_as_float(hi[2 * n] << 16),
+                                      p1 - __uint_as_float(hi[2 * n] & 0xffff0000u));
+                lo[2 * n + 1] = pack_bf16(p2 - __uint_as_float(hi[2 * n + 1] << 16),
+                                          p3 - __uint_as_float(hi[2 * n + 1] & 0xffff0000u));
+            }
+            {
+                const int row = (((lane >> 3) & 1) << 3) + (lane & 7), half = lane >> 4;
+                const uint32_t rb = vs + uint32_t(row * D * 2);
+#pragma unroll
+                for (int n = 0; n < D / 16; ++n) {
+                    uint32_t vb[4];
+                    ldsm4_t(rb + (uint32_t((n * 2 + half) ^ (row & 7)) << 4), vb);
+                    mma16816(o[2 * n], hi, vb[0], vb[1]);
+                    mma16816(o[2 * n + 1], hi, vb[2], vb[3]);
+                    mma16816(o[2 * n], lo, vb[0], vb[1]);
+                    mma16816(o[2 * n + 1], lo, vb[2], vb[3]);
+                }
+            }
+            __syncwarp();  // every lane has read the tile before it is overwritten
+            issue();
+            if (++slot == G::STAGES) slot = 0;
+        }
+
+        // ---- join the warps' results of the range
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
+        l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
+        l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+        const int nw = int(min(uint32_t(G::WARPS), r.t1 - r.t0));  // warps that had a tile
+        if (warp < nw) {
+            if ((lane & 3) == 0) {
+                sM[warp * ROWS + r0] = m0;
+                sM[warp * ROWS + r1] = m1;
+                sL[warp * ROWS + r0] = l0;
+                sL[warp * ROWS + r1] = l1;
+            }
+            float* ow = sO + warp * ROWS * G::OSTRIDE + (lane & 3) * 2;
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+                if (r0 < heads) *reinterpret_cast<float2*>(ow + r0 * G::OSTRIDE + n * 8) = make_float2(o[n][0], o[n][1]);
+                if (r1 < heads) *reinterpret_cast<float2*>(ow + r1 * G::OSTRIDE + n * 8) = make_float2(o[n][2], o[n][3]);
+            }
+        }
+        __syncthreads();
+        const bool whole = r.t1 - r.t0 == r.tiles;
+        float* mine = p.slots + size_t(2 * blockIdx.x + (first ? 0 : 1)) * (ATTN_SLOT_BYTES / 4);
+        for (int i = tid; i < heads * (D / 4); i += G::THREADS) {
+            const int row = i / (D / 4), c = (i % (D / 4)) * 4;
+            float top = -INFINITY;
+            for (int w = 0; w < nw; ++w) top = fmaxf(top, sM[w * ROWS + row]);
+            const float base = top == -INFINITY ? 0.f : top;
+            float l = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int w = 0; w < nw; ++w) {
+                const float f = exp2_of(sM[w * ROWS + row] - base);
+                const float4 v = *reinterpret_cast<const float4*>(sO + (w * ROWS + row) * G::OSTRIDE + c);
+                l = fmaf(f, sL[w * ROWS + row], l);
+                acc.x = fmaf(f, v.x, acc.x);
+                acc.y = fmaf(f, v.y, acc.y);
+                acc.z = fmaf(f, v.z, acc.z);
+                acc.w = fmaf(f, v.w, acc.w);
+            }
+            if (whole) {
+                const int64_t at = int64_t(r.b) * p.Hq + head0 + row;
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                *reinterpret_cast<uint2*>(p.out + at * D + c) =
+                    make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+                if (p.lse && c == 0) p.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * LN2;
+            } else {
+                *reinterpret_cast<float4*>(mine + 2 * ROWS + row * D + c) = acc;
+                if (c == 0) {
+                    mine[row] = top;
+                    mine[ROWS + row] = l;
+                }
+            }
+        }
+        if (!whole) {
+            // ---- the CTA that completes the group joins its partial results
+            uint32_t* flag = small;
+            const uint32_t c0 = range_owner(total, r.begin, nctas), c1 = range_owner(total, r.begin + r.tiles - 1, nctas);
+            const int n = int(c1 - c0) + 1;
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                uint32_t* a = p.arrived + size_t(r.b) * groups + r.g;
+                const bool last = atom_add_acq_rel_u32(a, 1u) == uint32_t(n) - 1;
+                if (last) *a = 0u;
+                flag[0] = last;
+            }
+            __syncthreads();
+            if (flag[0]) {
+                __threadfence();
+                // weights of the pieces, then their sum: every thread four columns of
+                // one row, the pieces dealt out over as many threads as there are
+                auto piece = [&](int i) -> const float* {
+                    const uint32_t c = c0 + uint32_t(i);
+                    const uint32_t which = range_start(total, c, nctas) >= r.begin ? 0u : 1u;
+                    return p.slots + size_t(2 * c + which) * (ATTN_SLOT_BYTES / 4);
+                };
+                float* sw = sO;                  // [n][heads] weights
+                float* st = sO + n * ROWS;       // [heads] maximum, then sum
+                float4* red = reinterpret_cast<float4*>(st + 2 * ROWS);
+                for (int row = warp; row < heads; row += G::WARPS) {
+                    float top = -INFINITY;
+                    for (int i = lane; i < n; i += 32) top = fmaxf(top, __ldcg(piece(i) + row));
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+                    const float base = top == -INFINITY ? 0.f : top;
+                    float l = 0.f;
+                    for (int i = lane; i < n; i += 32) {
+                        const float* s = piece(i);
+                        const float f = exp2_of(__ldcg(s + row) - base);
+                        sw[i * ROWS + row] = f;
+                        l = fmaf(f, __ldcg(s + ROWS + row), l);
+                    }
+#pragma unroll
+                    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
+                    if (lane == 0) {
+                        st[row] = top;
+                        st[ROWS + row] = l;
+                    }
+                }
+                __syncthreads();
+                const int items = heads * (D / 4);
+                const int parts = items >= G::THREADS ? 1 : G::THREADS / items;
+                for (int i0 = 0; i0 < items; i0 += G::THREADS) {
+                    const int item = parts > 1 ? tid % items : i0 + tid, part = parts > 1 ? tid / items : 0;
+                    const bool on = item < items && part < parts;
+                    const int row = item / (D / 4), c = (item % (D / 4)) * 4;
+                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                    if (on) {
+#pragma unroll 4
+                        for (int i = part; i < n; i += parts) {
+                            const float f = sw[i * ROWS + row];
+                            const float4 v = __ldcg(reinterpret_cast<const float4*>(piece(i) + 2 * ROWS + row * D + c));
+                            acc.x = fmaf(f, v.x, acc.x);
+                            acc.y = fmaf(f, v.y, acc.y);
+                            acc.z = fmaf(f, v.z, acc.z);
+                            acc.w = fmaf(f, v.w, acc.w);
+                        }
+                    }
+                    if (parts > 1) {
+                        if (on) red[part * items + item] = acc;
+                        __syncthreads();
+                        if (on && part == 0)
+                            for (int q = 1; q < parts; ++q) {
+                                const float4 v = red[q * items + item];
+                                acc.x += v.x;
+                                acc.y += v.y;
+                                acc.z += v.z;
+                                acc.w += v.w;
+                            }
+                    }
+                    if (on && part == 0) {
+                        const float l = st[ROWS + row];
+                        const float inv = l == 0.f ? 0.f : 1.f / l;
+                        const int64_t at = int64_t(r.b) * p.Hq + head0 + row;
+                        *reinterpret_cast<uint2*>(p.out + at * D + c) =
+                            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
+                        if (p.lse && c == 0) p.lse[at] = l == 0.f ? -INFINITY : (st[row] + log2f(l)) * LN2;
+                    }
+                }
+            }
+        }
+        __syncthreads();  // the join buffer is free for the next range
+        first = false;
+    }
+    copy_wait<0>();
+}
+
+template <int D>
+cudaError_t launch_attn(const AttnParams& p, int grid, cudaStream_t st) {
+    // set on every call: a device reset would forget it
+    cudaError_t e = cudaFuncSetAttribute(mk_paged_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         Geo<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    mk_paged_attention_kernel<D><<<grid, Geo<D>::THREADS, Geo<D>::SMEM, st>>>(p);
+    return cudaGetLastError();
+}
+
+// Groups of up to 16 query heads per sequence, 0 for sizes outside the limits.
+int64_t attn_groups(int B, int Hq, int Hkv) {
+    if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return 0;
+    return int64_t(Hkv) * ((Hq / Hkv + ROWS - 1) / ROWS);
+}
+
+}  // namespace
+}  // namespace mk
+
+using namespace mk;
+
+extern "C" size_t mk_paged_attention_workspace_size(int B, int Hq, int Hkv) {
+    const int64_t g = attn_groups(B, Hq, Hkv);
+    if (g == 0 || B > ATTN_MAX_B) return 0;
+    return ATTN_SLOTS_BYTES + ws_align(size_t(B) * size_t(g) * sizeof(uint32_t));
+}
+
+extern "C" mk_status_t mk_paged_attention(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                                          int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                                          const int32_t* block_table, const int32_t* seq_lens, int B, int Hq, int Hkv,
+                                          int D, int page_size, int max_pages, int num_pages, float scale, void* out,
+                                          float* lse, void* stream, void* workspace, size_t ws_bytes) {
+    if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || page_size < 1 || max_pages < 0 || num_pages < 0)
+        return MK_ERR_INVALID_ARG;
+    if (D != 64 && D != 128 && D != 256) return MK_ERR_UNSUPPORTED;
+    if (!std::isfinite(scale)) return MK_ERR_INVALID_ARG;
+    const int64_t groups = attn_groups(B, Hq, Hkv);
+    const int64_t cap = int64_t(max_pages) * page_size;
+    if (B > ATTN_MAX_B || cap > (int64_t(1) << 31) - KEYS) return MK_ERR_UNSUPPORTED;
+    // positions in the order of tiles are 32-bit
+    const int64_t tiles = int64_t(B) * ((cap + KEYS - 1) / KEYS);
+    if (tiles >= int64_t(1) << 31 || tiles * groups >= int64_t(1) << 31) return MK_ERR_UNSUPPORTED;
+    if (B > 0) {
+        if (!q || !seq_lens || !out) return MK_ERR_INVALID_ARG;
+        if (cap > 0 && (!k_cache || !v_cache || !block_table || num_pages < 1)) return MK_ERR_INVALID_ARG;
+        if (!host_aligned(q, 4) || !host_aligned(out, 8) || !host_aligned(k_cache, 16) || !host_aligned(v_cache, 16) ||
+            !host_aligned(block_table, 4) || !host_aligned(seq_lens, 4) || !host_aligned(lse, 4))
+            return MK_ERR_INVALID_ARG;
+        if (B > 1 && (q_stride < int64_t(Hq) * D || q_stride % 2 != 0)) return MK_ERR_INVALID_ARG;
+        // rows are copied in 16-byte pieces; the stride of a dimension of one is never used
+        const int64_t used[3] = {num_pages > 1 ? page_stride : 0, page_size > 1 ? token_stride : 0,
+                                 Hkv > 1 ? head_stride : 0};
+        for (const int64_t v : used)
+            if (v < 0 || v % 8 != 0) return MK_ERR_INVALID_ARG;
+    }
+    int dev = 0, sms = 0;
+    mk_status_t s = host_device(&dev, &sms);
+    if (s != MK_OK) return s;
+    if (B == 0) return MK_OK;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const size_t need = mk_paged_attention_workspace_size(B, Hq, Hkv);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    if (ws) {
+        if (ws_bytes < need || !host_aligned(ws, 256)) return MK_ERR_WORKSPACE;
+    } else {
+        void* w = nullptr;
+        if ((s = host_workspace(WS_ATTN, dev, st, need, need, &w)) != MK_OK) return s;
+        ws = static_cast<uint8_t*>(w);
+    }
+    AttnParams p{};
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k = static_cast<const __nv_bfloat16*>(k_cache);
+    p.v = static_cast<const __nv_bfloat16*>(v_cache);
+    p.table = block_table;
+    p.lens = seq_lens;
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.lse = lse;
+    p.slots = reinterpret_cast<float*>(ws);
+    p.arrived = reinterpret_cast<uint32_t*>(ws + ATTN_SLOTS_BYTES);
+    if (error_word(&p.err) != cudaSuccess) return MK_ERR_CUDA;
+    p.q_stride = q_stride;
+    p.page_stride = page_stride;
+    p.token_stride = token_stride;
+    p.head_stride = head_stride;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.page_size = page_size;
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.per_kv = Hq / Hkv;
+    p.chunks = (p.per_kv + ROWS - 1) / ROWS;
+    p.groups = int(groups);
+    p.scale2 = scale * LOG2E;
+    const int grid = std::min(sms, ATTN_MAX_CTAS);
+    const cudaError_t e = D == 64 ? launch_attn<64>(p, grid, st) : D == 128 ? launch_attn<128>(p, grid, st)
+                                                                           : launch_attn<256>(p, grid, st);
+    return e == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+}

@@ -158,6 +158,8 @@ enum Site : int {
     SITE_PAIR_ALIGN = 18,
     SITE_PAIR_CLUSTER = 19,
     SITE_BAR_SCANNED = 20,
+    SITE_PAGE_RANGE = 21,
+    SITE_SEQ_LEN = 22,
 };
 
 enum ErrCode : uint32_t { ERR_NONE = 0, ERR_TIMEOUT = 1, ERR_FAULT = 2 };

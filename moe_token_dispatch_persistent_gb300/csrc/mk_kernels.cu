@@ -57,13 +57,11 @@
 #include <cstddef>
 
 #include "mk_common.h"
+#include "mk_host.h"
 #include "mk_ptx.cuh"
 
 namespace mk {
 
-struct DevError {
-    uint32_t code, site, cta, info;
-};
 __device__ DevError g_error;
 
 // ------------------------------------------------------------ waiting ------
@@ -2803,6 +2801,13 @@ cudaError_t set_kernel_attributes() {
 
 cudaError_t fused_max_blocks_per_sm(int* n) {
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(n, mk_fused_kernel<0>, NTHREADS, SMEM_BYTES);
+}
+
+cudaError_t error_word(DevError** out) {
+    void* p = nullptr;
+    const cudaError_t err = cudaGetSymbolAddress(&p, g_error);
+    *out = static_cast<DevError*>(p);
+    return err;
 }
 
 cudaError_t read_and_clear_error(uint32_t out[4], cudaStream_t st) {

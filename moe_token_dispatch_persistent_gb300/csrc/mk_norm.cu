@@ -1,0 +1,271 @@
+// mk_norm.cu -- mk_add_rmsnorm: the residual's addition, the root-mean-square
+// norm, and its output in bf16 and / or e4m3 with a scale per 128 columns.
+//
+//   z = x + residual                      residual_out = bf16(z)
+//   y = z * rsqrt(mean(z^2) + eps) * w    out = bf16(y)
+//   per row and 128 columns: a = max |y|, scale = a / 448 (1 where a < 2^-100),
+//   out8 = e4m3(y / scale)
+//
+// z and y stay in 32-bit registers: the norm and the 8-bit values come from
+// the unrounded sum, and each output is rounded once.  One pass: a row is
+// read once, held by the warps that share it, and every output is written
+// from those registers.  Traffic bounds it (up to 9 bytes an element for 6
+// operations); for a few rows the latency of one launch does.
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+
+#include "mk.h"
+#include "mk_host.h"
+
+namespace mk {
+namespace {
+
+constexpr int NORM_CHUNK = 256;  // columns of a row that one warp takes at a time: 8 per lane, two 8-bit groups
+constexpr int NORM_GROUP = 128;  // columns per scale
+constexpr int NORM_MAX_H = 32768;
+constexpr int NORM_MAX_WARPS = 32;
+constexpr float E4M3_MAX = 448.f;
+constexpr float TINY_GROUP = 7.888609052210118e-31f;  // 2^-100
+
+struct NormParams {
+    const __nv_bfloat16* x;
+    const __nv_bfloat16* residual;  // or null
+    const __nv_bfloat16* weight;
+    __nv_bfloat16* out;             // or null
+    __nv_bfloat16* residual_out;    // or null
+    uint8_t* out8;                  // or null
+    float* scale;
+    int64_t x_stride, residual_stride;  // elements between rows
+    int T, H;
+    int warps_per_row, rows_per_cta;
+    float eps;
+};
+
+// The larger of the two, NaN if either is (fmaxf would drop it, and with it a
+// row that holds NaN would get a finite scale).
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Column of element i of a lane's eight in a chunk.  VEC: eight neighbours
+// (16-byte accesses), so lanes 0-15 hold the chunk's first group of 128 and
+// lanes 16-31 its second.  Otherwise 32 apart, so elements 0-3 of all lanes
+// are the first group and 4-7 the second, and accesses still coalesce.
+template <bool VEC>
+__device__ __forceinline__ int column(int chunk, int lane, int i) {
+    return chunk * NORM_CHUNK + (VEC ? lane * 8 + i : lane + 32 * i);
+}
+
+template <bool VEC>
+__device__ __forceinline__ void load8(const __nv_bfloat16* row, int chunk, int lane, int H, float (&v)[8]) {
+    if constexpr (VEC) {
+        const int c = column<true>(chunk, lane, 0);
+        const uint4 q = c < H ? __ldcs(reinterpret_cast<const uint4*>(row + c)) : make_uint4(0, 0, 0, 0);
+        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            v[2 * i] = __uint_as_float(u[i] << 16);
+            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+        }
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int c = column<false>(chunk, lane, i);
+            v[i] = c < H ? __bfloat162float(row[c]) : 0.f;
+        }
+    }
+}
+
+template <bool VEC>
+__device__ __forceinline__ void store8(__nv_bfloat16* row, int chunk, int lane, int H, const float (&v)[8]) {
+    if constexpr (VEC) {
+        const int c = column<true>(chunk, lane, 0);
+        if (c >= H) return;
+        uint32_t u[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+            u[i] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        *reinterpret_cast<uint4*>(row + c) = make_uint4(u[0], u[1], u[2], u[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int c = column<false>(chunk, lane, i);
+            if (c < H) row[c] = __float2bfloat16_rn(v[i]);
+        }
+    }
+}
+
+// The chunk's two groups in e4m3 with their scales.
+template <bool VEC>
+__device__ __forceinline__ void quantize8(uint8_t* row, float* scale_row, int chunk, int lane, int H,
+                                          const float (&y)[8]) {
+    float a[2];
+    if constexpr (VEC) {
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = max_nan(m, fabsf(y[i]));
+#pragma unroll
+        for (int d = 8; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+        a[0] = a[1] = m;  // of this lane's own half: one of the two groups
+    } else {
+#pragma unroll
+        for (int g = 0; g < 2; ++g) {
+            float m = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) m = max_nan(m, fabsf(y[4 * g + i]));
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) m = max_nan(m, __shfl_xor_sync(0xffffffffu, m, d));
+            a[g] = m;
+        }
+    }
+    float s[2], inv[2];
+#pragma unroll
+    for (int g = 0; g < 2; ++g) {
+        s[g] = a[g] < TINY_GROUP ? 1.f : a[g] / E4M3_MAX;
+        inv[g] = 1.f / s[g];
+    }
+    const int group = chunk * 2 + (VEC ? lane >> 4 : lane & 1);
+    if (VEC ? (lane & 15) == 0 : lane < 2)
+        if (group * NORM_GROUP < H) scale_row[group] = (!VEC && (lane & 1)) ? s[1] : s[0];
+    uint32_t q[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        q[i] = __nv_cvt_float_to_fp8(y[i] * inv[VEC ? 0 : i >> 2], __NV_SATFINITE, __NV_E4M3);
+    if constexpr (VEC) {
+        const int c = column<true>(chunk, lane, 0);
+        if (c < H)
+            *reinterpret_cast<uint2*>(row + c) =
+                make_uint2(q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24, q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int c = column<false>(chunk, lane, i);
+            if (c < H) row[c] = uint8_t(q[i]);
+        }
+    }
+}
+
+// C chunks of a row per warp; warps_per_row * C chunks cover the row.
+template <bool VEC, int C>
+__global__ void __launch_bounds__(NORM_MAX_WARPS * 32) mk_add_rmsnorm_kernel(const NormParams p) {
+    __shared__ float part[NORM_MAX_WARPS];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int wpr = p.warps_per_row;
+    const int mine = warp % wpr, first = warp - mine;
+    const int64_t row = int64_t(blockIdx.x) * p.rows_per_cta + warp / wpr;
+    const bool live = row < p.T;
+    const int H = p.H;
+    float z[C][8], w[C][8];
+    float sum = 0.f;
+    if (live) {
+        const __nv_bfloat16* xr = p.x + row * p.x_stride;
+        const __nv_bfloat16* rr = p.residual ? p.residual + row * p.residual_stride : nullptr;
+#pragma unroll
+        for (int j = 0; j < C; ++j) load8<VEC>(xr, mine + j * wpr, lane, H, z[j]);
+        if (rr) {
+            float r[C][8];
+#pragma unroll
+            for (int j = 0; j < C; ++j) load8<VEC>(rr, mine + j * wpr, lane, H, r[j]);
+#pragma unroll
+            for (int j = 0; j < C; ++j)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) z[j][i] += r[j][i];
+        }
+        // the weights do not depend on the sum: their loads run beside it
+#pragma unroll
+        for (int j = 0; j < C; ++j) load8<VEC>(p.weight, mine + j * wpr, lane, H, w[j]);
+#pragma unroll
+        for (int j = 0; j < C; ++j)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) sum = fmaf(z[j][i], z[j][i], sum);
+        if (p.residual_out)
+#pragma unroll
+            for (int j = 0; j < C; ++j) store8<VEC>(p.residual_out + row * H, mine + j * wpr, lane, H, z[j]);
+    }
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    if (wpr > 1) {  // the same for the whole CTA
+        if (lane == 0) part[warp] = sum;
+        __syncthreads();
+        sum = lane < wpr ? part[first + lane] : 0.f;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    }
+    if (!live) return;
+    const float rstd = rsqrtf(sum / float(H) + p.eps);
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[j][i] = z[j][i] * rstd * w[j][i];
+        if (p.out) store8<VEC>(p.out + row * H, mine + j * wpr, lane, H, z[j]);
+        if (p.out8)
+            quantize8<VEC>(p.out8 + row * H, p.scale + row * ((H + NORM_GROUP - 1) / NORM_GROUP), mine + j * wpr, lane,
+                           H, z[j]);
+    }
+}
+
+template <bool VEC>
+void launch_norm(const NormParams& p, int per_warp, int grid, cudaStream_t st) {
+    const int threads = p.warps_per_row * p.rows_per_cta * 32;
+    if (per_warp == 1) mk_add_rmsnorm_kernel<VEC, 1><<<grid, threads, 0, st>>>(p);
+    else if (per_warp == 2) mk_add_rmsnorm_kernel<VEC, 2><<<grid, threads, 0, st>>>(p);
+    else mk_add_rmsnorm_kernel<VEC, 4><<<grid, threads, 0, st>>>(p);
+}
+
+}  // namespace
+}  // namespace mk
+
+using namespace mk;
+
+extern "C" mk_status_t mk_add_rmsnorm(const void* x, int64_t x_stride, const void* residual, int64_t residual_stride,
+                                      const void* weight, int T, int H, float eps, void* out, void* out8, float* scale,
+                                      void* residual_out, void* stream) {
+    if (T < 0 || H < 1) return MK_ERR_INVALID_ARG;
+    if (H > NORM_MAX_H) return MK_ERR_UNSUPPORTED;
+    if (!(eps >= 0.f) || std::isinf(eps)) return MK_ERR_INVALID_ARG;
+    if (T > 0) {
+        if (!x || !weight || (!out && !out8) || (out8 != nullptr) != (scale != nullptr)) return MK_ERR_INVALID_ARG;
+        if (residual_out && !residual) return MK_ERR_INVALID_ARG;
+        if (!host_aligned(x, 2) || !host_aligned(residual, 2) || !host_aligned(weight, 2) || !host_aligned(out, 2) ||
+            !host_aligned(residual_out, 2) || !host_aligned(scale, 4))
+            return MK_ERR_INVALID_ARG;
+        if (T > 1 && (x_stride < H || (residual && residual_stride < H))) return MK_ERR_INVALID_ARG;
+    }
+    int dev = 0, sms = 0;
+    const mk_status_t s = host_device(&dev, &sms);
+    if (s != MK_OK) return s;
+    if (T == 0) return MK_OK;
+
+    NormParams p{};
+    p.x = static_cast<const __nv_bfloat16*>(x);
+    p.residual = static_cast<const __nv_bfloat16*>(residual);
+    p.weight = static_cast<const __nv_bfloat16*>(weight);
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.residual_out = static_cast<__nv_bfloat16*>(residual_out);
+    p.out8 = static_cast<uint8_t*>(out8);
+    p.scale = scale;
+    p.x_stride = x_stride;
+    p.residual_stride = residual_stride;
+    p.T = T;
+    p.H = H;
+    p.eps = eps;
+    const bool vec = H % 8 == 0 && (T == 1 || (x_stride % 8 == 0 && (!residual || residual_stride % 8 == 0))) &&
+                     host_aligned(x, 16) && host_aligned(residual, 16) && host_aligned(weight, 16) &&
+                     host_aligned(out, 16) && host_aligned(residual_out, 16) && host_aligned(out8, 8);
+    const int chunks = (H + NORM_CHUNK - 1) / NORM_CHUNK;
+    const int per_warp = chunks > 2 * NORM_MAX_WARPS ? 4 : chunks > NORM_MAX_WARPS ? 2 : 1;
+    p.warps_per_row = (chunks + per_warp - 1) / per_warp;
+    p.rows_per_cta = p.warps_per_row >= 8 ? 1 : 8 / p.warps_per_row;
+    const int grid = int((int64_t(T) + p.rows_per_cta - 1) / p.rows_per_cta);
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    if (vec) launch_norm<true>(p, per_warp, grid, st);
+    else launch_norm<false>(p, per_warp, grid, st);
+    return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+}
