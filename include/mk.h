@@ -362,6 +362,40 @@ mk_status_t mk_paged_attention(const void* q, int64_t q_stride, const void* k_ca
 /* Workspace bytes mk_paged_attention needs (0 for invalid sizes). */
 size_t mk_paged_attention_workspace_size(int B, int Hq, int Hkv);
 
+/* Weight types of mk_moe_ffn_decode. */
+enum { MK_WEIGHT_BF16 = 0, MK_WEIGHT_E4M3 = 1 };
+
+/* The whole gated expert layer for a few tokens (a decode step), in one
+ * kernel: routing and gates as points 1 and 2 above, then
+ *   h(t,j) = silu(x[t,:] . W1[e]) * (x[t,:] . W3[e])  for the j-th expert e,
+ *   out[t,:] = sum_j gate[t,j] * (h(t,j) . W2[e]),  j in order.
+ * With MK_WEIGHT_BF16, x and the weights are bf16 and the scale pointers
+ * NULL; h is carried with 16 significant bits.  With MK_WEIGHT_E4M3 they are
+ * e4m3 with scales: a weight stands for its value times the scale of its
+ * 128 x 128 block, x[t,c] for its value times x_scale[t, c/128] (what
+ * mk_add_rmsnorm writes); h is rounded to e4m3 likewise, per row and 128
+ * columns with the scale max |h| / 448 (1 where that maximum is below
+ * 2^-100), before its product.
+ *   x[T,H], logits[T,E] f32, W1[E,H,F], W3[E,H,F], W2[E,F,H],
+ *   x_scale[T,H/128] f32, W1_scale[E,H/128,F/128] f32, W3_scale likewise,
+ *   W2_scale[E,F/128,H/128] f32                                   -- read only
+ *   out[T,H] bf16                                                 -- written
+ * Limits: 0 <= T <= 128, 1 <= k <= min(E, 8), E <= 256, H and F multiples of
+ * 64 (bf16) or 128 (e4m3) up to 32768; x, weights and out 16-byte aligned,
+ * f32 arrays 4.  Only the chosen experts' weights are read, each once.
+ * workspace: NULL (library cache) or mk_moe_ffn_decode_workspace_size()
+ * bytes, 256-byte aligned, zero-filled before its first use and used by this
+ * entry point only (with any sizes); one stream at a time.  The kernel's CTAs
+ * wait for one another within bounds (2 s; then MK_ERR_TIMEOUT from
+ * mk_get_status()). */
+mk_status_t mk_moe_ffn_decode(const void* x, const float* x_scale, const float* logits, int T, int H, int E, int k,
+                              const void* W1, const void* W3, const void* W2, const float* W1_scale,
+                              const float* W3_scale, const float* W2_scale, int F, int weights, void* out,
+                              void* stream, void* workspace, size_t ws_bytes);
+
+/* Workspace bytes mk_moe_ffn_decode needs (0 for invalid sizes). */
+size_t mk_moe_ffn_decode_workspace_size(int T, int H, int F, int E, int k, int weights);
+
 /* Synchronise `stream`, then return and clear the device error word
  * (MK_ERR_TIMEOUT / MK_ERR_DEVICE_FAULT), or MK_ERR_CUDA if the stream holds
  * a CUDA error.  MK_OK when nothing was recorded. */

@@ -39,6 +39,8 @@ MK_GATHER_AUTO = 0
 MK_GATHER_STAGED = 1
 MK_GATHER_DIRECT = 2
 MK_GATHER_GATHER4 = 3
+MK_WEIGHT_BF16 = 0
+MK_WEIGHT_E4M3 = 1
 
 # Entry points declared in include/mk.h (checked by the tests).
 ABI_FUNCTIONS = (
@@ -55,6 +57,8 @@ ABI_FUNCTIONS = (
     "mk_add_rmsnorm",
     "mk_paged_attention",
     "mk_paged_attention_workspace_size",
+    "mk_moe_ffn_decode",
+    "mk_moe_ffn_decode_workspace_size",
     "mk_workspace_size",
     "mk_get_status",
     "mk_last_error_detail",
@@ -156,6 +160,11 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     h.mk_paged_attention.restype = _i
     h.mk_paged_attention_workspace_size.argtypes = [_i, _i, _i]
     h.mk_paged_attention_workspace_size.restype = ctypes.c_size_t
+    h.mk_moe_ffn_decode.argtypes = [_p, _p, _p, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p, _i, _i, _p, _p, _p,
+                                    ctypes.c_size_t]
+    h.mk_moe_ffn_decode.restype = _i
+    h.mk_moe_ffn_decode_workspace_size.argtypes = [_i, _i, _i, _i, _i, _i]
+    h.mk_moe_ffn_decode_workspace_size.restype = ctypes.c_size_t
     h.mk_get_status.argtypes = [_p]
     h.mk_get_status.restype = _i
     h.mk_last_error_detail.argtypes = [ctypes.POINTER(ctypes.c_int32)] * 3
@@ -541,3 +550,51 @@ def paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale=None, stre
     if check:
         _check(mk_get_status(stream), "device status")
     return dict(out=out, lse=lse)
+
+
+def mk_moe_ffn_decode(x, x_scale, logits, T, H, E, k, W1, W3, W2, W1_scale, W3_scale, W2_scale, F, weights, out,
+                      stream=None, workspace=None, ws_bytes: int = 0) -> int:
+    return int(lib().mk_moe_ffn_decode(_ptr(x), _ptr(x_scale), _ptr(logits), T, H, E, k, _ptr(W1), _ptr(W3), _ptr(W2),
+                                       _ptr(W1_scale), _ptr(W3_scale), _ptr(W2_scale), F, weights, _ptr(out),
+                                       _stream(stream), _ptr(workspace), int(ws_bytes)))
+
+
+def mk_moe_ffn_decode_workspace_size(T, H, F, E, k, weights=MK_WEIGHT_BF16) -> int:
+    return int(lib().mk_moe_ffn_decode_workspace_size(T, H, F, E, k, weights))
+
+
+def moe_ffn_decode(x, logits, W1, W3, W2, k, x_scale=None, W1_scale=None, W3_scale=None, W2_scale=None, stream=None,
+                   workspace=None, ws_bytes=0, check=True):
+    """The whole gated expert layer for a few tokens on torch tensors: x[T,H],
+    logits[T,E] f32, W1 and W3 [E,H,F], W2 [E,F,H], all bf16, or all
+    float8_e4m3fn with ``x_scale`` [T,H/128] (as add_rmsnorm gives it) and a
+    weight scale per 128 x 128 block.  Returns ``out`` [T,H] bf16."""
+    import torch
+
+    dev = x.device
+    _need(x.dim() == 2 and x.is_cuda and W1.dim() == 3, "x must be a CUDA [T,H] tensor and W1 [E,H,F]")
+    T, H = x.shape
+    E, _, F = W1.shape
+    fp8 = x.dtype == torch.float8_e4m3fn
+    _need(fp8 or x.dtype == torch.bfloat16, "x must be bf16 or float8_e4m3fn")
+    for t, shape, what in ((x, (T, H), "x"), (W1, (E, H, F), "W1"), (W3, (E, H, F), "W3"), (W2, (E, F, H), "W2")):
+        _need(t.shape == shape and t.dtype == x.dtype and t.device == dev and t.is_contiguous(),
+              f"{what} must be a contiguous {shape} tensor of x's type on x's device")
+    need = [(logits, (T, E), "logits")]
+    if fp8:
+        h, f = H // 128, F // 128
+        need += [(x_scale, (T, h), "x_scale"), (W1_scale, (E, h, f), "W1_scale"), (W3_scale, (E, h, f), "W3_scale"),
+                 (W2_scale, (E, f, h), "W2_scale")]
+    else:
+        _need(x_scale is W1_scale is W3_scale is W2_scale is None, "scales belong to float8_e4m3fn weights")
+    for t, shape, what in need:
+        _need(t is not None and t.shape == shape and t.dtype == torch.float32 and t.device == dev
+              and t.is_contiguous(), f"{what} must be a contiguous f32 {shape} tensor on x's device")
+    out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+    st = mk_moe_ffn_decode(x, x_scale, logits, T, H, E, k, W1, W3, W2, W1_scale, W3_scale, W2_scale, F,
+                           MK_WEIGHT_E4M3 if fp8 else MK_WEIGHT_BF16, out, stream, workspace, ws_bytes)
+    _used_on(stream, out)
+    _check(st, "mk_moe_ffn_decode")
+    if check:
+        _check(mk_get_status(stream), "device status")
+    return dict(out=out)

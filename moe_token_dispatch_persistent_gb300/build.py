@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libmk.so")
-UNITS = ["mk_kernels.cu", "mk_api.cu", "mk_noalloc.cu", "mk_norm.cu", "mk_attn.cu"]
+UNITS = ["mk_kernels.cu", "mk_api.cu", "mk_noalloc.cu", "mk_norm.cu", "mk_attn.cu", "mk_ffn.cu"]
 
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

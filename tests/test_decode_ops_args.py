@@ -74,3 +74,42 @@ def test_paged_attention_binding_refuses_wrong_tensors():
     q, kv = torch.zeros((1, 8, 64), dtype=torch.bfloat16), torch.zeros((2, 16, 4, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         mk.paged_attention(q, kv, kv, torch.zeros((1, 2), dtype=torch.int32), torch.ones(1, dtype=torch.int32))
+
+
+FFN = dict(x=64, x_scale=None, logits=64, T=4, H=512, E=8, k=2, W1=64, W3=64, W2=64, W1_scale=None, W3_scale=None,
+           W2_scale=None, F=1024, weights=mk.MK_WEIGHT_BF16, out=64, stream=1)
+FFN8 = dict(FFN, x_scale=64, W1_scale=64, W3_scale=64, W2_scale=64, weights=mk.MK_WEIGHT_E4M3)
+
+
+@pytest.mark.parametrize("base", [FFN, FFN8], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("change,want", [
+    (dict(T=-1), BAD), (dict(T=129), UNSUPPORTED), (dict(k=0), BAD), (dict(k=9, E=16), BAD), (dict(E=1), BAD),
+    (dict(E=257), UNSUPPORTED), (dict(H=0), BAD), (dict(H=500), BAD), (dict(F=1000), BAD),
+    (dict(H=32768 + 128), UNSUPPORTED), (dict(F=32768 + 128), UNSUPPORTED), (dict(weights=2), BAD),
+    (dict(x=None), BAD), (dict(logits=None), BAD), (dict(W1=None), BAD), (dict(W3=None), BAD), (dict(W2=None), BAD),
+    (dict(out=None), BAD), (dict(x=72), BAD), (dict(W2=72), BAD), (dict(out=72), BAD), (dict(logits=66), BAD),
+])
+def test_moe_ffn_decode_refusals(base, change, want):
+    assert mk.mk_moe_ffn_decode(**{**base, **change}) == want
+
+
+@pytest.mark.parametrize("name", ["x_scale", "W1_scale", "W3_scale", "W2_scale"])
+def test_moe_ffn_decode_scales_belong_to_8_bits(name):
+    assert mk.mk_moe_ffn_decode(**{**FFN, name: 64}) == BAD
+    assert mk.mk_moe_ffn_decode(**{**FFN8, name: None}) == BAD
+    assert mk.mk_moe_ffn_decode(**{**FFN8, name: 66}) == BAD
+    assert mk.mk_moe_ffn_decode(**{**FFN8, "H": 576}) == BAD  # a multiple of 64 only
+
+
+def test_moe_ffn_decode_workspace_size():
+    a = mk.mk_moe_ffn_decode_workspace_size(1, 512, 1024, 8, 2)
+    assert 0 < a < mk.mk_moe_ffn_decode_workspace_size(128, 512, 1024, 8, 2)
+    assert mk.mk_moe_ffn_decode_workspace_size(129, 512, 1024, 8, 2) == 0
+    assert mk.mk_moe_ffn_decode_workspace_size(1, 576, 1024, 8, 2, mk.MK_WEIGHT_E4M3) == 0
+
+
+def test_moe_ffn_decode_binding_refuses_wrong_tensors():
+    torch = pytest.importorskip("torch")
+    x, w = torch.zeros((2, 64), dtype=torch.bfloat16), torch.zeros((4, 64, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        mk.moe_ffn_decode(x, torch.zeros((2, 4)), w, w, w, 2)
