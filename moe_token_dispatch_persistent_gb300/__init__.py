@@ -443,19 +443,36 @@ def mk_add_rmsnorm(x, x_stride, residual, residual_stride, weight, T, H, eps, ou
                                     _ptr(out), _ptr(out8), _ptr(scale), _ptr(residual_out), _stream(stream)))
 
 
-def _need(ok, what: str):
-    if not ok:
-        raise ValueError(what)
+# The tensor forms below are called once per layer and token, so they do
+# little: checks without temporaries, the raw stream handle, one allocation
+# per output, and the C entry (on the host of a GB300 torch.cuda.current_stream
+# alone takes 2.9 us, the raw handle 0.1).
+
+_torch = None
+_raw_stream = None
 
 
-def _used_on(stream, *tensors):
-    """Tell torch's allocator that a torch stream other than the current one
-    uses tensors allocated here, so that their memory is not handed out while
-    it still does."""
-    if hasattr(stream, "cuda_stream"):
-        for t in tensors:
+def _load_torch():
+    global _torch, _raw_stream
+    import torch
+
+    _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+        lambda device: torch.cuda.current_stream(device).cuda_stream)
+    _torch = torch
+    return torch
+
+
+def _finish(status, what, stream, check, *outputs):
+    """Errors of a call, and the outputs' use of a torch stream that is not the
+    current one: the allocator must not hand their memory out while it runs."""
+    if stream is not None and hasattr(stream, "cuda_stream"):
+        for t in outputs:
             if t is not None:
                 t.record_stream(stream)
+    if status != MK_OK:
+        raise MkError(status, what)
+    if check:
+        _check(mk_get_status(stream), "device status")
 
 
 def add_rmsnorm(x, weight, residual=None, eps=1e-6, bf16=True, e4m3=False, residual_out=None, stream=None, check=True):
@@ -467,37 +484,45 @@ def add_rmsnorm(x, weight, residual=None, eps=1e-6, bf16=True, e4m3=False, resid
     and with a residual the new stream ``residual`` (in ``residual_out`` when
     given, which may be the residual itself).
     """
-    import torch
-
-    b16, dev = torch.bfloat16, x.device
-    _need(x.dim() == 2 and x.dtype == b16 and x.is_cuda and (x.stride(1) == 1 or x.shape[1] == 1),
-          "x must be a CUDA bf16 [T,H] tensor with contiguous rows")
+    torch = _torch or _load_torch()
+    b16 = torch.bfloat16
     T, H = x.shape
-    _need(weight.shape == (H,) and weight.dtype == b16 and weight.device == dev and weight.is_contiguous(),
-          "weight must be bf16 [H] on x's device")
-    _need(bf16 or e4m3, "no output asked for")
+    dev = x.get_device()
+    if dev < 0 or x.dtype is not b16 or (x.stride(1) != 1 and H != 1):
+        raise ValueError("x must be a CUDA bf16 [T,H] tensor with contiguous rows")
+    if weight.dtype is not b16 or weight.get_device() != dev or weight.shape != (H,) or not weight.is_contiguous():
+        raise ValueError("weight must be bf16 [H] on x's device")
+    empty = torch.empty
+    device = x.device
     o = {}
+    out = out8 = scale = p_out = p_out8 = p_scale = p_res = p_new = None
     if bf16:
-        o["out"] = torch.empty((T, H), dtype=b16, device=dev)
+        o["out"] = out = empty((T, H), dtype=b16, device=device)
+        p_out = out.data_ptr()
     if e4m3:
-        o["out8"] = torch.empty((T, H), dtype=torch.float8_e4m3fn, device=dev)
-        o["scale"] = torch.empty((T, -(-H // 128)), dtype=torch.float32, device=dev)
+        o["out8"] = out8 = empty((T, H), dtype=torch.float8_e4m3fn, device=device)
+        o["scale"] = scale = empty((T, -(-H // 128)), dtype=torch.float32, device=device)
+        p_out8, p_scale = out8.data_ptr(), scale.data_ptr()
+    elif not bf16:
+        raise ValueError("no output asked for")
+    r_stride = 0
     if residual is not None:
-        _need(residual.shape == (T, H) and residual.dtype == b16 and residual.device == dev
-              and (residual.stride(1) == 1 or H == 1), "residual must be bf16 [T,H] with contiguous rows on x's device")
+        if (residual.dtype is not b16 or residual.get_device() != dev or residual.shape != (T, H)
+                or (residual.stride(1) != 1 and H != 1)):
+            raise ValueError("residual must be bf16 [T,H] with contiguous rows on x's device")
         if residual_out is None:
-            residual_out = torch.empty((T, H), dtype=b16, device=dev)
-        _need(residual_out.shape == (T, H) and residual_out.dtype == b16 and residual_out.device == dev
-              and residual_out.is_contiguous(), "residual_out must be contiguous bf16 [T,H] on x's device")
+            residual_out = empty((T, H), dtype=b16, device=device)
+        elif (residual_out.dtype is not b16 or residual_out.get_device() != dev or residual_out.shape != (T, H)
+              or not residual_out.is_contiguous()):
+            raise ValueError("residual_out must be contiguous bf16 [T,H] on x's device")
         o["residual"] = residual_out
-    else:
-        _need(residual_out is None, "residual_out needs a residual")
-    st = mk_add_rmsnorm(x, x.stride(0), residual, residual.stride(0) if residual is not None else 0, weight, T, H, eps,
-                        o.get("out"), o.get("out8"), o.get("scale"), o.get("residual"), stream)
-    _used_on(stream, *o.values())
-    _check(st, "mk_add_rmsnorm")
-    if check:
-        _check(mk_get_status(stream), "device status")
+        r_stride, p_res, p_new = residual.stride(0), residual.data_ptr(), residual_out.data_ptr()
+    elif residual_out is not None:
+        raise ValueError("residual_out needs a residual")
+    status = lib().mk_add_rmsnorm(x.data_ptr(), x.stride(0), p_res, r_stride, weight.data_ptr(), T, H, eps, p_out, p_out8,
+                                  p_scale, p_new, _raw_stream(dev) if stream is None else _stream(stream))
+    if status or check or stream is not None:
+        _finish(status, "mk_add_rmsnorm", stream, check, out, out8, scale, residual_out)
     return o
 
 
@@ -524,32 +549,39 @@ def paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale=None, stre
     ``scale`` defaults to D ** -0.5.  Returns ``out`` [B,Hq,D] bf16 and
     ``lse`` [B,Hq] f32.
     """
-    import torch
-
-    b16, i32, dev = torch.bfloat16, torch.int32, q.device
-    _need(q.dim() == 3 and q.dtype == b16 and q.is_cuda, "q must be a CUDA bf16 [B,Hq,D] tensor")
+    torch = _torch or _load_torch()
+    b16, i32 = torch.bfloat16, torch.int32
     B, Hq, D = q.shape
-    _need(q.stride(2) == 1 and (Hq == 1 or q.stride(1) == D), "the heads of a sequence's q must be contiguous")
-    for t in (k_cache, v_cache):
-        _need(t.dim() == 4 and t.dtype == b16 and t.device == dev and t.shape[3] == D and t.stride(3) == 1,
-              "caches must be bf16 [pages, page_size, Hkv, D] on q's device, D contiguous")
-    _need(k_cache.shape == v_cache.shape and k_cache.stride() == v_cache.stride(),
-          "k_cache and v_cache must agree in shape and strides")
-    pages, page_size, Hkv, _ = k_cache.shape
-    _need(block_table.dim() == 2 and block_table.shape[0] == B and block_table.dtype == i32
-          and block_table.device == dev and block_table.is_contiguous(), "block_table must be i32 [B,max_pages]")
-    _need(seq_lens.shape == (B,) and seq_lens.dtype == i32 and seq_lens.device == dev and seq_lens.is_contiguous(),
-          "seq_lens must be i32 [B]")
-    out = torch.empty((B, Hq, D), dtype=b16, device=dev)
-    lse = torch.empty((B, Hq), dtype=torch.float32, device=dev)
-    st = mk_paged_attention(q, q.stride(0), k_cache, v_cache, *k_cache.stride()[:3], block_table, seq_lens, B, Hq, Hkv,
-                            D, page_size, block_table.shape[1], pages, D ** -0.5 if scale is None else scale, out, lse,
-                            stream, workspace, ws_bytes)
-    _used_on(stream, out, lse)
-    _check(st, "mk_paged_attention")
-    if check:
-        _check(mk_get_status(stream), "device status")
-    return dict(out=out, lse=lse)
+    dev = q.get_device()
+    if dev < 0 or q.dtype is not b16:
+        raise ValueError("q must be a CUDA bf16 [B,Hq,D] tensor")
+    q_stride, q_head, q_last = q.stride()
+    if q_last != 1 or (q_head != D and Hq != 1):
+        raise ValueError("the heads of a sequence's q must be contiguous")
+    pages, page_size, Hkv, kd = shape = k_cache.shape
+    page, token, head, last = strides = k_cache.stride()
+    if (kd != D or last != 1 or k_cache.dtype is not b16 or v_cache.dtype is not b16 or k_cache.get_device() != dev
+            or v_cache.get_device() != dev):
+        raise ValueError("caches must be bf16 [pages, page_size, Hkv, D] on q's device, D contiguous")
+    if v_cache.shape != shape or v_cache.stride() != strides:
+        raise ValueError("k_cache and v_cache must agree in shape and strides")
+    rows, max_pages = block_table.shape
+    if rows != B or block_table.dtype is not i32 or block_table.get_device() != dev or not block_table.is_contiguous():
+        raise ValueError("block_table must be i32 [B,max_pages]")
+    if (seq_lens.shape != (B,) or seq_lens.dtype is not i32 or seq_lens.get_device() != dev
+            or not seq_lens.is_contiguous()):
+        raise ValueError("seq_lens must be i32 [B]")
+    device = q.device
+    out = torch.empty((B, Hq, D), dtype=b16, device=device)
+    lse = torch.empty((B, Hq), dtype=torch.float32, device=device)
+    status = lib().mk_paged_attention(
+        q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(), page, token, head, block_table.data_ptr(),
+        seq_lens.data_ptr(), B, Hq, Hkv, D, page_size, max_pages, pages, D ** -0.5 if scale is None else scale,
+        out.data_ptr(), lse.data_ptr(), _raw_stream(dev) if stream is None else _stream(stream), _ptr(workspace),
+        ws_bytes)
+    if status or check or stream is not None:
+        _finish(status, "mk_paged_attention", stream, check, out, lse)
+    return {"out": out, "lse": lse}
 
 
 def mk_moe_ffn_decode(x, x_scale, logits, T, H, E, k, W1, W3, W2, W1_scale, W3_scale, W2_scale, F, weights, out,
@@ -569,32 +601,37 @@ def moe_ffn_decode(x, logits, W1, W3, W2, k, x_scale=None, W1_scale=None, W3_sca
     logits[T,E] f32, W1 and W3 [E,H,F], W2 [E,F,H], all bf16, or all
     float8_e4m3fn with ``x_scale`` [T,H/128] (as add_rmsnorm gives it) and a
     weight scale per 128 x 128 block.  Returns ``out`` [T,H] bf16."""
-    import torch
-
-    dev = x.device
-    _need(x.dim() == 2 and x.is_cuda and W1.dim() == 3, "x must be a CUDA [T,H] tensor and W1 [E,H,F]")
+    torch = _torch or _load_torch()
     T, H = x.shape
     E, _, F = W1.shape
-    fp8 = x.dtype == torch.float8_e4m3fn
-    _need(fp8 or x.dtype == torch.bfloat16, "x must be bf16 or float8_e4m3fn")
-    for t, shape, what in ((x, (T, H), "x"), (W1, (E, H, F), "W1"), (W3, (E, H, F), "W3"), (W2, (E, F, H), "W2")):
-        _need(t.shape == shape and t.dtype == x.dtype and t.device == dev and t.is_contiguous(),
-              f"{what} must be a contiguous {shape} tensor of x's type on x's device")
-    need = [(logits, (T, E), "logits")]
+    dev, dtype = x.get_device(), x.dtype
+    fp8 = dtype is torch.float8_e4m3fn
+    if dev < 0 or not (fp8 or dtype is torch.bfloat16):
+        raise ValueError("x must be a CUDA bf16 or float8_e4m3fn [T,H] tensor")
+    up = (E, H, F)
+    if W1.shape != up or W3.shape != up or W2.shape != (E, F, H):
+        raise ValueError("W1 and W3 must be [E,H,F] and W2 [E,F,H]")
+    for t in (x, W1, W3, W2):
+        if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+            raise ValueError("x and the weights must be contiguous, of one type and on one device")
+    scales = (x_scale, W1_scale, W3_scale, W2_scale)
+    need = ((logits, (T, E)),)
     if fp8:
         h, f = H // 128, F // 128
-        need += [(x_scale, (T, h), "x_scale"), (W1_scale, (E, h, f), "W1_scale"), (W3_scale, (E, h, f), "W3_scale"),
-                 (W2_scale, (E, f, h), "W2_scale")]
-    else:
-        _need(x_scale is W1_scale is W3_scale is W2_scale is None, "scales belong to float8_e4m3fn weights")
-    for t, shape, what in need:
-        _need(t is not None and t.shape == shape and t.dtype == torch.float32 and t.device == dev
-              and t.is_contiguous(), f"{what} must be a contiguous f32 {shape} tensor on x's device")
-    out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
-    st = mk_moe_ffn_decode(x, x_scale, logits, T, H, E, k, W1, W3, W2, W1_scale, W3_scale, W2_scale, F,
-                           MK_WEIGHT_E4M3 if fp8 else MK_WEIGHT_BF16, out, stream, workspace, ws_bytes)
-    _used_on(stream, out)
-    _check(st, "mk_moe_ffn_decode")
-    if check:
-        _check(mk_get_status(stream), "device status")
-    return dict(out=out)
+        need = (need[0], (x_scale, (T, h)), (W1_scale, (E, h, f)), (W3_scale, (E, h, f)), (W2_scale, (E, f, h)))
+    elif scales != (None, None, None, None):
+        raise ValueError("scales belong to float8_e4m3fn weights")
+    f32 = torch.float32
+    for t, shape in need:
+        if t is None or t.shape != shape or t.dtype is not f32 or t.get_device() != dev or not t.is_contiguous():
+            raise ValueError("logits [T,E], x_scale [T,H/128] and the weights' scales (a value per 128 x 128 block) "
+                             "must be contiguous f32 on x's device")
+    out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    status = lib().mk_moe_ffn_decode(
+        x.data_ptr(), x_scale.data_ptr() if fp8 else None, logits.data_ptr(), T, H, E, k, W1.data_ptr(), W3.data_ptr(),
+        W2.data_ptr(), *([t.data_ptr() for t in scales[1:]] if fp8 else (None, None, None)), F,
+        MK_WEIGHT_E4M3 if fp8 else MK_WEIGHT_BF16, out.data_ptr(),
+        _raw_stream(dev) if stream is None else _stream(stream), _ptr(workspace), ws_bytes)
+    if status or check or stream is not None:
+        _finish(status, "mk_moe_ffn_decode", stream, check, out)
+    return {"out": out}

@@ -49,6 +49,7 @@ struct DevInfo {
     mk_status_t status = MK_OK;
     int sms = 0;
     int max_blocks = 0;
+    DevError* err = nullptr;
 };
 
 std::mutex g_mu;
@@ -94,7 +95,9 @@ mk_status_t device_info(int* dev_out, DevInfo** info) {
         }
         if (major != 10 || minor != 3) {
             d.status = MK_ERR_UNSUPPORTED;
-        } else if (set_kernel_attributes() != cudaSuccess || fused_max_blocks_per_sm(&d.max_blocks) != cudaSuccess) {
+        } else if (set_kernel_attributes() != cudaSuccess || attn_kernel_attributes() != cudaSuccess ||
+                   ffn_kernel_attributes() != cudaSuccess || error_word(&d.err) != cudaSuccess ||
+                   fused_max_blocks_per_sm(&d.max_blocks) != cudaSuccess) {
             return MK_ERR_CUDA;
         } else if (d.max_blocks < 1) {
             d.status = MK_ERR_UNSUPPORTED;
@@ -254,11 +257,13 @@ mk_status_t cached_workspace(int dev, cudaStream_t st, size_t need, size_t zero_
 
 namespace mk {
 
-mk_status_t host_device(int* dev, int* sms) {
+mk_status_t host_device(int* dev, int* sms, DevError** err) {
     DevInfo* d = nullptr;
     const mk_status_t s = device_info(dev, &d);
-    if (s == MK_OK) *sms = d->sms;
-    return s;
+    if (s != MK_OK) return s;
+    *sms = d->sms;
+    *err = d->err;
+    return MK_OK;
 }
 
 mk_status_t host_workspace(WsKind kind, int dev, cudaStream_t st, size_t need, size_t zero_bytes, void** out) {

@@ -16,8 +16,8 @@
 // sharing it joins them, in the order of the keys.  The caller's lengths stay
 // on the device: every CTA builds the table of tiles itself.
 //
-// Inside a CTA the warps take every WARPS-th tile of a range and never wait
-// for one another: each has its own ring of tiles in shared memory, filled by
+// Inside a CTA the warps take every WARPS-th tile of a range (short groups go
+// to one warp each) and wait for one another only at a range's end: each has its own ring of tiles in shared memory, filled by
 // its own 16-byte asynchronous copies (any page size, any stride, keys past
 // the end filled with zeros), which run ahead across the ends of ranges.  The
 // heads are the rows of m16n8k16 products (a decode step has at most 16 rows
@@ -163,13 +163,39 @@ __device__ __forceinline__ bool next_range(uint32_t& pos, uint32_t end, const ui
     return true;
 }
 
-__device__ __forceinline__ uint32_t range_start(uint32_t total, uint32_t c, uint32_t n) {
-    return uint32_t(uint64_t(total) * c / n);
-}
-// The CTA whose range holds position p.
-__device__ __forceinline__ uint32_t range_owner(uint32_t total, uint32_t p, uint32_t n) {
-    return uint32_t((uint64_t(p + 1) * n - 1) / total);
-}
+// `total` positions cut into n ranges that differ by one position at most:
+// the first `more` of them hold `each` + 1.
+struct Cut {
+    uint32_t each, more;
+    __device__ Cut(uint32_t total, uint32_t n) : each(total / n), more(total - (total / n) * n) {}
+    __device__ uint32_t start(uint32_t c) const { return c * each + min(c, more); }
+    __device__ uint32_t owner(uint32_t p) const {
+        const uint32_t in_more = more * (each + 1);
+        return p < in_more ? p / (each + 1) : more + (p - in_more) / each;
+    }
+};
+
+// The ranges of a CTA as one of its warps sees them: groups that lie whole in
+// the CTA and have at most `small` tiles go to one warp each, in turn (their
+// results need no join); all warps share every other range.
+struct Walk {
+    uint32_t pos, end, small, turn;
+    const uint32_t* prefix;
+    int B, warp, warps;
+    uint32_t groups;
+    __device__ bool next(Range& r, bool& alone) {
+        while (next_range(pos, end, prefix, B, groups, r)) {
+            alone = r.t1 - r.t0 == r.tiles && r.tiles <= small;
+            if (!alone) return true;
+            if (int(turn) == warp) {
+                turn = turn + 1 == uint32_t(warps) ? 0u : turn + 1;
+                return true;
+            }
+            turn = turn + 1 == uint32_t(warps) ? 0u : turn + 1;
+        }
+        return false;
+    }
+};
 
 // Element offset of one key's row of a tile (row = lane for lanes 0-15), or
 // -1 when the key lies past the sequence.
@@ -243,25 +269,30 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
     // at least one tile per warp: a shorter range would only add partial results to join
     const uint32_t nctas = min(gridDim.x, (total + G::WARPS - 1) / G::WARPS);
     if (blockIdx.x >= nctas) return;
-    const uint32_t start = range_start(total, blockIdx.x, nctas), end = range_start(total, blockIdx.x + 1, nctas);
+    const Cut cut_at(total, nctas);
+    const uint32_t start = cut_at.start(blockIdx.x), end = cut_at.start(blockIdx.x + 1);
+    // A warp alone with a group takes its tiles one after the other; up to half
+    // of a warp's share of the range that evens out between the warps.
+    const uint32_t small_tiles = max(1u, (end - start) / (2 * G::WARPS));
 
     // ---- this warp's ring: loads run STAGES tiles ahead, across ranges
     const uint32_t ring = smem_u32(smem) + uint32_t(warp) * G::RING;
-    uint32_t load_pos = start, load_tile = 0;
+    Walk load_walk{start, end, small_tiles, 0u, prefix, p.B, warp, G::WARPS, groups};
+    uint32_t load_tile = 0;
     Range lr;
     int load_len = 0;
-    bool loading = true;
+    bool loading = true, load_alone = false;
     lr.t1 = 0;
     int64_t ahead = -1;  // row offset of the next tile to load
     auto seek = [&](uint32_t t) {
         load_tile = t;
         while (load_tile >= lr.t1) {
-            if (!next_range(load_pos, end, prefix, p.B, groups, lr)) {
+            if (!load_walk.next(lr, load_alone)) {
                 loading = false;
                 return;
             }
             load_len = length(lr.b);
-            load_tile = lr.t0 + uint32_t(warp);
+            load_tile = lr.t0 + (load_alone ? 0u : uint32_t(warp));
         }
         // the page is looked up one tile before its rows are copied
         ahead = key_offset(p, lr.b, lr.g / p.chunks, load_tile, lane, load_len);
@@ -282,7 +313,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
                 copy16(d, p.k + at, ok);
                 copy16(d + G::HALF, p.v + at, ok);
             }
-            seek(load_tile + G::WARPS);
+            seek(load_tile + (load_alone ? 1u : uint32_t(G::WARPS)));
         }
         copy_commit();
         if (++load_slot == G::STAGES) load_slot = 0;
@@ -291,10 +322,11 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
     for (int i = 0; i < G::STAGES; ++i) issue();
 
     const int r0 = lane >> 2, r1 = r0 + 8;  // this lane's rows (heads) of the products
-    uint32_t slot = 0, pos = start;
+    uint32_t slot = 0;
+    Walk walk{start, end, small_tiles, 0u, prefix, p.B, warp, G::WARPS, groups};
     Range r;
-    bool first = true;
-    while (next_range(pos, end, prefix, p.B, groups, r)) {
+    bool alone = false;
+    while (walk.next(r, alone)) {
         const int kv = r.g / p.chunks, head0 = kv * p.per_kv + (r.g % p.chunks) * ROWS;
         const int heads = min(ROWS, (kv + 1) * p.per_kv - head0);
         const int len = length(r.b);
@@ -319,7 +351,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
             for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
         float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
 
-        for (uint32_t t = r.t0 + warp; t < r.t1; t += G::WARPS) {
+        const uint32_t step = alone ? 1u : uint32_t(G::WARPS);
+        for (uint32_t t = r.t0 + (alone ? 0u : uint32_t(warp)); t < r.t1; t += step) {
             copy_wait<G::STAGES - 1>();
             __syncwarp();
             const uint32_t ks = ring + slot * (2 * G::HALF), vs = ks + G::HALF;
@@ -405,11 +438,29 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
             if (++slot == G::STAGES) slot = 0;
         }
 
-        // ---- join the warps' results of the range
         l0 += __shfl_xor_sync(0xffffffffu, l0, 1);
         l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
         l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
         l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
+        if (alone) {
+            // the whole group by this warp: straight to the output
+            const float i0 = l0 == 0.f ? 0.f : 1.f / l0, i1 = l1 == 0.f ? 0.f : 1.f / l1;
+            const int64_t at = int64_t(r.b) * p.Hq + head0;
+            uint32_t* w0 = reinterpret_cast<uint32_t*>(p.out + (at + r0) * D) + (lane & 3);
+            uint32_t* w1 = reinterpret_cast<uint32_t*>(p.out + (at + r1) * D) + (lane & 3);
+#pragma unroll
+            for (int n = 0; n < D / 8; ++n) {
+                if (r0 < heads) w0[n * 4] = pack_bf16(o[n][0] * i0, o[n][1] * i0);
+                if (r1 < heads) w1[n * 4] = pack_bf16(o[n][2] * i1, o[n][3] * i1);
+            }
+            if (p.lse && (lane & 3) == 0) {
+                if (r0 < heads) p.lse[at + r0] = l0 == 0.f ? -INFINITY : (m0 + log2f(l0)) * LN2;
+                if (r1 < heads) p.lse[at + r1] = l1 == 0.f ? -INFINITY : (m1 + log2f(l1)) * LN2;
+            }
+            continue;
+        }
+
+        // ---- join the warps' results of the range
         const int nw = int(min(uint32_t(G::WARPS), r.t1 - r.t0));  // warps that had a tile
         if (warp < nw) {
             if ((lane & 3) == 0) {
@@ -427,7 +478,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
         }
         __syncthreads();
         const bool whole = r.t1 - r.t0 == r.tiles;
-        float* mine = p.slots + size_t(2 * blockIdx.x + (first ? 0 : 1)) * (ATTN_SLOT_BYTES / 4);
+        // a CTA's first partial range takes its first slot, its last one the second
+        float* mine = p.slots + size_t(2 * blockIdx.x + (start >= r.begin ? 0 : 1)) * (ATTN_SLOT_BYTES / 4);
         for (int i = tid; i < heads * (D / 4); i += G::THREADS) {
             const int row = i / (D / 4), c = (i % (D / 4)) * 4;
             float top = -INFINITY;
@@ -461,7 +513,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
         if (!whole) {
             // ---- the CTA that completes the group joins its partial results
             uint32_t* flag = small;
-            const uint32_t c0 = range_owner(total, r.begin, nctas), c1 = range_owner(total, r.begin + r.tiles - 1, nctas);
+            const uint32_t c0 = cut_at.owner(r.begin), c1 = cut_at.owner(r.begin + r.tiles - 1);
             const int n = int(c1 - c0) + 1;
             __threadfence();
             __syncthreads();
@@ -478,7 +530,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
                 // one row, the pieces dealt out over as many threads as there are
                 auto piece = [&](int i) -> const float* {
                     const uint32_t c = c0 + uint32_t(i);
-                    const uint32_t which = range_start(total, c, nctas) >= r.begin ? 0u : 1u;
+                    const uint32_t which = cut_at.start(c) >= r.begin ? 0u : 1u;
                     return p.slots + size_t(2 * c + which) * (ATTN_SLOT_BYTES / 4);
                 };
                 float* sw = sO;                  // [n][heads] weights
@@ -547,17 +599,12 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
             }
         }
         __syncthreads();  // the join buffer is free for the next range
-        first = false;
     }
     copy_wait<0>();
 }
 
 template <int D>
 cudaError_t launch_attn(const AttnParams& p, int grid, cudaStream_t st) {
-    // set on every call: a device reset would forget it
-    cudaError_t e = cudaFuncSetAttribute(mk_paged_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         Geo<D>::SMEM);
-    if (e != cudaSuccess) return e;
     mk_paged_attention_kernel<D><<<grid, Geo<D>::THREADS, Geo<D>::SMEM, st>>>(p);
     return cudaGetLastError();
 }
@@ -568,7 +615,20 @@ int64_t attn_groups(int B, int Hq, int Hkv) {
     return int64_t(Hkv) * ((Hq / Hkv + ROWS - 1) / ROWS);
 }
 
+template <int D>
+cudaError_t attn_smem() {
+    return cudaFuncSetAttribute(mk_paged_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Geo<D>::SMEM);
+}
+
 }  // namespace
+
+cudaError_t attn_kernel_attributes() {
+    cudaError_t e;
+    if ((e = attn_smem<64>()) != cudaSuccess || (e = attn_smem<128>()) != cudaSuccess) return e;
+    return attn_smem<256>();
+}
+
 }  // namespace mk
 
 using namespace mk;
@@ -608,7 +668,8 @@ extern "C" mk_status_t mk_paged_attention(const void* q, int64_t q_stride, const
             if (v < 0 || v % 8 != 0) return MK_ERR_INVALID_ARG;
     }
     int dev = 0, sms = 0;
-    mk_status_t s = host_device(&dev, &sms);
+    DevError* err = nullptr;
+    mk_status_t s = host_device(&dev, &sms, &err);
     if (s != MK_OK) return s;
     if (B == 0) return MK_OK;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -631,7 +692,7 @@ extern "C" mk_status_t mk_paged_attention(const void* q, int64_t q_stride, const
     p.lse = lse;
     p.slots = reinterpret_cast<float*>(ws);
     p.arrived = reinterpret_cast<uint32_t*>(ws + ATTN_SLOTS_BYTES);
-    if (error_word(&p.err) != cudaSuccess) return MK_ERR_CUDA;
+    p.err = err;
     p.q_stride = q_stride;
     p.page_stride = page_stride;
     p.token_stride = token_stride;

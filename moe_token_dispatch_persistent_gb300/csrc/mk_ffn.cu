@@ -69,6 +69,12 @@ constexpr int GROUP8 = 128;        // rows and columns of an 8-bit scale block
 constexpr int FFN_MAX_STAGES = 6;
 constexpr int FFN_MAX_BUFS = 8;
 constexpr int RING_BYTES = FFN_MAX_STAGES * (STEP_BYTES + 16 * 128 * 2);  // six stages at up to 16 rows an expert
+// 8 bits: the scales of a step (up to 128 rows, then the two weight blocks) in
+// a ring of their own at the end, longer than the stages and accumulator
+// buffers that lie between their load and their use.
+constexpr int SCALE_SLOTS = 16, SCALE_FLOATS = FFN_MAX_T + 4;
+constexpr int SCALE_AT = RING_BYTES - SCALE_SLOTS * SCALE_FLOATS * 4;
+static_assert(SCALE_SLOTS >= FFN_MAX_STAGES + FFN_MAX_BUFS && SCALE_AT % 16 == 0, "scale ring");
 constexpr int MAX_TILES1 = MAX_E * (32768 / 128);
 constexpr int SLOTS = 5;           // per CTA: h pieces (first, last range; whole tile), output pieces (first, last)
 constexpr long long FFN_SPIN_NS = 2000000000LL;
@@ -110,6 +116,7 @@ struct FfnMaps {
 struct FfnSmem {
     uint64_t weights_in[FFN_MAX_STAGES], rows_in[FFN_MAX_STAGES], empty[FFN_MAX_STAGES];
     uint64_t acc_full[FFN_MAX_BUFS], acc_empty[FFN_MAX_BUFS];
+    uint64_t scales_in[SCALE_SLOTS], scales_out[SCALE_SLOTS];
     uint64_t drain;
     uint32_t tmem_base;
     int ok, last, chosen, most;  // most: rows of the busiest expert
@@ -134,8 +141,12 @@ struct Half {
     uint32_t ks;      // steps per tile
     uint32_t blocks;  // tiles per expert
     uint32_t total, ctas, start, end;
-    __device__ uint32_t first_step(uint32_t c) const { return uint32_t(uint64_t(total) * c / ctas); }
-    __device__ uint32_t owner(uint32_t step) const { return uint32_t((uint64_t(step + 1) * ctas - 1) / total); }
+    uint32_t each, more;  // steps per CTA; the first `more` CTAs take one more
+    __device__ uint32_t first_step(uint32_t c) const { return c * each + min(c, more); }
+    __device__ uint32_t owner(uint32_t step) const {
+        const uint32_t in_more = more * (each + 1);
+        return step < in_more ? step / (each + 1) : more + (step - in_more) / each;
+    }
 };
 
 __device__ __forceinline__ Half make_half(uint32_t ks, uint32_t blocks, uint32_t experts) {
@@ -144,6 +155,8 @@ __device__ __forceinline__ Half make_half(uint32_t ks, uint32_t blocks, uint32_t
     h.blocks = blocks;
     h.total = ks * blocks * experts;
     h.ctas = min(gridDim.x, h.total);  // every CTA that takes part has a step
+    h.each = h.total / h.ctas;
+    h.more = h.total - h.each * h.ctas;
     const bool in = blockIdx.x < h.ctas;
     h.start = in ? h.first_step(blockIdx.x) : 0u;
     h.end = in ? h.first_step(blockIdx.x + 1) : 0u;
@@ -372,14 +385,22 @@ __device__ void weight_loads(const FfnParams& p, const FfnMaps& m, FfnSmem* sm, 
     }
 }
 
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const float* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+
 template <bool FP8>
 __device__ void row_loads(const FfnParams& p, const FfnMaps& m, FfnSmem* sm, const Ring& rg, const Half (&half)[2],
                           const Waiter& w) {
     constexpr int KB = FP8 ? 128 : 64;
     const int lane = threadIdx.x & 31;
     uint8_t* ring = ffn_ring();
-    Turn st;
+    Turn st, sc;
     Issued mine;
+    auto leave = [&]() {
+        if (FP8) cp_async_wait_all();
+        mine.settle(sm->rows_in);
+    };
     for (int ph = 0; ph < 2; ++ph) {
         uint32_t pos = half[ph].start;
         Piece s;
@@ -390,7 +411,7 @@ __device__ void row_loads(const FfnParams& p, const FfnMaps& m, FfnSmem* sm, con
             if (ph == 1 && s.a != known) {
                 const bool in = await_geq(&p.ctl->ready[s.a], half[0].blocks, w, SITE_TILE_READY);
                 if (!__all_sync(0xffffffffu, in)) {
-                    mine.settle(sm->rows_in);
+                    leave();
                     return;
                 }
                 fence_proxy_async();  // the other CTAs' stores to h before the loads below
@@ -402,9 +423,23 @@ __device__ void row_loads(const FfnParams& p, const FfnMaps& m, FfnSmem* sm, con
                 const int i = off + min(4 * lane + q, n - 1);  // rows past the last repeat it; never stored
                 r[q] = ph == 0 ? sm->row_token[i] : i;
             }
+            // 8 bits: scales of this lane's rows lane, lane + 32, ... and of the two weight blocks
+            const int KB8 = (ph == 0 ? p.H : p.F) / GROUP8, NB8 = (ph == 0 ? p.F : p.H) / GROUP8;
+            const float* sx[FFN_MAX_T / 32];
+            const float* sw = nullptr;
+            if constexpr (FP8) {
+#pragma unroll
+                for (int q = 0; q < FFN_MAX_T / 32; ++q) {
+                    const int i = off + min(lane + 32 * q, n - 1);
+                    sx[q] = ph == 0 ? p.x_scale + size_t(sm->row_token[i]) * KB8 : p.h_scale + size_t(i) * KB8;
+                }
+                const size_t block = size_t(sm->expert[s.a]) * KB8 * NB8;
+                if (ph == 0) sw = (lane == 0 ? p.w1_scale : p.w3_scale) + block + s.blk;
+                else sw = p.w2_scale + block + min(2 * s.blk + (lane & 1), NB8 - 1);
+            }
             for (uint32_t k = s.k0; k < s.k1; ++k) {
                 if (!warp_await_mbar(&sm->empty[st.i], st.phase ^ 1u, w, SITE_STAGE_EMPTY)) {
-                    mine.settle(sm->rows_in);
+                    leave();
                     return;
                 }
                 uint64_t* fb = &sm->rows_in[st.i];
@@ -419,6 +454,19 @@ __device__ void row_loads(const FfnParams& p, const FfnMaps& m, FfnSmem* sm, con
                         tma_gather4(dst + N * 128 + lane * 512, &m.h, int(k) * KB, R + r[0], R + r[1], R + r[2],
                                     R + r[3], fb);
                     }
+                }
+                if constexpr (FP8) {
+                    if (!warp_await_mbar(&sm->scales_out[sc.i], sc.phase ^ 1u, w, SITE_ACC_EMPTY)) {
+                        leave();
+                        return;
+                    }
+                    const uint32_t to = smem_u32(ring + SCALE_AT) + sc.i * (SCALE_FLOATS * 4);
+#pragma unroll
+                    for (int q = 0; q < FFN_MAX_T / 32; ++q)
+                        if (lane + 32 * q < N) cp_async_4(to + (lane + 32 * q) * 4, sx[q] + k);
+                    if (lane < 2) cp_async_4(to + (FFN_MAX_T + lane) * 4, sw + size_t(k) * NB8);
+                    cp_async_mbar_arrive_noinc(&sm->scales_in[sc.i]);
+                    sc.next(SCALE_SLOTS);
                 }
                 __syncwarp();
                 st.next(rg.stages);
@@ -559,7 +607,7 @@ __device__ void drain_accumulators(const FfnParams& p, FfnSmem* sm, const Ring& 
     const int et = threadIdx.x - WARP_EPI * 32;
     constexpr int MAXB = FFN_MAX_T / 32;  // blocks of 16 columns per warp
     const uint32_t tq = sm->tmem_base + (uint32_t(quad * 32) << 16);
-    Turn buf;
+    Turn buf, sc;
     // A wait that gave up only stops the work: the barriers that the eight
     // warps share are still reached by all of them.
     bool ok = true;
@@ -622,52 +670,20 @@ __device__ void drain_accumulators(const FfnParams& p, FfnSmem* sm, const Ring& 
                 }
                 buf.next(rg.bufs);
             } else {
-                // scales of a step: lane i < 16 holds that of column i of each of the
-                // warp's blocks; loaded one step ahead
-                const int e = sm->expert[s.a];
-                const int KB = (ph == 0 ? p.H : p.F) / GROUP8, NB = (ph == 0 ? p.F : p.H) / GROUP8;
-                const float* sc[MAXB];
-                const float* w0;
-                const float* w1;
-                if (ph == 0) {
-                    w0 = p.w1_scale + size_t(e) * KB * NB + s.blk;
-                    w1 = p.w3_scale + size_t(e) * KB * NB + s.blk;
-                } else {
-                    w0 = p.w2_scale + size_t(e) * KB * NB + 2 * s.blk;
-                    w1 = w0 + (2 * s.blk + 1 < NB ? 1 : 0);
-                    // the scales of h come with its tiles
-                    if (ok) ok = __all_sync(0xffffffffu, await_geq(&p.ctl->ready[s.a], half[0].blocks, w, SITE_TILE_READY));
-                }
+                float acc0[MAXB][16], acc1[MAXB][16];
 #pragma unroll
-                for (int b = 0; b < MAXB; ++b) {
-                    const int i = off + min((set + 2 * b) * 16 + (lane & 15), n - 1);
-                    sc[b] = ph == 0 ? p.x_scale + size_t(sm->row_token[i]) * KB : p.h_scale + size_t(i) * KB;
-                }
-                float acc0[MAXB][16], acc1[MAXB][16], next[MAXB], f0, f1;
-#pragma unroll
-                for (int b = 0; b < MAXB; ++b) {
-                    next[b] = 0.f;
+                for (int b = 0; b < MAXB; ++b)
 #pragma unroll
                     for (int i = 0; i < 16; ++i) acc0[b][i] = acc1[b][i] = 0.f;
-                }
-                auto fetch = [&](uint32_t k) {
-                    f0 = __ldg(w0 + size_t(k) * NB);
-                    f1 = __ldg(w1 + size_t(k) * NB);
-#pragma unroll
-                    for (int b = 0; b < MAXB; ++b)
-                        if (set + 2 * b < nblk) next[b] = __ldcg(sc[b] + k);
-                };
-                if (ok) fetch(s.k0);
                 for (uint32_t k = s.k0; k < s.k1; ++k) {
-                    float cur[MAXB];
-#pragma unroll
-                    for (int b = 0; b < MAXB; ++b) cur[b] = next[b];
-                    const float c0 = f0, c1 = f1;
-                    if (ok && k + 1 < s.k1) fetch(k + 1);
+                    if (ok) ok = warp_await_mbar(&sm->scales_in[sc.i], sc.phase, w, SITE_ACC_FULL);
                     if (ok) ok = warp_await_mbar(&sm->acc_full[buf.i], buf.phase, w, SITE_ACC_FULL);
                     if (ok) {
                         tc_fence_after();
                         const uint32_t t0 = tq + buf.i * 2u * rg.acc_stride;
+                        const float* scale =
+                            reinterpret_cast<const float*>(ffn_ring() + SCALE_AT) + sc.i * SCALE_FLOATS;
+                        const float c0 = scale[FFN_MAX_T], c1 = scale[FFN_MAX_T + 1];
 #pragma unroll
                         for (int b = 0; b < MAXB; ++b) {
                             const int blk = set + 2 * b;
@@ -678,7 +694,7 @@ __device__ void drain_accumulators(const FfnParams& p, FfnSmem* sm, const Ring& 
                                 tmem_ld_wait();
 #pragma unroll
                                 for (int i = 0; i < 16; ++i) {
-                                    const float x = __shfl_sync(0xffffffffu, cur[b], i);
+                                    const float x = scale[blk * 16 + i];
                                     acc0[b][i] = fmaf(__uint_as_float(r0[i]), x * c0, acc0[b][i]);
                                     acc1[b][i] = fmaf(__uint_as_float(r1[i]), x * c1, acc1[b][i]);
                                 }
@@ -686,9 +702,13 @@ __device__ void drain_accumulators(const FfnParams& p, FfnSmem* sm, const Ring& 
                         }
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(&sm->acc_empty[buf.i]);
+                        if (lane == 0) {
+                            mbar_arrive(&sm->acc_empty[buf.i]);
+                            mbar_arrive(&sm->scales_out[sc.i]);
+                        }
                     }
                     buf.next(rg.bufs);
+                    sc.next(SCALE_SLOTS);
                 }
                 if (ok) {
 #pragma unroll
@@ -781,6 +801,10 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
             mbar_init(&sm->acc_full[i], 1);
             mbar_init(&sm->acc_empty[i], EPI_WARPS);
         }
+        for (int i = 0; i < SCALE_SLOTS; ++i) {
+            mbar_init(&sm->scales_in[i], 32);
+            mbar_init(&sm->scales_out[i], EPI_WARPS);
+        }
         mbar_init(&sm->drain, 1);
         fence_barrier_init();
         sm->ok = 1;
@@ -832,7 +856,7 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
         const int N = pad16(sm->most);
         rg.acc_stride = uint32_t(N);
         rg.stage_bytes = uint32_t(STEP_BYTES + N * 128 * (FP8 ? 1 : 2));
-        rg.stages = min(uint32_t(FFN_MAX_STAGES), uint32_t(RING_BYTES) / rg.stage_bytes);
+        rg.stages = min(uint32_t(FFN_MAX_STAGES), uint32_t(FP8 ? SCALE_AT : RING_BYTES) / rg.stage_bytes);
         rg.bufs = FP8 ? min(uint32_t(FFN_MAX_BUFS), 512u / (2u * rg.acc_stride)) : 2u;
 
         if (warp == WARP_A) weight_loads<FP8>(p, m, sm, rg, half, wp);
@@ -900,10 +924,6 @@ mk_status_t ffn_sizes(int T, int H, int E, int k, int F, int weights) {
 
 template <bool FP8>
 cudaError_t launch_ffn(const FfnParams& p, const FfnMaps& m, int grid, cudaStream_t st) {
-    // set on every call: a device reset would forget it
-    cudaError_t e =
-        cudaFuncSetAttribute(mk_moe_ffn_decode_kernel<FP8>, cudaFuncAttributeMaxDynamicSharedMemorySize, FFN_SMEM);
-    if (e != cudaSuccess) return e;
     // the CTAs wait for one another: a cooperative launch has all of them resident
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(grid);
@@ -919,6 +939,14 @@ cudaError_t launch_ffn(const FfnParams& p, const FfnMaps& m, int grid, cudaStrea
 }
 
 }  // namespace
+
+cudaError_t ffn_kernel_attributes() {
+    const cudaError_t e =
+        cudaFuncSetAttribute(mk_moe_ffn_decode_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, FFN_SMEM);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(mk_moe_ffn_decode_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, FFN_SMEM);
+}
+
 }  // namespace mk
 
 using namespace mk;
@@ -945,7 +973,8 @@ extern "C" mk_status_t mk_moe_ffn_decode(const void* x, const float* x_scale, co
             if ((v != nullptr) != fp8 || !host_aligned(v, 4)) return MK_ERR_INVALID_ARG;
     }
     int dev = 0, sms = 0;
-    if ((s = host_device(&dev, &sms)) != MK_OK) return s;
+    DevError* err = nullptr;
+    if ((s = host_device(&dev, &sms, &err)) != MK_OK) return s;
     if (T == 0) return MK_OK;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const FfnLayout L = ffn_layout(T, H, F, k, fp8);
@@ -971,7 +1000,7 @@ extern "C" mk_status_t mk_moe_ffn_decode(const void* x, const float* x_scale, co
     p.h_scale = reinterpret_cast<float*>(ws + L.h_scale);
     p.y = reinterpret_cast<float*>(ws + L.y);
     p.slots = reinterpret_cast<float*>(ws + L.slots);
-    if (error_word(&p.err) != cudaSuccess) return MK_ERR_CUDA;
+    p.err = err;
     p.T = T;
     p.H = H;
     p.F = F;

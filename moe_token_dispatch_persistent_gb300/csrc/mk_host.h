@@ -21,8 +21,13 @@ struct DevError {
 // Its address on the current device.
 cudaError_t error_word(DevError** out);
 
-// The current device: its id and SM count, or why it cannot be used.
-mk_status_t host_device(int* dev, int* sms);
+// The current device: its id, SM count and error word, or why it cannot be
+// used.  The first call on a device sets every kernel's attributes.
+mk_status_t host_device(int* dev, int* sms, DevError** err);
+
+// Kernel attributes of the units below, set once per device.
+cudaError_t attn_kernel_attributes();
+cudaError_t ffn_kernel_attributes();
 
 // Workspace caches, one per operator family: their control blocks differ.
 enum WsKind { WS_DISPATCH = 0, WS_EP = 1, WS_ATTN = 2, WS_FFN = 3, WS_KINDS = 4 };

@@ -239,7 +239,8 @@ extern "C" mk_status_t mk_add_rmsnorm(const void* x, int64_t x_stride, const voi
         if (T > 1 && (x_stride < H || (residual && residual_stride < H))) return MK_ERR_INVALID_ARG;
     }
     int dev = 0, sms = 0;
-    const mk_status_t s = host_device(&dev, &sms);
+    DevError* err = nullptr;
+    const mk_status_t s = host_device(&dev, &sms, &err);
     if (s != MK_OK) return s;
     if (T == 0) return MK_OK;
 
