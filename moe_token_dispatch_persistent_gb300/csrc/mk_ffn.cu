@@ -6,30 +6,29 @@
 //
 // For a few tokens the chosen experts' weights are all the traffic, each used
 // for the few rows routed to its expert, so the kernel is a stream of
-// weights: one step is 32 KiB of them, and the steps of all chosen experts in
-// a row are cut into one equal range per CTA, first those of W1 and W3, then
-// those of W2.  Every SM therefore reads the same number of bytes, whatever
-// the routing.
+// weights.  One step is 32 KiB of them, 256 columns wide; a unit of work is a
+// few consecutive steps of one block of columns: first the units of W1 and W3
+// of every chosen expert, then those of W2, taken in order from one counter.
+// SMs that read slower take fewer, and by the time the first expert's W2 is
+// reached its h has long been complete, unless it is the only one.
 //
 // The products run on tcgen05 with the weights as the 128-row operand (their
 // columns are its rows, M-major as they lie in memory, loaded by TMA) and the
-// expert's rows of x or h as the N = 16..128 columns, gathered by TMA
-// tile::gather4.  Roles of a CTA's warps: one loads weights and waits for
-// nothing but free stages, so across the boundary between the two halves the
-// stream goes on while h is still being completed; one gathers rows (and
-// waits for an expert's h before its first use); one issues products; eight
-// drain accumulators.
+// expert's rows of x or h as the columns (N = 16..128), gathered by TMA
+// tile::gather4.  Roles of a CTA's warps: one takes units and loads their
+// weights, waiting for nothing but free stages, so the stream goes on while an
+// h is still being completed; one gathers rows (and waits for an expert's h
+// before its first use); one issues products; eight drain accumulators.
 //
-// A tile (128 columns of W1 and W3, or 256 of W2, over all of K) may be split
-// over CTAs.  The pieces are fp32 sums in the workspace; for h the CTA that
-// delivers the last piece of a tile adds them up in their order, applies
-// SwiGLU and publishes the tile, and for the outputs the combine after the
-// last barrier of the grid adds the pieces of each token's k rows in order.
-// No result depends on which CTA was first.
+// A unit's sums are a piece in fp32 in the workspace.  The CTA that delivers
+// the last piece of 256 columns of h adds them up, applies SwiGLU and
+// publishes them; after the last barrier of the grid the combine adds the
+// pieces of each token's k rows.  Both add in the order of K: which CTA
+// computed a piece, and when, changes nothing.
 //
-// 16-bit weights: h is kept as the sum of two bf16 values (two products into
-// one accumulator, 16 significant bits), since the tensor core has time to
-// spare here and one rounding fewer reaches the output.  8-bit weights: a
+// 16-bit weights: h is kept as the sum of two bf16 values, which take
+// neighbouring columns of the same product (16 significant bits): the tensor
+// core has columns to spare here, and one rounding fewer reaches the output.  8-bit weights: a
 // weight scale per 128 x 128 block and a scale of x and h per row and 128
 // columns, so one step is one block of K; its products leave the tensor core
 // after each step and are added up in fp32 registers with their scales.
@@ -57,26 +56,44 @@ constexpr int FFN_MAX_CTAS = 160;
 
 // Warps: weight loads, products, eight draining accumulators (TMEM lanes
 // 32 * (warp % 4); two warps share a quarter and take turns at its column
-// blocks), row loads.
+// blocks), row loads, four that complete h.
 constexpr int WARP_A = 0, WARP_MMA = 1, WARP_EPI = 2, EPI_WARPS = 8, WARP_B = WARP_EPI + EPI_WARPS;
-constexpr int FFN_WARPS = WARP_B + 1;
+constexpr int WARP_FIN = WARP_B + 1, FIN_WARPS = 4;
+constexpr int FFN_WARPS = WARP_FIN + FIN_WARPS;
 constexpr int FFN_THREADS = FFN_WARPS * 32;
-constexpr int EPI_THREADS = EPI_WARPS * 32;
+
+// Rows of an expert that are multiplied together; an expert with more is
+// taken in parts, each reading its weights.  (Two accumulators of 64 columns
+// for the value and the remainder of h, twice, fill TMEM; with 8 bits the
+// sums of a step are kept in registers, and those end there too.)
+constexpr int MAX_N = 64;
+constexpr int MAX_PARTS = MAX_E + FFN_MAX_ROWS / MAX_N;
 
 constexpr int STEP_BYTES = 32768;  // weights of one step
 constexpr int ACC_COLS = 256;      // weight columns of a tile: two accumulators of 128
 constexpr int GROUP8 = 128;        // rows and columns of an 8-bit scale block
-constexpr int FFN_MAX_STAGES = 6;
+// Stages of the ring.  Four hold 19 MB of weights in flight over the GPU, 2.9
+// us of its bandwidth; with six every other access (row loads, pieces,
+// counters) waited behind 4.3 us of them and the kernel took 1-5% longer.
+constexpr int STAGES_F = 4;
 constexpr int FFN_MAX_BUFS = 8;
-constexpr int RING_BYTES = FFN_MAX_STAGES * (STEP_BYTES + 16 * 128 * 2);  // six stages at up to 16 rows an expert
-// 8 bits: the scales of a step (up to 128 rows, then the two weight blocks) in
-// a ring of their own at the end, longer than the stages and accumulator
+// A stage: the step's weights, then up to 64 rows (16 bits: twice, for h's values and remainders).
+template <bool FP8>
+constexpr int STAGE_F = STEP_BYTES + (FP8 ? 1 : 2) * MAX_N * 128;
+constexpr int RING_BYTES = STAGES_F * STAGE_F<false>;
+// 8 bits: the scales of a step (up to 64 rows, then the two weight blocks) in
+// a ring of their own after the stages, longer than the stages and accumulator
 // buffers that lie between their load and their use.
-constexpr int SCALE_SLOTS = 16, SCALE_FLOATS = FFN_MAX_T + 4;
-constexpr int SCALE_AT = RING_BYTES - SCALE_SLOTS * SCALE_FLOATS * 4;
-static_assert(SCALE_SLOTS >= FFN_MAX_STAGES + FFN_MAX_BUFS && SCALE_AT % 16 == 0, "scale ring");
-constexpr int MAX_TILES1 = MAX_E * (32768 / 128);
-constexpr int SLOTS = 5;           // per CTA: h pieces (first, last range; whole tile), output pieces (first, last)
+constexpr int SCALE_SLOTS = 16, SCALE_FLOATS = MAX_N + 4;
+constexpr int SCALE_AT = STAGES_F * STAGE_F<true>;
+static_assert(SCALE_SLOTS >= STAGES_F + FFN_MAX_BUFS && SCALE_AT + SCALE_SLOTS * SCALE_FLOATS * 4 <= RING_BYTES, "scale ring");
+constexpr int MAX_TILES1 = MAX_PARTS * (32768 / ACC_COLS);
+// Units: about this many per CTA, of at least this many steps.  Pieces of more
+// floats than this only where one unit covers all of K.
+constexpr uint32_t UNITS_PER_CTA = 16, MIN_CHUNK = 4;
+constexpr size_t PIECE_FLOATS = size_t(8) << 20;
+constexpr int INFO_SLOTS = 8;
+static_assert(INFO_SLOTS % FIN_WARPS == 0, "each completing warp's units keep to their slots");
 constexpr long long FFN_SPIN_NS = 2000000000LL;
 constexpr float E4M3_TOP = 448.f;
 constexpr float TINY = 7.888609052210118e-31f;  // 2^-100
@@ -86,9 +103,10 @@ struct FfnCtl {
     uint32_t done;    // CTAs whose output pieces are written
     uint32_t exited;
     uint32_t abort;
-    uint32_t pad[60];
-    uint32_t ready[MAX_E];            // tiles of h published, per chosen expert
-    uint32_t arrived[MAX_TILES1];     // pieces of an h tile delivered
+    uint32_t next;    // units taken beyond the first of every CTA
+    uint32_t pad[59];
+    uint32_t ready[MAX_PARTS];        // blocks of h published, per part of the chosen experts
+    uint32_t arrived[MAX_TILES1];     // pieces of each block of h delivered
 };
 
 struct FfnParams {
@@ -103,8 +121,8 @@ struct FfnParams {
     float* gates;       // [T*k] their gates (when routing is shared out)
     uint8_t* h;         // [2][T*k][F] bf16 (value and remainder) or [T*k][F] e4m3
     float* h_scale;     // [T*k][F/128]
-    float* y;           // [T*k][H] products of tiles that one CTA computed whole
-    float* slots;       // [ctas][SLOTS][T][256] pieces
+    float* piece[2];    // sums of the units: [matrix and chunk of K][T*k][columns, whole blocks]
+    size_t room[2];     // floats of each
     DevError* err;
     int T, H, F, E, k;
 };
@@ -113,71 +131,99 @@ struct FfnMaps {
     CUtensorMap x, w1, w3, w2, h;
 };
 
+// A unit of work as its CTA's warps see it.
+struct Unit {
+    int half, second;  // first or second half of the layer; W3 instead of W1
+    int a, expert;     // part of the chosen experts and its expert,
+    int n, off;        // its rows and the first of them
+    int blk, c;        // block of columns, chunk of K
+    uint32_t k0, k1;   // steps along K
+    int end;           // 1: no more units
+};
+
 struct FfnSmem {
-    uint64_t weights_in[FFN_MAX_STAGES], rows_in[FFN_MAX_STAGES], empty[FFN_MAX_STAGES];
+    uint64_t weights_in[STAGES_F], rows_in[STAGES_F], empty[STAGES_F];
     uint64_t acc_full[FFN_MAX_BUFS], acc_empty[FFN_MAX_BUFS];
     uint64_t scales_in[SCALE_SLOTS], scales_out[SCALE_SLOTS];
+    uint64_t info_in[INFO_SLOTS], info_out[INFO_SLOTS], piece_in[INFO_SLOTS];
     uint64_t drain;
+    Unit unit[INFO_SLOTS];         // this CTA's units in turn
     uint32_t tmem_base;
-    int ok, last, chosen, most;  // most: rows of the busiest expert
+    int ok, parts, most;           // most: rows of the largest part
     int scan[8];
-    float red[2][2][4];
-    uint16_t off[MAX_E + 1];       // per chosen expert: its first row,
-    uint8_t expert[MAX_E];         // its id
-    uint8_t count[MAX_E];          // and its rows
+    uint16_t off[MAX_PARTS];       // per part of the chosen experts: its first row,
+    uint8_t expert[MAX_PARTS];     // its expert
+    uint8_t count[MAX_PARTS];      // and its rows
     uint8_t row_token[FFN_MAX_ROWS];
-    uint16_t row_of[FFN_MAX_ROWS]; // per (token, choice): its row,
-    uint8_t act_of[FFN_MAX_ROWS];  // its place among the chosen experts
+    uint16_t row_of[FFN_MAX_ROWS]; // per (token, choice): its row
     float gate[FFN_MAX_ROWS];      // and its gate
 };
 constexpr int FFN_SMEM = RING_BYTES + int(sizeof(FfnSmem)) + 1024;
 static_assert(FFN_SMEM <= 232448, "dynamic shared memory of one CTA on sm_103");
 
 // Routing scratch, in the ring before the first load.
-constexpr int RS_IDS = 0, RS_MASK = FFN_MAX_ROWS, RS_PLACE = RS_MASK + MAX_E * (FFN_MAX_T / 8);
+constexpr int RS_IDS = 0, RS_MASK = FFN_MAX_ROWS, RS_FIRST = RS_MASK + MAX_E * (FFN_MAX_T / 8);
 
-// One half of the layer as seen by this CTA: steps [start, end) of `total`.
-struct Half {
-    uint32_t ks;      // steps per tile
-    uint32_t blocks;  // tiles per expert
-    uint32_t total, ctas, start, end;
-    uint32_t each, more;  // steps per CTA; the first `more` CTAs take one more
-    __device__ uint32_t first_step(uint32_t c) const { return c * each + min(c, more); }
-    __device__ uint32_t owner(uint32_t step) const {
-        const uint32_t in_more = more * (each + 1);
-        return step < in_more ? step / (each + 1) : more + (step - in_more) / each;
-    }
+// The layer's units, the same in every CTA.  Index 0: W1 and W3 (K = H,
+// columns F), 1: W2 (K = F, columns H).
+struct Plan {
+    uint32_t ms[2];      // steps along K of a matrix
+    uint32_t blocks[2];  // blocks of 256 columns
+    uint32_t chunk[2];   // steps of a unit
+    uint32_t chunks[2];  // units along K
+    uint32_t first_down, units;
 };
 
-__device__ __forceinline__ Half make_half(uint32_t ks, uint32_t blocks, uint32_t experts) {
-    Half h;
-    h.ks = ks;
-    h.blocks = blocks;
-    h.total = ks * blocks * experts;
-    h.ctas = min(gridDim.x, h.total);  // every CTA that takes part has a step
-    h.each = h.total / h.ctas;
-    h.more = h.total - h.each * h.ctas;
-    const bool in = blockIdx.x < h.ctas;
-    h.start = in ? h.first_step(blockIdx.x) : 0u;
-    h.end = in ? h.first_step(blockIdx.x + 1) : 0u;
-    return h;
+__device__ __forceinline__ Plan make_plan(const FfnParams& p, int step_rows, uint32_t parts, uint32_t most) {
+    Plan q;
+    q.ms[0] = uint32_t(p.H / step_rows);
+    q.ms[1] = uint32_t(p.F / step_rows);
+    q.blocks[0] = uint32_t((p.F + ACC_COLS - 1) / ACC_COLS);
+    q.blocks[1] = uint32_t((p.H + ACC_COLS - 1) / ACC_COLS);
+    const uint32_t steps = parts * (2 * q.ms[0] * q.blocks[0] + q.ms[1] * q.blocks[1]);
+    // Small units even out the SMs' speeds; every unit leaves a piece of `most`
+    // rows of 1 KiB next to its 32 KiB a step, so many rows want longer ones.
+    const uint32_t want = max(max(MIN_CHUNK, most / 2), steps / (gridDim.x * UNITS_PER_CTA));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const uint32_t rows = uint32_t(p.T * p.k) * (h == 0 ? 2 : 1);
+        const uint32_t fit = uint32_t(p.room[h] / (size_t(rows) * q.blocks[h] * ACC_COLS));
+        const uint32_t n = max(1u, min((q.ms[h] + want - 1) / want, fit));
+        q.chunk[h] = (q.ms[h] + n - 1) / n;
+        q.chunks[h] = (q.ms[h] + q.chunk[h] - 1) / q.chunk[h];
+    }
+    q.first_down = parts * 2 * q.chunks[0] * q.blocks[0];
+    q.units = q.first_down + parts * q.chunks[1] * q.blocks[1];
+    return q;
 }
 
-// Steps [k0, k1) of one tile.
-struct Piece {
-    uint32_t tile, k0, k1;
-    int a, blk;  // place of the expert, block of columns
-};
+// Neighbours in the order read neighbouring columns of the same rows of
+// weights (measured against a block of columns after the other: 109 us instead
+// of 114 on one token and two experts of 4096 x 14336, no change elsewhere).
+__device__ __forceinline__ Unit unit_of(const FfnSmem* sm, const Plan& q, uint32_t u) {
+    Unit s;
+    s.end = 0;
+    s.half = u >= q.first_down;
+    const uint32_t mats = s.half ? 1 : 2, blocks = q.blocks[s.half];
+    if (s.half) u -= q.first_down;
+    const uint32_t per = mats * q.chunks[s.half] * blocks;
+    s.a = int(u / per);
+    u -= uint32_t(s.a) * per;
+    s.c = int(u / (mats * blocks));
+    u -= uint32_t(s.c) * mats * blocks;
+    s.second = u >= blocks;
+    s.blk = int(s.second ? u - blocks : u);
+    s.k0 = uint32_t(s.c) * q.chunk[s.half];
+    s.k1 = min(q.ms[s.half], s.k0 + q.chunk[s.half]);
+    s.expert = sm->expert[s.a];
+    s.n = sm->count[s.a];
+    s.off = sm->off[s.a];
+    return s;
+}
 
-__device__ __forceinline__ bool next_piece(const Half& h, uint32_t& pos, Piece& s) {
-    if (pos >= h.end) return false;
-    s.tile = pos / h.ks;
-    s.k0 = pos - s.tile * h.ks;
-    s.k1 = min(h.ks, s.k0 + (h.end - pos));
-    s.a = int(s.tile / h.blocks);
-    s.blk = int(s.tile - uint32_t(s.a) * h.blocks);
-    pos += s.k1 - s.k0;
-    return true;
+// Row r of a unit's piece.
+__device__ __forceinline__ float* piece_row(const FfnParams& p, const Plan& q, int half, uint32_t part, int row) {
+    return p.piece[half] + (size_t(part) * (p.T * p.k) + row) * (size_t(q.blocks[half]) * ACC_COLS);
 }
 
 __device__ __forceinline__ uint8_t* ffn_ring() {
@@ -186,11 +232,6 @@ __device__ __forceinline__ uint8_t* ffn_ring() {
 }
 
 __device__ __forceinline__ int pad16(int n) { return (n + 15) & ~15; }
-
-template <int ID, int N>
-__device__ __forceinline__ void bar_sync() {
-    asm volatile("bar.sync %0, %1;" ::"n"(ID), "n"(N) : "memory");
-}
 
 __device__ __forceinline__ float nan_max(float a, float b) {
     float r;
@@ -257,7 +298,7 @@ __device__ void build_rows(const FfnParams& p, FfnSmem* sm, uint8_t* scratch) {
     constexpr int WORDS = FFN_MAX_T / 32;
     const uint8_t* ids = scratch + RS_IDS;
     uint32_t* mask = reinterpret_cast<uint32_t*>(scratch + RS_MASK);
-    uint8_t* place = scratch + RS_PLACE;
+    uint16_t* first_row = reinterpret_cast<uint16_t*>(scratch + RS_FIRST);
     const int rows = p.T * p.k;
     for (int i = tid; i < p.E * WORDS; i += FFN_THREADS) mask[i] = 0;
     if (tid == 0) sm->most = 0;
@@ -267,13 +308,13 @@ __device__ void build_rows(const FfnParams& p, FfnSmem* sm, uint8_t* scratch) {
         atomicOr(&mask[ids[i] * WORDS + (t >> 5)], 1u << (t & 31));
     }
     __syncthreads();
-    // rows and chosen experts before each expert, 16 bits each
+    // rows and parts before each expert, 16 bits each
     uint32_t mine = 0;
     if (tid < p.E) {
         int c = 0;
 #pragma unroll
         for (int w = 0; w < WORDS; ++w) c += __popc(mask[tid * WORDS + w]);
-        mine = uint32_t(c) | (c ? 1u << 16 : 0u);
+        mine = uint32_t(c) | uint32_t((c + MAX_N - 1) / MAX_N) << 16;
     }
     uint32_t run = mine;
 #pragma unroll
@@ -281,7 +322,7 @@ __device__ void build_rows(const FfnParams& p, FfnSmem* sm, uint8_t* scratch) {
         const uint32_t o = __shfl_up_sync(0xffffffffu, run, d);
         if (lane >= d) run += o;
     }
-    const uint32_t top = __reduce_max_sync(0xffffffffu, mine & 0xffffu);
+    const uint32_t top = __reduce_max_sync(0xffffffffu, min(mine & 0xffffu, uint32_t(MAX_N)));
     if (warp < MAX_E / 32) {
         if (lane == 31) sm->scan[warp] = int(run);
         if (lane == 0) atomicMax(&sm->most, int(top));
@@ -290,32 +331,31 @@ __device__ void build_rows(const FfnParams& p, FfnSmem* sm, uint8_t* scratch) {
     if (tid < MAX_E) {
         uint32_t base = run - mine;
         for (int w = 0; w < warp; ++w) base += uint32_t(sm->scan[w]);
-        const int a = int(base >> 16);
-        if (mine) {
-            sm->expert[a] = uint8_t(tid);
-            sm->count[a] = uint8_t(mine & 0xffffu);
-            sm->off[a] = uint16_t(base & 0xffffu);
-            place[tid] = uint8_t(a);
+        const int a = int(base >> 16), first = int(base & 0xffffu), c = int(mine & 0xffffu);
+        for (int i = 0; i < int(mine >> 16); ++i) {
+            sm->expert[a + i] = uint8_t(tid);
+            sm->count[a + i] = uint8_t(min(MAX_N, c - i * MAX_N));
+            sm->off[a + i] = uint16_t(first + i * MAX_N);
         }
-        if (tid == MAX_E - 1) sm->chosen = int((base + mine) >> 16);
+        first_row[tid] = uint16_t(first);
+        if (tid == MAX_E - 1) sm->parts = int((base + mine) >> 16);
     }
     __syncthreads();
     for (int i = tid; i < rows; i += FFN_THREADS) {
-        const int t = i / p.k, e = ids[i], a = place[e];
+        const int t = i / p.k, e = ids[i];
         int before = 0;
         for (int w = 0; w < (t >> 5); ++w) before += __popc(mask[e * WORDS + w]);
         before += __popc(mask[e * WORDS + (t >> 5)] & ((1u << (t & 31)) - 1u));
-        const int r = sm->off[a] + before;
+        const int r = first_row[e] + before;
         sm->row_of[i] = uint16_t(r);
-        sm->act_of[i] = uint8_t(a);
         sm->row_token[r] = uint8_t(t);
     }
 }
 
 // --------------------------------------------------------------- roles -----
 
-struct Ring {
-    uint32_t stages, stage_bytes, bufs, acc_stride;  // acc_stride: TMEM columns of one accumulator
+struct Accs {
+    uint32_t bufs, acc_stride;  // accumulator pairs, TMEM columns of one accumulator
 };
 
 struct Turn {  // position in a ring of n slots
@@ -338,7 +378,7 @@ struct Issued {
     }
     __device__ void settle(uint64_t* bars) const {
         const uint64_t t0 = globaltimer();
-        for (uint32_t i = 0; i < FFN_MAX_STAGES; ++i)
+        for (uint32_t i = 0; i < STAGES_F; ++i)
             if (any >> i & 1u)
                 while (!mbar_try_wait(&bars[i], parity >> i & 1u) && globaltimer() - t0 < 5000000ull) {
                 }
@@ -346,43 +386,69 @@ struct Issued {
     }
 };
 
+// The CTA's next unit, as the weight loads publish it.  False: no more, or a
+// wait gave up (ok is then false).
+__device__ __forceinline__ bool next_unit(FfnSmem* sm, Turn& in, const Waiter& w, Unit& s, bool& ok) {
+    if (!(ok = warp_await_mbar(&sm->info_in[in.i], in.phase, w, SITE_INFO_FULL))) return false;
+    s = sm->unit[in.i];
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(&sm->info_out[in.i]);
+    in.next(INFO_SLOTS);
+    return s.end == 0;
+}
+
 template <bool FP8>
-__device__ void weight_loads(const FfnParams& p, const FfnMaps& m, FfnSmem* sm, const Ring& rg, const Half (&half)[2],
+__device__ void weight_loads(const FfnParams& p, const FfnMaps& m, FfnSmem* sm, const Plan& pl,
                              const Waiter& w) {
     constexpr int KB = FP8 ? 128 : 64;   // rows of K in a step
     constexpr int CB = FP8 ? 128 : 64;   // columns of a box
     constexpr int BOX = KB * 128;        // bytes of a box
+    const int lane = threadIdx.x & 31;
     uint8_t* ring = ffn_ring();
     const uint64_t pol = l2_policy_evict_first();  // every weight is read once
-    Turn st;
+    Turn st, out;
     Issued mine;
-    for (int ph = 0; ph < 2; ++ph) {
-        const int ncol = ph == 0 ? p.F : p.H, krows = ph == 0 ? p.H : p.F;
-        uint32_t pos = half[ph].start;
-        Piece s;
-        while (next_piece(half[ph], pos, s)) {
-            const int row0 = sm->expert[s.a] * krows;
-            for (uint32_t k = s.k0; k < s.k1; ++k) {
-                if (!warp_await_mbar(&sm->empty[st.i], st.phase ^ 1u, w, SITE_STAGE_EMPTY)) {
-                    mine.settle(sm->weights_in);
-                    return;
-                }
-                uint64_t* fb = &sm->weights_in[st.i];
-                uint8_t* dst = ring + st.i * rg.stage_bytes;
-                mine.note(st);
-                mbar_arrive_expect_tx_elect(fb, STEP_BYTES);
-                const int row = row0 + int(k) * KB;
-#pragma unroll
-                for (int q = 0; q < STEP_BYTES / BOX; ++q) {
-                    // boxes past the matrix's edge read as zeros
-                    const int c = ph == 0 ? s.blk * 128 + (q * CB) % 128 : s.blk * ACC_COLS + q * CB;
-                    const CUtensorMap* map = ph == 1 ? &m.w2 : q * CB < 128 ? &m.w1 : &m.w3;
-                    tma_load_2d_elect_hint(dst + q * BOX, map, c < ncol ? c : ncol, row, fb, pol);
-                }
-                st.next(rg.stages);
-            }
+    uint32_t u = blockIdx.x;  // the first unit of every CTA needs no counter
+    int ends = 0;
+    while (true) {
+        if (!warp_await_mbar(&sm->info_out[out.i], out.phase ^ 1u, w, SITE_INFO_EMPTY)) break;
+        const bool more = u < pl.units;
+        uint32_t ahead = 0;  // taken while this unit's loads are issued
+        if (more && lane == 0) ahead = atom_add_relaxed_u32(&p.ctl->next, 1u);
+        Unit s = unit_of(sm, pl, more ? u : 0u);
+        s.end = !more;
+        if (lane == 0) {
+            sm->unit[out.i] = s;
+            mbar_arrive(&sm->info_in[out.i]);
         }
+        out.next(INFO_SLOTS);
+        if (!more) {
+            if (++ends == FIN_WARPS) return;  // each completing warp looks at every fourth slot only
+            continue;
+        }
+        const int ncol = s.half ? p.H : p.F;
+        const int row0 = s.expert * (s.half ? p.F : p.H);
+        const CUtensorMap* map = s.half ? &m.w2 : s.second ? &m.w3 : &m.w1;
+        for (uint32_t k = s.k0; k < s.k1; ++k) {
+            if (!warp_await_mbar(&sm->empty[st.i], st.phase ^ 1u, w, SITE_STAGE_EMPTY)) {
+                mine.settle(sm->weights_in);
+                return;
+            }
+            uint64_t* fb = &sm->weights_in[st.i];
+            uint8_t* dst = ring + st.i * STAGE_F<FP8>;
+            mine.note(st);
+            mbar_arrive_expect_tx_elect(fb, STEP_BYTES);
+#pragma unroll
+            for (int q = 0; q < STEP_BYTES / BOX; ++q) {
+                // boxes past the matrix's edge read as zeros
+                const int c = s.blk * ACC_COLS + q * CB;
+                tma_load_2d_elect_hint(dst + q * BOX, map, c < ncol ? c : ncol, row0 + int(k) * KB, fb, pol);
+            }
+            st.next(STAGES_F);
+        }
+        u = gridDim.x + __shfl_sync(0xffffffffu, ahead, 0);
     }
+    mine.settle(sm->weights_in);
 }
 
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const float* src) {
@@ -390,144 +456,134 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const float* src) {
 }
 
 template <bool FP8>
-__device__ void row_loads(const FfnParams& p, const FfnMaps& m, FfnSmem* sm, const Ring& rg, const Half (&half)[2],
+__device__ void row_loads(const FfnParams& p, const FfnMaps& m, FfnSmem* sm, const Plan& pl,
                           const Waiter& w) {
     constexpr int KB = FP8 ? 128 : 64;
     const int lane = threadIdx.x & 31;
     uint8_t* ring = ffn_ring();
-    Turn st, sc;
+    Turn st, sc, in;
     Issued mine;
-    auto leave = [&]() {
+    int known = -1;  // the part whose h is known to be complete
+    Unit s;
+    bool ok;
+    while (next_unit(sm, in, w, s, ok)) {
+        const int n = s.n, N = pad16(n), off = s.off;
+        const int parts = s.half && !FP8 ? 2 : 1;  // h: value and remainder
+        if (s.half && s.a != known) {
+            ok = __all_sync(0xffffffffu, await_geq(&p.ctl->ready[s.a], pl.blocks[0], w, SITE_TILE_READY));
+            fence_proxy_async();  // the other CTAs' stores to h before the loads below
+            known = s.a;
+        }
+        // Lanes take four rows each, the next ones the last n % 4 one by one: no
+        // row is read twice (what the rest of the N columns holds is never used).
+        const int fours = n >> 2, singles = n & 3;
+        const bool four = lane < fours, one = !four && lane < fours + singles;
+        const int first = four ? 4 * lane : 4 * fours + (lane - fours);
+        int r[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            const int i = off + min(first + q, n - 1);
+            r[q] = s.half ? i : sm->row_token[i];
+        }
+        // 8 bits: scales of this lane's rows lane, lane + 32, ... and of the two weight blocks
+        const int KB8 = (s.half ? p.F : p.H) / GROUP8, NB8 = (s.half ? p.H : p.F) / GROUP8;
+        const float* sx[MAX_N / 32];
+        const float* sw = nullptr;
+        if constexpr (FP8) {
+#pragma unroll
+            for (int q = 0; q < MAX_N / 32; ++q) {
+                const int i = off + min(lane + 32 * q, n - 1);
+                sx[q] = s.half ? p.h_scale + size_t(i) * KB8 : p.x_scale + size_t(sm->row_token[i]) * KB8;
+            }
+            sw = (s.half ? p.w2_scale : s.second ? p.w3_scale : p.w1_scale) +
+                 size_t(s.expert) * KB8 * NB8 + min(2 * s.blk + (lane & 1), NB8 - 1);
+        }
+        for (uint32_t k = s.k0; ok && k < s.k1; ++k) {
+            if (!(ok = warp_await_mbar(&sm->empty[st.i], st.phase ^ 1u, w, SITE_STAGE_EMPTY))) break;
+            uint64_t* fb = &sm->rows_in[st.i];
+            uint8_t* dst = ring + st.i * STAGE_F<FP8> + STEP_BYTES;
+            mine.note(st);
+            mbar_arrive_expect_tx_elect(fb, uint32_t(n * 128 * parts));
+            __syncwarp();
+            for (int q = 0; q < parts; ++q) {
+                const CUtensorMap* map = s.half ? &m.h : &m.x;
+                uint8_t* to = dst + (q * N + first) * 128;
+                const int R = q * p.T * p.k;
+                if (four) tma_gather4(to, map, int(k) * KB, R + r[0], R + r[1], R + r[2], R + r[3], fb);
+                else if (one) tma_load_2d(to, map, int(k) * KB, R + r[0], fb);
+            }
+            if constexpr (FP8) {
+                if (!(ok = warp_await_mbar(&sm->scales_out[sc.i], sc.phase ^ 1u, w, SITE_ACC_EMPTY))) break;
+                const uint32_t to = smem_u32(ring + SCALE_AT) + sc.i * (SCALE_FLOATS * 4);
+#pragma unroll
+                for (int q = 0; q < MAX_N / 32; ++q)
+                    if (lane + 32 * q < N) cp_async_4(to + (lane + 32 * q) * 4, sx[q] + k);
+                if (lane < 2) cp_async_4(to + (MAX_N + lane) * 4, sw + size_t(k) * NB8);
+                cp_async_mbar_arrive_noinc(&sm->scales_in[sc.i]);
+                sc.next(SCALE_SLOTS);
+            }
+            __syncwarp();
+            st.next(STAGES_F);
+        }
+        if (!ok) break;
+    }
+    if (!ok) {
         if (FP8) cp_async_wait_all();
         mine.settle(sm->rows_in);
-    };
-    for (int ph = 0; ph < 2; ++ph) {
-        uint32_t pos = half[ph].start;
-        Piece s;
-        int known = -1;
-        const int parts = ph == 1 && !FP8 ? 2 : 1;  // h: value and remainder
-        while (next_piece(half[ph], pos, s)) {
-            const int n = sm->count[s.a], N = pad16(n), off = sm->off[s.a];
-            if (ph == 1 && s.a != known) {
-                const bool in = await_geq(&p.ctl->ready[s.a], half[0].blocks, w, SITE_TILE_READY);
-                if (!__all_sync(0xffffffffu, in)) {
-                    leave();
-                    return;
-                }
-                fence_proxy_async();  // the other CTAs' stores to h before the loads below
-                known = s.a;
-            }
-            int r[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int i = off + min(4 * lane + q, n - 1);  // rows past the last repeat it; never stored
-                r[q] = ph == 0 ? sm->row_token[i] : i;
-            }
-            // 8 bits: scales of this lane's rows lane, lane + 32, ... and of the two weight blocks
-            const int KB8 = (ph == 0 ? p.H : p.F) / GROUP8, NB8 = (ph == 0 ? p.F : p.H) / GROUP8;
-            const float* sx[FFN_MAX_T / 32];
-            const float* sw = nullptr;
-            if constexpr (FP8) {
-#pragma unroll
-                for (int q = 0; q < FFN_MAX_T / 32; ++q) {
-                    const int i = off + min(lane + 32 * q, n - 1);
-                    sx[q] = ph == 0 ? p.x_scale + size_t(sm->row_token[i]) * KB8 : p.h_scale + size_t(i) * KB8;
-                }
-                const size_t block = size_t(sm->expert[s.a]) * KB8 * NB8;
-                if (ph == 0) sw = (lane == 0 ? p.w1_scale : p.w3_scale) + block + s.blk;
-                else sw = p.w2_scale + block + min(2 * s.blk + (lane & 1), NB8 - 1);
-            }
-            for (uint32_t k = s.k0; k < s.k1; ++k) {
-                if (!warp_await_mbar(&sm->empty[st.i], st.phase ^ 1u, w, SITE_STAGE_EMPTY)) {
-                    leave();
-                    return;
-                }
-                uint64_t* fb = &sm->rows_in[st.i];
-                uint8_t* dst = ring + st.i * rg.stage_bytes + STEP_BYTES;
-                mine.note(st);
-                mbar_arrive_expect_tx_elect(fb, uint32_t(N * 128 * parts));
-                __syncwarp();
-                if (4 * lane < N) {
-                    tma_gather4(dst + lane * 512, ph == 0 ? &m.x : &m.h, int(k) * KB, r[0], r[1], r[2], r[3], fb);
-                    if (parts == 2) {
-                        const int R = p.T * p.k;
-                        tma_gather4(dst + N * 128 + lane * 512, &m.h, int(k) * KB, R + r[0], R + r[1], R + r[2],
-                                    R + r[3], fb);
-                    }
-                }
-                if constexpr (FP8) {
-                    if (!warp_await_mbar(&sm->scales_out[sc.i], sc.phase ^ 1u, w, SITE_ACC_EMPTY)) {
-                        leave();
-                        return;
-                    }
-                    const uint32_t to = smem_u32(ring + SCALE_AT) + sc.i * (SCALE_FLOATS * 4);
-#pragma unroll
-                    for (int q = 0; q < FFN_MAX_T / 32; ++q)
-                        if (lane + 32 * q < N) cp_async_4(to + (lane + 32 * q) * 4, sx[q] + k);
-                    if (lane < 2) cp_async_4(to + (FFN_MAX_T + lane) * 4, sw + size_t(k) * NB8);
-                    cp_async_mbar_arrive_noinc(&sm->scales_in[sc.i]);
-                    sc.next(SCALE_SLOTS);
-                }
-                __syncwarp();
-                st.next(rg.stages);
-            }
-        }
     }
 }
 
+// A value that is the same on every lane, in a uniform register: without this
+// the compiler moves each operand of each product there one by one, and the
+// issue of the products takes longer than a step's loads.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __reduce_max_sync(0xffffffffu, v); }
+
 template <bool FP8>
-__device__ void products(FfnSmem* sm, const Ring& rg, const Half (&half)[2], const Waiter& w) {
-    const uint32_t ring = smem_u32(ffn_ring());
-    Turn st, buf;
+__device__ void products(FfnSmem* sm, const Accs& accs, const Waiter& w) {
+    const uint32_t bufs = uniform(accs.bufs), acc_stride = uniform(accs.acc_stride);
+    const uint32_t tmem = uniform(sm->tmem_base), ring = uniform(smem_u32(ffn_ring()));
+    Turn st, buf, in;
     bool issued = false, ok = true;
-    for (int ph = 0; ph < 2 && ok; ++ph) {
-        uint32_t pos = half[ph].start;
-        Piece s;
-        while (ok && next_piece(half[ph], pos, s)) {
-            const uint32_t N = uint32_t(pad16(sm->count[s.a]));
-            const uint32_t idesc = FP8 ? umma_idesc_e4m3(128, N, true, false) : umma_idesc_bf16(128, N, true, false);
-            for (uint32_t k = s.k0; k < s.k1; ++k) {
-                // 16 bits: one accumulation per piece; 8 bits: one per step
-                if (FP8 || k == s.k0) {
-                    if (!(ok = warp_await_mbar(&sm->acc_empty[buf.i], buf.phase ^ 1u, w, SITE_ACC_EMPTY))) break;
-                }
-                if (!(ok = warp_await_mbar(&sm->rows_in[st.i], st.phase, w, SITE_STAGE_FULL))) break;
-                if (!(ok = warp_await_mbar(&sm->weights_in[st.i], st.phase, w, SITE_STAGE_FULL))) break;
-                tc_fence_after();
-                const uint32_t d = sm->tmem_base + buf.i * 2u * rg.acc_stride;
-                const uint32_t a = ring + st.i * rg.stage_bytes, b = a + STEP_BYTES;
-                issued = true;
+    Unit s;
+    while (ok && next_unit(sm, in, w, s, ok)) {
+        // 16 bits: h's values and remainders are columns side by side
+        const uint32_t half = uniform(uint32_t(s.half)), steps = uniform(s.k1 - s.k0);
+        const uint32_t N = uniform(uint32_t(pad16(s.n))) * (FP8 ? 1 : 1 + half);
+        const uint32_t idesc = FP8 ? umma_idesc_e4m3(128, N, true, false) : umma_idesc_bf16(128, N, true, false);
+        for (uint32_t k = 0; k < steps; ++k) {
+            // 16 bits: one accumulation per unit; 8 bits: one per step
+            if (FP8 || k == 0) {
+                if (!(ok = warp_await_mbar(&sm->acc_empty[buf.i], buf.phase ^ 1u, w, SITE_ACC_EMPTY))) break;
+            }
+            if (!(ok = warp_await_mbar(&sm->rows_in[st.i], st.phase, w, SITE_STAGE_FULL))) break;
+            if (!(ok = warp_await_mbar(&sm->weights_in[st.i], st.phase, w, SITE_STAGE_FULL))) break;
+            tc_fence_after();
+            const uint32_t d = tmem + buf.i * 2u * acc_stride;
+            const uint32_t a = ring + st.i * STAGE_F<FP8>, b = a + STEP_BYTES;
+            issued = true;
+            // Rows K-major: 32 bytes per instruction along their swizzle span.
+            // Weights M-major, K rows in groups of 8 that lie 1024 bytes apart.  8
+            // bits: 128 columns are one swizzle span, 4 KiB per K = 32.  16 bits: two
+            // 64-column chunks 8 KiB apart, 2 KiB per K = 16.
+            constexpr uint32_t CHUNK = FP8 ? 16384 : 8192, ADVANCE = FP8 ? 4096 : 2048;
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk) {
+                const uint64_t a0 = umma_desc_sw128(a + kk * ADVANCE, CHUNK, 1024);
+                const uint64_t a1 = umma_desc_sw128(a + 16384 + kk * ADVANCE, CHUNK, 1024);
+                const uint64_t bd = umma_desc_sw128(b + kk * 32, 16, 1024);
                 if constexpr (FP8) {
-                    // 128 columns of weights are one swizzle span; K rows in groups of 8,
-                    // 1024 bytes apart: 4 KiB per K = 32
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint64_t bd = umma_desc_sw128(b + kk * 32, 16, 1024);
-                        tc_mma_f8_elect(d, umma_desc_sw128(a + kk * 4096, 16384, 1024), bd, idesc, kk != 0);
-                        tc_mma_f8_elect(d + rg.acc_stride, umma_desc_sw128(a + 16384 + kk * 4096, 16384, 1024), bd,
-                                        idesc, kk != 0);
-                    }
+                    tc_mma_f8_elect(d, a0, bd, idesc, kk != 0);
+                    tc_mma_f8_elect(d + acc_stride, a1, bd, idesc, kk != 0);
                 } else {
-                    // two 64-column chunks 8 KiB apart; 2 KiB per K = 16
-                    const int parts = ph + 1;
-#pragma unroll
-                    for (int kk = 0; kk < 4; ++kk) {
-                        const uint64_t a0 = umma_desc_sw128(a + kk * 2048, 8192, 1024);
-                        const uint64_t a1 = umma_desc_sw128(a + 16384 + kk * 2048, 8192, 1024);
-                        for (int q = 0; q < parts; ++q) {
-                            const uint64_t bd = umma_desc_sw128(b + q * N * 128 + kk * 32, 16, 1024);
-                            const uint32_t add = k != s.k0 || kk != 0 || q != 0;
-                            tc_mma_f16_elect(d, a0, bd, idesc, add);
-                            tc_mma_f16_elect(d + rg.acc_stride, a1, bd, idesc, add);
-                        }
-                    }
+                    tc_mma_f16_elect(d, a0, bd, idesc, k != 0 || kk != 0);
+                    tc_mma_f16_elect(d + acc_stride, a1, bd, idesc, k != 0 || kk != 0);
                 }
-                tc_commit_elect(&sm->empty[st.i]);
-                st.next(rg.stages);
-                if (FP8 || k + 1 == s.k1) {
-                    tc_commit_elect(&sm->acc_full[buf.i]);
-                    buf.next(rg.bufs);
-                }
+            }
+            tc_commit_elect(&sm->empty[st.i]);
+            st.next(STAGES_F);
+            if (FP8 || k + 1 == steps) {
+                tc_commit_elect(&sm->acc_full[buf.i]);
+                buf.next(bufs);
             }
         }
     }
@@ -541,242 +597,340 @@ __device__ void products(FfnSmem* sm, const Ring& rg, const Half (&half)[2], con
     __syncwarp();
 }
 
-__device__ __forceinline__ float* slot_of(const FfnParams& p, uint32_t cta, int which) {
-    return p.slots + (size_t(cta) * SLOTS + which) * size_t(p.T) * ACC_COLS;
-}
-
-// Pieces of a tile: CTAs [c0, c0 + n); the piece of CTA c lies in its slot
-// `first` if the tile holds the CTA's first step, else in the next one.
-struct Pieces {
-    uint32_t c0, n, begin;
-};
-__device__ __forceinline__ Pieces pieces_of(const Half& h, uint32_t tile) {
-    Pieces q;
-    q.begin = tile * h.ks;
-    q.c0 = h.owner(q.begin);
-    q.n = h.owner(q.begin + h.ks - 1) - q.c0 + 1;
-    return q;
-}
-__device__ __forceinline__ const float* piece(const FfnParams& p, const Half& h, const Pieces& q, uint32_t i,
-                                              int first) {
-    const uint32_t c = q.c0 + i;
-    return slot_of(p, c, first + (h.first_step(c) >= q.begin ? 0 : 1));
-}
-
-// h of a complete tile from its pieces, by the eight draining warps.
-template <bool FP8>
-__device__ void finish_tile(const FfnParams& p, FfnSmem* sm, const Half& hf, const Piece& s, const Pieces& q) {
-    const int et = threadIdx.x - WARP_EPI * 32, f = et & 127, side = et >> 7;
-    const int n = sm->count[s.a], off = sm->off[s.a], col = s.blk * 128 + f;
-    const size_t R = size_t(p.T) * p.k;
-    for (int i = side; i < n; i += 2) {
-        float a = 0.f, b = 0.f;
-        for (uint32_t j = 0; j < q.n; ++j) {
-            const float* src = q.n == 1 ? slot_of(p, q.c0, 2) : piece(p, hf, q, j, 0);
-            a += __ldcg(src + size_t(i) * ACC_COLS + f);
-            b += __ldcg(src + size_t(i) * ACC_COLS + 128 + f);
-        }
-        const float v = a / (1.f + expf(-a)) * b;
-        const size_t at = size_t(off + i) * p.F + col;
-        if constexpr (FP8) {
-            float top = fabsf(v);
+// A block of 256 columns of a part's h from its pieces, by one warp: eight
+// columns per lane.  ROWS rows and BATCH pieces of each matrix are loaded
+// together.
+template <bool FP8, int ROWS, int BATCH>
+__device__ __forceinline__ void complete_rows(const FfnParams& p, const Plan& pl, const Unit& s) {
+    const int lane = threadIdx.x & 31, col = s.blk * ACC_COLS + lane * 8;
+    const bool in = col < p.F;  // F is a multiple of 64
+    const size_t R = size_t(p.T) * p.k, stride = size_t(pl.blocks[0]) * ACC_COLS;
+    const int chunks = int(pl.chunks[0]);
+    for (int i0 = 0; i0 < s.n; i0 += ROWS) {
+        float v[2][ROWS][8];
 #pragma unroll
-            for (int d = 16; d > 0; d >>= 1) top = nan_max(top, __shfl_xor_sync(0xffffffffu, top, d));
-            float* red = sm->red[side][(i >> 1) & 1];
-            if ((f & 31) == 0) red[f >> 5] = top;
-            if (side == 0) bar_sync<2, 128>();
-            else bar_sync<3, 128>();
-            top = nan_max(nan_max(red[0], red[1]), nan_max(red[2], red[3]));
-            const float scale = top < TINY ? 1.f : top / E4M3_TOP;
-            p.h[at] = uint8_t(__nv_cvt_float_to_fp8(v * (1.f / scale), __NV_SATFINITE, __NV_E4M3));
-            if (f == 0) p.h_scale[size_t(off + i) * (p.F / GROUP8) + s.blk] = scale;
-        } else if (col < p.F) {
-            const __nv_bfloat16 hi = __float2bfloat16_rn(v);
-            __nv_bfloat16* h = reinterpret_cast<__nv_bfloat16*>(p.h);
-            h[at] = hi;
-            h[R * p.F + at] = __float2bfloat16_rn(v - __bfloat162float(hi));
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+            for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) v[m][r][i] = 0.f;
+        const float* src = piece_row(p, pl, 0, 0, s.off + i0) + col;
+        for (int c = 0; c < chunks; c += BATCH) {
+            float4 u[2][BATCH][ROWS][2];
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int x = 0; x < BATCH; ++x)
+#pragma unroll
+                    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            u[m][x][r][q] = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (in && c + x < chunks && i0 + r < s.n)
+                                u[m][x][r][q] = __ldcg(reinterpret_cast<const float4*>(
+                                    src + (size_t(m * chunks + c + x) * R + r) * stride + 4 * q));
+                        }
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int x = 0; x < BATCH; ++x)
+#pragma unroll
+                    for (int r = 0; r < ROWS; ++r)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) v[m][r][i] += (&u[m][x][r][i >> 2].x)[i & 3];
+        }
+#pragma unroll
+        for (int r = 0; r < ROWS; ++r) {
+            if (i0 + r >= s.n) break;
+            float* h = v[0][r];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h[i] = h[i] / (1.f + expf(-h[i])) * v[1][r][i];
+            const int row = s.off + i0 + r;
+            const size_t at = size_t(row) * p.F + col;
+            if constexpr (FP8) {
+                // 16 lanes hold a group of 128 columns
+                float top = 0.f;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) top = nan_max(top, fabsf(h[i]));
+#pragma unroll
+                for (int d = 8; d > 0; d >>= 1) top = nan_max(top, __shfl_xor_sync(0xffffffffu, top, d));
+                const float scale = top < TINY ? 1.f : top / E4M3_TOP, inv = 1.f / scale;
+                uint32_t q[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    q[i] = __nv_cvt_float2_to_fp8x2(make_float2(h[2 * i] * inv, h[2 * i + 1] * inv), __NV_SATFINITE,
+                                                    __NV_E4M3);
+                if (in) {
+                    *reinterpret_cast<uint2*>(p.h + at) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
+                    if ((lane & 15) == 0) p.h_scale[size_t(row) * (p.F / GROUP8) + 2 * s.blk + (lane >> 4)] = scale;
+                }
+            } else if (in) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __nv_bfloat162 b = __floats2bfloat162_rn(h[2 * i], h[2 * i + 1]);
+                    const __nv_bfloat162 l =
+                        __floats2bfloat162_rn(h[2 * i] - __low2float(b), h[2 * i + 1] - __high2float(b));
+                    hi[i] = *reinterpret_cast<const uint32_t*>(&b);
+                    lo[i] = *reinterpret_cast<const uint32_t*>(&l);
+                }
+                *reinterpret_cast<uint4*>(p.h + at * 2) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                *reinterpret_cast<uint4*>(p.h + (R * p.F + at) * 2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            }
         }
     }
 }
 
+// The completing warps: each follows every fourth of the CTA's units, counts
+// its piece once it is stored, and completes the block of h if that piece was
+// the last.  (The weights in flight make any round trip to L2 take several
+// microseconds, so these must not wait one after the other.)
 template <bool FP8>
-__device__ void drain_accumulators(const FfnParams& p, FfnSmem* sm, const Ring& rg, const Half (&half)[2],
-                                   const Waiter& w) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int quad = warp & 3, set = (warp - WARP_EPI) >> 2;
-    const int et = threadIdx.x - WARP_EPI * 32;
-    constexpr int MAXB = FFN_MAX_T / 32;  // blocks of 16 columns per warp
-    const uint32_t tq = sm->tmem_base + (uint32_t(quad * 32) << 16);
-    Turn buf, sc;
-    // A wait that gave up only stops the work: the barriers that the eight
-    // warps share are still reached by all of them.
-    bool ok = true;
-    for (int ph = 0; ph < 2; ++ph) {
-        const Half& hf = half[ph];
-        uint32_t pos = hf.start;
-        Piece s;
-        while (next_piece(hf, pos, s)) {
-            const int n = sm->count[s.a], off = sm->off[s.a];
-            const int nblk = pad16(n) / 16;
-            const Pieces q = pieces_of(hf, s.tile);
-            const bool whole = q.n == 1;
-            // where the sums go: row i, this lane's columns f (first accumulator) and 128 + f
-            const int f = quad * 32 + lane;
-            float* dst;
-            size_t stride = ACC_COLS;
-            bool in0 = true, in1 = true;
-            if (ph == 1 && whole) {
-                const int col = s.blk * ACC_COLS + f;
-                dst = p.y + size_t(off) * p.H + col;
-                stride = size_t(p.H);
-                in0 = col < p.H;
-                in1 = col + 128 < p.H;
-            } else {
-                const int which = ph == 0 ? (whole ? 2 : hf.start >= q.begin ? 0 : 1) : (hf.start >= q.begin ? 3 : 4);
-                dst = slot_of(p, blockIdx.x, which) + f;
-            }
-            auto put = [&](int blk, const float (&v0)[16], const float (&v1)[16]) {
+__device__ void complete_h(const FfnParams& p, FfnSmem* sm, const Plan& pl, const Waiter& w) {
+    const int lane = threadIdx.x & 31;
+    uint32_t it = threadIdx.x / 32 - WARP_FIN;
+    for (;; it += FIN_WARPS) {
+        const uint32_t slot = it % INFO_SLOTS, phase = it / INFO_SLOTS & 1u;
+        if (!warp_await_mbar(&sm->info_in[slot], phase, w, SITE_INFO_FULL)) return;
+        const Unit s = sm->unit[slot];
+        if (s.end) return;
+        // the slot is given back only after its piece, so that no second one comes in unseen
+        if (!warp_await_mbar(&sm->piece_in[slot], phase, w, SITE_INFO_FULL)) return;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->info_out[slot]);
+        if (s.half) continue;
+        uint32_t count = 0;
+        const uint32_t all = 2 * pl.chunks[0];
+        if (lane == 0) {
+            // releases the draining warps' stores, which the wait above has seen
+            uint32_t* a = &p.ctl->arrived[uint32_t(s.a) * pl.blocks[0] + s.blk];
+            count = atom_add_acq_rel_u32(a, 1u) + 1u;
+            if (count == all) *a = 0u;
+        }
+        if (__shfl_sync(0xffffffffu, count, 0) != all) continue;
+        __threadfence();
+        // about as many loads in flight either way
+        if (all == 2) complete_rows<FP8, 4, 1>(p, pl, s);
+        else if (all == 4) complete_rows<FP8, 2, 2>(p, pl, s);
+        else complete_rows<FP8, 1, 4>(p, pl, s);
+        __threadfence();
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) atom_add_acq_rel_u32(&p.ctl->ready[s.a], 1u);
+    }
+}
+
+// 8 bits: `steps` steps of one matrix, each with its own scales, summed in
+// registers: up to B blocks of 16 rows for this warp (set, set + 2, ...).
+template <int B, typename Put>
+__device__ __forceinline__ bool drain_steps8(FfnSmem* sm, const Accs& rg, const Waiter& w, uint32_t tq, uint32_t steps,
+                                             int set, int nblk, Turn& buf, Turn& sc, bool ok, const Put& put) {
+    const int lane = threadIdx.x & 31;
+    const float* scales = reinterpret_cast<const float*>(ffn_ring() + SCALE_AT);
+    float acc0[B][16], acc1[B][16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int r = blk * 16 + i;
-                    if (r < n) {
-                        float* d = dst + size_t(r) * stride;
-                        if (in0) __stcg(d, v0[i]);
-                        if (in1) __stcg(d + 128, v1[i]);
+    for (int b = 0; b < B; ++b)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) acc0[b][i] = acc1[b][i] = 0.f;
+    for (uint32_t k = 0; k < steps; ++k) {
+        if (ok) ok = warp_await_mbar(&sm->scales_in[sc.i], sc.phase, w, SITE_ACC_FULL);
+        if (ok) ok = warp_await_mbar(&sm->acc_full[buf.i], buf.phase, w, SITE_ACC_FULL);
+        if (ok) {
+            tc_fence_after();
+            const uint32_t t0 = tq + buf.i * 2u * rg.acc_stride;
+            const float* scale = scales + sc.i * SCALE_FLOATS;
+            const float c0 = scale[MAX_N], c1 = scale[MAX_N + 1];
+#pragma unroll
+            for (int b = 0; b < B; ++b) {
+                const int blk = set + 2 * b;
+                if (blk < nblk) {
+                    uint32_t r0[16], r1[16];
+                    tmem_ld_32x32b_x16(t0 + blk * 16, r0);
+                    tmem_ld_32x32b_x16(t0 + rg.acc_stride + blk * 16, r1);
+                    float4 x[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = *reinterpret_cast<const float4*>(scale + blk * 16 + 4 * i);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float v = (&x[i >> 2].x)[i & 3];
+                        acc0[b][i] = fmaf(__uint_as_float(r0[i]), v * c0, acc0[b][i]);
+                        acc1[b][i] = fmaf(__uint_as_float(r1[i]), v * c1, acc1[b][i]);
                     }
-                }
-            };
-            if constexpr (!FP8) {
-                if (ok) ok = warp_await_mbar(&sm->acc_full[buf.i], buf.phase, w, SITE_ACC_FULL);
-                if (ok) {
-                    tc_fence_after();
-                    const uint32_t t0 = tq + buf.i * 2u * rg.acc_stride;
-                    for (int blk = set; blk < nblk; blk += 2) {
-                        uint32_t r0[16], r1[16];
-                        tmem_ld_32x32b_x16(t0 + blk * 16, r0);
-                        tmem_ld_32x32b_x16(t0 + rg.acc_stride + blk * 16, r1);
-                        tmem_ld_wait();
-                        float v0[16], v1[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            v0[i] = __uint_as_float(r0[i]);
-                            v1[i] = __uint_as_float(r1[i]);
-                        }
-                        put(blk, v0, v1);
-                    }
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&sm->acc_empty[buf.i]);
-                }
-                buf.next(rg.bufs);
-            } else {
-                float acc0[MAXB][16], acc1[MAXB][16];
-#pragma unroll
-                for (int b = 0; b < MAXB; ++b)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) acc0[b][i] = acc1[b][i] = 0.f;
-                for (uint32_t k = s.k0; k < s.k1; ++k) {
-                    if (ok) ok = warp_await_mbar(&sm->scales_in[sc.i], sc.phase, w, SITE_ACC_FULL);
-                    if (ok) ok = warp_await_mbar(&sm->acc_full[buf.i], buf.phase, w, SITE_ACC_FULL);
-                    if (ok) {
-                        tc_fence_after();
-                        const uint32_t t0 = tq + buf.i * 2u * rg.acc_stride;
-                        const float* scale =
-                            reinterpret_cast<const float*>(ffn_ring() + SCALE_AT) + sc.i * SCALE_FLOATS;
-                        const float c0 = scale[FFN_MAX_T], c1 = scale[FFN_MAX_T + 1];
-#pragma unroll
-                        for (int b = 0; b < MAXB; ++b) {
-                            const int blk = set + 2 * b;
-                            if (blk < nblk) {
-                                uint32_t r0[16], r1[16];
-                                tmem_ld_32x32b_x16(t0 + blk * 16, r0);
-                                tmem_ld_32x32b_x16(t0 + rg.acc_stride + blk * 16, r1);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int i = 0; i < 16; ++i) {
-                                    const float x = scale[blk * 16 + i];
-                                    acc0[b][i] = fmaf(__uint_as_float(r0[i]), x * c0, acc0[b][i]);
-                                    acc1[b][i] = fmaf(__uint_as_float(r1[i]), x * c1, acc1[b][i]);
-                                }
-                            }
-                        }
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) {
-                            mbar_arrive(&sm->acc_empty[buf.i]);
-                            mbar_arrive(&sm->scales_out[sc.i]);
-                        }
-                    }
-                    buf.next(rg.bufs);
-                    sc.next(SCALE_SLOTS);
-                }
-                if (ok) {
-#pragma unroll
-                    for (int b = 0; b < MAXB; ++b)
-                        if (set + 2 * b < nblk) put(set + 2 * b, acc0[b], acc1[b]);
                 }
             }
-            if (ph == 0) {
-                // the CTA that delivers a tile's last piece completes the tile
-                __threadfence();
-                bar_sync<1, EPI_THREADS>();
-                if (!whole) {
-                    if (et == 0) {
-                        uint32_t* a = &p.ctl->arrived[s.tile];
-                        const bool last = atom_add_acq_rel_u32(a, 1u) == q.n - 1;
-                        if (last) *a = 0u;
-                        sm->last = last;
-                        __threadfence();
-                    }
-                    bar_sync<1, EPI_THREADS>();
-                }
-                if (whole || sm->last) {
-                    finish_tile<FP8>(p, sm, hf, s, q);
-                    __threadfence();
-                    fence_proxy_async();
-                    bar_sync<1, EPI_THREADS>();
-                    if (et == 0 && ok) atom_add_acq_rel_u32(&p.ctl->ready[s.a], 1u);
-                }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&sm->acc_empty[buf.i]);
+                mbar_arrive(&sm->scales_out[sc.i]);
             }
         }
+        buf.next(rg.bufs);
+        sc.next(SCALE_SLOTS);
+    }
+    if (ok) {
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (set + 2 * b < nblk) put(set + 2 * b, acc0[b], acc1[b]);
+    }
+    return ok;
+}
+
+template <bool FP8>
+__device__ void drain_accumulators(const FfnParams& p, FfnSmem* sm, const Accs& rg, const Plan& pl, const Waiter& w) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int quad = warp & 3, set = (warp - WARP_EPI) >> 2;
+    const uint32_t tq = sm->tmem_base + (uint32_t(quad * 32) << 16);
+    Turn buf, sc, in, done;
+    bool ok = true;
+    Unit s;
+    while (ok && next_unit(sm, in, w, s, ok)) {
+        const int n = s.n, nblk = pad16(n) / 16;
+        // where the sums go: row i, this lane's columns f (first accumulator) and 128 + f
+        const size_t stride = size_t(pl.blocks[s.half]) * ACC_COLS;
+        float* to = piece_row(p, pl, s.half, s.second * pl.chunks[0] + s.c, s.off) + s.blk * ACC_COLS + quad * 32 + lane;
+        auto put = [&](int blk, const float (&v0)[16], const float (&v1)[16]) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int r = blk * 16 + i;
+                if (r < n) {
+                    __stcg(to + size_t(r) * stride, v0[i]);
+                    __stcg(to + size_t(r) * stride + 128, v1[i]);
+                }
+            }
+        };
+        if constexpr (!FP8) {
+            ok = warp_await_mbar(&sm->acc_full[buf.i], buf.phase, w, SITE_ACC_FULL);
+            if (ok) {
+                tc_fence_after();
+                const uint32_t t0 = tq + buf.i * 2u * rg.acc_stride;
+                for (int blk = set; blk < nblk; blk += 2) {
+                    uint32_t r0[16], r1[16];
+                    float v0[16], v1[16];
+                    tmem_ld_32x32b_x16(t0 + blk * 16, r0);
+                    tmem_ld_32x32b_x16(t0 + rg.acc_stride + blk * 16, r1);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        v0[i] = __uint_as_float(r0[i]);
+                        v1[i] = __uint_as_float(r1[i]);
+                    }
+                    if (s.half) {
+                        // the products of h's remainders
+                        tmem_ld_32x32b_x16(t0 + (nblk + blk) * 16, r0);
+                        tmem_ld_32x32b_x16(t0 + rg.acc_stride + (nblk + blk) * 16, r1);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            v0[i] += __uint_as_float(r0[i]);
+                            v1[i] += __uint_as_float(r1[i]);
+                        }
+                    }
+                    put(blk, v0, v1);
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sm->acc_empty[buf.i]);
+            }
+            buf.next(rg.bufs);
+        } else {
+            // as few registers as the rows need
+            const uint32_t steps = s.k1 - s.k0;
+            if ((nblk - set + 1) / 2 <= 1) ok = drain_steps8<1>(sm, rg, w, tq, steps, set, nblk, buf, sc, ok, put);
+            else ok = drain_steps8<2>(sm, rg, w, tq, steps, set, nblk, buf, sc, ok, put);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->piece_in[done.i]);
+        done.next(INFO_SLOTS);
     }
     __threadfence();
 }
 
-// out[t] = sum over the k choices, in order, of gate * (the row's pieces, in order).
-__device__ void combine_rows(const FfnParams& p, const FfnSmem* sm, const Half& hf) {
-    const int lane = threadIdx.x & 31;
-    const int nb = (p.H + 127) / 128;
-    for (int item = blockIdx.x * FFN_WARPS + (threadIdx.x >> 5); item < p.T * nb; item += gridDim.x * FFN_WARPS) {
-        const int t = item / nb, cb = item - t * nb, col = cb * 128 + lane * 4;
-        if (col >= p.H) continue;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int j = 0; j < p.k; ++j) {
-            const int i = t * p.k + j, a = sm->act_of[i], r = sm->row_of[i];
-            const Pieces q = pieces_of(hf, uint32_t(a) * hf.blocks + uint32_t(cb >> 1));
-            float4 v;
-            if (q.n == 1) {
-                v = __ldcg(reinterpret_cast<const float4*>(p.y + size_t(r) * p.H + col));
-            } else {
-                v = make_float4(0.f, 0.f, 0.f, 0.f);
-                const size_t at = size_t(r - sm->off[a]) * ACC_COLS + (cb & 1) * 128 + lane * 4;
-                for (uint32_t c = 0; c < q.n; ++c) {
-                    const float4 u = __ldcg(reinterpret_cast<const float4*>(piece(p, hf, q, c, 3) + at));
-                    v.x += u.x;
-                    v.y += u.y;
-                    v.z += u.z;
-                    v.w += u.w;
+__device__ __forceinline__ void add4(float4& a, const float4& b) {
+    a.x += b.x;
+    a.y += b.y;
+    a.z += b.z;
+    a.w += b.w;
+}
+__device__ __forceinline__ void fma4(float4& a, float g, const float4& b) {
+    a.x = fmaf(g, b.x, a.x);
+    a.y = fmaf(g, b.y, a.y);
+    a.z = fmaf(g, b.z, a.z);
+    a.w = fmaf(g, b.w, a.w);
+}
+__device__ __forceinline__ void store_out(const FfnParams& p, int t, int col, const float4& v) {
+    const __nv_bfloat162 b0 = __floats2bfloat162_rn(v.x, v.y), b1 = __floats2bfloat162_rn(v.z, v.w);
+    *reinterpret_cast<uint2*>(p.out + size_t(t) * p.H + col) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
+}
+
+// out[t] = sum over the k choices, in order, of gate * the row's pieces, in order.
+__device__ void combine_rows(const FfnParams& p, const FfnSmem* sm, const Plan& pl) {
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int chunks = int(pl.chunks[1]), all = p.k * chunks;  // pieces of a token, choice by choice
+    // piece i of token t at column col, and its gate
+    auto load = [&](int t, int i, int col, float& g) {
+        const int j = i / chunks, c = i - j * chunks;
+        g = sm->gate[t * p.k + j];
+        return __ldcg(reinterpret_cast<const float4*>(piece_row(p, pl, 1, uint32_t(c), sm->row_of[t * p.k + j]) + col));
+    };
+    const int nb128 = (p.H + 127) / 128;
+    constexpr int TOGETHER = 8;  // loads in flight
+    if (all <= TOGETHER || p.T * nb128 >= int(gridDim.x) * FFN_WARPS / 2) {
+        // 128 columns of a token per warp
+        for (int item = blockIdx.x * FFN_WARPS + (tid >> 5); item < p.T * nb128; item += gridDim.x * FFN_WARPS) {
+            const int t = item / nb128, col = (item - t * nb128) * 128 + lane * 4;
+            if (col >= p.H) continue;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int i = 0; i < all; i += TOGETHER) {
+                float4 u[TOGETHER];
+                float g[TOGETHER];
+#pragma unroll
+                for (int x = 0; x < TOGETHER; ++x) {
+                    u[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                    g[x] = 0.f;
+                    if (i + x < all) u[x] = load(t, i + x, col, g[x]);
                 }
+#pragma unroll
+                for (int x = 0; x < TOGETHER; ++x)
+                    if (i + x < all) fma4(acc, g[x], u[x]);
             }
-            const float g = sm->gate[i];
-            acc.x = fmaf(g, v.x, acc.x);
-            acc.y = fmaf(g, v.y, acc.y);
-            acc.z = fmaf(g, v.z, acc.z);
-            acc.w = fmaf(g, v.w, acc.w);
+            store_out(p, t, col, acc);
         }
-        const __nv_bfloat162 b0 = __floats2bfloat162_rn(acc.x, acc.y), b1 = __floats2bfloat162_rn(acc.z, acc.w);
-        *reinterpret_cast<uint2*>(p.out + size_t(t) * p.H + col) =
-            make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
+        return;
+    }
+    // few rows in many pieces: 64 columns of a token per CTA, the pieces over
+    // its threads, summed in shared memory
+    constexpr int COLS = 16, SHARE = FFN_THREADS / COLS;  // float4 columns, threads per column
+    float4* red = reinterpret_cast<float4*>(ffn_ring());
+    const int c4 = tid % COLS, who = tid / COLS;
+    const int nb = p.H / 64, each = (all + SHARE - 1) / SHARE;
+    for (int item = blockIdx.x; item < p.T * nb; item += gridDim.x) {
+        const int t = item / nb, col = (item - t * nb) * 64 + c4 * 4;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        const int i1 = min(all, (who + 1) * each);
+        constexpr int BATCH = 4;
+        for (int i = who * each; i < i1; i += BATCH) {
+            float4 u[BATCH];
+            float g[BATCH];
+#pragma unroll
+            for (int x = 0; x < BATCH; ++x) {
+                u[x] = make_float4(0.f, 0.f, 0.f, 0.f);
+                g[x] = 0.f;
+                if (i + x < i1) u[x] = load(t, i + x, col, g[x]);
+            }
+#pragma unroll
+            for (int x = 0; x < BATCH; ++x)
+                if (i + x < i1) fma4(acc, g[x], u[x]);
+        }
+        red[tid] = acc;
+        __syncthreads();
+        if (who == 0) {
+            for (int x = 1; x < SHARE; ++x) add4(acc, red[x * COLS + c4]);
+            store_out(p, t, col, acc);
+        }
+        __syncthreads();
     }
 }
 
@@ -792,7 +946,7 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
     const Waiter wp{p.err, &p.ctl->abort, 2 * FFN_SPIN_NS};
 
     if (tid == 0) {
-        for (int i = 0; i < FFN_MAX_STAGES; ++i) {
+        for (int i = 0; i < STAGES_F; ++i) {
             mbar_init(&sm->weights_in[i], 1);
             mbar_init(&sm->rows_in[i], 1);
             mbar_init(&sm->empty[i], 1);
@@ -804,6 +958,11 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
         for (int i = 0; i < SCALE_SLOTS; ++i) {
             mbar_init(&sm->scales_in[i], 32);
             mbar_init(&sm->scales_out[i], EPI_WARPS);
+        }
+        for (int i = 0; i < INFO_SLOTS; ++i) {
+            mbar_init(&sm->info_in[i], 1);
+            mbar_init(&sm->info_out[i], 3 + EPI_WARPS);  // row loads, products, draining, one completing warp
+            mbar_init(&sm->piece_in[i], EPI_WARPS);
         }
         mbar_init(&sm->drain, 1);
         fence_barrier_init();
@@ -849,20 +1008,17 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
         __syncthreads();
         tc_fence_after();
 
-        constexpr int KB = FP8 ? 128 : 64;
-        const Half half[2] = {make_half(p.H / KB, (p.F + 127) / 128, sm->chosen),
-                              make_half(p.F / KB, (p.H + ACC_COLS - 1) / ACC_COLS, sm->chosen)};
-        Ring rg;
+        const Plan pl = make_plan(p, FP8 ? 128 : 64, uint32_t(sm->parts), uint32_t(sm->most));
+        Accs rg;
         const int N = pad16(sm->most);
-        rg.acc_stride = uint32_t(N);
-        rg.stage_bytes = uint32_t(STEP_BYTES + N * 128 * (FP8 ? 1 : 2));
-        rg.stages = min(uint32_t(FFN_MAX_STAGES), uint32_t(FP8 ? SCALE_AT : RING_BYTES) / rg.stage_bytes);
-        rg.bufs = FP8 ? min(uint32_t(FFN_MAX_BUFS), 512u / (2u * rg.acc_stride)) : 2u;
+        rg.acc_stride = uint32_t(N * (FP8 ? 1 : 2));
+        rg.bufs = min(uint32_t(FFN_MAX_BUFS), 512u / (2u * rg.acc_stride));
 
-        if (warp == WARP_A) weight_loads<FP8>(p, m, sm, rg, half, wp);
-        else if (warp == WARP_B) row_loads<FP8>(p, m, sm, rg, half, w);
-        else if (warp == WARP_MMA) products<FP8>(sm, rg, half, wp);
-        else drain_accumulators<FP8>(p, sm, rg, half, wp);
+        if (warp == WARP_A) weight_loads<FP8>(p, m, sm, pl, wp);
+        else if (warp == WARP_B) row_loads<FP8>(p, m, sm, pl, w);
+        else if (warp == WARP_MMA) products<FP8>(sm, rg, wp);
+        else if (warp >= WARP_FIN) complete_h<FP8>(p, sm, pl, wp);
+        else drain_accumulators<FP8>(p, sm, rg, pl, wp);
 
         __syncthreads();
         if (tid == 0) {
@@ -871,7 +1027,7 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
             sm->ok = await_geq(&p.ctl->done, gridDim.x, w, SITE_BAR_COMPUTED) && ld_relaxed_u32(w.abort) == 0u;
         }
         __syncthreads();
-        if (sm->ok) combine_rows(p, sm, half[1]);
+        if (sm->ok) combine_rows(p, sm, pl);
     }
     tc_fence_before();
     __syncthreads();
@@ -884,7 +1040,8 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
         FfnCtl* c = p.ctl;
         c->routed = 0;
         c->done = 0;
-        for (int i = 0; i < MAX_E; ++i) c->ready[i] = 0;
+        c->next = 0;
+        for (int i = 0; i < MAX_PARTS; ++i) c->ready[i] = 0;
         if (c->abort != 0)
             for (int i = 0; i < MAX_TILES1; ++i) c->arrived[i] = 0;  // a call that gave up left some
         c->abort = 0;
@@ -894,7 +1051,7 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
 }
 
 struct FfnLayout {
-    size_t ctl, ids, gates, h, h_scale, y, slots, total;
+    size_t ctl, ids, gates, h, h_scale, piece[2], room[2], total;
 };
 
 FfnLayout ffn_layout(int T, int H, int F, int k, bool fp8) {
@@ -906,8 +1063,12 @@ FfnLayout ffn_layout(int T, int H, int F, int k, bool fp8) {
     L.gates = o;    o = ws_align(o + R * 4);
     L.h = o;        o = ws_align(o + R * F * (fp8 ? 1 : 4));
     L.h_scale = o;  o = ws_align(o + (fp8 ? R * (F / GROUP8) * 4 : 0));
-    L.y = o;        o = ws_align(o + R * H * 4);
-    L.slots = o;    o = ws_align(o + size_t(FFN_MAX_CTAS) * SLOTS * T * ACC_COLS * 4);
+    for (int i = 0; i < 2; ++i) {
+        const size_t cols = (size_t(i == 0 ? F : H) + ACC_COLS - 1) / ACC_COLS * ACC_COLS;
+        L.room[i] = std::max(PIECE_FLOATS, R * cols * (i == 0 ? 2 : 1));  // one unit along K always fits
+        L.piece[i] = o;
+        o = ws_align(o + L.room[i] * 4);
+    }
     L.total = o;
     return L;
 }
@@ -998,8 +1159,10 @@ extern "C" mk_status_t mk_moe_ffn_decode(const void* x, const float* x_scale, co
     p.gates = reinterpret_cast<float*>(ws + L.gates);
     p.h = ws + L.h;
     p.h_scale = reinterpret_cast<float*>(ws + L.h_scale);
-    p.y = reinterpret_cast<float*>(ws + L.y);
-    p.slots = reinterpret_cast<float*>(ws + L.slots);
+    for (int i = 0; i < 2; ++i) {
+        p.piece[i] = reinterpret_cast<float*>(ws + L.piece[i]);
+        p.room[i] = L.room[i];
+    }
     p.err = err;
     p.T = T;
     p.H = H;
