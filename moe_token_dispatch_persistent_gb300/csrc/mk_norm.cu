@@ -15,6 +15,7 @@
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 
 #include "mk.h"
@@ -61,24 +62,27 @@ __device__ __forceinline__ int column(int chunk, int lane, int i) {
     return chunk * NORM_CHUNK + (VEC ? lane * 8 + i : lane + 32 * i);
 }
 
+// A lane's eight elements of a chunk, two to a word, zeros past the row's end.
 template <bool VEC>
-__device__ __forceinline__ void load8(const __nv_bfloat16* row, int chunk, int lane, int H, float (&v)[8]) {
+__device__ __forceinline__ uint4 load8(const __nv_bfloat16* row, int chunk, int lane, int H) {
     if constexpr (VEC) {
         const int c = column<true>(chunk, lane, 0);
-        const uint4 q = c < H ? __ldcs(reinterpret_cast<const uint4*>(row + c)) : make_uint4(0, 0, 0, 0);
-        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+        return c < H ? __ldcs(reinterpret_cast<const uint4*>(row + c)) : make_uint4(0, 0, 0, 0);
+    } else {
+        uint32_t u[4];
+        const uint16_t* r = reinterpret_cast<const uint16_t*>(row);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(u[i] << 16);
-            v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+            const int c0 = column<false>(chunk, lane, 2 * i), c1 = column<false>(chunk, lane, 2 * i + 1);
+            u[i] = (c0 < H ? uint32_t(r[c0]) : 0u) | (c1 < H ? uint32_t(r[c1]) << 16 : 0u);
         }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int c = column<false>(chunk, lane, i);
-            v[i] = c < H ? __bfloat162float(row[c]) : 0.f;
-        }
+        return make_uint4(u[0], u[1], u[2], u[3]);
     }
+}
+
+__device__ __forceinline__ float element(const uint4& q, int i) {
+    const uint32_t u = (&q.x)[i >> 1];
+    return __uint_as_float(i & 1 ? u & 0xffff0000u : u << 16);
 }
 
 template <bool VEC>
@@ -92,7 +96,7 @@ __device__ __forceinline__ void store8(__nv_bfloat16* row, int chunk, int lane, 
             const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
             u[i] = *reinterpret_cast<const uint32_t*>(&b);
         }
-        *reinterpret_cast<uint4*>(row + c) = make_uint4(u[0], u[1], u[2], u[3]);
+        __stcs(reinterpret_cast<uint4*>(row + c), make_uint4(u[0], u[1], u[2], u[3]));
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -141,8 +145,8 @@ __device__ __forceinline__ void quantize8(uint8_t* row, float* scale_row, int ch
     if constexpr (VEC) {
         const int c = column<true>(chunk, lane, 0);
         if (c < H)
-            *reinterpret_cast<uint2*>(row + c) =
-                make_uint2(q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24, q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24);
+            __stcs(reinterpret_cast<uint2*>(row + c), make_uint2(q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24,
+                                                                 q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24));
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -152,62 +156,69 @@ __device__ __forceinline__ void quantize8(uint8_t* row, float* scale_row, int ch
     }
 }
 
-// C chunks of a row per warp; warps_per_row * C chunks cover the row.
+// C chunks of a row per warp; warps_per_row * C chunks cover the row, and a
+// CTA's rows_per_cta rows are reduced together.  CTAs stay and take further
+// rows, whose loads are issued before the current ones are worked on (a CTA
+// per row instead: 107 us, not 97, for 16384 x 4096 with every output, 6.2
+// TB/s); the weights are loaded once.
 template <bool VEC, int C>
 __global__ void __launch_bounds__(NORM_MAX_WARPS * 32) mk_add_rmsnorm_kernel(const NormParams p) {
-    __shared__ float part[NORM_MAX_WARPS];
+    __shared__ float part[2][NORM_MAX_WARPS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int wpr = p.warps_per_row;
     const int mine = warp % wpr, first = warp - mine;
-    const int64_t row = int64_t(blockIdx.x) * p.rows_per_cta + warp / wpr;
-    const bool live = row < p.T;
-    const int H = p.H;
-    float z[C][8], w[C][8];
-    float sum = 0.f;
-    if (live) {
-        const __nv_bfloat16* xr = p.x + row * p.x_stride;
-        const __nv_bfloat16* rr = p.residual ? p.residual + row * p.residual_stride : nullptr;
+    const int H = p.H, groups = (H + NORM_GROUP - 1) / NORM_GROUP;
+    const int64_t stride = int64_t(gridDim.x) * p.rows_per_cta;
+    uint4 x[C], r[C], w[C];
+    auto fetch = [&](int64_t row) {
+        if (row >= p.T) return;
 #pragma unroll
-        for (int j = 0; j < C; ++j) load8<VEC>(xr, mine + j * wpr, lane, H, z[j]);
-        if (rr) {
-            float r[C][8];
+        for (int j = 0; j < C; ++j) x[j] = load8<VEC>(p.x + row * p.x_stride, mine + j * wpr, lane, H);
+        if (p.residual)
 #pragma unroll
-            for (int j = 0; j < C; ++j) load8<VEC>(rr, mine + j * wpr, lane, H, r[j]);
+            for (int j = 0; j < C; ++j) r[j] = load8<VEC>(p.residual + row * p.residual_stride, mine + j * wpr, lane, H);
+    };
+    int64_t base = int64_t(blockIdx.x) * p.rows_per_cta;
+    fetch(base + warp / wpr);
+#pragma unroll
+    for (int j = 0; j < C; ++j) w[j] = load8<VEC>(p.weight, mine + j * wpr, lane, H);
+    for (int turn = 0; base < p.T; base += stride, turn ^= 1) {
+        const int64_t row = base + warp / wpr;
+        const bool live = row < p.T;
+        float z[C][8];
+        float sum = 0.f;
+        if (live) {
 #pragma unroll
             for (int j = 0; j < C; ++j)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) z[j][i] += r[j][i];
+                for (int i = 0; i < 8; ++i) {
+                    z[j][i] = element(x[j], i);
+                    if (p.residual) z[j][i] += element(r[j], i);
+                    sum = fmaf(z[j][i], z[j][i], sum);
+                }
+            fetch(row + stride);
+            if (p.residual_out)
+#pragma unroll
+                for (int j = 0; j < C; ++j) store8<VEC>(p.residual_out + row * H, mine + j * wpr, lane, H, z[j]);
         }
-        // the weights do not depend on the sum: their loads run beside it
-#pragma unroll
-        for (int j = 0; j < C; ++j) load8<VEC>(p.weight, mine + j * wpr, lane, H, w[j]);
-#pragma unroll
-        for (int j = 0; j < C; ++j)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) sum = fmaf(z[j][i], z[j][i], sum);
-        if (p.residual_out)
-#pragma unroll
-            for (int j = 0; j < C; ++j) store8<VEC>(p.residual_out + row * H, mine + j * wpr, lane, H, z[j]);
-    }
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    if (wpr > 1) {  // the same for the whole CTA
-        if (lane == 0) part[warp] = sum;
-        __syncthreads();
-        sum = lane < wpr ? part[first + lane] : 0.f;
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-    }
-    if (!live) return;
-    const float rstd = rsqrtf(sum / float(H) + p.eps);
+        if (wpr > 1) {  // the same for the whole CTA
+            if (lane == 0) part[turn][warp] = sum;
+            __syncthreads();
+            sum = lane < wpr ? part[turn][first + lane] : 0.f;
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
+            for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        }
+        if (!live) continue;
+        const float rstd = rsqrtf(sum / float(H) + p.eps);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[j][i] = z[j][i] * rstd * w[j][i];
-        if (p.out) store8<VEC>(p.out + row * H, mine + j * wpr, lane, H, z[j]);
-        if (p.out8)
-            quantize8<VEC>(p.out8 + row * H, p.scale + row * ((H + NORM_GROUP - 1) / NORM_GROUP), mine + j * wpr, lane,
-                           H, z[j]);
+        for (int j = 0; j < C; ++j) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) z[j][i] = z[j][i] * rstd * element(w[j], i);
+            if (p.out) store8<VEC>(p.out + row * H, mine + j * wpr, lane, H, z[j]);
+            if (p.out8) quantize8<VEC>(p.out8 + row * H, p.scale + row * groups, mine + j * wpr, lane, H, z[j]);
+        }
     }
 }
 
@@ -261,10 +272,14 @@ extern "C" mk_status_t mk_add_rmsnorm(const void* x, int64_t x_stride, const voi
                      host_aligned(x, 16) && host_aligned(residual, 16) && host_aligned(weight, 16) &&
                      host_aligned(out, 16) && host_aligned(residual_out, 16) && host_aligned(out8, 8);
     const int chunks = (H + NORM_CHUNK - 1) / NORM_CHUNK;
-    const int per_warp = chunks > 2 * NORM_MAX_WARPS ? 4 : chunks > NORM_MAX_WARPS ? 2 : 1;
+    // A chunk per warp as far as a CTA's 32 warps go (all of a row is then loaded
+    // at once; two or four per warp measured within 4% on 4096 to 7168 columns).
+    const int per_warp = chunks <= NORM_MAX_WARPS ? 1 : chunks <= 2 * NORM_MAX_WARPS ? 2 : 4;
     p.warps_per_row = (chunks + per_warp - 1) / per_warp;
     p.rows_per_cta = p.warps_per_row >= 8 ? 1 : 8 / p.warps_per_row;
-    const int grid = int((int64_t(T) + p.rows_per_cta - 1) / p.rows_per_cta);
+    const int64_t wanted = (int64_t(T) + p.rows_per_cta - 1) / p.rows_per_cta;
+    const int resident = std::max(1, 1024 / (p.warps_per_row * p.rows_per_cta * 32));  // at 64 registers a thread
+    const int grid = int(std::min<int64_t>(wanted, int64_t(sms) * resident));
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     if (vec) launch_norm<true>(p, per_warp, grid, st);
     else launch_norm<false>(p, per_warp, grid, st);
