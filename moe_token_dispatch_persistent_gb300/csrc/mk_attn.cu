@@ -10,16 +10,17 @@
 //
 // Work.  A tile is 16 keys of one (sequence, group of up to 16 query heads
 // of one key-value head).  The tiles of all of them in a row are cut into one
-// equal range per CTA, whatever the lengths, so every SM streams the same
-// number of bytes; a range that covers a part of a (sequence, group) leaves
-// an unnormalised partial result, and the CTA that finishes last of those
-// sharing it joins them, in the order of the keys.  The caller's lengths stay
-// on the device: every CTA builds the table of tiles itself.
+// equal range per CTA, and that into one per warp, whatever the lengths, so
+// every warp streams the same number of bytes and waits for no other.  The
+// caller's lengths stay on the device: every CTA builds the table of tiles
+// itself.  A warp writes the results of groups that lie whole in its range.
+// What it has of the others is joined in shared memory when the CTA's ranges
+// are done, and what a CTA has of groups that it shares with others by the
+// CTA that is done last, in the order of the keys.
 //
-// Inside a CTA the warps take every WARPS-th tile of a range (short groups go
-// to one warp each) and wait for one another only at a range's end: each has its own ring of tiles in shared memory, filled by
-// its own 16-byte asynchronous copies (any page size, any stride, keys past
-// the end filled with zeros), which run ahead across the ends of ranges.  The
+// Each warp has its own ring of tiles in shared memory, filled by its own
+// 16-byte asynchronous copies (any page size, any stride, keys past the end
+// filled with zeros), which run ahead across the groups of its range.  The
 // heads are the rows of m16n8k16 products (a decode step has at most 16 rows
 // to offer, where tcgen05 wants 64 or 128, and the products take a small part
 // of the time that the bytes do), so scores and weights stay in registers.
@@ -39,8 +40,12 @@ namespace {
 
 constexpr int KEYS = 16;          // keys per tile
 constexpr int ROWS = 16;          // query heads per group (rows of the product)
+// A group counts as this many tiles more than it has: its queries, its first
+// tile's latency and its result cost about that, and short groups would
+// otherwise gather in a few warps.
+constexpr uint32_t EXTRA = 3;
 constexpr int ATTN_MAX_B = 4096;  // sequences (their tile counts sit in shared memory)
-constexpr int ATTN_MAX_CTAS = 256;
+constexpr int ATTN_MAX_CTAS = 160;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
@@ -53,17 +58,19 @@ struct Geo {
     static constexpr int HALF = KEYS * D * 2;         // one tile's keys (or values)
     static constexpr int RING = STAGES * 2 * HALF;    // per warp
     static constexpr int OSTRIDE = D + 8;             // floats between rows of the join buffer: no bank conflicts
-    static constexpr int SM_O = WARPS * RING;
-    static constexpr int SM_ML = SM_O + WARPS * ROWS * OSTRIDE * 4;
-    static constexpr int SM_PREFIX = SM_ML + 2 * WARPS * ROWS * 4;
-    static constexpr int SM_SMALL = SM_PREFIX + (ATTN_MAX_B + 1) * 4;
-    static constexpr int SMEM = SM_SMALL + 256;
+    static constexpr int SM_PREFIX = WARPS * RING;
+    static constexpr int SM_SMALL = SM_PREFIX + (ATTN_MAX_B + 1) * 4 + 12;
+    static constexpr int SMEM = SM_SMALL + 1024;
+    static constexpr int TAIL = ROWS * OSTRIDE + 2 * ROWS;  // floats of a warp's last result: O, m, l
+    static_assert(WARPS * TAIL * 4 <= SM_PREFIX, "the last results lie where the ring was");
     static constexpr int SLOT = 2 * ROWS + ROWS * D;  // floats of a partial result: m, l, O
     static_assert(SMEM <= 232448, "dynamic shared memory of one CTA on sm_103");
 };
 
 constexpr size_t ATTN_SLOT_BYTES = size_t(Geo<256>::SLOT) * 4;
-constexpr size_t ATTN_SLOTS_BYTES = 2 * ATTN_MAX_CTAS * ATTN_SLOT_BYTES;  // fixed, so the counters never move
+// Two partial results per CTA and one per warp; fixed, so the counters never move.
+constexpr size_t ATTN_HEADS_AT = 2 * ATTN_MAX_CTAS * ATTN_SLOT_BYTES;
+constexpr size_t ATTN_SLOTS_BYTES = ATTN_HEADS_AT + 8 * ATTN_MAX_CTAS * ATTN_SLOT_BYTES;
 
 struct AttnParams {
     const __nv_bfloat16* q;
@@ -73,7 +80,8 @@ struct AttnParams {
     const int32_t* lens;
     __nv_bfloat16* out;
     float* lse;                                   // or null
-    float* slots;                                 // two partial results per CTA
+    float* slots;                                 // two partial results per CTA,
+    float* heads;                                 // and the first of each warp
     uint32_t* arrived;                            // per (sequence, group); zero between calls
     DevError* err;
     int64_t q_stride, page_stride, token_stride, head_stride;
@@ -132,36 +140,61 @@ __device__ __forceinline__ float exp2_of(float x) {
     return r;
 }
 
-// Tiles [t0, t1) of group g of sequence b.
+// Tiles [t0, t1) of group g of sequence b.  In the order of positions that is
+// cut into ranges, EXTRA positions stand before a group's first tile.
 struct Range {
     int b, g;
     uint32_t t0, t1;
-    uint32_t begin;  // position of the group's first tile in the whole order
+    uint32_t begin;  // position of the group's first tile
     uint32_t tiles;  // tiles of the group
 };
-
-// The range that starts at position `pos`, up to the group's or the CTA's end; advances pos.
-__device__ __forceinline__ bool next_range(uint32_t& pos, uint32_t end, const uint32_t* prefix, int B, uint32_t groups,
-                                           Range& r) {
-    if (pos >= end) return false;
-    const uint32_t want = pos / groups;  // tiles of one group before it
-    int lo = 0, hi = B;                  // the last b with prefix[b] <= want that has tiles
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (prefix[mid] <= want) lo = mid;
-        else hi = mid;
-    }
-    const uint32_t n = prefix[lo + 1] - prefix[lo];
-    const uint32_t in = pos - prefix[lo] * groups;
-    r.b = lo;
-    r.g = int(in / n);
-    r.tiles = n;
-    r.t0 = in - uint32_t(r.g) * n;
-    r.t1 = min(n, r.t0 + (end - pos));
-    r.begin = pos - r.t0;
-    pos += r.t1 - r.t0;
-    return true;
+__host__ __device__ inline uint32_t positions_of(int len) {
+    return len > 0 ? uint32_t(len + KEYS - 1) / KEYS + EXTRA : 0u;
 }
+
+// The groups of the positions [pos, end) one after the other.
+struct Walk {
+    uint32_t pos, end;
+    const uint32_t* prefix;
+    int B;
+    uint32_t groups;
+    bool started;
+    // The next group that has tiles there.
+    __device__ bool next(Range& r) {
+        do {
+            if (pos >= end) return false;
+            uint32_t in = 0;  // position inside the group
+            if (!started) {
+                started = true;
+                const uint32_t want = pos / groups;  // positions of one group before it
+                int lo = 0, hi = B;                  // the last b with prefix[b] <= want that has keys
+                while (hi - lo > 1) {
+                    const int mid = (lo + hi) >> 1;
+                    if (prefix[mid] <= want) lo = mid;
+                    else hi = mid;
+                }
+                const uint32_t n = prefix[lo + 1] - prefix[lo];
+                in = pos - prefix[lo] * groups;
+                r.b = lo;
+                r.g = int(in / n);
+                in -= uint32_t(r.g) * n;
+                r.tiles = n - EXTRA;
+            } else if (uint32_t(++r.g) == groups) {
+                // the next sequence that has keys
+                r.g = 0;
+                do ++r.b;
+                while (prefix[r.b + 1] == prefix[r.b]);
+                r.tiles = prefix[r.b + 1] - prefix[r.b] - EXTRA;
+            }
+            const uint32_t to = min(r.tiles + EXTRA, in + (end - pos));
+            r.begin = pos - in + EXTRA;
+            r.t0 = in > EXTRA ? in - EXTRA : 0u;
+            r.t1 = to > EXTRA ? to - EXTRA : 0u;
+            pos += to - in;
+        } while (r.t1 <= r.t0);
+        return true;
+    }
+};
 
 // `total` positions cut into n ranges that differ by one position at most:
 // the first `more` of them hold `each` + 1.
@@ -172,28 +205,6 @@ struct Cut {
     __device__ uint32_t owner(uint32_t p) const {
         const uint32_t in_more = more * (each + 1);
         return p < in_more ? p / (each + 1) : more + (p - in_more) / each;
-    }
-};
-
-// The ranges of a CTA as one of its warps sees them: groups that lie whole in
-// the CTA and have at most `small` tiles go to one warp each, in turn (their
-// results need no join); all warps share every other range.
-struct Walk {
-    uint32_t pos, end, small, turn;
-    const uint32_t* prefix;
-    int B, warp, warps;
-    uint32_t groups;
-    __device__ bool next(Range& r, bool& alone) {
-        while (next_range(pos, end, prefix, B, groups, r)) {
-            alone = r.t1 - r.t0 == r.tiles && r.tiles <= small;
-            if (!alone) return true;
-            if (int(turn) == warp) {
-                turn = turn + 1 == uint32_t(warps) ? 0u : turn + 1;
-                return true;
-            }
-            turn = turn + 1 == uint32_t(warps) ? 0u : turn + 1;
-        }
-        return false;
     }
 };
 
@@ -211,6 +222,113 @@ __device__ __forceinline__ int64_t key_offset(const AttnParams& p, int b, int kv
     return page * p.page_stride + (key - slot * p.page_size) * p.token_stride + kv * p.head_stride;
 }
 
+// A warp's result of a group: O rows `stride` floats apart, maxima and sums.
+template <int D>
+__device__ __forceinline__ void put_partial(float* so, int stride, float* sm, float* sl, int heads,
+                                            const float (&o)[D / 8][4], float m0, float m1, float l0, float l1) {
+    const int lane = threadIdx.x & 31, r0 = lane >> 2, r1 = r0 + 8;
+    if ((lane & 3) == 0) {
+        sm[r0] = m0;
+        sm[r1] = m1;
+        sl[r0] = l0;
+        sl[r1] = l1;
+    }
+    float* ow = so + (lane & 3) * 2;
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) {
+        if (r0 < heads) *reinterpret_cast<float2*>(ow + r0 * stride + n * 8) = make_float2(o[n][0], o[n][1]);
+        if (r1 < heads) *reinterpret_cast<float2*>(ow + r1 * stride + n * 8) = make_float2(o[n][2], o[n][3]);
+    }
+}
+
+// Four columns of a head's partial result: maximum (in units of log 2), sum of
+// weights, weighted sum of values.
+struct Part {
+    float m = -INFINITY, l = 0.f;
+    float4 o = {0.f, 0.f, 0.f, 0.f};
+
+    __device__ void load(const float* slot, int row, int c, int D) {
+        m = __ldcg(slot + row);
+        l = __ldcg(slot + ROWS + row);
+        o = __ldcg(reinterpret_cast<const float4*>(slot + 2 * ROWS + row * D + c));
+    }
+    template <int N>
+    __device__ void add(const Part (&u)[N]) {
+        float top = m;
+#pragma unroll
+        for (int x = 0; x < N; ++x) top = fmaxf(top, u[x].m);
+        const float base = top == -INFINITY ? 0.f : top;
+        const float f = exp2_of(m - base);
+        m = top;
+        l *= f;
+        o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
+#pragma unroll
+        for (int x = 0; x < N; ++x) {
+            const float g = exp2_of(u[x].m - base);
+            l = fmaf(g, u[x].l, l);
+            o.x = fmaf(g, u[x].o.x, o.x);
+            o.y = fmaf(g, u[x].o.y, o.y);
+            o.z = fmaf(g, u[x].o.z, o.z);
+            o.w = fmaf(g, u[x].o.w, o.w);
+        }
+    }
+    __device__ void finish(const AttnParams& p, int b, int head, int c, int D) const {
+        const int64_t at = int64_t(b) * p.Hq + head;
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        *reinterpret_cast<uint2*>(p.out + at * D + c) =
+            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
+        if (p.lse && c == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
+    }
+};
+
+// The result of a group from the CTAs' partial results, by a whole CTA.  A
+// thread takes four columns of one head and, where there are more threads than
+// that, every parts-th piece; the parts are joined in shared memory.
+template <int D>
+__device__ void join_group(const AttnParams& p, const Range& r, const Cut& cut_at, float* smem_f) {
+    using G = Geo<D>;
+    const int tid = threadIdx.x;
+    const int kv = r.g / p.chunks, head0 = kv * p.per_kv + (r.g % p.chunks) * ROWS;
+    const int heads = min(ROWS, (kv + 1) * p.per_kv - head0);
+    const uint32_t c0 = cut_at.owner(r.begin), c1 = cut_at.owner(r.begin + r.tiles - 1);
+    const int n = int(c1 - c0) + 1;
+    const int items = heads * (D / 4), parts = min(n, max(1, G::THREADS / items));
+    Part* red = reinterpret_cast<Part*>(smem_f);
+    // a CTA's piece lies in its first slot if the group holds its range's start: that of the first CTA may not
+    const float* first = p.slots + size_t(2 * c0 + (cut_at.start(c0) >= r.begin ? 0 : 1)) * (ATTN_SLOT_BYTES / 4);
+    const float* other = p.slots + size_t(2 * c0) * (ATTN_SLOT_BYTES / 4);
+    __threadfence();
+    for (int i0 = 0; i0 < items; i0 += G::THREADS) {
+        const int item = parts > 1 ? tid % items : i0 + tid, part = parts > 1 ? tid / items : 0;
+        const bool on = item < items && part < parts;
+        const int row = item / (D / 4), c = (item % (D / 4)) * 4;
+        Part acc;
+        if (on) {
+            constexpr int BATCH = 8;
+            for (int i = part; i < n; i += BATCH * parts) {
+                Part u[BATCH];
+#pragma unroll
+                for (int x = 0; x < BATCH; ++x) {
+                    const int at = i + x * parts;
+                    if (at < n) u[x].load(at == 0 ? first : other + size_t(2 * at) * (ATTN_SLOT_BYTES / 4), row, c, D);
+                }
+                acc.add(u);
+            }
+        }
+        if (parts > 1) {
+            if (on) red[part * items + item] = acc;
+            __syncthreads();
+            if (on && part == 0)
+                for (int q = 1; q < parts; ++q) {
+                    const Part u[1] = {red[q * items + item]};
+                    acc.add(u);
+                }
+        }
+        if (on && part == 0) acc.finish(p, r.b, head0 + row, c, D);
+    }
+    __syncthreads();  // the buffer is free for another group
+}
+
 template <int D>
 __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(const AttnParams p) {
     using G = Geo<D>;
@@ -218,13 +336,10 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + G::SM_PREFIX);
     uint32_t* small = reinterpret_cast<uint32_t*>(smem + G::SM_SMALL);
-    float* sO = reinterpret_cast<float*>(smem + G::SM_O);
-    float* sM = reinterpret_cast<float*>(smem + G::SM_ML);
-    float* sL = sM + G::WARPS * ROWS;
     const uint32_t groups = uint32_t(p.groups);
     const int64_t cap = int64_t(p.max_pages) * p.page_size;
 
-    // ---- tiles per sequence, summed over the sequences before it
+    // ---- positions of one group of each sequence, summed over the sequences before it
     auto length = [&](int b) -> int {
         const int n = __ldg(p.lens + b);
         return n < 0 ? 0 : n > cap ? int(cap) : n;
@@ -236,7 +351,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
         for (int b = b0; b < b1; ++b) {
             const int n = __ldg(p.lens + b);
             if ((n < 0 || n > cap) && blockIdx.x == 0) attn_error(p.err, SITE_SEQ_LEN, uint32_t(n));
-            mine += uint32_t((length(b) + KEYS - 1) / KEYS);
+            mine += positions_of(length(b));
         }
         uint32_t run = mine;
 #pragma unroll
@@ -250,7 +365,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
         for (int w = 0; w < warp; ++w) base += small[w];
         for (int b = b0; b < b1; ++b) {
             prefix[b] = base;
-            base += uint32_t((length(b) + KEYS - 1) / KEYS);
+            base += positions_of(length(b));
         }
         if (b1 == p.B && b0 < b1) prefix[p.B] = base;
         __syncthreads();
@@ -266,56 +381,68 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
     }
 
     const uint32_t total = prefix[p.B] * groups;
-    // at least one tile per warp: a shorter range would only add partial results to join
+    // at least a position per warp: a shorter range would only add partial results to join
     const uint32_t nctas = min(gridDim.x, (total + G::WARPS - 1) / G::WARPS);
     if (blockIdx.x >= nctas) return;
     const Cut cut_at(total, nctas);
     const uint32_t start = cut_at.start(blockIdx.x), end = cut_at.start(blockIdx.x + 1);
-    // A warp alone with a group takes its tiles one after the other; up to half
-    // of a warp's share of the range that evens out between the warps.
-    const uint32_t small_tiles = max(1u, (end - start) / (2 * G::WARPS));
+    const Cut warp_cut(end - start, G::WARPS);
+    const uint32_t wstart = start + warp_cut.start(warp), wend = start + warp_cut.start(warp + 1);
 
-    // ---- this warp's ring: loads run STAGES tiles ahead, across ranges
+    // ---- this warp's ring: loads run STAGES tiles ahead, across groups
     const uint32_t ring = smem_u32(smem) + uint32_t(warp) * G::RING;
-    Walk load_walk{start, end, small_tiles, 0u, prefix, p.B, warp, G::WARPS, groups};
+    Walk load_walk{wstart, wend, prefix, p.B, groups, false};
     uint32_t load_tile = 0;
     Range lr;
     int load_len = 0;
-    bool loading = true, load_alone = false;
+    bool more = true;
     lr.t1 = 0;
-    int64_t ahead = -1;  // row offset of the next tile to load
-    auto seek = [&](uint32_t t) {
-        load_tile = t;
-        while (load_tile >= lr.t1) {
-            if (!load_walk.next(lr, load_alone)) {
-                loading = false;
+    // The pages of the next two tiles are looked up before their rows are copied.
+    int64_t off[2];   // this lane's row offsets
+    bool have[2];
+    auto look_up = [&](int64_t& o, bool& h) {
+        h = false;
+        if (!more) return;
+        if (load_tile >= lr.t1) {
+            if (!load_walk.next(lr)) {
+                more = false;
                 return;
             }
             load_len = length(lr.b);
-            load_tile = lr.t0 + (load_alone ? 0u : uint32_t(warp));
+            load_tile = lr.t0;
+            // the group's queries head for L1 while its first tiles do for shared memory
+            const int head = lr.g / p.chunks * p.per_kv + lr.g % p.chunks * ROWS + (lane & (ROWS - 1));
+            if (lane < ROWS && head < (lr.g / p.chunks + 1) * p.per_kv) {
+                const char* q = reinterpret_cast<const char*>(p.q + int64_t(lr.b) * p.q_stride + int64_t(head) * D);
+#pragma unroll
+                for (int i = 0; i < D * 2; i += 128) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + i));
+            }
         }
-        // the page is looked up one tile before its rows are copied
-        ahead = key_offset(p, lr.b, lr.g / p.chunks, load_tile, lane, load_len);
+        o = key_offset(p, lr.b, lr.g / p.chunks, load_tile, lane, load_len);
+        h = true;
+        ++load_tile;
     };
-    seek(0);
+    look_up(off[0], have[0]);
+    look_up(off[1], have[1]);
     uint32_t load_slot = 0;
     auto issue = [&]() {
-        if (loading) {
+        if (have[0]) {
             const uint32_t dst = ring + load_slot * (2 * G::HALF);
-            const int64_t off = ahead;
 #pragma unroll
             for (int i = 0; i < KEYS * G::CHUNKS / 32; ++i) {
                 const int piece = i * 32 + lane, row = piece / G::CHUNKS, c = piece % G::CHUNKS;
-                const int64_t ro = __shfl_sync(0xffffffffu, off, row);
+                const int64_t ro = __shfl_sync(0xffffffffu, off[0], row);
                 const bool ok = ro >= 0;
                 const int64_t at = (ok ? ro : 0) + c * 8;
                 const uint32_t d = dst + uint32_t(row * D * 2 + ((c ^ (row & 7)) << 4));
                 copy16(d, p.k + at, ok);
                 copy16(d + G::HALF, p.v + at, ok);
             }
-            seek(load_tile + (load_alone ? 1u : uint32_t(G::WARPS)));
         }
         copy_commit();
+        off[0] = off[1];
+        have[0] = have[1];
+        look_up(off[1], have[1]);
         if (++load_slot == G::STAGES) load_slot = 0;
     };
 #pragma unroll
@@ -323,10 +450,15 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
 
     const int r0 = lane >> 2, r1 = r0 + 8;  // this lane's rows (heads) of the products
     uint32_t slot = 0;
-    Walk walk{start, end, small_tiles, 0u, prefix, p.B, warp, G::WARPS, groups};
+    Walk walk{wstart, wend, prefix, p.B, groups, false};
     Range r;
-    bool alone = false;
-    while (walk.next(r, alone)) {
+    // A group that the warp does not hold whole is its first (kept in the
+    // workspace) or its last (kept in registers until the rings are free).
+    Range head, tail;
+    bool has_head = false, has_tail = false;
+    float o[D / 8][4];
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    while (walk.next(r)) {
         const int kv = r.g / p.chunks, head0 = kv * p.per_kv + (r.g % p.chunks) * ROWS;
         const int heads = min(ROWS, (kv + 1) * p.per_kv - head0);
         const int len = length(r.b);
@@ -344,15 +476,14 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
                 qa[kk][3] = r1 < heads ? q1[kk * 8 + 4] : 0u;
             }
         }
-        float o[D / 8][4];
 #pragma unroll
         for (int n = 0; n < D / 8; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
-        float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+        m0 = m1 = -INFINITY;
+        l0 = l1 = 0.f;
 
-        const uint32_t step = alone ? 1u : uint32_t(G::WARPS);
-        for (uint32_t t = r.t0 + (alone ? 0u : uint32_t(warp)); t < r.t1; t += step) {
+        for (uint32_t t = r.t0; t < r.t1; ++t) {
             copy_wait<G::STAGES - 1>();
             __syncwarp();
             const uint32_t ks = ring + slot * (2 * G::HALF), vs = ks + G::HALF;
@@ -442,8 +573,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
         l1 += __shfl_xor_sync(0xffffffffu, l1, 1);
         l0 += __shfl_xor_sync(0xffffffffu, l0, 2);
         l1 += __shfl_xor_sync(0xffffffffu, l1, 2);
-        if (alone) {
-            // the whole group by this warp: straight to the output
+        if (r.t1 - r.t0 == r.tiles) {
+            // the whole group: straight to the output
             const float i0 = l0 == 0.f ? 0.f : 1.f / l0, i1 = l1 == 0.f ? 0.f : 1.f / l1;
             const int64_t at = int64_t(r.b) * p.Hq + head0;
             uint32_t* w0 = reinterpret_cast<uint32_t*>(p.out + (at + r0) * D) + (lane & 3);
@@ -457,150 +588,103 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
                 if (r0 < heads) p.lse[at + r0] = l0 == 0.f ? -INFINITY : (m0 + log2f(l0)) * LN2;
                 if (r1 < heads) p.lse[at + r1] = l1 == 0.f ? -INFINITY : (m1 + log2f(l1)) * LN2;
             }
-            continue;
+        } else if (walk.pos < walk.end) {
+            head = r;
+            has_head = true;
+            float* s = p.heads + size_t(blockIdx.x * G::WARPS + warp) * (ATTN_SLOT_BYTES / 4);
+            put_partial<D>(s + 2 * ROWS, D, s, s + ROWS, heads, o, m0, m1, l0, l1);
+        } else {
+            tail = r;
+            has_tail = true;
         }
-
-        // ---- join the warps' results of the range
-        const int nw = int(min(uint32_t(G::WARPS), r.t1 - r.t0));  // warps that had a tile
-        if (warp < nw) {
-            if ((lane & 3) == 0) {
-                sM[warp * ROWS + r0] = m0;
-                sM[warp * ROWS + r1] = m1;
-                sL[warp * ROWS + r0] = l0;
-                sL[warp * ROWS + r1] = l1;
-            }
-            float* ow = sO + warp * ROWS * G::OSTRIDE + (lane & 3) * 2;
-#pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
-                if (r0 < heads) *reinterpret_cast<float2*>(ow + r0 * G::OSTRIDE + n * 8) = make_float2(o[n][0], o[n][1]);
-                if (r1 < heads) *reinterpret_cast<float2*>(ow + r1 * G::OSTRIDE + n * 8) = make_float2(o[n][2], o[n][3]);
-            }
-        }
-        __syncthreads();
-        const bool whole = r.t1 - r.t0 == r.tiles;
-        // a CTA's first partial range takes its first slot, its last one the second
-        float* mine = p.slots + size_t(2 * blockIdx.x + (start >= r.begin ? 0 : 1)) * (ATTN_SLOT_BYTES / 4);
-        for (int i = tid; i < heads * (D / 4); i += G::THREADS) {
-            const int row = i / (D / 4), c = (i % (D / 4)) * 4;
-            float top = -INFINITY;
-            for (int w = 0; w < nw; ++w) top = fmaxf(top, sM[w * ROWS + row]);
-            const float base = top == -INFINITY ? 0.f : top;
-            float l = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int w = 0; w < nw; ++w) {
-                const float f = exp2_of(sM[w * ROWS + row] - base);
-                const float4 v = *reinterpret_cast<const float4*>(sO + (w * ROWS + row) * G::OSTRIDE + c);
-                l = fmaf(f, sL[w * ROWS + row], l);
-                acc.x = fmaf(f, v.x, acc.x);
-                acc.y = fmaf(f, v.y, acc.y);
-                acc.z = fmaf(f, v.z, acc.z);
-                acc.w = fmaf(f, v.w, acc.w);
-            }
-            if (whole) {
-                const int64_t at = int64_t(r.b) * p.Hq + head0 + row;
-                const float inv = l == 0.f ? 0.f : 1.f / l;
-                *reinterpret_cast<uint2*>(p.out + at * D + c) =
-                    make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-                if (p.lse && c == 0) p.lse[at] = l == 0.f ? -INFINITY : (top + log2f(l)) * LN2;
-            } else {
-                *reinterpret_cast<float4*>(mine + 2 * ROWS + row * D + c) = acc;
-                if (c == 0) {
-                    mine[row] = top;
-                    mine[ROWS + row] = l;
-                }
-            }
-        }
-        if (!whole) {
-            // ---- the CTA that completes the group joins its partial results
-            uint32_t* flag = small;
-            const uint32_t c0 = cut_at.owner(r.begin), c1 = cut_at.owner(r.begin + r.tiles - 1);
-            const int n = int(c1 - c0) + 1;
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                uint32_t* a = p.arrived + size_t(r.b) * groups + r.g;
-                const bool last = atom_add_acq_rel_u32(a, 1u) == uint32_t(n) - 1;
-                if (last) *a = 0u;
-                flag[0] = last;
-            }
-            __syncthreads();
-            if (flag[0]) {
-                __threadfence();
-                // weights of the pieces, then their sum: every thread four columns of
-                // one row, the pieces dealt out over as many threads as there are
-                auto piece = [&](int i) -> const float* {
-                    const uint32_t c = c0 + uint32_t(i);
-                    const uint32_t which = cut_at.start(c) >= r.begin ? 0u : 1u;
-                    return p.slots + size_t(2 * c + which) * (ATTN_SLOT_BYTES / 4);
-                };
-                float* sw = sO;                  // [n][heads] weights
-                float* st = sO + n * ROWS;       // [heads] maximum, then sum
-                float4* red = reinterpret_cast<float4*>(st + 2 * ROWS);
-                for (int row = warp; row < heads; row += G::WARPS) {
-                    float top = -INFINITY;
-                    for (int i = lane; i < n; i += 32) top = fmaxf(top, __ldcg(piece(i) + row));
-#pragma unroll
-                    for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-                    const float base = top == -INFINITY ? 0.f : top;
-                    float l = 0.f;
-                    for (int i = lane; i < n; i += 32) {
-                        const float* s = piece(i);
-                        const float f = exp2_of(__ldcg(s + row) - base);
-                        sw[i * ROWS + row] = f;
-                        l = fmaf(f, __ldcg(s + ROWS + row), l);
-                    }
-#pragma unroll
-                    for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
-                    if (lane == 0) {
-                        st[row] = top;
-                        st[ROWS + row] = l;
-                    }
-                }
-                __syncthreads();
-                const int items = heads * (D / 4);
-                const int parts = items >= G::THREADS ? 1 : G::THREADS / items;
-                for (int i0 = 0; i0 < items; i0 += G::THREADS) {
-                    const int item = parts > 1 ? tid % items : i0 + tid, part = parts > 1 ? tid / items : 0;
-                    const bool on = item < items && part < parts;
-                    const int row = item / (D / 4), c = (item % (D / 4)) * 4;
-                    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (on) {
-#pragma unroll 4
-                        for (int i = part; i < n; i += parts) {
-                            const float f = sw[i * ROWS + row];
-                            const float4 v = __ldcg(reinterpret_cast<const float4*>(piece(i) + 2 * ROWS + row * D + c));
-                            acc.x = fmaf(f, v.x, acc.x);
-                            acc.y = fmaf(f, v.y, acc.y);
-                            acc.z = fmaf(f, v.z, acc.z);
-                            acc.w = fmaf(f, v.w, acc.w);
-                        }
-                    }
-                    if (parts > 1) {
-                        if (on) red[part * items + item] = acc;
-                        __syncthreads();
-                        if (on && part == 0)
-                            for (int q = 1; q < parts; ++q) {
-                                const float4 v = red[q * items + item];
-                                acc.x += v.x;
-                                acc.y += v.y;
-                                acc.z += v.z;
-                                acc.w += v.w;
-                            }
-                    }
-                    if (on && part == 0) {
-                        const float l = st[ROWS + row];
-                        const float inv = l == 0.f ? 0.f : 1.f / l;
-                        const int64_t at = int64_t(r.b) * p.Hq + head0 + row;
-                        *reinterpret_cast<uint2*>(p.out + at * D + c) =
-                            make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
-                        if (p.lse && c == 0) p.lse[at] = l == 0.f ? -INFINITY : (st[row] + log2f(l)) * LN2;
-                    }
-                }
-            }
-        }
-        __syncthreads();  // the join buffer is free for the next range
     }
     copy_wait<0>();
+
+    // ---- join what the CTA's warps have of the same groups
+    __shared__ Range pieces[2 * G::WARPS];  // in the order of positions; tiles 0: none
+    __syncthreads();  // the rings are free
+    if (lane == 0) {
+        head.tiles = has_head ? head.tiles : 0u;
+        tail.tiles = has_tail ? tail.tiles : 0u;
+        pieces[2 * warp] = head;
+        pieces[2 * warp + 1] = tail;
+    }
+    float* tails = reinterpret_cast<float*>(smem);
+    if (has_tail) {
+        const int kv = tail.g / p.chunks, head0 = kv * p.per_kv + (tail.g % p.chunks) * ROWS;
+        float* s = tails + warp * G::TAIL;
+        put_partial<D>(s, G::OSTRIDE, s + ROWS * G::OSTRIDE, s + ROWS * G::OSTRIDE + ROWS,
+                       min(ROWS, (kv + 1) * p.per_kv - head0), o, m0, m1, l0, l1);
+    }
+    __syncthreads();
+    Range open[2];  // groups shared with other CTAs: the first and the last one's
+    int nopen = 0;
+    uint32_t left = 0;  // pieces not joined yet, a bit each
+#pragma unroll
+    for (int i = 0; i < 2 * G::WARPS; ++i) left |= pieces[i].tiles != 0 ? 1u << i : 0u;
+    while (left) {
+        const Range q = pieces[__ffs(int(left)) - 1];
+        uint32_t same = 0;  // those of the first one's group
+#pragma unroll
+        for (int i = 0; i < 2 * G::WARPS; ++i)
+            if ((left >> i & 1u) && pieces[i].begin == q.begin) same |= 1u << i;
+        left &= ~same;
+        const int kv = q.g / p.chunks, head0 = kv * p.per_kv + (q.g % p.chunks) * ROWS;
+        const int heads = min(ROWS, (kv + 1) * p.per_kv - head0);
+        const bool whole = q.begin >= start && q.begin + q.tiles <= end;
+        // a CTA's first shared group takes its first slot, its last one the second
+        float* mine = p.slots + size_t(2 * blockIdx.x + (start >= q.begin ? 0 : 1)) * (ATTN_SLOT_BYTES / 4);
+        for (int item = tid; item < heads * (D / 4); item += G::THREADS) {
+            const int row = item / (D / 4), c = (item % (D / 4)) * 4;
+            Part acc;
+            for (uint32_t rest = same; rest;) {
+                constexpr int BATCH = 4;
+                Part u[BATCH];
+#pragma unroll
+                for (int x = 0; x < BATCH; ++x) {
+                    if (rest == 0) continue;
+                    const int i = __ffs(int(rest)) - 1, w = i >> 1;
+                    rest &= rest - 1;
+                    if (i & 1) {
+                        const float* s = tails + w * G::TAIL;
+                        u[x].m = s[ROWS * G::OSTRIDE + row];
+                        u[x].l = s[ROWS * G::OSTRIDE + ROWS + row];
+                        u[x].o = *reinterpret_cast<const float4*>(s + row * G::OSTRIDE + c);
+                    } else {
+                        u[x].load(p.heads + size_t(blockIdx.x * G::WARPS + w) * (ATTN_SLOT_BYTES / 4), row, c, D);
+                    }
+                }
+                acc.add(u);
+            }
+            if (whole) {
+                acc.finish(p, q.b, head0 + row, c, D);
+            } else {
+                __stcg(reinterpret_cast<float4*>(mine + 2 * ROWS + row * D + c), acc.o);
+                if (c == 0) {
+                    __stcg(mine + row, acc.m);
+                    __stcg(mine + ROWS + row, acc.l);
+                }
+            }
+        }
+        if (!whole) open[nopen++] = q;
+    }
+    if (nopen == 0) return;
+
+    // ---- groups shared with other CTAs: the one that arrives last joins their
+    // partial results
+    __threadfence();
+    __syncthreads();
+    if (tid < nopen) {
+        const Range& o = tid == 0 ? open[0] : open[1];
+        const uint32_t n = cut_at.owner(o.begin + o.tiles - 1) - cut_at.owner(o.begin) + 1;
+        uint32_t* a = p.arrived + size_t(o.b) * groups + o.g;
+        const bool last = atom_add_acq_rel_u32(a, 1u) == n - 1;
+        if (last) *a = 0u;
+        small[tid] = last;
+    }
+    __syncthreads();
+    for (int i = 0; i < nopen; ++i)
+        if (small[i]) join_group<D>(p, i == 0 ? open[0] : open[1], cut_at, tails);
 }
 
 template <int D>
@@ -652,7 +736,7 @@ extern "C" mk_status_t mk_paged_attention(const void* q, int64_t q_stride, const
     const int64_t cap = int64_t(max_pages) * page_size;
     if (B > ATTN_MAX_B || cap > (int64_t(1) << 31) - KEYS) return MK_ERR_UNSUPPORTED;
     // positions in the order of tiles are 32-bit
-    const int64_t tiles = int64_t(B) * ((cap + KEYS - 1) / KEYS);
+    const int64_t tiles = int64_t(B) * positions_of(int(cap));
     if (tiles >= int64_t(1) << 31 || tiles * groups >= int64_t(1) << 31) return MK_ERR_UNSUPPORTED;
     if (B > 0) {
         if (!q || !seq_lens || !out) return MK_ERR_INVALID_ARG;
@@ -691,6 +775,7 @@ extern "C" mk_status_t mk_paged_attention(const void* q, int64_t q_stride, const
     p.out = static_cast<__nv_bfloat16*>(out);
     p.lse = lse;
     p.slots = reinterpret_cast<float*>(ws);
+    p.heads = reinterpret_cast<float*>(ws + ATTN_HEADS_AT);
     p.arrived = reinterpret_cast<uint32_t*>(ws + ATTN_SLOTS_BYTES);
     p.err = err;
     p.q_stride = q_stride;

@@ -970,6 +970,8 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
         tma_prefetch_desc(&m.w1);
         tma_prefetch_desc(&m.w3);
         tma_prefetch_desc(&m.x);
+        tma_prefetch_desc(&m.w2);
+        tma_prefetch_desc(&m.h);
     }
     if (warp == WARP_MMA) {
         tmem_alloc(&sm->tmem_base, 512);
