@@ -56,9 +56,9 @@ constexpr int FFN_MAX_CTAS = 160;
 
 // Warps: weight loads, products, eight draining accumulators (TMEM lanes
 // 32 * (warp % 4); two warps share a quarter and take turns at its column
-// blocks), row loads, four that complete h.
+// blocks), row loads, counting of pieces, three that complete h.
 constexpr int WARP_A = 0, WARP_MMA = 1, WARP_EPI = 2, EPI_WARPS = 8, WARP_B = WARP_EPI + EPI_WARPS;
-constexpr int WARP_FIN = WARP_B + 1, FIN_WARPS = 4;
+constexpr int WARP_COUNT = WARP_B + 1, WARP_FIN = WARP_COUNT + 1, FIN_WARPS = 3;
 constexpr int FFN_WARPS = WARP_FIN + FIN_WARPS;
 constexpr int FFN_THREADS = FFN_WARPS * 32;
 
@@ -90,10 +90,10 @@ static_assert(SCALE_SLOTS >= STAGES_F + FFN_MAX_BUFS && SCALE_AT + SCALE_SLOTS *
 constexpr int MAX_TILES1 = MAX_PARTS * (32768 / ACC_COLS);
 // Units: about this many per CTA, of at least this many steps.  Pieces of more
 // floats than this only where one unit covers all of K.
-constexpr uint32_t UNITS_PER_CTA = 16, MIN_CHUNK = 4;
+constexpr uint32_t UNITS_PER_CTA = 8, MIN_CHUNK = 4;
 constexpr size_t PIECE_FLOATS = size_t(8) << 20;
 constexpr int INFO_SLOTS = 8;
-static_assert(INFO_SLOTS % FIN_WARPS == 0, "each completing warp's units keep to their slots");
+constexpr int JOBS = 2;  // blocks of h handed to the completing warps
 constexpr long long FFN_SPIN_NS = 2000000000LL;
 constexpr float E4M3_TOP = 448.f;
 constexpr float TINY = 7.888609052210118e-31f;  // 2^-100
@@ -151,6 +151,9 @@ struct FfnSmem {
     uint32_t tmem_base;
     int ok, parts, most;           // most: rows of the largest part
     int scan[8];
+    uint64_t job_in[JOBS], job_out[JOBS];
+    Unit job[JOBS];                // blocks of h being completed,
+    uint32_t job_left[JOBS];       // and the warps at work on them
     uint16_t off[MAX_PARTS];       // per part of the chosen experts: its first row,
     uint8_t expert[MAX_PARTS];     // its expert
     uint8_t count[MAX_PARTS];      // and its rows
@@ -180,15 +183,19 @@ __device__ __forceinline__ Plan make_plan(const FfnParams& p, int step_rows, uin
     q.ms[1] = uint32_t(p.F / step_rows);
     q.blocks[0] = uint32_t((p.F + ACC_COLS - 1) / ACC_COLS);
     q.blocks[1] = uint32_t((p.H + ACC_COLS - 1) / ACC_COLS);
-    const uint32_t steps = parts * (2 * q.ms[0] * q.blocks[0] + q.ms[1] * q.blocks[1]);
-    // Small units even out the SMs' speeds; every unit leaves a piece of `most`
-    // rows of 1 KiB next to its 32 KiB a step, so many rows want longer ones.
-    const uint32_t want = max(max(MIN_CHUNK, most / 2), steps / (gridDim.x * UNITS_PER_CTA));
+    const uint32_t steps[2] = {parts * 2 * q.ms[0] * q.blocks[0], parts * q.ms[1] * q.blocks[1]};
+    const uint32_t share = (steps[0] + steps[1]) / gridDim.x;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+        // Small units even out the SMs' speeds, but each leaves a piece of `most` rows
+        // of 1 KiB beside its 32 KiB a step, to be stored, counted and added up: about
+        // 8 units per CTA (16 cost up to 15%), and as many steps as rows while that
+        // leaves every CTA two units of either half (half as many steps: +18% with 12
+        // rows an expert).
+        const uint32_t want = max(max(MIN_CHUNK, share / UNITS_PER_CTA), min(most, steps[h] / gridDim.x / 2));
         const uint32_t rows = uint32_t(p.T * p.k) * (h == 0 ? 2 : 1);
         const uint32_t fit = uint32_t(p.room[h] / (size_t(rows) * q.blocks[h] * ACC_COLS));
-        const uint32_t n = max(1u, min((q.ms[h] + want - 1) / want, fit));
+        const uint32_t n = max(1u, min((q.ms[h] + want / 2) / want, fit));
         q.chunk[h] = (q.ms[h] + n - 1) / n;
         q.chunks[h] = (q.ms[h] + q.chunk[h] - 1) / q.chunk[h];
     }
@@ -409,7 +416,6 @@ __device__ void weight_loads(const FfnParams& p, const FfnMaps& m, FfnSmem* sm, 
     Turn st, out;
     Issued mine;
     uint32_t u = blockIdx.x;  // the first unit of every CTA needs no counter
-    int ends = 0;
     while (true) {
         if (!warp_await_mbar(&sm->info_out[out.i], out.phase ^ 1u, w, SITE_INFO_EMPTY)) break;
         const bool more = u < pl.units;
@@ -422,10 +428,7 @@ __device__ void weight_loads(const FfnParams& p, const FfnMaps& m, FfnSmem* sm, 
             mbar_arrive(&sm->info_in[out.i]);
         }
         out.next(INFO_SLOTS);
-        if (!more) {
-            if (++ends == FIN_WARPS) return;  // each completing warp looks at every fourth slot only
-            continue;
-        }
+        if (!more) return;
         const int ncol = s.half ? p.H : p.F;
         const int row0 = s.expert * (s.half ? p.F : p.H);
         const CUtensorMap* map = s.half ? &m.w2 : s.second ? &m.w3 : &m.w1;
@@ -597,16 +600,16 @@ __device__ void products(FfnSmem* sm, const Accs& accs, const Waiter& w) {
     __syncwarp();
 }
 
-// A block of 256 columns of a part's h from its pieces, by one warp: eight
-// columns per lane.  ROWS rows and BATCH pieces of each matrix are loaded
-// together.
+// ROWS rows from i0 on of a block of 256 columns of a part's h, from their
+// pieces, by one warp: eight columns per lane.  BATCH pieces of each matrix are
+// loaded together.
 template <bool FP8, int ROWS, int BATCH>
-__device__ __forceinline__ void complete_rows(const FfnParams& p, const Plan& pl, const Unit& s) {
+__device__ __forceinline__ void complete_rows(const FfnParams& p, const Plan& pl, const Unit& s, int i0) {
     const int lane = threadIdx.x & 31, col = s.blk * ACC_COLS + lane * 8;
     const bool in = col < p.F;  // F is a multiple of 64
     const size_t R = size_t(p.T) * p.k, stride = size_t(pl.blocks[0]) * ACC_COLS;
     const int chunks = int(pl.chunks[0]);
-    for (int i0 = 0; i0 < s.n; i0 += ROWS) {
+    {
         float v[2][ROWS][8];
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -644,7 +647,7 @@ __device__ __forceinline__ void complete_rows(const FfnParams& p, const Plan& pl
             if (i0 + r >= s.n) break;
             float* h = v[0][r];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h[i] = h[i] / (1.f + expf(-h[i])) * v[1][r][i];
+            for (int i = 0; i < 8; ++i) h[i] = __fdividef(h[i], 1.f + __expf(-h[i])) * v[1][r][i];
             const int row = s.off + i0 + r;
             const size_t at = size_t(row) * p.F + col;
             if constexpr (FP8) {
@@ -681,42 +684,90 @@ __device__ __forceinline__ void complete_rows(const FfnParams& p, const Plan& pl
     }
 }
 
-// The completing warps: each follows every fourth of the CTA's units, counts
-// its piece once it is stored, and completes the block of h if that piece was
-// the last.  (The weights in flight make any round trip to L2 take several
-// microseconds, so these must not wait one after the other.)
+// The counting warp: follows the CTA's units, counts each piece of h once it is
+// stored, and hands a block whose last piece that was to the completing warps.
+// The weights in flight make any round trip to L2 take several microseconds, so
+// while the next piece is there already, a count's result is looked at only
+// after the next count has been sent.
+__device__ void count_pieces(const FfnParams& p, FfnSmem* sm, const Plan& pl, const Waiter& w) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t all = 2 * pl.chunks[0];
+    Turn in, out;
+    Unit open;  // the unit whose count has been sent but not looked at
+    uint32_t open_count = 0;
+    bool is_open = false;
+    auto hand = [&](const Unit& s) {
+        if (!warp_await_mbar(&sm->job_out[out.i], out.phase ^ 1u, w, SITE_INFO_EMPTY)) return false;
+        if (lane == 0) {
+            __threadfence();  // the pieces that the other CTAs released
+            sm->job[out.i] = s;
+            sm->job_left[out.i] = FIN_WARPS;
+            mbar_arrive(&sm->job_in[out.i]);
+        }
+        out.next(JOBS);
+        return true;
+    };
+    while (true) {
+        if (is_open) {
+            const bool more = mbar_test(&sm->info_in[in.i], in.phase) && mbar_test(&sm->piece_in[in.i], in.phase);
+            if (!__all_sync(0xffffffffu, more)) {
+                is_open = false;
+                if (__shfl_sync(0xffffffffu, open_count, 0) == all && !hand(open)) return;
+            }
+        }
+        if (!warp_await_mbar(&sm->info_in[in.i], in.phase, w, SITE_INFO_FULL)) return;
+        const Unit s = sm->unit[in.i];
+        if (s.end) {
+            hand(s);
+            return;
+        }
+        // the slot is given back only after its piece, so that no second one comes in unseen
+        if (!warp_await_mbar(&sm->piece_in[in.i], in.phase, w, SITE_INFO_FULL)) return;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sm->info_out[in.i]);
+        in.next(INFO_SLOTS);
+        uint32_t count = 0;
+        if (s.half == 0 && lane == 0)  // releases the draining warps' stores, which the wait above has seen
+            count = atom_add_release_u32(&p.ctl->arrived[uint32_t(s.a) * pl.blocks[0] + s.blk], 1u) + 1u;
+        if (is_open && __shfl_sync(0xffffffffu, open_count, 0) == all && !hand(open)) return;
+        is_open = s.half == 0;
+        open = s;
+        open_count = count;
+    }
+}
+
+// A completing warp: its share of the rows of each block handed on.
 template <bool FP8>
 __device__ void complete_h(const FfnParams& p, FfnSmem* sm, const Plan& pl, const Waiter& w) {
-    const int lane = threadIdx.x & 31;
-    uint32_t it = threadIdx.x / 32 - WARP_FIN;
-    for (;; it += FIN_WARPS) {
-        const uint32_t slot = it % INFO_SLOTS, phase = it / INFO_SLOTS & 1u;
-        if (!warp_await_mbar(&sm->info_in[slot], phase, w, SITE_INFO_FULL)) return;
-        const Unit s = sm->unit[slot];
+    const int lane = threadIdx.x & 31, me = threadIdx.x / 32 - WARP_FIN;
+    Turn in;
+    int turn = 0;
+    while (true) {
+        if (!warp_await_mbar(&sm->job_in[in.i], in.phase, w, SITE_INFO_FULL)) return;
+        const Unit s = sm->job[in.i];
         if (s.end) return;
-        // the slot is given back only after its piece, so that no second one comes in unseen
-        if (!warp_await_mbar(&sm->piece_in[slot], phase, w, SITE_INFO_FULL)) return;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sm->info_out[slot]);
-        if (s.half) continue;
-        uint32_t count = 0;
-        const uint32_t all = 2 * pl.chunks[0];
-        if (lane == 0) {
-            // releases the draining warps' stores, which the wait above has seen
-            uint32_t* a = &p.ctl->arrived[uint32_t(s.a) * pl.blocks[0] + s.blk];
-            count = atom_add_acq_rel_u32(a, 1u) + 1u;
-            if (count == all) *a = 0u;
-        }
-        if (__shfl_sync(0xffffffffu, count, 0) != all) continue;
-        __threadfence();
+        if (me == 0 && lane == 0) p.ctl->arrived[uint32_t(s.a) * pl.blocks[0] + s.blk] = 0u;  // for the next call
+        // the warps take turns at the first rows: many blocks have few
+        const int me_now = (me + turn++) % FIN_WARPS;
         // about as many loads in flight either way
-        if (all == 2) complete_rows<FP8, 4, 1>(p, pl, s);
-        else if (all == 4) complete_rows<FP8, 2, 2>(p, pl, s);
-        else complete_rows<FP8, 1, 4>(p, pl, s);
+        if (pl.chunks[0] == 1)
+            for (int i = me_now * 4; i < s.n; i += FIN_WARPS * 4) complete_rows<FP8, 4, 1>(p, pl, s, i);
+        else if (pl.chunks[0] == 2)
+            for (int i = me_now * 2; i < s.n; i += FIN_WARPS * 2) complete_rows<FP8, 2, 2>(p, pl, s, i);
+        else
+            for (int i = me_now; i < s.n; i += FIN_WARPS) complete_rows<FP8, 1, 4>(p, pl, s, i);
         __threadfence();
         fence_proxy_async();
         __syncwarp();
-        if (lane == 0) atom_add_acq_rel_u32(&p.ctl->ready[s.a], 1u);
+        if (lane == 0) {
+            // the last of the warps publishes the block
+            if (atomicSub(&sm->job_left[in.i], 1u) == 1u) {
+                __threadfence();
+                atom_add_acq_rel_u32(&p.ctl->ready[s.a], 1u);
+            }
+            mbar_arrive(&sm->job_out[in.i]);
+        }
+        in.next(JOBS);
     }
 }
 
@@ -961,10 +1012,14 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
         }
         for (int i = 0; i < INFO_SLOTS; ++i) {
             mbar_init(&sm->info_in[i], 1);
-            mbar_init(&sm->info_out[i], 3 + EPI_WARPS);  // row loads, products, draining, one completing warp
+            mbar_init(&sm->info_out[i], 3 + EPI_WARPS);  // row loads, products, draining, counting
             mbar_init(&sm->piece_in[i], EPI_WARPS);
         }
         mbar_init(&sm->drain, 1);
+        for (int i = 0; i < JOBS; ++i) {
+            mbar_init(&sm->job_in[i], 1);
+            mbar_init(&sm->job_out[i], FIN_WARPS);
+        }
         fence_barrier_init();
         sm->ok = 1;
         tma_prefetch_desc(&m.w1);
@@ -1019,6 +1074,7 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
         if (warp == WARP_A) weight_loads<FP8>(p, m, sm, pl, wp);
         else if (warp == WARP_B) row_loads<FP8>(p, m, sm, pl, w);
         else if (warp == WARP_MMA) products<FP8>(sm, rg, wp);
+        else if (warp == WARP_COUNT) count_pieces(p, sm, pl, wp);
         else if (warp >= WARP_FIN) complete_h<FP8>(p, sm, pl, wp);
         else drain_accumulators<FP8>(p, sm, rg, pl, wp);
 
