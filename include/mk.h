@@ -343,7 +343,7 @@ mk_status_t mk_add_rmsnorm(const void* x, int64_t x_stride, const void* residual
  *   sequence's pages are not read), seq_lens[B] i32 (device)      -- read only
  *   out[B,Hq,D] bf16, lse[B,Hq] f32 (may be NULL)                 -- written
  * Limits: D = 64, 128 or 256; Hq a multiple of Hkv; any page_size >= 1;
- * B <= 4096; max_pages*page_size <= 2^31 - 16, and fewer than 2^31 tiles of
+ * B <= 4096; max_pages*page_size <= 2^31 - 32, and fewer than 2^31 tiles of
  * 16 keys and 16 query heads in all; strides non-negative multiples of 8
  * elements, caches 16-byte aligned, out 8, q 4 (q_stride even).  Keys and
  * values that are read are finite.  The lengths and pages are checked on the

@@ -8,7 +8,7 @@
 // the cache's bytes bound it: 4*D bytes per token and key-value head against
 // 4*D operations per query head.
 //
-// Work.  A tile is 16 keys of one (sequence, group of up to 16 query heads
+// Work.  A tile is 16 keys (32 with 64 columns a head) of one (sequence, group of up to 16 query heads
 // of one key-value head).  The tiles of all of them in a row are cut into one
 // equal range per CTA, and that into one per warp, whatever the lengths, so
 // every warp streams the same number of bytes and waits for no other.  The
@@ -38,7 +38,6 @@
 namespace mk {
 namespace {
 
-constexpr int KEYS = 16;          // keys per tile
 constexpr int ROWS = 16;          // query heads per group (rows of the product)
 // A group counts as this many tiles more than it has: its queries, its first
 // tile's latency and its result cost about that, and short groups would
@@ -52,25 +51,27 @@ constexpr float LN2 = 0.6931471805599453f;
 template <int D>
 struct Geo {
     static constexpr int WARPS = D == 256 ? 4 : 8;
-    static constexpr int STAGES = D == 64 ? 4 : 2;
+    static constexpr int STAGES = 2;
+    static constexpr int KEYS = D == 64 ? 32 : 16;    // keys per tile
     static constexpr int THREADS = WARPS * 32;
     static constexpr int CHUNKS = D / 8;              // 16-byte pieces of a row
     static constexpr int HALF = KEYS * D * 2;         // one tile's keys (or values)
     static constexpr int RING = STAGES * 2 * HALF;    // per warp
     static constexpr int OSTRIDE = D + 8;             // floats between rows of the join buffer: no bank conflicts
-    static constexpr int SM_PREFIX = WARPS * RING;
+    // A warp's result of its first group and of its last: O, m, l.  The last ones
+    // lie where the rings were.
+    static constexpr int PART = ROWS * OSTRIDE + 2 * ROWS;
+    static constexpr int SM_HEADS = WARPS * RING;
+    static constexpr int SM_PREFIX = SM_HEADS + WARPS * PART * 4;
     static constexpr int SM_SMALL = SM_PREFIX + (ATTN_MAX_B + 1) * 4 + 12;
     static constexpr int SMEM = SM_SMALL + 1024;
-    static constexpr int TAIL = ROWS * OSTRIDE + 2 * ROWS;  // floats of a warp's last result: O, m, l
-    static_assert(WARPS * TAIL * 4 <= SM_PREFIX, "the last results lie where the ring was");
+    static_assert(WARPS * PART * 4 <= SM_HEADS, "the last results lie where the rings were");
     static constexpr int SLOT = 2 * ROWS + ROWS * D;  // floats of a partial result: m, l, O
     static_assert(SMEM <= 232448, "dynamic shared memory of one CTA on sm_103");
 };
 
 constexpr size_t ATTN_SLOT_BYTES = size_t(Geo<256>::SLOT) * 4;
-// Two partial results per CTA and one per warp; fixed, so the counters never move.
-constexpr size_t ATTN_HEADS_AT = 2 * ATTN_MAX_CTAS * ATTN_SLOT_BYTES;
-constexpr size_t ATTN_SLOTS_BYTES = ATTN_HEADS_AT + 8 * ATTN_MAX_CTAS * ATTN_SLOT_BYTES;
+constexpr size_t ATTN_SLOTS_BYTES = 2 * ATTN_MAX_CTAS * ATTN_SLOT_BYTES;  // fixed, so the counters never move
 
 struct AttnParams {
     const __nv_bfloat16* q;
@@ -80,8 +81,7 @@ struct AttnParams {
     const int32_t* lens;
     __nv_bfloat16* out;
     float* lse;                                   // or null
-    float* slots;                                 // two partial results per CTA,
-    float* heads;                                 // and the first of each warp
+    float* slots;                                 // two partial results per CTA
     uint32_t* arrived;                            // per (sequence, group); zero between calls
     DevError* err;
     int64_t q_stride, page_stride, token_stride, head_stride;
@@ -148,8 +148,8 @@ struct Range {
     uint32_t begin;  // position of the group's first tile
     uint32_t tiles;  // tiles of the group
 };
-__host__ __device__ inline uint32_t positions_of(int len) {
-    return len > 0 ? uint32_t(len + KEYS - 1) / KEYS + EXTRA : 0u;
+__host__ __device__ inline uint32_t positions_of(int len, int keys) {
+    return len > 0 ? uint32_t(len + keys - 1) / uint32_t(keys) + EXTRA : 0u;
 }
 
 // The groups of the positions [pos, end) one after the other.
@@ -208,8 +208,9 @@ struct Cut {
     }
 };
 
-// Element offset of one key's row of a tile (row = lane for lanes 0-15), or
-// -1 when the key lies past the sequence.
+// Element offset of one key's row of a tile (row = lane, modulo the tile's
+// keys), or -1 when the key lies past the sequence.
+template <int KEYS>
 __device__ __forceinline__ int64_t key_offset(const AttnParams& p, int b, int kv, uint32_t tile, int lane, int len) {
     const int key = int(tile) * KEYS + (lane & (KEYS - 1));
     if (key >= len) return -1;
@@ -222,18 +223,20 @@ __device__ __forceinline__ int64_t key_offset(const AttnParams& p, int b, int kv
     return page * p.page_stride + (key - slot * p.page_size) * p.token_stride + kv * p.head_stride;
 }
 
-// A warp's result of a group: O rows `stride` floats apart, maxima and sums.
+// A warp's result of a group: O, m, l.
 template <int D>
-__device__ __forceinline__ void put_partial(float* so, int stride, float* sm, float* sl, int heads,
-                                            const float (&o)[D / 8][4], float m0, float m1, float l0, float l1) {
+__device__ __forceinline__ void put_partial(float* part, int heads, const float (&o)[D / 8][4], float m0, float m1,
+                                            float l0, float l1) {
+    constexpr int stride = Geo<D>::OSTRIDE;
     const int lane = threadIdx.x & 31, r0 = lane >> 2, r1 = r0 + 8;
+    float* sm = part + ROWS * stride;
     if ((lane & 3) == 0) {
         sm[r0] = m0;
         sm[r1] = m1;
-        sl[r0] = l0;
-        sl[r1] = l1;
+        sm[ROWS + r0] = l0;
+        sm[ROWS + r1] = l1;
     }
-    float* ow = so + (lane & 3) * 2;
+    float* ow = part + (lane & 3) * 2;
 #pragma unroll
     for (int n = 0; n < D / 8; ++n) {
         if (r0 < heads) *reinterpret_cast<float2*>(ow + r0 * stride + n * 8) = make_float2(o[n][0], o[n][1]);
@@ -297,7 +300,6 @@ __device__ void join_group(const AttnParams& p, const Range& r, const Cut& cut_a
     // a CTA's piece lies in its first slot if the group holds its range's start: that of the first CTA may not
     const float* first = p.slots + size_t(2 * c0 + (cut_at.start(c0) >= r.begin ? 0 : 1)) * (ATTN_SLOT_BYTES / 4);
     const float* other = p.slots + size_t(2 * c0) * (ATTN_SLOT_BYTES / 4);
-    __threadfence();
     for (int i0 = 0; i0 < items; i0 += G::THREADS) {
         const int item = parts > 1 ? tid % items : i0 + tid, part = parts > 1 ? tid / items : 0;
         const bool on = item < items && part < parts;
@@ -351,7 +353,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
         for (int b = b0; b < b1; ++b) {
             const int n = __ldg(p.lens + b);
             if ((n < 0 || n > cap) && blockIdx.x == 0) attn_error(p.err, SITE_SEQ_LEN, uint32_t(n));
-            mine += positions_of(length(b));
+            mine += positions_of(length(b), G::KEYS);
         }
         uint32_t run = mine;
 #pragma unroll
@@ -365,7 +367,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
         for (int w = 0; w < warp; ++w) base += small[w];
         for (int b = b0; b < b1; ++b) {
             prefix[b] = base;
-            base += positions_of(length(b));
+            base += positions_of(length(b), G::KEYS);
         }
         if (b1 == p.B && b0 < b1) prefix[p.B] = base;
         __syncthreads();
@@ -418,7 +420,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
                 for (int i = 0; i < D * 2; i += 128) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + i));
             }
         }
-        o = key_offset(p, lr.b, lr.g / p.chunks, load_tile, lane, load_len);
+        o = key_offset<G::KEYS>(p, lr.b, lr.g / p.chunks, load_tile, lane, load_len);
         h = true;
         ++load_tile;
     };
@@ -429,7 +431,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
         if (have[0]) {
             const uint32_t dst = ring + load_slot * (2 * G::HALF);
 #pragma unroll
-            for (int i = 0; i < KEYS * G::CHUNKS / 32; ++i) {
+            for (int i = 0; i < G::KEYS * G::CHUNKS / 32; ++i) {
                 const int piece = i * 32 + lane, row = piece / G::CHUNKS, c = piece % G::CHUNKS;
                 const int64_t ro = __shfl_sync(0xffffffffu, off[0], row);
                 const bool ok = ro >= 0;
@@ -452,8 +454,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
     uint32_t slot = 0;
     Walk walk{wstart, wend, prefix, p.B, groups, false};
     Range r;
-    // A group that the warp does not hold whole is its first (kept in the
-    // workspace) or its last (kept in registers until the rings are free).
+    // A group that the warp does not hold whole is its first (set aside in shared
+    // memory) or its last (kept in registers until the rings are free).
     Range head, tail;
     bool has_head = false, has_tail = false;
     float o[D / 8][4];
@@ -487,24 +489,28 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
             copy_wait<G::STAGES - 1>();
             __syncwarp();
             const uint32_t ks = ring + slot * (2 * G::HALF), vs = ks + G::HALF;
-            // scores: two tiles of 8 keys
-            float s[2][4] = {};
+            // scores: keys in tiles of 8
+            constexpr int NT = G::KEYS / 8;
+            float s[NT][4] = {};
             {
                 const int row = ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
                 const uint32_t rb = ks + uint32_t(row * D * 2);
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    uint32_t kb[4];
-                    ldsm4(rb + (uint32_t((kk * 2 + half) ^ (row & 7)) << 4), kb);
-                    mma16816(s[0], qa[kk], kb[0], kb[1]);
-                    mma16816(s[1], qa[kk], kb[2], kb[3]);
+#pragma unroll
+                    for (int n = 0; n < NT; n += 2) {
+                        uint32_t kb[4];
+                        ldsm4(rb + n * 8 * D * 2 + (uint32_t((kk * 2 + half) ^ (row & 7)) << 4), kb);
+                        mma16816(s[n], qa[kk], kb[0], kb[1]);
+                        mma16816(s[n + 1], qa[kk], kb[2], kb[3]);
+                    }
                 }
             }
-            const int key = int(t) * KEYS + (lane & 3) * 2;
-            const bool cut = int(t + 1) * KEYS > len;
+            const int key = int(t) * G::KEYS + (lane & 3) * 2;
+            const bool cut = int(t + 1) * G::KEYS > len;
             float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
+            for (int n = 0; n < NT; ++n) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     s[n][i] *= p.scale2;
@@ -536,23 +542,25 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
             }
             // a row whose scores are all -inf has weights 0, not e^(-inf + inf)
             const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
-            uint32_t hi[4], lo[4];
 #pragma unroll
-            for (int n = 0; n < 2; ++n) {
-                const float p0 = exp2_of(s[n][0] - b0), p1 = exp2_of(s[n][1] - b0);
-                const float p2 = exp2_of(s[n][2] - b1), p3 = exp2_of(s[n][3] - b1);
-                l0 += p0 + p1;
-                l1 += p2 + p3;
-                // each weight as the sum of two bf16 values: 16 significant bits reach the products
-                hi[2 * n] = pack_bf16(p0, p1);
-                hi[2 * n + 1] = pack_bf16(p2, p3);
-                lo[2 * n] = pack_bf16(p0 - __uint_as_float(hi[2 * n] << 16),
-                                      p1 - __uint_as_float(hi[2 * n] & 0xffff0000u));
-                lo[2 * n + 1] = pack_bf16(p2 - __uint_as_float(hi[2 * n + 1] << 16),
-                                          p3 - __uint_as_float(hi[2 * n + 1] & 0xffff0000u));
-            }
-            {
-                const int row = (((lane >> 3) & 1) << 3) + (lane & 7), half = lane >> 4;
+            for (int kk = 0; kk < NT / 2; ++kk) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    const float(&sn)[4] = s[2 * kk + n];
+                    const float p0 = exp2_of(sn[0] - b0), p1 = exp2_of(sn[1] - b0);
+                    const float p2 = exp2_of(sn[2] - b1), p3 = exp2_of(sn[3] - b1);
+                    l0 += p0 + p1;
+                    l1 += p2 + p3;
+                    // each weight as the sum of two bf16 values: 16 significant bits reach the products
+                    hi[2 * n] = pack_bf16(p0, p1);
+                    hi[2 * n + 1] = pack_bf16(p2, p3);
+                    lo[2 * n] = pack_bf16(p0 - __uint_as_float(hi[2 * n] << 16),
+                                          p1 - __uint_as_float(hi[2 * n] & 0xffff0000u));
+                    lo[2 * n + 1] = pack_bf16(p2 - __uint_as_float(hi[2 * n + 1] << 16),
+                                              p3 - __uint_as_float(hi[2 * n + 1] & 0xffff0000u));
+                }
+                const int row = kk * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), half = lane >> 4;
                 const uint32_t rb = vs + uint32_t(row * D * 2);
 #pragma unroll
                 for (int n = 0; n < D / 16; ++n) {
@@ -591,8 +599,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
         } else if (walk.pos < walk.end) {
             head = r;
             has_head = true;
-            float* s = p.heads + size_t(blockIdx.x * G::WARPS + warp) * (ATTN_SLOT_BYTES / 4);
-            put_partial<D>(s + 2 * ROWS, D, s, s + ROWS, heads, o, m0, m1, l0, l1);
+            put_partial<D>(reinterpret_cast<float*>(smem + G::SM_HEADS) + warp * G::PART, heads, o, m0, m1, l0, l1);
         } else {
             tail = r;
             has_tail = true;
@@ -610,11 +617,10 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
         pieces[2 * warp + 1] = tail;
     }
     float* tails = reinterpret_cast<float*>(smem);
+    const float* firsts = reinterpret_cast<const float*>(smem + G::SM_HEADS);
     if (has_tail) {
         const int kv = tail.g / p.chunks, head0 = kv * p.per_kv + (tail.g % p.chunks) * ROWS;
-        float* s = tails + warp * G::TAIL;
-        put_partial<D>(s, G::OSTRIDE, s + ROWS * G::OSTRIDE, s + ROWS * G::OSTRIDE + ROWS,
-                       min(ROWS, (kv + 1) * p.per_kv - head0), o, m0, m1, l0, l1);
+        put_partial<D>(tails + warp * G::PART, min(ROWS, (kv + 1) * p.per_kv - head0), o, m0, m1, l0, l1);
     }
     __syncthreads();
     Range open[2];  // groups shared with other CTAs: the first and the last one's
@@ -645,14 +651,10 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
                     if (rest == 0) continue;
                     const int i = __ffs(int(rest)) - 1, w = i >> 1;
                     rest &= rest - 1;
-                    if (i & 1) {
-                        const float* s = tails + w * G::TAIL;
-                        u[x].m = s[ROWS * G::OSTRIDE + row];
-                        u[x].l = s[ROWS * G::OSTRIDE + ROWS + row];
-                        u[x].o = *reinterpret_cast<const float4*>(s + row * G::OSTRIDE + c);
-                    } else {
-                        u[x].load(p.heads + size_t(blockIdx.x * G::WARPS + w) * (ATTN_SLOT_BYTES / 4), row, c, D);
-                    }
+                    const float* s = (i & 1 ? tails : firsts) + w * G::PART;
+                    u[x].m = s[ROWS * G::OSTRIDE + row];
+                    u[x].l = s[ROWS * G::OSTRIDE + ROWS + row];
+                    u[x].o = *reinterpret_cast<const float4*>(s + row * G::OSTRIDE + c);
                 }
                 acc.add(u);
             }
@@ -671,8 +673,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
     if (nopen == 0) return;
 
     // ---- groups shared with other CTAs: the one that arrives last joins their
-    // partial results
-    __threadfence();
+    // partial results (the count releases what the whole CTA has stored)
     __syncthreads();
     if (tid < nopen) {
         const Range& o = tid == 0 ? open[0] : open[1];
@@ -734,9 +735,9 @@ extern "C" mk_status_t mk_paged_attention(const void* q, int64_t q_stride, const
     if (!std::isfinite(scale)) return MK_ERR_INVALID_ARG;
     const int64_t groups = attn_groups(B, Hq, Hkv);
     const int64_t cap = int64_t(max_pages) * page_size;
-    if (B > ATTN_MAX_B || cap > (int64_t(1) << 31) - KEYS) return MK_ERR_UNSUPPORTED;
+    if (B > ATTN_MAX_B || cap > (int64_t(1) << 31) - 32) return MK_ERR_UNSUPPORTED;
     // positions in the order of tiles are 32-bit
-    const int64_t tiles = int64_t(B) * positions_of(int(cap));
+    const int64_t tiles = int64_t(B) * positions_of(int(cap), D == 64 ? Geo<64>::KEYS : Geo<128>::KEYS);
     if (tiles >= int64_t(1) << 31 || tiles * groups >= int64_t(1) << 31) return MK_ERR_UNSUPPORTED;
     if (B > 0) {
         if (!q || !seq_lens || !out) return MK_ERR_INVALID_ARG;
@@ -775,7 +776,6 @@ extern "C" mk_status_t mk_paged_attention(const void* q, int64_t q_stride, const
     p.out = static_cast<__nv_bfloat16*>(out);
     p.lse = lse;
     p.slots = reinterpret_cast<float*>(ws);
-    p.heads = reinterpret_cast<float*>(ws + ATTN_HEADS_AT);
     p.arrived = reinterpret_cast<uint32_t*>(ws + ATTN_SLOTS_BYTES);
     p.err = err;
     p.q_stride = q_stride;
