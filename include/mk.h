@@ -302,7 +302,13 @@ size_t mk_workspace_size(int T, int H, int F, int E, int k, const mk_config_t* c
  * without synchronising; arguments are checked first and nothing is launched
  * on a failure (MK_ERR_INVALID_ARG, MK_ERR_UNSUPPORTED); a device of compute
  * capability 10.3.  Sums, norms and softmax statistics are held in fp32 and
- * each output is rounded once.  Equal inputs give equal bits. */
+ * each output is rounded once.  Equal inputs give equal bits.
+ *
+ * They can be captured in a CUDA graph.  Under capture the library's
+ * workspace cache is not grown (MK_ERR_WORKSPACE): make a call of the same
+ * sizes on that stream before.  A captured call keeps the workspace's address,
+ * so while the graph lives give its stream no larger call, or capture with a
+ * caller workspace. */
 
 /* The residual's addition and the root-mean-square norm, in bf16 and / or in
  * 8 bits.  With z = x + residual (x alone when residual is NULL):

@@ -270,6 +270,12 @@ mk_status_t host_workspace(WsKind kind, int dev, cudaStream_t st, size_t need, s
     std::lock_guard<std::mutex> lock(g_mu);
     WsEntry& w = g_ws[kind][{dev, st}];
     if (w.bytes < need) {
+        if (kind == WS_ATTN || kind == WS_FFN) {
+            // memory allocated under stream capture would belong to the graph
+            cudaStreamCaptureStatus capturing;
+            if (cudaStreamIsCapturing(st, &capturing) != cudaSuccess) return MK_ERR_CUDA;
+            if (capturing != cudaStreamCaptureStatusNone) return MK_ERR_WORKSPACE;
+        }
         if (w.ptr && cudaFreeAsync(w.ptr, st) != cudaSuccess) return MK_ERR_CUDA;
         w.ptr = nullptr;
         w.bytes = 0;
