@@ -445,19 +445,31 @@ def mk_add_rmsnorm(x, x_stride, residual, residual_stride, weight, T, H, eps, ou
 
 # The tensor forms below are called once per layer and token, so they do
 # little: checks without temporaries, the raw stream handle, one allocation
-# per output, and the C entry (on the host of a GB300 torch.cuda.current_stream
-# alone takes 2.9 us, the raw handle 0.1).
+# per output, and the C entry.  On the host of a GB300 (us): torch.cuda.
+# current_stream 2.9, the raw handle 0.1; torch.empty 1.5, the allocator's own
+# entry 0.8.
 
 _torch = None
-_raw_stream = None
+_raw_stream = None  # device index -> cudaStream_t of its current stream
+_empty = None       # (shape, strides, dtype, device index) -> uninitialised CUDA tensor
 
 
 def _load_torch():
-    global _torch, _raw_stream
+    global _torch, _raw_stream, _empty
     import torch
 
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda device: torch.cuda.current_stream(device).cuda_stream)
+    guards = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
+    direct = getattr(guards, "_empty_strided_cuda", None)  # on the current device
+    current = getattr(torch._C, "_cuda_getDevice", None)
+
+    def empty(shape, strides, dtype, device):
+        if direct is not None and current is not None and current() == device:
+            return direct(shape, strides, dtype)
+        return torch.empty_strided(shape, strides, dtype=dtype, device=torch.device("cuda", device))
+
+    _empty = empty
     _torch = torch
     return torch
 
@@ -492,27 +504,27 @@ def add_rmsnorm(x, weight, residual=None, eps=1e-6, bf16=True, e4m3=False, resid
         raise ValueError("x must be a CUDA bf16 [T,H] tensor with contiguous rows")
     if weight.dtype is not b16 or weight.get_device() != dev or weight.shape != (H,) or not weight.is_contiguous():
         raise ValueError("weight must be bf16 [H] on x's device")
-    empty = torch.empty
-    device = x.device
+    empty, shape, strides = _empty, (T, H), (H, 1)
     o = {}
     out = out8 = scale = p_out = p_out8 = p_scale = p_res = p_new = None
     if bf16:
-        o["out"] = out = empty((T, H), dtype=b16, device=device)
+        o["out"] = out = empty(shape, strides, b16, dev)
         p_out = out.data_ptr()
     if e4m3:
-        o["out8"] = out8 = empty((T, H), dtype=torch.float8_e4m3fn, device=device)
-        o["scale"] = scale = empty((T, -(-H // 128)), dtype=torch.float32, device=device)
+        groups = -(-H // 128)
+        o["out8"] = out8 = empty(shape, strides, torch.float8_e4m3fn, dev)
+        o["scale"] = scale = empty((T, groups), (groups, 1), torch.float32, dev)
         p_out8, p_scale = out8.data_ptr(), scale.data_ptr()
     elif not bf16:
         raise ValueError("no output asked for")
     r_stride = 0
     if residual is not None:
-        if (residual.dtype is not b16 or residual.get_device() != dev or residual.shape != (T, H)
+        if (residual.dtype is not b16 or residual.get_device() != dev or residual.shape != shape
                 or (residual.stride(1) != 1 and H != 1)):
             raise ValueError("residual must be bf16 [T,H] with contiguous rows on x's device")
         if residual_out is None:
-            residual_out = empty((T, H), dtype=b16, device=device)
-        elif (residual_out.dtype is not b16 or residual_out.get_device() != dev or residual_out.shape != (T, H)
+            residual_out = empty(shape, strides, b16, dev)
+        elif (residual_out.dtype is not b16 or residual_out.get_device() != dev or residual_out.shape != shape
               or not residual_out.is_contiguous()):
             raise ValueError("residual_out must be contiguous bf16 [T,H] on x's device")
         o["residual"] = residual_out
@@ -571,9 +583,8 @@ def paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale=None, stre
     if (seq_lens.shape != (B,) or seq_lens.dtype is not i32 or seq_lens.get_device() != dev
             or not seq_lens.is_contiguous()):
         raise ValueError("seq_lens must be i32 [B]")
-    device = q.device
-    out = torch.empty((B, Hq, D), dtype=b16, device=device)
-    lse = torch.empty((B, Hq), dtype=torch.float32, device=device)
+    out = _empty((B, Hq, D), (Hq * D, D, 1), b16, dev)
+    lse = _empty((B, Hq), (Hq, 1), torch.float32, dev)
     status = lib().mk_paged_attention(
         q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(), page, token, head, block_table.data_ptr(),
         seq_lens.data_ptr(), B, Hq, Hkv, D, page_size, max_pages, pages, D ** -0.5 if scale is None else scale,
@@ -626,7 +637,7 @@ def moe_ffn_decode(x, logits, W1, W3, W2, k, x_scale=None, W1_scale=None, W3_sca
         if t is None or t.shape != shape or t.dtype is not f32 or t.get_device() != dev or not t.is_contiguous():
             raise ValueError("logits [T,E], x_scale [T,H/128] and the weights' scales (a value per 128 x 128 block) "
                              "must be contiguous f32 on x's device")
-    out = torch.empty((T, H), dtype=torch.bfloat16, device=x.device)
+    out = _empty((T, H), (H, 1), torch.bfloat16, dev)
     status = lib().mk_moe_ffn_decode(
         x.data_ptr(), x_scale.data_ptr() if fp8 else None, logits.data_ptr(), T, H, E, k, W1.data_ptr(), W3.data_ptr(),
         W2.data_ptr(), *([t.data_ptr() for t in scales[1:]] if fp8 else (None, None, None)), F,

@@ -432,6 +432,7 @@ __device__ void weight_loads(const FfnParams& p, const FfnMaps& m, FfnSmem* sm, 
         const int ncol = s.half ? p.H : p.F;
         const int row0 = s.expert * (s.half ? p.F : p.H);
         const CUtensorMap* map = s.half ? &m.w2 : s.second ? &m.w3 : &m.w1;
+#pragma unroll 1
         for (uint32_t k = s.k0; k < s.k1; ++k) {
             if (!warp_await_mbar(&sm->empty[st.i], st.phase ^ 1u, w, SITE_STAGE_EMPTY)) {
                 mine.settle(sm->weights_in);
@@ -501,6 +502,7 @@ __device__ void row_loads(const FfnParams& p, const FfnMaps& m, FfnSmem* sm, con
             sw = (s.half ? p.w2_scale : s.second ? p.w3_scale : p.w1_scale) +
                  size_t(s.expert) * KB8 * NB8 + min(2 * s.blk + (lane & 1), NB8 - 1);
         }
+#pragma unroll 1
         for (uint32_t k = s.k0; ok && k < s.k1; ++k) {
             if (!(ok = warp_await_mbar(&sm->empty[st.i], st.phase ^ 1u, w, SITE_STAGE_EMPTY))) break;
             uint64_t* fb = &sm->rows_in[st.i];
@@ -553,6 +555,7 @@ __device__ void products(FfnSmem* sm, const Accs& accs, const Waiter& w) {
         const uint32_t half = uniform(uint32_t(s.half)), steps = uniform(s.k1 - s.k0);
         const uint32_t N = uniform(uint32_t(pad16(s.n))) * (FP8 ? 1 : 1 + half);
         const uint32_t idesc = FP8 ? umma_idesc_e4m3(128, N, true, false) : umma_idesc_bf16(128, N, true, false);
+#pragma unroll 1
         for (uint32_t k = 0; k < steps; ++k) {
             // 16 bits: one accumulation per unit; 8 bits: one per step
             if (FP8 || k == 0) {
@@ -761,10 +764,7 @@ __device__ void complete_h(const FfnParams& p, FfnSmem* sm, const Plan& pl, cons
         __syncwarp();
         if (lane == 0) {
             // the last of the warps publishes the block
-            if (atomicSub(&sm->job_left[in.i], 1u) == 1u) {
-                __threadfence();
-                atom_add_acq_rel_u32(&p.ctl->ready[s.a], 1u);
-            }
+            if (atomicSub(&sm->job_left[in.i], 1u) == 1u) atom_add_acq_rel_u32(&p.ctl->ready[s.a], 1u);
             mbar_arrive(&sm->job_out[in.i]);
         }
         in.next(JOBS);
@@ -783,6 +783,7 @@ __device__ __forceinline__ bool drain_steps8(FfnSmem* sm, const Accs& rg, const 
     for (int b = 0; b < B; ++b)
 #pragma unroll
         for (int i = 0; i < 16; ++i) acc0[b][i] = acc1[b][i] = 0.f;
+#pragma unroll 1
     for (uint32_t k = 0; k < steps; ++k) {
         if (ok) ok = warp_await_mbar(&sm->scales_in[sc.i], sc.phase, w, SITE_ACC_FULL);
         if (ok) ok = warp_await_mbar(&sm->acc_full[buf.i], buf.phase, w, SITE_ACC_FULL);
@@ -856,6 +857,7 @@ __device__ void drain_accumulators(const FfnParams& p, FfnSmem* sm, const Accs& 
             if (ok) {
                 tc_fence_after();
                 const uint32_t t0 = tq + buf.i * 2u * rg.acc_stride;
+#pragma unroll 1
                 for (int blk = set; blk < nblk; blk += 2) {
                     uint32_t r0[16], r1[16];
                     float v0[16], v1[16];
@@ -895,7 +897,6 @@ __device__ void drain_accumulators(const FfnParams& p, FfnSmem* sm, const Accs& 
         if (lane == 0) mbar_arrive(&sm->piece_in[done.i]);
         done.next(INFO_SLOTS);
     }
-    __threadfence();
 }
 
 __device__ __forceinline__ void add4(float4& a, const float4& b) {
@@ -1080,7 +1081,7 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
 
         __syncthreads();
         if (tid == 0) {
-            __threadfence();
+            // releases what the whole CTA has stored
             atom_add_acq_rel_u32(&p.ctl->done, 1u);
             sm->ok = await_geq(&p.ctl->done, gridDim.x, w, SITE_BAR_COMPUTED) && ld_relaxed_u32(w.abort) == 0u;
         }
