@@ -385,7 +385,7 @@ enum { MK_WEIGHT_BF16 = 0, MK_WEIGHT_E4M3 = 1 };
  *   x[T,H], logits[T,E] f32, W1[E,H,F], W3[E,H,F], W2[E,F,H],
  *   x_scale[T,H/128] f32, W1_scale[E,H/128,F/128] f32, W3_scale likewise,
  *   W2_scale[E,F/128,H/128] f32                                   -- read only
- *   out[T,H] bf16                                                 -- written
+ *   out[T,H] bf16, overlapping no input                           -- written
  * Limits: 0 <= T <= 128, 1 <= k <= min(E, 8), E <= 256, H and F multiples of
  * 64 (bf16) or 128 (e4m3) up to 32768; x, weights and out 16-byte aligned,
  * f32 arrays 4.  Only the chosen experts' weights are read, each once.
@@ -410,7 +410,8 @@ mk_status_t mk_get_status(void* stream);
 /* Detail of the last recorded device error: site code and CTA (or -1). */
 void mk_last_error_detail(int32_t* site, int32_t* cta, int32_t* info);
 
-/* Facts about the last call on this thread (grid, role split, launches). */
+/* Facts about the last dispatch call on this thread (grid, role split,
+ * launches); the operators of a decode step do not change them. */
 void mk_last_launch_info(mk_launch_info_t* info);
 
 /* Copy the phase stamps of the last traced call (cfg.trace = 1) made with

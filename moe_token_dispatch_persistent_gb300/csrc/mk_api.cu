@@ -257,16 +257,18 @@ mk_status_t cached_workspace(int dev, cudaStream_t st, size_t need, size_t zero_
 
 namespace mk {
 
-mk_status_t host_device(int* dev, int* sms, DevError** err) {
+mk_status_t host_device(int* dev, int* sms, DevError** err) try {
     DevInfo* d = nullptr;
     const mk_status_t s = device_info(dev, &d);
     if (s != MK_OK) return s;
     *sms = d->sms;
     *err = d->err;
     return MK_OK;
+} catch (...) {
+    return MK_ERR_CUDA;
 }
 
-mk_status_t host_workspace(WsKind kind, int dev, cudaStream_t st, size_t need, size_t zero_bytes, void** out) {
+mk_status_t host_workspace(WsKind kind, int dev, cudaStream_t st, size_t need, size_t zero_bytes, void** out) try {
     std::lock_guard<std::mutex> lock(g_mu);
     WsEntry& w = g_ws[kind][{dev, st}];
     if (w.bytes < need) {
@@ -289,6 +291,8 @@ mk_status_t host_workspace(WsKind kind, int dev, cudaStream_t st, size_t need, s
     }
     *out = w.ptr;
     return MK_OK;
+} catch (...) {  // no memory for the cache's own entry
+    return MK_ERR_WORKSPACE;
 }
 
 CUresult host_encode_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t outer,
@@ -942,6 +946,7 @@ mk_status_t mk_read_trace(void* stream, const void* workspace, int T, int H, int
 void mk_release_workspace(void) {
     noalloc_forget_scratch();  // the allocation-free entry point looks its array up again
     std::lock_guard<std::mutex> lock(g_mu);
+    for (auto& d : g_dev) d.ready = false;  // after a device reset: attributes and addresses are looked up again
     int cur = 0;
     cudaGetDevice(&cur);
     // streams may be gone by now: synchronise the device, then free

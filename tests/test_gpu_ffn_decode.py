@@ -212,3 +212,16 @@ def test_agrees_with_the_dispatch_path():
     want.index_add_(0, o["src_index"].long() // 4, o["gate_w"].double()[:, None] * y)
     # both are fp32 sums; the dispatch path uses the fast exponential
     assert (layer.run().double() - want).abs().max() <= 2.0 ** -8 * want.abs().max() + 1e-4
+
+
+def test_offsets_past_32_bits():
+    # weights of more than 2^31 elements a matrix; only the last experts are used, and only they are set
+    E, H, F = 230, 4096, 2560
+    logits = torch.full((3, E), -5.0)
+    logits[:, E - 4:] = torch.randn((3, 4), generator=torch.Generator().manual_seed(1))
+    small = Layer(3, H, F, 4, 3, seed=14, logits=logits[:, E - 4:].contiguous())
+    W1, W3, W2 = (torch.empty((E, *w.shape[1:]), dtype=torch.bfloat16, device="cuda") for w in (small.W1, small.W3, small.W2))
+    for big, w in ((W1, small.W1), (W3, small.W3), (W2, small.W2)):
+        big[E - 4:] = w
+    out = mk.moe_ffn_decode(small.x, logits.cuda(), W1, W3, W2, 3)["out"]
+    assert torch.equal(out, small.run())

@@ -156,3 +156,23 @@ def test_no_rows_and_another_stream():
     assert mk.mk_get_status(side) == mk.MK_OK
     for name in here:
         assert torch.equal(here[name].view(torch.uint8), there[name].view(torch.uint8)), name
+
+
+def test_offsets_past_32_bits():
+    # rows 2^30 elements apart, and more than 2^31 elements of output
+    x, r, w = _rows(3, 72, 19), _rows(3, 72, 20), _rows(1, 72, 21)[0]
+    far = torch.empty(2 * (2 ** 30 + 8) + 72, dtype=torch.bfloat16, device="cuda").as_strided((3, 72), (2 ** 30 + 8, 1))
+    far.copy_(x)
+    o, want = mk.add_rmsnorm(far, w, residual=r, e4m3=True), mk.add_rmsnorm(x, w, residual=r, e4m3=True)
+    for name in o:
+        assert torch.equal(o[name].view(torch.uint8), want[name].view(torch.uint8)), name
+    del far
+    T, H = 2 ** 31 // 32768 + 9, 32768
+    big = torch.zeros((T, H), dtype=torch.bfloat16, device="cuda")
+    tail = _rows(5, H, 22)
+    big[-5:] = tail
+    w = _rows(1, H, 23)[0]
+    o, want = mk.add_rmsnorm(big, w, residual=big, e4m3=True), mk.add_rmsnorm(tail, w, residual=tail, e4m3=True)
+    for name in o:
+        assert torch.equal(o[name][-5:].view(torch.uint8), want[name].view(torch.uint8)), name
+    assert torch.all(o["out"][:-5:4096] == 0)
