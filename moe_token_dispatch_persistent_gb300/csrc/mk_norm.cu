@@ -272,9 +272,12 @@ extern "C" mk_status_t mk_add_rmsnorm(const void* x, int64_t x_stride, const voi
                      host_aligned(x, 16) && host_aligned(residual, 16) && host_aligned(weight, 16) &&
                      host_aligned(out, 16) && host_aligned(residual_out, 16) && host_aligned(out8, 8);
     const int chunks = (H + NORM_CHUNK - 1) / NORM_CHUNK;
-    // A chunk per warp as far as a CTA's 32 warps go (all of a row is then loaded
-    // at once; two or four per warp measured within 4% on 4096 to 7168 columns).
-    const int per_warp = chunks <= NORM_MAX_WARPS ? 1 : chunks <= 2 * NORM_MAX_WARPS ? 2 : 4;
+    // A chunk per warp while two CTAs fit an SM (16 warps a row), or as far as a
+    // CTA's 32 warps go when there is no more than a row per SM (all of a row is
+    // then loaded at once); two or four beyond.  8192 x 7168: 85 us with two
+    // chunks per warp, 92 with one.
+    const bool one = chunks <= NORM_MAX_WARPS / 2 || (T <= sms && chunks <= NORM_MAX_WARPS);
+    const int per_warp = one ? 1 : chunks <= 2 * NORM_MAX_WARPS ? 2 : 4;
     p.warps_per_row = (chunks + per_warp - 1) / per_warp;
     p.rows_per_cta = p.warps_per_row >= 8 ? 1 : 8 / p.warps_per_row;
     const int64_t wanted = (int64_t(T) + p.rows_per_cta - 1) / p.rows_per_cta;
