@@ -474,13 +474,39 @@ def _load_torch():
     return torch
 
 
-def _finish(status, what, stream, check, *outputs):
-    """Errors of a call, and the outputs' use of a torch stream that is not the
-    current one: the allocator must not hand their memory out while it runs."""
-    if stream is not None and hasattr(stream, "cuda_stream"):
-        for t in outputs:
+def _other_stream(stream, device):
+    """A stream that the caller names, as a torch stream; None when it is the
+    current one."""
+    handle = _stream(stream)
+    if handle == _raw_stream(device):
+        return None
+    if isinstance(stream, _torch.cuda.Stream):
+        return stream
+    return _torch.cuda.ExternalStream(handle, device) if handle else _torch.cuda.default_stream(device)
+
+
+def _empty_on(stream):
+    """_empty from a stream's own memory: what the current stream's pool gives
+    out may have earlier work of that stream pending on it."""
+    def empty(*args):
+        with _torch.cuda.stream(stream):
+            return _empty(*args)
+
+    return empty
+
+
+def _finish(status, what, stream, other, check, taken, made):
+    """Errors of a call.  When it ran on another stream than the current one,
+    the allocator is told who uses what: the other stream the caller's tensors
+    (`taken`), the current one those that the call has made."""
+    if other is not None:
+        for t in taken:
+            if hasattr(t, "record_stream"):
+                t.record_stream(other)
+        here = _torch.cuda.current_stream(other.device)
+        for t in made:
             if t is not None:
-                t.record_stream(stream)
+                t.record_stream(here)
     if status != MK_OK:
         raise MkError(status, what)
     if check:
@@ -504,9 +530,10 @@ def add_rmsnorm(x, weight, residual=None, eps=1e-6, bf16=True, e4m3=False, resid
         raise ValueError("x must be a CUDA bf16 [T,H] tensor with contiguous rows")
     if weight.dtype is not b16 or weight.get_device() != dev or weight.shape != (H,) or not weight.is_contiguous():
         raise ValueError("weight must be bf16 [H] on x's device")
-    empty, shape, strides = _empty, (T, H), (H, 1)
+    other = None if stream is None else _other_stream(stream, dev)
+    empty, shape, strides = _empty if other is None else _empty_on(other), (T, H), (H, 1)
     o = {}
-    out = out8 = scale = p_out = p_out8 = p_scale = p_res = p_new = None
+    out = out8 = scale = new = p_out = p_out8 = p_scale = p_res = p_new = None
     if bf16:
         o["out"] = out = empty(shape, strides, b16, dev)
         p_out = out.data_ptr()
@@ -523,7 +550,7 @@ def add_rmsnorm(x, weight, residual=None, eps=1e-6, bf16=True, e4m3=False, resid
                 or (residual.stride(1) != 1 and H != 1)):
             raise ValueError("residual must be bf16 [T,H] with contiguous rows on x's device")
         if residual_out is None:
-            residual_out = empty(shape, strides, b16, dev)
+            residual_out = new = empty(shape, strides, b16, dev)
         elif (residual_out.dtype is not b16 or residual_out.get_device() != dev or residual_out.shape != shape
               or not residual_out.is_contiguous()):
             raise ValueError("residual_out must be contiguous bf16 [T,H] on x's device")
@@ -533,8 +560,9 @@ def add_rmsnorm(x, weight, residual=None, eps=1e-6, bf16=True, e4m3=False, resid
         raise ValueError("residual_out needs a residual")
     status = lib().mk_add_rmsnorm(x.data_ptr(), x.stride(0), p_res, r_stride, weight.data_ptr(), T, H, eps, p_out, p_out8,
                                   p_scale, p_new, _raw_stream(dev) if stream is None else _stream(stream))
-    if status or check or stream is not None:
-        _finish(status, "mk_add_rmsnorm", stream, check, out, out8, scale, residual_out)
+    if status or check or other is not None:
+        _finish(status, "mk_add_rmsnorm", stream, other, check,
+                (x, weight, residual, None if new is residual_out else residual_out), (out, out8, scale, new))
     return o
 
 
@@ -583,15 +611,18 @@ def paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale=None, stre
     if (seq_lens.shape != (B,) or seq_lens.dtype is not i32 or seq_lens.get_device() != dev
             or not seq_lens.is_contiguous()):
         raise ValueError("seq_lens must be i32 [B]")
-    out = _empty((B, Hq, D), (Hq * D, D, 1), b16, dev)
-    lse = _empty((B, Hq), (Hq, 1), torch.float32, dev)
+    other = None if stream is None else _other_stream(stream, dev)
+    empty = _empty if other is None else _empty_on(other)
+    out = empty((B, Hq, D), (Hq * D, D, 1), b16, dev)
+    lse = empty((B, Hq), (Hq, 1), torch.float32, dev)
     status = lib().mk_paged_attention(
         q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(), page, token, head, block_table.data_ptr(),
         seq_lens.data_ptr(), B, Hq, Hkv, D, page_size, max_pages, pages, D ** -0.5 if scale is None else scale,
         out.data_ptr(), lse.data_ptr(), _raw_stream(dev) if stream is None else _stream(stream), _ptr(workspace),
         ws_bytes)
-    if status or check or stream is not None:
-        _finish(status, "mk_paged_attention", stream, check, out, lse)
+    if status or check or other is not None:
+        _finish(status, "mk_paged_attention", stream, other, check,
+                (q, k_cache, v_cache, block_table, seq_lens, workspace), (out, lse))
     return {"out": out, "lse": lse}
 
 
@@ -637,12 +668,13 @@ def moe_ffn_decode(x, logits, W1, W3, W2, k, x_scale=None, W1_scale=None, W3_sca
         if t is None or t.shape != shape or t.dtype is not f32 or t.get_device() != dev or not t.is_contiguous():
             raise ValueError("logits [T,E], x_scale [T,H/128] and the weights' scales (a value per 128 x 128 block) "
                              "must be contiguous f32 on x's device")
-    out = _empty((T, H), (H, 1), torch.bfloat16, dev)
+    other = None if stream is None else _other_stream(stream, dev)
+    out = (_empty if other is None else _empty_on(other))((T, H), (H, 1), torch.bfloat16, dev)
     status = lib().mk_moe_ffn_decode(
         x.data_ptr(), x_scale.data_ptr() if fp8 else None, logits.data_ptr(), T, H, E, k, W1.data_ptr(), W3.data_ptr(),
         W2.data_ptr(), *([t.data_ptr() for t in scales[1:]] if fp8 else (None, None, None)), F,
         MK_WEIGHT_E4M3 if fp8 else MK_WEIGHT_BF16, out.data_ptr(),
         _raw_stream(dev) if stream is None else _stream(stream), _ptr(workspace), ws_bytes)
-    if status or check or stream is not None:
-        _finish(status, "mk_moe_ffn_decode", stream, check, out)
+    if status or check or other is not None:
+        _finish(status, "mk_moe_ffn_decode", stream, other, check, (x, logits, W1, W3, W2, *scales, workspace), (out,))
     return {"out": out}
