@@ -451,27 +451,33 @@ def mk_add_rmsnorm(x, x_stride, residual, residual_stride, weight, T, H, eps, ou
 
 _torch = None
 _raw_stream = None  # device index -> cudaStream_t of its current stream
-_empty = None       # (shape, strides, dtype, device index) -> uninitialised CUDA tensor
+_device = None      # () -> index of the current device, the one the C entries launch on
+_empty = None       # (shape, strides, dtype, current device's index) -> uninitialised CUDA tensor
 
 
 def _load_torch():
-    global _torch, _raw_stream, _empty
+    global _torch, _raw_stream, _device, _empty
     import torch
 
     _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
         lambda device: torch.cuda.current_stream(device).cuda_stream)
     guards = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
     direct = getattr(guards, "_empty_strided_cuda", None)  # on the current device
-    current = getattr(torch._C, "_cuda_getDevice", None)
 
     def empty(shape, strides, dtype, device):
-        if direct is not None and current is not None and current() == device:
+        if direct is not None:
             return direct(shape, strides, dtype)
         return torch.empty_strided(shape, strides, dtype=dtype, device=torch.device("cuda", device))
 
     _empty = empty
+    _device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
     _torch = torch
     return torch
+
+
+def _on_device(dev):
+    if dev != _device():
+        raise ValueError(f"the tensors are on device {dev}, the current one is {_device()}")
 
 
 def _other_stream(stream, device):
@@ -528,6 +534,7 @@ def add_rmsnorm(x, weight, residual=None, eps=1e-6, bf16=True, e4m3=False, resid
     dev = x.get_device()
     if dev < 0 or x.dtype is not b16 or (x.stride(1) != 1 and H != 1):
         raise ValueError("x must be a CUDA bf16 [T,H] tensor with contiguous rows")
+    _on_device(dev)
     if weight.dtype is not b16 or weight.get_device() != dev or weight.shape != (H,) or not weight.is_contiguous():
         raise ValueError("weight must be bf16 [H] on x's device")
     other = None if stream is None else _other_stream(stream, dev)
@@ -595,6 +602,7 @@ def paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale=None, stre
     dev = q.get_device()
     if dev < 0 or q.dtype is not b16:
         raise ValueError("q must be a CUDA bf16 [B,Hq,D] tensor")
+    _on_device(dev)
     q_stride, q_head, q_last = q.stride()
     if q_last != 1 or (q_head != D and Hq != 1):
         raise ValueError("the heads of a sequence's q must be contiguous")
@@ -650,6 +658,7 @@ def moe_ffn_decode(x, logits, W1, W3, W2, k, x_scale=None, W1_scale=None, W3_sca
     fp8 = dtype is torch.float8_e4m3fn
     if dev < 0 or not (fp8 or dtype is torch.bfloat16):
         raise ValueError("x must be a CUDA bf16 or float8_e4m3fn [T,H] tensor")
+    _on_device(dev)
     up = (E, H, F)
     if W1.shape != up or W3.shape != up or W2.shape != (E, F, H):
         raise ValueError("W1 and W3 must be [E,H,F] and W2 [E,F,H]")

@@ -101,3 +101,13 @@ def test_outputs_stay_while_the_current_stream_uses_them(case):
         other = torch.zeros(shape, dtype=torch.bfloat16, device="cuda")
     torch.cuda.synchronize()
     assert torch.equal(_bits(seen), _bits(want)) and other.shape == shape
+
+
+@pytest.mark.parametrize("case", [_norm, _attention, _ffn])
+def test_refuses_tensors_of_a_device_that_is_not_current(case, monkeypatch):
+    # the kernel would run on the current device, with the other's addresses
+    tensors, run = case()
+    run(tensors)
+    monkeypatch.setattr(mk, "_device", lambda: 1)
+    with pytest.raises(ValueError, match="current"):
+        run(tensors)
