@@ -307,8 +307,8 @@ size_t mk_workspace_size(int T, int H, int F, int E, int k, const mk_config_t* c
  * They can be captured in a CUDA graph.  Under capture the library's
  * workspace cache is not grown (MK_ERR_WORKSPACE): make a call of the same
  * sizes on that stream before.  A captured call keeps the workspace's address,
- * so while the graph lives give its stream no larger call, or capture with a
- * caller workspace. */
+ * so while the graph lives give its stream no larger call and replay no two
+ * graphs of one stream at a time, or capture with a caller workspace. */
 
 /* The residual's addition and the root-mean-square norm, in bf16 and / or in
  * 8 bits.  With z = x + residual (x alone when residual is NULL):
@@ -376,7 +376,8 @@ enum { MK_WEIGHT_BF16 = 0, MK_WEIGHT_E4M3 = 1 };
  *   h(t,j) = silu(x[t,:] . W1[e]) * (x[t,:] . W3[e])  for the j-th expert e,
  *   out[t,:] = sum_j gate[t,j] * (h(t,j) . W2[e]),  j in order.
  * With MK_WEIGHT_BF16, x and the weights are bf16 and the scale pointers
- * NULL; h is carried with 16 significant bits.  With MK_WEIGHT_E4M3 they are
+ * NULL; h is carried with 16 significant bits (infinite beyond the range of
+ * bf16).  With MK_WEIGHT_E4M3 they are
  * e4m3 with scales: a weight stands for its value times the scale of its
  * 128 x 128 block, x[t,c] for its value times x_scale[t, c/128] (what
  * mk_add_rmsnorm writes); h is rounded to e4m3 likewise, per row and 128

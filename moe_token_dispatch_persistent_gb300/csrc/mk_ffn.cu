@@ -682,8 +682,10 @@ __device__ __forceinline__ void complete_rows(const FfnParams& p, const Plan& pl
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const __nv_bfloat162 b = __floats2bfloat162_rn(h[2 * i], h[2 * i + 1]);
-                    const __nv_bfloat162 l =
-                        __floats2bfloat162_rn(h[2 * i] - __low2float(b), h[2 * i + 1] - __high2float(b));
+                    const float b0 = __low2float(b), b1 = __high2float(b);
+                    // nothing remains of an infinite value (inf - inf would be NaN)
+                    const __nv_bfloat162 l = __floats2bfloat162_rn(fabsf(b0) == INFINITY ? 0.f : h[2 * i] - b0,
+                                                                   fabsf(b1) == INFINITY ? 0.f : h[2 * i + 1] - b1);
                     hi[i] = *reinterpret_cast<const uint32_t*>(&b);
                     lo[i] = *reinterpret_cast<const uint32_t*>(&l);
                 }

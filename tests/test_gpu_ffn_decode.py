@@ -225,3 +225,13 @@ def test_offsets_past_32_bits():
         big[E - 4:] = w
     out = mk.moe_ffn_decode(small.x, logits.cuda(), W1, W3, W2, 3)["out"]
     assert torch.equal(out, small.run())
+
+
+def test_hidden_values_past_the_16_bit_range_are_infinite():
+    # h[:, 0] overflows for the first two tokens; the third's are zeros
+    layer = Layer(3, 128, 192, 1, 1, seed=13)
+    layer.x[:2], layer.x[2] = 1.0, 0.0
+    layer.W1[0, :, 0], layer.W3[0, :, 0] = 1e20, 1e20
+    layer.W2[0, 0, 5] = 0.25
+    out = layer.run().float()
+    assert torch.equal(out[:2], torch.sign(layer.W2[0, 0].float()).expand(2, -1) * INF) and torch.all(out[2] == 0)
