@@ -8,15 +8,17 @@
 // the cache's bytes bound it: 4*D bytes per token and key-value head against
 // 4*D operations per query head.
 //
-// Work.  A tile is 16 keys (32 with 64 columns a head) of one (sequence, group of up to 16 query heads
-// of one key-value head).  The tiles of all of them in a row are cut into one
-// equal range per CTA, and that into one per warp, whatever the lengths, so
-// every warp streams the same number of bytes and waits for no other.  The
-// caller's lengths stay on the device: every CTA builds the table of tiles
-// itself.  A warp writes the results of groups that lie whole in its range.
-// What it has of the others is joined in shared memory when the CTA's ranges
-// are done, and what a CTA has of groups that it shares with others by the
-// CTA that is done last, in the order of the keys.
+// Work.  A tile is 16 keys (32 with 64 columns a head) of one (sequence, group
+// of up to 16 query heads of one key-value head).  The tiles of all of them in
+// a row are cut into one equal range per CTA, and that into one per warp,
+// whatever the lengths, so every warp streams the same number of bytes and
+// waits for no other.  (With 256 columns a head two warps share a range, half
+// of the columns each, and add up their parts of the scores.)  The caller's
+// lengths stay on the device: every CTA builds the table of tiles itself.  A
+// warp writes the results of groups that lie whole in its range.  What it has
+// of the others is joined in shared memory when the CTA's ranges are done, and
+// what a CTA has of groups that it shares with others by the CTA that is done
+// last, in the order of the keys.
 //
 // Each warp has its own ring of tiles in shared memory, filled by its own
 // 16-byte asynchronous copies (any page size, any stride, keys past the end
@@ -26,8 +28,9 @@
 // of the time that the bytes do), so scores and weights stay in registers.
 //
 // Measured on GB300: four sequences of 131071 keys, 8 key-value heads of 128:
-// 317 us, 6.8 TB/s; 64 sequences of 0 to 16384 keys (449 MB) 82 us, of which 67
-// until the last keys are in; one of 8191 keys 13.9 us (latency).
+// 317 us, 6.8 TB/s; 13 of 47828 keys, 4 of 256: 360 to 372 us, 6.8 to 7.1
+// TB/s; 64 sequences of 0 to 16384 keys (449 MB) 82 us, of which 67 until the
+// last keys are in; one of 8191 keys 13.9 us (latency).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -54,24 +57,33 @@ constexpr float LN2 = 0.6931471805599453f;
 
 template <int D>
 struct Geo {
-    static constexpr int WARPS = D == 256 ? 4 : 8;
+    static constexpr int WARPS = 8;
+    // Warps that share a range, each with an equal part of the columns: one warp with
+    // all 256 leaves room for four rings, a warp per scheduler, and its own latencies
+    // bound it (13 sequences of 47828 keys, 4 heads of 256: 547 us, with two 360 to
+    // 372).  With 128 columns two warps gain nothing on long sequences (90 us either
+    // way) and lose on many short ones (222 of 0 to 1518 keys, 24 heads each: 76, 93).
+    static constexpr int SPLIT = D == 256 ? 2 : 1;
+    static constexpr int RANGES = WARPS / SPLIT;
+    static constexpr int COLS = D / SPLIT;            // columns of a warp
     static constexpr int STAGES = 2;
     static constexpr int KEYS = D == 64 ? 32 : 16;    // keys per tile
     static constexpr int THREADS = WARPS * 32;
-    static constexpr int CHUNKS = D / 8;              // 16-byte pieces of a row
-    static constexpr int HALF = KEYS * D * 2;         // one tile's keys (or values)
+    static constexpr int CHUNKS = COLS / 8;           // 16-byte pieces of a row's part
+    static constexpr int HALF = KEYS * COLS * 2;      // a warp's part of one tile's keys (or values)
     static constexpr int RING = STAGES * 2 * HALF;    // per warp
     static constexpr int OSTRIDE = D + 8;             // floats between rows of the join buffer: no bank conflicts
-    // A warp's result of its first group and of its last: O, m, l.  The last ones
+    // The result of a range's first group and of its last: O, m, l.  The last ones
     // lie where the rings were.
     static constexpr int PART = ROWS * OSTRIDE + 2 * ROWS;
     static constexpr int SM_HEADS = WARPS * RING;
-    static constexpr int SM_PREFIX = SM_HEADS + WARPS * PART * 4;
+    static constexpr int SM_PREFIX = SM_HEADS + RANGES * PART * 4;
     static constexpr int SM_SMALL = SM_PREFIX + (ATTN_MAX_B + 1) * 4 + 12;
-    static constexpr int SMEM = SM_SMALL + 1024;
-    static_assert(WARPS * PART * 4 <= SM_HEADS, "the last results lie where the rings were");
+    static constexpr int SM_SCORES = SM_SMALL + 128;  // partial scores of warps that share a range, twice
+    static constexpr int SMEM = SM_SCORES + (SPLIT > 1 ? 2 * WARPS * (KEYS / 8) * 512 : 0);
+    static_assert(RANGES * PART * 4 <= SM_HEADS, "the last results lie where the rings were");
     static constexpr int SLOT = 2 * ROWS + ROWS * D;  // floats of a partial result: m, l, O
-    static_assert(SMEM <= 232448, "dynamic shared memory of one CTA on sm_103");
+    static_assert(SMEM + 2 * RANGES * 24 <= 232448, "shared memory of one CTA on sm_103");
 };
 
 constexpr size_t ATTN_SLOT_BYTES = size_t(Geo<256>::SLOT) * 4;
@@ -227,22 +239,22 @@ __device__ __forceinline__ int64_t key_offset(const AttnParams& p, int b, int kv
     return page * p.page_stride + (key - slot * p.page_size) * p.token_stride + kv * p.head_stride;
 }
 
-// A warp's result of a group: O, m, l.
+// A warp's result of a group: its columns of O, m, l.
 template <int D>
-__device__ __forceinline__ void put_partial(float* part, int heads, const float (&o)[D / 8][4], float m0, float m1,
-                                            float l0, float l1) {
+__device__ __forceinline__ void put_partial(float* part, int heads, int side, const float (&o)[Geo<D>::COLS / 8][4],
+                                            float m0, float m1, float l0, float l1) {
     constexpr int stride = Geo<D>::OSTRIDE;
     const int lane = threadIdx.x & 31, r0 = lane >> 2, r1 = r0 + 8;
     float* sm = part + ROWS * stride;
-    if ((lane & 3) == 0) {
+    if (side == 0 && (lane & 3) == 0) {
         sm[r0] = m0;
         sm[r1] = m1;
         sm[ROWS + r0] = l0;
         sm[ROWS + r1] = l1;
     }
-    float* ow = part + (lane & 3) * 2;
+    float* ow = part + side * Geo<D>::COLS + (lane & 3) * 2;
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n) {
+    for (int n = 0; n < Geo<D>::COLS / 8; ++n) {
         if (r0 < heads) *reinterpret_cast<float2*>(ow + r0 * stride + n * 8) = make_float2(o[n][0], o[n][1]);
         if (r1 < heads) *reinterpret_cast<float2*>(ow + r1 * stride + n * 8) = make_float2(o[n][2], o[n][3]);
     }
@@ -385,17 +397,19 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
     }
 
     const uint32_t total = prefix[p.B] * groups;
-    // At least a position per warp, and one more for every four heads of a group
+    // At least a position per range, and one more for every four heads of a group
     // beyond the first four: a shorter range only adds partial results to join
     // (10 sequences, 16 heads, up to 12043 keys: 34 us with one position, 21 with
     // four; 16 sequences of one head a group: 12 us with one, 16 with four).
-    const uint32_t least = uint32_t(G::WARPS * max(1, min(ROWS, p.per_kv) / 4));
+    const uint32_t least = uint32_t(G::RANGES * max(1, min(ROWS, p.per_kv) / 4));
     const uint32_t nctas = min(gridDim.x, (total + least - 1) / least);
     if (blockIdx.x >= nctas) return;
     const Cut cut_at(total, nctas);
     const uint32_t start = cut_at.start(blockIdx.x), end = cut_at.start(blockIdx.x + 1);
-    const Cut warp_cut(end - start, G::WARPS);
-    const uint32_t wstart = start + warp_cut.start(warp), wend = start + warp_cut.start(warp + 1);
+    const int range = warp / G::SPLIT, side = warp % G::SPLIT;  // this warp's range, and its part of the columns
+    const Cut warp_cut(end - start, G::RANGES);
+    const uint32_t wstart = start + warp_cut.start(range), wend = start + warp_cut.start(range + 1);
+    const __nv_bfloat16 *my_q = p.q + side * G::COLS, *my_k = p.k + side * G::COLS, *my_v = p.v + side * G::COLS;
 
     // ---- this warp's ring: loads run STAGES tiles ahead, across groups
     const uint32_t ring = smem_u32(smem) + uint32_t(warp) * G::RING;
@@ -421,9 +435,9 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
             // the group's queries head for L1 while its first tiles do for shared memory
             const int head = lr.g / p.chunks * p.per_kv + lr.g % p.chunks * ROWS + (lane & (ROWS - 1));
             if (lane < ROWS && head < (lr.g / p.chunks + 1) * p.per_kv) {
-                const char* q = reinterpret_cast<const char*>(p.q + int64_t(lr.b) * p.q_stride + int64_t(head) * D);
+                const char* q = reinterpret_cast<const char*>(my_q + int64_t(lr.b) * p.q_stride + int64_t(head) * D);
 #pragma unroll
-                for (int i = 0; i < D * 2; i += 128) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + i));
+                for (int i = 0; i < G::COLS * 2; i += 128) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + i));
             }
         }
         o = key_offset<G::KEYS>(p, lr.b, lr.g / p.chunks, load_tile, lane, load_len);
@@ -442,9 +456,9 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
                 const int64_t ro = __shfl_sync(0xffffffffu, off[0], row);
                 const bool ok = ro >= 0;
                 const int64_t at = (ok ? ro : 0) + c * 8;
-                const uint32_t d = dst + uint32_t(row * D * 2 + ((c ^ (row & 7)) << 4));
-                copy16(d, p.k + at, ok);
-                copy16(d + G::HALF, p.v + at, ok);
+                const uint32_t d = dst + uint32_t(row * G::COLS * 2 + ((c ^ (row & 7)) << 4));
+                copy16(d, my_k + at, ok);
+                copy16(d + G::HALF, my_v + at, ok);
             }
         }
         copy_commit();
@@ -457,27 +471,27 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
     for (int i = 0; i < G::STAGES; ++i) issue();
 
     const int r0 = lane >> 2, r1 = r0 + 8;  // this lane's rows (heads) of the products
-    uint32_t slot = 0;
+    uint32_t slot = 0, turn = 0;
     Walk walk{wstart, wend, prefix, p.B, groups, false};
     Range r;
-    // A group that the warp does not hold whole is its first (set aside in shared
+    // A group that the range does not hold whole is its first (set aside in shared
     // memory) or its last (kept in registers until the rings are free).
     Range head, tail;
     bool has_head = false, has_tail = false;
-    float o[D / 8][4];
+    float o[G::COLS / 8][4];
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     while (walk.next(r)) {
         const int kv = r.g / p.chunks, head0 = kv * p.per_kv + (r.g % p.chunks) * ROWS;
         const int heads = min(ROWS, (kv + 1) * p.per_kv - head0);
         const int len = length(r.b);
         // query rows as A fragments
-        uint32_t qa[D / 16][4];
+        uint32_t qa[G::COLS / 16][4];
         {
-            const __nv_bfloat16* qb = p.q + int64_t(r.b) * p.q_stride + int64_t(head0) * D + (lane & 3) * 2;
+            const __nv_bfloat16* qb = my_q + int64_t(r.b) * p.q_stride + int64_t(head0) * D + (lane & 3) * 2;
             const uint32_t* q0 = reinterpret_cast<const uint32_t*>(qb + int64_t(r0 < heads ? r0 : 0) * D);
             const uint32_t* q1 = reinterpret_cast<const uint32_t*>(qb + int64_t(r1 < heads ? r1 : 0) * D);
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
+            for (int kk = 0; kk < G::COLS / 16; ++kk) {
                 qa[kk][0] = r0 < heads ? q0[kk * 8] : 0u;
                 qa[kk][1] = r1 < heads ? q1[kk * 8] : 0u;
                 qa[kk][2] = r0 < heads ? q0[kk * 8 + 4] : 0u;
@@ -485,7 +499,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
             }
         }
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n)
+        for (int n = 0; n < G::COLS / 8; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) o[n][i] = 0.f;
         m0 = m1 = -INFINITY;
@@ -500,17 +514,35 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
             float s[NT][4] = {};
             {
                 const int row = ((lane >> 4) << 3) + (lane & 7), half = (lane >> 3) & 1;
-                const uint32_t rb = ks + uint32_t(row * D * 2);
+                const uint32_t rb = ks + uint32_t(row * G::COLS * 2);
 #pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
+                for (int kk = 0; kk < G::COLS / 16; ++kk) {
 #pragma unroll
                     for (int n = 0; n < NT; n += 2) {
                         uint32_t kb[4];
-                        ldsm4(rb + n * 8 * D * 2 + (uint32_t((kk * 2 + half) ^ (row & 7)) << 4), kb);
+                        ldsm4(rb + n * 8 * G::COLS * 2 + (uint32_t((kk * 2 + half) ^ (row & 7)) << 4), kb);
                         mma16816(s[n], qa[kk], kb[0], kb[1]);
                         mma16816(s[n + 1], qa[kk], kb[2], kb[3]);
                     }
                 }
+            }
+            if constexpr (G::SPLIT == 2) {
+                // the other warp's columns: both add the same two sums, and have all else alike
+                static_assert(G::RANGES <= 15, "one named barrier each");
+                float4* at = reinterpret_cast<float4*>(smem + G::SM_SCORES) + turn * (G::WARPS * NT * 32) + lane;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    at[(warp * NT + n) * 32] = make_float4(s[n][0], s[n][1], s[n][2], s[n][3]);
+                asm volatile("bar.sync %0, 64;" ::"r"(1 + range) : "memory");
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    const float4 u = at[((warp ^ 1) * NT + n) * 32];
+                    s[n][0] += u.x;
+                    s[n][1] += u.y;
+                    s[n][2] += u.z;
+                    s[n][3] += u.w;
+                }
+                turn ^= 1u;  // the next tile's go beside these: one barrier a tile
             }
             const int key = int(t) * G::KEYS + (lane & 3) * 2;
             const bool cut = int(t + 1) * G::KEYS > len;
@@ -539,7 +571,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
                 l0 *= f0;
                 l1 *= f1;
 #pragma unroll
-                for (int n = 0; n < D / 8; ++n) {
+                for (int n = 0; n < G::COLS / 8; ++n) {
                     o[n][0] *= f0;
                     o[n][1] *= f0;
                     o[n][2] *= f1;
@@ -567,9 +599,9 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
                                               p3 - __uint_as_float(hi[2 * n + 1] & 0xffff0000u));
                 }
                 const int row = kk * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), half = lane >> 4;
-                const uint32_t rb = vs + uint32_t(row * D * 2);
+                const uint32_t rb = vs + uint32_t(row * G::COLS * 2);
 #pragma unroll
-                for (int n = 0; n < D / 16; ++n) {
+                for (int n = 0; n < G::COLS / 16; ++n) {
                     uint32_t vb[4];
                     ldsm4_t(rb + (uint32_t((n * 2 + half) ^ (row & 7)) << 4), vb);
                     mma16816(o[2 * n], hi, vb[0], vb[1]);
@@ -591,21 +623,21 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
             // the whole group: straight to the output
             const float i0 = l0 == 0.f ? 0.f : 1.f / l0, i1 = l1 == 0.f ? 0.f : 1.f / l1;
             const int64_t at = int64_t(r.b) * p.Hq + head0;
-            uint32_t* w0 = reinterpret_cast<uint32_t*>(p.out + (at + r0) * D) + (lane & 3);
-            uint32_t* w1 = reinterpret_cast<uint32_t*>(p.out + (at + r1) * D) + (lane & 3);
+            uint32_t* w0 = reinterpret_cast<uint32_t*>(p.out + (at + r0) * D + side * G::COLS) + (lane & 3);
+            uint32_t* w1 = reinterpret_cast<uint32_t*>(p.out + (at + r1) * D + side * G::COLS) + (lane & 3);
 #pragma unroll
-            for (int n = 0; n < D / 8; ++n) {
+            for (int n = 0; n < G::COLS / 8; ++n) {
                 if (r0 < heads) w0[n * 4] = pack_bf16(o[n][0] * i0, o[n][1] * i0);
                 if (r1 < heads) w1[n * 4] = pack_bf16(o[n][2] * i1, o[n][3] * i1);
             }
-            if (p.lse && (lane & 3) == 0) {
+            if (p.lse && side == 0 && (lane & 3) == 0) {
                 if (r0 < heads) p.lse[at + r0] = l0 == 0.f ? -INFINITY : (m0 + log2f(l0)) * LN2;
                 if (r1 < heads) p.lse[at + r1] = l1 == 0.f ? -INFINITY : (m1 + log2f(l1)) * LN2;
             }
         } else if (walk.pos < walk.end) {
             head = r;
             has_head = true;
-            put_partial<D>(reinterpret_cast<float*>(smem + G::SM_HEADS) + warp * G::PART, heads, o, m0, m1, l0, l1);
+            put_partial<D>(reinterpret_cast<float*>(smem + G::SM_HEADS) + range * G::PART, heads, side, o, m0, m1, l0, l1);
         } else {
             tail = r;
             has_tail = true;
@@ -613,32 +645,32 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
     }
     copy_wait<0>();
 
-    // ---- join what the CTA's warps have of the same groups
-    __shared__ Range pieces[2 * G::WARPS];  // in the order of positions; tiles 0: none
+    // ---- join what the CTA's ranges have of the same groups
+    __shared__ Range pieces[2 * G::RANGES];  // in the order of positions; tiles 0: none
     __syncthreads();  // the rings are free
-    if (lane == 0) {
+    if (side == 0 && lane == 0) {
         head.tiles = has_head ? head.tiles : 0u;
         tail.tiles = has_tail ? tail.tiles : 0u;
-        pieces[2 * warp] = head;
-        pieces[2 * warp + 1] = tail;
+        pieces[2 * range] = head;
+        pieces[2 * range + 1] = tail;
     }
     float* tails = reinterpret_cast<float*>(smem);
     const float* firsts = reinterpret_cast<const float*>(smem + G::SM_HEADS);
     if (has_tail) {
         const int kv = tail.g / p.chunks, head0 = kv * p.per_kv + (tail.g % p.chunks) * ROWS;
-        put_partial<D>(tails + warp * G::PART, min(ROWS, (kv + 1) * p.per_kv - head0), o, m0, m1, l0, l1);
+        put_partial<D>(tails + range * G::PART, min(ROWS, (kv + 1) * p.per_kv - head0), side, o, m0, m1, l0, l1);
     }
     __syncthreads();
     Range open[2];  // groups shared with other CTAs: the first and the last one's
     int nopen = 0;
     uint32_t left = 0;  // pieces not joined yet, a bit each
 #pragma unroll
-    for (int i = 0; i < 2 * G::WARPS; ++i) left |= pieces[i].tiles != 0 ? 1u << i : 0u;
+    for (int i = 0; i < 2 * G::RANGES; ++i) left |= pieces[i].tiles != 0 ? 1u << i : 0u;
     while (left) {
         const Range q = pieces[__ffs(int(left)) - 1];
         uint32_t same = 0;  // those of the first one's group
 #pragma unroll
-        for (int i = 0; i < 2 * G::WARPS; ++i)
+        for (int i = 0; i < 2 * G::RANGES; ++i)
             if ((left >> i & 1u) && pieces[i].begin == q.begin) same |= 1u << i;
         left &= ~same;
         const int kv = q.g / p.chunks, head0 = kv * p.per_kv + (q.g % p.chunks) * ROWS;
