@@ -52,6 +52,7 @@
 #include "mk_common.h"
 #include "mk_host.h"
 #include "mk_ptx.cuh"
+#include "mk_quant.cuh"
 #include "mk_wait.cuh"
 
 namespace mk {
@@ -102,8 +103,6 @@ constexpr size_t PIECE_FLOATS = size_t(8) << 20;
 constexpr int INFO_SLOTS = 8;
 constexpr int JOBS = 2;  // blocks of h handed to the completing warps
 constexpr long long FFN_SPIN_NS = 2000000000LL;
-constexpr float E4M3_TOP = 448.f;
-constexpr float TINY = 7.888609052210118e-31f;  // 2^-100
 
 struct FfnCtl {
     uint32_t routed;  // CTAs whose tokens are routed
@@ -246,12 +245,6 @@ __device__ __forceinline__ uint8_t* ffn_ring() {
 }
 
 __device__ __forceinline__ int pad16(int n) { return (n + 15) & ~15; }
-
-__device__ __forceinline__ float nan_max(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
 
 // ------------------------------------------------------------- routing -----
 
@@ -664,18 +657,18 @@ __device__ __forceinline__ void complete_rows(const FfnParams& p, const Plan& pl
                 // 16 lanes hold a group of 128 columns
                 float top = 0.f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) top = nan_max(top, fabsf(h[i]));
+                for (int i = 0; i < 8; ++i) top = max_nan(top, fabsf(h[i]));
 #pragma unroll
-                for (int d = 8; d > 0; d >>= 1) top = nan_max(top, __shfl_xor_sync(0xffffffffu, top, d));
-                const float scale = top < TINY ? 1.f : top / E4M3_TOP, inv = 1.f / scale;
+                for (int d = 8; d > 0; d >>= 1) top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, d));
+                const GroupScale scale(top);
                 uint32_t q[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    q[i] = __nv_cvt_float2_to_fp8x2(make_float2(h[2 * i] * inv, h[2 * i + 1] * inv), __NV_SATFINITE,
+                    q[i] = __nv_cvt_float2_to_fp8x2(make_float2(scale.of(h[2 * i]), scale.of(h[2 * i + 1])), __NV_SATFINITE,
                                                     __NV_E4M3);
                 if (in) {
                     *reinterpret_cast<uint2*>(p.h + at) = make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16);
-                    if ((lane & 15) == 0) p.h_scale[size_t(row) * (p.F / GROUP8) + 2 * s.blk + (lane >> 4)] = scale;
+                    if ((lane & 15) == 0) p.h_scale[size_t(row) * (p.F / GROUP8) + 2 * s.blk + (lane >> 4)] = scale.scale;
                 }
             } else if (in) {
                 uint32_t hi[4], lo[4];

@@ -20,6 +20,7 @@
 
 #include "mk.h"
 #include "mk_host.h"
+#include "mk_quant.cuh"
 
 namespace mk {
 namespace {
@@ -28,8 +29,6 @@ constexpr int NORM_CHUNK = 256;  // columns of a row that one warp takes at a ti
 constexpr int NORM_GROUP = 128;  // columns per scale
 constexpr int NORM_MAX_H = 32768;
 constexpr int NORM_MAX_WARPS = 32;
-constexpr float E4M3_MAX = 448.f;
-constexpr float TINY_GROUP = 7.888609052210118e-31f;  // 2^-100
 
 struct NormParams {
     const __nv_bfloat16* x;
@@ -44,14 +43,6 @@ struct NormParams {
     int warps_per_row, rows_per_cta;
     float eps;
 };
-
-// The larger of the two, NaN if either is (fmaxf would drop it, and with it a
-// row that holds NaN would get a finite scale).
-__device__ __forceinline__ float max_nan(float a, float b) {
-    float r;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-    return r;
-}
 
 // Column of element i of a lane's eight in a chunk.  VEC: eight neighbours
 // (16-byte accesses), so lanes 0-15 hold the chunk's first group of 128 and
@@ -129,29 +120,24 @@ __device__ __forceinline__ void quantize8(uint8_t* row, float* scale_row, int ch
             a[g] = m;
         }
     }
-    float s[2], inv[2];
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-        s[g] = a[g] < TINY_GROUP ? 1.f : a[g] / E4M3_MAX;
-        inv[g] = 1.f / s[g];
-    }
+    const GroupScale s[2] = {GroupScale(a[0]), GroupScale(a[1])};
     const int group = chunk * 2 + (VEC ? lane >> 4 : lane & 1);
     if (VEC ? (lane & 15) == 0 : lane < 2)
-        if (group * NORM_GROUP < H) scale_row[group] = (!VEC && (lane & 1)) ? s[1] : s[0];
-    uint32_t q[8];
+        if (group * NORM_GROUP < H) scale_row[group] = (!VEC && (lane & 1)) ? s[1].scale : s[0].scale;
+    uint32_t q[4];  // two values each
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        q[i] = __nv_cvt_float_to_fp8(y[i] * inv[VEC ? 0 : i >> 2], __NV_SATFINITE, __NV_E4M3);
+    for (int i = 0; i < 4; ++i) {
+        const GroupScale& g = s[VEC ? 0 : i >> 1];
+        q[i] = __nv_cvt_float2_to_fp8x2(make_float2(g.of(y[2 * i]), g.of(y[2 * i + 1])), __NV_SATFINITE, __NV_E4M3);
+    }
     if constexpr (VEC) {
         const int c = column<true>(chunk, lane, 0);
-        if (c < H)
-            __stcs(reinterpret_cast<uint2*>(row + c), make_uint2(q[0] | q[1] << 8 | q[2] << 16 | q[3] << 24,
-                                                                 q[4] | q[5] << 8 | q[6] << 16 | q[7] << 24));
+        if (c < H) __stcs(reinterpret_cast<uint2*>(row + c), make_uint2(q[0] | q[1] << 16, q[2] | q[3] << 16));
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int c = column<false>(chunk, lane, i);
-            if (c < H) row[c] = uint8_t(q[i]);
+            if (c < H) row[c] = uint8_t(q[i >> 1] >> (8 * (i & 1)));
         }
     }
 }

@@ -176,3 +176,26 @@ def test_offsets_past_32_bits():
     for name in o:
         assert torch.equal(o[name][-5:].view(torch.uint8), want[name].view(torch.uint8)), name
     assert torch.all(o["out"][:-5:4096] == 0)
+
+
+@pytest.mark.parametrize("H", [32768, 32767])  # 16-byte accesses, and single elements
+def test_8_bit_values_are_of_the_quotient(H):
+    # x = +-1 and eps = 0 make y the weights themselves, so the stored scale and
+    # e4m3(y / scale) are known: every significand of a group's largest value
+    # against every significand, in four binades
+    m = 1 + torch.arange(128, dtype=torch.float64) / 128
+    w = m[:, None].repeat(1, 128).repeat_interleave(4, 0)  # 512 groups: the largest value, and
+    for i in range(4):
+        w[i::4, 1:] = m[1:] * 2.0 ** (-1 - i)              # the others below it
+    x = torch.ones((3, H)).bfloat16()
+    x[1] = -1
+    for half in (w[:256], w[256:]):
+        weight = half.reshape(-1)[:H].bfloat16().cuda()
+        o = mk.add_rmsnorm(x.cuda(), weight, eps=0.0, e4m3=True)
+        assert torch.equal(o["out"].cpu(), x * weight.cpu())
+        y = torch.zeros(32768)
+        y[:H] = weight.float().cpu()
+        scale = y.view(256, 128).amax(1) / 448
+        want = (y.view(256, 128) / scale[:, None]).to(torch.float8_e4m3fn).float().view(-1)[:H]
+        assert torch.equal(o["scale"].cpu(), scale.expand(3, -1))
+        assert torch.equal(o["out8"].float().cpu(), want * x.float())
