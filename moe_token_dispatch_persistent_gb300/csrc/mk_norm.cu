@@ -155,6 +155,10 @@ __global__ void __launch_bounds__(NORM_MAX_WARPS * 32) mk_add_rmsnorm_kernel(con
     const int mine = warp % wpr, first = warp - mine;
     const int H = p.H, groups = (H + NORM_GROUP - 1) / NORM_GROUP;
     const int64_t stride = int64_t(gridDim.x) * p.rows_per_cta;
+    // Whether a thread has registers for the next row and the weights.  If not, a
+    // row is loaded in its own turn and the weights come from L1 (with spills instead:
+    // 2048 x 32768 154 us, so 107; 8192 x 7167 242, so 144; 2048 x 32767 650, so 301).
+    constexpr bool AHEAD = C <= (VEC ? 2 : 1);
     uint4 x[C], r[C], w[C];
     auto fetch = [&](int64_t row) {
         if (row >= p.T) return;
@@ -165,15 +169,18 @@ __global__ void __launch_bounds__(NORM_MAX_WARPS * 32) mk_add_rmsnorm_kernel(con
             for (int j = 0; j < C; ++j) r[j] = load8<VEC>(p.residual + row * p.residual_stride, mine + j * wpr, lane, H);
     };
     int64_t base = int64_t(blockIdx.x) * p.rows_per_cta;
-    fetch(base + warp / wpr);
+    if (AHEAD) {
+        fetch(base + warp / wpr);
 #pragma unroll
-    for (int j = 0; j < C; ++j) w[j] = load8<VEC>(p.weight, mine + j * wpr, lane, H);
+        for (int j = 0; j < C; ++j) w[j] = load8<VEC>(p.weight, mine + j * wpr, lane, H);
+    }
     for (int turn = 0; base < p.T; base += stride, turn ^= 1) {
         const int64_t row = base + warp / wpr;
         const bool live = row < p.T;
         float z[C][8];
         float sum = 0.f;
         if (live) {
+            if (!AHEAD) fetch(row);
 #pragma unroll
             for (int j = 0; j < C; ++j)
 #pragma unroll
@@ -182,7 +189,7 @@ __global__ void __launch_bounds__(NORM_MAX_WARPS * 32) mk_add_rmsnorm_kernel(con
                     if (p.residual) z[j][i] += element(r[j], i);
                     sum = fmaf(z[j][i], z[j][i], sum);
                 }
-            fetch(row + stride);
+            if (AHEAD) fetch(row + stride);
             if (p.residual_out)
 #pragma unroll
                 for (int j = 0; j < C; ++j) store8<VEC>(p.residual_out + row * H, mine + j * wpr, lane, H, z[j]);
@@ -200,6 +207,7 @@ __global__ void __launch_bounds__(NORM_MAX_WARPS * 32) mk_add_rmsnorm_kernel(con
         const float rstd = rsqrtf(sum / float(H) + p.eps);
 #pragma unroll
         for (int j = 0; j < C; ++j) {
+            if (!AHEAD) w[j] = load8<VEC>(p.weight, mine + j * wpr, lane, H);
 #pragma unroll
             for (int i = 0; i < 8; ++i) z[j][i] = z[j][i] * rstd * element(w[j], i);
             if (p.out) store8<VEC>(p.out + row * H, mine + j * wpr, lane, H, z[j]);
