@@ -9,16 +9,17 @@
 // 4*D operations per query head.
 //
 // Work.  A tile is 16 keys (32 with 64 columns a head) of one (sequence, group
-// of up to 16 query heads of one key-value head).  The tiles of all of them in
-// a row are cut into one equal range per CTA, and that into one per warp,
-// whatever the lengths, so every warp streams the same number of bytes and
-// waits for no other.  (With 256 columns a head two warps share a range, half
-// of the columns each, and add up their parts of the scores.)  The caller's
-// lengths stay on the device: every CTA builds the table of tiles itself.  A
-// warp writes the results of groups that lie whole in its range.  What it has
-// of the others is joined in shared memory when the CTA's ranges are done, and
-// what a CTA has of groups that it shares with others by the CTA that is done
-// last, in the order of the keys.
+// of up to 16 or 32 query heads of one key-value head).  The tiles of all of
+// them in a row are cut into one equal range per CTA, and that into one per
+// warp, whatever the lengths, so every warp streams the same number of bytes
+// and waits for no other.  Two warps share a range with 256 columns a head
+// (half of the columns each, and they add up their parts of the scores) and in
+// groups of 32 heads (16 each, and a ring of tiles).  The caller's lengths stay
+// on the device: every CTA builds the table of tiles itself.  A warp writes the
+// results of groups that lie whole in its range.  What it has of the others is
+// joined in shared memory when the CTA's ranges are done, and what a CTA has of
+// groups that it shares with others by the CTA that is done last, in the order
+// of the keys.
 //
 // Each warp has its own ring of tiles in shared memory, filled by its own
 // 16-byte asynchronous copies (any page size, any stride, keys past the end
@@ -45,7 +46,7 @@
 namespace mk {
 namespace {
 
-constexpr int ROWS = 16;          // query heads per group (rows of the product)
+constexpr int ROWS = 16;          // query heads per warp (rows of the product)
 // A group counts as this many tiles more than it has: its queries, its first
 // tile's latency and its result cost about that, and short groups would
 // otherwise gather in a few warps.
@@ -55,38 +56,43 @@ constexpr int ATTN_MAX_CTAS = 160;
 constexpr float LOG2E = 1.4426950408889634f;
 constexpr float LN2 = 0.6931471805599453f;
 
-template <int D>
+// D columns a head, groups of R * 16 query heads.
+template <int D, int R>
 struct Geo {
     static constexpr int WARPS = 8;
+    static constexpr int GROUP = R * ROWS;
     // Warps that share a range, each with an equal part of the columns: one warp with
     // all 256 leaves room for four rings, a warp per scheduler, and its own latencies
     // bound it (13 sequences of 47828 keys, 4 heads of 256: 547 us, with two 360 to
     // 372).  With 128 columns two warps gain nothing on long sequences (90 us either
     // way) and lose on many short ones (222 of 0 to 1518 keys, 24 heads each: 76, 93).
     static constexpr int SPLIT = D == 256 ? 2 : 1;
-    static constexpr int RANGES = WARPS / SPLIT;
+    // Warps that share a range: with R = 2 a ring of tiles too, with 16 heads each.
+    static constexpr int MATES = SPLIT * R;
+    static_assert(MATES <= 2, "they meet in pairs");
+    static constexpr int RANGES = WARPS / MATES;
     static constexpr int COLS = D / SPLIT;            // columns of a warp
-    static constexpr int STAGES = 2;
+    static constexpr int STAGES = 2 * R;
     static constexpr int KEYS = D == 64 ? 32 : 16;    // keys per tile
     static constexpr int THREADS = WARPS * 32;
     static constexpr int CHUNKS = COLS / 8;           // 16-byte pieces of a row's part
     static constexpr int HALF = KEYS * COLS * 2;      // a warp's part of one tile's keys (or values)
-    static constexpr int RING = STAGES * 2 * HALF;    // per warp
+    static constexpr int RING = STAGES * 2 * HALF;    // of R warps
     static constexpr int OSTRIDE = D + 8;             // floats between rows of the join buffer: no bank conflicts
     // The result of a range's first group and of its last: O, m, l.  The last ones
     // lie where the rings were.
-    static constexpr int PART = ROWS * OSTRIDE + 2 * ROWS;
-    static constexpr int SM_HEADS = WARPS * RING;
+    static constexpr int PART = GROUP * OSTRIDE + 2 * GROUP;
+    static constexpr int SM_HEADS = WARPS / R * RING;
     static constexpr int SM_PREFIX = SM_HEADS + RANGES * PART * 4;
     static constexpr int SM_SMALL = SM_PREFIX + (ATTN_MAX_B + 1) * 4 + 12;
     static constexpr int SM_SCORES = SM_SMALL + 128;  // partial scores of warps that share a range, twice
     static constexpr int SMEM = SM_SCORES + (SPLIT > 1 ? 2 * WARPS * (KEYS / 8) * 512 : 0);
     static_assert(RANGES * PART * 4 <= SM_HEADS, "the last results lie where the rings were");
-    static constexpr int SLOT = 2 * ROWS + ROWS * D;  // floats of a partial result: m, l, O
+    static constexpr int SLOT = 2 * GROUP + GROUP * D;  // floats of a partial result: m, l, O
     static_assert(SMEM + 2 * RANGES * 24 <= 232448, "shared memory of one CTA on sm_103");
 };
 
-constexpr size_t ATTN_SLOT_BYTES = size_t(Geo<256>::SLOT) * 4;
+constexpr size_t ATTN_SLOT_BYTES = size_t(std::max(Geo<256, 1>::SLOT, Geo<128, 2>::SLOT)) * 4;
 constexpr size_t ATTN_SLOTS_BYTES = 2 * ATTN_MAX_CTAS * ATTN_SLOT_BYTES;  // fixed, so the counters never move
 
 struct AttnParams {
@@ -115,6 +121,9 @@ __device__ __forceinline__ void attn_error(DevError* e, uint32_t site, uint32_t 
         e->info = info;
     }
 }
+
+// The two warps of a range meet, and see what each has written and copied.
+__device__ __forceinline__ void pair_sync(int range) { asm volatile("bar.sync %0, 64;" ::"r"(1 + range) : "memory"); }
 
 // 16 bytes global -> shared; zeros when !ok (the source is then not read).
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
@@ -240,21 +249,21 @@ __device__ __forceinline__ int64_t key_offset(const AttnParams& p, int b, int kv
 }
 
 // A warp's result of a group: its columns of O, m, l.
-template <int D>
-__device__ __forceinline__ void put_partial(float* part, int heads, int side, const float (&o)[Geo<D>::COLS / 8][4],
+template <typename G>
+__device__ __forceinline__ void put_partial(float* part, int heads, int row0, int side, const float (&o)[G::COLS / 8][4],
                                             float m0, float m1, float l0, float l1) {
-    constexpr int stride = Geo<D>::OSTRIDE;
+    constexpr int stride = G::OSTRIDE;
     const int lane = threadIdx.x & 31, r0 = lane >> 2, r1 = r0 + 8;
-    float* sm = part + ROWS * stride;
+    float* sm = part + G::GROUP * stride + row0;
     if (side == 0 && (lane & 3) == 0) {
         sm[r0] = m0;
         sm[r1] = m1;
-        sm[ROWS + r0] = l0;
-        sm[ROWS + r1] = l1;
+        sm[G::GROUP + r0] = l0;
+        sm[G::GROUP + r1] = l1;
     }
-    float* ow = part + side * Geo<D>::COLS + (lane & 3) * 2;
+    float* ow = part + row0 * stride + side * G::COLS + (lane & 3) * 2;
 #pragma unroll
-    for (int n = 0; n < Geo<D>::COLS / 8; ++n) {
+    for (int n = 0; n < G::COLS / 8; ++n) {
         if (r0 < heads) *reinterpret_cast<float2*>(ow + r0 * stride + n * 8) = make_float2(o[n][0], o[n][1]);
         if (r1 < heads) *reinterpret_cast<float2*>(ow + r1 * stride + n * 8) = make_float2(o[n][2], o[n][3]);
     }
@@ -266,10 +275,10 @@ struct Part {
     float m = -INFINITY, l = 0.f;
     float4 o = {0.f, 0.f, 0.f, 0.f};
 
-    __device__ void load(const float* slot, int row, int c, int D) {
+    __device__ void load(const float* slot, int group, int row, int c, int D) {
         m = __ldcg(slot + row);
-        l = __ldcg(slot + ROWS + row);
-        o = __ldcg(reinterpret_cast<const float4*>(slot + 2 * ROWS + row * D + c));
+        l = __ldcg(slot + group + row);
+        o = __ldcg(reinterpret_cast<const float4*>(slot + 2 * group + row * D + c));
     }
     template <int N>
     __device__ void add(const Part (&u)[N]) {
@@ -303,12 +312,12 @@ struct Part {
 // The result of a group from the partial results of CTAs [c0, c0 + n), by a
 // whole CTA.  A thread takes four columns of one head and, where there are more threads than
 // that, every parts-th piece; the parts are joined in shared memory.
-template <int D>
+template <int D, int R>
 __device__ void join_group(const AttnParams& p, const Range& r, uint32_t c0, int n, uint32_t which0, float* smem_f) {
-    using G = Geo<D>;
+    using G = Geo<D, R>;
     const int tid = threadIdx.x;
-    const int kv = r.g / p.chunks, head0 = kv * p.per_kv + (r.g % p.chunks) * ROWS;
-    const int heads = min(ROWS, (kv + 1) * p.per_kv - head0);
+    const int kv = r.g / p.chunks, head0 = kv * p.per_kv + (r.g % p.chunks) * G::GROUP;
+    const int heads = min(G::GROUP, (kv + 1) * p.per_kv - head0);
     const int items = heads * (D / 4), parts = min(n, max(1, G::THREADS / items));
     Part* red = reinterpret_cast<Part*>(smem_f);
     // the first CTA's piece may lie in its second slot; the others' ranges start in the group
@@ -326,7 +335,7 @@ __device__ void join_group(const AttnParams& p, const Range& r, uint32_t c0, int
 #pragma unroll
                 for (int x = 0; x < BATCH; ++x) {
                     const int at = i + x * parts;
-                    if (at < n) u[x].load(at == 0 ? first : other + size_t(2 * at) * (ATTN_SLOT_BYTES / 4), row, c, D);
+                    if (at < n) u[x].load(at == 0 ? first : other + size_t(2 * at) * (ATTN_SLOT_BYTES / 4), G::GROUP, row, c, D);
                 }
                 acc.add(u);
             }
@@ -345,9 +354,9 @@ __device__ void join_group(const AttnParams& p, const Range& r, uint32_t c0, int
     __syncthreads();  // the buffer is free for another group
 }
 
-template <int D>
-__global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(const AttnParams p) {
-    using G = Geo<D>;
+template <int D, int R>
+__global__ void __launch_bounds__(Geo<D, R>::THREADS, 1) mk_paged_attention_kernel(const AttnParams p) {
+    using G = Geo<D, R>;
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + G::SM_PREFIX);
@@ -397,7 +406,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
     }
 
     const uint32_t total = prefix[p.B] * groups;
-    // At least a position per range, and one more for every four heads of a group
+    // At least a position per range, and one more for every four heads of a warp
     // beyond the first four: a shorter range only adds partial results to join
     // (10 sequences, 16 heads, up to 12043 keys: 34 us with one position, 21 with
     // four; 16 sequences of one head a group: 12 us with one, 16 with four).
@@ -406,13 +415,15 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
     if (blockIdx.x >= nctas) return;
     const Cut cut_at(total, nctas);
     const uint32_t start = cut_at.start(blockIdx.x), end = cut_at.start(blockIdx.x + 1);
-    const int range = warp / G::SPLIT, side = warp % G::SPLIT;  // this warp's range, and its part of the columns
+    // this warp's range, its place there, its part of the columns and its first head of a group
+    const int range = warp / G::MATES, mate = warp % G::MATES;
+    const int side = G::SPLIT > 1 ? mate : 0, row0 = R > 1 ? mate * ROWS : 0;
     const Cut warp_cut(end - start, G::RANGES);
     const uint32_t wstart = start + warp_cut.start(range), wend = start + warp_cut.start(range + 1);
     const __nv_bfloat16 *my_q = p.q + side * G::COLS, *my_k = p.k + side * G::COLS, *my_v = p.v + side * G::COLS;
 
     // ---- this warp's ring: loads run STAGES tiles ahead, across groups
-    const uint32_t ring = smem_u32(smem) + uint32_t(warp) * G::RING;
+    const uint32_t ring = smem_u32(smem) + uint32_t(warp / R) * G::RING;
     Walk load_walk{wstart, wend, prefix, p.B, groups, false};
     uint32_t load_tile = 0;
     Range lr;
@@ -433,7 +444,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
             load_len = length(lr.b);
             load_tile = lr.t0;
             // the group's queries head for L1 while its first tiles do for shared memory
-            const int head = lr.g / p.chunks * p.per_kv + lr.g % p.chunks * ROWS + (lane & (ROWS - 1));
+            const int head = lr.g / p.chunks * p.per_kv + lr.g % p.chunks * G::GROUP + row0 + (lane & (ROWS - 1));
             if (lane < ROWS && head < (lr.g / p.chunks + 1) * p.per_kv) {
                 const char* q = reinterpret_cast<const char*>(my_q + int64_t(lr.b) * p.q_stride + int64_t(head) * D);
 #pragma unroll
@@ -451,8 +462,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
         if (have[0]) {
             const uint32_t dst = ring + load_slot * (2 * G::HALF);
 #pragma unroll
-            for (int i = 0; i < G::KEYS * G::CHUNKS / 32; ++i) {
-                const int piece = i * 32 + lane, row = piece / G::CHUNKS, c = piece % G::CHUNKS;
+            for (int i = 0; i < G::KEYS * G::CHUNKS / (32 * R); ++i) {
+                const int piece = (i * R + (R > 1 ? mate : 0)) * 32 + lane, row = piece / G::CHUNKS, c = piece % G::CHUNKS;
                 const int64_t ro = __shfl_sync(0xffffffffu, off[0], row);
                 const bool ok = ro >= 0;
                 const int64_t at = (ok ? ro : 0) + c * 8;
@@ -467,8 +478,10 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
         look_up(off[1], have[1]);
         if (++load_slot == G::STAGES) load_slot = 0;
     };
+    // With a ring of its own a warp refills a stage when it has used it; two warps
+    // meet before each tile, so the stage before is free then.
 #pragma unroll
-    for (int i = 0; i < G::STAGES; ++i) issue();
+    for (int i = 0; i < G::STAGES - (R > 1); ++i) issue();
 
     const int r0 = lane >> 2, r1 = r0 + 8;  // this lane's rows (heads) of the products
     uint32_t slot = 0, turn = 0;
@@ -481,8 +494,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
     float o[G::COLS / 8][4];
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     while (walk.next(r)) {
-        const int kv = r.g / p.chunks, head0 = kv * p.per_kv + (r.g % p.chunks) * ROWS;
-        const int heads = min(ROWS, (kv + 1) * p.per_kv - head0);
+        const int kv = r.g / p.chunks, head0 = kv * p.per_kv + (r.g % p.chunks) * G::GROUP + row0;
+        const int heads = min(ROWS, (kv + 1) * p.per_kv - head0);  // none or fewer for a second warp
         const int len = length(r.b);
         // query rows as A fragments
         uint32_t qa[G::COLS / 16][4];
@@ -506,8 +519,15 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
         l0 = l1 = 0.f;
 
         for (uint32_t t = r.t0; t < r.t1; ++t) {
-            copy_wait<G::STAGES - 1>();
-            __syncwarp();
+            if constexpr (R > 1) {
+                // both warps' copies of the tile are in, and both have used the one before
+                copy_wait<G::STAGES - 2>();
+                pair_sync(range);
+                issue();
+            } else {
+                copy_wait<G::STAGES - 1>();
+                __syncwarp();
+            }
             const uint32_t ks = ring + slot * (2 * G::HALF), vs = ks + G::HALF;
             // scores: keys in tiles of 8
             constexpr int NT = G::KEYS / 8;
@@ -528,12 +548,11 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
             }
             if constexpr (G::SPLIT == 2) {
                 // the other warp's columns: both add the same two sums, and have all else alike
-                static_assert(G::RANGES <= 15, "one named barrier each");
                 float4* at = reinterpret_cast<float4*>(smem + G::SM_SCORES) + turn * (G::WARPS * NT * 32) + lane;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
                     at[(warp * NT + n) * 32] = make_float4(s[n][0], s[n][1], s[n][2], s[n][3]);
-                asm volatile("bar.sync %0, 64;" ::"r"(1 + range) : "memory");
+                pair_sync(range);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
                     const float4 u = at[((warp ^ 1) * NT + n) * 32];
@@ -610,8 +629,10 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
                     mma16816(o[2 * n + 1], lo, vb[2], vb[3]);
                 }
             }
-            __syncwarp();  // every lane has read the tile before it is overwritten
-            issue();
+            if constexpr (R == 1) {
+                __syncwarp();  // every lane has read the tile before it is overwritten
+                issue();
+            }
             if (++slot == G::STAGES) slot = 0;
         }
 
@@ -637,7 +658,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
         } else if (walk.pos < walk.end) {
             head = r;
             has_head = true;
-            put_partial<D>(reinterpret_cast<float*>(smem + G::SM_HEADS) + range * G::PART, heads, side, o, m0, m1, l0, l1);
+            put_partial<G>(reinterpret_cast<float*>(smem + G::SM_HEADS) + range * G::PART, heads, row0, side, o, m0, m1, l0,
+                           l1);
         } else {
             tail = r;
             has_tail = true;
@@ -648,7 +670,7 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
     // ---- join what the CTA's ranges have of the same groups
     __shared__ Range pieces[2 * G::RANGES];  // in the order of positions; tiles 0: none
     __syncthreads();  // the rings are free
-    if (side == 0 && lane == 0) {
+    if (mate == 0 && lane == 0) {
         head.tiles = has_head ? head.tiles : 0u;
         tail.tiles = has_tail ? tail.tiles : 0u;
         pieces[2 * range] = head;
@@ -657,8 +679,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
     float* tails = reinterpret_cast<float*>(smem);
     const float* firsts = reinterpret_cast<const float*>(smem + G::SM_HEADS);
     if (has_tail) {
-        const int kv = tail.g / p.chunks, head0 = kv * p.per_kv + (tail.g % p.chunks) * ROWS;
-        put_partial<D>(tails + range * G::PART, min(ROWS, (kv + 1) * p.per_kv - head0), side, o, m0, m1, l0, l1);
+        const int kv = tail.g / p.chunks, head0 = kv * p.per_kv + (tail.g % p.chunks) * G::GROUP + row0;
+        put_partial<G>(tails + range * G::PART, min(ROWS, (kv + 1) * p.per_kv - head0), row0, side, o, m0, m1, l0, l1);
     }
     __syncthreads();
     Range open[2];  // groups shared with other CTAs: the first and the last one's
@@ -673,8 +695,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
         for (int i = 0; i < 2 * G::RANGES; ++i)
             if ((left >> i & 1u) && pieces[i].begin == q.begin) same |= 1u << i;
         left &= ~same;
-        const int kv = q.g / p.chunks, head0 = kv * p.per_kv + (q.g % p.chunks) * ROWS;
-        const int heads = min(ROWS, (kv + 1) * p.per_kv - head0);
+        const int kv = q.g / p.chunks, head0 = kv * p.per_kv + (q.g % p.chunks) * G::GROUP;
+        const int heads = min(G::GROUP, (kv + 1) * p.per_kv - head0);
         const bool whole = q.begin >= start && q.begin + q.tiles <= end;
         // a CTA's first shared group takes its first slot, its last one the second
         float* mine = p.slots + size_t(2 * blockIdx.x + (start >= q.begin ? 0 : 1)) * (ATTN_SLOT_BYTES / 4);
@@ -690,8 +712,8 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
                     const int i = __ffs(int(rest)) - 1, w = i >> 1;
                     rest &= rest - 1;
                     const float* s = (i & 1 ? tails : firsts) + w * G::PART;
-                    u[x].m = s[ROWS * G::OSTRIDE + row];
-                    u[x].l = s[ROWS * G::OSTRIDE + ROWS + row];
+                    u[x].m = s[G::GROUP * G::OSTRIDE + row];
+                    u[x].l = s[G::GROUP * G::OSTRIDE + G::GROUP + row];
                     u[x].o = *reinterpret_cast<const float4*>(s + row * G::OSTRIDE + c);
                 }
                 acc.add(u);
@@ -699,10 +721,10 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
             if (whole) {
                 acc.finish(p, q.b, head0 + row, c, D);
             } else {
-                __stcg(reinterpret_cast<float4*>(mine + 2 * ROWS + row * D + c), acc.o);
+                __stcg(reinterpret_cast<float4*>(mine + 2 * G::GROUP + row * D + c), acc.o);
                 if (c == 0) {
                     __stcg(mine + row, acc.m);
-                    __stcg(mine + ROWS + row, acc.l);
+                    __stcg(mine + G::GROUP + row, acc.l);
                 }
             }
         }
@@ -726,12 +748,15 @@ __global__ void __launch_bounds__(Geo<D>::THREADS, 1) mk_paged_attention_kernel(
     __syncthreads();
     for (int i = 0; i < nopen; ++i)
         if (small[4 * i])
-            join_group<D>(p, i == 0 ? open[0] : open[1], small[4 * i + 1], int(small[4 * i]), small[4 * i + 2], tails);
+            join_group<D, R>(p, i == 0 ? open[0] : open[1], small[4 * i + 1], int(small[4 * i]), small[4 * i + 2], tails);
 }
 
-template <int D>
-cudaError_t launch_attn(const AttnParams& p, int grid, cudaStream_t st) {
-    mk_paged_attention_kernel<D><<<grid, Geo<D>::THREADS, Geo<D>::SMEM, st>>>(p);
+template <int D, int R>
+cudaError_t launch_attn(AttnParams& p, int grid, cudaStream_t st) {
+    using G = Geo<D, R>;
+    p.chunks = (p.per_kv + G::GROUP - 1) / G::GROUP;
+    p.groups = p.chunks * p.Hkv;
+    mk_paged_attention_kernel<D, R><<<grid, G::THREADS, G::SMEM, st>>>(p);
     return cudaGetLastError();
 }
 
@@ -741,18 +766,20 @@ int64_t attn_groups(int B, int Hq, int Hkv) {
     return int64_t(Hkv) * ((Hq / Hkv + ROWS - 1) / ROWS);
 }
 
-template <int D>
+template <int D, int R>
 cudaError_t attn_smem() {
-    return cudaFuncSetAttribute(mk_paged_attention_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Geo<D>::SMEM);
+    return cudaFuncSetAttribute(mk_paged_attention_kernel<D, R>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Geo<D, R>::SMEM);
 }
 
 }  // namespace
 
 cudaError_t attn_kernel_attributes() {
     cudaError_t e;
-    if ((e = attn_smem<64>()) != cudaSuccess || (e = attn_smem<128>()) != cudaSuccess) return e;
-    return attn_smem<256>();
+    if ((e = attn_smem<64, 1>()) != cudaSuccess || (e = attn_smem<64, 2>()) != cudaSuccess ||
+        (e = attn_smem<128, 1>()) != cudaSuccess || (e = attn_smem<128, 2>()) != cudaSuccess)
+        return e;
+    return attn_smem<256, 1>();
 }
 
 }  // namespace mk
@@ -778,7 +805,7 @@ extern "C" mk_status_t mk_paged_attention(const void* q, int64_t q_stride, const
     const int64_t cap = int64_t(max_pages) * page_size;
     if (B > ATTN_MAX_B || cap > (int64_t(1) << 31) - 32) return MK_ERR_UNSUPPORTED;
     // positions in the order of tiles are 32-bit
-    const int64_t tiles = int64_t(B) * positions_of(int(cap), D == 64 ? Geo<64>::KEYS : Geo<128>::KEYS);
+    const int64_t tiles = int64_t(B) * positions_of(int(cap), D == 64 ? Geo<64, 1>::KEYS : Geo<128, 1>::KEYS);
     if (tiles >= int64_t(1) << 31 || tiles * groups >= int64_t(1) << 31) return MK_ERR_UNSUPPORTED;
     if (B > 0) {
         if (!q || !seq_lens || !out) return MK_ERR_INVALID_ARG;
@@ -830,11 +857,22 @@ extern "C" mk_status_t mk_paged_attention(const void* q, int64_t q_stride, const
     p.max_pages = max_pages;
     p.num_pages = num_pages;
     p.per_kv = Hq / Hkv;
-    p.chunks = (p.per_kv + ROWS - 1) / ROWS;
-    p.groups = int(groups);
     p.scale2 = scale * LOG2E;
     const int grid = std::min(sms, ATTN_MAX_CTAS);
-    const cudaError_t e = D == 64 ? launch_attn<64>(p, grid, st) : D == 128 ? launch_attn<128>(p, grid, st)
-                                                                           : launch_attn<256>(p, grid, st);
+    // Groups of 32 heads, two warps on a tile, where groups of 16 would pass over the
+    // keys an even number of times and there is a group of 32 per CTA: with that many
+    // the passes over a group's keys follow one another on the same SM, and the later
+    // ones find them in L2 no more (32 sequences of 4096 keys, 8 key-value heads, 24
+    // query heads each: 135 us, with groups of 16 170).  With fewer groups the passes
+    // run side by side, and groups of 16 have more ranges (one sequence of 8191 keys,
+    // 32 heads: 27 us, with groups of 16 22); with an odd number the second warp of the
+    // last group has nothing to do (16 sequences of 30000, 48 heads: 123 and 116).
+    const int passes = (p.per_kv + ROWS - 1) / ROWS;
+    const bool wide = passes % 2 == 0 && int64_t(B) * Hkv * (passes / 2) >= grid;
+    const cudaError_t e = D == 256          ? launch_attn<256, 1>(p, grid, st)
+                          : D == 128 && wide ? launch_attn<128, 2>(p, grid, st)
+                          : D == 128         ? launch_attn<128, 1>(p, grid, st)
+                          : wide             ? launch_attn<64, 2>(p, grid, st)
+                                             : launch_attn<64, 1>(p, grid, st);
     return e == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }

@@ -203,3 +203,12 @@ def test_bad_pages_and_lengths_are_reported():
         assert torch.equal(o["out"][1], good["out"][1])
     assert mk.mk_get_status() == mk.MK_OK
     assert torch.equal(c.run()["out"], good["out"])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("B,per_kv", [(200, 17), (160, 32), (90, 33), (200, 24), (80, 64)])
+def test_more_than_16_heads_and_many_sequences(B, per_kv, D):
+    lens = [(i * 37) % 150 for i in range(B)]
+    lens[-1], lens[B // 2] = 2000, 0
+    c = Case(lens, 2 * per_kv, 2, D, 16, seed=B + per_kv)
+    c.check(c.run())
