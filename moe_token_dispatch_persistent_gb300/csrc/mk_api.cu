@@ -37,6 +37,20 @@ cudaError_t read_and_clear_error(uint32_t out[4], cudaStream_t st);
 void noalloc_forget_scratch();
 }  // namespace mk
 
+namespace mk {
+
+// A cached buffer.  A call locks it from its look-up until its work is
+// enqueued; g_mu guards the maps alone, and is never held while waiting for an
+// entry.
+struct WsEntry {
+    std::mutex mu;
+    bool dropped = false;  // released, and in no map any more
+    void* ptr = nullptr;
+    size_t bytes = 0;
+};
+
+}  // namespace mk
+
 using namespace mk;
 
 namespace {
@@ -59,12 +73,8 @@ PFN_cuStreamWaitValue32_v11070 g_wait_value = nullptr;
 thread_local mk_launch_info_t g_last_info{};
 uint32_t g_last_err[4] = {0, 0, 0, 0};
 
-struct WsEntry {
-    void* ptr = nullptr;
-    size_t bytes = 0;
-};
 // One cache per layout of the control block (all but WS_DISPATCH are zeroed whole).
-std::map<std::pair<int, cudaStream_t>, WsEntry> g_ws[WS_KINDS];
+std::map<std::pair<int, cudaStream_t>, std::shared_ptr<WsEntry>> g_ws[WS_KINDS];
 
 struct HostStage {
     void* ptr = nullptr;
@@ -246,13 +256,6 @@ CUresult encode_2d(CUtensorMap* m, const void* base, uint64_t inner, uint64_t ou
     return host_encode_2d(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, base, inner, outer, row_bytes, box_inner, box_outer);
 }
 
-// The library's dispatch (or expert-parallel) workspace for (device, stream).
-// A new dispatch buffer's bookkeeping part (everything before the staging
-// rows) is zeroed; expert-parallel buffers whole.
-mk_status_t cached_workspace(int dev, cudaStream_t st, size_t need, size_t zero_bytes, void** out, bool ep = false) {
-    return host_workspace(ep ? WS_EP : WS_DISPATCH, dev, st, need, zero_bytes, out);
-}
-
 }  // namespace
 
 namespace mk {
@@ -268,9 +271,19 @@ mk_status_t host_device(int* dev, int* sms, DevError** err) try {
     return MK_ERR_CUDA;
 }
 
-mk_status_t host_workspace(WsKind kind, int dev, cudaStream_t st, size_t need, size_t zero_bytes, void** out) try {
-    std::lock_guard<std::mutex> lock(g_mu);
-    WsEntry& w = g_ws[kind][{dev, st}];
+mk_status_t Workspace::get(WsKind kind, int dev, cudaStream_t st, size_t need, size_t zero_bytes) try {
+    do {  // again when the entry was released meanwhile
+        {
+            std::lock_guard<std::mutex> lock(g_mu);
+            auto it = g_ws[kind].find({dev, st});
+            if (it == g_ws[kind].end())
+                it = g_ws[kind].emplace(std::make_pair(dev, st), std::make_shared<WsEntry>()).first;
+            if (lock_.owns_lock()) lock_.unlock();
+            entry_ = it->second;
+        }
+        lock_ = std::unique_lock<std::mutex>(entry_->mu);
+    } while (entry_->dropped);
+    WsEntry& w = *entry_;
     if (w.bytes < need) {
         if (kind == WS_ATTN || kind == WS_FFN) {
             // memory allocated under stream capture would belong to the graph
@@ -289,7 +302,7 @@ mk_status_t host_workspace(WsKind kind, int dev, cudaStream_t st, size_t need, s
         if (cudaMemsetAsync(w.ptr, 0, kind == WS_DISPATCH ? zero_bytes : grow, st) != cudaSuccess) return MK_ERR_CUDA;
         w.bytes = grow;
     }
-    *out = w.ptr;
+    ptr_ = static_cast<uint8_t*>(w.ptr);
     return MK_OK;
 } catch (...) {  // no memory for the cache's own entry
     return MK_ERR_WORKSPACE;
@@ -412,12 +425,13 @@ mk_status_t run_path(const void* x, const float* logits, int T, int H, int E, in
     if (nch > grid * MAX_CHUNKS_PER_CTA) return MK_ERR_UNSUPPORTED;
     const WsLayout L = ws_layout(T, H, E, k, !direct);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
+    Workspace cached;  // held until the launch below
     if (ws) {
         if (ws_bytes < L.total || !aligned(ws, 256)) return MK_ERR_WORKSPACE;
     } else {
-        void* p = nullptr;
-        if ((s = cached_workspace(dev, st, L.total, L.xs, &p)) != MK_OK) return s;
-        ws = static_cast<uint8_t*>(p);
+        // zeroed: the bookkeeping part, everything before the staging rows
+        if ((s = cached.get(WS_DISPATCH, dev, st, L.total, L.xs)) != MK_OK) return s;
+        ws = cached.data();
     }
 
     Params p{};
@@ -610,12 +624,12 @@ mk_status_t run_ep(const void* x, const float* logits, int T, int H, int E, int 
     // completion counts: a rank's (row, N-block) results in 32 bits
     if (uint64_t(T) * uint64_t(k) * uint64_t(nb) >= (uint64_t(1) << 32)) return MK_ERR_UNSUPPORTED;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
+    Workspace cached;  // held until the launch below
     if (ws) {
         if (ws_bytes < L.total || !aligned(ws, 256)) return MK_ERR_WORKSPACE;
     } else {
-        void* pw = nullptr;
-        if ((s = cached_workspace(dev, st, L.total, L.total, &pw, true)) != MK_OK) return s;
-        ws = static_cast<uint8_t*>(pw);
+        if ((s = cached.get(WS_EP, dev, st, L.total, L.total)) != MK_OK) return s;
+        ws = cached.data();
     }
 
     Params p{};
@@ -930,11 +944,18 @@ mk_status_t mk_read_trace(void* stream, const void* workspace, int T, int H, int
     if (cudaGetDevice(&dev) != cudaSuccess) return MK_ERR_CUDA;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const uint8_t* ws = static_cast<const uint8_t*>(workspace);
+    std::shared_ptr<WsEntry> entry;
+    std::unique_lock<std::mutex> held;
     if (!ws) {
-        std::lock_guard<std::mutex> lock(g_mu);
-        auto it = g_ws[WS_DISPATCH].find({dev, st});
-        if (it == g_ws[WS_DISPATCH].end()) return MK_ERR_INVALID_ARG;
-        ws = static_cast<const uint8_t*>(it->second.ptr);
+        {
+            std::lock_guard<std::mutex> lock(g_mu);
+            auto it = g_ws[WS_DISPATCH].find({dev, st});
+            if (it == g_ws[WS_DISPATCH].end()) return MK_ERR_INVALID_ARG;
+            entry = it->second;
+        }
+        held = std::unique_lock<std::mutex>(entry->mu);
+        ws = static_cast<const uint8_t*>(entry->ptr);
+        if (!ws) return MK_ERR_INVALID_ARG;
     }
     const WsLayout L = ws_layout(T, H, E, k);
     const size_t want = size_t(MAX_GRID) * TRACE_SLOTS;
@@ -945,20 +966,28 @@ mk_status_t mk_read_trace(void* stream, const void* workspace, int T, int H, int
 
 void mk_release_workspace(void) {
     noalloc_forget_scratch();  // the allocation-free entry point looks its array up again
-    std::lock_guard<std::mutex> lock(g_mu);
-    for (auto& d : g_dev) d.ready = false;  // after a device reset: attributes and addresses are looked up again
     int cur = 0;
     cudaGetDevice(&cur);
     // streams may be gone by now: synchronise the device, then free
     for (auto& cache : g_ws) {
-        for (auto& kv : cache) {
-            if (!kv.second.ptr) continue;
+        std::map<std::pair<int, cudaStream_t>, std::shared_ptr<WsEntry>> mine;
+        {
+            std::lock_guard<std::mutex> lock(g_mu);
+            mine.swap(cache);
+        }
+        for (auto& kv : mine) {
+            std::lock_guard<std::mutex> held(kv.second->mu);  // a call that has it enqueues its work first
+            kv.second->dropped = true;
+            if (!kv.second->ptr) continue;
             cudaSetDevice(kv.first.first);
             cudaDeviceSynchronize();
-            cudaFree(kv.second.ptr);
+            cudaFree(kv.second->ptr);
+            kv.second->ptr = nullptr;
+            kv.second->bytes = 0;
         }
-        cache.clear();
     }
+    std::lock_guard<std::mutex> lock(g_mu);
+    for (auto& d : g_dev) d.ready = false;  // after a device reset: attributes and addresses are looked up again
     for (auto& kv : g_host_stage) {
         cudaSetDevice(kv.first.first);
         cudaDeviceSynchronize();

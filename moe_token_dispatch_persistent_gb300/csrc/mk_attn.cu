@@ -828,12 +828,12 @@ extern "C" mk_status_t mk_paged_attention(const void* q, int64_t q_stride, const
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const size_t need = mk_paged_attention_workspace_size(B, Hq, Hkv);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
+    Workspace cached;  // held until the launch below
     if (ws) {
         if (ws_bytes < need || !host_aligned(ws, 256)) return MK_ERR_WORKSPACE;
     } else {
-        void* w = nullptr;
-        if ((s = host_workspace(WS_ATTN, dev, st, need, need, &w)) != MK_OK) return s;
-        ws = static_cast<uint8_t*>(w);
+        if ((s = cached.get(WS_ATTN, dev, st, need, need)) != MK_OK) return s;
+        ws = cached.data();
     }
     AttnParams p{};
     p.q = static_cast<const __nv_bfloat16*>(q);

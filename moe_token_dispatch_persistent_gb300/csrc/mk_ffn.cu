@@ -1208,12 +1208,12 @@ extern "C" mk_status_t mk_moe_ffn_decode(const void* x, const float* x_scale, co
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const FfnLayout L = ffn_layout(T, H, F, k, fp8);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
+    Workspace cached;  // held until the launch below
     if (ws) {
         if (ws_bytes < L.total || !host_aligned(ws, 256)) return MK_ERR_WORKSPACE;
     } else {
-        void* v = nullptr;
-        if ((s = host_workspace(WS_FFN, dev, st, L.total, L.total, &v)) != MK_OK) return s;
-        ws = static_cast<uint8_t*>(v);
+        if ((s = cached.get(WS_FFN, dev, st, L.total, L.total)) != MK_OK) return s;
+        ws = cached.data();
     }
     FfnParams p{};
     p.logits = logits;

@@ -8,6 +8,8 @@
 
 #include <cstddef>
 #include <cstdint>
+#include <memory>
+#include <mutex>
 
 #include "mk.h"
 
@@ -32,10 +34,22 @@ cudaError_t ffn_kernel_attributes();
 // Workspace caches, one per operator family: their control blocks differ.
 enum WsKind { WS_DISPATCH = 0, WS_EP = 1, WS_ATTN = 2, WS_FFN = 3, WS_KINDS = 4 };
 
-// The library's workspace of that kind for (device, stream), grown on demand
-// on `st`.  Of a new buffer the first `zero_bytes` are zeroed (WS_DISPATCH) or
-// all of it (the others, whose counters move with the sizes).
-mk_status_t host_workspace(WsKind kind, int dev, cudaStream_t st, size_t need, size_t zero_bytes, void** out);
+// The library's workspace of a kind for (device, stream), grown on demand on
+// `st`.  Of a new buffer the first `zero_bytes` are zeroed (WS_DISPATCH) or all
+// of it (the others, whose counters move with the sizes).  The object holds the
+// buffer: keep it until the call's work is enqueued, so that no other thread's
+// call frees what this one is about to use.
+struct WsEntry;
+class Workspace {
+  public:
+    mk_status_t get(WsKind kind, int dev, cudaStream_t st, size_t need, size_t zero_bytes);
+    uint8_t* data() const { return ptr_; }
+
+  private:
+    std::shared_ptr<WsEntry> entry_;
+    std::unique_lock<std::mutex> lock_;  // of the entry
+    uint8_t* ptr_ = nullptr;
+};
 
 // A 2-D tensor map in the 128-byte swizzle (out-of-range reads give zeros).
 CUresult host_encode_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t outer,

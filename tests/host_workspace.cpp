@@ -1,0 +1,295 @@
+// The library's workspace caches without a GPU: mk_api.cu compiled as host code
+// against a CUDA runtime that only keeps a log per stream.  Each scenario
+// drives public entry points and then checks, in the order of the stream,
+// that every launch finds its workspace allocated and nobody else's.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <atomic>
+#include <chrono>
+#include <condition_variable>
+#include <cstdio>
+#include <cstdlib>
+#include <cstring>
+#include <functional>
+#include <map>
+#include <mutex>
+#include <string>
+#include <thread>
+#include <vector>
+
+#include "mk.h"
+#include "mk_common.h"
+#include "mk_host.h"
+
+// ------------------------------------------------------- the fake runtime --
+
+namespace {
+
+enum What { ALLOC, FREE, ZERO, LAUNCH, SYNC };
+struct Op {
+    What what;
+    uintptr_t ptr;
+    cudaStream_t stream;
+    bool captured;
+};
+
+std::mutex mu;
+std::vector<Op> ops;                          // in the order they were enqueued
+std::map<uintptr_t, size_t> sizes;
+uintptr_t next_ptr = 0x10000000;
+std::map<cudaStream_t, bool> capturing;
+std::map<cudaStream_t, unsigned long long> ids;  // of handles that do not stand for themselves
+thread_local unsigned long long per_thread_id = 0;
+std::atomic<unsigned long long> threads_seen{1000};
+thread_local std::function<void()> on_encode;  // between a call's workspace and its launch
+
+bool is_capturing(cudaStream_t s) {
+    auto it = capturing.find(s);
+    return it != capturing.end() && it->second;
+}
+void log(What w, const void* p, cudaStream_t s) {
+    ops.push_back({w, reinterpret_cast<uintptr_t>(p), s, is_capturing(s)});
+}
+
+CUresult CUDAAPI fake_encode(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill) {
+    if (on_encode) {
+        auto f = std::move(on_encode);
+        on_encode = nullptr;
+        f();
+    }
+    return CUDA_SUCCESS;
+}
+
+cudaError_t launched(const void* ws, cudaStream_t st) {
+    std::lock_guard<std::mutex> l(mu);
+    log(LAUNCH, ws, st);
+    return cudaSuccess;
+}
+
+}  // namespace
+
+extern "C" {
+cudaError_t cudaGetDevice(int* d) { return *d = 0, cudaSuccess; }
+cudaError_t cudaSetDevice(int) { return cudaSuccess; }
+cudaError_t cudaDeviceGetAttribute(int* v, cudaDeviceAttr a, int) {
+    *v = a == cudaDevAttrComputeCapabilityMajor ? 10 : a == cudaDevAttrComputeCapabilityMinor ? 3 : 152;
+    return cudaSuccess;
+}
+cudaError_t cudaGetDriverEntryPointByVersion(const char* name, void** fn, unsigned, unsigned long long,
+                                             cudaDriverEntryPointQueryResult* q) {
+    const bool enc = std::strcmp(name, "cuTensorMapEncodeTiled") == 0;
+    *fn = enc ? reinterpret_cast<void*>(fake_encode) : nullptr;
+    *q = enc ? cudaDriverEntryPointSuccess : cudaDriverEntryPointSymbolNotFound;
+    return cudaSuccess;
+}
+cudaError_t cudaMallocAsync(void** p, size_t n, cudaStream_t s) {
+    std::lock_guard<std::mutex> l(mu);
+    *p = reinterpret_cast<void*>(next_ptr);
+    sizes[next_ptr] = n;
+    next_ptr += (n + 0xffff) & ~size_t(0xffff);
+    log(ALLOC, *p, s);
+    return cudaSuccess;
+}
+cudaError_t cudaFreeAsync(void* p, cudaStream_t s) {
+    std::lock_guard<std::mutex> l(mu);
+    log(FREE, p, s);
+    return cudaSuccess;
+}
+cudaError_t cudaMemsetAsync(void* p, int, size_t, cudaStream_t s) {
+    std::lock_guard<std::mutex> l(mu);
+    log(ZERO, p, s);
+    return cudaSuccess;
+}
+cudaError_t cudaFree(void* p) {
+    std::lock_guard<std::mutex> l(mu);
+    log(SYNC, nullptr, nullptr);
+    log(FREE, p, nullptr);
+    return cudaSuccess;
+}
+cudaError_t cudaDeviceSynchronize() {
+    std::lock_guard<std::mutex> l(mu);
+    log(SYNC, nullptr, nullptr);
+    return cudaSuccess;
+}
+cudaError_t cudaStreamIsCapturing(cudaStream_t s, cudaStreamCaptureStatus* c) {
+    std::lock_guard<std::mutex> l(mu);
+    *c = is_capturing(s) ? cudaStreamCaptureStatusActive : cudaStreamCaptureStatusNone;
+    return cudaSuccess;
+}
+cudaError_t cudaStreamGetId(cudaStream_t s, unsigned long long* id) {
+    std::lock_guard<std::mutex> l(mu);
+    if (s == cudaStreamPerThread) {
+        if (!per_thread_id) per_thread_id = ++threads_seen;
+        *id = per_thread_id;
+    } else if (s == nullptr || s == cudaStreamLegacy) {
+        *id = 1;
+    } else {
+        auto it = ids.find(s);
+        *id = it != ids.end() ? it->second : 5000000 + reinterpret_cast<uintptr_t>(s);
+    }
+    return cudaSuccess;
+}
+// what no scenario reaches
+cudaError_t cudaMalloc(void**, size_t) { return cudaErrorNotSupported; }
+cudaError_t cudaMemset(void*, int, size_t) { return cudaErrorNotSupported; }
+cudaError_t cudaMemcpyAsync(void*, const void*, size_t, cudaMemcpyKind, cudaStream_t) { return cudaErrorNotSupported; }
+cudaError_t cudaStreamSynchronize(cudaStream_t) { return cudaSuccess; }
+cudaError_t cudaStreamCreateWithFlags(cudaStream_t*, unsigned) { return cudaErrorNotSupported; }
+cudaError_t cudaStreamDestroy(cudaStream_t) { return cudaSuccess; }
+cudaError_t cudaStreamWaitEvent(cudaStream_t, cudaEvent_t, unsigned) { return cudaErrorNotSupported; }
+cudaError_t cudaEventCreateWithFlags(cudaEvent_t*, unsigned) { return cudaErrorNotSupported; }
+cudaError_t cudaEventDestroy(cudaEvent_t) { return cudaSuccess; }
+cudaError_t cudaEventRecord(cudaEvent_t, cudaStream_t) { return cudaErrorNotSupported; }
+cudaError_t cudaGetLastError() { return cudaSuccess; }
+}
+
+namespace mk {
+cudaError_t launch_fused(const Params& p, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+                         const CUtensorMap&, int, cudaStream_t st) {
+    return launched(p.ctl, st);
+}
+cudaError_t launch_unfused(const Params& p, const CUtensorMap&, const CUtensorMap&, const CUtensorMap&,
+                           const CUtensorMap&, int, cudaStream_t st) {
+    return launched(p.ctl, st);
+}
+cudaError_t launch_ep(const Params& p, const CUtensorMap*, const CUtensorMap&, const CUtensorMap&, int,
+                      cudaStream_t st) {
+    return launched(p.ep_ctl[0], st);
+}
+cudaError_t set_kernel_attributes() { return cudaSuccess; }
+cudaError_t attn_kernel_attributes() { return cudaSuccess; }
+cudaError_t ffn_kernel_attributes() { return cudaSuccess; }
+cudaError_t fused_max_blocks_per_sm(int* n) { return *n = 1, cudaSuccess; }
+cudaError_t read_and_clear_error(uint32_t out[4], cudaStream_t) { return out[0] = 0, cudaSuccess; }
+cudaError_t error_word(DevError** out) { return *out = nullptr, cudaSuccess; }
+void noalloc_forget_scratch() {}
+}  // namespace mk
+
+// ------------------------------------------------------------- scenarios --
+
+namespace {
+
+int failures = 0;
+void expect(bool ok, const char* what) {
+    if (!ok) {
+        std::printf("FAILED: %s\n", what);
+        ++failures;
+    }
+}
+
+// One dispatch call of T tokens: the larger T, the larger its workspace.
+mk_status_t call(cudaStream_t st, int T) {
+    void* p = reinterpret_cast<void*>(0x100);
+    mk_config_t c;
+    mk_config_default(&c);
+    c.gather = MK_GATHER_STAGED;
+    return mk_moe_dispatch_gemm_ex(p, static_cast<float*>(p), T, 64, 8, 2, p, 64, p, static_cast<int32_t*>(p),
+                                   static_cast<int32_t*>(p), static_cast<float*>(p), st, &c, nullptr, 0);
+}
+// The same through the expert-parallel cache.
+mk_status_t call_ep(cudaStream_t st, int T) {
+    void* p = reinterpret_cast<void*>(0x100);
+    return mk_moe_ep_sim(p, static_cast<float*>(p), T, 64, 8, 2, p, 64, 2, p, static_cast<int32_t*>(p),
+                         static_cast<int32_t*>(p), static_cast<float*>(p), nullptr, st, nullptr, nullptr, 0);
+}
+
+cudaStream_t stream(int i) { return reinterpret_cast<cudaStream_t>(uintptr_t(0x5000 + 16 * i)); }
+
+// The allocation that holds an address.
+uintptr_t buffer_of(uintptr_t p) {
+    auto it = sizes.upper_bound(p);
+    return it == sizes.begin() ? 0 : (--it)->first;
+}
+// Every launch after its buffer's allocation on the same stream and before its release.
+void expect_live() {
+    std::map<uintptr_t, bool> live;
+    for (const Op& o : ops) {
+        if (o.what == ALLOC) live[o.ptr] = true;
+        if (o.what == FREE) live[o.ptr] = false;
+        if (o.what == LAUNCH) expect(live[buffer_of(o.ptr)], "a launch finds its workspace allocated");
+    }
+}
+int count(What w) {
+    int n = 0;
+    for (const Op& o : ops) n += o.what == w;
+    return n;
+}
+
+// Two threads on one stream; the second needs a larger buffer while the first
+// stands between its look-up and its launch.
+void growth(mk_status_t (*one)(cudaStream_t, int)) {
+    expect(one(stream(0), 64) == MK_OK, "first call");
+    std::mutex m;
+    std::condition_variable cv;
+    bool inside = false, grown = false;
+    std::thread a([&] {
+        on_encode = [&] {
+            std::unique_lock<std::mutex> l(m);
+            inside = true;
+            cv.notify_all();
+            // the other call gets the time to pass this one, if it can
+            cv.wait_for(l, std::chrono::milliseconds(500), [&] { return grown; });
+        };
+        expect(one(stream(0), 64) == MK_OK, "the small call");
+    });
+    std::thread b([&] {
+        {
+            std::unique_lock<std::mutex> l(m);
+            cv.wait(l, [&] { return inside; });
+        }
+        expect(one(stream(0), 4096) == MK_OK, "the large call");
+        std::lock_guard<std::mutex> l(m);
+        grown = true;
+        cv.notify_all();
+    });
+    a.join();
+    b.join();
+    expect(count(LAUNCH) == 3, "three launches");
+    expect(count(FREE) == 1, "the small buffer is given back");
+    expect_live();
+}
+
+// The buffers are released while another thread stands there.
+void release_under_a_call() {
+    std::mutex m;
+    std::condition_variable cv;
+    bool inside = false, released = false;
+    std::thread a([&] {
+        on_encode = [&] {
+            std::unique_lock<std::mutex> l(m);
+            inside = true;
+            cv.notify_all();
+            cv.wait_for(l, std::chrono::milliseconds(500), [&] { return released; });
+        };
+        expect(call(stream(0), 64) == MK_OK, "the call");
+    });
+    std::thread b([&] {
+        {
+            std::unique_lock<std::mutex> l(m);
+            cv.wait(l, [&] { return inside; });
+        }
+        mk_release_workspace();
+        std::lock_guard<std::mutex> l(m);
+        released = true;
+        cv.notify_all();
+    });
+    a.join();
+    b.join();
+    expect(call(stream(0), 64) == MK_OK, "a call afterwards");
+    expect_live();
+}
+
+}  // namespace
+
+int main(int argc, char** argv) {
+    const std::string name = argc > 1 ? argv[1] : "";
+    if (name == "growth") growth(call);
+    else if (name == "growth_ep") growth(call_ep);
+    else if (name == "release") release_under_a_call();
+    else return std::printf("no such scenario\n"), 2;
+    std::printf("%s: %zu operations, %d failures\n", name.c_str(), ops.size(), failures);
+    return failures ? 1 : 0;
+}
