@@ -43,6 +43,12 @@
  * legacy default stream) and return without synchronising.  A fault or a
  * bounded wait that ran out inside the kernel is recorded in a per-device
  * error word; mk_get_status() synchronises the stream and reports it.
+ *
+ * Threads.  Calls may come from several host threads; those that use the
+ * library's workspace of one stream are enqueued one after another.  The
+ * per-thread default stream has a workspace in each thread that used it, kept
+ * until mk_release_workspace().  A call on a new stream that got the handle of
+ * a destroyed one waits for the device once.
  */
 #ifndef MK_H
 #define MK_H

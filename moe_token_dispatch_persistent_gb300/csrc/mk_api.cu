@@ -18,6 +18,7 @@
 #include <cstring>
 #include <map>
 #include <mutex>
+#include <tuple>
 #include <utility>
 
 #include "mk.h"
@@ -45,6 +46,7 @@ namespace mk {
 struct WsEntry {
     std::mutex mu;
     bool dropped = false;  // released, and in no map any more
+    unsigned long long stream = 0;  // id of the stream that used it last
     void* ptr = nullptr;
     size_t bytes = 0;
 };
@@ -74,7 +76,17 @@ thread_local mk_launch_info_t g_last_info{};
 uint32_t g_last_err[4] = {0, 0, 0, 0};
 
 // One cache per layout of the control block (all but WS_DISPATCH are zeroed whole).
-std::map<std::pair<int, cudaStream_t>, std::shared_ptr<WsEntry>> g_ws[WS_KINDS];
+// The per-thread default stream, one handle for a stream in every thread, has
+// the stream's id in its key (0 in the others).
+using WsKey = std::tuple<int, cudaStream_t, unsigned long long>;
+std::map<WsKey, std::shared_ptr<WsEntry>> g_ws[WS_KINDS];
+
+cudaError_t ws_key(int dev, cudaStream_t st, WsKey* key, unsigned long long* id) {
+    const cudaError_t e = cudaStreamGetId(st, id);
+    *key = WsKey(dev, st, st == cudaStreamPerThread ? *id : 0ull);
+    return e;
+}
+
 
 struct HostStage {
     void* ptr = nullptr;
@@ -86,7 +98,7 @@ struct HostStage {
                                      // do not accept stream-ordered pool memory)
     uint32_t seq = 0;                // calls made with this stage (chunk flags hold it)
 };
-std::map<std::pair<int, cudaStream_t>, HostStage> g_host_stage;
+std::map<WsKey, HostStage> g_host_stage;
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -272,18 +284,28 @@ mk_status_t host_device(int* dev, int* sms, DevError** err) try {
 }
 
 mk_status_t Workspace::get(WsKind kind, int dev, cudaStream_t st, size_t need, size_t zero_bytes) try {
+    WsKey key;
+    unsigned long long id = 0;
+    if (ws_key(dev, st, &key, &id) != cudaSuccess) return MK_ERR_CUDA;
     do {  // again when the entry was released meanwhile
         {
             std::lock_guard<std::mutex> lock(g_mu);
-            auto it = g_ws[kind].find({dev, st});
-            if (it == g_ws[kind].end())
-                it = g_ws[kind].emplace(std::make_pair(dev, st), std::make_shared<WsEntry>()).first;
+            auto it = g_ws[kind].find(key);
+            if (it == g_ws[kind].end()) it = g_ws[kind].emplace(key, std::make_shared<WsEntry>()).first;
             if (lock_.owns_lock()) lock_.unlock();
             entry_ = it->second;
         }
         lock_ = std::unique_lock<std::mutex>(entry_->mu);
     } while (entry_->dropped);
     WsEntry& w = *entry_;
+    if (w.ptr && w.stream != id) {
+        // the handle of a stream that is gone: its work may still run on the buffer
+        cudaStreamCaptureStatus capturing;
+        if (cudaStreamIsCapturing(st, &capturing) != cudaSuccess) return MK_ERR_CUDA;
+        if (capturing != cudaStreamCaptureStatusNone) return MK_ERR_WORKSPACE;
+        if (cudaDeviceSynchronize() != cudaSuccess) return MK_ERR_CUDA;
+    }
+    w.stream = id;
     if (w.bytes < need) {
         if (kind == WS_ATTN || kind == WS_FFN) {
             // memory allocated under stream capture would belong to the graph
@@ -833,9 +855,12 @@ mk_status_t mk_moe_dispatch_gemm_host(const void* x_host, const float* logits_ho
                  o_done = ws_align(o_g + rows * 4), total = ws_align(o_done + size_t(nchunks) * 4);
     uint8_t* base = nullptr;
     HostStage* hs = nullptr;
+    WsKey key;
+    unsigned long long id = 0;
+    if (ws_key(dev, st, &key, &id) != cudaSuccess) return MK_ERR_CUDA;
     {
         std::lock_guard<std::mutex> lock(g_mu);
-        HostStage& h = g_host_stage[{dev, st}];
+        HostStage& h = g_host_stage[key];
         if (h.bytes < total) {
             if (h.ptr && cudaFreeAsync(h.ptr, st) != cudaSuccess) return MK_ERR_CUDA;
             h.ptr = nullptr;
@@ -947,9 +972,12 @@ mk_status_t mk_read_trace(void* stream, const void* workspace, int T, int H, int
     std::shared_ptr<WsEntry> entry;
     std::unique_lock<std::mutex> held;
     if (!ws) {
+        WsKey key;
+        unsigned long long id = 0;
+        if (ws_key(dev, st, &key, &id) != cudaSuccess) return MK_ERR_CUDA;
         {
             std::lock_guard<std::mutex> lock(g_mu);
-            auto it = g_ws[WS_DISPATCH].find({dev, st});
+            auto it = g_ws[WS_DISPATCH].find(key);
             if (it == g_ws[WS_DISPATCH].end()) return MK_ERR_INVALID_ARG;
             entry = it->second;
         }
@@ -970,7 +998,7 @@ void mk_release_workspace(void) {
     cudaGetDevice(&cur);
     // streams may be gone by now: synchronise the device, then free
     for (auto& cache : g_ws) {
-        std::map<std::pair<int, cudaStream_t>, std::shared_ptr<WsEntry>> mine;
+        std::map<WsKey, std::shared_ptr<WsEntry>> mine;
         {
             std::lock_guard<std::mutex> lock(g_mu);
             mine.swap(cache);
@@ -979,7 +1007,7 @@ void mk_release_workspace(void) {
             std::lock_guard<std::mutex> held(kv.second->mu);  // a call that has it enqueues its work first
             kv.second->dropped = true;
             if (!kv.second->ptr) continue;
-            cudaSetDevice(kv.first.first);
+            cudaSetDevice(std::get<0>(kv.first));
             cudaDeviceSynchronize();
             cudaFree(kv.second->ptr);
             kv.second->ptr = nullptr;
@@ -989,7 +1017,7 @@ void mk_release_workspace(void) {
     std::lock_guard<std::mutex> lock(g_mu);
     for (auto& d : g_dev) d.ready = false;  // after a device reset: attributes and addresses are looked up again
     for (auto& kv : g_host_stage) {
-        cudaSetDevice(kv.first.first);
+        cudaSetDevice(std::get<0>(kv.first));
         cudaDeviceSynchronize();
         if (kv.second.ptr) cudaFree(kv.second.ptr);
         if (kv.second.copy) cudaStreamDestroy(kv.second.copy);

@@ -282,6 +282,41 @@ void release_under_a_call() {
     expect_live();
 }
 
+// The per-thread default stream is one handle for another stream in each thread.
+void per_thread() {
+    uintptr_t mine[2] = {0, 0};
+    for (int i = 0; i < 2; ++i)
+        std::thread([&, i] {
+            expect(call(cudaStreamPerThread, 64) == MK_OK, "the call");
+            expect(call(cudaStreamPerThread, 64) == MK_OK, "the call again");
+            mine[i] = buffer_of(ops.back().ptr);
+        }).join();
+    expect(mine[0] != mine[1], "two threads' streams have a workspace each");
+    expect(count(ALLOC) == 2, "and keep it");
+    expect_live();
+}
+
+// A stream is destroyed and another gets its handle: the first one's work may
+// still be running on the buffer.
+void recycled_handle() {
+    expect(call(stream(3), 64) == MK_OK, "first stream");
+    ids[stream(3)] = 77;
+    expect(call(stream(3), 64) == MK_OK, "second stream");
+    uintptr_t last = 0;
+    bool settled = true;
+    for (const Op& o : ops) {
+        if (o.what == SYNC) settled = true;
+        if (o.what != LAUNCH) continue;
+        expect(settled || buffer_of(o.ptr) != last, "work of the old stream has ended before its buffer is used");
+        last = buffer_of(o.ptr);
+        settled = false;
+    }
+    const int before = count(SYNC);
+    expect(call(stream(3), 64) == MK_OK, "second stream again");
+    expect(count(SYNC) == before, "no wait in later calls");
+    expect_live();
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
@@ -289,6 +324,8 @@ int main(int argc, char** argv) {
     if (name == "growth") growth(call);
     else if (name == "growth_ep") growth(call_ep);
     else if (name == "release") release_under_a_call();
+    else if (name == "per_thread") per_thread();
+    else if (name == "recycled_handle") recycled_handle();
     else return std::printf("no such scenario\n"), 2;
     std::printf("%s: %zu operations, %d failures\n", name.c_str(), ops.size(), failures);
     return failures ? 1 : 0;

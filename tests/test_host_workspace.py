@@ -22,7 +22,7 @@ def harness(tmp_path_factory):
     return exe
 
 
-@pytest.mark.parametrize("scenario", ["growth", "growth_ep", "release"])
+@pytest.mark.parametrize("scenario", ["growth", "growth_ep", "release", "per_thread", "recycled_handle"])
 def test_scenario(harness, scenario):
     run = subprocess.run([harness, scenario], capture_output=True, text=True, timeout=60)
     assert run.returncode == 0, run.stdout + run.stderr
