@@ -81,12 +81,29 @@ uint32_t g_last_err[4] = {0, 0, 0, 0};
 using WsKey = std::tuple<int, cudaStream_t, unsigned long long>;
 std::map<WsKey, std::shared_ptr<WsEntry>> g_ws[WS_KINDS];
 
-cudaError_t ws_key(int dev, cudaStream_t st, WsKey* key, unsigned long long* id) {
-    const cudaError_t e = cudaStreamGetId(st, id);
-    *key = WsKey(dev, st, st == cudaStreamPerThread ? *id : 0ull);
-    return e;
-}
+// The id is 0 under stream capture, which does not survive the question: the
+// per-thread stream then takes the one that the thread learned before.
+struct StreamState {
+    WsKey key;
+    unsigned long long id = 0;
+    bool capturing = false;
+};
+thread_local unsigned long long t_per_thread[kMaxDevices] = {};
 
+cudaError_t stream_state(int dev, cudaStream_t st, StreamState* out) {
+    cudaStreamCaptureStatus status;
+    cudaError_t e = cudaStreamIsCapturing(st, &status);
+    if (e != cudaSuccess) return e;
+    out->capturing = status != cudaStreamCaptureStatusNone;
+    if (!out->capturing && (e = cudaStreamGetId(st, &out->id)) != cudaSuccess) return e;
+    unsigned long long own = 0;
+    if (st == cudaStreamPerThread) {
+        if (!out->capturing) t_per_thread[dev] = out->id;
+        own = t_per_thread[dev];
+    }
+    out->key = WsKey(dev, st, own);
+    return cudaSuccess;
+}
 
 struct HostStage {
     void* ptr = nullptr;
@@ -284,9 +301,9 @@ mk_status_t host_device(int* dev, int* sms, DevError** err) try {
 }
 
 mk_status_t Workspace::get(WsKind kind, int dev, cudaStream_t st, size_t need, size_t zero_bytes) try {
-    WsKey key;
-    unsigned long long id = 0;
-    if (ws_key(dev, st, &key, &id) != cudaSuccess) return MK_ERR_CUDA;
+    StreamState stream;
+    if (stream_state(dev, st, &stream) != cudaSuccess) return MK_ERR_CUDA;
+    const WsKey& key = stream.key;
     do {  // again when the entry was released meanwhile
         {
             std::lock_guard<std::mutex> lock(g_mu);
@@ -298,21 +315,14 @@ mk_status_t Workspace::get(WsKind kind, int dev, cudaStream_t st, size_t need, s
         lock_ = std::unique_lock<std::mutex>(entry_->mu);
     } while (entry_->dropped);
     WsEntry& w = *entry_;
-    if (w.ptr && w.stream != id) {
+    if (!stream.capturing) {
         // the handle of a stream that is gone: its work may still run on the buffer
-        cudaStreamCaptureStatus capturing;
-        if (cudaStreamIsCapturing(st, &capturing) != cudaSuccess) return MK_ERR_CUDA;
-        if (capturing != cudaStreamCaptureStatusNone) return MK_ERR_WORKSPACE;
-        if (cudaDeviceSynchronize() != cudaSuccess) return MK_ERR_CUDA;
+        if (w.ptr && w.stream != stream.id && cudaDeviceSynchronize() != cudaSuccess) return MK_ERR_CUDA;
+        w.stream = stream.id;
     }
-    w.stream = id;
     if (w.bytes < need) {
-        if (kind == WS_ATTN || kind == WS_FFN) {
-            // memory allocated under stream capture would belong to the graph
-            cudaStreamCaptureStatus capturing;
-            if (cudaStreamIsCapturing(st, &capturing) != cudaSuccess) return MK_ERR_CUDA;
-            if (capturing != cudaStreamCaptureStatusNone) return MK_ERR_WORKSPACE;
-        }
+        // memory allocated under stream capture would belong to the graph
+        if (stream.capturing && (kind == WS_ATTN || kind == WS_FFN)) return MK_ERR_WORKSPACE;
         if (w.ptr && cudaFreeAsync(w.ptr, st) != cudaSuccess) return MK_ERR_CUDA;
         w.ptr = nullptr;
         w.bytes = 0;
@@ -855,12 +865,11 @@ mk_status_t mk_moe_dispatch_gemm_host(const void* x_host, const float* logits_ho
                  o_done = ws_align(o_g + rows * 4), total = ws_align(o_done + size_t(nchunks) * 4);
     uint8_t* base = nullptr;
     HostStage* hs = nullptr;
-    WsKey key;
-    unsigned long long id = 0;
-    if (ws_key(dev, st, &key, &id) != cudaSuccess) return MK_ERR_CUDA;
+    StreamState stream_now;
+    if (stream_state(dev, st, &stream_now) != cudaSuccess) return MK_ERR_CUDA;
     {
         std::lock_guard<std::mutex> lock(g_mu);
-        HostStage& h = g_host_stage[key];
+        HostStage& h = g_host_stage[stream_now.key];
         if (h.bytes < total) {
             if (h.ptr && cudaFreeAsync(h.ptr, st) != cudaSuccess) return MK_ERR_CUDA;
             h.ptr = nullptr;
@@ -972,12 +981,11 @@ mk_status_t mk_read_trace(void* stream, const void* workspace, int T, int H, int
     std::shared_ptr<WsEntry> entry;
     std::unique_lock<std::mutex> held;
     if (!ws) {
-        WsKey key;
-        unsigned long long id = 0;
-        if (ws_key(dev, st, &key, &id) != cudaSuccess) return MK_ERR_CUDA;
+        StreamState now;
+        if (stream_state(dev, st, &now) != cudaSuccess) return MK_ERR_CUDA;
         {
             std::lock_guard<std::mutex> lock(g_mu);
-            auto it = g_ws[WS_DISPATCH].find(key);
+            auto it = g_ws[WS_DISPATCH].find(now.key);
             if (it == g_ws[WS_DISPATCH].end()) return MK_ERR_INVALID_ARG;
             entry = it->second;
         }

@@ -40,6 +40,7 @@ std::map<uintptr_t, size_t> sizes;
 uintptr_t next_ptr = 0x10000000;
 std::map<cudaStream_t, bool> capturing;
 std::map<cudaStream_t, unsigned long long> ids;  // of handles that do not stand for themselves
+bool invalidated = false;                     // a call that a capture does not survive
 thread_local unsigned long long per_thread_id = 0;
 std::atomic<unsigned long long> threads_seen{1000};
 thread_local std::function<void()> on_encode;  // between a call's workspace and its launch
@@ -111,6 +112,7 @@ cudaError_t cudaFree(void* p) {
 }
 cudaError_t cudaDeviceSynchronize() {
     std::lock_guard<std::mutex> l(mu);
+    for (const auto& c : capturing) invalidated = invalidated || c.second;
     log(SYNC, nullptr, nullptr);
     return cudaSuccess;
 }
@@ -121,6 +123,10 @@ cudaError_t cudaStreamIsCapturing(cudaStream_t s, cudaStreamCaptureStatus* c) {
 }
 cudaError_t cudaStreamGetId(cudaStream_t s, unsigned long long* id) {
     std::lock_guard<std::mutex> l(mu);
+    if (is_capturing(s)) {  // the capture is lost with this
+        invalidated = true;
+        return cudaErrorStreamCaptureUnsupported;
+    }
     if (s == cudaStreamPerThread) {
         if (!per_thread_id) per_thread_id = ++threads_seen;
         *id = per_thread_id;
@@ -317,6 +323,18 @@ void recycled_handle() {
     expect_live();
 }
 
+// A captured call takes the buffer of the call before.
+void captured_call(cudaStream_t st) {
+    expect(call(st, 64) == MK_OK, "call before the capture");
+    const uintptr_t first = buffer_of(ops.back().ptr);
+    capturing[st] = true;
+    expect(call(st, 64) == MK_OK, "a captured call");
+    capturing[st] = false;
+    expect(buffer_of(ops.back().ptr) == first && ops.back().captured, "on the same buffer");
+    expect(!invalidated, "the capture survives");
+    expect_live();
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
@@ -326,6 +344,8 @@ int main(int argc, char** argv) {
     else if (name == "release") release_under_a_call();
     else if (name == "per_thread") per_thread();
     else if (name == "recycled_handle") recycled_handle();
+    else if (name == "captured_call") captured_call(stream(4));
+    else if (name == "captured_call_per_thread") captured_call(cudaStreamPerThread);
     else return std::printf("no such scenario\n"), 2;
     std::printf("%s: %zu operations, %d failures\n", name.c_str(), ops.size(), failures);
     return failures ? 1 : 0;

@@ -22,7 +22,8 @@ def harness(tmp_path_factory):
     return exe
 
 
-@pytest.mark.parametrize("scenario", ["growth", "growth_ep", "release", "per_thread", "recycled_handle"])
+@pytest.mark.parametrize("scenario", ["growth", "growth_ep", "release", "per_thread", "recycled_handle",
+                                      "captured_call", "captured_call_per_thread"])
 def test_scenario(harness, scenario):
     run = subprocess.run([harness, scenario], capture_output=True, text=True, timeout=60)
     assert run.returncode == 0, run.stdout + run.stderr
