@@ -156,7 +156,9 @@ mk_status_t mk_moe_dispatch_gemm(const void* x, const float* logits, int T, int 
 
 /* As mk_moe_dispatch_gemm with an explicit configuration (NULL = defaults)
  * and an optional caller workspace.  With workspace == NULL the library's
- * cache is used (grown with cudaMallocAsync on `stream`).  A caller
+ * cache is used (grown with cudaMallocAsync on `stream`; under stream capture
+ * a buffer of the cache that is large enough becomes the captured calls', else
+ * the graph allocates and frees its own).  A caller
  * workspace must hold mk_workspace_size() bytes, be 256-byte aligned, and be
  * zero-filled before its first use (the kernels leave it ready for the next
  * call).  One workspace serves one stream at a time. */
@@ -312,9 +314,10 @@ size_t mk_workspace_size(int T, int H, int F, int E, int k, const mk_config_t* c
  *
  * They can be captured in a CUDA graph.  Under capture the library's
  * workspace cache is not grown (MK_ERR_WORKSPACE): make a call of the same
- * sizes on that stream before.  A captured call keeps the workspace's address,
- * so while the graph lives give its stream no larger call and replay no two
- * graphs of one stream at a time, or capture with a caller workspace. */
+ * sizes on that stream before, and order replays after it.  The buffer that a
+ * captured call uses belongs from then on to the captured calls of its stream
+ * (later calls get another) and stays until mk_release_workspace(): replay no
+ * two graphs of one stream at a time, or capture with a caller workspace. */
 
 /* The residual's addition and the root-mean-square norm, in bf16 and / or in
  * 8 bits.  With z = x + residual (x alone when residual is NULL):
@@ -435,7 +438,8 @@ mk_status_t mk_read_trace(void* stream, const void* workspace, int T, int H, int
                           size_t n);
 
 /* Free the library's workspace cache on every device (synchronises), and
- * forget the device addresses mk_moe_dispatch_gemm_noalloc looked up. */
+ * forget the device addresses mk_moe_dispatch_gemm_noalloc looked up.  Graphs
+ * that hold calls with the library's workspace cannot be replayed after. */
 void mk_release_workspace(void);
 
 /* Static string for a status code. */

@@ -19,7 +19,7 @@
 #include <map>
 #include <mutex>
 #include <tuple>
-#include <utility>
+#include <vector>
 
 #include "mk.h"
 #include "mk_common.h"
@@ -49,6 +49,13 @@ struct WsEntry {
     unsigned long long stream = 0;  // id of the stream that used it last
     void* ptr = nullptr;
     size_t bytes = 0;
+    // Calls under stream capture keep the addresses: the buffer they use leaves
+    // `ptr` for them, is shared by the captured calls of the stream, and once too
+    // small for them is kept beside the next one.
+    void* graph = nullptr;
+    size_t graph_bytes = 0;
+    std::vector<void*> kept;
+    const void* last = nullptr;  // of the last call
 };
 
 }  // namespace mk
@@ -315,14 +322,38 @@ mk_status_t Workspace::get(WsKind kind, int dev, cudaStream_t st, size_t need, s
         lock_ = std::unique_lock<std::mutex>(entry_->mu);
     } while (entry_->dropped);
     WsEntry& w = *entry_;
-    if (!stream.capturing) {
+    if (stream.capturing) {
+        if (w.graph_bytes < need && w.bytes >= need) {
+            if (w.graph) w.kept.push_back(w.graph);
+            w.graph = w.ptr;
+            w.graph_bytes = w.bytes;
+            w.ptr = nullptr;
+            w.bytes = 0;
+        }
+        if (w.graph_bytes >= need) {
+            w.last = ptr_ = static_cast<uint8_t*>(w.graph);
+            return MK_OK;
+        }
+        // memory allocated here is the graph's
+        if (kind == WS_ATTN || kind == WS_FFN) return MK_ERR_WORKSPACE;
+        if (cudaMallocAsync(&own_, need, st) != cudaSuccess) {
+            own_ = nullptr;
+            return MK_ERR_CUDA;
+        }
+        stream_ = st;
+        if (cudaMemsetAsync(own_, 0, kind == WS_DISPATCH ? zero_bytes : need, st) != cudaSuccess) return MK_ERR_CUDA;
+        ptr_ = static_cast<uint8_t*>(own_);
+        return MK_OK;
+    }
+    if (w.stream != stream.id) {
         // the handle of a stream that is gone: its work may still run on the buffer
-        if (w.ptr && w.stream != stream.id && cudaDeviceSynchronize() != cudaSuccess) return MK_ERR_CUDA;
+        if (w.ptr && cudaDeviceSynchronize() != cudaSuccess) return MK_ERR_CUDA;
+        if (w.graph) w.kept.push_back(w.graph);
+        w.graph = nullptr;
+        w.graph_bytes = 0;
         w.stream = stream.id;
     }
     if (w.bytes < need) {
-        // memory allocated under stream capture would belong to the graph
-        if (stream.capturing && (kind == WS_ATTN || kind == WS_FFN)) return MK_ERR_WORKSPACE;
         if (w.ptr && cudaFreeAsync(w.ptr, st) != cudaSuccess) return MK_ERR_CUDA;
         w.ptr = nullptr;
         w.bytes = 0;
@@ -334,10 +365,14 @@ mk_status_t Workspace::get(WsKind kind, int dev, cudaStream_t st, size_t need, s
         if (cudaMemsetAsync(w.ptr, 0, kind == WS_DISPATCH ? zero_bytes : grow, st) != cudaSuccess) return MK_ERR_CUDA;
         w.bytes = grow;
     }
-    ptr_ = static_cast<uint8_t*>(w.ptr);
+    w.last = ptr_ = static_cast<uint8_t*>(w.ptr);
     return MK_OK;
 } catch (...) {  // no memory for the cache's own entry
     return MK_ERR_WORKSPACE;
+}
+
+Workspace::~Workspace() {
+    if (own_) cudaFreeAsync(own_, stream_);  // after the launch, in the graph
 }
 
 CUresult host_encode_2d(CUtensorMap* m, CUtensorMapDataType type, const void* base, uint64_t inner, uint64_t outer,
@@ -990,7 +1025,7 @@ mk_status_t mk_read_trace(void* stream, const void* workspace, int T, int H, int
             entry = it->second;
         }
         held = std::unique_lock<std::mutex>(entry->mu);
-        ws = static_cast<const uint8_t*>(entry->ptr);
+        ws = static_cast<const uint8_t*>(entry->last);
         if (!ws) return MK_ERR_INVALID_ARG;
     }
     const WsLayout L = ws_layout(T, H, E, k);
@@ -1013,13 +1048,14 @@ void mk_release_workspace(void) {
         }
         for (auto& kv : mine) {
             std::lock_guard<std::mutex> held(kv.second->mu);  // a call that has it enqueues its work first
-            kv.second->dropped = true;
-            if (!kv.second->ptr) continue;
+            WsEntry& w = *kv.second;
+            w.dropped = true;
+            if (!w.ptr && !w.graph && w.kept.empty()) continue;
             cudaSetDevice(std::get<0>(kv.first));
             cudaDeviceSynchronize();
-            cudaFree(kv.second->ptr);
-            kv.second->ptr = nullptr;
-            kv.second->bytes = 0;
+            if (w.ptr) cudaFree(w.ptr);
+            if (w.graph) cudaFree(w.graph);
+            for (void* p : w.kept) cudaFree(p);
         }
     }
     std::lock_guard<std::mutex> lock(g_mu);

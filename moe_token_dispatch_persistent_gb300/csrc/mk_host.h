@@ -38,10 +38,17 @@ enum WsKind { WS_DISPATCH = 0, WS_EP = 1, WS_ATTN = 2, WS_FFN = 3, WS_KINDS = 4 
 // `st`.  Of a new buffer the first `zero_bytes` are zeroed (WS_DISPATCH) or all
 // of it (the others, whose counters move with the sizes).  The object holds the
 // buffer: keep it until the call's work is enqueued, so that no other thread's
-// call frees what this one is about to use.
+// call frees what this one is about to use.  A call under stream capture gets
+// what an earlier call on the stream left, which is then the captured calls'
+// alone; without that, memory of the graph (WS_DISPATCH, WS_EP) or
+// MK_ERR_WORKSPACE (the others).
 struct WsEntry;
 class Workspace {
   public:
+    Workspace() = default;
+    Workspace(const Workspace&) = delete;
+    Workspace& operator=(const Workspace&) = delete;
+    ~Workspace();
     mk_status_t get(WsKind kind, int dev, cudaStream_t st, size_t need, size_t zero_bytes);
     uint8_t* data() const { return ptr_; }
 
@@ -49,6 +56,8 @@ class Workspace {
     std::shared_ptr<WsEntry> entry_;
     std::unique_lock<std::mutex> lock_;  // of the entry
     uint8_t* ptr_ = nullptr;
+    void* own_ = nullptr;                // memory of the graph that the call is captured in
+    cudaStream_t stream_ = nullptr;
 };
 
 // A 2-D tensor map in the 128-byte swizzle (out-of-range reads give zeros).

@@ -16,6 +16,7 @@
 #include <mutex>
 #include <string>
 #include <thread>
+#include <utility>
 #include <vector>
 
 #include "mk.h"
@@ -335,6 +336,70 @@ void captured_call(cudaStream_t st) {
     expect_live();
 }
 
+// What a captured call uses is the graph's: no later call frees it or works in it.
+void capture_keeps(mk_status_t (*one)(cudaStream_t, int)) {
+    const cudaStream_t st = stream(1);
+    auto captured = [&](int T) {
+        capturing[st] = true;
+        expect(one(st, T) == MK_OK, "a captured call");
+        capturing[st] = false;
+        return buffer_of(ops.back().ptr);
+    };
+    expect(one(st, 64) == MK_OK, "call before the capture");
+    const uintptr_t graph = captured(64);
+    expect(one(st, 64) == MK_OK, "the same call afterwards");
+    expect(buffer_of(ops.back().ptr) != graph, "works in another buffer");
+    expect(one(st, 4096) == MK_OK, "a larger one");
+    const uintptr_t second = captured(4096);
+    expect(one(st, 4096) == MK_OK, "the larger one afterwards");
+    expect(buffer_of(ops.back().ptr) != second, "works in another buffer");
+    expect(captured(64) == second, "smaller calls share what captured calls of the stream have");
+    ids[st] = 99;  // another stream with that handle
+    expect(one(st, 64) == MK_OK, "the other stream's call");
+    for (const Op& o : ops) expect(o.what != FREE || (o.ptr != graph && o.ptr != second), "a graph's buffer stays");
+    for (const Op& o : ops) expect(!o.captured || o.what == LAUNCH, "nothing but launches is captured");
+    mk_release_workspace();
+    int freed = 0;
+    for (const Op& o : ops) freed += o.what == FREE && (o.ptr == graph || o.ptr == second);
+    expect(freed == 2, "until everything is released");
+    expect(!invalidated, "the captures survive");
+    expect_live();
+}
+
+// Without an earlier call on the stream the memory is the graph's own.
+void capture_alone() {
+    const cudaStream_t st = stream(2);
+    capturing[st] = true;
+    expect(call(st, 64) == MK_OK, "a captured call");
+    capturing[st] = false;
+    expect(ops.size() == 4 && ops[0].what == ALLOC && ops[1].what == ZERO && ops[2].what == LAUNCH &&
+               ops[3].what == FREE && ops[3].ptr == ops[0].ptr,
+           "allocated, zeroed, used and freed in the graph");
+    const uintptr_t graph = ops[0].ptr;
+    expect(call(st, 64) == MK_OK, "a call afterwards");
+    expect(buffer_of(ops.back().ptr) != graph, "works in another buffer");
+    expect_live();
+}
+
+// The operators of a decode step refuse that.
+void capture_refused() {
+    const cudaStream_t st = stream(2);
+    auto get = [&](size_t need) {
+        mk::Workspace w;
+        const mk_status_t s = w.get(mk::WS_FFN, 0, st, need, need);
+        expect((s == MK_OK) == (w.data() != nullptr), "a buffer with MK_OK");
+        return s;
+    };
+    capturing[st] = true;
+    expect(get(1000) == MK_ERR_WORKSPACE, "no buffer yet");
+    capturing[st] = false;
+    expect(get(1000) == MK_OK, "a call");
+    capturing[st] = true;
+    expect(get(1000) == MK_OK, "its buffer");
+    expect(get(100000) == MK_ERR_WORKSPACE, "too small");
+    for (const Op& o : ops) expect(!o.captured, "nothing is captured");
+}
+
 }  // namespace
 
 int main(int argc, char** argv) {
@@ -346,6 +411,10 @@ int main(int argc, char** argv) {
     else if (name == "recycled_handle") recycled_handle();
     else if (name == "captured_call") captured_call(stream(4));
     else if (name == "captured_call_per_thread") captured_call(cudaStreamPerThread);
+    else if (name == "capture_keeps") capture_keeps(call);
+    else if (name == "capture_keeps_ep") capture_keeps(call_ep);
+    else if (name == "capture_alone") capture_alone();
+    else if (name == "capture_refused") capture_refused();
     else return std::printf("no such scenario\n"), 2;
     std::printf("%s: %zu operations, %d failures\n", name.c_str(), ops.size(), failures);
     return failures ? 1 : 0;

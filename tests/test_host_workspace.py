@@ -23,7 +23,8 @@ def harness(tmp_path_factory):
 
 
 @pytest.mark.parametrize("scenario", ["growth", "growth_ep", "release", "per_thread", "recycled_handle",
-                                      "captured_call", "captured_call_per_thread"])
+                                      "captured_call", "captured_call_per_thread", "capture_keeps",
+                                      "capture_keeps_ep", "capture_alone", "capture_refused"])
 def test_scenario(harness, scenario):
     run = subprocess.run([harness, scenario], capture_output=True, text=True, timeout=60)
     assert run.returncode == 0, run.stdout + run.stderr
