@@ -763,16 +763,17 @@ __device__ void complete_h(const FfnParams& p, FfnSmem* sm, const Plan& pl, cons
         else
             for (int i = me_now; i < s.n; i += FIN_WARPS) complete_rows<FP8, 1, 4>(p, pl, s, i);
         fence_proxy_async();
-        bool publish;  // the warp that had all the rows does, or the last of them
-        if (s.n <= rows) {
-            publish = me_now == 0;
-            __syncwarp();
-        } else {
-            __threadfence();
-            __syncwarp();
-            publish = lane == 0 && atomicSub(&sm->job_left[in.i], 1u) == 1u;
-        }
+        __syncwarp();
         if (lane == 0) {
+            // The warp that had all the rows publishes, or the last of them, which has
+            // then seen the other warps' rows: fences around the count, and the release
+            // below covers what this thread has seen.
+            bool publish = me_now == 0;
+            if (s.n > rows) {
+                __threadfence_block();
+                publish = atomicSub(&sm->job_left[in.i], 1u) == 1u;
+                __threadfence_block();
+            }
             if (publish) atom_add_acq_rel_u32(&p.ctl->ready[s.a], 1u);  // releases the rows
             mbar_arrive(&sm->job_out[in.i]);
         }
