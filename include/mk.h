@@ -383,7 +383,8 @@ enum { MK_WEIGHT_BF16 = 0, MK_WEIGHT_E4M3 = 1 };
 /* The whole gated expert layer for a few tokens (a decode step), in one
  * kernel: routing and gates as points 1 and 2 above, then
  *   h(t,j) = silu(x[t,:] . W1[e]) * (x[t,:] . W3[e])  for the j-th expert e,
- *   out[t,:] = sum_j gate[t,j] * (h(t,j) . W2[e]),  j in order.
+ *   out[t,:] = sum_j gate[t,j] * (h(t,j) . W2[e]),  j in order, without the
+ *   experts whose logit is -inf: their weights are not read.
  * With MK_WEIGHT_BF16, x and the weights are bf16 and the scale pointers
  * NULL; h is carried with 16 significant bits (infinite beyond the range of
  * bf16).  With MK_WEIGHT_E4M3 they are

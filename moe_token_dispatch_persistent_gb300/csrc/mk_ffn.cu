@@ -1,7 +1,8 @@
 // mk_ffn.cu -- mk_moe_ffn_decode: the whole gated expert layer for a few
 // tokens in one persistent kernel.
 //
-//   experts of token t: the k largest logits; gates: softmax over them
+//   experts of token t: the k largest logits; gates: softmax over them (an
+//   expert whose logit is -inf is left out)
 //   h = silu(x . W1[e]) * (x . W3[e]),   out[t] = sum_j gate_j h . W2[e_j]
 //
 // For a few tokens the chosen experts' weights are all the traffic, each used
@@ -164,11 +165,16 @@ struct FfnSmem {
     uint8_t expert[MAX_PARTS];     // its expert
     uint8_t count[MAX_PARTS];      // and its rows
     uint8_t row_token[FFN_MAX_ROWS];
-    uint16_t row_of[FFN_MAX_ROWS]; // per (token, choice): its row
-    float gate[FFN_MAX_ROWS];      // and its gate
+    uint16_t row_of[FFN_MAX_ROWS]; // per (token, choice): its row or NO_ROW
+    float gate[FFN_MAX_ROWS];      // and its gate or MASKED
 };
 constexpr int FFN_SMEM = RING_BYTES + int(sizeof(FfnSmem)) + 1024;
 static_assert(FFN_SMEM <= 232448, "dynamic shared memory of one CTA on sm_103");
+
+// The gate of a chosen expert whose logit is -inf, which gets no row: its
+// weights are not read, and nothing that they hold reaches the output.
+constexpr float MASKED = -1.f;
+constexpr uint16_t NO_ROW = 0xffff;
 
 // Routing scratch, in the ring before the first load.
 constexpr int RS_IDS = 0, RS_MASK = FFN_MAX_ROWS, RS_FIRST = RS_MASK + MAX_E * (FFN_MAX_T / 8);
@@ -259,7 +265,7 @@ __device__ __forceinline__ float unordered(uint32_t u) {
 }
 
 // One token by one warp: the k largest logits in descending order, ties to
-// the lower expert, and the softmax over them (0 where the logit is -inf).
+// the lower expert, and the softmax over them (MASKED where the logit is -inf).
 __device__ void route_token(const FfnParams& p, int t, uint8_t* ids, float* gates) {
     const int lane = threadIdx.x & 31;
     const float* row = p.logits + size_t(t) * p.E;
@@ -293,7 +299,7 @@ __device__ void route_token(const FfnParams& p, int t, uint8_t* ids, float* gate
     for (int j = 0; j < p.k; ++j) sum += __shfl_sync(0xffffffffu, w, j);
     if (lane < p.k) {
         ids[t * p.k + lane] = uint8_t(id);
-        gates[t * p.k + lane] = sum > 0.f ? w / sum : 0.f;
+        gates[t * p.k + lane] = value == -INFINITY ? MASKED : sum > 0.f ? w / sum : 0.f;
     }
 }
 
@@ -311,6 +317,7 @@ __device__ void build_rows(const FfnParams& p, FfnSmem* sm, uint8_t* scratch) {
     if (tid == 0) sm->most = 0;
     __syncthreads();
     for (int i = tid; i < rows; i += FFN_THREADS) {
+        if (sm->gate[i] == MASKED) continue;
         const int t = i / p.k;
         atomicOr(&mask[ids[i] * WORDS + (t >> 5)], 1u << (t & 31));
     }
@@ -349,6 +356,10 @@ __device__ void build_rows(const FfnParams& p, FfnSmem* sm, uint8_t* scratch) {
     }
     __syncthreads();
     for (int i = tid; i < rows; i += FFN_THREADS) {
+        if (sm->gate[i] == MASKED) {
+            sm->row_of[i] = NO_ROW;
+            continue;
+        }
         const int t = i / p.k, e = ids[i];
         int before = 0;
         for (int w = 0; w < (t >> 5); ++w) before += __popc(mask[e * WORDS + w]);
@@ -933,9 +944,10 @@ __device__ void combine_rows(const FfnParams& p, const FfnSmem* sm, const Plan& 
     const int chunks = int(pl.chunks[1]), all = p.k * chunks;  // pieces of a token, choice by choice
     // piece i of token t at column col, and its gate
     auto load = [&](int t, int i, int col, float& g) {
-        const int j = i / chunks, c = i - j * chunks;
+        const int j = i / chunks, c = i - j * chunks, row = sm->row_of[t * p.k + j];
+        if (row == NO_ROW) return make_float4(0.f, 0.f, 0.f, 0.f);
         g = sm->gate[t * p.k + j];
-        return __ldcg(reinterpret_cast<const float4*>(piece_row(p, pl, 1, uint32_t(c), sm->row_of[t * p.k + j]) + col));
+        return __ldcg(reinterpret_cast<const float4*>(piece_row(p, pl, 1, uint32_t(c), row) + col));
     };
     const int nb128 = (p.H + 127) / 128;
     constexpr int TOGETHER = 8;  // loads in flight
@@ -1078,7 +1090,7 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
 
         const Plan pl = make_plan(p, FP8 ? 128 : 64, uint32_t(sm->parts), uint32_t(sm->most));
         Accs rg;
-        const int N = pad16(sm->most);
+        const int N = pad16(max(sm->most, 1));  // no rows at all: every logit is -inf
         rg.acc_stride = uint32_t(N * (FP8 ? 1 : 2));
         rg.bufs = min(uint32_t(FFN_MAX_BUFS), 512u / (2u * rg.acc_stride));
 

@@ -1,5 +1,5 @@
 """mk_moe_ffn_decode at the edges of its own plan: blocks of h that several warps
-complete.  Layers, reference and tolerances are those of
+complete, experts that are chosen but masked.  Layers, reference and tolerances are those of
 test_gpu_ffn_decode.py."""
 import pytest
 
@@ -31,3 +31,36 @@ def test_rows_completed_by_several_warps_are_seen(T, H, F, E, k, fp8):
     assert mk.mk_get_status() == mk.MK_OK
     layer.check(outs[0])
     assert all(torch.equal(o, outs[0]) for o in outs)
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("T,H,F", [(1, 1024, 1024), (5, 256, 384), (40, 256, 384), (128, 256, 256)])
+def test_masked_experts_are_not_used(T, H, F, fp8):
+    # fewer live experts than k: the others' weights may hold anything
+    gen = torch.Generator().manual_seed(T)
+    E, k, live = 12, 4, [3, 7, 8]
+    logits = torch.full((T, E), -float("inf"))
+    logits[:, live] = torch.randn((T, len(live)), generator=gen)
+    if T > 1:
+        logits[1] = -float("inf")          # no expert at all
+        logits[2, [3, 7]] = -float("inf")  # one
+    logits[0, 8] = -200.0                  # a gate that is 0 in 32 bits, of an expert that is used
+    layer = Layer(T, H, F, E, k, fp8, seed=T, logits=logits)
+    want = layer.run()
+    layer.check(want)
+    dead = [e for e in range(E) if e not in live]
+    for w in (layer.W1, layer.W3, layer.W2):
+        w.view(torch.uint8)[dead] = 0x7f if fp8 else 0xff  # NaN
+    out = layer.run()
+    assert torch.equal(out, want)
+    if T > 1:
+        assert torch.all(out[1] == 0)
+
+
+@pytest.mark.parametrize("T", [1, 9, 100])
+def test_every_expert_masked(T):
+    layer = Layer(T, 256, 320, 8, 2, seed=1, logits=torch.full((T, 8), -float("inf")))
+    for w in (layer.W1, layer.W3, layer.W2):
+        w.fill_(float("nan"))
+    for _ in range(3):
+        assert torch.all(layer.run() == 0)
