@@ -360,8 +360,10 @@ mk_status_t mk_add_rmsnorm(const void* x, int64_t x_stride, const void* residual
  * Limits: D = 64, 128 or 256; Hq a multiple of Hkv; any page_size >= 1;
  * B <= 4096; max_pages*page_size <= 2^31 - 32, and fewer than 2^31 tiles of
  * 16 keys and 16 query heads in all; strides non-negative multiples of 8
- * elements, caches 16-byte aligned, out 8, q 4 (q_stride even).  Keys and
- * values that are read are finite.  The lengths and pages are checked on the
+ * elements, caches 16-byte aligned, out 8, q 4 (q_stride even).  Infinite
+ * values give infinite outputs (one whose weight is below 2^-100 of the
+ * largest may give NaN); a score that is NaN or +inf makes its head's out and
+ * lse NaN.  The lengths and pages are checked on the
  * device: a length outside [0, max_pages*page_size] is clamped, a page
  * outside [0, num_pages) is not read (its keys count as zeros), and either is
  * reported by mk_get_status() as MK_ERR_DEVICE_FAULT.

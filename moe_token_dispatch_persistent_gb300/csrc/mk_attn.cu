@@ -165,6 +165,19 @@ __device__ __forceinline__ float exp2_of(float x) {
     return r;
 }
 
+// Two weights as the sum of two bf16 values each: 16 significant bits reach the
+// products (the sum of the weights is of all 24).  The first is the weight cut
+// off; the second, what remains and 2^-23 of the weight, is above 0 for every
+// weight above 2^-110, so both products with an infinite value are infinite, of
+// its sign (rounded to nearest, the remainder may be 0 or negative, and the sum
+// of the products NaN).
+__device__ __forceinline__ void split_weights(float p0, float p1, uint32_t& hi, uint32_t& lo) {
+    const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
+    constexpr float ABOVE = 1.f + 1.1920928955078125e-7f;
+    hi = __byte_perm(u0, u1, 0x7632);
+    lo = pack_bf16(fmaf(p0, ABOVE, -__uint_as_float(u0 & 0xffff0000u)), fmaf(p1, ABOVE, -__uint_as_float(u1 & 0xffff0000u)));
+}
+
 // Tiles [t0, t1) of group g of sequence b.  In the order of positions that is
 // cut into ranges, EXTRA positions stand before a group's first tile.
 struct Range {
@@ -609,13 +622,8 @@ __global__ void __launch_bounds__(Geo<D, R>::THREADS, 1) mk_paged_attention_kern
                     const float p2 = exp2_of(sn[2] - b1), p3 = exp2_of(sn[3] - b1);
                     l0 += p0 + p1;
                     l1 += p2 + p3;
-                    // each weight as the sum of two bf16 values: 16 significant bits reach the products
-                    hi[2 * n] = pack_bf16(p0, p1);
-                    hi[2 * n + 1] = pack_bf16(p2, p3);
-                    lo[2 * n] = pack_bf16(p0 - __uint_as_float(hi[2 * n] << 16),
-                                          p1 - __uint_as_float(hi[2 * n] & 0xffff0000u));
-                    lo[2 * n + 1] = pack_bf16(p2 - __uint_as_float(hi[2 * n + 1] << 16),
-                                              p3 - __uint_as_float(hi[2 * n + 1] & 0xffff0000u));
+                    split_weights(p0, p1, hi[2 * n], lo[2 * n]);
+                    split_weights(p2, p3, hi[2 * n + 1], lo[2 * n + 1]);
                 }
                 const int row = kk * 16 + (((lane >> 3) & 1) << 3) + (lane & 7), half = lane >> 4;
                 const uint32_t rb = vs + uint32_t(row * G::COLS * 2);
