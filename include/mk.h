@@ -388,8 +388,7 @@ enum { MK_WEIGHT_BF16 = 0, MK_WEIGHT_E4M3 = 1 };
  *   out[t,:] = sum_j gate[t,j] * (h(t,j) . W2[e]),  j in order, without the
  *   experts whose logit is -inf: their weights are not read.
  * With MK_WEIGHT_BF16, x and the weights are bf16 and the scale pointers
- * NULL; h is carried with 16 significant bits (infinite beyond the range of
- * bf16).  With MK_WEIGHT_E4M3 they are
+ * NULL; h is carried with 16 significant bits.  With MK_WEIGHT_E4M3 they are
  * e4m3 with scales: a weight stands for its value times the scale of its
  * 128 x 128 block, x[t,c] for its value times x_scale[t, c/128] (what
  * mk_add_rmsnorm writes); h is rounded to e4m3 likewise, per row and 128

@@ -614,6 +614,20 @@ __device__ void products(FfnSmem* sm, const Accs& accs, const Waiter& w) {
     __syncwarp();
 }
 
+// Two values of h as the sum of two bf16 values each: the value cut off, and
+// what remains with 2^-23 of the value, so that both have its sign and their
+// products with an infinite weight are one infinity (rounded to nearest, the
+// remainder may be 0 or of the other sign, and the sum NaN).  Of an infinite or
+// NaN value both are that.
+__device__ __forceinline__ void split_pair(float h0, float h1, uint32_t& hi, uint32_t& lo) {
+    const float c0 = __uint_as_float(__float_as_uint(h0) & 0xffff0000u), c1 = __uint_as_float(__float_as_uint(h1) & 0xffff0000u);
+    constexpr float ABOVE = 1.1920928955078125e-7f;
+    const float r0 = fabsf(h0) < INFINITY ? fmaf(h0, ABOVE, h0 - c0) : h0, r1 = fabsf(h1) < INFINITY ? fmaf(h1, ABOVE, h1 - c1) : h1;
+    hi = __byte_perm(__float_as_uint(h0), __float_as_uint(h1), 0x7632);
+    const __nv_bfloat162 l = __floats2bfloat162_rn(r0, r1);
+    lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+
 // ROWS rows from i0 on of a block of 256 columns of a part's h, from their
 // pieces, by one warp: eight columns per lane.  BATCH pieces of each matrix are
 // loaded together.
@@ -684,15 +698,7 @@ __device__ __forceinline__ void complete_rows(const FfnParams& p, const Plan& pl
             } else if (in) {
                 uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(h[2 * i], h[2 * i + 1]);
-                    const float b0 = __low2float(b), b1 = __high2float(b);
-                    // nothing remains of an infinite value (inf - inf would be NaN)
-                    const __nv_bfloat162 l = __floats2bfloat162_rn(fabsf(b0) == INFINITY ? 0.f : h[2 * i] - b0,
-                                                                   fabsf(b1) == INFINITY ? 0.f : h[2 * i + 1] - b1);
-                    hi[i] = *reinterpret_cast<const uint32_t*>(&b);
-                    lo[i] = *reinterpret_cast<const uint32_t*>(&l);
-                }
+                for (int i = 0; i < 4; ++i) split_pair(h[2 * i], h[2 * i + 1], hi[i], lo[i]);
                 *reinterpret_cast<uint4*>(p.h + at * 2) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                 *reinterpret_cast<uint4*>(p.h + (R * p.F + at) * 2) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
             }

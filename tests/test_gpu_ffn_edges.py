@@ -64,3 +64,39 @@ def test_every_expert_masked(T):
         w.fill_(float("nan"))
     for _ in range(3):
         assert torch.all(layer.run() == 0)
+
+
+@pytest.mark.parametrize("T", [3, 40])
+def test_infinite_weights_of_the_second_half(T):
+    # h enters the product in two parts: both have its sign
+    layer = Layer(T, 256, 320, 1, 1, seed=T)
+    want = layer.run()
+    x = layer.x.double()
+    a = x @ layer.W1[0].double()
+    h = a * torch.sigmoid(a) * (x @ layer.W3[0].double())
+    layer.W2[0, 37, 100], layer.W2[0, 250, 9], layer.W2[0, 11, 200] = float("inf"), -float("inf"), float("nan")
+    out = layer.run()
+    rest = [c for c in range(256) if c not in (100, 9, 200)]
+    assert torch.equal(out[:, rest], want[:, rest])
+    assert torch.equal(out[:, 100].double(), torch.sign(h[:, 37]) * float("inf"))
+    assert torch.equal(out[:, 9].double(), torch.sign(h[:, 250]) * -float("inf"))
+    assert torch.all(torch.isnan(out[:, 200]))
+
+
+def test_hidden_values_next_to_the_largest():
+    # h between the largest bf16 and the largest 32-bit value is finite, and times a small weight so is the output
+    layer = Layer(2, 64, 64, 1, 1, seed=3)
+    for w in (layer.W1, layer.W3, layer.W2):
+        w.zero_()
+    layer.x.zero_()
+    layer.x[:, 0] = 1.0
+    layer.x[:, 1] = 2.0 ** -9
+    big = 2.0 ** 65 * (2 - 2.0 ** -7)
+    layer.W1[0, 0, 5], layer.W1[0, 1, 5] = big, 2.0 ** 65 * 2.5
+    layer.W3[0, 0, 5] = 2.0 ** 62
+    layer.W2[0, 5, 7] = 2.0 ** -100
+    h = (big + 2.0 ** -9 * 2.0 ** 65 * 2.5) * 2.0 ** 62
+    assert (2 - 2.0 ** -8) * 2.0 ** 127 < h < (2 - 2.0 ** -23) * 2.0 ** 127  # nearest in bf16 is infinity
+    out = layer.run().double()
+    assert torch.all((out[:, 7] - h * 2.0 ** -100).abs() <= 2.0 ** -8 * h * 2.0 ** -100)
+    assert torch.all(out[:, [c for c in range(64) if c != 7]] == 0)
