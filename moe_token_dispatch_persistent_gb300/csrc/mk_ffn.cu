@@ -674,8 +674,12 @@ __device__ __forceinline__ void complete_rows(const FfnParams& p, const Plan& pl
         for (int r = 0; r < ROWS; ++r) {
             if (i0 + r >= s.n) break;
             float* h = v[0][r];
+            // SwiGLU.  The fast exponential is off by 2^-17 of it where a is -88 and far
+            // less where the gate is open.  The fast division gives 0 where a
+            // denominator lies above 2^126, so a quarter of both is divided.
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h[i] = __fdividef(h[i], 1.f + __expf(-h[i])) * v[1][r][i];
+            for (int i = 0; i < 8; ++i)
+                h[i] = __fdividef(0.25f * h[i], fmaf(0.25f, __expf(-h[i]), 0.25f)) * v[1][r][i];
             const int row = s.off + i0 + r;
             const size_t at = size_t(row) * p.F + col;
             if constexpr (FP8) {

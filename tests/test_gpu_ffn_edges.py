@@ -1,6 +1,8 @@
 """mk_moe_ffn_decode at the edges of its own plan: blocks of h that several warps
 complete, experts that are chosen but masked.  Layers, reference and tolerances are those of
 test_gpu_ffn_decode.py."""
+import math
+
 import pytest
 
 import moe_token_dispatch_persistent_gb300 as mk
@@ -100,3 +102,24 @@ def test_hidden_values_next_to_the_largest():
     out = layer.run().double()
     assert torch.all((out[:, 7] - h * 2.0 ** -100).abs() <= 2.0 ** -8 * h * 2.0 ** -100)
     assert torch.all(out[:, [c for c in range(64) if c != 7]] == 0)
+
+
+@pytest.mark.parametrize("a", [-88.0, -80.0, -20.0])
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_large_denominators_of_the_gate(fp8, a):
+    # 1 + e^-a is up to 2^127: silu(a) is tiny, its product with a large second factor is not
+    layer = Layer(3, 128, 128, 1, 1, fp8, seed=5)
+    layer.x, layer.W1, layer.W3, layer.W2 = (torch.zeros(s, device="cuda") for s in ((3, 128), *[(1, 128, 128)] * 3))
+    layer.x[:, 0] = 1.0
+    layer.W1[0, 0, 0], layer.W3[0, 0, 0], layer.W2[0, 0, 0] = 2 * a, 1.0, 1.0
+    scale = {"W1": 0.5, "W3": 2.0 ** 120, "W2": 1.0}
+    for n, s in scale.items():
+        w = getattr(layer, n)
+        setattr(layer, n, w.to(torch.float8_e4m3fn) if fp8 else (w * s).bfloat16())
+        layer.scales[n + "_scale"] = torch.full((1, 1, 1), s, device="cuda")
+    layer.x = layer.x.to(torch.float8_e4m3fn) if fp8 else layer.x.bfloat16()
+    layer.scales = {**layer.scales, "x_scale": torch.ones(3, 1, device="cuda")} if fp8 else {}
+    h = a / (1 + math.exp(-a)) * 2.0 ** 120
+    out = layer.run()[:, 0].double()
+    # the largest h of its group is 448 in 8 bits: its e4m3 value is exact up to the scale's own rounding
+    assert torch.all((out - h).abs() <= (2.0 ** -8 + 2.0 ** -14) * abs(h))
