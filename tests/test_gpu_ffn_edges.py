@@ -123,3 +123,22 @@ def test_large_denominators_of_the_gate(fp8, a):
     out = layer.run()[:, 0].double()
     # the largest h of its group is 448 in 8 bits: its e4m3 value is exact up to the scale's own rounding
     assert torch.all((out - h).abs() <= (2.0 ** -8 + 2.0 ** -14) * abs(h))
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("T", [14, 15, 16, 17])
+def test_every_cta_routes_or_they_share(T, fp8):
+    # a CTA has 15 warps: up to 15 tokens each routes all of them, with more they divide them
+    layer = Layer(T, 256, 384, 9, 3, fp8, seed=T)
+    layer.check(layer.run())
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+@pytest.mark.parametrize("rows", [1, 3, 4, 5, 16, 17, 48, 49, 63, 64, 65, 68, 127, 128])
+def test_rows_of_an_expert(rows, fp8):
+    # 64 rows are multiplied together, an expert with more is taken in parts; rows are loaded in fours and single ones
+    T = max(rows, 70)
+    logits = torch.zeros((T, 5))
+    logits[:rows, 2], logits[rows:, 4] = 3.0, 3.0
+    layer = Layer(T, 256, 384, 5, 1, fp8, seed=rows, logits=logits)
+    layer.check(layer.run())
