@@ -1025,8 +1025,8 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
     FfnSmem* sm = reinterpret_cast<FfnSmem*>(ring + RING_BYTES);
     const int tid = threadIdx.x, warp = tid >> 5;
     const Waiter w{p.err, &p.ctl->abort, FFN_SPIN_NS};
-    // waits inside the pipeline stall because something upstream does: they
-    // get longer, so that the one that is recorded is the one at the root
+    // waits inside the pipeline and for the other CTAs' ends stall because something
+    // upstream does: they get longer, so that the one that is recorded is the one at the root
     const Waiter wp{p.err, &p.ctl->abort, 2 * FFN_SPIN_NS};
 
     if (tid == 0) {
@@ -1115,7 +1115,7 @@ __global__ void __launch_bounds__(FFN_THREADS, 1)
         if (tid == 0) {
             // releases what the whole CTA has stored
             atom_add_acq_rel_u32(&p.ctl->done, 1u);
-            sm->ok = await_geq(&p.ctl->done, gridDim.x, w, SITE_BAR_COMPUTED) && ld_relaxed_u32(w.abort) == 0u;
+            sm->ok = await_geq(&p.ctl->done, gridDim.x, wp, SITE_BAR_COMPUTED) && ld_relaxed_u32(w.abort) == 0u;
         }
         __syncthreads();
         if (sm->ok) combine_rows(p, sm, pl);

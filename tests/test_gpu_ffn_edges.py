@@ -142,3 +142,23 @@ def test_rows_of_an_expert(rows, fp8):
     logits[:rows, 2], logits[rows:, 4] = 3.0, 3.0
     layer = Layer(T, 256, 384, 5, 1, fp8, seed=rows, logits=logits)
     layer.check(layer.run())
+
+
+@pytest.mark.parametrize("fp8", [False, True], ids=["bf16", "e4m3"])
+def test_a_wait_that_runs_out_is_reported_and_leaves_the_workspace_ready(fp8):
+    # a count of pieces that is never reached: the first block of h is not published, the
+    # products of W2 wait for it within their limit (2 s) and every warp of every CTA ends
+    layer = Layer(20, 512, 1024, 8, 2, fp8, seed=1)
+    want = layer.run()
+    bytes_ = mk.mk_moe_ffn_decode_workspace_size(20, 512, 1024, 8, 2, mk.MK_WEIGHT_E4M3 if fp8 else mk.MK_WEIGHT_BF16)
+    ws = torch.zeros(bytes_ // 4, dtype=torch.int32, device="cuda")
+    first_count = 64 + 256 + 1024 // 64  # after the control words and the parts' counters
+    ws[first_count] = 1000
+    layer.run(workspace=ws, ws_bytes=bytes_, check=False)
+    assert mk.mk_get_status() == mk.MK_ERR_TIMEOUT
+    assert mk.mk_last_error_detail()["site"] == 4  # waiting for a part's h
+    assert mk.mk_get_status() == mk.MK_OK  # reading the status cleared it
+    assert not torch.any(ws[:first_count + 4096])  # every counter is 0 again
+    for _ in range(2):
+        assert torch.equal(layer.run(workspace=ws, ws_bytes=bytes_), want)
+    layer.check(want)
