@@ -400,7 +400,8 @@ enum { MK_WEIGHT_BF16 = 0, MK_WEIGHT_E4M3 = 1 };
  *   out[T,H] bf16, overlapping no input                           -- written
  * Limits: 0 <= T <= 128, 1 <= k <= min(E, 8), E <= 256, H and F multiples of
  * 64 (bf16) or 128 (e4m3) up to 32768; x, weights and out 16-byte aligned,
- * f32 arrays 4.  Only the chosen experts' weights are read, each once.
+ * f32 arrays 4.  Only the chosen experts' weights are read: once for
+ * every 64 rows (or fewer) that choose the expert.
  * workspace: NULL (library cache) or mk_moe_ffn_decode_workspace_size()
  * bytes, 256-byte aligned, zero-filled before its first use and used by this
  * entry point only (with any sizes); one stream at a time.  The kernel's CTAs

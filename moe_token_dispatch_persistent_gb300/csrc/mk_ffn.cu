@@ -6,10 +6,11 @@
 //   h = silu(x . W1[e]) * (x . W3[e]),   out[t] = sum_j gate_j h . W2[e_j]
 //
 // For a few tokens the chosen experts' weights are all the traffic, each used
-// for the few rows routed to its expert, so the kernel is a stream of
-// weights.  One step is 32 KiB of them, 256 columns wide; a unit of work is a
-// few consecutive steps of one block of columns: first the units of W1 and W3
-// of every chosen expert, then those of W2, taken in order from one counter.
+// for the few rows routed to its expert, so the kernel is a stream of weights
+// (read once for up to 64 rows of an expert, twice for one with 65 to 128).
+// One step is 32 KiB of them, 256 columns wide; a unit of work is a few
+// consecutive steps of one block of columns: first the units of W1 and W3 of
+// every chosen expert, then those of W2, taken in order from one counter.
 // SMs that read slower take fewer, and by the time the first expert's W2 is
 // reached its h has long been complete, unless it is the only one.
 //
@@ -423,7 +424,7 @@ __device__ void weight_loads(const FfnParams& p, const FfnMaps& m, FfnSmem* sm, 
     constexpr int BOX = KB * 128;        // bytes of a box
     const int lane = threadIdx.x & 31;
     uint8_t* ring = ffn_ring();
-    const uint64_t pol = l2_policy_evict_first();  // every weight is read once
+    const uint64_t pol = l2_policy_evict_first();  // weights are read once, but for experts of more than 64 rows
     Turn st, out;
     Issued mine;
     uint32_t u = blockIdx.x;  // the first unit of every CTA needs no counter
