@@ -310,7 +310,9 @@ size_t mk_workspace_size(int T, int H, int F, int E, int k, const mk_config_t* c
  * without synchronising; arguments are checked first and nothing is launched
  * on a failure (MK_ERR_INVALID_ARG, MK_ERR_UNSUPPORTED); a device of compute
  * capability 10.3.  Sums, norms and softmax statistics are held in fp32 and
- * each output is rounded once.  Equal inputs give equal bits.
+ * each output is rounded once from them; the operands of products that have
+ * fewer bits (h, the attention's weights) are named at their entry.  Equal
+ * inputs give equal bits.
  *
  * They can be captured in a CUDA graph.  Under capture the library's
  * workspace cache is not grown (MK_ERR_WORKSPACE): make a call of the same
@@ -348,7 +350,9 @@ mk_status_t mk_add_rmsnorm(const void* x, int64_t x_stride, const void* residual
  *   s_j = scale * q[b,h,:] . k(j,c,:)  for j < n,   m = max_j s_j,
  *   out[b,h,:] = sum_j e^(s_j - m) v(j,c,:) / sum_j e^(s_j - m),
  *   lse[b,h] = log sum_j e^(s_j);
- * without keys (n = 0, or every score -inf) out is 0 and lse -inf.  Key j of
+ * without keys (n = 0, or every score -inf) out is 0 and lse -inf.  The weight
+ * e^(s_j - m) enters the product with v with 16 significant bits, its sum with
+ * 24 (the exponential is off by 2^-21 of it at most).  Key j of
  * sequence b lies in page block_table[b, j / page_size] at token
  * j % page_size: element page*page_stride + token*token_stride +
  * c*head_stride of k_cache and of v_cache, D elements in a row.  Nothing past

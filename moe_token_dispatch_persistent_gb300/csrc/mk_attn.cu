@@ -159,6 +159,8 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&b);
 }
+// The hardware's exponential, off by 2^-22 of its value at most: a sixty-fourth of
+// what the weights lose in the products below.
 __device__ __forceinline__ float exp2_of(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -166,11 +168,12 @@ __device__ __forceinline__ float exp2_of(float x) {
 }
 
 // Two weights as the sum of two bf16 values each: 16 significant bits reach the
-// products (the sum of the weights is of all 24).  The first is the weight cut
-// off; the second, what remains and 2^-23 of the weight, is above 0 for every
-// weight above 2^-110, so both products with an infinite value are infinite, of
-// its sign (rounded to nearest, the remainder may be 0 or negative, and the sum
-// of the products NaN).
+// products (the sum of the weights is of all 24), a 256th of the output's own
+// rounding, where one bf16 value would be as coarse as that.  The first is the
+// weight cut off; the second, what remains and 2^-23 of the weight, is above 0
+// for every weight above 2^-110, so both products with an infinite value are
+// infinite, of its sign (rounded to nearest, the remainder may be 0 or negative,
+// and the sum of the products NaN).
 __device__ __forceinline__ void split_weights(float p0, float p1, uint32_t& hi, uint32_t& lo) {
     const uint32_t u0 = __float_as_uint(p0), u1 = __float_as_uint(p1);
     constexpr float ABOVE = 1.f + 1.1920928955078125e-7f;
