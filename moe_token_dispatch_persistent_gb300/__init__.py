@@ -455,6 +455,18 @@ _device = None      # () -> index of the current device, the one the C entries l
 _empty = None       # (shape, strides, dtype, current device's index) -> uninitialised CUDA tensor
 
 
+def _allocates(entry):
+    """Whether the allocator's own entry, which torch does not document, does what it is used for."""
+    import torch
+
+    try:
+        t = entry((3, 5), (5, 1), torch.bfloat16)
+        return (type(t) is torch.Tensor and t.shape == (3, 5) and t.stride() == (5, 1) and t.dtype is torch.bfloat16
+                and t.get_device() == torch.cuda.current_device())
+    except Exception:  # missing, or another signature
+        return False
+
+
 def _load_torch():
     global _torch, _raw_stream, _device, _empty
     import torch
@@ -463,6 +475,8 @@ def _load_torch():
         lambda device: torch.cuda.current_stream(device).cuda_stream)
     guards = getattr(getattr(torch._C, "_dynamo", None), "guards", None)
     direct = getattr(guards, "_empty_strided_cuda", None)  # on the current device
+    if not _allocates(direct):
+        direct = None
 
     def empty(shape, strides, dtype, device):
         if direct is not None:
