@@ -625,7 +625,8 @@ def paged_attention(q, k_cache, v_cache, block_table, seq_lens, scale=None, stre
     if (kd != D or last != 1 or k_cache.dtype is not b16 or v_cache.dtype is not b16 or k_cache.get_device() != dev
             or v_cache.get_device() != dev):
         raise ValueError("caches must be bf16 [pages, page_size, Hkv, D] on q's device, D contiguous")
-    if v_cache.shape != shape or v_cache.stride() != strides:
+    if v_cache.shape != shape or (v_cache.stride() != strides and any(
+            n > 1 and a != b for n, a, b in zip(shape, strides, v_cache.stride()))):
         raise ValueError("k_cache and v_cache must agree in shape and strides")
     rows, max_pages = block_table.shape
     if rows != B or block_table.dtype is not i32 or block_table.get_device() != dev or not block_table.is_contiguous():

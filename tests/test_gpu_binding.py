@@ -1,5 +1,5 @@
-"""The tensor forms' outputs when torch's internal allocation entry is missing
-or does something else than it is used for."""
+"""The tensor forms: outputs when torch's internal allocation entry is missing or
+does something else than it is used for, strides that say nothing."""
 import pytest
 
 import moe_token_dispatch_persistent_gb300 as mk
@@ -43,3 +43,18 @@ def test_outputs_whatever_the_internal_entry_does(entry, monkeypatch):
         t = got[name]
         assert t.dtype == dtype and t.is_cuda and t.is_contiguous() and t.shape == want[name].shape
         assert torch.equal(t.view(torch.uint8), want[name].view(torch.uint8))
+
+
+def test_strides_of_dimensions_of_one_do_not_matter():
+    kv = torch.randn(4, 2, 1, 1, 64, device="cuda").bfloat16()
+    k, v = kv[:, 0], kv[:, 1]
+    q = torch.randn(2, 4, 64, device="cuda").bfloat16()
+    table = torch.arange(4, dtype=torch.int32, device="cuda").view(2, 2)
+    lens = torch.tensor([2, 1], dtype=torch.int32, device="cuda")
+    want = mk.paged_attention(q, k, v, table, lens)
+    odd = v.as_strided(v.shape, (v.stride(0), 999, 7, 1), v.storage_offset())
+    for a, b in ((k, odd), (k.as_strided(k.shape, (k.stride(0), 13, 0, 1), k.storage_offset()), v)):
+        got = mk.paged_attention(q, a, b, table, lens)
+        assert torch.equal(got["out"], want["out"]) and torch.equal(got["lse"], want["lse"])
+    with pytest.raises(ValueError, match="strides"):
+        mk.paged_attention(q, k, v.contiguous(), table, lens)
