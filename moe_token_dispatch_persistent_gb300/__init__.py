@@ -445,7 +445,9 @@ def mk_add_rmsnorm(x, x_stride, residual, residual_stride, weight, T, H, eps, ou
 
 # The tensor forms below are called once per layer and token, so they do
 # little: checks without temporaries, the raw stream handle, one allocation
-# per output, and the C entry.  On the host of a GB300 (us): torch.cuda.
+# per output, and the C entry.  ``check`` waits for the stream and looks at the
+# device's error word, as in the forms above: leave it out in a decode loop and
+# under stream capture.  On the host of a GB300 (us): torch.cuda.
 # current_stream 2.9, the raw handle 0.1; torch.empty 1.5, the allocator's own
 # entry 0.8.
 
@@ -665,7 +667,8 @@ def moe_ffn_decode(x, logits, W1, W3, W2, k, x_scale=None, W1_scale=None, W3_sca
     """The whole gated expert layer for a few tokens on torch tensors: x[T,H],
     logits[T,E] f32, W1 and W3 [E,H,F], W2 [E,F,H], all bf16, or all
     float8_e4m3fn with ``x_scale`` [T,H/128] (as add_rmsnorm gives it) and a
-    weight scale per 128 x 128 block.  Returns ``out`` [T,H] bf16."""
+    weight scale per 128 x 128 block.  An expert whose logit is -inf is left
+    out.  Returns ``out`` [T,H] bf16."""
     torch = _torch or _load_torch()
     T, H = x.shape
     E, _, F = W1.shape

@@ -24,14 +24,14 @@
 // Each warp has its own ring of tiles in shared memory, filled by its own
 // 16-byte asynchronous copies (any page size, any stride, keys past the end
 // filled with zeros), which run ahead across the groups of its range.  The
-// heads are the rows of m16n8k16 products (a decode step has at most 16 rows
-// to offer, where tcgen05 wants 64 or 128, and the products take a small part
-// of the time that the bytes do), so scores and weights stay in registers.
+// heads are the rows of m16n8k16 products, so scores and weights stay in
+// registers.  tcgen05 wants 64 or 128 rows: keys could be those, not tried; up
+// to 16 heads the products take a small part of the time that the bytes do.
 //
 // Measured on GB300: four sequences of 131071 keys, 8 key-value heads of 128:
-// 317 us, 6.8 TB/s; 13 of 47828 keys, 4 of 256: 360 to 372 us, 6.8 to 7.1
-// TB/s; 64 sequences of 0 to 16384 keys (449 MB) 82 us, of which 67 until the
-// last keys are in; one of 8191 keys 13.9 us (latency).
+// 308 to 317 us, 6.8 to 7.0 TB/s; 13 of 47828 keys, 4 of 256: 360 to 373 us,
+// 6.8 to 7.1 TB/s; 64 sequences of 0 to 16384 keys (449 MB) 80 us, of which 67
+// until the last keys are in; one of 8191 keys 13.9 us (latency).
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -64,7 +64,7 @@ struct Geo {
     // Warps that share a range, each with an equal part of the columns: one warp with
     // all 256 leaves room for four rings, a warp per scheduler, and its own latencies
     // bound it (13 sequences of 47828 keys, 4 heads of 256: 547 us, with two 360 to
-    // 372).  With 128 columns two warps gain nothing on long sequences (90 us either
+    // 373).  With 128 columns two warps gain nothing on long sequences (90 us either
     // way) and lose on many short ones (222 of 0 to 1518 keys, 24 heads each: 76, 93).
     static constexpr int SPLIT = D == 256 ? 2 : 1;
     // Warps that share a range: with R = 2 a ring of tiles too, with 16 heads each.
@@ -874,7 +874,7 @@ extern "C" mk_status_t mk_paged_attention(const void* q, int64_t q_stride, const
     // keys an even number of times and there is a group of 32 per CTA: with that many
     // the passes over a group's keys follow one another on the same SM, and the later
     // ones find them in L2 no more (32 sequences of 4096 keys, 8 key-value heads, 24
-    // query heads each: 135 us, with groups of 16 170).  With fewer groups the passes
+    // query heads each: 136 us, with groups of 16 170).  With fewer groups the passes
     // run side by side, and groups of 16 have more ranges (one sequence of 8191 keys,
     // 32 heads: 27 us, with groups of 16 22); with an odd number the second warp of the
     // last group has nothing to do (16 sequences of 30000, 48 heads: 123 and 116).

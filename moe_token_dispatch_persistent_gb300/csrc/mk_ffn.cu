@@ -37,10 +37,12 @@
 // tensor core after each step and are added up in fp32 registers with their
 // scales.
 //
-// Measured on GB300: 128 tokens over 256 e4m3 experts of 7168 x 2048 1.59 ms, 48
-// tokens over 112 bf16 experts of 4096 x 1536 0.59 ms (both 7.0 TB/s of
-// weights), one token over two of 4096 x 14336 0.113 ms (6.3 TB/s), two tokens
-// through a layer of 512 x 1024 22 us (latency).
+// Measured on GB300: 128 tokens over 256 e4m3 experts of 7168 x 2048 1.55 to
+// 1.59 ms, 48 tokens over 112 bf16 experts of 4096 x 1536 0.58 to 0.59 ms (both
+// 7.0 TB/s of weights or more), one token over two of 4096 x 14336 0.112 ms (6.3
+// TB/s), two tokens through a layer of 512 x 1024 22 us (latency).  More rows an
+// expert cost more: 77 tokens over 7 bf16 experts of 3840 x 1984 (44 rows each)
+// 104 us, 3.1 TB/s; over 4 of 4096 x 14336 64 rows each 351 us, 128 rows 621.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -70,7 +72,7 @@ constexpr int FFN_MAX_CTAS = 160;
 constexpr int WARP_A = 0, WARP_MMA = 1, WARP_EPI = 2, EPI_WARPS = 8, WARP_B = WARP_EPI + EPI_WARPS;
 constexpr int WARP_COUNT = WARP_B + 1, WARP_FIN = WARP_COUNT + 1, FIN_WARPS = 3;
 constexpr int FFN_WARPS = WARP_FIN + FIN_WARPS;
-constexpr int FFN_THREADS = FFN_WARPS * 32;
+constexpr int FFN_THREADS = FFN_WARPS * 32;  // 128 registers each: about 200 bytes of them are spilled
 
 // Rows of an expert that are multiplied together; an expert with more is
 // taken in parts, each reading its weights.  (Two accumulators of 64 columns

@@ -156,8 +156,10 @@ __global__ void __launch_bounds__(NORM_MAX_WARPS * 32) mk_add_rmsnorm_kernel(con
     const int H = p.H, groups = (H + NORM_GROUP - 1) / NORM_GROUP;
     const int64_t stride = int64_t(gridDim.x) * p.rows_per_cta;
     // Whether a thread has registers for the next row and the weights.  If not, a
-    // row is loaded in its own turn and the weights come from L1 (with spills instead:
-    // 2048 x 32768 154 us, so 107; 8192 x 7167 242, so 144; 2048 x 32767 650, so 301).
+    // row is loaded in its own turn and the weights come from L1 (with them in registers
+    // and spills for it: 2048 x 32768 154 us, so 108; 8192 x 7167 242, so 144; 2048 x
+    // 32767 650, so 300).  At 64 registers 20 bytes are spilled with VEC and two chunks,
+    // 100 without VEC and four; the other forms have none.
     constexpr bool AHEAD = C <= (VEC ? 2 : 1);
     uint4 x[C], r[C], w[C];
     auto fetch = [&](int64_t row) {
