@@ -262,9 +262,10 @@ size_t mk_ep_workspace_size(int T, int H, int F, int E, int k, int ranks);
  * and a second, library-owned stream waits on the flags and copies the rows,
  * in copies of 1, 1, 2, 4, ... chunks; other configurations copy after the
  * kernel.  With cfg->n_group = 0 this call orders the work tile by tile
- * (all N-blocks of a tile together), so rows complete in order.  Device staging comes from the library cache.  The library's
- * stream and chunk flags belong to (device, stream); calls on one stream run
- * one after another. */
+ * (all N-blocks of a tile together), so rows complete in order.  Device
+ * staging comes from the library cache.  It, the library's stream and the
+ * chunk flags belong to (device, stream); calls on one stream run one after
+ * another, from whichever host threads they come. */
 mk_status_t mk_moe_dispatch_gemm_host(const void* x_host, const float* logits_host, int T, int H, int E,
                                       int k, const void* W, int F, void* y_sorted_host,
                                       int32_t* src_index_host, int32_t* expert_offsets_host,

@@ -113,6 +113,8 @@ cudaError_t stream_state(int dev, cudaStream_t st, StreamState* out) {
 }
 
 struct HostStage {
+    std::mutex mu;         // held for a whole call, which waits for the stream anyway
+    bool dropped = false;  // released, and in the map no more
     void* ptr = nullptr;
     size_t bytes = 0;
     cudaStream_t copy = nullptr;     // streams finished result chunks to the host
@@ -122,7 +124,25 @@ struct HostStage {
                                      // do not accept stream-ordered pool memory)
     uint32_t seq = 0;                // calls made with this stage (chunk flags hold it)
 };
-std::map<WsKey, HostStage> g_host_stage;
+std::map<WsKey, std::shared_ptr<HostStage>> g_host_stage;
+
+// The stage of (device, stream), locked; null without memory for it.
+std::shared_ptr<HostStage> host_stage(const WsKey& key, std::unique_lock<std::mutex>* lock) try {
+    while (true) {
+        std::shared_ptr<HostStage> h;
+        {
+            std::lock_guard<std::mutex> map_lock(g_mu);
+            auto it = g_host_stage.find(key);
+            if (it == g_host_stage.end()) it = g_host_stage.emplace(key, std::make_shared<HostStage>()).first;
+            h = it->second;
+        }
+        *lock = std::unique_lock<std::mutex>(h->mu);
+        if (!h->dropped) return h;
+        lock->unlock();
+    }
+} catch (...) {
+    return nullptr;
+}
 
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
@@ -898,32 +918,28 @@ mk_status_t mk_moe_dispatch_gemm_host(const void* x_host, const float* logits_ho
     const size_t o_x = 0, o_l = ws_align(o_x + size_t(T) * H * 2), o_y = ws_align(o_l + size_t(T) * E * 4),
                  o_s = ws_align(o_y + ybytes), o_o = ws_align(o_s + rows * 4), o_g = ws_align(o_o + size_t(E + 1) * 4),
                  o_done = ws_align(o_g + rows * 4), total = ws_align(o_done + size_t(nchunks) * 4);
-    uint8_t* base = nullptr;
-    HostStage* hs = nullptr;
     StreamState stream_now;
     if (stream_state(dev, st, &stream_now) != cudaSuccess) return MK_ERR_CUDA;
-    {
-        std::lock_guard<std::mutex> lock(g_mu);
-        HostStage& h = g_host_stage[stream_now.key];
-        if (h.bytes < total) {
-            if (h.ptr && cudaFreeAsync(h.ptr, st) != cudaSuccess) return MK_ERR_CUDA;
-            h.ptr = nullptr;
-            h.bytes = 0;
-            if (cudaMallocAsync(&h.ptr, total, st) != cudaSuccess) return MK_ERR_CUDA;
-            h.bytes = total;
-
-        }
-        if (streamed && !h.copy) {
-            if (cudaStreamCreateWithFlags(&h.copy, cudaStreamNonBlocking) != cudaSuccess ||
-                cudaEventCreateWithFlags(&h.copied, cudaEventDisableTiming) != cudaSuccess ||
-                cudaEventCreateWithFlags(&h.computed, cudaEventDisableTiming) != cudaSuccess ||
-                cudaMalloc(&h.flags, kMaxChunks * sizeof(uint32_t)) != cudaSuccess ||
-                cudaMemset(h.flags, 0, kMaxChunks * sizeof(uint32_t)) != cudaSuccess)  // below every sequence number
-                return MK_ERR_CUDA;
-        }
-        base = static_cast<uint8_t*>(h.ptr);
-        hs = &h;
+    std::shared_ptr<HostStage> hs;
+    std::unique_lock<std::mutex> stage_lock;  // given back before the stage
+    hs = host_stage(stream_now.key, &stage_lock);
+    if (!hs) return MK_ERR_WORKSPACE;
+    if (hs->bytes < total) {
+        if (hs->ptr && cudaFreeAsync(hs->ptr, st) != cudaSuccess) return MK_ERR_CUDA;
+        hs->ptr = nullptr;
+        hs->bytes = 0;
+        if (cudaMallocAsync(&hs->ptr, total, st) != cudaSuccess) return MK_ERR_CUDA;
+        hs->bytes = total;
     }
+    if (streamed && !hs->copy) {
+        if (cudaStreamCreateWithFlags(&hs->copy, cudaStreamNonBlocking) != cudaSuccess ||
+            cudaEventCreateWithFlags(&hs->copied, cudaEventDisableTiming) != cudaSuccess ||
+            cudaEventCreateWithFlags(&hs->computed, cudaEventDisableTiming) != cudaSuccess ||
+            cudaMalloc(&hs->flags, kMaxChunks * sizeof(uint32_t)) != cudaSuccess ||
+            cudaMemset(hs->flags, 0, kMaxChunks * sizeof(uint32_t)) != cudaSuccess)  // below every sequence number
+            return MK_ERR_CUDA;
+    }
+    uint8_t* const base = static_cast<uint8_t*>(hs->ptr);
     if (T > 0) {
         if (cudaMemcpyAsync(base + o_x, x_host, size_t(T) * H * 2, cudaMemcpyHostToDevice, st) != cudaSuccess ||
             cudaMemcpyAsync(base + o_l, logits_host, size_t(T) * E * 4, cudaMemcpyHostToDevice, st) != cudaSuccess)
@@ -1058,18 +1074,24 @@ void mk_release_workspace(void) {
             for (void* p : w.kept) cudaFree(p);
         }
     }
-    std::lock_guard<std::mutex> lock(g_mu);
-    for (auto& d : g_dev) d.ready = false;  // after a device reset: attributes and addresses are looked up again
-    for (auto& kv : g_host_stage) {
+    std::map<WsKey, std::shared_ptr<HostStage>> stages;
+    {
+        std::lock_guard<std::mutex> lock(g_mu);
+        stages.swap(g_host_stage);
+        for (auto& d : g_dev) d.ready = false;  // after a device reset: attributes and addresses are looked up again
+    }
+    for (auto& kv : stages) {
+        HostStage& h = *kv.second;
+        std::lock_guard<std::mutex> held(h.mu);
+        h.dropped = true;
         cudaSetDevice(std::get<0>(kv.first));
         cudaDeviceSynchronize();
-        if (kv.second.ptr) cudaFree(kv.second.ptr);
-        if (kv.second.copy) cudaStreamDestroy(kv.second.copy);
-        if (kv.second.copied) cudaEventDestroy(kv.second.copied);
-        if (kv.second.computed) cudaEventDestroy(kv.second.computed);
-        if (kv.second.flags) cudaFree(kv.second.flags);
+        if (h.ptr) cudaFree(h.ptr);
+        if (h.copy) cudaStreamDestroy(h.copy);
+        if (h.copied) cudaEventDestroy(h.copied);
+        if (h.computed) cudaEventDestroy(h.computed);
+        if (h.flags) cudaFree(h.flags);
     }
-    g_host_stage.clear();
     cudaSetDevice(cur);
 }
 

@@ -27,7 +27,7 @@
 
 namespace {
 
-enum What { ALLOC, FREE, ZERO, LAUNCH, SYNC };
+enum What { ALLOC, FREE, ZERO, LAUNCH, SYNC, COPY };
 struct Op {
     What what;
     uintptr_t ptr;
@@ -139,10 +139,14 @@ cudaError_t cudaStreamGetId(cudaStream_t s, unsigned long long* id) {
     }
     return cudaSuccess;
 }
+cudaError_t cudaMemcpyAsync(void* to, const void* from, size_t, cudaMemcpyKind kind, cudaStream_t s) {
+    std::lock_guard<std::mutex> l(mu);
+    log(COPY, kind == cudaMemcpyHostToDevice ? to : from, s);
+    return cudaSuccess;
+}
 // what no scenario reaches
 cudaError_t cudaMalloc(void**, size_t) { return cudaErrorNotSupported; }
 cudaError_t cudaMemset(void*, int, size_t) { return cudaErrorNotSupported; }
-cudaError_t cudaMemcpyAsync(void*, const void*, size_t, cudaMemcpyKind, cudaStream_t) { return cudaErrorNotSupported; }
 cudaError_t cudaStreamSynchronize(cudaStream_t) { return cudaSuccess; }
 cudaError_t cudaStreamCreateWithFlags(cudaStream_t*, unsigned) { return cudaErrorNotSupported; }
 cudaError_t cudaStreamDestroy(cudaStream_t) { return cudaSuccess; }
@@ -203,6 +207,13 @@ mk_status_t call_ep(cudaStream_t st, int T) {
                          static_cast<int32_t*>(p), static_cast<float*>(p), nullptr, st, nullptr, nullptr, 0);
 }
 
+// Host buffers in and out, through the staging of the stream.
+mk_status_t call_host(cudaStream_t st, int T) {
+    void* p = reinterpret_cast<void*>(0x100);
+    return mk_moe_dispatch_gemm_host(p, static_cast<float*>(p), T, 64, 8, 2, p, 64, p, static_cast<int32_t*>(p),
+                                     static_cast<int32_t*>(p), static_cast<float*>(p), st, nullptr);
+}
+
 cudaStream_t stream(int i) { return reinterpret_cast<cudaStream_t>(uintptr_t(0x5000 + 16 * i)); }
 
 // The allocation that holds an address.
@@ -217,6 +228,7 @@ void expect_live() {
         if (o.what == ALLOC) live[o.ptr] = true;
         if (o.what == FREE) live[o.ptr] = false;
         if (o.what == LAUNCH) expect(live[buffer_of(o.ptr)], "a launch finds its workspace allocated");
+        if (o.what == COPY) expect(live[buffer_of(o.ptr)], "a copy finds its staging allocated");
     }
 }
 int count(What w) {
@@ -255,12 +267,12 @@ void growth(mk_status_t (*one)(cudaStream_t, int)) {
     a.join();
     b.join();
     expect(count(LAUNCH) == 3, "three launches");
-    expect(count(FREE) == 1, "the small buffer is given back");
+    expect(count(FREE) == (one == call_host ? 2 : 1), "the small buffers are given back");
     expect_live();
 }
 
 // The buffers are released while another thread stands there.
-void release_under_a_call() {
+void release_under_a_call(mk_status_t (*one)(cudaStream_t, int)) {
     std::mutex m;
     std::condition_variable cv;
     bool inside = false, released = false;
@@ -271,7 +283,7 @@ void release_under_a_call() {
             cv.notify_all();
             cv.wait_for(l, std::chrono::milliseconds(500), [&] { return released; });
         };
-        expect(call(stream(0), 64) == MK_OK, "the call");
+        expect(one(stream(0), 64) == MK_OK, "the call");
     });
     std::thread b([&] {
         {
@@ -285,7 +297,7 @@ void release_under_a_call() {
     });
     a.join();
     b.join();
-    expect(call(stream(0), 64) == MK_OK, "a call afterwards");
+    expect(one(stream(0), 64) == MK_OK, "a call afterwards");
     expect_live();
 }
 
@@ -406,7 +418,9 @@ int main(int argc, char** argv) {
     const std::string name = argc > 1 ? argv[1] : "";
     if (name == "growth") growth(call);
     else if (name == "growth_ep") growth(call_ep);
-    else if (name == "release") release_under_a_call();
+    else if (name == "growth_host") growth(call_host);
+    else if (name == "release") release_under_a_call(call);
+    else if (name == "release_host") release_under_a_call(call_host);
     else if (name == "per_thread") per_thread();
     else if (name == "recycled_handle") recycled_handle();
     else if (name == "captured_call") captured_call(stream(4));

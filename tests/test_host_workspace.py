@@ -22,7 +22,7 @@ def harness(tmp_path_factory):
     return exe
 
 
-@pytest.mark.parametrize("scenario", ["growth", "growth_ep", "release", "per_thread", "recycled_handle",
+@pytest.mark.parametrize("scenario", ["growth", "growth_ep", "growth_host", "release", "release_host", "per_thread", "recycled_handle",
                                       "captured_call", "captured_call_per_thread", "capture_keeps",
                                       "capture_keeps_ep", "capture_alone", "capture_refused"])
 def test_scenario(harness, scenario):
