@@ -420,6 +420,67 @@ mk_status_t mk_moe_ffn_decode(const void* x, const float* x_scale, const float* 
 /* Workspace bytes mk_moe_ffn_decode needs (0 for invalid sizes). */
 size_t mk_moe_ffn_decode_workspace_size(int T, int H, int F, int E, int k, int weights);
 
+/* ------------------------------------------------------------------------
+ * Operators that fill, share and read a paged key-value cache.  Conventions as
+ * for the operators of a decode step above.
+ *
+ * A cache of MK_CACHE_BF16 is what mk_paged_attention reads.  One of
+ * MK_CACHE_FP4 holds of each row of D columns D/2 bytes, two e2m1 values each
+ * (0, 0.5, 1, 1.5, 2, 3, 4, 6 and a sign; the even column in the low half), and
+ * beside them D/16 e4m3 scales, one per 16 columns: value * scale stands for
+ * y / factor, with an optional fp32 factor per key-value head.  Quantized are
+ *   scale = max(2^-9, e4m3(max |y / factor| / 6)),  value = e2m1(y / factor / scale),
+ * to nearest, ties to even, limited to the types' largest values; a NaN among
+ * the 16 makes them all NaN (by their scale).  72 bytes a row of 128 against 256. */
+enum { MK_CACHE_NONE = 0, MK_CACHE_BF16 = 1, MK_CACHE_FP4 = 2 };
+
+/* Pairs of columns that are rotated: i and i + rot/2, or 2i and 2i + 1. */
+enum { MK_PAIR_HALVES = 0, MK_PAIR_NEIGHBOURS = 1 };
+
+/* Arguments of mk_qk_norm_rope.  Strides of q, k and v in elements, of a cache
+ * in its units (bf16 elements, or bytes), of its scales in bytes. */
+typedef struct mk_qk_norm_rope {
+    const void *q, *k, *v;            /* [T,Hq,D], [T,Hkv,D], [T,Hkv,D] bf16; v only with a cache */
+    int64_t q_stride, q_head_stride;  /* between tokens, between heads */
+    int64_t k_stride, k_head_stride;
+    int64_t v_stride, v_head_stride;
+    const void *q_weight, *k_weight;  /* [D] bf16, or NULL: not normalized */
+    const int32_t* positions;         /* [axes,T] */
+    int64_t position_stride;          /* between axes */
+    const float* inv_freq;            /* [rot/2], finite */
+    const uint8_t* pair_axis;         /* HOST [rot/2]: the axis of each pair; NULL: the first */
+    void *q_out, *k_out, *v_out;      /* [T,Hq,D], [T,Hkv,D], [T,Hkv,D] bf16; see below */
+    const int64_t* slots;             /* [T]: page * page_size + token in the page; negative: none */
+    void *k_cache, *v_cache;
+    int64_t page_stride, token_stride, head_stride;
+    void *k_scales, *v_scales;        /* MK_CACHE_FP4 only */
+    int64_t scale_page_stride, scale_token_stride, scale_head_stride;
+    const float *k_factor, *v_factor; /* [Hkv], or NULL: 1 */
+    int32_t T, Hq, Hkv, D, rot, axes, pairs, cache, page_size, num_pages;
+    float eps;
+    int32_t reserved;                 /* zero */
+} mk_qk_norm_rope_t;
+
+/* Norms of the queries' and keys' heads, their rotation by position, and the
+ * way of keys and values into a cache, in one pass:
+ *   y = x * rsqrt(mean(x^2) + eps) * weight      over a head's D columns,
+ *   angle = positions[axis(i),t] * inv_freq[i]    for pair i of the first rot
+ *   columns: (a, b) -> (a cos - b sin, b cos + a sin); the others pass.
+ * The angle is exact to 2^-31 of a turn for any position.  q_out gets the
+ * queries; k_out, if not NULL, the keys; with a cache, the keys and the values
+ * (as they are) of token t go to slots[t], and with MK_CACHE_FP4 k_out and v_out
+ * (both may be NULL) get what the cache holds of them.  Without a cache k_out is
+ * needed, and v and v_out are not used.  A token with a negative slot is left
+ * out of the cache; one with a slot past the pool too, and it is reported by
+ * mk_get_status() (MK_ERR_DEVICE_FAULT).  The slots of a call must differ.
+ * q_out may be q itself, and k_out k, where their rows lie one after the other;
+ * no other outputs overlap inputs.
+ * Limits: D and rot multiples of 16, D <= 256, rot <= D (0: no rotation), axes
+ * <= 4, heads <= 65536; q, k, v, the weights and outputs 16-byte aligned with
+ * strides of multiples of 8 elements; a bf16 cache likewise, a 4-bit cache
+ * 4-byte aligned with strides of multiples of 4 bytes. */
+mk_status_t mk_qk_norm_rope(const mk_qk_norm_rope_t* args, void* stream);
+
 /* Synchronise `stream`, then return and clear the device error word
  * (MK_ERR_TIMEOUT / MK_ERR_DEVICE_FAULT), or MK_ERR_CUDA if the stream holds
  * a CUDA error.  MK_OK when nothing was recorded. */

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libmk.so")
@@ -41,6 +42,11 @@ MK_GATHER_DIRECT = 2
 MK_GATHER_GATHER4 = 3
 MK_WEIGHT_BF16 = 0
 MK_WEIGHT_E4M3 = 1
+MK_CACHE_NONE = 0
+MK_CACHE_BF16 = 1
+MK_CACHE_FP4 = 2
+MK_PAIR_HALVES = 0
+MK_PAIR_NEIGHBOURS = 1
 
 # Entry points declared in include/mk.h (checked by the tests).
 ABI_FUNCTIONS = (
@@ -59,6 +65,7 @@ ABI_FUNCTIONS = (
     "mk_paged_attention_workspace_size",
     "mk_moe_ffn_decode",
     "mk_moe_ffn_decode_workspace_size",
+    "mk_qk_norm_rope",
     "mk_workspace_size",
     "mk_get_status",
     "mk_last_error_detail",
@@ -117,6 +124,25 @@ _i = ctypes.c_int
 _i64 = ctypes.c_int64
 
 
+class mk_qk_norm_rope_t(ctypes.Structure):
+    _fields_ = (
+        [(n, _p) for n in ("q", "k", "v")]
+        + [(n, _i64) for n in ("q_stride", "q_head_stride", "k_stride", "k_head_stride", "v_stride", "v_head_stride")]
+        + [("q_weight", _p), ("k_weight", _p), ("positions", _p), ("position_stride", _i64), ("inv_freq", _p)]
+        + [(n, _p) for n in ("pair_axis", "q_out", "k_out", "v_out", "slots", "k_cache", "v_cache")]
+        + [(n, _i64) for n in ("page_stride", "token_stride", "head_stride")]
+        + [("k_scales", _p), ("v_scales", _p)]
+        + [(n, _i64) for n in ("scale_page_stride", "scale_token_stride", "scale_head_stride")]
+        + [("k_factor", _p), ("v_factor", _p)]
+        + [(n, ctypes.c_int32) for n in ("T", "Hq", "Hkv", "D", "rot", "axes", "pairs", "cache", "page_size", "num_pages")]
+        + [("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+    )
+
+
+# The same in order, for a call's arguments packed at once (a field at a time costs 6 us).
+_rope_args = struct.Struct("=3Q6q3QqQ7Q3q2Q3q2Q10ifi")
+
+
 def lib(path: str | None = None) -> ctypes.CDLL:
     """The loaded CUDA library (raises MkLibraryMissing if it was not built)."""
     global _lib_handle
@@ -165,6 +191,8 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     h.mk_moe_ffn_decode.restype = _i
     h.mk_moe_ffn_decode_workspace_size.argtypes = [_i, _i, _i, _i, _i, _i]
     h.mk_moe_ffn_decode_workspace_size.restype = ctypes.c_size_t
+    h.mk_qk_norm_rope.argtypes = [_p, _p]
+    h.mk_qk_norm_rope.restype = _i
     h.mk_get_status.argtypes = [_p]
     h.mk_get_status.restype = _i
     h.mk_last_error_detail.argtypes = [ctypes.POINTER(ctypes.c_int32)] * 3
@@ -705,3 +733,153 @@ def moe_ffn_decode(x, logits, W1, W3, W2, k, x_scale=None, W1_scale=None, W3_sca
     if status or check or other is not None:
         _finish(status, "mk_moe_ffn_decode", stream, other, check, (x, logits, W1, W3, W2, *scales, workspace), (out,))
     return {"out": out}
+
+
+# ------------------------------------- operators of a key-value cache --
+
+def mk_qk_norm_rope(args: mk_qk_norm_rope_t, stream=None) -> int:
+    return int(lib().mk_qk_norm_rope(ctypes.addressof(args) if args is not None else None, _stream(stream)))
+
+
+def fp4_cache(pages, page_size, heads, D, device="cuda"):
+    """Memory for a layer's keys and values in 4 bits: ``k_cache`` and
+    ``v_cache`` [pages, page_size, heads, D/2] uint8, ``k_scales`` and
+    ``v_scales`` [pages, page_size, heads, D/16] float8_e4m3fn, zeros.  A head's
+    rows of a page lie side by side, so that one head's scales fill whole
+    32-byte sectors of memory."""
+    import torch
+
+    def rows(cols, dtype):
+        t = torch.zeros((2, pages, heads, page_size, cols), dtype=torch.uint8, device=device).view(dtype)
+        return t.transpose(2, 3)
+
+    values, scales = rows(D // 2, torch.uint8), rows(D // 16, torch.float8_e4m3fn)
+    return dict(k_cache=values[0], v_cache=values[1], k_scales=scales[0], v_scales=scales[1])
+
+
+def _cache_pair(k, v, dtype, cols, what):
+    """Shape and strides that the two tensors of a cache share."""
+    if k.dtype is not dtype or v.dtype is not dtype or k.get_device() != v.get_device() or k.dim() != 4:
+        raise ValueError(f"{what} must be {dtype} [pages, page_size, Hkv, {cols}] on q's device")
+    shape, strides = k.shape, k.stride()
+    if v.shape != shape or (v.stride() != strides and any(
+            n > 1 and a != b for n, a, b in zip(shape, strides, v.stride()))):
+        raise ValueError(f"{what} must agree in shape and strides")
+    if shape[3] != cols or (strides[3] != 1 and cols != 1):
+        raise ValueError(f"{what} must have {cols} contiguous values a row")
+    return shape, strides
+
+
+def _fp4_cache_checks(dev, D, shape, k_cache, k_scales, v_scales, Hkv, factors):
+    """Strides of the scales and pointers of the factors of a 4-bit cache."""
+    torch = _torch
+    s_shape, s_strides = _cache_pair(k_scales, v_scales, torch.float8_e4m3fn, D // 16, "k_scales and v_scales")
+    if s_shape[:3] != shape[:3] or k_scales.get_device() != dev:
+        raise ValueError("the scales must be [pages, page_size, Hkv, D/16] of the caches' pages")
+    for f in factors:
+        if f is not None and (f.shape != (Hkv,) or f.dtype is not torch.float32 or f.get_device() != dev
+                              or not f.is_contiguous()):
+            raise ValueError("k_factor and v_factor must be f32 [Hkv] on q's device")
+    return s_strides
+
+
+def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e-6, interleaved=False, pair_axis=None,
+                 v=None, slots=None, k_cache=None, v_cache=None, k_scales=None, v_scales=None, k_factor=None,
+                 v_factor=None, keep=None, stream=None, check=True):
+    """Norms of the heads of queries and keys, their rotation by position and
+    the way of keys and values into a paged cache, on torch tensors: q[T,Hq,D],
+    k[T,Hkv,D] bf16 (tokens and heads may be strided), positions [T] or
+    [axes,T] i32, inv_freq [rot/2] f32 (the first ``rot`` columns of a head are
+    rotated; ``interleaved``: neighbours as pairs, else i and i + rot/2).
+
+    ``pair_axis``: a whole number per pair, the row of ``positions`` that turns
+    it.  ``q_weight`` and ``k_weight`` [D] bf16; without one, no norm.
+
+    With a cache: v[T,Hkv,D] bf16, slots[T] i64 (page * page_size + token in the
+    page; negative: none), and ``k_cache``, ``v_cache`` [pages, page_size, Hkv,
+    D] bf16, or [.., D/2] uint8 with ``k_scales``, ``v_scales`` [.., D/16]
+    float8_e4m3fn (see ``fp4_cache``) and, if wanted, ``k_factor``, ``v_factor``
+    [Hkv] f32.
+
+    Returns ``q`` [T,Hq,D] bf16; without a cache, or with ``keep``, ``k`` too,
+    and with ``keep`` and a 4-bit cache ``k`` and ``v`` as the cache holds them.
+    """
+    torch = _torch or _load_torch()
+    b16 = torch.bfloat16
+    T, Hq, D = q.shape
+    dev = q.get_device()
+    if dev < 0 or q.dtype is not b16:
+        raise ValueError("q must be a CUDA bf16 [T,Hq,D] tensor")
+    _on_device(dev)
+    Hkv = k.shape[1] if k.dim() == 3 else 0
+    q_strides, k_strides, v_strides = q.stride(), k.stride(), (0, 0, 1)
+    if k.dtype is not b16 or k.get_device() != dev or k.shape != (T, Hkv, D) or q_strides[2] != 1 or k_strides[2] != 1:
+        raise ValueError("q and k must be bf16 [T,heads,D] on one device, a head's columns contiguous")
+    half = inv_freq.shape[0] if inv_freq.dim() == 1 else -1
+    if half < 0 or inv_freq.dtype is not torch.float32 or inv_freq.get_device() != dev or not inv_freq.is_contiguous():
+        raise ValueError("inv_freq must be f32 [rot/2] on q's device")
+    axes = positions.shape[0] if positions.dim() == 2 else 1
+    if (positions.shape not in ((T,), (axes, T)) or positions.dtype is not torch.int32 or positions.get_device() != dev
+            or (T > 1 and positions.stride(-1) != 1)):
+        raise ValueError("positions must be i32 [T] or [axes,T] on q's device")
+    for w in (q_weight, k_weight):
+        if w is not None and (w.dtype is not b16 or w.get_device() != dev or w.shape != (D,) or not w.is_contiguous()):
+            raise ValueError("q_weight and k_weight must be bf16 [D] on q's device")
+    each = p_axis = None
+    if pair_axis is not None:
+        if len(pair_axis) != half or any(not 0 <= a < axes for a in pair_axis):
+            raise ValueError("pair_axis must name a row of positions for each of inv_freq")
+        each = (ctypes.c_uint8 * max(half, 1))(*pair_axis)
+        p_axis = ctypes.addressof(each)
+    elif axes > 1:
+        raise ValueError("positions of several axes need pair_axis")
+    cache, page_size, pages = MK_CACHE_NONE, 0, 0
+    strides = s_strides = (0, 0, 0)
+    if k_cache is None:
+        if any(t is not None for t in (v, slots, v_cache, k_scales, v_scales, k_factor, v_factor)):
+            raise ValueError("v, slots, scales and factors belong to a cache")
+        if keep is False:
+            raise ValueError("without a cache the keys are an output")
+    else:
+        if v is None or slots is None or v_cache is None:
+            raise ValueError("a cache needs v, slots, k_cache and v_cache")
+        v_strides = v.stride()
+        if v.dtype is not b16 or v.get_device() != dev or v.shape != (T, Hkv, D) or v_strides[2] != 1:
+            raise ValueError("v must be bf16 [T,Hkv,D] on q's device")
+        if (slots.shape != (T,) or slots.dtype is not torch.int64 or slots.get_device() != dev
+                or not slots.is_contiguous()):
+            raise ValueError("slots must be i64 [T] on q's device")
+        fp4 = k_cache.dtype is torch.uint8
+        cache = MK_CACHE_FP4 if fp4 else MK_CACHE_BF16
+        shape, strides = _cache_pair(k_cache, v_cache, torch.uint8 if fp4 else b16, D // 2 if fp4 else D,
+                                     "k_cache and v_cache")
+        pages, page_size = shape[0], shape[1]
+        if k_cache.get_device() != dev or shape[2] != Hkv:
+            raise ValueError("k_cache and v_cache must be [pages, page_size, Hkv, columns] on q's device")
+        if fp4:
+            if k_scales is None or v_scales is None:
+                raise ValueError("a 4-bit cache needs k_scales and v_scales")
+            s_strides = _fp4_cache_checks(dev, D, shape, k_cache, k_scales, v_scales, Hkv, (k_factor, v_factor))
+        elif any(t is not None for t in (k_scales, v_scales, k_factor, v_factor)):
+            raise ValueError("scales and factors belong to a 4-bit cache")
+    other = None if stream is None else _other_stream(stream, dev)
+    empty = _empty if other is None else _empty_on(other)
+    o = {"q": empty((T, Hq, D), (Hq * D, D, 1), b16, dev)}
+    if cache == MK_CACHE_NONE or keep:
+        o["k"] = empty((T, Hkv, D), (Hkv * D, D, 1), b16, dev)
+        if cache == MK_CACHE_FP4:
+            o["v"] = empty((T, Hkv, D), (Hkv * D, D, 1), b16, dev)
+    ptr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+    args = _rope_args.pack(
+        q.data_ptr(), k.data_ptr(), ptr(v), q_strides[0], q_strides[1], k_strides[0], k_strides[1], v_strides[0],
+        v_strides[1], ptr(q_weight), ptr(k_weight), positions.data_ptr(), positions.stride(0) if axes > 1 else 0,
+        inv_freq.data_ptr(), p_axis or 0, o["q"].data_ptr(), ptr(o.get("k")), ptr(o.get("v")), ptr(slots), ptr(k_cache),
+        ptr(v_cache), strides[0], strides[1], strides[2], ptr(k_scales), ptr(v_scales), s_strides[0], s_strides[1],
+        s_strides[2], ptr(k_factor), ptr(v_factor), T, Hq, Hkv, D, 2 * half, axes,
+        MK_PAIR_NEIGHBOURS if interleaved else MK_PAIR_HALVES, cache, page_size, pages, eps, 0)
+    status = lib().mk_qk_norm_rope(args, _raw_stream(dev) if stream is None else _stream(stream))
+    if status or check or other is not None:
+        _finish(status, "mk_qk_norm_rope", stream, other, check,
+                (q, k, v, positions, inv_freq, q_weight, k_weight, slots, k_cache, v_cache, k_scales, v_scales, k_factor,
+                 v_factor), o.values())
+    return o

@@ -1,0 +1,85 @@
+"""The cache's operators refuse bad arguments before any CUDA call (so these run
+without a GPU), and the bindings refuse wrong tensors."""
+import ctypes
+
+import pytest
+
+import moe_token_dispatch_persistent_gb300 as mk
+from moe_token_dispatch_persistent_gb300 import build as mkbuild
+
+BAD, UNSUPPORTED = mk.MK_ERR_INVALID_ARG, mk.MK_ERR_UNSUPPORTED
+NAN, INF = float("nan"), float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    mkbuild.build()
+    return mk.lib()
+
+
+# pointers are never read: 64 stands for one that is aligned
+ROPE = dict(q=64, k=64, q_stride=1024, q_head_stride=128, k_stride=512, k_head_stride=128, q_weight=64, k_weight=64,
+            positions=64, inv_freq=64, q_out=64, k_out=64, T=4, Hq=8, Hkv=4, D=128, rot=128, axes=1, eps=1e-6)
+BF16 = dict(ROPE, v=64, v_stride=512, v_head_stride=128, slots=64, k_cache=64, v_cache=64, page_stride=8192,
+            token_stride=512, head_stride=128, cache=mk.MK_CACHE_BF16, page_size=16, num_pages=20)
+FP4 = dict(BF16, k_scales=64, v_scales=64, page_stride=4096, token_stride=256, head_stride=64, scale_page_stride=512,
+           scale_token_stride=32, scale_head_stride=8, k_factor=64, v_factor=64, v_out=64, cache=mk.MK_CACHE_FP4)
+
+
+def rope(fields):
+    return mk.mk_qk_norm_rope(mk.mk_qk_norm_rope_t(**fields), 1)
+
+
+def test_argument_block_has_one_layout():
+    assert ctypes.sizeof(mk.mk_qk_norm_rope_t) == mk._rope_args.size == 296
+    assert mk.mk_qk_norm_rope(None, 1) == BAD
+
+
+@pytest.mark.parametrize("base", [ROPE, BF16, FP4], ids=["none", "bf16", "fp4"])
+@pytest.mark.parametrize("change,want", [
+    (dict(T=-1), BAD), (dict(Hq=0), BAD), (dict(Hkv=0), BAD), (dict(D=120), BAD), (dict(D=0), BAD), (dict(D=272, rot=128), UNSUPPORTED),
+    (dict(rot=136), BAD), (dict(rot=144), BAD), (dict(rot=-16), BAD), (dict(rot=24), BAD),
+    (dict(axes=0), BAD), (dict(axes=5), UNSUPPORTED), (dict(axes=2), BAD), (dict(pairs=2), BAD), (dict(cache=3), BAD),
+    (dict(cache=-1), BAD), (dict(reserved=1), BAD), (dict(Hq=65537), UNSUPPORTED),
+    (dict(eps=-1e-6), BAD), (dict(eps=NAN), BAD), (dict(eps=INF), BAD),
+    (dict(q=None), BAD), (dict(k=None), BAD), (dict(q_out=None), BAD), (dict(positions=None), BAD), (dict(inv_freq=None), BAD),
+    (dict(q=72), BAD), (dict(k=72), BAD), (dict(q_out=72), BAD), (dict(k_out=72), BAD), (dict(q_weight=66), BAD),
+    (dict(k_weight=72), BAD), (dict(positions=66), BAD), (dict(inv_freq=66), BAD),
+    (dict(q_stride=1028), BAD), (dict(k_head_stride=132), BAD), (dict(q_head_stride=-128), BAD),
+])
+def test_qk_norm_rope_refusals(base, change, want):
+    assert rope({**base, **change}) == want
+
+
+@pytest.mark.parametrize("base", [BF16, FP4], ids=["bf16", "fp4"])
+@pytest.mark.parametrize("change", [
+    dict(v=None), dict(v=72), dict(v_stride=516), dict(slots=None), dict(slots=68), dict(k_cache=None), dict(v_cache=None),
+    dict(k_cache=66), dict(v_cache=66), dict(page_size=0), dict(num_pages=-1), dict(page_stride=-16), dict(token_stride=-8),
+    dict(head_stride=2), dict(page_stride=8194)])
+def test_qk_norm_rope_cache_refusals(base, change):
+    assert rope({**base, **change}) == BAD
+
+
+@pytest.mark.parametrize("change", [dict(k_scales=None), dict(v_scales=None), dict(scale_page_stride=-1), dict(scale_head_stride=-8),
+                                    dict(k_factor=66), dict(v_factor=66), dict(v_out=72)])
+def test_qk_norm_rope_scales_refusals(change):
+    assert rope({**FP4, **change}) == BAD
+
+
+def test_qk_norm_rope_outputs_belong_to_their_form():
+    assert rope({**ROPE, "k_out": None}) == BAD   # without a cache the keys go nowhere
+    assert rope({**BF16, "v_out": 64}) == BAD     # a bf16 cache holds the values as they are
+
+
+def test_qk_norm_rope_pair_axis_is_checked():
+    each = (ctypes.c_uint8 * 64)(*([0, 1] * 31 + [0, 2]))
+    assert rope({**ROPE, "axes": 2, "pair_axis": ctypes.addressof(each)}) == BAD
+    each[0] = 1
+    assert rope({**ROPE, "axes": 1, "pair_axis": ctypes.addressof(each)}) == BAD
+
+
+def test_qk_norm_rope_binding_refuses_wrong_tensors():
+    torch = pytest.importorskip("torch")
+    q = torch.zeros((2, 4, 64), dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        mk.qk_norm_rope(q, q, torch.zeros(2, dtype=torch.int32), torch.zeros(32))  # not on a GPU
