@@ -481,6 +481,37 @@ typedef struct mk_qk_norm_rope {
  * 4-byte aligned with strides of multiples of 4 bytes. */
 mk_status_t mk_qk_norm_rope(const mk_qk_norm_rope_t* args, void* stream);
 
+/* mk_paged_attention over a cache of MK_CACHE_FP4: the same formulas with
+ *   k(j,c,:) = value * scale * k_factor[c],   v likewise with v_factor,
+ * products and sums in fp32, except that the weights e^(s_j - m) enter the
+ * product with v with 11 significant bits (those below 2^-24 of the largest
+ * with fewer; below 2^-34 they count as 0 there).  Element (page, token, head)
+ * of a cache's values begins at byte page*page_stride + token*token_stride +
+ * head*head_stride, D/2 bytes in a row; of its scales at page*scale_page_stride
+ * + ..., D/16 bytes.  k and v share strides.  A cache whose rows of one head lie
+ * side by side in a page is read fastest: D/16 bytes of scales are less than
+ * the 32 that memory moves at a time.
+ *   q[B,Hq,D] bf16 with q_stride elements between sequences, k_factor[Hkv] and
+ *   v_factor[Hkv] f32 (may be NULL: 1), the others as above        -- read only
+ * Limits as above, but: q 16-byte aligned and q_stride a multiple of 8; values
+ * 16-byte aligned with strides of multiples of 16 bytes; scales D/16-byte
+ * aligned with strides of multiples of D/16; fewer than 2^31 tiles of 16 keys
+ * and 8 query heads in all.  A scale that is NaN makes its columns NaN, an infinite or
+ * NaN query its head's out and lse.  Errors and lengths as above.
+ * workspace: NULL (library cache) or mk_paged_attention_fp4_workspace_size()
+ * bytes, 256-byte aligned, zero-filled before its first use and used by this
+ * entry point only; one stream at a time. */
+mk_status_t mk_paged_attention_fp4(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                                   int64_t page_stride, int64_t token_stride, int64_t head_stride, const void* k_scales,
+                                   const void* v_scales, int64_t scale_page_stride, int64_t scale_token_stride,
+                                   int64_t scale_head_stride, const float* k_factor, const float* v_factor,
+                                   const int32_t* block_table, const int32_t* seq_lens, int B, int Hq, int Hkv, int D,
+                                   int page_size, int max_pages, int num_pages, float scale, void* out, float* lse,
+                                   void* stream, void* workspace, size_t ws_bytes);
+
+/* Workspace bytes mk_paged_attention_fp4 needs (0 for invalid sizes). */
+size_t mk_paged_attention_fp4_workspace_size(int B, int Hq, int Hkv);
+
 /* Synchronise `stream`, then return and clear the device error word
  * (MK_ERR_TIMEOUT / MK_ERR_DEVICE_FAULT), or MK_ERR_CUDA if the stream holds
  * a CUDA error.  MK_OK when nothing was recorded. */

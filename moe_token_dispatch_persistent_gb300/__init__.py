@@ -66,6 +66,8 @@ ABI_FUNCTIONS = (
     "mk_moe_ffn_decode",
     "mk_moe_ffn_decode_workspace_size",
     "mk_qk_norm_rope",
+    "mk_paged_attention_fp4",
+    "mk_paged_attention_fp4_workspace_size",
     "mk_workspace_size",
     "mk_get_status",
     "mk_last_error_detail",
@@ -193,6 +195,11 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     h.mk_moe_ffn_decode_workspace_size.restype = ctypes.c_size_t
     h.mk_qk_norm_rope.argtypes = [_p, _p]
     h.mk_qk_norm_rope.restype = _i
+    h.mk_paged_attention_fp4.argtypes = [_p, _i64, _p, _p, _i64, _i64, _i64, _p, _p, _i64, _i64, _i64, _p, _p, _p, _p,
+                                         _i, _i, _i, _i, _i, _i, _i, ctypes.c_float, _p, _p, _p, _p, ctypes.c_size_t]
+    h.mk_paged_attention_fp4.restype = _i
+    h.mk_paged_attention_fp4_workspace_size.argtypes = [_i, _i, _i]
+    h.mk_paged_attention_fp4_workspace_size.restype = ctypes.c_size_t
     h.mk_get_status.argtypes = [_p]
     h.mk_get_status.restype = _i
     h.mk_last_error_detail.argtypes = [ctypes.POINTER(ctypes.c_int32)] * 3
@@ -883,3 +890,67 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e
                 (q, k, v, positions, inv_freq, q_weight, k_weight, slots, k_cache, v_cache, k_scales, v_scales, k_factor,
                  v_factor), o.values())
     return o
+
+
+def mk_paged_attention_fp4(q, q_stride, k_cache, v_cache, page_stride, token_stride, head_stride, k_scales, v_scales,
+                           scale_page_stride, scale_token_stride, scale_head_stride, k_factor, v_factor, block_table,
+                           seq_lens, B, Hq, Hkv, D, page_size, max_pages, num_pages, scale, out, lse=None, stream=None,
+                           workspace=None, ws_bytes: int = 0) -> int:
+    return int(lib().mk_paged_attention_fp4(
+        _ptr(q), q_stride, _ptr(k_cache), _ptr(v_cache), page_stride, token_stride, head_stride, _ptr(k_scales),
+        _ptr(v_scales), scale_page_stride, scale_token_stride, scale_head_stride, _ptr(k_factor), _ptr(v_factor),
+        _ptr(block_table), _ptr(seq_lens), B, Hq, Hkv, D, page_size, max_pages, num_pages, scale, _ptr(out), _ptr(lse),
+        _stream(stream), _ptr(workspace), int(ws_bytes)))
+
+
+def mk_paged_attention_fp4_workspace_size(B, Hq, Hkv) -> int:
+    return int(lib().mk_paged_attention_fp4_workspace_size(B, Hq, Hkv))
+
+
+def paged_attention_fp4(q, k_cache, v_cache, k_scales, v_scales, block_table, seq_lens, scale=None, k_factor=None,
+                        v_factor=None, stream=None, workspace=None, ws_bytes=0, check=True):
+    """Attention of one new token per sequence over a 4-bit cache, on torch
+    tensors: q[B,Hq,D] bf16, k_cache and v_cache [pages, page_size, Hkv, D/2]
+    uint8, k_scales and v_scales [pages, page_size, Hkv, D/16] float8_e4m3fn (as
+    ``fp4_cache`` makes them and ``qk_norm_rope`` fills them), k_factor and
+    v_factor [Hkv] f32 or None, block_table[B,max_pages] i32, seq_lens[B] i32.
+
+    ``scale`` defaults to D ** -0.5.  Returns ``out`` [B,Hq,D] bf16 and
+    ``lse`` [B,Hq] f32.
+    """
+    torch = _torch or _load_torch()
+    b16, i32 = torch.bfloat16, torch.int32
+    B, Hq, D = q.shape
+    dev = q.get_device()
+    if dev < 0 or q.dtype is not b16:
+        raise ValueError("q must be a CUDA bf16 [B,Hq,D] tensor")
+    _on_device(dev)
+    q_stride, q_head, q_last = q.stride()
+    if q_last != 1 or (q_head != D and Hq != 1):
+        raise ValueError("the heads of a sequence's q must be contiguous")
+    shape, strides = _cache_pair(k_cache, v_cache, torch.uint8, D // 2, "k_cache and v_cache")
+    pages, page_size, Hkv, _ = shape
+    if k_cache.get_device() != dev:
+        raise ValueError("k_cache and v_cache must be on q's device")
+    s_strides = _fp4_cache_checks(dev, D, shape, k_cache, k_scales, v_scales, Hkv, (k_factor, v_factor))
+    rows, max_pages = block_table.shape
+    if rows != B or block_table.dtype is not i32 or block_table.get_device() != dev or not block_table.is_contiguous():
+        raise ValueError("block_table must be i32 [B,max_pages]")
+    if (seq_lens.shape != (B,) or seq_lens.dtype is not i32 or seq_lens.get_device() != dev
+            or not seq_lens.is_contiguous()):
+        raise ValueError("seq_lens must be i32 [B]")
+    other = None if stream is None else _other_stream(stream, dev)
+    empty = _empty if other is None else _empty_on(other)
+    out = empty((B, Hq, D), (Hq * D, D, 1), b16, dev)
+    lse = empty((B, Hq), (Hq, 1), torch.float32, dev)
+    status = lib().mk_paged_attention_fp4(
+        q.data_ptr(), q_stride, k_cache.data_ptr(), v_cache.data_ptr(), strides[0], strides[1], strides[2],
+        k_scales.data_ptr(), v_scales.data_ptr(), s_strides[0], s_strides[1], s_strides[2],
+        None if k_factor is None else k_factor.data_ptr(), None if v_factor is None else v_factor.data_ptr(),
+        block_table.data_ptr(), seq_lens.data_ptr(), B, Hq, Hkv, D, page_size, max_pages, pages,
+        D ** -0.5 if scale is None else scale, out.data_ptr(), lse.data_ptr(),
+        _raw_stream(dev) if stream is None else _stream(stream), _ptr(workspace), ws_bytes)
+    if status or check or other is not None:
+        _finish(status, "mk_paged_attention_fp4", stream, other, check,
+                (q, k_cache, v_cache, k_scales, v_scales, k_factor, v_factor, block_table, seq_lens, workspace), (out, lse))
+    return {"out": out, "lse": lse}

@@ -355,7 +355,7 @@ mk_status_t Workspace::get(WsKind kind, int dev, cudaStream_t st, size_t need, s
             return MK_OK;
         }
         // memory allocated here is the graph's
-        if (kind == WS_ATTN || kind == WS_FFN) return MK_ERR_WORKSPACE;
+        if (kind != WS_DISPATCH && kind != WS_EP) return MK_ERR_WORKSPACE;
         if (cudaMallocAsync(&own_, need, st) != cudaSuccess) {
             own_ = nullptr;
             return MK_ERR_CUDA;

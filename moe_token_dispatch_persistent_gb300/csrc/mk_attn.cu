@@ -39,6 +39,7 @@
 #include <cmath>
 
 #include "mk.h"
+#include "mk_attn_split.cuh"
 #include "mk_common.h"
 #include "mk_host.h"
 #include "mk_ptx.cuh"
@@ -47,15 +48,6 @@ namespace mk {
 namespace {
 
 constexpr int ROWS = 16;          // query heads per warp (rows of the product)
-// A group counts as this many tiles more than it has: its queries, its first
-// tile's latency and its result cost about that, and short groups would
-// otherwise gather in a few warps.
-constexpr uint32_t EXTRA = 3;
-constexpr int ATTN_MAX_B = 4096;  // sequences (their tile counts sit in shared memory)
-constexpr int ATTN_MAX_CTAS = 160;
-constexpr float LOG2E = 1.4426950408889634f;
-constexpr float LN2 = 0.6931471805599453f;
-
 // D columns a head, groups of R * 16 query heads.
 template <int D, int R>
 struct Geo {
@@ -92,8 +84,7 @@ struct Geo {
     static_assert(SMEM + 2 * RANGES * 24 <= 232448, "shared memory of one CTA on sm_103");
 };
 
-constexpr size_t ATTN_SLOT_BYTES = size_t(std::max(Geo<256, 1>::SLOT, Geo<128, 2>::SLOT)) * 4;
-constexpr size_t ATTN_SLOTS_BYTES = 2 * ATTN_MAX_CTAS * ATTN_SLOT_BYTES;  // fixed, so the counters never move
+static_assert(std::max(Geo<256, 1>::SLOT, Geo<128, 2>::SLOT) <= ATTN_SLOT_FLOATS, "a partial result fits its slot");
 
 struct AttnParams {
     const __nv_bfloat16* q;
@@ -112,28 +103,12 @@ struct AttnParams {
     int chunks;                                   // groups per key-value head
     int groups;                                   // groups per sequence
     float scale2;                                 // scale * log2(e)
-};
 
-__device__ __forceinline__ void attn_error(DevError* e, uint32_t site, uint32_t info) {
-    if (atomicCAS(&e->code, 0u, uint32_t(ERR_FAULT)) == 0u) {
-        e->site = site;
-        e->cta = blockIdx.x;
-        e->info = info;
-    }
-}
+    __device__ float value_factor(int) const { return 1.f; }
+};
 
 // The two warps of a range meet, and see what each has written and copied.
 __device__ __forceinline__ void pair_sync(int range) { asm volatile("bar.sync %0, 64;" ::"r"(1 + range) : "memory"); }
-
-// 16 bytes global -> shared; zeros when !ok (the source is then not read).
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool ok) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -155,18 +130,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&b);
-}
-// The hardware's exponential, off by 2^-22 of its value at most: a sixty-fourth of
-// what the weights lose in the products below.
-__device__ __forceinline__ float exp2_of(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-
 // Two weights as the sum of two bf16 values each: 16 significant bits reach the
 // products (the sum of the weights is of all 24), a 256th of the output's own
 // rounding, where one bf16 value would be as coarse as that.  The first is the
@@ -180,74 +143,6 @@ __device__ __forceinline__ void split_weights(float p0, float p1, uint32_t& hi, 
     hi = __byte_perm(u0, u1, 0x7632);
     lo = pack_bf16(fmaf(p0, ABOVE, -__uint_as_float(u0 & 0xffff0000u)), fmaf(p1, ABOVE, -__uint_as_float(u1 & 0xffff0000u)));
 }
-
-// Tiles [t0, t1) of group g of sequence b.  In the order of positions that is
-// cut into ranges, EXTRA positions stand before a group's first tile.
-struct Range {
-    int b, g;
-    uint32_t t0, t1;
-    uint32_t begin;  // position of the group's first tile
-    uint32_t tiles;  // tiles of the group
-};
-__host__ __device__ inline uint32_t positions_of(int len, int keys) {
-    return len > 0 ? uint32_t(len + keys - 1) / uint32_t(keys) + EXTRA : 0u;
-}
-
-// The groups of the positions [pos, end) one after the other.
-struct Walk {
-    uint32_t pos, end;
-    const uint32_t* prefix;
-    int B;
-    uint32_t groups;
-    bool started;
-    // The next group that has tiles there.
-    __device__ bool next(Range& r) {
-        do {
-            if (pos >= end) return false;
-            uint32_t in = 0;  // position inside the group
-            if (!started) {
-                started = true;
-                const uint32_t want = pos / groups;  // positions of one group before it
-                int lo = 0, hi = B;                  // the last b with prefix[b] <= want that has keys
-                while (hi - lo > 1) {
-                    const int mid = (lo + hi) >> 1;
-                    if (prefix[mid] <= want) lo = mid;
-                    else hi = mid;
-                }
-                const uint32_t n = prefix[lo + 1] - prefix[lo];
-                in = pos - prefix[lo] * groups;
-                r.b = lo;
-                r.g = int(in / n);
-                in -= uint32_t(r.g) * n;
-                r.tiles = n - EXTRA;
-            } else if (uint32_t(++r.g) == groups) {
-                // the next sequence that has keys
-                r.g = 0;
-                do ++r.b;
-                while (prefix[r.b + 1] == prefix[r.b]);
-                r.tiles = prefix[r.b + 1] - prefix[r.b] - EXTRA;
-            }
-            const uint32_t to = min(r.tiles + EXTRA, in + (end - pos));
-            r.begin = pos - in + EXTRA;
-            r.t0 = in > EXTRA ? in - EXTRA : 0u;
-            r.t1 = to > EXTRA ? to - EXTRA : 0u;
-            pos += to - in;
-        } while (r.t1 <= r.t0);
-        return true;
-    }
-};
-
-// `total` positions cut into n ranges that differ by one position at most:
-// the first `more` of them hold `each` + 1.
-struct Cut {
-    uint32_t each, more;
-    __device__ Cut(uint32_t total, uint32_t n) : each(total / n), more(total - (total / n) * n) {}
-    __device__ uint32_t start(uint32_t c) const { return c * each + min(c, more); }
-    __device__ uint32_t owner(uint32_t p) const {
-        const uint32_t in_more = more * (each + 1);
-        return p < in_more ? p / (each + 1) : more + (p - in_more) / each;
-    }
-};
 
 // Element offset of one key's row of a tile (row = lane, modulo the tile's
 // keys), or -1 when the key lies past the sequence.
@@ -285,91 +180,6 @@ __device__ __forceinline__ void put_partial(float* part, int heads, int row0, in
     }
 }
 
-// Four columns of a head's partial result: maximum (in units of log 2), sum of
-// weights, weighted sum of values.
-struct Part {
-    float m = -INFINITY, l = 0.f;
-    float4 o = {0.f, 0.f, 0.f, 0.f};
-
-    __device__ void load(const float* slot, int group, int row, int c, int D) {
-        m = __ldcg(slot + row);
-        l = __ldcg(slot + group + row);
-        o = __ldcg(reinterpret_cast<const float4*>(slot + 2 * group + row * D + c));
-    }
-    template <int N>
-    __device__ void add(const Part (&u)[N]) {
-        float top = m;
-#pragma unroll
-        for (int x = 0; x < N; ++x) top = fmaxf(top, u[x].m);
-        const float base = top == -INFINITY ? 0.f : top;
-        const float f = exp2_of(m - base);
-        m = top;
-        l *= f;
-        o = make_float4(o.x * f, o.y * f, o.z * f, o.w * f);
-#pragma unroll
-        for (int x = 0; x < N; ++x) {
-            const float g = exp2_of(u[x].m - base);
-            l = fmaf(g, u[x].l, l);
-            o.x = fmaf(g, u[x].o.x, o.x);
-            o.y = fmaf(g, u[x].o.y, o.y);
-            o.z = fmaf(g, u[x].o.z, o.z);
-            o.w = fmaf(g, u[x].o.w, o.w);
-        }
-    }
-    __device__ void finish(const AttnParams& p, int b, int head, int c, int D) const {
-        const int64_t at = int64_t(b) * p.Hq + head;
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        *reinterpret_cast<uint2*>(p.out + at * D + c) =
-            make_uint2(pack_bf16(o.x * inv, o.y * inv), pack_bf16(o.z * inv, o.w * inv));
-        if (p.lse && c == 0) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * LN2;
-    }
-};
-
-// The result of a group from the partial results of CTAs [c0, c0 + n), by a
-// whole CTA.  A thread takes four columns of one head and, where there are more threads than
-// that, every parts-th piece; the parts are joined in shared memory.
-template <int D, int R>
-__device__ void join_group(const AttnParams& p, const Range& r, uint32_t c0, int n, uint32_t which0, float* smem_f) {
-    using G = Geo<D, R>;
-    const int tid = threadIdx.x;
-    const int kv = r.g / p.chunks, head0 = kv * p.per_kv + (r.g % p.chunks) * G::GROUP;
-    const int heads = min(G::GROUP, (kv + 1) * p.per_kv - head0);
-    const int items = heads * (D / 4), parts = min(n, max(1, G::THREADS / items));
-    Part* red = reinterpret_cast<Part*>(smem_f);
-    // the first CTA's piece may lie in its second slot; the others' ranges start in the group
-    const float* first = p.slots + size_t(2 * c0 + which0) * (ATTN_SLOT_BYTES / 4);
-    const float* other = p.slots + size_t(2 * c0) * (ATTN_SLOT_BYTES / 4);
-    for (int i0 = 0; i0 < items; i0 += G::THREADS) {
-        const int item = parts > 1 ? tid % items : i0 + tid, part = parts > 1 ? tid / items : 0;
-        const bool on = item < items && part < parts;
-        const int row = item / (D / 4), c = (item % (D / 4)) * 4;
-        Part acc;
-        if (on) {
-            constexpr int BATCH = 4;
-            for (int i = part; i < n; i += BATCH * parts) {
-                Part u[BATCH];
-#pragma unroll
-                for (int x = 0; x < BATCH; ++x) {
-                    const int at = i + x * parts;
-                    if (at < n) u[x].load(at == 0 ? first : other + size_t(2 * at) * (ATTN_SLOT_BYTES / 4), G::GROUP, row, c, D);
-                }
-                acc.add(u);
-            }
-        }
-        if (parts > 1) {
-            if (on) red[part * items + item] = acc;
-            __syncthreads();
-            if (on && part == 0)
-                for (int q = 1; q < parts; ++q) {
-                    const Part u[1] = {red[q * items + item]};
-                    acc.add(u);
-                }
-        }
-        if (on && part == 0) acc.finish(p, r.b, head0 + row, c, D);
-    }
-    __syncthreads();  // the buffer is free for another group
-}
-
 template <int D, int R>
 __global__ void __launch_bounds__(Geo<D, R>::THREADS, 1) mk_paged_attention_kernel(const AttnParams p) {
     using G = Geo<D, R>;
@@ -378,48 +188,9 @@ __global__ void __launch_bounds__(Geo<D, R>::THREADS, 1) mk_paged_attention_kern
     uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + G::SM_PREFIX);
     uint32_t* small = reinterpret_cast<uint32_t*>(smem + G::SM_SMALL);
     const uint32_t groups = uint32_t(p.groups);
-    const int64_t cap = int64_t(p.max_pages) * p.page_size;
 
-    // ---- positions of one group of each sequence, summed over the sequences before it
-    auto length = [&](int b) -> int {
-        const int n = __ldg(p.lens + b);
-        return n < 0 ? 0 : n > cap ? int(cap) : n;
-    };
-    {
-        const int per = (p.B + G::THREADS - 1) / G::THREADS;
-        const int b0 = min(p.B, tid * per), b1 = min(p.B, b0 + per);
-        uint32_t mine = 0;
-        for (int b = b0; b < b1; ++b) {
-            const int n = __ldg(p.lens + b);
-            if ((n < 0 || n > cap) && blockIdx.x == 0) attn_error(p.err, SITE_SEQ_LEN, uint32_t(n));
-            mine += positions_of(length(b), G::KEYS);
-        }
-        uint32_t run = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t o = __shfl_up_sync(0xffffffffu, run, d);
-            if (lane >= d) run += o;
-        }
-        if (lane == 31) small[warp] = run;
-        __syncthreads();
-        uint32_t base = run - mine;
-        for (int w = 0; w < warp; ++w) base += small[w];
-        for (int b = b0; b < b1; ++b) {
-            prefix[b] = base;
-            base += positions_of(length(b), G::KEYS);
-        }
-        if (b1 == p.B && b0 < b1) prefix[p.B] = base;
-        __syncthreads();
-    }
-
-    // sequences without keys: zeros and -inf
-    for (int b = blockIdx.x; b < p.B; b += gridDim.x) {
-        if (prefix[b + 1] != prefix[b]) continue;
-        uint2* o = reinterpret_cast<uint2*>(p.out + int64_t(b) * p.Hq * D);
-        for (int i = tid; i < p.Hq * D / 4; i += G::THREADS) o[i] = make_uint2(0u, 0u);
-        if (p.lse)
-            for (int i = tid; i < p.Hq; i += G::THREADS) p.lse[int64_t(b) * p.Hq + i] = -INFINITY;
-    }
+    auto length = [&](int b) -> int { return length_of(p, b); };
+    count_positions<D, G::KEYS, G::THREADS>(p, prefix, small);
 
     const uint32_t total = prefix[p.B] * groups;
     // At least a position per range, and one more for every four heads of a warp
@@ -679,87 +450,17 @@ __global__ void __launch_bounds__(Geo<D, R>::THREADS, 1) mk_paged_attention_kern
     copy_wait<0>();
 
     // ---- join what the CTA's ranges have of the same groups
-    __shared__ Range pieces[2 * G::RANGES];  // in the order of positions; tiles 0: none
-    __syncthreads();  // the rings are free
-    if (mate == 0 && lane == 0) {
-        head.tiles = has_head ? head.tiles : 0u;
-        tail.tiles = has_tail ? tail.tiles : 0u;
-        pieces[2 * range] = head;
-        pieces[2 * range + 1] = tail;
-    }
     float* tails = reinterpret_cast<float*>(smem);
     const float* firsts = reinterpret_cast<const float*>(smem + G::SM_HEADS);
+    __syncthreads();  // the rings are free
     if (has_tail) {
         const int kv = tail.g / p.chunks, head0 = kv * p.per_kv + (tail.g % p.chunks) * G::GROUP + row0;
         put_partial<G>(tails + range * G::PART, min(ROWS, (kv + 1) * p.per_kv - head0), row0, side, o, m0, m1, l0, l1);
     }
-    __syncthreads();
-    Range open[2];  // groups shared with other CTAs: the first and the last one's
-    int nopen = 0;
-    uint32_t left = 0;  // pieces not joined yet, a bit each
-#pragma unroll
-    for (int i = 0; i < 2 * G::RANGES; ++i) left |= pieces[i].tiles != 0 ? 1u << i : 0u;
-    while (left) {
-        const Range q = pieces[__ffs(int(left)) - 1];
-        uint32_t same = 0;  // those of the first one's group
-#pragma unroll
-        for (int i = 0; i < 2 * G::RANGES; ++i)
-            if ((left >> i & 1u) && pieces[i].begin == q.begin) same |= 1u << i;
-        left &= ~same;
-        const int kv = q.g / p.chunks, head0 = kv * p.per_kv + (q.g % p.chunks) * G::GROUP;
-        const int heads = min(G::GROUP, (kv + 1) * p.per_kv - head0);
-        const bool whole = q.begin >= start && q.begin + q.tiles <= end;
-        // a CTA's first shared group takes its first slot, its last one the second
-        float* mine = p.slots + size_t(2 * blockIdx.x + (start >= q.begin ? 0 : 1)) * (ATTN_SLOT_BYTES / 4);
-        for (int item = tid; item < heads * (D / 4); item += G::THREADS) {
-            const int row = item / (D / 4), c = (item % (D / 4)) * 4;
-            Part acc;
-            for (uint32_t rest = same; rest;) {
-                constexpr int BATCH = 4;
-                Part u[BATCH];
-#pragma unroll
-                for (int x = 0; x < BATCH; ++x) {
-                    if (rest == 0) continue;
-                    const int i = __ffs(int(rest)) - 1, w = i >> 1;
-                    rest &= rest - 1;
-                    const float* s = (i & 1 ? tails : firsts) + w * G::PART;
-                    u[x].m = s[G::GROUP * G::OSTRIDE + row];
-                    u[x].l = s[G::GROUP * G::OSTRIDE + G::GROUP + row];
-                    u[x].o = *reinterpret_cast<const float4*>(s + row * G::OSTRIDE + c);
-                }
-                acc.add(u);
-            }
-            if (whole) {
-                acc.finish(p, q.b, head0 + row, c, D);
-            } else {
-                __stcg(reinterpret_cast<float4*>(mine + 2 * G::GROUP + row * D + c), acc.o);
-                if (c == 0) {
-                    __stcg(mine + row, acc.m);
-                    __stcg(mine + G::GROUP + row, acc.l);
-                }
-            }
-        }
-        if (!whole) open[nopen++] = q;
-    }
-    if (nopen == 0) return;
-
-    // ---- groups shared with other CTAs: the one that arrives last joins their
-    // partial results (the count releases what the whole CTA has stored)
-    __syncthreads();
-    if (tid < nopen) {
-        const Range& o = tid == 0 ? open[0] : open[1];
-        const uint32_t c0 = cut_at.owner(o.begin), n = cut_at.owner(o.begin + o.tiles - 1) - c0 + 1;
-        uint32_t* a = p.arrived + size_t(o.b) * groups + o.g;
-        const bool last = atom_add_acq_rel_u32(a, 1u) == n - 1;
-        if (last) *a = 0u;
-        small[4 * tid] = last ? n : 0u;
-        small[4 * tid + 1] = c0;
-        small[4 * tid + 2] = cut_at.start(c0) >= o.begin ? 0u : 1u;
-    }
-    __syncthreads();
-    for (int i = 0; i < nopen; ++i)
-        if (small[4 * i])
-            join_group<D, R>(p, i == 0 ? open[0] : open[1], small[4 * i + 1], int(small[4 * i]), small[4 * i + 2], tails);
+    head.tiles = has_head ? head.tiles : 0u;
+    tail.tiles = has_tail ? tail.tiles : 0u;
+    join_ranges<D, G::GROUP, G::RANGES, G::THREADS>(p, head, tail, range, mate == 0 && lane == 0, tails, firsts, small, cut_at,
+                                                   start, end);
 }
 
 template <int D, int R>
@@ -790,7 +491,8 @@ cudaError_t attn_kernel_attributes() {
     if ((e = attn_smem<64, 1>()) != cudaSuccess || (e = attn_smem<64, 2>()) != cudaSuccess ||
         (e = attn_smem<128, 1>()) != cudaSuccess || (e = attn_smem<128, 2>()) != cudaSuccess)
         return e;
-    return attn_smem<256, 1>();
+    if ((e = attn_smem<256, 1>()) != cudaSuccess) return e;
+    return attn4_kernel_attributes();
 }
 
 }  // namespace mk

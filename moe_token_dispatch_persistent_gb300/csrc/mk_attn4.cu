@@ -1,0 +1,664 @@
+// mk_attn4.cu -- mk_paged_attention_fp4: attention of one new token per sequence
+// over a paged cache in 4 bits, split over the caches' lengths and joined.
+//
+//   k = e2m1 * e4m3 scale of its 16 columns * factor of its head, v likewise,
+//   s_j = scale * q . k_j,   out = sum_j e^(s_j - m) v_j / l,
+//   m = max_j s_j,  l = sum_j e^(s_j - m),  lse = m + log l
+//
+// A row of 128 columns is 72 bytes, so a key and its value have 6 cycles of an SM
+// at the copy rate: the instructions that unpack, scale and multiply 256 values
+// bound it as much as the bytes do, and their count decides.
+//
+// The products have keys (of the scores) or columns (of the output) as their 16
+// rows and query heads as their 8 columns, so up to 8 heads waste nothing and 16
+// share the unpacked values.  The order of the columns in a score's sum is free:
+// a lane takes D/4 neighbouring ones of a key, 16 bytes with 128, and the queries
+// are laid out alike.  Of a value it takes D/8 neighbouring columns of four keys;
+// pairs of keys are formed while the values have 4 bits.  value * scale has 6
+// significant bits and is exact in fp16; the queries keep their 8 there, moved by
+// a power of two per head; the weights e^(s - m) are rounded to fp16, 11 bits, an
+// eighth of the output's own rounding, and moved by 2^10 so that those above
+// 2^-24 of the largest keep all of them.
+//
+// Work is cut and joined as in mk_attn_split.cuh.  A tile is KEYS keys of one
+// (sequence, group of up to 8 or 16 query heads of one key-value head); each warp
+// has a ring of tiles in shared memory, filled by its own asynchronous copies.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+
+#include "mk.h"
+#include "mk_attn_split.cuh"
+#include "mk_common.h"
+#include "mk_fp4.cuh"
+#include "mk_host.h"
+
+namespace mk {
+namespace {
+
+// D columns a head, groups of NT * 8 query heads.
+template <int D, int NT>
+struct Geo4 {
+    static constexpr int GROUP = NT * 8;
+    static constexpr int KEYS = D == 256 ? 16 : 32;  // per tile
+    static constexpr int WARPS = D == 64 ? 16 : D == 128 ? (NT == 1 ? 12 : 8) : (NT == 1 ? 8 : 6);
+    static constexpr int STAGES = D == 64 ? (NT == 1 ? 4 : 3) : D == 128 ? (NT == 1 ? 2 : 3) : (NT == 1 ? 3 : 4);
+    static constexpr int THREADS = WARPS * 32;
+    static constexpr int ROW = D / 2;         // bytes of a row's values
+    static constexpr int SROW = D / 16;       // bytes of its scales
+    static constexpr int VALUES = KEYS * ROW;
+    static constexpr int SCALES = KEYS * SROW;
+    static constexpr int STAGE = 2 * VALUES + 2 * SCALES;
+    static constexpr int RING = STAGES * STAGE;
+    static constexpr int PART = GROUP * (D + 8) + 2 * GROUP;  // floats of a range's result: O, m, l
+    static constexpr int SM_HEADS = WARPS * RING;             // results of ranges' first groups; the last ones lie on the rings
+    static constexpr int SM_PREFIX = SM_HEADS + WARPS * PART * 4;
+    static constexpr int SM_SMALL = SM_PREFIX + (ATTN_MAX_B + 1) * 4 + 12;
+    static constexpr int SMEM = SM_SMALL + 128;
+    static_assert(WARPS * PART * 4 <= SM_HEADS, "the last results lie where the rings were");
+    static_assert(2 * GROUP + GROUP * D <= ATTN_SLOT_FLOATS, "a partial result fits its slot");
+    static_assert(SMEM + 2 * WARPS * 24 <= 232448, "shared memory of one CTA on sm_103");
+};
+
+constexpr float WEIGHT_SHIFT = 10.f;  // weights are 2^10 e^(s - m)
+constexpr float WEIGHT_MOST = 15.f;   // log2 of the largest: one above starts a new maximum
+
+struct Attn4Params {
+    const __nv_bfloat16* q;
+    const uint8_t *k, *v, *k_scales, *v_scales;
+    const float *k_factor, *v_factor;  // or null
+    const int32_t* table;
+    const int32_t* lens;
+    __nv_bfloat16* out;
+    float* lse;                        // or null
+    float* slots;
+    uint32_t* arrived;
+    DevError* err;
+    int64_t q_stride;
+    int64_t page_stride, token_stride, head_stride;  // bytes
+    int64_t scale_page, scale_token, scale_head;     // bytes
+    int B, Hq, Hkv, page_size, max_pages, num_pages;
+    int per_kv, chunks, groups;
+    float scale2;                      // scale * log2(e)
+
+    __device__ float value_factor(int kv) const { return v_factor ? __ldg(v_factor + kv) : 1.f; }
+};
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t a) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint32_t low_twice(uint32_t h2) { return __byte_perm(h2, 0, 0x1010); }
+__device__ __forceinline__ uint32_t high_twice(uint32_t h2) { return __byte_perm(h2, 0, 0x3232); }
+
+template <int BYTES>
+__device__ __forceinline__ void copy_small(uint32_t dst, const void* src, bool ok) {
+    if constexpr (BYTES == 16) copy16(dst, src, ok);
+    else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(ok ? BYTES : 0) : "memory");
+}
+template <int WORDS>
+__device__ __forceinline__ void load_words(uint32_t addr, uint32_t (&w)[WORDS]) {
+    if constexpr (WORDS == 1) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
+    else if constexpr (WORDS == 2) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
+    else
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ uint32_t load_u8(uint32_t addr) {
+    uint32_t r;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
+    return r;
+}
+__device__ __forceinline__ uint32_t load_u16(uint32_t addr) {
+    uint32_t r;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
+    return r;
+}
+
+// Where a row's 16-byte chunk lies in its tile, without bank conflicts for the
+// reads below.  Keys lie in order.  Of values, keys 2c, 2c + 1, 2c + 8 and 2c + 9
+// of 16 go to a lane, so rows c, 4 + c, 8 + c, 12 + c hold them.
+template <int D>
+__device__ __forceinline__ uint32_t key_at(int row, int chunk) {
+    return uint32_t(row * (D / 2) + ((D == 256 ? chunk ^ (row & 1) : chunk) << 4));
+}
+__device__ __forceinline__ int value_row(int key) { return (key & ~7) | ((key & 1) << 2) | ((key >> 1) & 3); }
+template <int D>
+__device__ __forceinline__ uint32_t value_at(int row, int chunk) {
+    return uint32_t(row * (D / 2) + ((D == 64 ? chunk : D == 128 ? chunk ^ (row & 2) : chunk ^ ((row & 3) << 1)) << 4));
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp4_kernel(const Attn4Params p) {
+    using G = Geo4<D, NT>;
+    constexpr int KEYS = G::KEYS, GROUP = G::GROUP, MT = KEYS / 16;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = lane >> 2, c = lane & 3;  // row and pair of columns of this lane in the products
+    uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + G::SM_PREFIX);
+    uint32_t* small = reinterpret_cast<uint32_t*>(smem + G::SM_SMALL);
+    const uint32_t groups = uint32_t(p.groups);
+    count_positions<D, KEYS, G::THREADS>(p, prefix, small);
+
+    const uint32_t total = prefix[p.B] * groups;
+    const uint32_t least = uint32_t(G::WARPS);  // a position per warp
+    const uint32_t nctas = min(gridDim.x, (total + least - 1) / least);
+    if (blockIdx.x >= nctas) return;
+    const Cut cut_at(total, nctas);
+    const uint32_t start = cut_at.start(blockIdx.x), end = cut_at.start(blockIdx.x + 1);
+    const Cut warp_cut(end - start, G::WARPS);
+    const uint32_t wstart = start + warp_cut.start(warp), wend = start + warp_cut.start(warp + 1);
+
+    // ---- this warp's ring: loads run STAGES tiles ahead, across groups
+    const uint32_t ring = smem_u32(smem) + uint32_t(warp) * G::RING;
+    Walk load_walk{wstart, wend, prefix, p.B, groups, false};
+    Range lr;
+    uint32_t load_tile = 0;
+    int load_len = 0;
+    bool more = true;
+    lr.t1 = 0;
+    // A lane looks up the rows of one key, two tiles before they are copied.
+    struct Ahead {
+        int64_t row, srow;  // byte offsets, -1: past the end
+        bool have;
+    } ahead[2];
+    auto look_up = [&](Ahead& a) {
+        a.have = false;
+        if (!more) return;
+        if (load_tile >= lr.t1) {
+            if (!load_walk.next(lr)) {
+                more = false;
+                return;
+            }
+            load_len = length_of(p, lr.b);
+            load_tile = lr.t0;
+        }
+        a.have = true;
+        a.row = a.srow = -1;
+        const int key = int(load_tile) * KEYS + (lane & (KEYS - 1));
+        ++load_tile;
+        if (key >= load_len) return;
+        const int slot = key / p.page_size, token = key - slot * p.page_size, kv = lr.g / p.chunks;
+        const int page = __ldg(p.table + int64_t(lr.b) * p.max_pages + slot);
+        if (page < 0 || page >= p.num_pages) {
+            attn_error(p.err, SITE_PAGE_RANGE, uint32_t(page));
+            return;
+        }
+        a.row = page * p.page_stride + token * p.token_stride + kv * p.head_stride;
+        a.srow = page * p.scale_page + token * p.scale_token + kv * p.scale_head;
+    };
+    look_up(ahead[0]);
+    look_up(ahead[1]);
+    uint32_t load_slot = 0;
+    auto issue = [&]() {
+        const Ahead a = ahead[0];
+        if (a.have) {
+            const uint32_t ks = ring + load_slot * G::STAGE, vs = ks + G::VALUES, kss = vs + G::VALUES, vss = kss + G::SCALES;
+            constexpr int CHUNKS = G::ROW / 16;
+#pragma unroll
+            for (int i = 0; i < KEYS * CHUNKS / 32; ++i) {
+                const int piece = i * 32 + lane, row = piece / CHUNKS, chunk = piece % CHUNKS;
+                const int64_t ro = __shfl_sync(0xffffffffu, a.row, row);
+                const bool ok = ro >= 0;
+                const int64_t at = (ok ? ro : 0) + chunk * 16;
+                copy16(ks + key_at<D>(row, chunk), p.k + at, ok);
+                copy16(vs + value_at<D>(value_row(row), chunk), p.v + at, ok);
+            }
+            const bool ok = a.srow >= 0;
+            const int64_t at = ok ? a.srow : 0;
+            if (KEYS == 32 || lane < KEYS) {
+                copy_small<G::SROW>(kss + uint32_t(lane * G::SROW), p.k_scales + at, ok);
+                copy_small<G::SROW>(vss + uint32_t(value_row(lane) * G::SROW), p.v_scales + at, ok);
+            }
+        }
+        copy_commit();
+        ahead[0] = ahead[1];
+        look_up(ahead[1]);
+        if (++load_slot == G::STAGES) load_slot = 0;
+    };
+#pragma unroll
+    for (int i = 0; i < G::STAGES; ++i) issue();
+
+    uint32_t slot = 0;
+    Walk walk{wstart, wend, prefix, p.B, groups, false};
+    Range r, head, tail;
+    bool has_head = false, has_tail = false;
+    // Output columns g * D/8 + 2t and + 2t + 1 of heads 8n + 2c and 8n + 2c + 1.
+    float o[NT][D / 16][4];
+    float m[NT][2], l[NT][2];
+
+    auto put = [&](float* part, int heads) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int row = n * 8 + 2 * c + i;
+                if (g == 0) {
+                    part[GROUP * (D + 8) + row] = m[n][i] - WEIGHT_SHIFT;
+                    part[GROUP * (D + 8) + GROUP + row] = l[n][i];
+                }
+                float* to = part + row * (D + 8) + g * (D / 8);
+                if (row < heads)
+#pragma unroll
+                    for (int t = 0; t < D / 16; t += 2)
+                        *reinterpret_cast<float4*>(to + 2 * t) =
+                            make_float4(o[n][t][i], o[n][t][2 + i], o[n][t + 1][i], o[n][t + 1][2 + i]);
+            }
+    };
+
+    while (walk.next(r)) {
+        const int kv = r.g / p.chunks, head0 = kv * p.per_kv + (r.g % p.chunks) * GROUP;
+        const int heads = min(GROUP, (kv + 1) * p.per_kv - head0);
+        const int len = length_of(p, r.b);
+        // Queries as the columns of the products: lane (g, c) holds columns c * D/4 ..
+        // of head 8n + g.  A power of two takes a head's largest to 2^14 .. 2^15.
+        uint32_t qb[NT][D / 16][2];
+        float f[NT][2];  // from products to scores in units of log 2
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const bool on = n * 8 + g < heads;
+            const uint4* src = reinterpret_cast<const uint4*>(p.q + int64_t(r.b) * p.q_stride + int64_t(head0 + (on ? n * 8 + g : 0)) * D + c * (D / 4));
+            uint4 raw[D / 32];
+            uint32_t top = 0;
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) {
+                raw[i] = on ? __ldg(src + i) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t u = (&raw[i].x)[j] & 0x7fff7fffu;
+                    top = max(top, max(u >> 16, u & 0xffffu));
+                }
+            }
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = int(top >> 7);  // biased exponent of the largest; 0 or 255: as it is
+            const int up = e == 0 || e == 255 ? 0 : min(141 - e, 126);
+            const float by = __uint_as_float(uint32_t(up + 127) << 23);
+            const float back = __uint_as_float(uint32_t(127 - up) << 23);
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const uint32_t u = (&raw[i].x)[j];
+                    qb[n][2 * i + j / 2][j % 2] = pack_h2(__uint_as_float(u << 16) * by, __uint_as_float(u & 0xffff0000u) * by);
+                }
+            const float unit = p.scale2 * (p.k_factor ? __ldg(p.k_factor + kv) : 1.f);
+            f[n][0] = unit * __shfl_sync(0xffffffffu, back, 8 * c);
+            f[n][1] = unit * __shfl_sync(0xffffffffu, back, 8 * c + 4);
+#pragma unroll
+            for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) o[n][t][i] = 0.f;
+            m[n][0] = m[n][1] = -INFINITY;
+            l[n][0] = l[n][1] = 0.f;
+        }
+
+        for (uint32_t t = r.t0; t < r.t1; ++t) {
+            copy_wait<G::STAGES - 1>();
+            __syncwarp();
+            const uint32_t ks = ring + slot * G::STAGE, vs = ks + G::VALUES, kss = vs + G::VALUES, vss = kss + G::SCALES;
+
+            // ---- scores: 16 keys by 8 heads
+            float s[MT][NT][4] = {};
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                uint32_t w[2][D / 32], sc[2][D / 64];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int row = mt * 16 + h * 8 + g;
+                    if constexpr (D == 64) {
+                        load_words<2>(ks + uint32_t(row * G::ROW + c * 8), w[h]);
+                        sc[h][0] = low_twice(halves_of_e4m3x2(load_u8(kss + uint32_t(row * 4 + c))));
+                    } else if constexpr (D == 128) {
+                        load_words<4>(ks + key_at<D>(row, c), w[h]);
+                        const uint32_t two = halves_of_e4m3x2(load_u16(kss + uint32_t(row * 8 + 2 * c)));
+                        sc[h][0] = low_twice(two);
+                        sc[h][1] = high_twice(two);
+                    } else {
+                        uint32_t a[4], b[4], four[1];
+                        load_words<4>(ks + key_at<D>(row, 2 * c), a);
+                        load_words<4>(ks + key_at<D>(row, 2 * c + 1), b);
+                        load_words<1>(kss + uint32_t(row * 16 + 4 * c), four);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            w[h][i] = a[i];
+                            w[h][4 + i] = b[i];
+                        }
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t two = halves_of_e4m3x2(four[0] >> (16 * i));
+                            sc[h][2 * i] = low_twice(two);
+                            sc[h][2 * i + 1] = high_twice(two);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    uint32_t a[2][4];
+                    halves_of_e2m1x8(w[0][i], a[0][0], a[0][2], a[1][0], a[1][2]);
+                    halves_of_e2m1x8(w[1][i], a[0][1], a[0][3], a[1][1], a[1][3]);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x) {
+                        a[x][0] = mul_h2(a[x][0], sc[0][i / 2]);
+                        a[x][2] = mul_h2(a[x][2], sc[0][i / 2]);
+                        a[x][1] = mul_h2(a[x][1], sc[1][i / 2]);
+                        a[x][3] = mul_h2(a[x][3], sc[1][i / 2]);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma_f16(s[mt][n], a[x], qb[n][2 * i + x][0], qb[n][2 * i + x][1]);
+                    }
+                }
+            }
+
+            // ---- weights
+            const bool cut = int(t + 1) * KEYS > len;
+            uint32_t pb[MT][NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                if (cut) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int key = int(t) * KEYS + mt * 16 + (i >> 1) * 8 + g;
+                            // a score below all others, whatever the factor's sign
+                            s[mt][n][i] = key < len ? s[mt][n][i] * f[n][i & 1] : -INFINITY;
+                        }
+                } else {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s[mt][n][i] *= f[n][i & 1];
+                }
+                float x0 = -INFINITY, x1 = -INFINITY;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    x0 = fmaxf(x0, fmaxf(s[mt][n][0], s[mt][n][2]));
+                    x1 = fmaxf(x1, fmaxf(s[mt][n][1], s[mt][n][3]));
+                }
+                // The maximum is taken anew only when a weight would pass 2^15 (from nothing: at
+                // any score); until then the one before stands for it.
+                constexpr float ROOM = WEIGHT_MOST - WEIGHT_SHIFT;
+                if (__any_sync(0xffffffffu, x0 > m[n][0] + ROOM || x1 > m[n][1] + ROOM)) {
+#pragma unroll
+                    for (int d = 4; d < 32; d <<= 1) {
+                        x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
+                        x1 = fmaxf(x1, __shfl_xor_sync(0xffffffffu, x1, d));
+                    }
+                    const float n0 = fmaxf(m[n][0], x0), n1 = fmaxf(m[n][1], x1);
+                    const float f0 = m[n][0] == -INFINITY ? 0.f : exp2_of(m[n][0] - n0);
+                    const float f1 = m[n][1] == -INFINITY ? 0.f : exp2_of(m[n][1] - n1);
+                    m[n][0] = n0;
+                    m[n][1] = n1;
+                    l[n][0] *= f0;
+                    l[n][1] *= f1;
+#pragma unroll
+                    for (int j = 0; j < D / 16; ++j) {
+                        o[n][j][0] *= f0;
+                        o[n][j][1] *= f1;
+                        o[n][j][2] *= f0;
+                        o[n][j][3] *= f1;
+                    }
+                }
+                // a head whose scores are all -inf has weights 0, not e^(-inf + inf)
+                const float b0 = m[n][0] == -INFINITY ? 0.f : m[n][0] - WEIGHT_SHIFT;
+                const float b1 = m[n][1] == -INFINITY ? 0.f : m[n][1] - WEIGHT_SHIFT;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    const float p0 = exp2_of(s[mt][n][0] - b0), p1 = exp2_of(s[mt][n][1] - b1);
+                    const float p2 = exp2_of(s[mt][n][2] - b0), p3 = exp2_of(s[mt][n][3] - b1);
+                    l[n][0] += p0 + p2;
+                    l[n][1] += p1 + p3;
+                    pb[mt][n][0] = transpose8(pack_h2(p0, p1));
+                    pb[mt][n][1] = transpose8(pack_h2(p2, p3));
+                }
+            }
+
+            // ---- output: 16 columns by 8 heads, over 16 keys
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+                constexpr int WORDS = D / 64;  // of a key's columns here
+                uint32_t w[4][WORDS], sb[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int row = mt * 16 + 4 * j + c;
+                    if constexpr (D == 64) {
+                        load_words<1>(vs + uint32_t(row * G::ROW + g * 4), w[j]);
+                        sb[j] = load_u8(vss + uint32_t(row * 4 + g / 2));
+                    } else if constexpr (D == 128) {
+                        load_words<2>(vs + value_at<D>(row, g / 2) + uint32_t(g & 1) * 8, w[j]);
+                        sb[j] = load_u8(vss + uint32_t(row * 8 + g));
+                    } else {
+                        load_words<4>(vs + value_at<D>(row, g), w[j]);
+                        sb[j] = load_u16(vss + uint32_t(row * 16 + 2 * g));
+                    }
+                }
+                // scales of the pairs of keys, for the first and the second 16 of the columns
+                uint32_t s01[2], s23[2];
+                s01[0] = halves_of_e4m3x2(__byte_perm(sb[0], sb[1], 0x0040));
+                s23[0] = halves_of_e4m3x2(__byte_perm(sb[2], sb[3], 0x0040));
+                if constexpr (D == 256) {
+                    s01[1] = halves_of_e4m3x2(__byte_perm(sb[0], sb[1], 0x0051));
+                    s23[1] = halves_of_e4m3x2(__byte_perm(sb[2], sb[3], 0x0051));
+                }
+#pragma unroll
+                for (int i = 0; i < WORDS; ++i) {
+                    constexpr uint32_t LOW = 0x0f0f0f0fu;
+                    uint32_t a[4][4];
+                    // bytes of one column of two keys
+                    halves_of_e2m1x8((w[0][i] & LOW) | ((w[1][i] << 4) & ~LOW), a[0][0], a[1][0], a[2][0], a[3][0]);
+                    halves_of_e2m1x8(((w[0][i] >> 4) & LOW) | (w[1][i] & ~LOW), a[0][1], a[1][1], a[2][1], a[3][1]);
+                    halves_of_e2m1x8((w[2][i] & LOW) | ((w[3][i] << 4) & ~LOW), a[0][2], a[1][2], a[2][2], a[3][2]);
+                    halves_of_e2m1x8(((w[2][i] >> 4) & LOW) | (w[3][i] & ~LOW), a[0][3], a[1][3], a[2][3], a[3][3]);
+#pragma unroll
+                    for (int x = 0; x < 4; ++x) {
+                        const int half = D == 256 ? i / 2 : 0;
+                        a[x][0] = mul_h2(a[x][0], s01[half]);
+                        a[x][1] = mul_h2(a[x][1], s01[half]);
+                        a[x][2] = mul_h2(a[x][2], s23[half]);
+                        a[x][3] = mul_h2(a[x][3], s23[half]);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma_f16(o[n][4 * i + x], a[x], pb[mt][n][0], pb[mt][n][1]);
+                    }
+                }
+            }
+            __syncwarp();  // every lane has read the tile before it is overwritten
+            issue();
+            if (++slot == G::STAGES) slot = 0;
+        }
+
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int d = 4; d < 32; d <<= 1) {
+                l[n][0] += __shfl_xor_sync(0xffffffffu, l[n][0], d);
+                l[n][1] += __shfl_xor_sync(0xffffffffu, l[n][1], d);
+            }
+        if (r.t1 - r.t0 == r.tiles) {
+            // the whole group: straight to the output
+            const float factor = p.value_factor(kv);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int row = n * 8 + 2 * c + i;
+                    if (row >= heads) continue;
+                    const float inv = l[n][i] == 0.f ? 0.f : factor / l[n][i];
+                    const int64_t at = int64_t(r.b) * p.Hq + head0 + row;
+                    uint2* to = reinterpret_cast<uint2*>(p.out + at * D + g * (D / 8));
+#pragma unroll
+                    for (int t = 0; t < D / 16; t += 2)
+                        to[t / 2] = make_uint2(pack_bf16(o[n][t][i] * inv, o[n][t][2 + i] * inv),
+                                               pack_bf16(o[n][t + 1][i] * inv, o[n][t + 1][2 + i] * inv));
+                    if (p.lse && g == 0)
+                        p.lse[at] = l[n][i] == 0.f ? -INFINITY : (m[n][i] - WEIGHT_SHIFT + log2f(l[n][i])) * LN2;
+                }
+        } else if (walk.pos < walk.end) {
+            head = r;
+            has_head = true;
+            put(reinterpret_cast<float*>(smem + G::SM_HEADS) + warp * G::PART, heads);
+        } else {
+            tail = r;
+            has_tail = true;
+        }
+    }
+    copy_wait<0>();
+
+    float* tails = reinterpret_cast<float*>(smem);
+    const float* firsts = reinterpret_cast<const float*>(smem + G::SM_HEADS);
+    __syncthreads();  // the rings are free
+    if (has_tail) {
+        const int kv = tail.g / p.chunks, head0 = kv * p.per_kv + (tail.g % p.chunks) * GROUP;
+        put(tails + warp * G::PART, min(GROUP, (kv + 1) * p.per_kv - head0));
+    }
+    head.tiles = has_head ? head.tiles : 0u;
+    tail.tiles = has_tail ? tail.tiles : 0u;
+    join_ranges<D, GROUP, G::WARPS, G::THREADS>(p, head, tail, warp, lane == 0, tails, firsts, small, cut_at, start, end);
+}
+
+template <int D, int NT>
+cudaError_t launch_attn4(Attn4Params& p, int grid, cudaStream_t st) {
+    using G = Geo4<D, NT>;
+    p.chunks = (p.per_kv + G::GROUP - 1) / G::GROUP;
+    p.groups = p.chunks * p.Hkv;
+    mk_paged_attention_fp4_kernel<D, NT><<<grid, G::THREADS, G::SMEM, st>>>(p);
+    return cudaGetLastError();
+}
+template <int D>
+cudaError_t launch_attn4(Attn4Params& p, int grid, cudaStream_t st) {
+    return p.per_kv <= 8 ? launch_attn4<D, 1>(p, grid, st) : launch_attn4<D, 2>(p, grid, st);
+}
+
+// Groups of up to 8 query heads per sequence (the smallest), 0 for sizes outside the limits.
+int64_t attn4_groups(int B, int Hq, int Hkv) {
+    if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0) return 0;
+    return int64_t(Hkv) * ((Hq / Hkv + 7) / 8);
+}
+
+template <int D, int NT>
+cudaError_t attn4_smem() {
+    return cudaFuncSetAttribute(mk_paged_attention_fp4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Geo4<D, NT>::SMEM);
+}
+
+}  // namespace
+
+cudaError_t attn4_kernel_attributes() {
+    for (const cudaError_t e : {attn4_smem<64, 1>(), attn4_smem<64, 2>(), attn4_smem<128, 1>(), attn4_smem<128, 2>(),
+                                attn4_smem<256, 1>(), attn4_smem<256, 2>()})
+        if (e != cudaSuccess) return e;
+    return cudaSuccess;
+}
+
+}  // namespace mk
+
+using namespace mk;
+
+extern "C" size_t mk_paged_attention_fp4_workspace_size(int B, int Hq, int Hkv) {
+    const int64_t g = attn4_groups(B, Hq, Hkv);
+    if (g == 0 || B > ATTN_MAX_B) return 0;
+    return ATTN_SLOTS_BYTES + ws_align(size_t(B) * size_t(g) * sizeof(uint32_t));
+}
+
+extern "C" mk_status_t mk_paged_attention_fp4(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                                              int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                                              const void* k_scales, const void* v_scales, int64_t scale_page_stride,
+                                              int64_t scale_token_stride, int64_t scale_head_stride, const float* k_factor,
+                                              const float* v_factor, const int32_t* block_table, const int32_t* seq_lens,
+                                              int B, int Hq, int Hkv, int D, int page_size, int max_pages, int num_pages,
+                                              float scale, void* out, float* lse, void* stream, void* workspace,
+                                              size_t ws_bytes) {
+    if (B < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || page_size < 1 || max_pages < 0 || num_pages < 0)
+        return MK_ERR_INVALID_ARG;
+    if (D != 64 && D != 128 && D != 256) return MK_ERR_UNSUPPORTED;
+    if (!std::isfinite(scale)) return MK_ERR_INVALID_ARG;
+    const int64_t groups = attn4_groups(B, Hq, Hkv);
+    const int64_t cap = int64_t(max_pages) * page_size;
+    if (B > ATTN_MAX_B || cap > (int64_t(1) << 31) - 32) return MK_ERR_UNSUPPORTED;
+    // positions in the order of tiles are 32-bit
+    const int64_t tiles = int64_t(B) * positions_of(int(cap), Geo4<256, 1>::KEYS);
+    if (tiles >= int64_t(1) << 31 || tiles * groups >= int64_t(1) << 31) return MK_ERR_UNSUPPORTED;
+    if (B > 0) {
+        if (!q || !seq_lens || !out) return MK_ERR_INVALID_ARG;
+        if (cap > 0 && (!k_cache || !v_cache || !k_scales || !v_scales || !block_table || num_pages < 1)) return MK_ERR_INVALID_ARG;
+        const size_t row = size_t(D) / 16;  // scales of a row are copied at once
+        if (!host_aligned(q, 16) || !host_aligned(out, 8) || !host_aligned(k_cache, 16) || !host_aligned(v_cache, 16) ||
+            !host_aligned(k_scales, row) || !host_aligned(v_scales, row) || !host_aligned(block_table, 4) ||
+            !host_aligned(seq_lens, 4) || !host_aligned(lse, 4) || !host_aligned(k_factor, 4) || !host_aligned(v_factor, 4))
+            return MK_ERR_INVALID_ARG;
+        if (B > 1 && (q_stride < int64_t(Hq) * D || q_stride % 8 != 0)) return MK_ERR_INVALID_ARG;
+        // the stride of a dimension of one is never used
+        const auto used = [](int n, int64_t s) { return n > 1 ? s : int64_t(0); };
+        for (const int64_t v : {used(num_pages, page_stride), used(page_size, token_stride), used(Hkv, head_stride)})
+            if (v < 0 || v % 16 != 0) return MK_ERR_INVALID_ARG;
+        for (const int64_t v : {used(num_pages, scale_page_stride), used(page_size, scale_token_stride), used(Hkv, scale_head_stride)})
+            if (v < 0 || v % int64_t(row) != 0) return MK_ERR_INVALID_ARG;
+    }
+    int dev = 0, sms = 0;
+    DevError* err = nullptr;
+    mk_status_t s = host_device(&dev, &sms, &err);
+    if (s != MK_OK) return s;
+    if (B == 0) return MK_OK;
+    const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const size_t need = mk_paged_attention_fp4_workspace_size(B, Hq, Hkv);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    Workspace cached;  // held until the launch below
+    if (ws) {
+        if (ws_bytes < need || !host_aligned(ws, 256)) return MK_ERR_WORKSPACE;
+    } else {
+        if ((s = cached.get(WS_ATTN4, dev, st, need, need)) != MK_OK) return s;
+        ws = cached.data();
+    }
+    Attn4Params p{};
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.k = static_cast<const uint8_t*>(k_cache);
+    p.v = static_cast<const uint8_t*>(v_cache);
+    p.k_scales = static_cast<const uint8_t*>(k_scales);
+    p.v_scales = static_cast<const uint8_t*>(v_scales);
+    p.k_factor = k_factor;
+    p.v_factor = v_factor;
+    p.table = block_table;
+    p.lens = seq_lens;
+    p.out = static_cast<__nv_bfloat16*>(out);
+    p.lse = lse;
+    p.slots = reinterpret_cast<float*>(ws);
+    p.arrived = reinterpret_cast<uint32_t*>(ws + ATTN_SLOTS_BYTES);
+    p.err = err;
+    p.q_stride = q_stride;
+    p.page_stride = page_stride;
+    p.token_stride = token_stride;
+    p.head_stride = head_stride;
+    p.scale_page = scale_page_stride;
+    p.scale_token = scale_token_stride;
+    p.scale_head = scale_head_stride;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.page_size = page_size;
+    p.max_pages = max_pages;
+    p.num_pages = num_pages;
+    p.per_kv = Hq / Hkv;
+    p.scale2 = scale * LOG2E;
+    const int grid = std::min(sms, ATTN_MAX_CTAS);
+    const cudaError_t e = D == 64 ? launch_attn4<64>(p, grid, st) : D == 128 ? launch_attn4<128>(p, grid, st) : launch_attn4<256>(p, grid, st);
+    return e == cudaSuccess ? MK_OK : MK_ERR_CUDA;
+}

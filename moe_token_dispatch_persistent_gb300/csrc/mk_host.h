@@ -28,11 +28,12 @@ cudaError_t error_word(DevError** out);
 mk_status_t host_device(int* dev, int* sms, DevError** err);
 
 // Kernel attributes of the units below, set once per device.
-cudaError_t attn_kernel_attributes();
+cudaError_t attn_kernel_attributes();  // mk_attn4.cu's too
+cudaError_t attn4_kernel_attributes();
 cudaError_t ffn_kernel_attributes();
 
 // Workspace caches, one per operator family: their control blocks differ.
-enum WsKind { WS_DISPATCH = 0, WS_EP = 1, WS_ATTN = 2, WS_FFN = 3, WS_KINDS = 4 };
+enum WsKind { WS_DISPATCH = 0, WS_EP = 1, WS_ATTN = 2, WS_FFN = 3, WS_ATTN4 = 4, WS_PAGES = 5, WS_KINDS = 6 };
 
 // The library's workspace of a kind for (device, stream), grown on demand on
 // `st`.  Of a new buffer the first `zero_bytes` are zeroed (WS_DISPATCH) or all

@@ -83,3 +83,44 @@ def test_qk_norm_rope_binding_refuses_wrong_tensors():
     q = torch.zeros((2, 4, 64), dtype=torch.bfloat16)
     with pytest.raises(ValueError):
         mk.qk_norm_rope(q, q, torch.zeros(2, dtype=torch.int32), torch.zeros(32))  # not on a GPU
+
+
+ATTN = dict(q=64, q_stride=1024, k_cache=64, v_cache=64, page_stride=4096, token_stride=256, head_stride=64, k_scales=64,
+            v_scales=64, scale_page_stride=512, scale_token_stride=32, scale_head_stride=8, k_factor=64, v_factor=64,
+            block_table=64, seq_lens=64, B=2, Hq=8, Hkv=4, D=128, page_size=16, max_pages=10, num_pages=20, scale=0.1, out=64,
+            lse=64, stream=1)
+
+
+@pytest.mark.parametrize("change,want", [
+    (dict(B=-1), BAD), (dict(Hq=0), BAD), (dict(Hkv=0), BAD), (dict(Hkv=3), BAD), (dict(page_size=0), BAD),
+    (dict(max_pages=-1), BAD), (dict(num_pages=-1), BAD), (dict(num_pages=0), BAD),
+    (dict(D=96), UNSUPPORTED), (dict(B=4097), UNSUPPORTED),
+    (dict(max_pages=2 ** 27), UNSUPPORTED),                # a length would pass 31 bits
+    (dict(B=4096, max_pages=2 ** 17), UNSUPPORTED),         # the tiles of all sequences would
+    (dict(scale=NAN), BAD), (dict(scale=INF), BAD),
+    (dict(q=None), BAD), (dict(k_cache=None), BAD), (dict(v_cache=None), BAD), (dict(k_scales=None), BAD),
+    (dict(v_scales=None), BAD), (dict(block_table=None), BAD), (dict(seq_lens=None), BAD), (dict(out=None), BAD),
+    (dict(q=72), BAD), (dict(k_cache=72), BAD), (dict(v_cache=72), BAD), (dict(k_scales=68), BAD), (dict(v_scales=68), BAD),
+    (dict(out=68), BAD), (dict(lse=66), BAD), (dict(k_factor=66), BAD), (dict(v_factor=66), BAD),
+    (dict(q_stride=1020), BAD), (dict(q_stride=1028), BAD),
+    (dict(page_stride=4104), BAD), (dict(token_stride=248), BAD), (dict(head_stride=-64), BAD),
+    (dict(scale_page_stride=508), BAD), (dict(scale_token_stride=36), BAD), (dict(scale_head_stride=-8), BAD),
+])
+def test_paged_attention_fp4_refusals(change, want):
+    assert mk.mk_paged_attention_fp4(**{**ATTN, **change}) == want
+
+
+def test_paged_attention_fp4_workspace_size():
+    one = mk.mk_paged_attention_fp4_workspace_size(1, 32, 8)
+    assert 0 < one <= mk.mk_paged_attention_fp4_workspace_size(4096, 32, 8)
+    for args in ((1, 32, 5), (4097, 32, 8), (-1, 32, 8)):
+        assert mk.mk_paged_attention_fp4_workspace_size(*args) == 0
+
+
+def test_paged_attention_fp4_binding_refuses_wrong_tensors():
+    torch = pytest.importorskip("torch")
+    q = torch.zeros((1, 8, 64), dtype=torch.bfloat16)
+    z = mk.fp4_cache(2, 16, 4, 64, device="cpu")
+    assert z["k_cache"].shape == (2, 16, 4, 32) and z["k_scales"].shape == (2, 16, 4, 4)
+    with pytest.raises(ValueError):
+        mk.paged_attention_fp4(q, block_table=torch.zeros((1, 2), dtype=torch.int32), seq_lens=torch.ones(1, dtype=torch.int32), **z)
