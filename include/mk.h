@@ -512,6 +512,67 @@ mk_status_t mk_paged_attention_fp4(const void* q, int64_t q_stride, const void* 
 /* Workspace bytes mk_paged_attention_fp4 needs (0 for invalid sizes). */
 size_t mk_paged_attention_fp4_workspace_size(int B, int Hq, int Hkv);
 
+/* Pages of a pool, shared between sequences.  The state is on the device:
+ *   block_table[rows,max_pages] i32: row s holds the pages of sequence s, of
+ *     which ceil(seq_lens[s] / page_size) count; entries behind them are
+ *     neither read nor changed,
+ *   seq_lens[rows] i32,
+ *   refs[num_pages] i32: the rows that hold a page; 0: it is free.
+ * Lists (parent, child, seqs, count: n entries, i32) are on the device too.  A
+ * call whose list names a sequence outside the table, one sequence twice (a
+ * parent may be), a count outside [0, most] or more room than a row has, or
+ * that would need more pages than are free, changes nothing; mk_get_status()
+ * then reports MK_ERR_DEVICE_FAULT.  An entry that is no page is left out, and
+ * reported.  Results are whole numbers and the same for equal states.
+ * Buffers: n_caches of them, each with num_pages pages of page_bytes[i] bytes,
+ * page_strides[i] bytes apart, from caches[i] on (device); the three arrays are
+ * HOST arrays, read before the call returns.  Pages move as fast as a copy where
+ * addresses, strides and sizes are multiples of 16 bytes.
+ * Limits: rows <= 65536, n <= 4096, max_pages*page_size < 2^31, num_pages <=
+ * 2^30, page_bytes <= 2^31.  workspace: NULL (library cache) or
+ * mk_pages_workspace_size(max_pages, num_pages, n) bytes, 256-byte aligned, of
+ * any content; one stream at a time. */
+
+/* Page src[i] to page dst[i], i < n, in every buffer.  The pages of dst differ,
+ * and none of them is in src.  n has no limit here. */
+mk_status_t mk_copy_pages(void* const* caches, const int64_t* page_strides, const int64_t* page_bytes, int n_caches,
+                          int num_pages, const int32_t* src, const int32_t* dst, int n, void* stream);
+
+/* Sequence child[i] gives its pages back and from now on holds those of
+ * parent[i] as they were before the call, the last one, which may not be full,
+ * among them (mk_extend_sequences copies it when one of them goes on).  A child
+ * may be another's parent, or its own. */
+mk_status_t mk_fork_sequences(int32_t* block_table, int32_t* seq_lens, int32_t* refs, int rows, int max_pages,
+                              int num_pages, int page_size, const int32_t* parent, const int32_t* child, int n,
+                              void* stream, void* workspace, size_t ws_bytes);
+
+/* The sequences of the list give their pages back; their lengths become 0. */
+mk_status_t mk_free_sequences(const int32_t* block_table, int32_t* seq_lens, int32_t* refs, int rows, int max_pages,
+                              int num_pages, int page_size, const int32_t* seqs, int n, void* stream);
+
+/* Room for count[i] <= most new tokens of sequence seqs[i], in the order of the
+ * list: if its last page is not full and other rows hold it, those of the list
+ * that were already given a copy not counted, it gets a copy of it (in every buffer); then
+ * as many more pages as it needs.  New pages are the lowest free ones.
+ * slots[n,most] i64 (may be NULL): the place of each new token, page *
+ * page_size + token, -1 behind the last.  seq_lens counts the new tokens. */
+mk_status_t mk_extend_sequences(int32_t* block_table, int32_t* seq_lens, int32_t* refs, int rows, int max_pages,
+                                int num_pages, int page_size, const int32_t* seqs, const int32_t* count, int n, int most,
+                                int64_t* slots, void* const* caches, const int64_t* page_strides,
+                                const int64_t* page_bytes, int n_caches, void* stream, void* workspace, size_t ws_bytes);
+
+/* The pages in use, `used` of them, become the first ones: the i-th one of
+ * index >= used moves to the i-th free one below, in every buffer, and table_out
+ * and refs_out (which may be block_table and refs) say so; the buffers' pages
+ * from used on are then free. */
+mk_status_t mk_compact_pages(const int32_t* block_table, const int32_t* seq_lens, const int32_t* refs, int rows,
+                             int max_pages, int num_pages, int page_size, int32_t* table_out, int32_t* refs_out,
+                             void* const* caches, const int64_t* page_strides, const int64_t* page_bytes, int n_caches,
+                             void* stream, void* workspace, size_t ws_bytes);
+
+/* Workspace bytes that each of these four needs at most (0 for invalid sizes). */
+size_t mk_pages_workspace_size(int max_pages, int num_pages, int n);
+
 /* Synchronise `stream`, then return and clear the device error word
  * (MK_ERR_TIMEOUT / MK_ERR_DEVICE_FAULT), or MK_ERR_CUDA if the stream holds
  * a CUDA error.  MK_OK when nothing was recorded. */

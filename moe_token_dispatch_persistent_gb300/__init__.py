@@ -68,6 +68,12 @@ ABI_FUNCTIONS = (
     "mk_qk_norm_rope",
     "mk_paged_attention_fp4",
     "mk_paged_attention_fp4_workspace_size",
+    "mk_copy_pages",
+    "mk_fork_sequences",
+    "mk_free_sequences",
+    "mk_extend_sequences",
+    "mk_compact_pages",
+    "mk_pages_workspace_size",
     "mk_workspace_size",
     "mk_get_status",
     "mk_last_error_detail",
@@ -200,6 +206,21 @@ def lib(path: str | None = None) -> ctypes.CDLL:
     h.mk_paged_attention_fp4.restype = _i
     h.mk_paged_attention_fp4_workspace_size.argtypes = [_i, _i, _i]
     h.mk_paged_attention_fp4_workspace_size.restype = ctypes.c_size_t
+    pool = [_p, _p, _p, _i, _i, _i, _i]
+    buffers = [_p, _p, _p, _i]
+    end = [_p, _p, ctypes.c_size_t]
+    h.mk_copy_pages.argtypes = buffers + [_i, _p, _p, _i, _p]
+    h.mk_copy_pages.restype = _i
+    h.mk_fork_sequences.argtypes = pool + [_p, _p, _i] + end
+    h.mk_fork_sequences.restype = _i
+    h.mk_free_sequences.argtypes = pool + [_p, _i, _p]
+    h.mk_free_sequences.restype = _i
+    h.mk_extend_sequences.argtypes = pool + [_p, _p, _i, _i, _p] + buffers + end
+    h.mk_extend_sequences.restype = _i
+    h.mk_compact_pages.argtypes = pool + [_p, _p] + buffers + end
+    h.mk_compact_pages.restype = _i
+    h.mk_pages_workspace_size.argtypes = [_i, _i, _i]
+    h.mk_pages_workspace_size.restype = ctypes.c_size_t
     h.mk_get_status.argtypes = [_p]
     h.mk_get_status.restype = _i
     h.mk_last_error_detail.argtypes = [ctypes.POINTER(ctypes.c_int32)] * 3
@@ -954,3 +975,188 @@ def paged_attention_fp4(q, k_cache, v_cache, k_scales, v_scales, block_table, se
         _finish(status, "mk_paged_attention_fp4", stream, other, check,
                 (q, k_cache, v_cache, k_scales, v_scales, k_factor, v_factor, block_table, seq_lens, workspace), (out, lse))
     return {"out": out, "lse": lse}
+
+
+# Buffers in the C forms below: a list of (device pointer or tensor, bytes between pages, bytes of a page).
+
+def _buffers(caches):
+    n = len(caches)
+    return ((ctypes.c_void_p * n)(*[_ptr(b[0]) for b in caches]), (ctypes.c_int64 * n)(*[b[1] for b in caches]),
+            (ctypes.c_int64 * n)(*[b[2] for b in caches]), n)
+
+
+def mk_copy_pages(caches, num_pages, src, dst, n, stream=None) -> int:
+    return int(lib().mk_copy_pages(*_buffers(caches), num_pages, _ptr(src), _ptr(dst), n, _stream(stream)))
+
+
+def mk_fork_sequences(block_table, seq_lens, refs, rows, max_pages, num_pages, page_size, parent, child, n, stream=None,
+                      workspace=None, ws_bytes: int = 0) -> int:
+    return int(lib().mk_fork_sequences(_ptr(block_table), _ptr(seq_lens), _ptr(refs), rows, max_pages, num_pages, page_size,
+                                       _ptr(parent), _ptr(child), n, _stream(stream), _ptr(workspace), int(ws_bytes)))
+
+
+def mk_free_sequences(block_table, seq_lens, refs, rows, max_pages, num_pages, page_size, seqs, n, stream=None) -> int:
+    return int(lib().mk_free_sequences(_ptr(block_table), _ptr(seq_lens), _ptr(refs), rows, max_pages, num_pages, page_size,
+                                       _ptr(seqs), n, _stream(stream)))
+
+
+def mk_extend_sequences(block_table, seq_lens, refs, rows, max_pages, num_pages, page_size, seqs, count, n, most, slots,
+                        caches, stream=None, workspace=None, ws_bytes: int = 0) -> int:
+    return int(lib().mk_extend_sequences(_ptr(block_table), _ptr(seq_lens), _ptr(refs), rows, max_pages, num_pages,
+                                         page_size, _ptr(seqs), _ptr(count), n, most, _ptr(slots), *_buffers(caches),
+                                         _stream(stream), _ptr(workspace), int(ws_bytes)))
+
+
+def mk_compact_pages(block_table, seq_lens, refs, rows, max_pages, num_pages, page_size, table_out, refs_out, caches,
+                     stream=None, workspace=None, ws_bytes: int = 0) -> int:
+    return int(lib().mk_compact_pages(_ptr(block_table), _ptr(seq_lens), _ptr(refs), rows, max_pages, num_pages, page_size,
+                                      _ptr(table_out), _ptr(refs_out), *_buffers(caches), _stream(stream), _ptr(workspace),
+                                      int(ws_bytes)))
+
+
+def mk_pages_workspace_size(max_pages, num_pages, n) -> int:
+    return int(lib().mk_pages_workspace_size(max_pages, num_pages, n))
+
+
+def _page_buffers(caches, dev, pages=None):
+    """C arrays of tensors whose first dimension is the page and whose pages are
+    dense, in whatever order of the other dimensions."""
+    base, strides, sizes = [], [], []
+    seen = None
+    for t in caches:
+        if t.get_device() != dev:
+            raise ValueError("the caches must be on one device")
+        layout = (t.shape, t.stride(), t.dtype)
+        if layout != seen:  # a layer's is the one before's
+            shape, stride, _ = seen = layout
+            if len(shape) < 2:
+                raise ValueError("a cache's first dimension is its pages")
+            if pages is None:
+                pages = shape[0]
+            dense = 1
+            for s, n in sorted(zip(stride[1:], shape[1:])):
+                if n > 1 and s != dense:
+                    raise ValueError("the values of a page must lie one after the other")
+                dense *= n
+            if shape[0] != pages:
+                raise ValueError("the caches must have the same number of pages")
+            size = t.element_size()
+            block, step = dense * size, stride[0] * size
+        base.append(t.data_ptr())
+        strides.append(step)
+        sizes.append(block)
+    n = len(base)
+    return ((ctypes.c_void_p * n)(*base), (ctypes.c_int64 * n)(*strides), (ctypes.c_int64 * n)(*sizes), n), pages
+
+
+def _i32_list(t, dev, n, what):
+    if t.dtype is not _torch.int32 or t.get_device() != dev or not t.is_contiguous() or t.dim() != 1 or (
+            n is not None and t.shape[0] != n):
+        raise ValueError(f"{what} must be i32 on the table's device, one entry for each sequence of the list")
+    return t.shape[0]
+
+
+def _pool(block_table, seq_lens, refs, page_size):
+    """Arguments of a pool that every entry takes."""
+    torch = _torch or _load_torch()
+    dev = block_table.get_device()
+    if dev < 0 or block_table.dtype is not torch.int32 or block_table.dim() != 2 or not block_table.is_contiguous():
+        raise ValueError("block_table must be a CUDA i32 [rows,max_pages] tensor")
+    _on_device(dev)
+    rows, max_pages = block_table.shape
+    for t, shape, what in ((seq_lens, (rows,), "seq_lens must be i32 [rows]"), (refs, None, "refs must be i32 [pages]")):
+        if t.dtype is not torch.int32 or t.get_device() != dev or t.dim() != 1 or not t.is_contiguous() or (
+                shape is not None and t.shape != shape):
+            raise ValueError(what + " on the table's device")
+    return dev, (block_table.data_ptr(), seq_lens.data_ptr(), refs.data_ptr(), rows, max_pages, refs.shape[0], page_size)
+
+
+def copy_pages(caches, src, dst, stream=None, check=True):
+    """Copies page ``src[i]`` to page ``dst[i]`` in each of ``caches``, tensors
+    [pages, ...] whose pages are dense (a layer's keys or values, in bf16 or 4
+    bits, or their scales); src and dst i32 on the caches' device.  The pages of
+    dst differ, and none of them is in src."""
+    torch = _torch or _load_torch()
+    dev = src.get_device()
+    if dev < 0 or src.dtype is not torch.int32:
+        raise ValueError("src must be a CUDA i32 tensor")
+    _on_device(dev)
+    n = _i32_list(src, dev, None, "src")
+    _i32_list(dst, dev, n, "dst")
+    buffers, pages = _page_buffers(caches, dev)
+    other = None if stream is None else _other_stream(stream, dev)
+    status = lib().mk_copy_pages(*buffers, pages or 0, src.data_ptr(), dst.data_ptr(), n,
+                                 _raw_stream(dev) if stream is None else _stream(stream))
+    if status or check or other is not None:
+        _finish(status, "mk_copy_pages", stream, other, check, (src, dst, *caches), ())
+
+
+def fork_sequences(block_table, seq_lens, refs, parent, child, page_size, stream=None, workspace=None, ws_bytes=0, check=True):
+    """Sequence ``child[i]`` gives its pages back and shares those of
+    ``parent[i]`` (as before the call): block_table[rows,max_pages],
+    seq_lens[rows], refs[pages], parent and child, all i32, change in place."""
+    dev, pool = _pool(block_table, seq_lens, refs, page_size)
+    n = _i32_list(child, dev, None, "child")
+    _i32_list(parent, dev, n, "parent")
+    other = None if stream is None else _other_stream(stream, dev)
+    status = lib().mk_fork_sequences(*pool, parent.data_ptr(), child.data_ptr(), n,
+                                     _raw_stream(dev) if stream is None else _stream(stream), _ptr(workspace), ws_bytes)
+    if status or check or other is not None:
+        _finish(status, "mk_fork_sequences", stream, other, check, (block_table, seq_lens, refs, parent, child, workspace), ())
+
+
+def free_sequences(block_table, seq_lens, refs, seqs, page_size, stream=None, check=True):
+    """The sequences ``seqs`` (i32) give their pages back; their lengths become 0."""
+    dev, pool = _pool(block_table, seq_lens, refs, page_size)
+    n = _i32_list(seqs, dev, None, "seqs")
+    other = None if stream is None else _other_stream(stream, dev)
+    status = lib().mk_free_sequences(*pool, seqs.data_ptr(), n, _raw_stream(dev) if stream is None else _stream(stream))
+    if status or check or other is not None:
+        _finish(status, "mk_free_sequences", stream, other, check, (block_table, seq_lens, refs, seqs), ())
+
+
+def extend_sequences(block_table, seq_lens, refs, seqs, count, most, caches, page_size, stream=None, workspace=None,
+                     ws_bytes=0, check=True):
+    """Makes room for ``count[i]`` (at most ``most``) new tokens of sequence
+    ``seqs[i]``: a last page that is not full and shared is copied in each of
+    ``caches`` first, new pages are the lowest free ones.  Returns their places,
+    i64 [len(seqs), most] (-1 behind the last), as ``qk_norm_rope`` takes them."""
+    dev, pool = _pool(block_table, seq_lens, refs, page_size)
+    n = _i32_list(seqs, dev, None, "seqs")
+    _i32_list(count, dev, n, "count")
+    buffers, _ = _page_buffers(caches, dev, refs.shape[0])
+    other = None if stream is None else _other_stream(stream, dev)
+    slots = (_empty if other is None else _empty_on(other))((n, most), (most, 1), _torch.int64, dev)
+    status = lib().mk_extend_sequences(*pool, seqs.data_ptr(), count.data_ptr(), n, most, slots.data_ptr(), *buffers,
+                                       _raw_stream(dev) if stream is None else _stream(stream), _ptr(workspace), ws_bytes)
+    if status or check or other is not None:
+        _finish(status, "mk_extend_sequences", stream, other, check,
+                (block_table, seq_lens, refs, seqs, count, workspace, *caches), (slots,))
+    return slots
+
+
+def compact_pages(block_table, seq_lens, refs, caches, page_size, table_out=None, refs_out=None, stream=None, workspace=None,
+                  ws_bytes=0, check=True):
+    """Moves the pages in use to the front of each of ``caches``.  Returns
+    ``block_table`` and ``refs`` as they are then, in ``table_out`` and
+    ``refs_out`` when given (which may be block_table and refs themselves)."""
+    dev, pool = _pool(block_table, seq_lens, refs, page_size)
+    buffers, _ = _page_buffers(caches, dev, refs.shape[0])
+    other = None if stream is None else _other_stream(stream, dev)
+    empty = _empty if other is None else _empty_on(other)
+    made = []
+    i32 = _torch.int32
+    if table_out is None:
+        made.append(table_out := empty((pool[3], pool[4]), (pool[4], 1), i32, dev))
+    elif table_out.dtype is not i32 or table_out.get_device() != dev or table_out.shape != block_table.shape or not table_out.is_contiguous():
+        raise ValueError("table_out must be like block_table")
+    if refs_out is None:
+        made.append(refs_out := empty((pool[5],), (1,), i32, dev))
+    elif refs_out.dtype is not i32 or refs_out.get_device() != dev or refs_out.shape != refs.shape or not refs_out.is_contiguous():
+        raise ValueError("refs_out must be like refs")
+    status = lib().mk_compact_pages(*pool, table_out.data_ptr(), refs_out.data_ptr(), *buffers,
+                                    _raw_stream(dev) if stream is None else _stream(stream), _ptr(workspace), ws_bytes)
+    if status or check or other is not None:
+        _finish(status, "mk_compact_pages", stream, other, check,
+                (block_table, seq_lens, refs, table_out, refs_out, workspace, *caches), made)
+    return {"block_table": table_out, "refs": refs_out}

@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_build")
 LIB = os.path.join(OUT_DIR, "libmk.so")
 UNITS = ["mk_kernels.cu", "mk_api.cu", "mk_noalloc.cu", "mk_norm.cu", "mk_attn.cu", "mk_ffn.cu",
-         "mk_rope.cu", "mk_attn4.cu"]
+         "mk_rope.cu", "mk_attn4.cu", "mk_pages.cu"]
 
 NVCC = os.environ.get("NVCC", "nvcc")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

@@ -124,3 +124,71 @@ def test_paged_attention_fp4_binding_refuses_wrong_tensors():
     assert z["k_cache"].shape == (2, 16, 4, 32) and z["k_scales"].shape == (2, 16, 4, 4)
     with pytest.raises(ValueError):
         mk.paged_attention_fp4(q, block_table=torch.zeros((1, 2), dtype=torch.int32), seq_lens=torch.ones(1, dtype=torch.int32), **z)
+
+
+POOL = dict(block_table=64, seq_lens=64, refs=64, rows=4, max_pages=10, num_pages=20, page_size=16, n=2, stream=1)
+BUF = dict(caches=[(64, 1024, 512)])
+FORK = (mk.mk_fork_sequences, dict(POOL, parent=64, child=64))
+FREE = (mk.mk_free_sequences, dict(POOL, seqs=64))
+EXTEND = (mk.mk_extend_sequences, dict(POOL, seqs=64, count=64, most=3, slots=64, **BUF))
+COMPACT = (mk.mk_compact_pages, {k: v for k, v in dict(POOL, table_out=64, refs_out=64, **BUF).items() if k != "n"})
+COPY = (mk.mk_copy_pages, dict(num_pages=20, src=64, dst=64, n=2, stream=1, **BUF))
+ENTRIES = [FORK, FREE, EXTEND, COMPACT]
+NAMES = ["fork", "free", "extend", "compact"]
+
+
+@pytest.mark.parametrize("entry", ENTRIES, ids=NAMES)
+@pytest.mark.parametrize("change,want", [
+    (dict(rows=-1), BAD), (dict(max_pages=-1), BAD), (dict(num_pages=-1), BAD), (dict(page_size=0), BAD),
+    (dict(rows=65537), UNSUPPORTED), (dict(max_pages=2 ** 27), UNSUPPORTED), (dict(num_pages=2 ** 30 + 1), UNSUPPORTED),
+    (dict(block_table=None), BAD), (dict(seq_lens=None), BAD), (dict(refs=None), BAD),
+    (dict(block_table=66), BAD), (dict(seq_lens=66), BAD), (dict(refs=66), BAD),
+])
+def test_pool_refusals(entry, change, want):
+    call, fields = entry
+    assert call(**{**fields, **change}) == want
+
+
+@pytest.mark.parametrize("entry", [FORK, FREE, EXTEND, COPY], ids=["fork", "free", "extend", "copy"])
+def test_list_refusals(entry):
+    call, fields = entry
+    for name in ("parent", "child", "seqs", "count", "src", "dst"):
+        if name in fields:
+            assert call(**{**fields, name: None}) == BAD
+            assert call(**{**fields, name: 66}) == BAD
+    assert call(**{**fields, "n": -1}) == BAD
+    if call is not mk.mk_copy_pages:
+        assert call(**{**fields, "n": 4097}) == UNSUPPORTED
+
+
+@pytest.mark.parametrize("entry", [EXTEND, COMPACT, COPY], ids=["extend", "compact", "copy"])
+@pytest.mark.parametrize("caches", [[(None, 1024, 512)], [(64, 511, 512)], [(64, 1024, 0)], [(64, 2 ** 33, 2 ** 31 + 1)],
+                                    [(64, 1024, 512), (64, -1, 512)]])
+def test_buffer_refusals(entry, caches):
+    call, fields = entry
+    assert call(**{**fields, "caches": caches}) == BAD
+
+
+def test_extend_and_compact_refusals():
+    assert mk.mk_extend_sequences(**{**EXTEND[1], "most": -1}) == BAD
+    assert mk.mk_extend_sequences(**{**EXTEND[1], "slots": 68}) == BAD
+    for name in ("table_out", "refs_out"):
+        assert mk.mk_compact_pages(**{**COMPACT[1], name: None}) == BAD
+        assert mk.mk_compact_pages(**{**COMPACT[1], name: 66}) == BAD
+
+
+def test_pages_workspace_size():
+    assert 0 < mk.mk_pages_workspace_size(10, 20, 2) < mk.mk_pages_workspace_size(1000, 20, 4096)
+    for args in ((-1, 20, 2), (10, -1, 2), (10, 20, 4097), (10, 20, -1)):
+        assert mk.mk_pages_workspace_size(*args) == 0
+
+
+def test_page_operators_bindings_refuse_wrong_tensors():
+    torch = pytest.importorskip("torch")
+    z = torch.zeros(4, dtype=torch.int32)
+    table = torch.zeros((4, 4), dtype=torch.int32)
+    for call in (lambda: mk.copy_pages([], z, z), lambda: mk.fork_sequences(table, z, z, z, z, 4),
+                 lambda: mk.free_sequences(table, z, z, z, 4), lambda: mk.extend_sequences(table, z, z, z, z, 1, [], 4),
+                 lambda: mk.compact_pages(table, z, z, [], 4)):
+        with pytest.raises(ValueError):
+            call()
