@@ -82,17 +82,24 @@ struct Attn4Params {
     int64_t scale_page, scale_token, scale_head;     // bytes
     int B, Hq, Hkv, page_size, max_pages, num_pages;
     int per_kv, chunks, groups;
+    int page_shift;                    // log2 of page_size, or -1
     float scale2;                      // scale * log2(e)
 
     __device__ float value_factor(int kv) const { return v_factor ? __ldg(v_factor + kv) : 1.f; }
 };
 
 __device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
+    asm(
         "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%10, %10, %10, %10};"
+        : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
 __device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
     uint32_t r;
@@ -112,46 +119,49 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
 __device__ __forceinline__ uint32_t low_twice(uint32_t h2) { return __byte_perm(h2, 0, 0x1010); }
 __device__ __forceinline__ uint32_t high_twice(uint32_t h2) { return __byte_perm(h2, 0, 0x3232); }
 
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// The first n bytes, then zeros.
+__device__ __forceinline__ void copy_part(uint32_t dst, const void* src, int n) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
 template <int BYTES>
 __device__ __forceinline__ void copy_small(uint32_t dst, const void* src, bool ok) {
     if constexpr (BYTES == 16) copy16(dst, src, ok);
     else asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(BYTES), "r"(ok ? BYTES : 0) : "memory");
 }
 template <int WORDS>
-__device__ __forceinline__ void load_words(uint32_t addr, uint32_t (&w)[WORDS]) {
-    if constexpr (WORDS == 1) asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr) : "memory");
-    else if constexpr (WORDS == 2) asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr) : "memory");
-    else
-        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(addr) : "memory");
+__device__ __forceinline__ void load_words(const uint8_t* at, uint32_t (&w)[WORDS]) {
+    if constexpr (WORDS == 1) {
+        w[0] = *reinterpret_cast<const uint32_t*>(at);
+    } else if constexpr (WORDS == 2) {
+        const uint2 u = *reinterpret_cast<const uint2*>(at);
+        w[0] = u.x;
+        w[1] = u.y;
+    } else {
+        const uint4 u = *reinterpret_cast<const uint4*>(at);
+        w[0] = u.x;
+        w[1] = u.y;
+        w[2] = u.z;
+        w[3] = u.w;
+    }
 }
-__device__ __forceinline__ uint32_t load_u8(uint32_t addr) {
-    uint32_t r;
-    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
-    return r;
-}
-__device__ __forceinline__ uint32_t load_u16(uint32_t addr) {
-    uint32_t r;
-    asm volatile("ld.shared.u16 %0, [%1];" : "=r"(r) : "r"(addr) : "memory");
-    return r;
+__device__ __forceinline__ uint32_t load_u16(const uint8_t* at) { return *reinterpret_cast<const uint16_t*>(at); }
+
+// The key of the products' row r, of each 8: an order in which the lanes that read
+// shared memory together meet different banks (rows of D/2 bytes lie in order).
+template <int D>
+__device__ __forceinline__ int key_of(int r) {
+    return D == 64 ? int(0x57463120u >> (4 * r) & 7u) : r ^ ((r >> 1) & 1);
 }
 
-// Where a row's 16-byte chunk lies in its tile, without bank conflicts for the
-// reads below.  Keys lie in order.  Of values, keys 2c, 2c + 1, 2c + 8 and 2c + 9
-// of 16 go to a lane, so rows c, 4 + c, 8 + c, 12 + c hold them.
-template <int D>
-__device__ __forceinline__ uint32_t key_at(int row, int chunk) {
-    return uint32_t(row * (D / 2) + ((D == 256 ? chunk ^ (row & 1) : chunk) << 4));
-}
-__device__ __forceinline__ int value_row(int key) { return (key & ~7) | ((key & 1) << 2) | ((key >> 1) & 3); }
-template <int D>
-__device__ __forceinline__ uint32_t value_at(int row, int chunk) {
-    return uint32_t(row * (D / 2) + ((D == 64 ? chunk : D == 128 ? chunk ^ (row & 2) : chunk ^ ((row & 3) << 1)) << 4));
-}
-
-template <int D, int NT>
+// LINEAR: the keys of a tile lie in one page, a head's rows one after the other, so
+// a tile's copies have one base.  Otherwise every row is looked up.
+template <int D, int NT, bool LINEAR>
 __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp4_kernel(const Attn4Params p) {
     using G = Geo4<D, NT>;
-    constexpr int KEYS = G::KEYS, GROUP = G::GROUP, MT = KEYS / 16;
+    constexpr int KEYS = G::KEYS, GROUP = G::GROUP, MT = KEYS / 16, ROW = G::ROW, SROW = G::SROW;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = lane >> 2, c = lane & 3;  // row and pair of columns of this lane in the products
@@ -170,75 +180,140 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
     const uint32_t wstart = start + warp_cut.start(warp), wend = start + warp_cut.start(warp + 1);
 
     // ---- this warp's ring: loads run STAGES tiles ahead, across groups
-    const uint32_t ring = smem_u32(smem) + uint32_t(warp) * G::RING;
+    uint8_t* const ring_ptr = smem + warp * G::RING;
+    const uint32_t ring = smem_u32(ring_ptr);
     Walk load_walk{wstart, wend, prefix, p.B, groups, false};
     Range lr;
     uint32_t load_tile = 0;
     int load_len = 0;
     bool more = true;
     lr.t1 = 0;
-    // A lane looks up the rows of one key, two tiles before they are copied.
-    struct Ahead {
-        int64_t row, srow;  // byte offsets, -1: past the end
-        bool have;
-    } ahead[2];
-    auto look_up = [&](Ahead& a) {
-        a.have = false;
-        if (!more) return;
+    uint32_t load_slot = 0;
+    constexpr int CHUNKS = ROW / 16, PIECES = KEYS * CHUNKS / 32;  // of a row; of a lane
+    // The next tile's group and length; false when the range has no more.
+    auto next_tile = [&]() -> bool {
+        if (!more) return false;
         if (load_tile >= lr.t1) {
-            if (!load_walk.next(lr)) {
-                more = false;
-                return;
-            }
+            if (!load_walk.next(lr)) return more = false;
             load_len = length_of(p, lr.b);
             load_tile = lr.t0;
         }
-        a.have = true;
-        a.row = a.srow = -1;
+        return true;
+    };
+    auto page_of = [&](int slot) { return __ldg(p.table + int64_t(lr.b) * p.max_pages + slot); };
+    auto good_page = [&](int page) {
+        if (page >= 0 && page < p.num_pages) return true;
+        attn_error(p.err, SITE_PAGE_RANGE, uint32_t(page));
+        return false;
+    };
+    // LINEAR: where the tile's values and scales are (this lane's first piece of
+    // them), and the page after the tile's, looked up when its own began.
+    const uint8_t *k_at = nullptr, *v_at = nullptr, *s_at = nullptr;
+    int page_tiles = 0, page_slot = 0, page_next = 0;
+    bool page_ok = false;
+    const int tiles_a_page = p.page_size / KEYS;
+    constexpr int SCALE_LANES = G::SCALES / 16;  // lanes that copy the keys' scales, and as many the values'
+    const uint8_t* const scales = lane < SCALE_LANES ? p.k_scales + lane * 16 : p.v_scales + (lane - SCALE_LANES) * 16;
+    // Otherwise: the row of one key per lane, two tiles before it is copied.
+    struct Ahead {
+        int page, token, kv;
+        bool have, in;
+    } ahead[2];
+    auto look_up = [&](Ahead& a) {
+        a.in = false;
+        if (!(a.have = next_tile())) return;
         const int key = int(load_tile) * KEYS + (lane & (KEYS - 1));
         ++load_tile;
         if (key >= load_len) return;
-        const int slot = key / p.page_size, token = key - slot * p.page_size, kv = lr.g / p.chunks;
-        const int page = __ldg(p.table + int64_t(lr.b) * p.max_pages + slot);
-        if (page < 0 || page >= p.num_pages) {
-            attn_error(p.err, SITE_PAGE_RANGE, uint32_t(page));
-            return;
-        }
-        a.row = page * p.page_stride + token * p.token_stride + kv * p.head_stride;
-        a.srow = page * p.scale_page + token * p.scale_token + kv * p.scale_head;
+        a.in = true;
+        const int slot = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+        a.token = key - slot * p.page_size;
+        a.kv = lr.g / p.chunks;
+        a.page = page_of(slot);
     };
-    look_up(ahead[0]);
-    look_up(ahead[1]);
-    uint32_t load_slot = 0;
-    auto issue = [&]() {
-        const Ahead a = ahead[0];
-        if (a.have) {
-            const uint32_t ks = ring + load_slot * G::STAGE, vs = ks + G::VALUES, kss = vs + G::VALUES, vss = kss + G::SCALES;
-            constexpr int CHUNKS = G::ROW / 16;
-#pragma unroll
-            for (int i = 0; i < KEYS * CHUNKS / 32; ++i) {
-                const int piece = i * 32 + lane, row = piece / CHUNKS, chunk = piece % CHUNKS;
-                const int64_t ro = __shfl_sync(0xffffffffu, a.row, row);
-                const bool ok = ro >= 0;
-                const int64_t at = (ok ? ro : 0) + chunk * 16;
-                copy16(ks + key_at<D>(row, chunk), p.k + at, ok);
-                copy16(vs + value_at<D>(value_row(row), chunk), p.v + at, ok);
-            }
-            const bool ok = a.srow >= 0;
-            const int64_t at = ok ? a.srow : 0;
-            if (KEYS == 32 || lane < KEYS) {
-                copy_small<G::SROW>(kss + uint32_t(lane * G::SROW), p.k_scales + at, ok);
-                copy_small<G::SROW>(vss + uint32_t(value_row(lane) * G::SROW), p.v_scales + at, ok);
-            }
-        }
-        copy_commit();
-        ahead[0] = ahead[1];
+    if constexpr (!LINEAR) {
+        look_up(ahead[0]);
         look_up(ahead[1]);
+    }
+    auto issue = [&]() {
+        if constexpr (LINEAR) {
+            const bool fresh = load_tile >= lr.t1;  // another group
+            if (next_tile()) {
+                if (fresh || page_tiles == 0) {
+                    const int key = int(load_tile) * KEYS, kv = lr.g / p.chunks;
+                    page_slot = fresh ? (p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size) : page_slot + 1;
+                    const int page = fresh ? page_of(page_slot) : page_next;
+                    const int token = key - page_slot * p.page_size;
+                    page_ok = good_page(page);
+                    const int64_t at = page_ok ? page * p.page_stride + token * ROW + kv * p.head_stride : 0;
+                    k_at = p.k + at + lane * 16;
+                    v_at = p.v + at + lane * 16;
+                    s_at = scales + (page_ok ? page * p.scale_page + token * SROW + kv * p.scale_head : 0);
+                    page_tiles = tiles_a_page - token / KEYS;
+                    if ((page_slot + 1) * int64_t(p.page_size) < load_len) page_next = page_of(page_slot + 1);
+                }
+                const uint32_t dst = ring + load_slot * G::STAGE + lane * 16;
+                const int rows = page_ok ? load_len - int(load_tile) * KEYS : 0;  // of the tile, and more
+                if (rows >= KEYS) {
+#pragma unroll
+                    for (int i = 0; i < PIECES; ++i) {
+                        copy16(dst + i * 512, k_at + i * 512);
+                        copy16(dst + G::VALUES + i * 512, v_at + i * 512);
+                    }
+                    if (2 * SCALE_LANES == 32 || lane < 2 * SCALE_LANES) copy16(dst + 2 * G::VALUES, s_at);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < PIECES; ++i) {
+                        const bool in = (i * 32 + lane) / CHUNKS < rows;
+                        copy16(dst + i * 512, in ? k_at + i * 512 : p.k, in);
+                        copy16(dst + G::VALUES + i * 512, in ? v_at + i * 512 : p.v, in);
+                    }
+                    // a piece holds the scales of 16 / SROW keys, some of which may be past the end
+                    if (lane < 2 * SCALE_LANES) {
+                        const int left = (rows - (lane % SCALE_LANES) * (16 / SROW)) * SROW;
+                        copy_part(dst + 2 * G::VALUES, left > 0 ? s_at : p.k_scales, max(0, min(16, left)));
+                    }
+                }
+                k_at += KEYS * ROW;
+                v_at += KEYS * ROW;
+                s_at += KEYS * SROW;
+                ++load_tile;
+                --page_tiles;
+            }
+            copy_commit();
+        } else {
+            const Ahead a = ahead[0];
+            if (a.have) {
+                const bool ok = a.in && good_page(a.page);
+                const uint32_t ks = ring + load_slot * G::STAGE, kss = ks + 2 * G::VALUES;
+                const int64_t own = ok ? a.page * p.page_stride + a.token * p.token_stride + a.kv * p.head_stride : -1;
+#pragma unroll
+                for (int i = 0; i < PIECES; ++i) {
+                    const int piece = i * 32 + lane, row = piece / CHUNKS, chunk = piece % CHUNKS;
+                    const int64_t ro = __shfl_sync(0xffffffffu, own, row);
+                    const bool in = ro >= 0;
+                    const int64_t at = (in ? ro : 0) + chunk * 16;
+                    copy16(ks + piece * 16, p.k + at, in);
+                    copy16(ks + G::VALUES + piece * 16, p.v + at, in);
+                }
+                const int64_t sat = ok ? a.page * p.scale_page + a.token * p.scale_token + a.kv * p.scale_head : 0;
+                if (KEYS == 32 || lane < KEYS) {
+                    copy_small<SROW>(kss + uint32_t(lane * SROW), p.k_scales + sat, ok);
+                    copy_small<SROW>(kss + G::SCALES + uint32_t(lane * SROW), p.v_scales + sat, ok);
+                }
+            }
+            copy_commit();
+            ahead[0] = ahead[1];
+            look_up(ahead[1]);
+        }
         if (++load_slot == G::STAGES) load_slot = 0;
     };
 #pragma unroll
     for (int i = 0; i < G::STAGES; ++i) issue();
 
+    // Where this lane reads: its column's D/8 bytes of key key_of(g), and D/16 bytes of
+    // the values of the keys key_of(2c), key_of(2c + 1) and 8 on from these.
+    const int kg = key_of<D>(g), va = key_of<D>(2 * c), vb = key_of<D>(2 * c + 1);
     uint32_t slot = 0;
     Walk walk{wstart, wend, prefix, p.B, groups, false};
     Range r, head, tail;
@@ -246,6 +321,7 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
     // Output columns g * D/8 + 2t and + 2t + 1 of heads 8n + 2c and 8n + 2c + 1.
     float o[NT][D / 16][4];
     float m[NT][2], l[NT][2];
+    float base[NT][2], most[NT][2];  // from m: added to scores for weights, and what no score may pass
 
     auto put = [&](float* part, int heads) {
 #pragma unroll
@@ -271,9 +347,12 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
         const int heads = min(GROUP, (kv + 1) * p.per_kv - head0);
         const int len = length_of(p, r.b);
         // Queries as the columns of the products: lane (g, c) holds columns c * D/4 ..
-        // of head 8n + g.  A power of two takes a head's largest to 2^14 .. 2^15.
+        // of head 8n + g.  A power of two takes a head's largest to 2^14 .. 2^15, and a
+        // negative scale's sign goes with it, so that the largest product is the largest
+        // score.
         uint32_t qb[NT][D / 16][2];
-        float f[NT][2];  // from products to scores in units of log 2
+        float f[NT][2];  // from products to scores in units of log 2; not negative
+        const float unit = p.scale2 * (p.k_factor ? __ldg(p.k_factor + kv) : 1.f);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             const bool on = n * 8 + g < heads;
@@ -293,7 +372,7 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
             const int e = int(top >> 7);  // biased exponent of the largest; 0 or 255: as it is
             const int up = e == 0 || e == 255 ? 0 : min(141 - e, 126);
-            const float by = __uint_as_float(uint32_t(up + 127) << 23);
+            const float by = copysignf(__uint_as_float(uint32_t(up + 127) << 23), unit);
             const float back = __uint_as_float(uint32_t(127 - up) << 23);
 #pragma unroll
             for (int i = 0; i < D / 32; ++i)
@@ -302,43 +381,46 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
                     const uint32_t u = (&raw[i].x)[j];
                     qb[n][2 * i + j / 2][j % 2] = pack_h2(__uint_as_float(u << 16) * by, __uint_as_float(u & 0xffff0000u) * by);
                 }
-            const float unit = p.scale2 * (p.k_factor ? __ldg(p.k_factor + kv) : 1.f);
-            f[n][0] = unit * __shfl_sync(0xffffffffu, back, 8 * c);
-            f[n][1] = unit * __shfl_sync(0xffffffffu, back, 8 * c + 4);
+            f[n][0] = fabsf(unit) * __shfl_sync(0xffffffffu, back, 8 * c);
+            f[n][1] = fabsf(unit) * __shfl_sync(0xffffffffu, back, 8 * c + 4);
 #pragma unroll
             for (int t = 0; t < D / 16; ++t)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[n][t][i] = 0.f;
             m[n][0] = m[n][1] = -INFINITY;
             l[n][0] = l[n][1] = 0.f;
+            base[n][0] = base[n][1] = 0.f;
+            most[n][0] = most[n][1] = -INFINITY;
         }
 
         for (uint32_t t = r.t0; t < r.t1; ++t) {
+            const uint8_t *ks = ring_ptr + slot * G::STAGE, *vs = ks + G::VALUES, *kss = vs + G::VALUES, *vss = kss + G::SCALES;
+            const bool cut = int(t + 1) * KEYS > len;
             copy_wait<G::STAGES - 1>();
             __syncwarp();
-            const uint32_t ks = ring + slot * G::STAGE, vs = ks + G::VALUES, kss = vs + G::VALUES, vss = kss + G::SCALES;
 
             // ---- scores: 16 keys by 8 heads
-            float s[MT][NT][4] = {};
+            float s[MT][NT][4];
 #pragma unroll
             for (int mt = 0; mt < MT; ++mt) {
                 uint32_t w[2][D / 32], sc[2][D / 64];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int row = mt * 16 + h * 8 + g;
+                    const uint8_t* row = ks + ((mt * 16 + h * 8 + kg) * ROW + c * (D / 8));
+                    const uint8_t* srow = kss + ((mt * 16 + h * 8 + kg) * SROW + c * (D / 64));
                     if constexpr (D == 64) {
-                        load_words<2>(ks + uint32_t(row * G::ROW + c * 8), w[h]);
-                        sc[h][0] = low_twice(halves_of_e4m3x2(load_u8(kss + uint32_t(row * 4 + c))));
+                        load_words<2>(row, w[h]);
+                        sc[h][0] = low_twice(halves_of_e4m3x2(*srow));
                     } else if constexpr (D == 128) {
-                        load_words<4>(ks + key_at<D>(row, c), w[h]);
-                        const uint32_t two = halves_of_e4m3x2(load_u16(kss + uint32_t(row * 8 + 2 * c)));
+                        load_words<4>(row, w[h]);
+                        const uint32_t two = halves_of_e4m3x2(load_u16(srow));
                         sc[h][0] = low_twice(two);
                         sc[h][1] = high_twice(two);
                     } else {
                         uint32_t a[4], b[4], four[1];
-                        load_words<4>(ks + key_at<D>(row, 2 * c), a);
-                        load_words<4>(ks + key_at<D>(row, 2 * c + 1), b);
-                        load_words<1>(kss + uint32_t(row * 16 + 4 * c), four);
+                        load_words<4>(row, a);
+                        load_words<4>(row + 16, b);
+                        load_words<1>(srow, four);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             w[h][i] = a[i];
@@ -364,41 +446,41 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
                         a[x][1] = mul_h2(a[x][1], sc[1][i / 2]);
                         a[x][3] = mul_h2(a[x][3], sc[1][i / 2]);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma_f16(s[mt][n], a[x], qb[n][2 * i + x][0], qb[n][2 * i + x][1]);
+                        for (int n = 0; n < NT; ++n) {
+                            if (i == 0 && x == 0) mma_f16_first(s[mt][n], a[x], qb[n][0][0], qb[n][0][1]);
+                            else mma_f16(s[mt][n], a[x], qb[n][2 * i + x][0], qb[n][2 * i + x][1]);
+                        }
                     }
                 }
             }
 
             // ---- weights
-            const bool cut = int(t + 1) * KEYS > len;
             uint32_t pb[MT][NT][2];
+            uint32_t out = 0;  // a bit per key of this lane that lies past the end
+            if (cut) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (int(t) * KEYS + mt * 16 + h * 8 + kg < len) continue;
+                        out |= 1u << (mt * 2 + h);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) s[mt][n][2 * h] = s[mt][n][2 * h + 1] = -3e38f;
+                    }
+            }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                if (cut) {
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int key = int(t) * KEYS + mt * 16 + (i >> 1) * 8 + g;
-                            // a score below all others, whatever the factor's sign
-                            s[mt][n][i] = key < len ? s[mt][n][i] * f[n][i & 1] : -INFINITY;
-                        }
-                } else {
-#pragma unroll
-                    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) s[mt][n][i] *= f[n][i & 1];
-                }
                 float x0 = -INFINITY, x1 = -INFINITY;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
                     x0 = fmaxf(x0, fmaxf(s[mt][n][0], s[mt][n][2]));
                     x1 = fmaxf(x1, fmaxf(s[mt][n][1], s[mt][n][3]));
                 }
+                x0 *= f[n][0];
+                x1 *= f[n][1];
                 // The maximum is taken anew only when a weight would pass 2^15 (from nothing: at
                 // any score); until then the one before stands for it.
-                constexpr float ROOM = WEIGHT_MOST - WEIGHT_SHIFT;
-                if (__any_sync(0xffffffffu, x0 > m[n][0] + ROOM || x1 > m[n][1] + ROOM)) {
+                if (__any_sync(0xffffffffu, x0 > most[n][0] || x1 > most[n][1])) {
 #pragma unroll
                     for (int d = 4; d < 32; d <<= 1) {
                         x0 = fmaxf(x0, __shfl_xor_sync(0xffffffffu, x0, d));
@@ -409,6 +491,11 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
                     const float f1 = m[n][1] == -INFINITY ? 0.f : exp2_of(m[n][1] - n1);
                     m[n][0] = n0;
                     m[n][1] = n1;
+                    most[n][0] = n0 + (WEIGHT_MOST - WEIGHT_SHIFT);
+                    most[n][1] = n1 + (WEIGHT_MOST - WEIGHT_SHIFT);
+                    // a head whose scores are all -inf has weights 0, not e^(-inf + inf)
+                    base[n][0] = n0 == -INFINITY ? 0.f : WEIGHT_SHIFT - n0;
+                    base[n][1] = n1 == -INFINITY ? 0.f : WEIGHT_SHIFT - n1;
                     l[n][0] *= f0;
                     l[n][1] *= f1;
 #pragma unroll
@@ -419,17 +506,20 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
                         o[n][j][3] *= f1;
                     }
                 }
-                // a head whose scores are all -inf has weights 0, not e^(-inf + inf)
-                const float b0 = m[n][0] == -INFINITY ? 0.f : m[n][0] - WEIGHT_SHIFT;
-                const float b1 = m[n][1] == -INFINITY ? 0.f : m[n][1] - WEIGHT_SHIFT;
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    const float p0 = exp2_of(s[mt][n][0] - b0), p1 = exp2_of(s[mt][n][1] - b1);
-                    const float p2 = exp2_of(s[mt][n][2] - b0), p3 = exp2_of(s[mt][n][3] - b1);
-                    l[n][0] += p0 + p2;
-                    l[n][1] += p1 + p3;
-                    pb[mt][n][0] = transpose8(pack_h2(p0, p1));
-                    pb[mt][n][1] = transpose8(pack_h2(p2, p3));
+                    float w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) w[i] = exp2_of(fmaf(s[mt][n][i], f[n][i & 1], base[n][i & 1]));
+                    if (cut) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (out >> (mt * 2 + (i >> 1)) & 1u) w[i] = 0.f;
+                    }
+                    l[n][0] += w[0] + w[2];
+                    l[n][1] += w[1] + w[3];
+                    pb[mt][n][0] = transpose8(pack_h2(w[0], w[1]));
+                    pb[mt][n][1] = transpose8(pack_h2(w[2], w[3]));
                 }
             }
 
@@ -440,17 +530,10 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
                 uint32_t w[4][WORDS], sb[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const int row = mt * 16 + 4 * j + c;
-                    if constexpr (D == 64) {
-                        load_words<1>(vs + uint32_t(row * G::ROW + g * 4), w[j]);
-                        sb[j] = load_u8(vss + uint32_t(row * 4 + g / 2));
-                    } else if constexpr (D == 128) {
-                        load_words<2>(vs + value_at<D>(row, g / 2) + uint32_t(g & 1) * 8, w[j]);
-                        sb[j] = load_u8(vss + uint32_t(row * 8 + g));
-                    } else {
-                        load_words<4>(vs + value_at<D>(row, g), w[j]);
-                        sb[j] = load_u16(vss + uint32_t(row * 16 + 2 * g));
-                    }
+                    const int key = mt * 16 + (j >> 1) * 8 + (j & 1 ? vb : va);
+                    load_words<WORDS>(vs + (key * ROW + g * (D / 16)), w[j]);
+                    if constexpr (D == 256) sb[j] = load_u16(vss + (key * SROW + 2 * g));
+                    else sb[j] = vss[key * SROW + (D == 64 ? g / 2 : g)];
                 }
                 // scales of the pairs of keys, for the first and the second 16 of the columns
                 uint32_t s01[2], s23[2];
@@ -535,17 +618,19 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
     join_ranges<D, GROUP, G::WARPS, G::THREADS>(p, head, tail, warp, lane == 0, tails, firsts, small, cut_at, start, end);
 }
 
-template <int D, int NT>
+template <int D, int NT, bool LINEAR>
 cudaError_t launch_attn4(Attn4Params& p, int grid, cudaStream_t st) {
     using G = Geo4<D, NT>;
     p.chunks = (p.per_kv + G::GROUP - 1) / G::GROUP;
     p.groups = p.chunks * p.Hkv;
-    mk_paged_attention_fp4_kernel<D, NT><<<grid, G::THREADS, G::SMEM, st>>>(p);
+    mk_paged_attention_fp4_kernel<D, NT, LINEAR><<<grid, G::THREADS, G::SMEM, st>>>(p);
     return cudaGetLastError();
 }
 template <int D>
-cudaError_t launch_attn4(Attn4Params& p, int grid, cudaStream_t st) {
-    return p.per_kv <= 8 ? launch_attn4<D, 1>(p, grid, st) : launch_attn4<D, 2>(p, grid, st);
+cudaError_t launch_attn4(Attn4Params& p, bool rows, int grid, cudaStream_t st) {
+    const bool linear = rows && p.page_size % Geo4<D, 1>::KEYS == 0;
+    if (p.per_kv <= 8) return linear ? launch_attn4<D, 1, true>(p, grid, st) : launch_attn4<D, 1, false>(p, grid, st);
+    return linear ? launch_attn4<D, 2, true>(p, grid, st) : launch_attn4<D, 2, false>(p, grid, st);
 }
 
 // Groups of up to 8 query heads per sequence (the smallest), 0 for sizes outside the limits.
@@ -556,7 +641,10 @@ int64_t attn4_groups(int B, int Hq, int Hkv) {
 
 template <int D, int NT>
 cudaError_t attn4_smem() {
-    return cudaFuncSetAttribute(mk_paged_attention_fp4_kernel<D, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    const cudaError_t e = cudaFuncSetAttribute(mk_paged_attention_fp4_kernel<D, NT, true>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, Geo4<D, NT>::SMEM);
+    if (e != cudaSuccess) return e;
+    return cudaFuncSetAttribute(mk_paged_attention_fp4_kernel<D, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                 Geo4<D, NT>::SMEM);
 }
 
@@ -658,7 +746,15 @@ extern "C" mk_status_t mk_paged_attention_fp4(const void* q, int64_t q_stride, c
     p.num_pages = num_pages;
     p.per_kv = Hq / Hkv;
     p.scale2 = scale * LOG2E;
+    p.page_shift = -1;
+    if ((page_size & (page_size - 1)) == 0)
+        for (p.page_shift = 0; (1 << p.page_shift) < page_size;) ++p.page_shift;
+    const auto whole16 = [](int n, int64_t s) { return n <= 1 || s % 16 == 0; };
+    const bool linear = token_stride == D / 2 && scale_token_stride == D / 16 && host_aligned(k_scales, 16) &&
+                        host_aligned(v_scales, 16) && whole16(num_pages, scale_page_stride) && whole16(Hkv, scale_head_stride);
     const int grid = std::min(sms, ATTN_MAX_CTAS);
-    const cudaError_t e = D == 64 ? launch_attn4<64>(p, grid, st) : D == 128 ? launch_attn4<128>(p, grid, st) : launch_attn4<256>(p, grid, st);
+    const cudaError_t e = D == 64    ? launch_attn4<64>(p, linear, grid, st)
+                          : D == 128 ? launch_attn4<128>(p, linear, grid, st)
+                                     : launch_attn4<256>(p, linear, grid, st);
     return e == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }
