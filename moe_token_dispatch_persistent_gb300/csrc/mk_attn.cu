@@ -81,7 +81,7 @@ struct Geo {
     static constexpr int SMEM = SM_SCORES + (SPLIT > 1 ? 2 * WARPS * (KEYS / 8) * 512 : 0);
     static_assert(RANGES * PART * 4 <= SM_HEADS, "the last results lie where the rings were");
     static constexpr int SLOT = 2 * GROUP + GROUP * D;  // floats of a partial result: m, l, O
-    static_assert(SMEM + 2 * RANGES * 24 <= 232448, "shared memory of one CTA on sm_103");
+    static_assert(SMEM + 2 * RANGES * 28 + 16 <= 232448, "shared memory of one CTA on sm_103");
 };
 
 static_assert(std::max(Geo<256, 1>::SLOT, Geo<128, 2>::SLOT) <= ATTN_SLOT_FLOATS, "a partial result fits its slot");

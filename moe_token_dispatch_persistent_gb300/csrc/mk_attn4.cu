@@ -39,13 +39,18 @@
 namespace mk {
 namespace {
 
+// What a CTA's ranges have of their first groups, where shared memory has no room
+// for it.  Fixed, so the counters never move.
+constexpr int ATTN4_HEADS_FLOATS = 34 * 1024;
+constexpr size_t ATTN4_HEADS_BYTES = size_t(ATTN_MAX_CTAS) * ATTN4_HEADS_FLOATS * 4;
+
 // D columns a head, groups of NT * 8 query heads.
 template <int D, int NT>
 struct Geo4 {
     static constexpr int GROUP = NT * 8;
     static constexpr int KEYS = D == 256 ? 16 : 32;  // per tile
-    static constexpr int WARPS = D == 64 ? 16 : D == 128 ? (NT == 1 ? 12 : 8) : (NT == 1 ? 8 : 6);
-    static constexpr int STAGES = D == 64 ? (NT == 1 ? 4 : 3) : D == 128 ? (NT == 1 ? 2 : 3) : (NT == 1 ? 3 : 4);
+    static constexpr int WARPS = D == 64 ? 16 : D == 128 ? (NT == 1 ? 12 : 8) : (NT == 1 ? 12 : 8);
+    static constexpr int STAGES = D == 64 ? (NT == 1 ? 4 : 3) : D == 128 ? (NT == 1 ? 2 : 3) : (NT == 1 ? 2 : 4);
     static constexpr int THREADS = WARPS * 32;
     static constexpr int ROW = D / 2;         // bytes of a row's values
     static constexpr int SROW = D / 16;       // bytes of its scales
@@ -54,16 +59,20 @@ struct Geo4 {
     static constexpr int STAGE = 2 * VALUES + 2 * SCALES;
     static constexpr int RING = STAGES * STAGE;
     static constexpr int PART = GROUP * (D + 8) + 2 * GROUP;  // floats of a range's result: O, m, l
-    static constexpr int SM_HEADS = WARPS * RING;             // results of ranges' first groups; the last ones lie on the rings
-    static constexpr int SM_PREFIX = SM_HEADS + WARPS * PART * 4;
+    // The results of ranges' last groups lie where the rings were; those of their first
+    // ones beside them, or in the workspace where there is no room.
+    static constexpr bool HEADS_SHARED = WARPS * (RING + PART * 4) <= 215000;
+    static constexpr int SM_HEADS = WARPS * RING > WARPS * PART * 4 ? WARPS * RING : WARPS * PART * 4;
+    static constexpr int SM_PREFIX = SM_HEADS + (HEADS_SHARED ? WARPS * PART * 4 : 0);
     static constexpr int SM_SMALL = SM_PREFIX + (ATTN_MAX_B + 1) * 4 + 12;
     static constexpr int SMEM = SM_SMALL + 128;
-    static_assert(WARPS * PART * 4 <= SM_HEADS, "the last results lie where the rings were");
+    static_assert(HEADS_SHARED || WARPS * PART <= ATTN4_HEADS_FLOATS, "the first results fit the workspace");
     static_assert(2 * GROUP + GROUP * D <= ATTN_SLOT_FLOATS, "a partial result fits its slot");
-    static_assert(SMEM + 2 * WARPS * 24 <= 232448, "shared memory of one CTA on sm_103");
+    static_assert(SMEM + 2 * WARPS * 28 + 16 <= 232448, "shared memory of one CTA on sm_103");
 };
 
 constexpr float WEIGHT_SHIFT = 10.f;  // weights are 2^10 e^(s - m)
+constexpr float OUT = -3e38f;        // a product of a key past the end
 constexpr float WEIGHT_MOST = 15.f;   // log2 of the largest: one above starts a new maximum
 
 struct Attn4Params {
@@ -75,6 +84,7 @@ struct Attn4Params {
     __nv_bfloat16* out;
     float* lse;                        // or null
     float* slots;
+    float* heads;                      // ATTN4_HEADS_FLOATS per CTA
     uint32_t* arrived;
     DevError* err;
     int64_t q_stride;
@@ -82,7 +92,9 @@ struct Attn4Params {
     int64_t scale_page, scale_token, scale_head;     // bytes
     int B, Hq, Hkv, page_size, max_pages, num_pages;
     int per_kv, chunks, groups;
-    int page_shift;                    // log2 of page_size, or -1
+    uint32_t page_units, scale_units;  // strides between pages in 16 bytes (UNIT > 0)
+    int page_shift;                    // log2 of page_size, or -1:
+    uint32_t page_magic, page_more;    // key / page_size is the high word of key * page_magic, shifted
     float scale2;                      // scale * log2(e)
 
     __device__ float value_factor(int kv) const { return v_factor ? __ldg(v_factor + kv) : 1.f; }
@@ -104,6 +116,24 @@ __device__ __forceinline__ void mma_f16_first(float (&c)[4], const uint32_t (&a)
 __device__ __forceinline__ uint32_t mul_h2(uint32_t a, uint32_t b) {
     uint32_t r;
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+// Two heads at once.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c, r;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 r, a, b, c;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 r, a, b;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
 __device__ __forceinline__ uint32_t pack_h2(float lo, float hi) {
@@ -156,9 +186,9 @@ __device__ __forceinline__ int key_of(int r) {
     return D == 64 ? int(0x57463120u >> (4 * r) & 7u) : r ^ ((r >> 1) & 1);
 }
 
-// LINEAR: the keys of a tile lie in one page, a head's rows one after the other, so
-// a tile's copies have one base.  Otherwise every row is looked up.
-template <int D, int NT, bool LINEAR>
+// UNIT: that many keys of a tile lie in one page, a head's rows one after the other,
+// so their copies have one base.  0: every row is looked up by itself.
+template <int D, int NT, int UNIT>
 __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp4_kernel(const Attn4Params p) {
     using G = Geo4<D, NT>;
     constexpr int KEYS = G::KEYS, GROUP = G::GROUP, MT = KEYS / 16, ROW = G::ROW, SROW = G::SROW;
@@ -188,7 +218,6 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
     int load_len = 0;
     bool more = true;
     lr.t1 = 0;
-    uint32_t load_slot = 0;
     constexpr int CHUNKS = ROW / 16, PIECES = KEYS * CHUNKS / 32;  // of a row; of a lane
     // The next tile's group and length; false when the range has no more.
     auto next_tile = [&]() -> bool {
@@ -197,24 +226,36 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
             if (!load_walk.next(lr)) return more = false;
             load_len = length_of(p, lr.b);
             load_tile = lr.t0;
+            // the group's queries head for L1 while its first tiles do for shared memory
+            const int kv = lr.g / p.chunks, head = kv * p.per_kv + (lr.g % p.chunks) * GROUP + (lane & (GROUP - 1));
+            if (head < (kv + 1) * p.per_kv && lane < GROUP * (D / 64)) {
+                const __nv_bfloat16* q = p.q + int64_t(lr.b) * p.q_stride + int64_t(head) * D + lane / GROUP * 64;
+                asm volatile("prefetch.global.L1 [%0];" ::"l"(q));
+            }
         }
         return true;
     };
-    auto page_of = [&](int slot) { return __ldg(p.table + int64_t(lr.b) * p.max_pages + slot); };
+    auto slot_of = [&](int key) { return p.page_shift >= 0 ? key >> p.page_shift : int(__umulhi(uint32_t(key), p.page_magic) >> p.page_more); };
     auto good_page = [&](int page) {
         if (page >= 0 && page < p.num_pages) return true;
         attn_error(p.err, SITE_PAGE_RANGE, uint32_t(page));
         return false;
     };
-    // LINEAR: where the tile's values and scales are (this lane's first piece of
-    // them), and the page after the tile's, looked up when its own began.
-    const uint8_t *k_at = nullptr, *v_at = nullptr, *s_at = nullptr;
-    int page_tiles = 0, page_slot = 0, page_next = 0;
-    bool page_ok = false;
-    const int tiles_a_page = p.page_size / KEYS;
+    // UNIT > 0: where the next unit's values and scales are (this lane's first piece of
+    // them), the same of the group's page 0, what is left of the page, and the page after
+    // it, looked up when it began.  A lane's pieces of a unit's scales: those of its own
+    // unit of the tile.
+    constexpr int U = UNIT > 0 ? UNIT : KEYS, UNITS = KEYS / U;
+    constexpr int UNIT_BYTES = U * ROW, UNIT_PIECES = (UNIT_BYTES + 511) / 512, UNIT_LANES = UNIT_BYTES < 512 ? UNIT_BYTES / 16 : 32;
     constexpr int SCALE_LANES = G::SCALES / 16;  // lanes that copy the keys' scales, and as many the values'
-    const uint8_t* const scales = lane < SCALE_LANES ? p.k_scales + lane * 16 : p.v_scales + (lane - SCALE_LANES) * 16;
-    // Otherwise: the row of one key per lane, two tiles before it is copied.
+    const int scale_byte = (lane % SCALE_LANES) * 16, scale_unit = lane < 2 * SCALE_LANES ? scale_byte / (U * SROW) : -1;
+    const uint8_t* const scales = (lane < SCALE_LANES ? p.k_scales : p.v_scales) + scale_byte % (U * SROW);
+    const uint32_t lane_dst = ring + lane * 16;
+    const uint8_t *k_at = nullptr, *v_at = nullptr, *s_at = nullptr, *k_kv = nullptr, *v_kv = nullptr, *s_kv = nullptr;
+    const int32_t* table = nullptr;
+    int page_left = 0, page_next = 0, pages_more = 0;
+    bool page_ok = false;
+    // Else a lane looks up the row of one key, two tiles before it is copied.
     struct Ahead {
         int page, token, kv;
         bool have, in;
@@ -226,66 +267,84 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
         ++load_tile;
         if (key >= load_len) return;
         a.in = true;
-        const int slot = p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size;
+        const int slot = slot_of(key);
         a.token = key - slot * p.page_size;
         a.kv = lr.g / p.chunks;
-        a.page = page_of(slot);
+        a.page = __ldg(p.table + int64_t(lr.b) * p.max_pages + slot);
     };
-    if constexpr (!LINEAR) {
+    if constexpr (UNIT == 0) {
         look_up(ahead[0]);
         look_up(ahead[1]);
     }
+    uint32_t load_at = 0;  // the stage's place in the ring
     auto issue = [&]() {
-        if constexpr (LINEAR) {
+        if constexpr (UNIT > 0) {
             const bool fresh = load_tile >= lr.t1;  // another group
             if (next_tile()) {
-                if (fresh || page_tiles == 0) {
-                    const int key = int(load_tile) * KEYS, kv = lr.g / p.chunks;
-                    page_slot = fresh ? (p.page_shift >= 0 ? key >> p.page_shift : key / p.page_size) : page_slot + 1;
-                    const int page = fresh ? page_of(page_slot) : page_next;
-                    const int token = key - page_slot * p.page_size;
-                    page_ok = good_page(page);
-                    const int64_t at = page_ok ? page * p.page_stride + token * ROW + kv * p.head_stride : 0;
-                    k_at = p.k + at + lane * 16;
-                    v_at = p.v + at + lane * 16;
-                    s_at = scales + (page_ok ? page * p.scale_page + token * SROW + kv * p.scale_head : 0);
-                    page_tiles = tiles_a_page - token / KEYS;
-                    if ((page_slot + 1) * int64_t(p.page_size) < load_len) page_next = page_of(page_slot + 1);
+                int left = load_len - int(load_tile) * KEYS, token = 0;  // keys from here to the end
+                if (fresh) {
+                    const int key = int(load_tile) * KEYS, kv = lr.g / p.chunks, slot = slot_of(key);
+                    table = p.table + int64_t(lr.b) * p.max_pages + slot;
+                    page_next = __ldg(table);
+                    token = key - slot * p.page_size;
+                    pages_more = slot_of(load_len - 1) - slot;
+                    const int64_t head = kv * p.head_stride + (lane & (UNIT_LANES - 1)) * 16;
+                    k_kv = p.k + head;
+                    v_kv = p.v + head;
+                    s_kv = scales + kv * p.scale_head;
+                    page_left = 0;
                 }
-                const uint32_t dst = ring + load_slot * G::STAGE + lane * 16;
-                const int rows = page_ok ? load_len - int(load_tile) * KEYS : 0;  // of the tile, and more
-                if (rows >= KEYS) {
 #pragma unroll
-                    for (int i = 0; i < PIECES; ++i) {
-                        copy16(dst + i * 512, k_at + i * 512);
-                        copy16(dst + G::VALUES + i * 512, v_at + i * 512);
+                for (int u = 0; u < UNITS; ++u) {
+                    if (page_left == 0 && left > 0) {
+                        page_ok = good_page(page_next);
+                        const uint32_t page = page_ok ? uint32_t(page_next) : 0u;
+                        const uint64_t at = uint64_t(page) * p.page_units * 16 + uint32_t(token * ROW);
+                        k_at = k_kv + at;
+                        v_at = v_kv + at;
+                        s_at = s_kv + (uint64_t(page) * p.scale_units * 16 + uint32_t(token * SROW));
+                        page_left = p.page_size - token;
+                        token = 0;
+                        if (--pages_more >= 0) page_next = __ldg(++table);
                     }
-                    if (2 * SCALE_LANES == 32 || lane < 2 * SCALE_LANES) copy16(dst + 2 * G::VALUES, s_at);
-                } else {
+                    const uint32_t dst = lane_dst + load_at + (UNIT_LANES == 32 ? u * UNIT_BYTES : u / 2 * 512);
+                    const bool mine = UNIT_LANES == 32 || lane / UNIT_LANES == u % 2;
+                    const uint32_t scale_dst = lane_dst + load_at + 2 * G::VALUES;
+                    if (page_ok && left >= U) {
 #pragma unroll
-                    for (int i = 0; i < PIECES; ++i) {
-                        const bool in = (i * 32 + lane) / CHUNKS < rows;
-                        copy16(dst + i * 512, in ? k_at + i * 512 : p.k, in);
-                        copy16(dst + G::VALUES + i * 512, in ? v_at + i * 512 : p.v, in);
+                        for (int i = 0; i < UNIT_PIECES; ++i)
+                            if (mine) {
+                                copy16(dst + i * 512, k_at + i * 512);
+                                copy16(dst + G::VALUES + i * 512, v_at + i * 512);
+                            }
+                        if (scale_unit == u) copy16(scale_dst, s_at);
+                    } else {  // zeros past the end, and for a page outside the pool
+                        const int rows = page_ok ? left : 0;
+#pragma unroll
+                        for (int i = 0; i < UNIT_PIECES; ++i)
+                            if (mine) {
+                                const bool in = (i * 32 + (lane & (UNIT_LANES - 1))) / CHUNKS < rows;
+                                copy16(dst + i * 512, in ? k_at + i * 512 : p.k, in);
+                                copy16(dst + G::VALUES + i * 512, in ? v_at + i * 512 : p.v, in);
+                            }
+                        // a piece holds the scales of 16 / SROW keys
+                        const int bytes = rows * SROW - scale_byte % (U * SROW);
+                        if (scale_unit == u) copy_part(scale_dst, bytes > 0 ? s_at : p.k_scales, max(0, min(16, bytes)));
                     }
-                    // a piece holds the scales of 16 / SROW keys, some of which may be past the end
-                    if (lane < 2 * SCALE_LANES) {
-                        const int left = (rows - (lane % SCALE_LANES) * (16 / SROW)) * SROW;
-                        copy_part(dst + 2 * G::VALUES, left > 0 ? s_at : p.k_scales, max(0, min(16, left)));
-                    }
+                    k_at += UNIT_BYTES;
+                    v_at += UNIT_BYTES;
+                    s_at += U * SROW;
+                    page_left -= U;
+                    left -= U;
                 }
-                k_at += KEYS * ROW;
-                v_at += KEYS * ROW;
-                s_at += KEYS * SROW;
                 ++load_tile;
-                --page_tiles;
             }
             copy_commit();
         } else {
             const Ahead a = ahead[0];
             if (a.have) {
                 const bool ok = a.in && good_page(a.page);
-                const uint32_t ks = ring + load_slot * G::STAGE, kss = ks + 2 * G::VALUES;
+                const uint32_t ks = ring + load_at, kss = ks + 2 * G::VALUES;
                 const int64_t own = ok ? a.page * p.page_stride + a.token * p.token_stride + a.kv * p.head_stride : -1;
 #pragma unroll
                 for (int i = 0; i < PIECES; ++i) {
@@ -306,7 +365,7 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
             ahead[0] = ahead[1];
             look_up(ahead[1]);
         }
-        if (++load_slot == G::STAGES) load_slot = 0;
+        load_at = load_at + G::STAGE == G::RING ? 0u : load_at + G::STAGE;
     };
 #pragma unroll
     for (int i = 0; i < G::STAGES; ++i) issue();
@@ -314,15 +373,17 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
     // Where this lane reads: its column's D/8 bytes of key key_of(g), and D/16 bytes of
     // the values of the keys key_of(2c), key_of(2c + 1) and 8 on from these.
     const int kg = key_of<D>(g), va = key_of<D>(2 * c), vb = key_of<D>(2 * c + 1);
-    uint32_t slot = 0;
+    uint32_t at = 0;  // the tile's stage
     Walk walk{wstart, wend, prefix, p.B, groups, false};
     Range r, head, tail;
     bool has_head = false, has_tail = false;
     // Output columns g * D/8 + 2t and + 2t + 1 of heads 8n + 2c and 8n + 2c + 1.
     float o[NT][D / 16][4];
-    float m[NT][2], l[NT][2];
-    float base[NT][2], most[NT][2];  // from m: added to scores for weights, and what no score may pass
+    float m[NT][2], most[NT][2];  // reference of the weights, and what no score may pass
+    float2 l[NT], base[NT];       // sums of the weights, and what is added to scores for them
 
+    float* const first_results = G::HEADS_SHARED ? reinterpret_cast<float*>(smem + G::SM_HEADS)
+                                                 : p.heads + size_t(blockIdx.x) * ATTN4_HEADS_FLOATS;
     auto put = [&](float* part, int heads) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -331,7 +392,7 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
                 const int row = n * 8 + 2 * c + i;
                 if (g == 0) {
                     part[GROUP * (D + 8) + row] = m[n][i] - WEIGHT_SHIFT;
-                    part[GROUP * (D + 8) + GROUP + row] = l[n][i];
+                    part[GROUP * (D + 8) + GROUP + row] = i ? l[n].y : l[n].x;
                 }
                 float* to = part + row * (D + 8) + g * (D / 8);
                 if (row < heads)
@@ -388,13 +449,12 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
 #pragma unroll
                 for (int i = 0; i < 4; ++i) o[n][t][i] = 0.f;
             m[n][0] = m[n][1] = -INFINITY;
-            l[n][0] = l[n][1] = 0.f;
-            base[n][0] = base[n][1] = 0.f;
+            l[n] = base[n] = make_float2(0.f, 0.f);
             most[n][0] = most[n][1] = -INFINITY;
         }
 
         for (uint32_t t = r.t0; t < r.t1; ++t) {
-            const uint8_t *ks = ring_ptr + slot * G::STAGE, *vs = ks + G::VALUES, *kss = vs + G::VALUES, *vss = kss + G::SCALES;
+            const uint8_t *ks = ring_ptr + at, *vs = ks + G::VALUES, *kss = vs + G::VALUES, *vss = kss + G::SCALES;
             const bool cut = int(t + 1) * KEYS > len;
             copy_wait<G::STAGES - 1>();
             __syncwarp();
@@ -456,25 +516,26 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
 
             // ---- weights
             uint32_t pb[MT][NT][2];
-            uint32_t out = 0;  // a bit per key of this lane that lies past the end
             if (cut) {
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        if (int(t) * KEYS + mt * 16 + h * 8 + kg < len) continue;
-                        out |= 1u << (mt * 2 + h);
+                    for (int h = 0; h < 2; ++h)
+                        if (int(t) * KEYS + mt * 16 + h * 8 + kg >= len)
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) s[mt][n][2 * h] = s[mt][n][2 * h + 1] = -3e38f;
-                    }
+                            for (int n = 0; n < NT; ++n) s[mt][n][2 * h] = s[mt][n][2 * h + 1] = OUT;
             }
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                float x0 = -INFINITY, x1 = -INFINITY;
+                float x0 = s[0][n][0], x1 = s[0][n][1];
 #pragma unroll
                 for (int mt = 0; mt < MT; ++mt) {
-                    x0 = fmaxf(x0, fmaxf(s[mt][n][0], s[mt][n][2]));
-                    x1 = fmaxf(x1, fmaxf(s[mt][n][1], s[mt][n][3]));
+                    if (mt > 0) {
+                        x0 = fmaxf(x0, s[mt][n][0]);
+                        x1 = fmaxf(x1, s[mt][n][1]);
+                    }
+                    x0 = fmaxf(x0, s[mt][n][2]);
+                    x1 = fmaxf(x1, s[mt][n][3]);
                 }
                 x0 *= f[n][0];
                 x1 *= f[n][1];
@@ -494,10 +555,9 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
                     most[n][0] = n0 + (WEIGHT_MOST - WEIGHT_SHIFT);
                     most[n][1] = n1 + (WEIGHT_MOST - WEIGHT_SHIFT);
                     // a head whose scores are all -inf has weights 0, not e^(-inf + inf)
-                    base[n][0] = n0 == -INFINITY ? 0.f : WEIGHT_SHIFT - n0;
-                    base[n][1] = n1 == -INFINITY ? 0.f : WEIGHT_SHIFT - n1;
-                    l[n][0] *= f0;
-                    l[n][1] *= f1;
+                    base[n] = make_float2(n0 == -INFINITY ? 0.f : WEIGHT_SHIFT - n0, n1 == -INFINITY ? 0.f : WEIGHT_SHIFT - n1);
+                    l[n].x *= f0;
+                    l[n].y *= f1;
 #pragma unroll
                     for (int j = 0; j < D / 16; ++j) {
                         o[n][j][0] *= f0;
@@ -506,21 +566,28 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
                         o[n][j][3] *= f1;
                     }
                 }
+                float2 w[MT][2];  // of two heads each, by key
 #pragma unroll
-                for (int mt = 0; mt < MT; ++mt) {
-                    float w[4];
+                for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) w[i] = exp2_of(fmaf(s[mt][n][i], f[n][i & 1], base[n][i & 1]));
-                    if (cut) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            if (out >> (mt * 2 + (i >> 1)) & 1u) w[i] = 0.f;
+                    for (int h = 0; h < 2; ++h) {
+                        const float2 x = fma2(make_float2(s[mt][n][2 * h], s[mt][n][2 * h + 1]), make_float2(f[n][0], f[n][1]), base[n]);
+                        w[mt][h] = make_float2(exp2_of(x.x), exp2_of(x.y));
                     }
-                    l[n][0] += w[0] + w[2];
-                    l[n][1] += w[1] + w[3];
-                    pb[mt][n][0] = transpose8(pack_h2(w[0], w[1]));
-                    pb[mt][n][1] = transpose8(pack_h2(w[2], w[3]));
+                if (cut) {
+#pragma unroll
+                    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            if (int(t) * KEYS + mt * 16 + h * 8 + kg >= len) w[mt][h] = make_float2(0.f, 0.f);
                 }
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        l[n] = add2(l[n], w[mt][h]);
+                        pb[mt][n][h] = transpose8(pack_h2(w[mt][h].x, w[mt][h].y));
+                    }
             }
 
             // ---- output: 16 columns by 8 heads, over 16 keys
@@ -566,15 +633,15 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
             }
             __syncwarp();  // every lane has read the tile before it is overwritten
             issue();
-            if (++slot == G::STAGES) slot = 0;
+            at = at + G::STAGE == G::RING ? 0u : at + G::STAGE;
         }
 
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int d = 4; d < 32; d <<= 1) {
-                l[n][0] += __shfl_xor_sync(0xffffffffu, l[n][0], d);
-                l[n][1] += __shfl_xor_sync(0xffffffffu, l[n][1], d);
+                l[n].x += __shfl_xor_sync(0xffffffffu, l[n].x, d);
+                l[n].y += __shfl_xor_sync(0xffffffffu, l[n].y, d);
             }
         if (r.t1 - r.t0 == r.tiles) {
             // the whole group: straight to the output
@@ -585,20 +652,20 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
                 for (int i = 0; i < 2; ++i) {
                     const int row = n * 8 + 2 * c + i;
                     if (row >= heads) continue;
-                    const float inv = l[n][i] == 0.f ? 0.f : factor / l[n][i];
-                    const int64_t at = int64_t(r.b) * p.Hq + head0 + row;
-                    uint2* to = reinterpret_cast<uint2*>(p.out + at * D + g * (D / 8));
+                    const float sum = i ? l[n].y : l[n].x, inv = sum == 0.f ? 0.f : factor / sum;
+                    const int64_t row_at = int64_t(r.b) * p.Hq + head0 + row;
+                    uint2* to = reinterpret_cast<uint2*>(p.out + row_at * D + g * (D / 8));
 #pragma unroll
                     for (int t = 0; t < D / 16; t += 2)
                         to[t / 2] = make_uint2(pack_bf16(o[n][t][i] * inv, o[n][t][2 + i] * inv),
                                                pack_bf16(o[n][t + 1][i] * inv, o[n][t + 1][2 + i] * inv));
                     if (p.lse && g == 0)
-                        p.lse[at] = l[n][i] == 0.f ? -INFINITY : (m[n][i] - WEIGHT_SHIFT + log2f(l[n][i])) * LN2;
+                        p.lse[row_at] = sum == 0.f ? -INFINITY : (m[n][i] - WEIGHT_SHIFT + log2f(sum)) * LN2;
                 }
         } else if (walk.pos < walk.end) {
             head = r;
             has_head = true;
-            put(reinterpret_cast<float*>(smem + G::SM_HEADS) + warp * G::PART, heads);
+            put(first_results + warp * G::PART, heads);
         } else {
             tail = r;
             has_tail = true;
@@ -607,7 +674,6 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
     copy_wait<0>();
 
     float* tails = reinterpret_cast<float*>(smem);
-    const float* firsts = reinterpret_cast<const float*>(smem + G::SM_HEADS);
     __syncthreads();  // the rings are free
     if (has_tail) {
         const int kv = tail.g / p.chunks, head0 = kv * p.per_kv + (tail.g % p.chunks) * GROUP;
@@ -615,22 +681,27 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
     }
     head.tiles = has_head ? head.tiles : 0u;
     tail.tiles = has_tail ? tail.tiles : 0u;
-    join_ranges<D, GROUP, G::WARPS, G::THREADS>(p, head, tail, warp, lane == 0, tails, firsts, small, cut_at, start, end);
+    join_ranges<D, GROUP, G::WARPS, G::THREADS>(p, head, tail, warp, lane == 0, tails, first_results, small, cut_at, start, end);
 }
 
-template <int D, int NT, bool LINEAR>
+template <int D, int NT, int UNIT>
 cudaError_t launch_attn4(Attn4Params& p, int grid, cudaStream_t st) {
     using G = Geo4<D, NT>;
     p.chunks = (p.per_kv + G::GROUP - 1) / G::GROUP;
     p.groups = p.chunks * p.Hkv;
-    mk_paged_attention_fp4_kernel<D, NT, LINEAR><<<grid, G::THREADS, G::SMEM, st>>>(p);
+    mk_paged_attention_fp4_kernel<D, NT, UNIT><<<grid, G::THREADS, G::SMEM, st>>>(p);
     return cudaGetLastError();
+}
+template <int D, int NT>
+cudaError_t launch_attn4(Attn4Params& p, bool rows, int grid, cudaStream_t st) {
+    if (rows && Geo4<D, NT>::KEYS == 32 && p.page_size % 32 == 0) return launch_attn4<D, NT, Geo4<D, NT>::KEYS>(p, grid, st);
+    if (rows && p.page_size % 16 == 0) return launch_attn4<D, NT, 16>(p, grid, st);
+    if (rows && p.page_size % 8 == 0) return launch_attn4<D, NT, 8>(p, grid, st);
+    return launch_attn4<D, NT, 0>(p, grid, st);
 }
 template <int D>
 cudaError_t launch_attn4(Attn4Params& p, bool rows, int grid, cudaStream_t st) {
-    const bool linear = rows && p.page_size % Geo4<D, 1>::KEYS == 0;
-    if (p.per_kv <= 8) return linear ? launch_attn4<D, 1, true>(p, grid, st) : launch_attn4<D, 1, false>(p, grid, st);
-    return linear ? launch_attn4<D, 2, true>(p, grid, st) : launch_attn4<D, 2, false>(p, grid, st);
+    return p.per_kv <= 8 ? launch_attn4<D, 1>(p, rows, grid, st) : launch_attn4<D, 2>(p, rows, grid, st);
 }
 
 // Groups of up to 8 query heads per sequence (the smallest), 0 for sizes outside the limits.
@@ -639,13 +710,16 @@ int64_t attn4_groups(int B, int Hq, int Hkv) {
     return int64_t(Hkv) * ((Hq / Hkv + 7) / 8);
 }
 
+template <int D, int NT, int UNIT>
+cudaError_t attn4_smem() {
+    return cudaFuncSetAttribute(mk_paged_attention_fp4_kernel<D, NT, UNIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                Geo4<D, NT>::SMEM);
+}
 template <int D, int NT>
 cudaError_t attn4_smem() {
-    const cudaError_t e = cudaFuncSetAttribute(mk_paged_attention_fp4_kernel<D, NT, true>,
-                                               cudaFuncAttributeMaxDynamicSharedMemorySize, Geo4<D, NT>::SMEM);
-    if (e != cudaSuccess) return e;
-    return cudaFuncSetAttribute(mk_paged_attention_fp4_kernel<D, NT, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Geo4<D, NT>::SMEM);
+    for (const cudaError_t e : {attn4_smem<D, NT, Geo4<D, NT>::KEYS>(), attn4_smem<D, NT, 16>(), attn4_smem<D, NT, 8>(), attn4_smem<D, NT, 0>()})
+        if (e != cudaSuccess) return e;
+    return cudaSuccess;
 }
 
 }  // namespace
@@ -664,7 +738,7 @@ using namespace mk;
 extern "C" size_t mk_paged_attention_fp4_workspace_size(int B, int Hq, int Hkv) {
     const int64_t g = attn4_groups(B, Hq, Hkv);
     if (g == 0 || B > ATTN_MAX_B) return 0;
-    return ATTN_SLOTS_BYTES + ws_align(size_t(B) * size_t(g) * sizeof(uint32_t));
+    return ATTN_SLOTS_BYTES + ATTN4_HEADS_BYTES + ws_align(size_t(B) * size_t(g) * sizeof(uint32_t));
 }
 
 extern "C" mk_status_t mk_paged_attention_fp4(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
@@ -729,7 +803,8 @@ extern "C" mk_status_t mk_paged_attention_fp4(const void* q, int64_t q_stride, c
     p.out = static_cast<__nv_bfloat16*>(out);
     p.lse = lse;
     p.slots = reinterpret_cast<float*>(ws);
-    p.arrived = reinterpret_cast<uint32_t*>(ws + ATTN_SLOTS_BYTES);
+    p.heads = reinterpret_cast<float*>(ws + ATTN_SLOTS_BYTES);
+    p.arrived = reinterpret_cast<uint32_t*>(ws + ATTN_SLOTS_BYTES + ATTN4_HEADS_BYTES);
     p.err = err;
     p.q_stride = q_stride;
     p.page_stride = page_stride;
@@ -746,15 +821,22 @@ extern "C" mk_status_t mk_paged_attention_fp4(const void* q, int64_t q_stride, c
     p.num_pages = num_pages;
     p.per_kv = Hq / Hkv;
     p.scale2 = scale * LOG2E;
-    p.page_shift = -1;
-    if ((page_size & (page_size - 1)) == 0)
-        for (p.page_shift = 0; (1 << p.page_shift) < page_size;) ++p.page_shift;
-    const auto whole16 = [](int n, int64_t s) { return n <= 1 || s % 16 == 0; };
-    const bool linear = token_stride == D / 2 && scale_token_stride == D / 16 && host_aligned(k_scales, 16) &&
-                        host_aligned(v_scales, 16) && whole16(num_pages, scale_page_stride) && whole16(Hkv, scale_head_stride);
+    // page_size = 2^31 / ... : the quotient of any key below 2^31 by multiplication (Granlund
+    // and Montgomery 1994): with 2^l >= page_size > 2^(l-1), magic = ceil(2^(31+l) / page_size).
+    int l = 0;
+    while ((int64_t(1) << l) < page_size) ++l;
+    p.page_shift = (page_size & (page_size - 1)) == 0 ? l : -1;
+    p.page_magic = p.page_shift >= 0 ? 0 : uint32_t(((uint64_t(1) << (31 + l)) + uint32_t(page_size) - 1) / uint32_t(page_size));
+    p.page_more = l > 0 ? l - 1 : 0;
+    const auto units = [](int n, int64_t s) { return n <= 1 || (s % 16 == 0 && s / 16 <= int64_t(UINT32_MAX)); };
+    const bool rows = token_stride == D / 2 && scale_token_stride == D / 16 && host_aligned(k_scales, 16) &&
+                      host_aligned(v_scales, 16) && units(num_pages, page_stride) && units(num_pages, scale_page_stride) &&
+                      (Hkv <= 1 || scale_head_stride % 16 == 0);
+    p.page_units = rows && num_pages > 1 ? uint32_t(page_stride / 16) : 0;
+    p.scale_units = rows && num_pages > 1 ? uint32_t(scale_page_stride / 16) : 0;
     const int grid = std::min(sms, ATTN_MAX_CTAS);
-    const cudaError_t e = D == 64    ? launch_attn4<64>(p, linear, grid, st)
-                          : D == 128 ? launch_attn4<128>(p, linear, grid, st)
-                                     : launch_attn4<256>(p, linear, grid, st);
+    const cudaError_t e = D == 64    ? launch_attn4<64>(p, rows, grid, st)
+                          : D == 128 ? launch_attn4<128>(p, rows, grid, st)
+                                     : launch_attn4<256>(p, rows, grid, st);
     return e == cudaSuccess ? MK_OK : MK_ERR_CUDA;
 }

@@ -288,52 +288,63 @@ __device__ __forceinline__ void join_ranges(const P& p, const Range& head, const
         pieces[2 * range + 1] = tail;
     }
     __syncthreads();
-    Range open[2];  // groups shared with other CTAs: the first and the last one's
-    int nopen = 0;
-    uint32_t left = 0;  // pieces not joined yet, a bit each
-#pragma unroll
-    for (int i = 0; i < 2 * RANGES; ++i) left |= pieces[i].tiles != 0 ? 1u << i : 0u;
-    while (left) {
-        const Range q = pieces[__ffs(int(left)) - 1];
-        uint32_t same = 0;  // those of the first one's group
-#pragma unroll
-        for (int i = 0; i < 2 * RANGES; ++i)
-            if ((left >> i & 1u) && pieces[i].begin == q.begin) same |= 1u << i;
-        left &= ~same;
+    // the pieces of each group, a bit each, the groups in the order of positions; and the
+    // places of those shared with other CTAs: the first and the last one's
+    __shared__ uint32_t masks[2 * RANGES];
+    __shared__ uint32_t open_at[2], counts[2];
+    if (tid < 32) {
+        const Range q = pieces[min(tid, 2 * RANGES - 1)];
+        const bool on = tid < 2 * RANGES && q.tiles != 0;
+        const uint32_t same = __match_any_sync(0xffffffffu, on ? q.begin : 0xffffffffu);
+        const bool first = on && __ffs(int(same)) - 1 == tid;
+        const uint32_t before = (1u << tid) - 1u, firsts_of = __ballot_sync(0xffffffffu, first);
+        const uint32_t opens = __ballot_sync(0xffffffffu, first && !(q.begin >= start && q.begin + q.tiles <= end));
+        if (first) {
+            const int at = __popc(firsts_of & before);
+            masks[at] = same;
+            if (opens >> tid & 1u) open_at[__popc(opens & before)] = uint32_t(at);
+        }
+        if (tid == 0) {
+            counts[0] = uint32_t(__popc(firsts_of));
+            counts[1] = uint32_t(__popc(opens));
+        }
+    }
+    __syncthreads();
+    constexpr int ITEMS = GROUP * (D / 4);
+    const int nopen = int(counts[1]);
+    for (int it = tid; it < int(counts[0]) * ITEMS; it += THREADS) {
+        const uint32_t same = masks[it / ITEMS];
+        const int item = it % ITEMS, row = item / (D / 4), c = (item % (D / 4)) * 4;
+        const Range q = pieces[__ffs(int(same)) - 1];
         const int kv = q.g / p.chunks, head0 = kv * p.per_kv + (q.g % p.chunks) * GROUP;
-        const int heads = min(GROUP, (kv + 1) * p.per_kv - head0);
-        const bool whole = q.begin >= start && q.begin + q.tiles <= end;
-        // a CTA's first shared group takes its first slot, its last one the second
-        float* mine = p.slots + size_t(2 * blockIdx.x + (start >= q.begin ? 0 : 1)) * ATTN_SLOT_FLOATS;
-        for (int item = tid; item < heads * (D / 4); item += THREADS) {
-            const int row = item / (D / 4), c = (item % (D / 4)) * 4;
-            Part acc;
-            for (uint32_t rest = same; rest;) {
-                constexpr int BATCH = 4;
-                Part u[BATCH];
+        if (row >= min(GROUP, (kv + 1) * p.per_kv - head0)) continue;
+        Part acc;
+        for (uint32_t rest = same; rest;) {
+            constexpr int BATCH = 4;
+            Part u[BATCH];
 #pragma unroll
-                for (int x = 0; x < BATCH; ++x) {
-                    if (rest == 0) continue;
-                    const int i = __ffs(int(rest)) - 1, w = i >> 1;
-                    rest &= rest - 1;
-                    const float* s = (i & 1 ? tails : firsts) + w * PART;
-                    u[x].m = s[GROUP * OSTRIDE + row];
-                    u[x].l = s[GROUP * OSTRIDE + GROUP + row];
-                    u[x].o = *reinterpret_cast<const float4*>(s + row * OSTRIDE + c);
-                }
-                acc.add(u);
+            for (int x = 0; x < BATCH; ++x) {
+                if (rest == 0) continue;
+                const int i = __ffs(int(rest)) - 1, w = i >> 1;
+                rest &= rest - 1;
+                const float* s = (i & 1 ? tails : firsts) + w * PART;
+                u[x].m = s[GROUP * OSTRIDE + row];
+                u[x].l = s[GROUP * OSTRIDE + GROUP + row];
+                u[x].o = *reinterpret_cast<const float4*>(s + row * OSTRIDE + c);
             }
-            if (whole) {
-                acc.finish(p, q.b, head0 + row, c, D);
-            } else {
-                __stcg(reinterpret_cast<float4*>(mine + 2 * GROUP + row * D + c), acc.o);
-                if (c == 0) {
-                    __stcg(mine + row, acc.m);
-                    __stcg(mine + GROUP + row, acc.l);
-                }
+            acc.add(u);
+        }
+        if (q.begin >= start && q.begin + q.tiles <= end) {
+            acc.finish(p, q.b, head0 + row, c, D);
+        } else {
+            // a CTA's first shared group takes its first slot, its last one the second
+            float* mine = p.slots + size_t(2 * blockIdx.x + (start >= q.begin ? 0 : 1)) * ATTN_SLOT_FLOATS;
+            __stcg(reinterpret_cast<float4*>(mine + 2 * GROUP + row * D + c), acc.o);
+            if (c == 0) {
+                __stcg(mine + row, acc.m);
+                __stcg(mine + GROUP + row, acc.l);
             }
         }
-        if (!whole) open[nopen++] = q;
     }
     if (nopen == 0) return;
 
@@ -341,7 +352,7 @@ __device__ __forceinline__ void join_ranges(const P& p, const Range& head, const
     // partial results (the count releases what the whole CTA has stored)
     __syncthreads();
     if (tid < nopen) {
-        const Range& o = tid == 0 ? open[0] : open[1];
+        const Range o = pieces[__ffs(int(masks[open_at[tid]])) - 1];
         const uint32_t c0 = cut_at.owner(o.begin), n = cut_at.owner(o.begin + o.tiles - 1) - c0 + 1;
         uint32_t* a = p.arrived + size_t(o.b) * groups + o.g;
         const bool last = atom_add_acq_rel_u32(a, 1u) == n - 1;
@@ -353,7 +364,8 @@ __device__ __forceinline__ void join_ranges(const P& p, const Range& head, const
     __syncthreads();
     for (int i = 0; i < nopen; ++i)
         if (small[4 * i])
-            join_group<D, GROUP, THREADS>(p, i == 0 ? open[0] : open[1], small[4 * i + 1], int(small[4 * i]), small[4 * i + 2], tails);
+            join_group<D, GROUP, THREADS>(p, pieces[__ffs(int(masks[open_at[i]])) - 1], small[4 * i + 1], int(small[4 * i]),
+                                          small[4 * i + 2], tails);
 }
 
 }  // namespace
