@@ -288,33 +288,25 @@ __device__ __forceinline__ void join_ranges(const P& p, const Range& head, const
         pieces[2 * range + 1] = tail;
     }
     __syncthreads();
-    // the pieces of each group, a bit each, the groups in the order of positions; and the
-    // places of those shared with other CTAs: the first and the last one's
-    __shared__ uint32_t masks[2 * RANGES];
-    __shared__ uint32_t open_at[2], counts[2];
-    if (tid < 32) {
-        const Range q = pieces[min(tid, 2 * RANGES - 1)];
-        const bool on = tid < 2 * RANGES && q.tiles != 0;
-        const uint32_t same = __match_any_sync(0xffffffffu, on ? q.begin : 0xffffffffu);
-        const bool first = on && __ffs(int(same)) - 1 == tid;
-        const uint32_t before = (1u << tid) - 1u, firsts_of = __ballot_sync(0xffffffffu, first);
-        const uint32_t opens = __ballot_sync(0xffffffffu, first && !(q.begin >= start && q.begin + q.tiles <= end));
-        if (first) {
-            const int at = __popc(firsts_of & before);
-            masks[at] = same;
-            if (opens >> tid & 1u) open_at[__popc(opens & before)] = uint32_t(at);
-        }
-        if (tid == 0) {
-            counts[0] = uint32_t(__popc(firsts_of));
-            counts[1] = uint32_t(__popc(opens));
-        }
-    }
-    __syncthreads();
-    constexpr int ITEMS = GROUP * (D / 4);
-    const int nopen = int(counts[1]);
-    for (int it = tid; it < int(counts[0]) * ITEMS; it += THREADS) {
-        const uint32_t same = masks[it / ITEMS];
-        const int item = it % ITEMS, row = item / (D / 4), c = (item % (D / 4)) * 4;
+    // Every warp sorts the pieces out for itself: those of a group follow one another.
+    const int lane = tid & 31;
+    const Range mine_piece = pieces[min(lane, 2 * RANGES - 1)];
+    const bool on = lane < 2 * RANGES && mine_piece.tiles != 0;
+    const uint32_t lower = (1u << lane) - 1u, all = __ballot_sync(0xffffffffu, on);
+    const uint32_t begin_before = __shfl_sync(0xffffffffu, mine_piece.begin, 31 - __clz(int((all & lower) | 1u)));
+    const uint32_t firsts_of = __ballot_sync(0xffffffffu, on && ((all & lower) == 0 || begin_before != mine_piece.begin));
+    // groups shared with other CTAs: the first and the last one's
+    uint32_t opens = __ballot_sync(0xffffffffu, (firsts_of >> lane & 1u) && !(mine_piece.begin >= start && mine_piece.begin + mine_piece.tiles <= end));
+    const int nopen = __popc(opens);
+    // four columns of a head each; a warp's are of one group
+    const int items = (min(GROUP, p.per_kv) * (D / 4) + 31) & ~31;
+    uint32_t groups_left = firsts_of;
+    for (int item = tid; groups_left; item += THREADS) {
+        for (; groups_left && item >= items; item -= items) groups_left &= groups_left - 1u;
+        if (!groups_left) break;
+        const uint32_t later = groups_left & (groups_left - 1u);
+        const uint32_t same = all & ~((groups_left & (0u - groups_left)) - 1u) & (later ? (later & (0u - later)) - 1u : 0xffffffffu);
+        const int row = item / (D / 4), c = (item % (D / 4)) * 4;
         const Range q = pieces[__ffs(int(same)) - 1];
         const int kv = q.g / p.chunks, head0 = kv * p.per_kv + (q.g % p.chunks) * GROUP;
         if (row >= min(GROUP, (kv + 1) * p.per_kv - head0)) continue;
@@ -352,7 +344,7 @@ __device__ __forceinline__ void join_ranges(const P& p, const Range& head, const
     // partial results (the count releases what the whole CTA has stored)
     __syncthreads();
     if (tid < nopen) {
-        const Range o = pieces[__ffs(int(masks[open_at[tid]])) - 1];
+        const Range o = pieces[__ffs(int(tid == 0 ? opens : opens & (opens - 1u))) - 1];
         const uint32_t c0 = cut_at.owner(o.begin), n = cut_at.owner(o.begin + o.tiles - 1) - c0 + 1;
         uint32_t* a = p.arrived + size_t(o.b) * groups + o.g;
         const bool last = atom_add_acq_rel_u32(a, 1u) == n - 1;
@@ -362,10 +354,10 @@ __device__ __forceinline__ void join_ranges(const P& p, const Range& head, const
         small[4 * tid + 2] = cut_at.start(c0) >= o.begin ? 0u : 1u;
     }
     __syncthreads();
-    for (int i = 0; i < nopen; ++i)
+    for (int i = 0; i < nopen; ++i, opens &= opens - 1u)
         if (small[4 * i])
-            join_group<D, GROUP, THREADS>(p, pieces[__ffs(int(masks[open_at[i]])) - 1], small[4 * i + 1], int(small[4 * i]),
-                                          small[4 * i + 2], tails);
+            join_group<D, GROUP, THREADS>(p, pieces[__ffs(int(opens)) - 1], small[4 * i + 1], int(small[4 * i]), small[4 * i + 2],
+                                          tails);
 }
 
 }  // namespace
