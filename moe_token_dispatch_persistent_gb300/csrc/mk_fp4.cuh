@@ -69,15 +69,38 @@ __device__ __forceinline__ void halves_of_e2m1x8(uint32_t w, uint32_t& a, uint32
         : "r"(w));
 }
 
-// y / f as the division would round it: the product with the reciprocal,
-// corrected once by what it leaves of y (see GroupScale).
-struct Quotient {
-    float f, inv, rest;
+// Packed pairs of fp32.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, r;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "mul.rn.f32x2 r, a, b;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 a, b, c, r;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 r, a, b, c;\n\tmov.b64 {%0, %1}, r;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
 
-    __device__ __forceinline__ explicit Quotient(float by) : f(by), inv(1.f / by), rest(isfinite(by) ? by : 0.f) {}
+// y / f of finite y as the division would round it: the product with the
+// reciprocal, corrected once by what it leaves of y (see GroupScale).
+struct Quotient {
+    float f, inv;
+
+    __device__ __forceinline__ explicit Quotient(float by) : f(by), inv(1.f / by) {}
     __device__ __forceinline__ float of(float y) const {
         const float q = y * inv;
-        return fabsf(q) < INFINITY ? fmaf(fmaf(-q, rest, y), inv, q) : q;
+        return fmaf(fmaf(-q, f, y), inv, q);
+    }
+    __device__ __forceinline__ float2 of(float2 y) const {
+        const float2 i2 = make_float2(inv, inv), q = mul2(y, i2);
+        return fma2(fma2(q, make_float2(-f, -f), y), i2, q);
     }
 };
 

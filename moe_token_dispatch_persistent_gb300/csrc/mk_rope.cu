@@ -20,6 +20,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "mk.h"
 #include "mk_fp4.cuh"
@@ -33,6 +34,7 @@ constexpr int ROPE_PAIRS = ROPE_MAX_D / 2;
 constexpr int ROPE_AXES = 4;
 constexpr int ROPE_WARPS = 8;
 constexpr int ROPE_AHEAD = 4;  // rows in flight per lane
+constexpr int ROPE_CTAS = 4;   // of an SM: 64 registers a thread
 
 struct RopeParams {
     const __nv_bfloat16 *q, *k, *v;
@@ -87,212 +89,343 @@ __device__ __forceinline__ void unpack8(const uint4& q, float (&y)[8]) {
     }
 }
 
-// LANES hold a row.  HALVES: column i pairs with i + rot/2, else i even with i + 1.
-template <int LANES, bool HALVES, int CACHE>
-__global__ void __launch_bounds__(ROPE_WARPS * 32) mk_qk_norm_rope_kernel(const RopeParams p) {
-    constexpr int ROWS = 32 / LANES;      // rows that a warp holds at a time
-    constexpr int MINE = HALVES ? 8 : 4;  // pairs of a lane's columns
-    __shared__ __align__(16) float2 table[ROPE_WARPS][ROPE_PAIRS];
+// A lane's four pairs (a, b) of columns, the first two and the last two pairs side
+// by side.  HALVES: a's are four neighbouring columns, in x and y, and b's another
+// four, in z and w; else a's are the low halves of the four words.
+struct Pairs {
+    float2 a[2], b[2];
+};
+template <bool HALVES>
+__device__ __forceinline__ Pairs unpack_pairs(const uint4& q) {
+    const auto lo = [](uint32_t u) { return __uint_as_float(u << 16); };
+    const auto hi = [](uint32_t u) { return __uint_as_float(u & 0xffff0000u); };
+    Pairs p;
+    if constexpr (HALVES) {
+        p.a[0] = make_float2(lo(q.x), hi(q.x));
+        p.a[1] = make_float2(lo(q.y), hi(q.y));
+        p.b[0] = make_float2(lo(q.z), hi(q.z));
+        p.b[1] = make_float2(lo(q.w), hi(q.w));
+    } else {
+        p.a[0] = make_float2(lo(q.x), lo(q.y));
+        p.b[0] = make_float2(hi(q.x), hi(q.y));
+        p.a[1] = make_float2(lo(q.z), lo(q.w));
+        p.b[1] = make_float2(hi(q.z), hi(q.w));
+    }
+    return p;
+}
+template <bool HALVES>
+__device__ __forceinline__ uint4 pack_pairs(const Pairs& p) {
+    if constexpr (HALVES)
+        return make_uint4(pack2(p.a[0].x, p.a[0].y), pack2(p.a[1].x, p.a[1].y), pack2(p.b[0].x, p.b[0].y), pack2(p.b[1].x, p.b[1].y));
+    else
+        return make_uint4(pack2(p.a[0].x, p.b[0].x), pack2(p.a[0].y, p.b[0].y), pack2(p.a[1].x, p.b[1].x), pack2(p.a[1].y, p.b[1].y));
+}
+
+// LANES hold a row, eight columns each.  HALVES: column i pairs with i + rot/2, else
+// i even with i + 1.  A lane's columns are four pairs, so a rotation stays in it:
+// with HALVES 4l .. and rot/2 + 4l .., otherwise, and past rot, 8l ..
+// WHOLE: every lane has columns, and all of them are rotated.
+template <int LANES, bool HALVES, int CACHE, bool WHOLE>
+__global__ void __launch_bounds__(ROPE_WARPS * 32, ROPE_CTAS) mk_qk_norm_rope_kernel(const __grid_constant__ RopeParams p) {
+    constexpr int ROWS = 32 / LANES;  // rows that a warp holds at a time
+    // 4-bit keys with HALVES: a scale's 16 columns lie in two neighbouring lanes only if a
+    // lane's eight follow one another, so the two of a pair meet by a shuffle.
+    constexpr bool KEYS_IN_ORDER = HALVES && CACHE == MK_CACHE_FP4;
+    constexpr int PAIRS = LANES * 4;
+    __shared__ uint64_t units[PAIRS];
+    __shared__ __align__(16) float2 table[ROPE_WARPS][PAIRS];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int sub = lane / LANES, l = lane % LANES, c = l * 8;
-    const int half = p.rot / 2;
-    const bool live = c < p.D, turned = c < p.rot;
-    const int pair0 = HALVES ? (c < half ? c : c - half) : c / 2;
-    const int partner = HALVES && turned ? (c < half ? lane + half / 8 : lane - half / 8) : lane;
+    const int D = WHOLE ? LANES * 8 : p.D, rot = WHOLE ? D : p.rot, half = rot / 2;
+    const bool live = WHOLE || c < D, turned = WHOLE || c < rot;
+    const int c0 = HALVES && turned ? l * 4 : c, c1 = HALVES && turned ? half + l * 4 : c + 4;
     const int steps = p.q_steps + p.k_steps + p.v_steps;
 
-    uint64_t unit[ROPE_PAIRS / 32];
-#pragma unroll
-    for (int i = 0; i < ROPE_PAIRS / 32; ++i) {
-        const int pair = i * 32 + lane;
-        unit[i] = pair < half ? turns_per_position(__ldg(p.inv_freq + pair)) : 0;
-    }
+    for (int pair = threadIdx.x; pair < half; pair += ROPE_WARPS * 32) units[pair] = turns_per_position(__ldg(p.inv_freq + pair));
+    __syncthreads();
     const uint4 none = make_uint4(0, 0, 0, 0);
-    uint4 wq = none, wk = none;
-    if (live && p.q_weight) wq = __ldg(reinterpret_cast<const uint4*>(p.q_weight + c));
-    if (live && p.k_weight) wk = __ldg(reinterpret_cast<const uint4*>(p.k_weight + c));
+    auto load_pairs = [&](const __nv_bfloat16* row) {
+        if constexpr (HALVES) {
+            const uint2 a = *reinterpret_cast<const uint2*>(row + c0), b = *reinterpret_cast<const uint2*>(row + c1);
+            return make_uint4(a.x, a.y, b.x, b.y);
+        } else {
+            return *reinterpret_cast<const uint4*>(row + c);
+        }
+    };
+    auto store_pairs = [&](__nv_bfloat16* row, const uint4& v) {
+        if constexpr (HALVES) {
+            *reinterpret_cast<uint2*>(row + c0) = make_uint2(v.x, v.y);
+            *reinterpret_cast<uint2*>(row + c1) = make_uint2(v.z, v.w);
+        } else {
+            *reinterpret_cast<uint4*>(row + c) = v;
+        }
+    };
+    const float inv_d = 1.f / float(D);
+
+    // The root mean square's reciprocal; `sum` of a lane's squares.
+    auto rstd_of = [&](float sum) {
+#pragma unroll
+        for (int d = LANES / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        return rsqrtf(fmaf(sum, inv_d, p.eps));
+    };
 
     for (int64_t item = int64_t(blockIdx.x) * ROPE_WARPS + warp; item < p.items; item += int64_t(gridDim.x) * ROPE_WARPS) {
-        const int t = int(item / p.parts), part = int(item - int64_t(t) * p.parts);
+        const int t = p.parts == 1 ? int(item) : int(item / p.parts), part = int(item - int64_t(t) * p.parts);
         const int s0 = int(int64_t(steps) * part / p.parts), s1 = int(int64_t(steps) * (part + 1) / p.parts);
 
-        auto load = [&](int s) -> uint4 {
-            if (s >= s1 || !live) return none;
-            const __nv_bfloat16* row;
-            int h = s * ROWS + sub, heads = p.Hq;
-            if (s < p.q_steps) {
-                row = p.q + t * p.q_stride + h * p.q_head;
-            } else if (s < p.q_steps + p.k_steps) {
-                h -= p.q_steps * ROWS;
-                heads = p.Hkv;
-                row = p.k + t * p.k_stride + h * p.k_head;
-            } else {
-                h -= (p.q_steps + p.k_steps) * ROWS;
-                heads = p.Hkv;
-                row = p.v + t * p.v_stride + h * p.v_head;
-            }
-            return h < heads ? *reinterpret_cast<const uint4*>(row + c) : none;
-        };
-        uint4 x[ROPE_AHEAD];
-#pragma unroll
-        for (int i = 0; i < ROPE_AHEAD; ++i) x[i] = load(s0 + i);
-
-        // where the token's keys and values go; -1: nowhere
-        int64_t page = -1, token = 0;
-        if (CACHE != MK_CACHE_NONE) {
-            const int64_t slot = __ldg(p.slots + t);
-            if (slot >= p.capacity) {
-                if (lane == 0) cache_error(p.err, 2u /* fault */, SITE_SLOT_RANGE, uint32_t(t));
-            } else if (slot >= 0) {
-                page = slot < (int64_t(1) << 31) ? int64_t(uint32_t(slot) / uint32_t(p.page_size)) : slot / p.page_size;
-                token = slot - page * p.page_size;
-            }
-        }
-
-        // sines and cosines of the token's pairs, then of this lane's
-        float cs[MINE], sn[MINE];
+        const int64_t slot = CACHE != MK_CACHE_NONE ? __ldg(p.slots + t) : 0;
+        // sines and cosines of the token's pairs
         if (s0 < p.q_steps + p.k_steps && half > 0) {
             __syncwarp();
 #pragma unroll
-            for (int i = 0; i < ROPE_PAIRS / 32; ++i) {
+            for (int i = 0; i < (PAIRS + 31) / 32; ++i) {
                 const int pair = i * 32 + lane;
                 if (pair < half) {
                     const int64_t pos = __ldg(p.positions + p.axis[pair] * p.position_stride + t);
-                    const int64_t turn = int64_t(uint64_t(pos) * unit[i]);
+                    const int64_t turn = int64_t(uint64_t(pos) * units[pair]);
                     float sine, cosine;
                     sincospif(float(int32_t(turn >> 32)) * 4.656612873077393e-10f /* 2^-31 */, &sine, &cosine);
                     table[warp][pair] = make_float2(cosine, sine);
                 }
             }
             __syncwarp();
-            if (turned) {
-#pragma unroll
-                for (int i = 0; i < MINE; ++i) {
-                    const float2 e = table[warp][pair0 + i];
-                    cs[i] = e.x;
-                    sn[i] = HALVES && c < half ? -e.y : e.y;
-                }
-            }
         }
 
-        auto norm_and_turn = [&](float (&y)[8], const void* weight, const uint4& w) {
+        // What the columns of a pair give to the turned pair, weights and angle together:
+        // a' = rstd (ca a - sb b), b' = rstd (cb b + sa a).
+        struct Turn {
+            float2 ca[2], cb[2], sa[2], sb[2];
+        };
+        auto turn_of = [&](const __nv_bfloat16* weight) {
+            Turn u;
+            Pairs f = unpack_pairs<HALVES>(live && weight ? load_pairs(weight) : none);
+            float4 e[2];  // cosines and sines of two pairs each
+            e[0] = e[1] = make_float4(1.f, 0.f, 1.f, 0.f);
+            if (turned) {
+                e[0] = *reinterpret_cast<const float4*>(&table[warp][l * 4]);
+                e[1] = *reinterpret_cast<const float4*>(&table[warp][l * 4 + 2]);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (!weight) f.a[i] = f.b[i] = make_float2(1.f, 1.f);
+                const float2 cs = make_float2(e[i].x, e[i].z), sn = make_float2(e[i].y, e[i].w);
+                u.ca[i] = mul2(f.a[i], cs);
+                u.cb[i] = mul2(f.b[i], cs);
+                u.sa[i] = mul2(f.a[i], sn);
+                u.sb[i] = mul2(f.b[i], make_float2(-sn.x, -sn.y));
+            }
+            return u;
+        };
+        auto norm_and_turn = [&](Pairs& y, const void* weight, const Turn& u) {
+            float rstd = 1.f;
+            if (weight) {
+                float2 sum = mul2(y.a[0], y.a[0]);
+                sum = fma2(y.a[1], y.a[1], sum);
+                sum = fma2(y.b[0], y.b[0], sum);
+                sum = fma2(y.b[1], y.b[1], sum);
+                rstd = rstd_of(sum.x + sum.y);
+            }
+            const float2 r = make_float2(rstd, rstd);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float2 a = y.a[i], b = y.b[i];
+                y.a[i] = mul2(a, u.ca[i]);
+                y.b[i] = mul2(b, u.cb[i]);
+                if (turned) {  // (else an infinite partner would make it NaN)
+                    y.a[i] = fma2(b, u.sb[i], y.a[i]);
+                    y.b[i] = fma2(a, u.sa[i], y.b[i]);
+                }
+                y.a[i] = mul2(y.a[i], r);
+                y.b[i] = mul2(y.b[i], r);
+            }
+        };
+        // The same of eight neighbouring columns, whose partners another lane holds.
+        auto norm_and_turn_in_order = [&](float (&y)[8], const __nv_bfloat16* weight) {
             if (weight) {
                 float sum = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) sum = fmaf(y[i], y[i], sum);
+                const float rstd = rstd_of(sum);
+                float f[8];
+                unpack8(live ? __ldg(reinterpret_cast<const uint4*>(weight + c)) : none, f);
 #pragma unroll
-                for (int d = LANES / 2; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-                const float rstd = rsqrtf(sum / float(p.D) + p.eps);
-                float wf[8];
-                unpack8(w, wf);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] = y[i] * rstd * wf[i];
+                for (int i = 0; i < 8; ++i) y[i] = y[i] * rstd * f[i];
             }
-            if (HALVES) {
-                float o[8];
+            const int partner = !turned ? lane : c < half ? lane + half / 8 : lane - half / 8;
+            float o[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, y[i], partner);
-                if (turned)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) y[i] = fmaf(o[i], sn[i % MINE], y[i] * cs[i % MINE]);
-            } else if (turned) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float a = y[2 * i], b = y[2 * i + 1];
-                    y[2 * i] = fmaf(-b, sn[i], a * cs[i]);
-                    y[2 * i + 1] = fmaf(a, sn[i], b * cs[i]);
-                }
-            }
-        };
-        // a row of keys or values into the cache; `out`: what the cache holds of it, or null
-        auto keep = [&](const float (&y)[8], uint8_t* cache, uint8_t* scales, const float* factor, int h, __nv_bfloat16* out) {
-            const bool on = live && h < p.Hkv;
-            if constexpr (CACHE == MK_CACHE_BF16) {
-                const uint4 b = pack8(y);
-                if (on && page >= 0)
-                    *reinterpret_cast<uint4*>(cache + page * p.page_stride + token * p.token_stride + h * p.head_stride + c * 2) = b;
-                if (on && out) *reinterpret_cast<uint4*>(out + c) = b;
-            } else if constexpr (CACHE == MK_CACHE_FP4) {
-                const float f = factor && on ? __ldg(factor + h) : 1.f;
-                float g[8], a = 0.f;
-                const Quotient by(f);
+            for (int i = 0; i < 8; ++i) o[i] = __shfl_sync(0xffffffffu, y[i], partner);
+            if (turned)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
-                    g[i] = factor ? by.of(y[i]) : y[i];
-                    a = max_nan(a, fabsf(g[i]));
+                    const float2 e = table[warp][(c < half ? c : c - half) + i];
+                    y[i] = fmaf(o[i], c < half ? -e.y : e.y, y[i] * e.x);
                 }
-                a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, 1));
-                const uint32_t byte = fp4_scale(a);
-                const float scale = float_of_half(halves_of_e4m3x2(byte));
-                const Quotient unit_of(scale);
-                uint32_t w = 0;
+        };
+        // Eight neighbouring columns into a 4-bit cache (the lane's place in it); `out`: what
+        // it holds of them, or null.
+        auto keep = [&](const float (&y)[8], bool on, uint8_t* cache, uint8_t* scales, const float* factor, __nv_bfloat16* out) {
+            const float f = factor && on ? __ldg(factor) : 1.f;
+            float a = 0.f;
+            float2 g[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w |= e2m1x2_of(unit_of.of(g[2 * i]), unit_of.of(g[2 * i + 1])) << (8 * i);
-                if (on && page >= 0) {
-                    *reinterpret_cast<uint32_t*>(cache + page * p.page_stride + token * p.token_stride + h * p.head_stride + c / 2) = w;
-                    if ((l & 1) == 0)
-                        scales[page * p.scale_page + token * p.scale_token + h * p.scale_head + c / FP4_GROUP] = uint8_t(byte);
-                }
-                if (on && out) {
-                    uint32_t e[4];
-                    halves_of_e2m1x8(w, e[0], e[1], e[2], e[3]);
-                    float held[8];
+            for (int i = 0; i < 4; ++i) {
+                g[i] = make_float2(y[2 * i], y[2 * i + 1]);
+                a = max_nan(a, max_nan(fabsf(g[i].x), fabsf(g[i].y)));
+            }
+            a = max_nan(a, __shfl_xor_sync(0xffffffffu, a, 1));
+            if (!(a < 3e38f)) {
+                // infinite and NaN values: a scale of 448 or NaN, and what is beyond the largest value is that
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        held[2 * i] = float_of_half(e[i]) * scale * f;
-                        held[2 * i + 1] = float_of_half(e[i] >> 16) * scale * f;
-                    }
-                    *reinterpret_cast<uint4*>(out + c) = pack8(held);
+                for (int i = 0; i < 4; ++i)
+                    g[i] = make_float2(fminf(fmaxf(g[i].x / f, -1e30f), 1e30f), fminf(fmaxf(g[i].y / f, -1e30f), 1e30f));
+                a = fabsf(a / f);
+            } else if (factor) {
+                const Quotient by(f);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) g[i] = by.of(g[i]);
+                a = fabsf(by.of(a));  // of the largest: the largest
+            }
+            const uint32_t byte = fp4_scale(a);
+            const float scale = float_of_half(halves_of_e4m3x2(byte));
+            const Quotient by(scale);
+            uint32_t e[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                g[i] = by.of(g[i]);
+                e[i] = e2m1x2_of(g[i].x, g[i].y);
+            }
+            const uint32_t w = __byte_perm(__byte_perm(e[0], e[1], 0x0040), __byte_perm(e[2], e[3], 0x0040), 0x5410);
+            if (on && cache) {
+                *reinterpret_cast<uint32_t*>(cache) = w;
+                if ((l & 1) == 0) *scales = uint8_t(byte);
+            }
+            if (on && out) {
+                const float2 by2 = make_float2(scale, scale), f2 = make_float2(f, f);
+                halves_of_e2m1x8(w, e[0], e[1], e[2], e[3]);
+                float held[8];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 v = mul2(mul2(make_float2(float_of_half(e[i]), float_of_half(e[i] >> 16)), by2), f2);
+                    held[2 * i] = v.x;
+                    held[2 * i + 1] = v.y;
                 }
-            } else {
-                if (on && out) *reinterpret_cast<uint4*>(out + c) = pack8(y);
+                *reinterpret_cast<uint4*>(out + c) = pack8(held);
             }
         };
 
-        for (int s = s0; s < s1; s += ROPE_AHEAD) {
+        // The rows of one kind, AHEAD of them on their way at a time; this lane's first one is
+        // of head h, `src` its place.
+        auto rows = [&](auto ahead, int first, int n, int heads, const __nv_bfloat16* src, int64_t stride, auto&& load, auto&& work) {
+            constexpr int AHEAD = decltype(ahead)::value;
+            const int a = max(s0 - first, 0), b = min(s1 - first, n);
+            int h = a * ROWS + sub;
+            src += h * stride;
+            for (int s = a; s < b; s += AHEAD) {
+                uint4 x[AHEAD];
 #pragma unroll
-            for (int i = 0; i < ROPE_AHEAD; ++i) {
-                if (s + i >= s1) break;  // the same for the whole warp
-                const uint4 raw = x[i];
-                float y[8];
-                unpack8(raw, y);
-                x[i] = load(s + i + ROPE_AHEAD);
-                int h = (s + i) * ROWS + sub;
-                if (s + i < p.q_steps) {
-                    norm_and_turn(y, p.q_weight, wq);
-                    if (live && h < p.Hq)
-                        *reinterpret_cast<uint4*>(p.q_out + (int64_t(t) * p.Hq + h) * p.D + c) = pack8(y);
-                } else if (s + i < p.q_steps + p.k_steps) {
-                    h -= p.q_steps * ROWS;
-                    norm_and_turn(y, p.k_weight, wk);
-                    keep(y, p.k_cache, p.k_scales, p.k_factor, h,
-                         p.k_out ? p.k_out + (int64_t(t) * p.Hkv + h) * p.D : nullptr);
-                } else {
-                    h -= (p.q_steps + p.k_steps) * ROWS;
-                    if constexpr (CACHE == MK_CACHE_BF16) {  // as they are
-                        if (live && h < p.Hkv && page >= 0)
-                            *reinterpret_cast<uint4*>(p.v_cache + page * p.page_stride + token * p.token_stride +
-                                                      h * p.head_stride + c * 2) = raw;
-                    } else {
-                        keep(y, p.v_cache, p.v_scales, p.v_factor, h,
-                             p.v_out ? p.v_out + (int64_t(t) * p.Hkv + h) * p.D : nullptr);
-                    }
+                for (int i = 0; i < AHEAD; ++i) {
+                    const bool on = s + i < b && live && h + i * ROWS < heads;
+                    x[i] = on ? load(src + i * ROWS * stride) : none;
                 }
+#pragma unroll
+                for (int i = 0; i < AHEAD; ++i)
+                    if (s + i < b) work(h + i * ROWS, live && h + i * ROWS < heads, x[i]);
+                h += AHEAD * ROWS;
+                src += AHEAD * ROWS * stride;
             }
+        };
+        using Deep = std::integral_constant<int, ROPE_AHEAD>;
+        using Shallow = std::integral_constant<int, CACHE == MK_CACHE_FP4 ? 2 : ROPE_AHEAD>;  // the code of 4 bits is long
+        if (s0 < p.q_steps) {
+            const Turn u = turn_of(p.q_weight);
+            __nv_bfloat16* const out = p.q_out + int64_t(t) * p.Hq * D;
+            rows(Deep{}, 0, p.q_steps, p.Hq, p.q + t * p.q_stride, p.q_head, load_pairs, [&](int h, bool on, const uint4& x) {
+                Pairs y = unpack_pairs<HALVES>(x);
+                norm_and_turn(y, p.q_weight, u);
+                if (on) store_pairs(out + h * D, pack_pairs<HALVES>(y));
+            });
+        }
+        if (s1 <= p.q_steps) continue;
+        // where the token's keys and values go, or nowhere
+        int64_t kept = 0, kept_scales = 0;
+        bool stored = false;
+        if constexpr (CACHE != MK_CACHE_NONE) {
+            stored = slot >= 0 && slot < p.capacity;
+            if (slot >= p.capacity && lane == 0) cache_error(p.err, 2u /* fault */, SITE_SLOT_RANGE, uint32_t(t));
+            if (stored) {
+                const int64_t page = slot < (int64_t(1) << 31) ? int64_t(uint32_t(slot) / uint32_t(p.page_size)) : slot / p.page_size;
+                const int64_t token = slot - page * p.page_size;
+                kept = page * p.page_stride + token * p.token_stride;
+                kept_scales = page * p.scale_page + token * p.scale_token;
+            }
+        }
+        if (s0 < p.q_steps + p.k_steps) {
+            __nv_bfloat16* const out = p.k_out ? p.k_out + int64_t(t) * p.Hkv * D : nullptr;
+            if constexpr (CACHE == MK_CACHE_FP4) {
+                Turn u;
+                if constexpr (!KEYS_IN_ORDER) u = turn_of(p.k_weight);
+                const auto load = [&](const __nv_bfloat16* row) { return KEYS_IN_ORDER ? *reinterpret_cast<const uint4*>(row + c) : load_pairs(row); };
+                rows(Shallow{}, p.q_steps, p.k_steps, p.Hkv, p.k + t * p.k_stride, p.k_head, load, [&](int h, bool on, const uint4& x) {
+                    float y[8];
+                    if constexpr (KEYS_IN_ORDER) {
+                        unpack8(x, y);
+                        norm_and_turn_in_order(y, p.k_weight);
+                    } else {
+                        Pairs z = unpack_pairs<HALVES>(x);
+                        norm_and_turn(z, p.k_weight, u);
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            y[4 * i] = z.a[i].x;
+                            y[4 * i + 1] = z.b[i].x;
+                            y[4 * i + 2] = z.a[i].y;
+                            y[4 * i + 3] = z.b[i].y;
+                        }
+                    }
+                    keep(y, on, stored ? p.k_cache + kept + h * p.head_stride + c / 2 : nullptr,
+                         p.k_scales + kept_scales + h * p.scale_head + c / FP4_GROUP, p.k_factor ? p.k_factor + h : nullptr,
+                         out ? out + h * D : nullptr);
+                });
+            } else {
+                const Turn u = turn_of(p.k_weight);
+                rows(Deep{}, p.q_steps, p.k_steps, p.Hkv, p.k + t * p.k_stride, p.k_head, load_pairs, [&](int h, bool on, const uint4& x) {
+                    Pairs y = unpack_pairs<HALVES>(x);
+                    norm_and_turn(y, p.k_weight, u);
+                    const uint4 v = pack_pairs<HALVES>(y);
+                    if (CACHE == MK_CACHE_BF16 && on && stored)
+                        store_pairs(reinterpret_cast<__nv_bfloat16*>(p.k_cache + kept + h * p.head_stride), v);
+                    if (on && out) store_pairs(out + h * D, v);
+                });
+            }
+        }
+        if constexpr (CACHE != MK_CACHE_NONE) {
+            const auto load = [&](const __nv_bfloat16* row) { return *reinterpret_cast<const uint4*>(row + c); };
+            __nv_bfloat16* const out = p.v_out ? p.v_out + int64_t(t) * p.Hkv * D : nullptr;
+            rows(Shallow{}, p.q_steps + p.k_steps, p.v_steps, p.Hkv, p.v + t * p.v_stride, p.v_head, load, [&](int h, bool on, const uint4& x) {
+                if constexpr (CACHE == MK_CACHE_BF16) {  // as they are
+                    if (on && stored) *reinterpret_cast<uint4*>(p.v_cache + kept + h * p.head_stride + c * 2) = x;
+                } else {
+                    float y[8];
+                    unpack8(x, y);
+                    keep(y, on, stored ? p.v_cache + kept + h * p.head_stride + c / 2 : nullptr,
+                         p.v_scales + kept_scales + h * p.scale_head + c / FP4_GROUP, p.v_factor ? p.v_factor + h : nullptr,
+                         out ? out + h * D : nullptr);
+                }
+            });
         }
     }
 }
 
-template <int LANES, bool HALVES>
-void launch_rope(const RopeParams& p, int cache, int grid, cudaStream_t st) {
-    if (cache == MK_CACHE_NONE) mk_qk_norm_rope_kernel<LANES, HALVES, MK_CACHE_NONE><<<grid, ROPE_WARPS * 32, 0, st>>>(p);
-    else if (cache == MK_CACHE_BF16) mk_qk_norm_rope_kernel<LANES, HALVES, MK_CACHE_BF16><<<grid, ROPE_WARPS * 32, 0, st>>>(p);
-    else mk_qk_norm_rope_kernel<LANES, HALVES, MK_CACHE_FP4><<<grid, ROPE_WARPS * 32, 0, st>>>(p);
+template <int LANES, bool HALVES, int CACHE>
+void launch_rope(const RopeParams& p, int grid, cudaStream_t st) {
+    if (p.D == LANES * 8 && p.rot == p.D) mk_qk_norm_rope_kernel<LANES, HALVES, CACHE, true><<<grid, ROPE_WARPS * 32, 0, st>>>(p);
+    else mk_qk_norm_rope_kernel<LANES, HALVES, CACHE, false><<<grid, ROPE_WARPS * 32, 0, st>>>(p);
 }
 template <int LANES>
 void launch_rope(const RopeParams& p, bool halves, int cache, int grid, cudaStream_t st) {
-    if (halves) launch_rope<LANES, true>(p, cache, grid, st);
-    else launch_rope<LANES, false>(p, cache, grid, st);
+    if (cache == MK_CACHE_NONE) halves ? launch_rope<LANES, true, MK_CACHE_NONE>(p, grid, st) : launch_rope<LANES, false, MK_CACHE_NONE>(p, grid, st);
+    else if (cache == MK_CACHE_BF16) halves ? launch_rope<LANES, true, MK_CACHE_BF16>(p, grid, st) : launch_rope<LANES, false, MK_CACHE_BF16>(p, grid, st);
+    else halves ? launch_rope<LANES, true, MK_CACHE_FP4>(p, grid, st) : launch_rope<LANES, false, MK_CACHE_FP4>(p, grid, st);
 }
 
 bool row_strides(const void* base, int64_t token, int64_t head) {
@@ -402,12 +535,14 @@ extern "C" mk_status_t mk_qk_norm_rope(const mk_qk_norm_rope_t* a, void* stream)
     p.k_steps = (a->Hkv + rows - 1) / rows;
     p.v_steps = stored ? p.k_steps : 0;
     const int steps = p.q_steps + p.k_steps + p.v_steps;
-    // A warp per token when the tokens alone fill the GPU twice over, else as many
-    // parts of a token's heads as fill it.
-    const int64_t room = int64_t(sms) * ROPE_WARPS * 8;
-    p.parts = int(std::max<int64_t>(1, std::min<int64_t>(steps, room / a->T)));
+    // A warp per token when there are enough of them; else parts of a token's heads, of
+    // four turns or more (each part computes the token's sines), or of one where all of
+    // them are at work at once all the same.
+    const int64_t warps = int64_t(sms) * ROPE_CTAS * ROPE_WARPS;
+    const int64_t most = int64_t(a->T) * steps * 2 <= warps ? steps : (steps + 3) / 4;
+    p.parts = int(std::max<int64_t>(1, std::min<int64_t>(most, warps / a->T)));
     p.items = int64_t(a->T) * p.parts;
-    const int grid = int(std::min<int64_t>((p.items + ROPE_WARPS - 1) / ROPE_WARPS, int64_t(sms) * 8));
+    const int grid = int(std::min<int64_t>((p.items + ROPE_WARPS - 1) / ROPE_WARPS, int64_t(sms) * ROPE_CTAS));
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool halves = a->pairs == MK_PAIR_HALVES;
     if (lanes == 4) launch_rope<4>(p, halves, a->cache, grid, st);
