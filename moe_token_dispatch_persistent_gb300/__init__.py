@@ -787,9 +787,9 @@ def fp4_cache(pages, page_size, heads, D, device="cuda"):
 
 def _cache_pair(k, v, dtype, cols, what):
     """Shape and strides that the two tensors of a cache share."""
-    if k.dtype is not dtype or v.dtype is not dtype or k.get_device() != v.get_device() or k.dim() != 4:
-        raise ValueError(f"{what} must be {dtype} [pages, page_size, Hkv, {cols}] on q's device")
     shape, strides = k.shape, k.stride()
+    if k.dtype is not dtype or v.dtype is not dtype or k.get_device() != v.get_device() or len(shape) != 4:
+        raise ValueError(f"{what} must be {dtype} [pages, page_size, Hkv, {cols}] on q's device")
     if v.shape != shape or (v.stride() != strides and any(
             n > 1 and a != b for n, a, b in zip(shape, strides, v.stride()))):
         raise ValueError(f"{what} must agree in shape and strides")
@@ -798,14 +798,14 @@ def _cache_pair(k, v, dtype, cols, what):
     return shape, strides
 
 
-def _fp4_cache_checks(dev, D, shape, k_cache, k_scales, v_scales, Hkv, factors):
-    """Strides of the scales and pointers of the factors of a 4-bit cache."""
+def _fp4_cache_checks(dev, D, shape, k_scales, v_scales, Hkv, k_factor, v_factor):
+    """Strides of the scales of a 4-bit cache."""
     torch = _torch
     s_shape, s_strides = _cache_pair(k_scales, v_scales, torch.float8_e4m3fn, D // 16, "k_scales and v_scales")
     if s_shape[:3] != shape[:3] or k_scales.get_device() != dev:
         raise ValueError("the scales must be [pages, page_size, Hkv, D/16] of the caches' pages")
-    for f in factors:
-        if f is not None and (f.shape != (Hkv,) or f.dtype is not torch.float32 or f.get_device() != dev
+    for f in (k_factor, v_factor):
+        if f is not None and (f.dtype is not torch.float32 or f.get_device() != dev or f.shape != (Hkv,)
                               or not f.is_contiguous()):
             raise ValueError("k_factor and v_factor must be f32 [Hkv] on q's device")
     return s_strides
@@ -833,27 +833,41 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e
     and with ``keep`` and a 4-bit cache ``k`` and ``v`` as the cache holds them.
     """
     torch = _torch or _load_torch()
-    b16 = torch.bfloat16
+    b16, i32, f32 = torch.bfloat16, torch.int32, torch.float32
     T, Hq, D = q.shape
     dev = q.get_device()
     if dev < 0 or q.dtype is not b16:
         raise ValueError("q must be a CUDA bf16 [T,Hq,D] tensor")
     _on_device(dev)
     Hkv = k.shape[1] if k.dim() == 3 else 0
-    q_strides, k_strides, v_strides = q.stride(), k.stride(), (0, 0, 1)
-    if k.dtype is not b16 or k.get_device() != dev or k.shape != (T, Hkv, D) or q_strides[2] != 1 or k_strides[2] != 1:
-        raise ValueError("q and k must be bf16 [T,heads,D] on one device, a head's columns contiguous")
-    half = inv_freq.shape[0] if inv_freq.dim() == 1 else -1
-    if half < 0 or inv_freq.dtype is not torch.float32 or inv_freq.get_device() != dev or not inv_freq.is_contiguous():
+    heads = (T, Hkv, D)
+    q_stride, q_head, q_last = q.stride()
+    if k.dtype is not b16 or k.get_device() != dev or k.shape != heads:
+        raise ValueError("q and k must be bf16 [T,heads,D] on one device")
+    k_stride, k_head, k_last = k.stride()
+    if q_last != 1 or k_last != 1:
+        raise ValueError("the columns of a head must be contiguous")
+    if inv_freq.dtype is not f32 or inv_freq.dim() != 1 or inv_freq.get_device() != dev or not inv_freq.is_contiguous():
         raise ValueError("inv_freq must be f32 [rot/2] on q's device")
-    axes = positions.shape[0] if positions.dim() == 2 else 1
-    if (positions.shape not in ((T,), (axes, T)) or positions.dtype is not torch.int32 or positions.get_device() != dev
-            or (T > 1 and positions.stride(-1) != 1)):
-        raise ValueError("positions must be i32 [T] or [axes,T] on q's device")
-    for w in (q_weight, k_weight):
-        if w is not None and (w.dtype is not b16 or w.get_device() != dev or w.shape != (D,) or not w.is_contiguous()):
-            raise ValueError("q_weight and k_weight must be bf16 [D] on q's device")
-    each = p_axis = None
+    half = inv_freq.shape[0]
+    axes, pos_stride = 1, 0
+    if positions.dim() == 2:
+        axes = positions.shape[0]
+        pos_stride, last = positions.stride()
+        good = positions.shape[1] == T and (last == 1 or T <= 1)
+    else:
+        good = positions.shape == (T,) and positions.is_contiguous()
+    if not good or positions.dtype is not i32 or positions.get_device() != dev:
+        raise ValueError("positions must be i32 [T] or [axes,T] on q's device, an axis contiguous")
+    p_qw = p_kw = p_axis = p_v = p_slots = p_kc = p_vc = p_ks = p_vs = p_kf = p_vf = p_k = p_held = 0
+    if q_weight is not None:
+        if q_weight.dtype is not b16 or q_weight.get_device() != dev or q_weight.shape != (D,) or not q_weight.is_contiguous():
+            raise ValueError("q_weight must be bf16 [D] on q's device")
+        p_qw = q_weight.data_ptr()
+    if k_weight is not None:
+        if k_weight.dtype is not b16 or k_weight.get_device() != dev or k_weight.shape != (D,) or not k_weight.is_contiguous():
+            raise ValueError("k_weight must be bf16 [D] on q's device")
+        p_kw = k_weight.data_ptr()
     if pair_axis is not None:
         if len(pair_axis) != half or any(not 0 <= a < axes for a in pair_axis):
             raise ValueError("pair_axis must name a row of positions for each of inv_freq")
@@ -861,49 +875,58 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e
         p_axis = ctypes.addressof(each)
     elif axes > 1:
         raise ValueError("positions of several axes need pair_axis")
-    cache, page_size, pages = MK_CACHE_NONE, 0, 0
-    strides = s_strides = (0, 0, 0)
+    cache, page_size, pages, v_stride, v_head = MK_CACHE_NONE, 0, 0, 0, 0
+    page, token, head = s_page, s_token, s_head = 0, 0, 0
     if k_cache is None:
-        if any(t is not None for t in (v, slots, v_cache, k_scales, v_scales, k_factor, v_factor)):
+        if not (v is None and slots is None and v_cache is None and k_scales is None and v_scales is None
+                and k_factor is None and v_factor is None):
             raise ValueError("v, slots, scales and factors belong to a cache")
         if keep is False:
             raise ValueError("without a cache the keys are an output")
+        keep = True
     else:
         if v is None or slots is None or v_cache is None:
             raise ValueError("a cache needs v, slots, k_cache and v_cache")
-        v_strides = v.stride()
-        if v.dtype is not b16 or v.get_device() != dev or v.shape != (T, Hkv, D) or v_strides[2] != 1:
+        if v.dtype is not b16 or v.get_device() != dev or v.shape != heads:
             raise ValueError("v must be bf16 [T,Hkv,D] on q's device")
-        if (slots.shape != (T,) or slots.dtype is not torch.int64 or slots.get_device() != dev
-                or not slots.is_contiguous()):
+        v_stride, v_head, v_last = v.stride()
+        if v_last != 1:
+            raise ValueError("the columns of a head must be contiguous")
+        if slots.dtype is not torch.int64 or slots.get_device() != dev or slots.shape != (T,) or not slots.is_contiguous():
             raise ValueError("slots must be i64 [T] on q's device")
         fp4 = k_cache.dtype is torch.uint8
-        cache = MK_CACHE_FP4 if fp4 else MK_CACHE_BF16
-        shape, strides = _cache_pair(k_cache, v_cache, torch.uint8 if fp4 else b16, D // 2 if fp4 else D,
-                                     "k_cache and v_cache")
-        pages, page_size = shape[0], shape[1]
-        if k_cache.get_device() != dev or shape[2] != Hkv:
+        shape, (page, token, head, _) = _cache_pair(k_cache, v_cache, torch.uint8 if fp4 else b16, D // 2 if fp4 else D,
+                                                    "k_cache and v_cache")
+        pages, page_size, n, _ = shape
+        if k_cache.get_device() != dev or n != Hkv:
             raise ValueError("k_cache and v_cache must be [pages, page_size, Hkv, columns] on q's device")
         if fp4:
+            cache = MK_CACHE_FP4
             if k_scales is None or v_scales is None:
                 raise ValueError("a 4-bit cache needs k_scales and v_scales")
-            s_strides = _fp4_cache_checks(dev, D, shape, k_cache, k_scales, v_scales, Hkv, (k_factor, v_factor))
-        elif any(t is not None for t in (k_scales, v_scales, k_factor, v_factor)):
-            raise ValueError("scales and factors belong to a 4-bit cache")
+            s_page, s_token, s_head, _ = _fp4_cache_checks(dev, D, shape, k_scales, v_scales, Hkv, k_factor, v_factor)
+            p_ks, p_vs = k_scales.data_ptr(), v_scales.data_ptr()
+            p_kf = 0 if k_factor is None else k_factor.data_ptr()
+            p_vf = 0 if v_factor is None else v_factor.data_ptr()
+        else:
+            cache = MK_CACHE_BF16
+            if not (k_scales is None and v_scales is None and k_factor is None and v_factor is None):
+                raise ValueError("scales and factors belong to a 4-bit cache")
+        p_v, p_slots, p_kc, p_vc = v.data_ptr(), slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
     other = None if stream is None else _other_stream(stream, dev)
     empty = _empty if other is None else _empty_on(other)
-    o = {"q": empty((T, Hq, D), (Hq * D, D, 1), b16, dev)}
-    if cache == MK_CACHE_NONE or keep:
-        o["k"] = empty((T, Hkv, D), (Hkv * D, D, 1), b16, dev)
+    out = empty((T, Hq, D), (Hq * D, D, 1), b16, dev)
+    o = {"q": out}
+    if keep:
+        o["k"] = t = empty(heads, (Hkv * D, D, 1), b16, dev)
+        p_k = t.data_ptr()
         if cache == MK_CACHE_FP4:
-            o["v"] = empty((T, Hkv, D), (Hkv * D, D, 1), b16, dev)
-    ptr = lambda t: 0 if t is None else t.data_ptr()  # noqa: E731
+            o["v"] = t = empty(heads, (Hkv * D, D, 1), b16, dev)
+            p_held = t.data_ptr()
     args = _rope_args.pack(
-        q.data_ptr(), k.data_ptr(), ptr(v), q_strides[0], q_strides[1], k_strides[0], k_strides[1], v_strides[0],
-        v_strides[1], ptr(q_weight), ptr(k_weight), positions.data_ptr(), positions.stride(0) if axes > 1 else 0,
-        inv_freq.data_ptr(), p_axis or 0, o["q"].data_ptr(), ptr(o.get("k")), ptr(o.get("v")), ptr(slots), ptr(k_cache),
-        ptr(v_cache), strides[0], strides[1], strides[2], ptr(k_scales), ptr(v_scales), s_strides[0], s_strides[1],
-        s_strides[2], ptr(k_factor), ptr(v_factor), T, Hq, Hkv, D, 2 * half, axes,
+        q.data_ptr(), k.data_ptr(), p_v, q_stride, q_head, k_stride, k_head, v_stride, v_head, p_qw, p_kw,
+        positions.data_ptr(), pos_stride, inv_freq.data_ptr(), p_axis, out.data_ptr(), p_k, p_held, p_slots, p_kc, p_vc, page,
+        token, head, p_ks, p_vs, s_page, s_token, s_head, p_kf, p_vf, T, Hq, Hkv, D, 2 * half, axes,
         MK_PAIR_NEIGHBOURS if interleaved else MK_PAIR_HALVES, cache, page_size, pages, eps, 0)
     status = lib().mk_qk_norm_rope(args, _raw_stream(dev) if stream is None else _stream(stream))
     if status or check or other is not None:
@@ -953,7 +976,7 @@ def paged_attention_fp4(q, k_cache, v_cache, k_scales, v_scales, block_table, se
     pages, page_size, Hkv, _ = shape
     if k_cache.get_device() != dev:
         raise ValueError("k_cache and v_cache must be on q's device")
-    s_strides = _fp4_cache_checks(dev, D, shape, k_cache, k_scales, v_scales, Hkv, (k_factor, v_factor))
+    s_strides = _fp4_cache_checks(dev, D, shape, k_scales, v_scales, Hkv, k_factor, v_factor)
     rows, max_pages = block_table.shape
     if rows != B or block_table.dtype is not i32 or block_table.get_device() != dev or not block_table.is_contiguous():
         raise ValueError("block_table must be i32 [B,max_pages]")
@@ -1018,17 +1041,20 @@ def mk_pages_workspace_size(max_pages, num_pages, n) -> int:
     return int(lib().mk_pages_workspace_size(max_pages, num_pages, n))
 
 
+_i64_arrays = {}  # C array types by length
+
+
 def _page_buffers(caches, dev, pages=None):
-    """C arrays of tensors whose first dimension is the page and whose pages are
-    dense, in whatever order of the other dimensions."""
+    """The three C arrays of tensors whose first dimension is the page and whose
+    pages are dense, in whatever order of the other dimensions: their addresses,
+    their length, what holds them, and the number of pages."""
     base, strides, sizes = [], [], []
-    seen = None
+    shape = stride = dtype = None
     for t in caches:
         if t.get_device() != dev:
             raise ValueError("the caches must be on one device")
-        layout = (t.shape, t.stride(), t.dtype)
-        if layout != seen:  # a layer's is the one before's
-            shape, stride, _ = seen = layout
+        if t.shape != shape or t.stride() != stride or t.dtype is not dtype:  # a layer's is the one before's
+            shape, stride, dtype = t.shape, t.stride(), t.dtype
             if len(shape) < 2:
                 raise ValueError("a cache's first dimension is its pages")
             if pages is None:
@@ -1046,7 +1072,12 @@ def _page_buffers(caches, dev, pages=None):
         strides.append(step)
         sizes.append(block)
     n = len(base)
-    return ((ctypes.c_void_p * n)(*base), (ctypes.c_int64 * n)(*strides), (ctypes.c_int64 * n)(*sizes), n), pages
+    kind = _i64_arrays.get(n)
+    if kind is None:
+        kind = _i64_arrays[n] = ctypes.c_int64 * (3 * n)
+    arrays = kind(*base, *strides, *sizes)
+    at = ctypes.addressof(arrays)
+    return at, at + 8 * n, at + 16 * n, n, arrays, pages
 
 
 def _i32_list(t, dev, n, what):
@@ -1083,9 +1114,9 @@ def copy_pages(caches, src, dst, stream=None, check=True):
     _on_device(dev)
     n = _i32_list(src, dev, None, "src")
     _i32_list(dst, dev, n, "dst")
-    buffers, pages = _page_buffers(caches, dev)
+    base, strides, sizes, number, _held, pages = _page_buffers(caches, dev)
     other = None if stream is None else _other_stream(stream, dev)
-    status = lib().mk_copy_pages(*buffers, pages or 0, src.data_ptr(), dst.data_ptr(), n,
+    status = lib().mk_copy_pages(base, strides, sizes, number, pages or 0, src.data_ptr(), dst.data_ptr(), n,
                                  _raw_stream(dev) if stream is None else _stream(stream))
     if status or check or other is not None:
         _finish(status, "mk_copy_pages", stream, other, check, (src, dst, *caches), ())
@@ -1124,11 +1155,12 @@ def extend_sequences(block_table, seq_lens, refs, seqs, count, most, caches, pag
     dev, pool = _pool(block_table, seq_lens, refs, page_size)
     n = _i32_list(seqs, dev, None, "seqs")
     _i32_list(count, dev, n, "count")
-    buffers, _ = _page_buffers(caches, dev, refs.shape[0])
+    base, strides, sizes, number, _held, _ = _page_buffers(caches, dev, refs.shape[0])
     other = None if stream is None else _other_stream(stream, dev)
     slots = (_empty if other is None else _empty_on(other))((n, most), (most, 1), _torch.int64, dev)
-    status = lib().mk_extend_sequences(*pool, seqs.data_ptr(), count.data_ptr(), n, most, slots.data_ptr(), *buffers,
-                                       _raw_stream(dev) if stream is None else _stream(stream), _ptr(workspace), ws_bytes)
+    status = lib().mk_extend_sequences(*pool, seqs.data_ptr(), count.data_ptr(), n, most, slots.data_ptr(), base, strides,
+                                       sizes, number, _raw_stream(dev) if stream is None else _stream(stream), _ptr(workspace),
+                                       ws_bytes)
     if status or check or other is not None:
         _finish(status, "mk_extend_sequences", stream, other, check,
                 (block_table, seq_lens, refs, seqs, count, workspace, *caches), (slots,))
@@ -1141,7 +1173,7 @@ def compact_pages(block_table, seq_lens, refs, caches, page_size, table_out=None
     ``block_table`` and ``refs`` as they are then, in ``table_out`` and
     ``refs_out`` when given (which may be block_table and refs themselves)."""
     dev, pool = _pool(block_table, seq_lens, refs, page_size)
-    buffers, _ = _page_buffers(caches, dev, refs.shape[0])
+    base, strides, sizes, number, _held, _ = _page_buffers(caches, dev, refs.shape[0])
     other = None if stream is None else _other_stream(stream, dev)
     empty = _empty if other is None else _empty_on(other)
     made = []
@@ -1154,7 +1186,7 @@ def compact_pages(block_table, seq_lens, refs, caches, page_size, table_out=None
         made.append(refs_out := empty((pool[5],), (1,), i32, dev))
     elif refs_out.dtype is not i32 or refs_out.get_device() != dev or refs_out.shape != refs.shape or not refs_out.is_contiguous():
         raise ValueError("refs_out must be like refs")
-    status = lib().mk_compact_pages(*pool, table_out.data_ptr(), refs_out.data_ptr(), *buffers,
+    status = lib().mk_compact_pages(*pool, table_out.data_ptr(), refs_out.data_ptr(), base, strides, sizes, number,
                                     _raw_stream(dev) if stream is None else _stream(stream), _ptr(workspace), ws_bytes)
     if status or check or other is not None:
         _finish(status, "mk_compact_pages", stream, other, check,

@@ -10,8 +10,8 @@
 // reported.
 //
 // The lists are short, so the latency of dependent loads and of the launches
-// bounds all but the moved bytes, which go at the rate of a copy: units of 16 KiB,
-// one per CTA at a time, 64 bytes in flight per thread.
+// bounds all but the moved bytes, which go at the rate of a copy: units of 32 KiB,
+// one per CTA at a time, 128 bytes in flight per thread.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -30,7 +30,7 @@ constexpr int MAX_ROWS = 65536;        // rows of a block table
 constexpr int MAX_PAGES = 1 << 30;
 constexpr int MAX_CACHES = 128;        // buffers of one copying launch (its parameters)
 constexpr int COPY_THREADS = 256;
-constexpr int COPY_DEEP = 4;           // pieces in flight per thread
+constexpr int COPY_DEEP = 8;           // pieces in flight per thread
 constexpr int PLAN_THREADS = 1024;
 
 // Buffers whose pages move together.
@@ -63,7 +63,7 @@ __device__ __forceinline__ void move_pages(const Buffers& b, const int32_t* src,
                                            DevError* err) {
     const uint32_t units = b.first[b.n];
     for (int64_t u = blockIdx.x; u < int64_t(moves) * units; u += gridDim.x) {
-        const int i = int(u / units);
+        const int i = u <= UINT32_MAX ? int(uint32_t(u) / units) : int(u / units);
         const uint32_t in = uint32_t(u - int64_t(i) * units);
         int lo = 0, hi = b.n;  // the last buffer with first <= in
         while (hi - lo > 1) {
@@ -89,6 +89,10 @@ __global__ void __launch_bounds__(COPY_THREADS) mk_copy_pages_kernel(const __gri
                                                                      const int32_t* dst, int moves, int num_pages, DevError* err) {
     move_pages(b, src, dst, moves, num_pages, err);
 }
+
+// A kernel that was launched to start beside the one before it waits here until that
+// one is done and its results are seen.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 struct Pool {
     int32_t* table;
@@ -124,33 +128,15 @@ __device__ bool list_is_good(const Pool& p, const int32_t* list, int n, uint32_t
 // ---- fork: the children give their pages back and hold their parents'
 
 // First the counts, and the parents' rows as they were into `kept` (a child may
-// be another's parent); a CTA per pair.  kept_len[i]: -1 when the call is refused.
-__global__ void __launch_bounds__(256) mk_fork_count_kernel(Pool p, const int32_t* parent, const int32_t* child, int n,
-                                                            int32_t* kept, int32_t* kept_len) {
-    __shared__ uint32_t seen[MAX_ROWS / 32];
-    __shared__ int bad;
-    const int i = blockIdx.x;
-    bool good = list_is_good(p, child, n, seen, &bad);
-    if (good) {  // a parent may be named any number of times
-        for (int j = threadIdx.x; j < n; j += blockDim.x) {
-            const int s = __ldg(parent + j);
-            if (s < 0 || s >= p.rows) atomicMin(&bad, j);
-        }
-        __syncthreads();
-        good = bad == INT_MAX;
-        if (!good && threadIdx.x == 0 && i == 0) cache_error(p.err, ERR_FAULT, SITE_SEQUENCE, uint32_t(bad));
-    }
-    if (!good) {
-        if (threadIdx.x == 0) kept_len[i] = -1;
-        return;
-    }
-    const int from = __ldg(parent + i), to = __ldg(child + i), len = p.lens[from], old = p.lens[to];
+// be another's parent), then the rows.  Threads [t0, ..), `step` apart, take pair i.
+__device__ __forceinline__ void fork_count(const Pool& p, int from, int to, int32_t* kept, int32_t* kept_len, int t0, int step) {
+    const int len = p.lens[from], old = p.lens[to];
     const int32_t *theirs = p.table + int64_t(from) * p.max_pages, *before = p.table + int64_t(to) * p.max_pages;
     const int np = p.pages_of(len), no = p.pages_of(old);
-    for (int j = threadIdx.x; j < max(np, no); j += blockDim.x) {
+    for (int j = t0; j < max(np, no); j += step) {
         if (j < np) {
             const int page = theirs[j];
-            kept[int64_t(i) * p.max_pages + j] = page;
+            kept[j] = page;
             if (p.holds(page)) atomicAdd(p.refs + page, 1);
             else cache_error(p.err, ERR_FAULT, SITE_PAGE_INDEX, uint32_t(page));
         }
@@ -160,15 +146,52 @@ __global__ void __launch_bounds__(256) mk_fork_count_kernel(Pool p, const int32_
             else cache_error(p.err, ERR_FAULT, SITE_PAGE_INDEX, uint32_t(page));
         }
     }
-    if (threadIdx.x == 0) kept_len[i] = max(len, 0);
+    if (t0 == 0) *kept_len = max(len, 0);
+}
+__device__ __forceinline__ void fork_row(const Pool& p, int to, const int32_t* kept, int len, int t0, int step) {
+    const int np = p.pages_of(len);
+    for (int j = t0; j < np; j += step) p.table[int64_t(to) * p.max_pages + j] = kept[j];
+    if (t0 == 0) p.lens[to] = len;
+}
+__device__ bool fork_is_good(const Pool& p, const int32_t* parent, const int32_t* child, int n, uint32_t* seen, int* bad) {
+    if (!list_is_good(p, child, n, seen, bad)) return false;
+    for (int j = threadIdx.x; j < n; j += blockDim.x) {  // a parent may be named any number of times
+        const int s = __ldg(parent + j);
+        if (s < 0 || s >= p.rows) atomicMin(bad, j);
+    }
+    __syncthreads();
+    if (*bad == INT_MAX) return true;
+    if (threadIdx.x == 0 && blockIdx.x == 0) cache_error(p.err, ERR_FAULT, SITE_SEQUENCE, uint32_t(*bad));
+    return false;
+}
+// A CTA per pair; kept_len[i]: -1 when the call is refused.
+__global__ void __launch_bounds__(256) mk_fork_count_kernel(Pool p, const int32_t* parent, const int32_t* child, int n,
+                                                            int32_t* kept, int32_t* kept_len) {
+    __shared__ uint32_t seen[MAX_ROWS / 32];
+    __shared__ int bad;
+    const int i = blockIdx.x;
+    if (fork_is_good(p, parent, child, n, seen, &bad))
+        fork_count(p, __ldg(parent + i), __ldg(child + i), kept + int64_t(i) * p.max_pages, kept_len + i, threadIdx.x, 256);
+    else if (threadIdx.x == 0)
+        kept_len[i] = -1;
 }
 __global__ void __launch_bounds__(256) mk_fork_rows_kernel(Pool p, const int32_t* child, const int32_t* kept, const int32_t* kept_len) {
+    wait_for_previous();
     const int i = blockIdx.x, len = kept_len[i];
-    if (len < 0) return;
-    const int to = __ldg(child + i), np = p.pages_of(len);
-    for (int j = threadIdx.x; j < np; j += blockDim.x)
-        p.table[int64_t(to) * p.max_pages + j] = kept[int64_t(i) * p.max_pages + j];
-    if (threadIdx.x == 0) p.lens[to] = len;
+    if (len >= 0) fork_row(p, __ldg(child + i), kept + int64_t(i) * p.max_pages, len, threadIdx.x, 256);
+}
+// All of it by one CTA, a warp per pair: for a few sequences one launch less on the host
+// (a fork and an extension of one pair 30 us there, 36 with the two above; 12 on the GPU).
+constexpr int FORK_FEW = PLAN_THREADS / 32;
+__global__ void __launch_bounds__(PLAN_THREADS) mk_fork_few_kernel(Pool p, const int32_t* parent, const int32_t* child, int n,
+                                                                   int32_t* kept, int32_t* kept_len) {
+    __shared__ uint32_t seen[MAX_ROWS / 32];
+    __shared__ int bad;
+    if (!fork_is_good(p, parent, child, n, seen, &bad)) return;
+    const int i = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (i < n) fork_count(p, __ldg(parent + i), __ldg(child + i), kept + int64_t(i) * p.max_pages, kept_len + i, lane, 32);
+    __syncthreads();
+    if (i < n) fork_row(p, __ldg(child + i), kept + int64_t(i) * p.max_pages, kept_len[i], lane, 32);
 }
 
 // ---- free
@@ -337,6 +360,7 @@ __global__ void __launch_bounds__(PLAN_THREADS) mk_extend_plan_kernel(Pool p, co
 __global__ void __launch_bounds__(COPY_THREADS) mk_extend_kernel(Pool p, const __grid_constant__ Buffers b, const int32_t* seqs,
                                                                  const int32_t* count, int n, int most, const Extension* head,
                                                                  const int32_t* src, const int32_t* dst, int64_t* slots) {
+    wait_for_previous();
     const Extension e = *head;
     if (slots)
         for (int64_t x = int64_t(blockIdx.x) * COPY_THREADS + threadIdx.x; x < int64_t(n) * most; x += int64_t(gridDim.x) * COPY_THREADS) {
@@ -377,6 +401,7 @@ struct Compaction {
 __global__ void __launch_bounds__(256) mk_compact_plan_kernel(const int32_t* refs, int num_pages, int each, const int32_t* counts,
                                                               Compaction* head, int32_t* src, int32_t* dst, int32_t* rank) {
     __shared__ int part[32];
+    wait_for_previous();
     const int tid = threadIdx.x, parts = gridDim.x;
     int used = 0, before = 0;
     for (int i = tid; i < parts; i += 256) {
@@ -419,6 +444,7 @@ struct CompactOut {
 };
 __global__ void __launch_bounds__(COPY_THREADS) mk_compact_kernel(Pool p, CompactOut c, const __grid_constant__ Buffers b, const Compaction* head,
                                                                   const int32_t* src, const int32_t* dst, const int32_t* rank) {
+    wait_for_previous();
     const Compaction e = *head;
     const int64_t t0 = int64_t(blockIdx.x) * COPY_THREADS + threadIdx.x, step = int64_t(gridDim.x) * COPY_THREADS;
     for (int64_t x = t0; x < int64_t(p.rows) * p.max_pages; x += step) {
@@ -486,7 +512,7 @@ Buffers some_buffers(const CacheList& c, int i0) {
     return b;
 }
 
-int copy_grid(int sms) { return sms * 8; }
+int copy_grid(int sms) { return sms * 32; }
 
 mk_status_t pool_arguments(const void* table, const void* lens, const void* refs, int rows, int max_pages, int num_pages,
                            int page_size, int n) {
@@ -509,6 +535,21 @@ mk_status_t workspace_of(Workspace& cached, int dev, cudaStream_t st, void* work
     const mk_status_t s = cached.get(WS_PAGES, dev, st, need, need);
     *out = cached.data();
     return s;
+}
+// Launches a kernel that begins with wait_for_previous(): its CTAs are set up while the
+// one before it ends (1 us each).
+template <typename... P, typename... A>
+void launch_behind(void (*kernel)(P...), int grid, int threads, cudaStream_t st, A&&... args) {
+    cudaLaunchConfig_t c{};
+    c.gridDim = dim3(unsigned(grid));
+    c.blockDim = dim3(unsigned(threads));
+    c.stream = st;
+    cudaLaunchAttribute a{};
+    a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    a.val.programmaticStreamSerializationAllowed = 1;
+    c.attrs = &a;
+    c.numAttrs = 1;
+    cudaLaunchKernelEx(&c, kernel, P(args)...);
 }
 mk_status_t launched() { return cudaGetLastError() == cudaSuccess ? MK_OK : MK_ERR_CUDA; }
 
@@ -564,8 +605,12 @@ extern "C" mk_status_t mk_fork_sequences(int32_t* block_table, int32_t* seq_lens
     int32_t* kept_len = reinterpret_cast<int32_t*>(ws);
     int32_t* kept = reinterpret_cast<int32_t*>(ws + ws_align(size_t(n) * 4));
     const Pool p{block_table, seq_lens, refs, err, rows, max_pages, num_pages, page_size};
-    mk_fork_count_kernel<<<n, 256, 0, st>>>(p, parent, child, n, kept, kept_len);
-    mk_fork_rows_kernel<<<n, 256, 0, st>>>(p, child, kept, kept_len);
+    if (n <= FORK_FEW) {
+        mk_fork_few_kernel<<<1, PLAN_THREADS, 0, st>>>(p, parent, child, n, kept, kept_len);
+    } else {
+        mk_fork_count_kernel<<<n, 256, 0, st>>>(p, parent, child, n, kept, kept_len);
+        launch_behind(mk_fork_rows_kernel, n, 256, st, p, child, kept, kept_len);
+    }
     return launched();
 }
 
@@ -610,7 +655,7 @@ extern "C" mk_status_t mk_extend_sequences(int32_t* block_table, int32_t* seq_le
         const Buffers b = some_buffers(c, i);
         const int64_t work = std::max<int64_t>(int64_t(n) * b.first[b.n], (int64_t(n) * most + COPY_THREADS - 1) / COPY_THREADS);
         const int grid = int(std::max<int64_t>(1, std::min<int64_t>(work, copy_grid(sms))));
-        if (i == 0) mk_extend_kernel<<<grid, COPY_THREADS, 0, st>>>(p, b, seqs, count, n, most, head, src, dst, slots);
+        if (i == 0) launch_behind(mk_extend_kernel, grid, COPY_THREADS, st, p, b, seqs, count, n, most, head, src, dst, slots);
         else mk_extend_more_kernel<<<grid, COPY_THREADS, 0, st>>>(p, b, head, src, dst);
     }
     return launched();
@@ -649,10 +694,10 @@ extern "C" mk_status_t mk_compact_pages(const int32_t* block_table, const int32_
     const Pool p{nullptr, const_cast<int32_t*>(seq_lens), nullptr, err, rows, max_pages, num_pages, page_size};
     const CompactOut out{block_table, refs, table_out, refs_out};
     mk_compact_count_kernel<<<parts, 256, 0, st>>>(refs, num_pages, each, counts);
-    mk_compact_plan_kernel<<<parts, 256, 0, st>>>(refs, num_pages, each, counts, head, src, dst, rank);
+    launch_behind(mk_compact_plan_kernel, parts, 256, st, refs, num_pages, each, counts, head, src, dst, rank);
     for (int i = 0; i < std::max(1, n_caches); i += MAX_CACHES) {
         const Buffers b = some_buffers(c, i);
-        if (i == 0) mk_compact_kernel<<<copy_grid(sms), COPY_THREADS, 0, st>>>(p, out, b, head, src, dst, rank);
+        if (i == 0) launch_behind(mk_compact_kernel, copy_grid(sms), COPY_THREADS, st, p, out, b, head, src, dst, rank);
         else mk_compact_more_kernel<<<copy_grid(sms), COPY_THREADS, 0, st>>>(p, b, head, src, dst);
     }
     return launched();
