@@ -457,10 +457,14 @@ __global__ void __launch_bounds__(Geo<D, R>::THREADS, 1) mk_paged_attention_kern
         const int kv = tail.g / p.chunks, head0 = kv * p.per_kv + (tail.g % p.chunks) * G::GROUP + row0;
         put_partial<G>(tails + range * G::PART, min(ROWS, (kv + 1) * p.per_kv - head0), row0, side, o, m0, m1, l0, l1);
     }
-    head.tiles = has_head ? head.tiles : 0u;
-    tail.tiles = has_tail ? tail.tiles : 0u;
-    join_ranges<D, G::GROUP, G::RANGES, G::THREADS>(p, head, tail, range, mate == 0 && lane == 0, tails, firsts, small, cut_at,
-                                                   start, end);
+    __shared__ Range pieces[2 * G::RANGES];
+    if (mate == 0 && lane == 0) {
+        head.tiles = has_head ? head.tiles : 0u;
+        tail.tiles = has_tail ? tail.tiles : 0u;
+        pieces[2 * range] = head;
+        pieces[2 * range + 1] = tail;
+    }
+    join_ranges<D, G::GROUP, G::RANGES, G::THREADS>(p, pieces, tails, firsts, small, cut_at, start, end);
 }
 
 template <int D, int R>

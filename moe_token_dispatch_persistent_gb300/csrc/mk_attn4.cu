@@ -49,7 +49,7 @@ template <int D, int NT>
 struct Geo4 {
     static constexpr int GROUP = NT * 8;
     static constexpr int KEYS = D == 256 ? 16 : 32;  // per tile
-    static constexpr int WARPS = D == 64 ? 16 : D == 128 ? (NT == 1 ? 12 : 8) : (NT == 1 ? 12 : 8);
+    static constexpr int WARPS = D == 64 ? (NT == 1 ? 16 : 12) : NT == 1 ? 12 : 8;
     static constexpr int STAGES = D == 64 ? (NT == 1 ? 4 : 3) : D == 128 ? (NT == 1 ? 2 : 3) : (NT == 1 ? 2 : 4);
     static constexpr int THREADS = WARPS * 32;
     static constexpr int ROW = D / 2;         // bytes of a row's values
@@ -61,11 +61,16 @@ struct Geo4 {
     static constexpr int PART = GROUP * (D + 8) + 2 * GROUP;  // floats of a range's result: O, m, l
     // The results of ranges' last groups lie where the rings were; those of their first
     // ones beside them, or in the workspace where there is no room.
-    static constexpr bool HEADS_SHARED = WARPS * (RING + PART * 4) <= 215000;
+    // The queries of 16 heads, laid out for the products, lie in shared memory: in registers
+    // they leave room for fewer warps (____).
+    static constexpr bool Q_SHARED = NT == 2 || D == 256;
+    static constexpr int Q_BYTES = Q_SHARED ? NT * (D / 16) * 2 * 32 * 4 : 0;  // of a warp
+    static constexpr bool HEADS_SHARED = WARPS * (RING + PART * 4 + Q_BYTES) <= 215000;
     static constexpr int SM_HEADS = WARPS * RING > WARPS * PART * 4 ? WARPS * RING : WARPS * PART * 4;
     static constexpr int SM_PREFIX = SM_HEADS + (HEADS_SHARED ? WARPS * PART * 4 : 0);
     static constexpr int SM_SMALL = SM_PREFIX + (ATTN_MAX_B + 1) * 4 + 12;
-    static constexpr int SMEM = SM_SMALL + 128;
+    static constexpr int SM_Q = (SM_SMALL + 128 + 15) / 16 * 16;
+    static constexpr int SMEM = SM_Q + WARPS * Q_BYTES;
     static_assert(HEADS_SHARED || WARPS * PART <= ATTN4_HEADS_FLOATS, "the first results fit the workspace");
     static_assert(2 * GROUP + GROUP * D <= ATTN_SLOT_FLOATS, "a partial result fits its slot");
     static_assert(SMEM + 2 * WARPS * 28 + 16 <= 232448, "shared memory of one CTA on sm_103");
@@ -241,7 +246,8 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
     const int scale_byte = (lane % SCALE_LANES) * 16, scale_unit = lane < 2 * SCALE_LANES ? scale_byte / (U * SROW) : -1;
     const uint8_t* const scales = (lane < SCALE_LANES ? p.k_scales : p.v_scales) + scale_byte % (U * SROW);
     const uint32_t lane_dst = ring + lane * 16;
-    const uint8_t *k_at = nullptr, *v_at = nullptr, *s_at = nullptr, *k_kv = nullptr, *v_kv = nullptr, *s_kv = nullptr;
+    const uint8_t *k_at = nullptr, *v_at = nullptr, *s_at = nullptr;
+    int64_t head_at = 0, head_scales = 0;
     const int32_t* table = nullptr;
     int page_left = 0, page_next = 0, pages_more = 0;
     bool page_ok = false;
@@ -278,10 +284,8 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
                     page_next = __ldg(table);
                     token = key - slot * p.page_size;
                     pages_more = slot_of(load_len - 1) - slot;
-                    const int64_t head = kv * p.head_stride + (lane & (UNIT_LANES - 1)) * 16;
-                    k_kv = p.k + head;
-                    v_kv = p.v + head;
-                    s_kv = scales + kv * p.scale_head;
+                    head_at = kv * p.head_stride + (lane & (UNIT_LANES - 1)) * 16;
+                    head_scales = kv * p.scale_head;
                     page_left = 0;
                 }
 #pragma unroll
@@ -289,10 +293,10 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
                     if (page_left == 0 && left > 0) {
                         page_ok = good_page(page_next);
                         const uint32_t page = page_ok ? uint32_t(page_next) : 0u;
-                        const uint64_t at = uint64_t(page) * p.page_units * 16 + uint32_t(token * ROW);
-                        k_at = k_kv + at;
-                        v_at = v_kv + at;
-                        s_at = s_kv + (uint64_t(page) * p.scale_units * 16 + uint32_t(token * SROW));
+                        const uint64_t at = uint64_t(page) * p.page_units * 16 + uint32_t(token * ROW) + head_at;
+                        k_at = p.k + at;
+                        v_at = p.v + at;
+                        s_at = scales + (uint64_t(page) * p.scale_units * 16 + uint32_t(token * SROW) + head_scales);
                         page_left = p.page_size - token;
                         token = 0;
                         if (--pages_more >= 0) page_next = __ldg(++table);
@@ -365,8 +369,14 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
     const int kg = key_of<D>(g), va = key_of<D>(2 * c), vb = key_of<D>(2 * c + 1);
     uint32_t at = 0;  // the tile's stage
     Walk walk{wstart, wend, prefix, p.B, groups, false};
-    Range r, head, tail;
-    bool has_head = false, has_tail = false;
+    Range r;
+    // A group that the range does not hold whole is its first (its result is set aside) or
+    // its last (kept in registers until the rings are free).
+    __shared__ Range pieces[2 * G::WARPS];
+    Range* const mine = pieces + 2 * warp;
+    if (lane < 2) mine[lane].tiles = 0;
+    __syncwarp();
+    bool has_tail = false;
     // Output columns g * D/8 + 2t and + 2t + 1 of heads 8n + 2c and 8n + 2c + 1.
     float o[NT][D / 16][4];
     float m[NT][2], most[NT][2];  // reference of the weights, and what no score may pass
@@ -393,6 +403,7 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
             }
     };
 
+    uint2* const q_shared = reinterpret_cast<uint2*>(smem + G::SM_Q + (G::Q_SHARED ? warp * G::Q_BYTES : 0)) + lane;
     while (walk.next(r)) {
         const int kv = r.g / p.chunks, head0 = kv * p.per_kv + (r.g % p.chunks) * GROUP;
         const int heads = min(GROUP, (kv + 1) * p.per_kv - head0);
@@ -401,7 +412,7 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
         // of head 8n + g.  A power of two takes a head's largest to 2^14 .. 2^15, and a
         // negative scale's sign goes with it, so that the largest product is the largest
         // score.
-        uint32_t qb[NT][D / 16][2];
+        uint32_t qb[G::Q_SHARED ? 1 : NT][D / 16][2];
         float f[NT][2];  // from products to scores in units of log 2; not negative
         const float unit = p.scale2 * (p.k_factor ? __ldg(p.k_factor + kv) : 1.f);
 #pragma unroll
@@ -430,8 +441,11 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const uint32_t u = (&raw[i].x)[j];
-                    qb[n][2 * i + j / 2][j % 2] = pack_h2(__uint_as_float(u << 16) * by, __uint_as_float(u & 0xffff0000u) * by);
+                    qb[G::Q_SHARED ? 0 : n][2 * i + j / 2][j % 2] = pack_h2(__uint_as_float(u << 16) * by, __uint_as_float(u & 0xffff0000u) * by);
                 }
+            if constexpr (G::Q_SHARED)
+#pragma unroll
+                for (int x = 0; x < D / 16; ++x) q_shared[(n * (D / 16) + x) * 32] = make_uint2(qb[0][x][0], qb[0][x][1]);
             f[n][0] = fabsf(unit) * __shfl_sync(0xffffffffu, back, 8 * c);
             f[n][1] = fabsf(unit) * __shfl_sync(0xffffffffu, back, 8 * c + 4);
 #pragma unroll
@@ -451,21 +465,20 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
 
             // ---- scores: 16 keys by 8 heads
             float s[MT][NT][4];
-#pragma unroll
-            for (int mt = 0; mt < MT; ++mt) {
-                uint32_t w[2][D / 32], sc[2][D / 64];
+            uint32_t w[MT][2][D / 32], sc[MT][2][D / 64];
+            auto load_keys = [&](int mt) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const uint8_t* row = ks + ((mt * 16 + h * 8 + kg) * ROW + c * (D / 8));
                     const uint8_t* srow = kss + ((mt * 16 + h * 8 + kg) * SROW + c * (D / 64));
                     if constexpr (D == 64) {
-                        load_words<2>(row, w[h]);
-                        sc[h][0] = low_twice(halves_of_e4m3x2(*srow));
+                        load_words<2>(row, w[mt][h]);
+                        sc[mt][h][0] = low_twice(halves_of_e4m3x2(*srow));
                     } else if constexpr (D == 128) {
-                        load_words<4>(row, w[h]);
+                        load_words<4>(row, w[mt][h]);
                         const uint32_t two = halves_of_e4m3x2(load_u16(srow));
-                        sc[h][0] = low_twice(two);
-                        sc[h][1] = high_twice(two);
+                        sc[mt][h][0] = low_twice(two);
+                        sc[mt][h][1] = high_twice(two);
                     } else {
                         uint32_t a[4], b[4], four[1];
                         load_words<4>(row, a);
@@ -473,33 +486,63 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
                         load_words<1>(srow, four);
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
-                            w[h][i] = a[i];
-                            w[h][4 + i] = b[i];
+                            w[mt][h][i] = a[i];
+                            w[mt][h][4 + i] = b[i];
                         }
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const uint32_t two = halves_of_e4m3x2(four[0] >> (16 * i));
-                            sc[h][2 * i] = low_twice(two);
-                            sc[h][2 * i + 1] = high_twice(two);
+                            sc[mt][h][2 * i] = low_twice(two);
+                            sc[mt][h][2 * i + 1] = high_twice(two);
                         }
                     }
                 }
+            };
+            // two products' columns of 16 keys
+            auto unpack_keys = [&](int mt, int i, uint32_t (&a)[2][4]) {
+                halves_of_e2m1x8(w[mt][0][i], a[0][0], a[0][2], a[1][0], a[1][2]);
+                halves_of_e2m1x8(w[mt][1][i], a[0][1], a[0][3], a[1][1], a[1][3]);
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    a[x][0] = mul_h2(a[x][0], sc[mt][0][i / 2]);
+                    a[x][2] = mul_h2(a[x][2], sc[mt][0][i / 2]);
+                    a[x][1] = mul_h2(a[x][1], sc[mt][1][i / 2]);
+                    a[x][3] = mul_h2(a[x][3], sc[mt][1][i / 2]);
+                }
+            };
+            auto score = [&](int mt, int n, bool first, const uint32_t (&a)[4], uint32_t q0, uint32_t q1) {
+                if (first) mma_f16_first(s[mt][n], a, q0, q1);
+                else mma_f16(s[mt][n], a, q0, q1);
+            };
+            if constexpr (G::Q_SHARED) {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) load_keys(mt);
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) {
-                    uint32_t a[2][4];
-                    halves_of_e2m1x8(w[0][i], a[0][0], a[0][2], a[1][0], a[1][2]);
-                    halves_of_e2m1x8(w[1][i], a[0][1], a[0][3], a[1][1], a[1][3]);
+                    uint32_t a[MT][2][4];
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        a[x][0] = mul_h2(a[x][0], sc[0][i / 2]);
-                        a[x][2] = mul_h2(a[x][2], sc[0][i / 2]);
-                        a[x][1] = mul_h2(a[x][1], sc[1][i / 2]);
-                        a[x][3] = mul_h2(a[x][3], sc[1][i / 2]);
+                    for (int mt = 0; mt < MT; ++mt) unpack_keys(mt, i, a[mt]);
+#pragma unroll
+                    for (int x = 0; x < 2; ++x)
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
-                            if (i == 0 && x == 0) mma_f16_first(s[mt][n], a[x], qb[n][0][0], qb[n][0][1]);
-                            else mma_f16(s[mt][n], a[x], qb[n][2 * i + x][0], qb[n][2 * i + x][1]);
+                            const uint2 q = q_shared[(n * (D / 16) + 2 * i + x) * 32];
+#pragma unroll
+                            for (int mt = 0; mt < MT; ++mt) score(mt, n, i == 0 && x == 0, a[mt][x], q.x, q.y);
                         }
+                }
+            } else {
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt) {
+                    load_keys(mt);
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        uint32_t a[2][4];
+                        unpack_keys(mt, i, a);
+#pragma unroll
+                        for (int x = 0; x < 2; ++x)
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) score(mt, n, i == 0 && x == 0, a[x], qb[n][2 * i + x][0], qb[n][2 * i + x][1]);
                     }
                 }
             }
@@ -653,11 +696,10 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
                         p.lse[row_at] = sum == 0.f ? -INFINITY : (m[n][i] - WEIGHT_SHIFT + log2f(sum)) * LN2;
                 }
         } else if (walk.pos < walk.end) {
-            head = r;
-            has_head = true;
+            if (lane == 0) mine[0] = r;
             put(first_results + warp * G::PART, heads);
         } else {
-            tail = r;
+            if (lane == 0) mine[1] = r;
             has_tail = true;
         }
     }
@@ -666,12 +708,10 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
     float* tails = reinterpret_cast<float*>(smem);
     __syncthreads();  // the rings are free
     if (has_tail) {
-        const int kv = tail.g / p.chunks, head0 = kv * p.per_kv + (tail.g % p.chunks) * GROUP;
+        const int kv = r.g / p.chunks, head0 = kv * p.per_kv + (r.g % p.chunks) * GROUP;
         put(tails + warp * G::PART, min(GROUP, (kv + 1) * p.per_kv - head0));
     }
-    head.tiles = has_head ? head.tiles : 0u;
-    tail.tiles = has_tail ? tail.tiles : 0u;
-    join_ranges<D, GROUP, G::WARPS, G::THREADS>(p, head, tail, warp, lane == 0, tails, first_results, small, cut_at, start, end);
+    join_ranges<D, GROUP, G::WARPS, G::THREADS>(p, pieces, tails, first_results, small, cut_at, start, end);
 }
 
 template <int D, int NT, int UNIT>

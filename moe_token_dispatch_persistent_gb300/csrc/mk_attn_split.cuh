@@ -269,24 +269,18 @@ __device__ void join_group(const P& p, const Range& r, uint32_t c0, int n, uint3
 
 // What the CTA's ranges have of groups that none of them holds whole: joined in
 // shared memory, and where other CTAs hold parts of them too, by the CTA that is
-// done last, in the order of the keys.  `head` and `tail`: this range's first
-// and last group (tiles 0: none), published by one thread of the range;
-// `firsts` and `tails` hold the ranges' results, each GROUP rows of D + 8
-// floats, GROUP maxima and GROUP sums.  Called after every warp has written
-// its results; the groups that `cut_at`'s CTAs share arrive at p.arrived.
+// done last, in the order of the keys.  pieces[2 i] and [2 i + 1] are range i's first
+// and last group (tiles 0: none), in shared memory; `firsts` and `tails` hold the
+// ranges' results, each GROUP rows of D + 8 floats, GROUP maxima and GROUP sums.
+// Called after every warp has written its results; the groups that `cut_at`'s CTAs
+// share arrive at p.arrived.
 template <int D, int GROUP, int RANGES, int THREADS, typename P>
-__device__ __forceinline__ void join_ranges(const P& p, const Range& head, const Range& tail, int range, bool publishes,
-                                            float* tails, const float* firsts, uint32_t* small, const Cut& cut_at,
-                                            uint32_t start, uint32_t end) {
+__device__ __forceinline__ void join_ranges(const P& p, const Range* pieces, float* tails, const float* firsts, uint32_t* small,
+                                            const Cut& cut_at, uint32_t start, uint32_t end) {
     constexpr int OSTRIDE = D + 8, PART = GROUP * OSTRIDE + 2 * GROUP;
     static_assert(RANGES <= 16, "a bit for each piece");
-    __shared__ Range pieces[2 * RANGES];  // in the order of positions; tiles 0: none
     const int tid = threadIdx.x;
     const uint32_t groups = uint32_t(p.groups);
-    if (publishes) {
-        pieces[2 * range] = head;
-        pieces[2 * range + 1] = tail;
-    }
     __syncthreads();
     // Every warp sorts the pieces out for itself: those of a group follow one another.
     const int lane = tid & 31;
