@@ -49,7 +49,7 @@ template <int D, int NT>
 struct Geo4 {
     static constexpr int GROUP = NT * 8;
     static constexpr int KEYS = D == 256 ? 16 : 32;  // per tile
-    static constexpr int WARPS = D == 64 ? (NT == 1 ? 16 : 12) : NT == 1 ? 12 : 8;
+    static constexpr int WARPS = D == 64 ? (NT == 1 ? 16 : NT == 2 ? 12 : 8) : NT == 1 ? 12 : 8;
     static constexpr int STAGES = D == 64 ? (NT == 1 ? 4 : 3) : D == 128 ? (NT == 1 ? 2 : 3) : (NT == 1 ? 2 : 4);
     static constexpr int THREADS = WARPS * 32;
     static constexpr int ROW = D / 2;         // bytes of a row's values
@@ -63,7 +63,7 @@ struct Geo4 {
     // ones beside them, or in the workspace where there is no room.
     // The queries of 16 heads, laid out for the products, lie in shared memory: in registers
     // they leave room for fewer warps (____).
-    static constexpr bool Q_SHARED = NT == 2 || D == 256;
+    static constexpr bool Q_SHARED = NT > 1 || D == 256;
     static constexpr int Q_BYTES = Q_SHARED ? NT * (D / 16) * 2 * 32 * 4 : 0;  // of a warp
     static constexpr bool HEADS_SHARED = WARPS * (RING + PART * 4 + Q_BYTES) <= 215000;
     static constexpr int SM_HEADS = WARPS * RING > WARPS * PART * 4 ? WARPS * RING : WARPS * PART * 4;
@@ -222,11 +222,10 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
             load_len = length_of(p, lr.b);
             load_tile = lr.t0;
             // the group's queries head for L1 while its first tiles do for shared memory
-            const int kv = lr.g / p.chunks, head = kv * p.per_kv + (lr.g % p.chunks) * GROUP + (lane & (GROUP - 1));
-            if (head < (kv + 1) * p.per_kv && lane < GROUP * (D / 64)) {
-                const __nv_bfloat16* q = p.q + int64_t(lr.b) * p.q_stride + int64_t(head) * D + lane / GROUP * 64;
-                asm volatile("prefetch.global.L1 [%0];" ::"l"(q));
-            }
+            const int kv = lr.g / p.chunks, head0 = kv * p.per_kv + (lr.g % p.chunks) * GROUP;
+            const int heads = min(GROUP, (kv + 1) * p.per_kv - head0);
+            const char* q = reinterpret_cast<const char*>(p.q + int64_t(lr.b) * p.q_stride + int64_t(head0) * D);
+            for (int i = lane; i < heads * (D / 64); i += 32) asm volatile("prefetch.global.L1 [%0];" ::"l"(q + i * 128));
         }
         return true;
     };
@@ -729,9 +728,15 @@ cudaError_t launch_attn4(Attn4Params& p, bool rows, int grid, cudaStream_t st) {
     if (rows && p.page_size % 8 == 0) return launch_attn4<D, NT, 8>(p, grid, st);
     return launch_attn4<D, NT, 0>(p, grid, st);
 }
+// Groups of 8 heads, of 16, or, where that takes fewer passes over the keys and the
+// registers are there, of 24 (32 sequences of 4096 keys, 8 key-value heads of 24: 70 us, by
+// groups of 16 87; 222 short sequences with one of 24: 21 and 19).
 template <int D>
 cudaError_t launch_attn4(Attn4Params& p, bool rows, int grid, cudaStream_t st) {
-    return p.per_kv <= 8 ? launch_attn4<D, 1>(p, rows, grid, st) : launch_attn4<D, 2>(p, rows, grid, st);
+    if (p.per_kv <= 8) return launch_attn4<D, 1>(p, rows, grid, st);
+    if constexpr (D < 256)
+        if ((p.per_kv + 23) / 24 < (p.per_kv + 15) / 16) return launch_attn4<D, 3>(p, rows, grid, st);
+    return launch_attn4<D, 2>(p, rows, grid, st);
 }
 
 // Groups of up to 8 query heads per sequence (the smallest), 0 for sizes outside the limits.
@@ -755,7 +760,7 @@ cudaError_t attn4_smem() {
 }  // namespace
 
 cudaError_t attn4_kernel_attributes() {
-    for (const cudaError_t e : {attn4_smem<64, 1>(), attn4_smem<64, 2>(), attn4_smem<128, 1>(), attn4_smem<128, 2>(),
+    for (const cudaError_t e : {attn4_smem<64, 1>(), attn4_smem<64, 2>(), attn4_smem<64, 3>(), attn4_smem<128, 1>(), attn4_smem<128, 2>(), attn4_smem<128, 3>(),
                                 attn4_smem<256, 1>(), attn4_smem<256, 2>()})
         if (e != cudaSuccess) return e;
     return cudaSuccess;
