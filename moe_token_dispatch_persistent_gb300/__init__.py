@@ -869,10 +869,12 @@ def qk_norm_rope(q, k, positions, inv_freq, q_weight=None, k_weight=None, eps=1e
             raise ValueError("k_weight must be bf16 [D] on q's device")
         p_kw = k_weight.data_ptr()
     if pair_axis is not None:
-        if len(pair_axis) != half or any(not 0 <= a < axes for a in pair_axis):
+        each = bytes(pair_axis) if not isinstance(pair_axis, int) else b""  # (ValueError for a number outside a byte)
+        if len(each) != half or (half and max(each) >= axes):
             raise ValueError("pair_axis must name a row of positions for each of inv_freq")
-        each = (ctypes.c_uint8 * max(half, 1))(*pair_axis)
-        p_axis = ctypes.addressof(each)
+        if half:
+            each = (ctypes.c_uint8 * half).from_buffer_copy(each)
+            p_axis = ctypes.addressof(each)
     elif axes > 1:
         raise ValueError("positions of several axes need pair_axis")
     cache, page_size, pages, v_stride, v_head = MK_CACHE_NONE, 0, 0, 0, 0

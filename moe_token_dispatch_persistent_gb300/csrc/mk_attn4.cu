@@ -61,8 +61,10 @@ struct Geo4 {
     static constexpr int PART = GROUP * (D + 8) + 2 * GROUP;  // floats of a range's result: O, m, l
     // The results of ranges' last groups lie where the rings were; those of their first
     // ones beside them, or in the workspace where there is no room.
-    // The queries of 16 heads, laid out for the products, lie in shared memory: in registers
-    // they leave room for fewer warps (____).
+    // The queries of 16 heads or of 256 columns, laid out for the products, lie in shared
+    // memory: in registers they cost spills, which find little L1 beside the rings (13
+    // sequences of 47828 keys, 4 heads of 256: 142 us, so 136; 32 of 4096, 8 x 16 heads of
+    // 128: 55, so 53).
     static constexpr bool Q_SHARED = NT > 1 || D == 256;
     static constexpr int Q_BYTES = Q_SHARED ? NT * (D / 16) * 2 * 32 * 4 : 0;  // of a warp
     static constexpr bool HEADS_SHARED = WARPS * (RING + PART * 4 + Q_BYTES) <= 215000;

@@ -256,7 +256,9 @@ __global__ void __launch_bounds__(PLAN_THREADS) mk_extend_plan_kernel(Pool p, co
     __shared__ int first[MAX_LIST];   // its place among the fresh pages
     __shared__ int part[32];
     __shared__ int bad;
+    __shared__ unsigned long long wanted;  // pages, at most
     const int tid = threadIdx.x;
+    if (tid == 0) wanted = 0;
     bool good = list_is_good(p, seqs, n, seen, &bad);
     if (good) {
         for (int i = tid; i < n; i += PLAN_THREADS) {
@@ -272,9 +274,11 @@ __global__ void __launch_bounds__(PLAN_THREADS) mk_extend_plan_kernel(Pool p, co
                 if (!p.holds(page)) atomicMin(&bad, i);
             }
             last[i] = page;
+            // (of all sequences they may pass 32 bits, and below they are counted in those)
+            atomicAdd(&wanted, static_cast<unsigned long long>(p.pages_of(len + more) - p.pages_of(len)));
         }
         __syncthreads();
-        good = bad == INT_MAX;
+        good = bad == INT_MAX && wanted <= static_cast<unsigned long long>(p.num_pages);
         if (!good && tid == 0) cache_error(p.err, ERR_FAULT, SITE_POOL_FULL, uint32_t(bad));
     }
     if (!good) {

@@ -133,6 +133,14 @@ def test_page_sizes(page):
     c.check(c.run())
 
 
+@pytest.mark.parametrize("D", [64, 256])
+@pytest.mark.parametrize("page,layout", [(1, "heads"), (3, "heads"), (8, "heads"), (8, "tokens"), (24, "heads"), (32, "heads"),
+                                         (48, "heads"), (96, "tokens")])
+def test_page_sizes_of_other_heads(D, page, layout):
+    c = Case([5, page, page + 1, 3 * page - 1, 700, 0, 2 * page], 20, 2, D, page, seed=page, layout=layout)
+    c.check(c.run())
+
+
 @pytest.mark.parametrize("lens", [[1], [16], [127], [128], [129], [5000], [0], [0, 0, 0], [5999, 1], [1, 5999],
                                   [33] * 300], ids=str)
 @pytest.mark.parametrize("Hkv", [1, 4])

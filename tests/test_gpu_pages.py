@@ -221,6 +221,17 @@ def test_refused_lists_change_nothing():
     assert p.refs.min() == 1
 
 
+def test_more_pages_than_32_bits_count_are_refused():
+    # rows of 2^31 - 1 pages of one token each; their table is never looked at
+    state = (i32([[0]]), i32([0] * 3), i32([0] * 8))
+    before = [t.clone() for t in state]
+    slots = torch.zeros((3, 1), dtype=torch.int64, device="cuda")
+    counts = i32([2 ** 31 - 2] * 3)
+    assert mk.mk_extend_sequences(*state, 3, 2 ** 31 - 1, 8, 1, i32([0, 1, 2]), counts, 3, 2 ** 31 - 2, None, []) == mk.MK_OK
+    assert mk.mk_get_status() == mk.MK_ERR_DEVICE_FAULT
+    assert all(torch.equal(a, b) for a, b in zip(state, before)) and slots.sum() == 0
+
+
 def test_entries_that_are_no_pages_are_reported():
     p = Pool(3, 4, 10, 2)
     p.extend([0, 1], [6, 3])
