@@ -274,8 +274,9 @@ __global__ void __launch_bounds__(PLAN_THREADS) mk_extend_plan_kernel(Pool p, co
                 if (!p.holds(page)) atomicMin(&bad, i);
             }
             last[i] = page;
-            // (of all sequences they may pass 32 bits, and below they are counted in those)
-            atomicAdd(&wanted, static_cast<unsigned long long>(p.pages_of(len + more) - p.pages_of(len)));
+            // of all sequences they may pass 32 bits, in which they are counted below
+            if (int64_t(n) * p.max_pages > INT_MAX)
+                atomicAdd(&wanted, static_cast<unsigned long long>(p.pages_of(len + more) - p.pages_of(len)));
         }
         __syncthreads();
         good = bad == INT_MAX && wanted <= static_cast<unsigned long long>(p.num_pages);
