@@ -1061,13 +1061,16 @@ def _page_buffers(caches, dev, pages=None):
                 raise ValueError("a cache's first dimension is its pages")
             if pages is None:
                 pages = shape[0]
-            dense = 1
-            for s, n in sorted(zip(stride[1:], shape[1:])):
-                if n > 1 and s != dense:
-                    raise ValueError("the values of a page must lie one after the other")
-                dense *= n
             if shape[0] != pages:
                 raise ValueError("the caches must have the same number of pages")
+            if pages and t.is_contiguous():
+                dense = t.numel() // pages
+            else:
+                dense = 1
+                for s, n in sorted(zip(stride[1:], shape[1:])):
+                    if n > 1 and s != dense:
+                        raise ValueError("the values of a page must lie one after the other")
+                    dense *= n
             size = t.element_size()
             block, step = dense * size, stride[0] * size
         base.append(t.data_ptr())

@@ -21,8 +21,13 @@
 // 2^-24 of the largest keep all of them.
 //
 // Work is cut and joined as in mk_attn_split.cuh.  A tile is KEYS keys of one
-// (sequence, group of up to 8 or 16 query heads of one key-value head); each warp
+// (sequence, group of up to 8, 16 or 24 query heads of one key-value head); each warp
 // has a ring of tiles in shared memory, filled by its own asynchronous copies.
+//
+// Measured on GB300: four sequences of 131071 keys, 8 key-value heads of 128: 108 us,
+// 5.6 TB/s (535 instructions a tile of 32 keys, 2.5 a cycle and SM); 64 sequences of 0
+// to 16384 keys in pages of 24 (128 MB) 42 us, of which 4 until the first copies and 7
+// for the joins; one of 8191 keys 11.8 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -45,12 +50,13 @@ constexpr int ATTN4_HEADS_FLOATS = 34 * 1024;
 constexpr size_t ATTN4_HEADS_BYTES = size_t(ATTN_MAX_CTAS) * ATTN4_HEADS_FLOATS * 4;
 
 // D columns a head, groups of NT * 8 query heads.
-template <int D, int NT>
+template <int D, int NT, int UNIT>
 struct Geo4 {
     static constexpr int GROUP = NT * 8;
-    static constexpr int KEYS = D == 256 ? 16 : 32;  // per tile
+    // Per tile.  (16 sequences of 50000 keys, 12 heads of 64: 130 us with 64, 150 with 32.)
+    static constexpr int KEYS = D == 256 ? 16 : D == 64 && NT == 1 && UNIT > 0 ? 64 : 32;
     static constexpr int WARPS = D == 64 ? (NT == 1 ? 16 : NT == 2 ? 12 : 8) : NT == 1 ? 12 : 8;
-    static constexpr int STAGES = D == 64 ? (NT == 1 ? 4 : 3) : D == 128 ? (NT == 1 ? 2 : 3) : (NT == 1 ? 2 : 4);
+    static constexpr int STAGES = KEYS == 64 ? 2 : D == 64 ? (NT == 1 ? 4 : 3) : D == 128 ? (NT == 1 ? 2 : 3) : (NT == 1 ? 2 : 4);
     static constexpr int THREADS = WARPS * 32;
     static constexpr int ROW = D / 2;         // bytes of a row's values
     static constexpr int SROW = D / 16;       // bytes of its scales
@@ -186,8 +192,8 @@ __device__ __forceinline__ int key_of(int r) {
 // UNIT: that many keys of a tile lie in one page, a head's rows one after the other,
 // so their copies have one base.  0: every row is looked up by itself.
 template <int D, int NT, int UNIT>
-__global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp4_kernel(const Attn4Params p) {
-    using G = Geo4<D, NT>;
+__global__ void __launch_bounds__(Geo4<D, NT, UNIT>::THREADS, 1) mk_paged_attention_fp4_kernel(const Attn4Params p) {
+    using G = Geo4<D, NT, UNIT>;
     constexpr int KEYS = G::KEYS, GROUP = G::GROUP, MT = KEYS / 16, ROW = G::ROW, SROW = G::SROW;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -717,7 +723,7 @@ __global__ void __launch_bounds__(Geo4<D, NT>::THREADS, 1) mk_paged_attention_fp
 
 template <int D, int NT, int UNIT>
 cudaError_t launch_attn4(Attn4Params& p, int grid, cudaStream_t st) {
-    using G = Geo4<D, NT>;
+    using G = Geo4<D, NT, UNIT>;
     p.chunks = (p.per_kv + G::GROUP - 1) / G::GROUP;
     p.groups = p.chunks * p.Hkv;
     mk_paged_attention_fp4_kernel<D, NT, UNIT><<<grid, G::THREADS, G::SMEM, st>>>(p);
@@ -725,7 +731,7 @@ cudaError_t launch_attn4(Attn4Params& p, int grid, cudaStream_t st) {
 }
 template <int D, int NT>
 cudaError_t launch_attn4(Attn4Params& p, bool rows, int grid, cudaStream_t st) {
-    if (rows && Geo4<D, NT>::KEYS == 32 && p.page_size % 32 == 0) return launch_attn4<D, NT, Geo4<D, NT>::KEYS>(p, grid, st);
+    if (rows && p.page_size % Geo4<D, NT, 16>::KEYS == 0) return launch_attn4<D, NT, Geo4<D, NT, 16>::KEYS>(p, grid, st);
     if (rows && p.page_size % 16 == 0) return launch_attn4<D, NT, 16>(p, grid, st);
     if (rows && p.page_size % 8 == 0) return launch_attn4<D, NT, 8>(p, grid, st);
     return launch_attn4<D, NT, 0>(p, grid, st);
@@ -750,11 +756,11 @@ int64_t attn4_groups(int B, int Hq, int Hkv) {
 template <int D, int NT, int UNIT>
 cudaError_t attn4_smem() {
     return cudaFuncSetAttribute(mk_paged_attention_fp4_kernel<D, NT, UNIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                Geo4<D, NT>::SMEM);
+                                Geo4<D, NT, UNIT>::SMEM);
 }
 template <int D, int NT>
 cudaError_t attn4_smem() {
-    for (const cudaError_t e : {attn4_smem<D, NT, Geo4<D, NT>::KEYS>(), attn4_smem<D, NT, 16>(), attn4_smem<D, NT, 8>(), attn4_smem<D, NT, 0>()})
+    for (const cudaError_t e : {attn4_smem<D, NT, Geo4<D, NT, 16>::KEYS>(), attn4_smem<D, NT, 16>(), attn4_smem<D, NT, 8>(), attn4_smem<D, NT, 0>()})
         if (e != cudaSuccess) return e;
     return cudaSuccess;
 }
@@ -794,7 +800,7 @@ extern "C" mk_status_t mk_paged_attention_fp4(const void* q, int64_t q_stride, c
     const int64_t cap = int64_t(max_pages) * page_size;
     if (B > ATTN_MAX_B || cap > (int64_t(1) << 31) - 32) return MK_ERR_UNSUPPORTED;
     // positions in the order of tiles are 32-bit
-    const int64_t tiles = int64_t(B) * positions_of(int(cap), Geo4<256, 1>::KEYS);
+    const int64_t tiles = int64_t(B) * positions_of(int(cap), Geo4<256, 1, 0>::KEYS);
     if (tiles >= int64_t(1) << 31 || tiles * groups >= int64_t(1) << 31) return MK_ERR_UNSUPPORTED;
     if (B > 0) {
         if (!q || !seq_lens || !out) return MK_ERR_INVALID_ARG;

@@ -228,6 +228,15 @@ def test_workspace_and_empty_batch():
     assert o["out"].shape == (0, 4, 64) and o["lse"].shape == (0, 4)
 
 
+def test_tables_and_pools_without_pages():
+    q = torch.randn((3, 8, 64), device="cuda").bfloat16()
+    lens = torch.zeros(3, dtype=torch.int32, device="cuda")
+    for pages in (0, 4):
+        z = mk.fp4_cache(pages, 16, 2, 64)
+        o = mk.paged_attention_fp4(q, block_table=torch.zeros((3, 0), dtype=torch.int32, device="cuda"), seq_lens=lens, **z)
+        assert torch.all(o["out"] == 0) and torch.all(o["lse"] == -float("inf"))
+
+
 def test_offsets_past_32_bits():
     # a pool of more than 2^32 bytes, with the sequence in its last pages
     page, Hkv, D = 64, 8, 128

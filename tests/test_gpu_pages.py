@@ -232,6 +232,23 @@ def test_more_pages_than_32_bits_count_are_refused():
     assert all(torch.equal(a, b) for a, b in zip(state, before)) and slots.sum() == 0
 
 
+def test_empty_pools_tables_and_lists():
+    none = i32([])
+    p = Pool(2, 0, 0, 4)
+    p.caches = []
+    p.extend([0], [0])
+    p.fork([0], [1])
+    p.free([0, 1])
+    o = mk.compact_pages(*p.state(), [], 4)
+    assert o["block_table"].shape == (2, 0) and o["refs"].shape == (0,)
+    q = Pool(2, 3, 0, 4)
+    assert mk.compact_pages(*q.state(), [], 4)["block_table"].tolist() == q.table.tolist()
+    for pool in (p, q):
+        mk.fork_sequences(*pool.state(), none, none, 4)
+        mk.free_sequences(*pool.state(), none, 4)
+        assert mk.extend_sequences(*pool.state(), none, none, 3, [], 4).shape == (0, 3)
+
+
 def test_entries_that_are_no_pages_are_reported():
     p = Pool(3, 4, 10, 2)
     p.extend([0, 1], [6, 3])
