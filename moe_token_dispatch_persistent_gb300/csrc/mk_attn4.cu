@@ -109,6 +109,7 @@ struct Attn4Params {
     int page_shift;                    // log2 of page_size, or -1:
     uint32_t page_magic, page_more;    // key / page_size is the high word of key * page_magic, shifted
     float scale2;                      // scale * log2(e)
+    uint32_t sixteen, byte;            // 16 and 256
 
     __device__ float value_factor(int kv) const { return v_factor ? __ldg(v_factor + kv) : 1.f; }
 };
@@ -149,8 +150,21 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t a) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
     return r;
 }
-__device__ __forceinline__ uint32_t low_twice(uint32_t h2) { return __byte_perm(h2, 0, 0x1010); }
-__device__ __forceinline__ uint32_t high_twice(uint32_t h2) { return __byte_perm(h2, 0, 0x3232); }
+// One half in both.  LEAN: without an instruction where the multiply can take it so.
+template <bool LEAN>
+__device__ __forceinline__ uint32_t low_twice(uint32_t h2) {
+    if constexpr (!LEAN) return __byte_perm(h2, 0, 0x1010);
+    uint32_t r;
+    asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {l, l};\n\t}" : "=r"(r) : "r"(h2));
+    return r;
+}
+template <bool LEAN>
+__device__ __forceinline__ uint32_t high_twice(uint32_t h2) {
+    if constexpr (!LEAN) return __byte_perm(h2, 0, 0x3232);
+    uint32_t r;
+    asm("{\n\t.reg .f16 l, h;\n\tmov.b32 {l, h}, %1;\n\tmov.b32 %0, {h, h};\n\t}" : "=r"(r) : "r"(h2));
+    return r;
+}
 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -194,6 +208,13 @@ __device__ __forceinline__ int key_of(int r) {
 template <int D, int NT, int UNIT>
 __global__ void __launch_bounds__(Geo4<D, NT, UNIT>::THREADS, 1) mk_paged_attention_fp4_kernel(const Attn4Params p) {
     using G = Geo4<D, NT, UNIT>;
+    // Shifts and pairs of bytes as multiply-adds, by factors that the compiler does not
+    // know: with 8 heads the ALU has most of the work, and the pipe of the multiplies has
+    // room (108 us, so 105.7, for 4 x 131071 keys; 150 to 130, so 126, with heads of 64;
+    // with 16 heads 155, so 161).
+    constexpr bool LEAN = NT == 1;
+    const auto shift4 = [&](uint32_t w) { return LEAN ? w * p.sixteen : w << 4; };
+    const auto two_bytes = [&](uint32_t lo, uint32_t hi) { return LEAN ? hi * p.byte + lo : __byte_perm(lo, hi, 0x0040); };
     constexpr int KEYS = G::KEYS, GROUP = G::GROUP, MT = KEYS / 16, ROW = G::ROW, SROW = G::SROW;
     extern __shared__ __align__(128) uint8_t smem[];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -480,12 +501,12 @@ __global__ void __launch_bounds__(Geo4<D, NT, UNIT>::THREADS, 1) mk_paged_attent
                     const uint8_t* srow = kss + ((mt * 16 + h * 8 + kg) * SROW + c * (D / 64));
                     if constexpr (D == 64) {
                         load_words<2>(row, w[mt][h]);
-                        sc[mt][h][0] = low_twice(halves_of_e4m3x2(*srow));
+                        sc[mt][h][0] = low_twice<LEAN>(halves_of_e4m3x2(*srow));
                     } else if constexpr (D == 128) {
                         load_words<4>(row, w[mt][h]);
                         const uint32_t two = halves_of_e4m3x2(load_u16(srow));
-                        sc[mt][h][0] = low_twice(two);
-                        sc[mt][h][1] = high_twice(two);
+                        sc[mt][h][0] = low_twice<LEAN>(two);
+                        sc[mt][h][1] = high_twice<LEAN>(two);
                     } else {
                         uint32_t a[4], b[4], four[1];
                         load_words<4>(row, a);
@@ -499,8 +520,8 @@ __global__ void __launch_bounds__(Geo4<D, NT, UNIT>::THREADS, 1) mk_paged_attent
 #pragma unroll
                         for (int i = 0; i < 2; ++i) {
                             const uint32_t two = halves_of_e4m3x2(four[0] >> (16 * i));
-                            sc[mt][h][2 * i] = low_twice(two);
-                            sc[mt][h][2 * i + 1] = high_twice(two);
+                            sc[mt][h][2 * i] = low_twice<LEAN>(two);
+                            sc[mt][h][2 * i + 1] = high_twice<LEAN>(two);
                         }
                     }
                 }
@@ -644,8 +665,8 @@ __global__ void __launch_bounds__(Geo4<D, NT, UNIT>::THREADS, 1) mk_paged_attent
                 }
                 // scales of the pairs of keys, for the first and the second 16 of the columns
                 uint32_t s01[2], s23[2];
-                s01[0] = halves_of_e4m3x2(__byte_perm(sb[0], sb[1], 0x0040));
-                s23[0] = halves_of_e4m3x2(__byte_perm(sb[2], sb[3], 0x0040));
+                s01[0] = halves_of_e4m3x2(D == 256 ? __byte_perm(sb[0], sb[1], 0x0040) : two_bytes(sb[0], sb[1]));
+                s23[0] = halves_of_e4m3x2(D == 256 ? __byte_perm(sb[2], sb[3], 0x0040) : two_bytes(sb[2], sb[3]));
                 if constexpr (D == 256) {
                     s01[1] = halves_of_e4m3x2(__byte_perm(sb[0], sb[1], 0x0051));
                     s23[1] = halves_of_e4m3x2(__byte_perm(sb[2], sb[3], 0x0051));
@@ -655,9 +676,9 @@ __global__ void __launch_bounds__(Geo4<D, NT, UNIT>::THREADS, 1) mk_paged_attent
                     constexpr uint32_t LOW = 0x0f0f0f0fu;
                     uint32_t a[4][4];
                     // bytes of one column of two keys
-                    halves_of_e2m1x8((w[0][i] & LOW) | ((w[1][i] << 4) & ~LOW), a[0][0], a[1][0], a[2][0], a[3][0]);
+                    halves_of_e2m1x8((w[0][i] & LOW) | (shift4(w[1][i]) & ~LOW), a[0][0], a[1][0], a[2][0], a[3][0]);
                     halves_of_e2m1x8(((w[0][i] >> 4) & LOW) | (w[1][i] & ~LOW), a[0][1], a[1][1], a[2][1], a[3][1]);
-                    halves_of_e2m1x8((w[2][i] & LOW) | ((w[3][i] << 4) & ~LOW), a[0][2], a[1][2], a[2][2], a[3][2]);
+                    halves_of_e2m1x8((w[2][i] & LOW) | (shift4(w[3][i]) & ~LOW), a[0][2], a[1][2], a[2][2], a[3][2]);
                     halves_of_e2m1x8(((w[2][i] >> 4) & LOW) | (w[3][i] & ~LOW), a[0][3], a[1][3], a[2][3], a[3][3]);
 #pragma unroll
                     for (int x = 0; x < 4; ++x) {
@@ -864,6 +885,8 @@ extern "C" mk_status_t mk_paged_attention_fp4(const void* q, int64_t q_stride, c
     p.num_pages = num_pages;
     p.per_kv = Hq / Hkv;
     p.scale2 = scale * LOG2E;
+    p.sixteen = 16;
+    p.byte = 256;
     // page_size = 2^31 / ... : the quotient of any key below 2^31 by multiplication (Granlund
     // and Montgomery 1994): with 2^l >= page_size > 2^(l-1), magic = ceil(2^(31+l) / page_size).
     int l = 0;
