@@ -24,8 +24,8 @@
 // (sequence, group of up to 8, 16 or 24 query heads of one key-value head); each warp
 // has a ring of tiles in shared memory, filled by its own asynchronous copies.
 //
-// Measured on GB300: four sequences of 131071 keys, 8 key-value heads of 128: 108 us,
-// 5.6 TB/s (535 instructions a tile of 32 keys, 2.5 a cycle and SM); 64 sequences of 0
+// Measured on GB300: four sequences of 131071 keys, 8 key-value heads of 128: 106 us,
+// 5.7 TB/s (535 instructions a tile of 32 keys, 2.5 a cycle and SM); 64 sequences of 0
 // to 16384 keys in pages of 24 (128 MB) 42 us, of which 4 until the first copies and 7
 // for the joins; one of 8191 keys 11.8 us.
 #include <cuda_bf16.h>
@@ -225,7 +225,11 @@ __global__ void __launch_bounds__(Geo4<D, NT, UNIT>::THREADS, 1) mk_paged_attent
     count_positions<D, KEYS, G::THREADS>(p, prefix, small);
 
     const uint32_t total = prefix[p.B] * groups;
-    const uint32_t least = uint32_t(G::WARPS);  // a position per warp
+    // A position per warp, or two where partial results are large: a shorter range only
+    // adds some to join (one sequence of 8191 keys, 8 heads a group: 11.7 us with one, 12.1
+    // with two; 16 heads 19.1 and 16.8; 8 of 256 columns 23.2 and 21.1; two of 10000 keys,
+    // 24 heads 28.0 and 30.7).
+    const uint32_t least = uint32_t(G::WARPS * (NT == 2 || (NT == 1 && D == 256) ? 2 : 1));
     const uint32_t nctas = min(gridDim.x, (total + least - 1) / least);
     if (blockIdx.x >= nctas) return;
     const Cut cut_at(total, nctas);

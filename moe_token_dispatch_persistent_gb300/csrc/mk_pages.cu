@@ -318,18 +318,30 @@ __global__ void __launch_bounds__(PLAN_THREADS) mk_extend_plan_kernel(Pool p, co
         need += total;
         moved += moves;
     }
-    // the lowest free pages
+    // the lowest free pages: a lane takes 32 neighbouring ones, which its warp reads together
     int found = 0;
-    constexpr int EACH = 8;
-    for (int p0 = 0; p0 < p.num_pages && found < need; p0 += PLAN_THREADS * EACH) {
-        const int at = p0 + tid * EACH;
+    const int warp = tid >> 5, lane = tid & 31;
+    for (int p0 = 0; p0 < p.num_pages && found < need; p0 += PLAN_THREADS * 32) {
+        const int first_page = p0 + warp * 1024;
         uint32_t free = 0;
 #pragma unroll
-        for (int j = 0; j < EACH; ++j)
-            if (at + j < p.num_pages && p.refs[at + j] == 0) free |= 1u << j;
+        for (int k0 = 0; k0 < 32; k0 += 8) {
+            if (first_page + k0 * 32 >= p.num_pages) break;  // the same for the whole warp
+            int r[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int at = first_page + (k0 + k) * 32 + lane;
+                r[k] = at < p.num_pages ? p.refs[at] : 1;
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const uint32_t word = __ballot_sync(0xffffffffu, r[k] == 0);
+                if (lane == k0 + k) free = word;
+            }
+        }
         int total;
         int to = found + scan(__popc(free), part, &total);
-        for (; free && to < need; free &= free - 1) fresh[to++] = at + __ffs(free) - 1;
+        for (; free && to < need; free &= free - 1) fresh[to++] = first_page + lane * 32 + __ffs(free) - 1;
         found += total;
     }
     if (found < need) {
@@ -351,7 +363,6 @@ __global__ void __launch_bounds__(PLAN_THREADS) mk_extend_plan_kernel(Pool p, co
         last[i] = -2;
     }
     __syncthreads();
-    const int warp = tid >> 5, lane = tid & 31;
     for (int i = warp; i < n; i += PLAN_THREADS / 32) {
         const int s = __ldg(seqs + i), len = p.lens[s], more = __ldg(count + i);
         const int have = p.pages_of(len), want = p.pages_of(len + more), from = first[i] + (last[i] == -2);

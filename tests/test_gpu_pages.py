@@ -197,6 +197,21 @@ def test_many_sharers_and_rows():
     p.check()
 
 
+@pytest.mark.parametrize("pages,free", [(70001, 90), (32768, 1), (8193, 60), (1025, 60), (31, 4)])
+def test_lowest_free_pages_of_full_pools(pages, free):
+    rng = np.random.default_rng(pages)
+    p = Pool(3, 64, pages, 1, caches=[torch.arange(pages * 4, device="cuda", dtype=torch.int32).view(pages, 4)])
+    where = rng.permutation(pages)[:free]
+    p.refs.fill_(1)
+    p.refs[torch.from_numpy(where).cuda()] = 0
+    p.model.refs = p.refs.tolist()
+    a = free // 3
+    p.extend([2, 0], [a, free // 2])
+    p.check()
+    p.extend([1], [min(64, free - a - free // 2)])
+    p.check()
+
+
 def test_refused_lists_change_nothing():
     p = Pool(4, 3, 8, 4)
     p.extend([0, 1], [10, 5])
