@@ -455,7 +455,7 @@ typedef struct mk_qk_norm_rope {
     int64_t page_stride, token_stride, head_stride;
     void *k_scales, *v_scales;        /* MK_CACHE_FP4 only */
     int64_t scale_page_stride, scale_token_stride, scale_head_stride;
-    const float *k_factor, *v_factor; /* [Hkv], or NULL: 1 */
+    const float *k_factor, *v_factor; /* [Hkv], or NULL: 1; normal numbers, y / factor below 2^126 */
     int32_t T, Hq, Hkv, D, rot, axes, pairs, cache, page_size, num_pages;
     float eps;
     int32_t reserved;                 /* zero */

@@ -25,7 +25,7 @@
 // has a ring of tiles in shared memory, filled by its own asynchronous copies.
 //
 // Measured on GB300: four sequences of 131071 keys, 8 key-value heads of 128: 106 us,
-// 5.7 TB/s (535 instructions a tile of 32 keys, 2.5 a cycle and SM); 64 sequences of 0
+// 5.7 TB/s (524 instructions a tile of 32 keys, 2.2 a cycle and SM); 64 sequences of 0
 // to 16384 keys in pages of 24 (128 MB) 42 us, of which 4 until the first copies and 7
 // for the joins; one of 8191 keys 11.8 us.
 #include <cuda_bf16.h>
@@ -491,7 +491,7 @@ __global__ void __launch_bounds__(Geo4<D, NT, UNIT>::THREADS, 1) mk_paged_attent
 
         for (uint32_t t = r.t0; t < r.t1; ++t) {
             const uint8_t *ks = ring_ptr + at, *vs = ks + G::VALUES, *kss = vs + G::VALUES, *vss = kss + G::SCALES;
-            const bool cut = int(t + 1) * KEYS > len;
+            const bool cut = len - int(t) * KEYS < KEYS;  // (the tile's end may be 2^31)
             copy_wait<G::STAGES - 1>();
             __syncwarp();
 
@@ -891,8 +891,8 @@ extern "C" mk_status_t mk_paged_attention_fp4(const void* q, int64_t q_stride, c
     p.scale2 = scale * LOG2E;
     p.sixteen = 16;
     p.byte = 256;
-    // page_size = 2^31 / ... : the quotient of any key below 2^31 by multiplication (Granlund
-    // and Montgomery 1994): with 2^l >= page_size > 2^(l-1), magic = ceil(2^(31+l) / page_size).
+    // key / page_size of any key below 2^31 by multiplication (Granlund and Montgomery 1994):
+    // with 2^l >= page_size > 2^(l-1), magic = ceil(2^(31+l) / page_size).
     int l = 0;
     while ((int64_t(1) << l) < page_size) ++l;
     p.page_shift = (page_size & (page_size - 1)) == 0 ? l : -1;

@@ -75,7 +75,7 @@ struct Range {
     uint32_t tiles;  // tiles of the group
 };
 __host__ __device__ inline uint32_t positions_of(int len, int keys) {
-    return len > 0 ? uint32_t(len + keys - 1) / uint32_t(keys) + EXTRA : 0u;
+    return len > 0 ? (uint32_t(len) + uint32_t(keys) - 1) / uint32_t(keys) + EXTRA : 0u;
 }
 
 // The groups of the positions [pos, end) one after the other.

@@ -71,7 +71,7 @@ __device__ __forceinline__ void move_pages(const Buffers& b, const int32_t* src,
             if (b.first[mid] <= in) lo = mid;
             else hi = mid;
         }
-        const int from = __ldg(src + i), to = __ldg(dst + i);
+        const int from = src[i], to = dst[i];  // (not by the read-only path: the kernel before may have written them)
         if (from < 0 || from >= num_pages || to < 0 || to >= num_pages) {
             if (threadIdx.x == 0) cache_error(err, ERR_FAULT, SITE_PAGE_INDEX, uint32_t(from < 0 || from >= num_pages ? from : to));
             continue;

@@ -302,3 +302,23 @@ def test_more_than_16_heads_and_many_sequences(B, per_kv, D):
     lens[-1], lens[B // 2] = 2000, 0
     c = Case(lens, 2 * per_kv, 2, D, 16, seed=B + per_kv)
     c.check(c.run())
+
+
+@pytest.mark.parametrize("D,page", [(64, 16), (64, 8), (64, 1), (128, 16), (256, 16)])
+def test_longest_sequence(D, page):
+    """2^31 - 32 keys, all of them of one page, with scores of -D: a key behind the last one, whose
+    score would be 0, would outweigh them all.  All weights are the same number near 2^10, so a sum of 2^18 of
+    them in a lane is off by no more than that number's distance from 2^10, 2^-16 of it."""
+    n = 2 ** 31 - 32
+    c = mk.fp4_cache(1, page, 1, D)
+    for x in ("k_cache", "v_cache"):
+        c[x].fill_(0x22)  # ones
+    for x in ("k_scales", "v_scales"):
+        c[x].view(torch.uint8).fill_(0x38)  # of 1
+    q = -torch.ones((1, 1, D), dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros((1, n // page), dtype=torch.int32, device="cuda")
+    lens = torch.tensor([n], dtype=torch.int32, device="cuda")
+    got = mk.paged_attention_fp4(q, **c, block_table=table, seq_lens=lens, scale=1.0)
+    assert (got["out"] == 1).all()
+    want = np.log(float(n)) - D
+    assert abs(got["lse"].item() - want) <= 2.0 ** -15 + 2.0 ** -22 * abs(want)
