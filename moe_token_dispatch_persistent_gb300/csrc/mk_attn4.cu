@@ -24,8 +24,8 @@
 // (sequence, group of up to 8, 16 or 24 query heads of one key-value head); each warp
 // has a ring of tiles in shared memory, filled by its own asynchronous copies.
 //
-// Measured on GB300: four sequences of 131071 keys, 8 key-value heads of 128: 106 us,
-// 5.7 TB/s (524 instructions a tile of 32 keys, 2.2 a cycle and SM); 64 sequences of 0
+// Measured on GB300: four sequences of 131071 keys, 8 key-value heads of 128: 105 us,
+// 5.7 TB/s (524 instructions a tile of 32 keys, 2.3 a cycle and SM); 64 sequences of 0
 // to 16384 keys in pages of 24 (128 MB) 42 us, of which 4 until the first copies and 7
 // for the joins; one of 8191 keys 11.8 us.
 #include <cuda_bf16.h>
