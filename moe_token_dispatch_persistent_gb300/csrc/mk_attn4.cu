@@ -305,34 +305,40 @@ __global__ void __launch_bounds__(Geo4<D, NT, UNIT>::THREADS, 1) mk_paged_attent
         look_up(ahead[1]);
     }
     uint32_t load_at = 0;  // the stage's place in the ring
+    // The next page of the group, from its first key.
+    auto enter_page = [&]() {
+        page_ok = good_page(page_next);
+        const uint32_t page = page_ok ? uint32_t(page_next) : 0u;
+        const uint64_t at = uint64_t(page) * p.page_units * 16 + head_at;
+        k_at = p.k + at;
+        v_at = p.v + at;
+        s_at = scales + (uint64_t(page) * p.scale_units * 16 + head_scales);
+        page_left = p.page_size;
+        if (--pages_more >= 0) page_next = __ldg(++table);
+    };
     auto issue = [&]() {
         if constexpr (UNIT > 0) {
             const bool fresh = load_tile >= lr.t1;  // another group
             if (next_tile()) {
-                int left = load_len - int(load_tile) * KEYS, token = 0;  // keys from here to the end
+                int left = load_len - int(load_tile) * KEYS;  // keys from here to the end
                 if (fresh) {
                     const int key = int(load_tile) * KEYS, kv = lr.g / p.chunks, slot = slot_of(key);
                     table = p.table + int64_t(lr.b) * p.max_pages + slot;
                     page_next = __ldg(table);
-                    token = key - slot * p.page_size;
+                    const uint32_t token = uint32_t(key - slot * p.page_size);
                     pages_more = slot_of(load_len - 1) - slot;
                     head_at = kv * p.head_stride + (lane & (UNIT_LANES - 1)) * 16;
                     head_scales = kv * p.scale_head;
-                    page_left = 0;
+                    enter_page();
+                    // (of a page of 2^31 - 32 keys: offsets in it pass 32 bits)
+                    k_at += uint64_t(token) * ROW;
+                    v_at += uint64_t(token) * ROW;
+                    s_at += uint64_t(token) * SROW;
+                    page_left -= int(token);
                 }
 #pragma unroll
                 for (int u = 0; u < UNITS; ++u) {
-                    if (page_left == 0 && left > 0) {
-                        page_ok = good_page(page_next);
-                        const uint32_t page = page_ok ? uint32_t(page_next) : 0u;
-                        const uint64_t at = uint64_t(page) * p.page_units * 16 + uint32_t(token * ROW) + head_at;
-                        k_at = p.k + at;
-                        v_at = p.v + at;
-                        s_at = scales + (uint64_t(page) * p.scale_units * 16 + uint32_t(token * SROW) + head_scales);
-                        page_left = p.page_size - token;
-                        token = 0;
-                        if (--pages_more >= 0) page_next = __ldg(++table);
-                    }
+                    if (page_left == 0 && left > 0) enter_page();
                     const uint32_t dst = lane_dst + load_at + (UNIT_LANES == 32 ? u * UNIT_BYTES : u / 2 * 512);
                     const bool mine = UNIT_LANES == 32 || lane / UNIT_LANES == u % 2;
                     const uint32_t scale_dst = lane_dst + load_at + 2 * G::VALUES;
