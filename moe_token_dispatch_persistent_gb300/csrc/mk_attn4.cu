@@ -470,8 +470,10 @@ __global__ void __launch_bounds__(Geo4<D, NT, UNIT>::THREADS, 1) mk_paged_attent
             }
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const int e = int(top >> 7);  // biased exponent of the largest; 0 or 255: as it is
-            const int up = e == 0 || e == 255 ? 0 : min(141 - e, 126);
+            // the largest's biased exponent; below 2^-112 they move by 2^126, whose inverse is
+            // still a normal number (subnormals, from 2^-133 on, to 2^-7 and more); 255: as they are
+            const int e = int(top >> 7);
+            const int up = e == 255 ? 0 : min(141 - e, 126);
             const float by = copysignf(__uint_as_float(uint32_t(up + 127) << 23), unit);
             const float back = __uint_as_float(uint32_t(127 - up) << 23);
 #pragma unroll
