@@ -466,8 +466,10 @@ typedef struct mk_qk_norm_rope {
  *   y = x * rsqrt(mean(x^2) + eps) * weight      over a head's D columns,
  *   angle = positions[axis(i),t] * inv_freq[i]    for pair i of the first rot
  *   columns: (a, b) -> (a cos - b sin, b cos + a sin); the others pass.
- * The angle is exact to 2^-25 of a turn for any position and frequencies up to 4.  q_out gets the
- * queries; k_out, if not NULL, the keys; with a cache, the keys and the values
+ * A frequency is held in steps of 2^-64 of a turn, so the angle is exact to 2^-31 of a
+ * turn for any position and frequencies up to 4; sines and cosines are then off by
+ * 2^-21 of themselves, those of small angles and next to their zeros too (frequencies
+ * of 2^-36 or more).  q_out gets the queries; k_out, if not NULL, the keys; with a cache, the keys and the values
  * (as they are) of token t go to slots[t], and with MK_CACHE_FP4 k_out and v_out
  * (both may be NULL) get what the cache holds of them.  Without a cache k_out is
  * needed, and v and v_out are not used.  A token with a negative slot is left

@@ -9,7 +9,8 @@
 // Angles.  pos * inv_freq in 32 bits would be off by whole radians for far
 // positions.  Of the angle only the part below a turn counts, so a frequency is
 // held as the 64-bit fraction of a turn that one position adds, and the angle is
-// its product with the position modulo 2^64: exact, three integer products.
+// its product with the position modulo 2^64: exact, three integer products.  Its
+// distance from the nearest quarter turn is what the functions get.
 //
 // A row of D columns is held by D/8 lanes (rounded up to 4, 8, 16 or 32), eight
 // columns each, four whole pairs; a warp takes one token, or a part of its heads
@@ -185,9 +186,22 @@ __global__ void __launch_bounds__(ROPE_WARPS * 32, ROPE_CTAS) mk_qk_norm_rope_ke
                 const int pair = i * 32 + lane;
                 if (pair < half) {
                     const int64_t pos = __ldg(p.positions + p.axis[pair] * p.position_stride + t);
-                    const int64_t turn = int64_t(uint64_t(pos) * units[pair]);
+                    // the nearest quarter turn and what is left of it, at most an eighth: near a zero
+                    // of either function, small angles among them, it keeps 24 bits of its own
+                    const uint64_t turn = uint64_t(pos) * units[pair];
+                    const uint32_t quarter = uint32_t((turn + (uint64_t(1) << 61)) >> 62);
+                    const int64_t left = int64_t(turn - (uint64_t(quarter) << 62));
                     float sine, cosine;
-                    sincospif(float(int32_t(turn >> 32)) * 4.656612873077393e-10f /* 2^-31 */, &sine, &cosine);
+                    sincospif(float(left) * 1.0842021724855044e-19f /* 2^-63 */, &sine, &cosine);
+                    if (quarter & 1) {
+                        const float c = cosine;
+                        cosine = -sine;
+                        sine = c;
+                    }
+                    if (quarter & 2) {
+                        cosine = -cosine;
+                        sine = -sine;
+                    }
                     table[warp][pair] = make_float2(cosine, sine);
                 }
             }
