@@ -382,7 +382,8 @@ mk_status_t Workspace::get(WsKind kind, int dev, cudaStream_t st, size_t need, s
             w.ptr = nullptr;
             return MK_ERR_CUDA;
         }
-        if (cudaMemsetAsync(w.ptr, 0, kind == WS_DISPATCH ? zero_bytes : grow, st) != cudaSuccess) return MK_ERR_CUDA;
+        const size_t zeroed = kind == WS_DISPATCH || kind == WS_PAGES ? zero_bytes : grow;
+        if (zeroed && cudaMemsetAsync(w.ptr, 0, zeroed, st) != cudaSuccess) return MK_ERR_CUDA;
         w.bytes = grow;
     }
     w.last = ptr_ = static_cast<uint8_t*>(w.ptr);

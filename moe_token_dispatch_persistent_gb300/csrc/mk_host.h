@@ -36,9 +36,9 @@ cudaError_t ffn_kernel_attributes();
 enum WsKind { WS_DISPATCH = 0, WS_EP = 1, WS_ATTN = 2, WS_FFN = 3, WS_ATTN4 = 4, WS_PAGES = 5, WS_KINDS = 6 };
 
 // The library's workspace of a kind for (device, stream), grown on demand on
-// `st`.  Of a new buffer the first `zero_bytes` are zeroed (WS_DISPATCH) or all
-// of it (the others, whose counters move with the sizes).  The object holds the
-// buffer: keep it until the call's work is enqueued, so that no other thread's
+// `st`.  Of a new buffer the first `zero_bytes` are zeroed (WS_DISPATCH, WS_PAGES)
+// or all of it (the others, whose counters move with the sizes).  The object holds
+// the buffer: keep it until the call's work is enqueued, so that no other thread's
 // call frees what this one is about to use.  A call under stream capture gets
 // what an earlier call on the stream left, which is then the captured calls'
 // alone; without that, memory of the graph (WS_DISPATCH, WS_EP) or

@@ -127,31 +127,9 @@ __device__ bool list_is_good(const Pool& p, const int32_t* list, int n, uint32_t
 
 // ---- fork: the children give their pages back and hold their parents'
 
-// First the counts, and the parents' rows as they were into `kept` (a child may
-// be another's parent), then the rows.  Threads [t0, ..), `step` apart, take pair i.
-__device__ __forceinline__ void fork_count(const Pool& p, int from, int to, int32_t* kept, int32_t* kept_len, int t0, int step) {
-    const int len = p.lens[from], old = p.lens[to];
-    const int32_t *theirs = p.table + int64_t(from) * p.max_pages, *before = p.table + int64_t(to) * p.max_pages;
-    const int np = p.pages_of(len), no = p.pages_of(old);
-    for (int j = t0; j < max(np, no); j += step) {
-        if (j < np) {
-            const int page = theirs[j];
-            kept[j] = page;
-            if (p.holds(page)) atomicAdd(p.refs + page, 1);
-            else cache_error(p.err, ERR_FAULT, SITE_PAGE_INDEX, uint32_t(page));
-        }
-        if (j < no) {
-            const int page = before[j];
-            if (p.holds(page)) atomicSub(p.refs + page, 1);
-            else cache_error(p.err, ERR_FAULT, SITE_PAGE_INDEX, uint32_t(page));
-        }
-    }
-    if (t0 == 0) *kept_len = max(len, 0);
-}
-__device__ __forceinline__ void fork_row(const Pool& p, int to, const int32_t* kept, int len, int t0, int step) {
-    const int np = p.pages_of(len);
-    for (int j = t0; j < np; j += step) p.table[int64_t(to) * p.max_pages + j] = kept[j];
-    if (t0 == 0) p.lens[to] = len;
+__device__ __forceinline__ void count_page(const Pool& p, int page, int by) {
+    if (p.holds(page)) atomicAdd(p.refs + page, by);
+    else cache_error(p.err, ERR_FAULT, SITE_PAGE_INDEX, uint32_t(page));
 }
 __device__ bool fork_is_good(const Pool& p, const int32_t* parent, const int32_t* child, int n, uint32_t* seen, int* bad) {
     if (!list_is_good(p, child, n, seen, bad)) return false;
@@ -164,34 +142,109 @@ __device__ bool fork_is_good(const Pool& p, const int32_t* parent, const int32_t
     if (threadIdx.x == 0 && blockIdx.x == 0) cache_error(p.err, ERR_FAULT, SITE_SEQUENCE, uint32_t(*bad));
     return false;
 }
-// A CTA per pair; kept_len[i]: -1 when the call is refused.
+// First the counts, a CTA per pair, and the lengths as they were; lens_before[i]: -1 when
+// the call is refused.
 __global__ void __launch_bounds__(256) mk_fork_count_kernel(Pool p, const int32_t* parent, const int32_t* child, int n,
-                                                            int32_t* kept, int32_t* kept_len) {
+                                                            int32_t* lens_before) {
     __shared__ uint32_t seen[MAX_ROWS / 32];
     __shared__ int bad;
     const int i = blockIdx.x;
-    if (fork_is_good(p, parent, child, n, seen, &bad))
-        fork_count(p, __ldg(parent + i), __ldg(child + i), kept + int64_t(i) * p.max_pages, kept_len + i, threadIdx.x, 256);
-    else if (threadIdx.x == 0)
-        kept_len[i] = -1;
+    if (!fork_is_good(p, parent, child, n, seen, &bad)) {
+        if (threadIdx.x == 0) lens_before[i] = -1;
+        return;
+    }
+    const int from = __ldg(parent + i), to = __ldg(child + i), len = p.lens[from];
+    const int32_t *theirs = p.table + int64_t(from) * p.max_pages, *own = p.table + int64_t(to) * p.max_pages;
+    const int np = p.pages_of(len), no = p.pages_of(p.lens[to]);
+    for (int j = threadIdx.x; j < max(np, no); j += 256) {
+        if (j < np) count_page(p, theirs[j], 1);
+        if (j < no) count_page(p, own[j], -1);
+    }
+    if (threadIdx.x == 0) lens_before[i] = max(len, 0);
 }
-__global__ void __launch_bounds__(256) mk_fork_rows_kernel(Pool p, const int32_t* child, const int32_t* kept, const int32_t* kept_len) {
+// Then the rows.  A child may be another's parent, so a CTA takes all pairs' entries of
+// some columns into registers before it writes any of them: rows of any length need no
+// memory beside the table (224 pairs of 125 pages 7.0 us; with the parents' rows copied
+// aside by the counting launch 6.0, but 64 of 8192 pages 21.7 for 20.4).  LIST: pairs at
+// most.  COLS: a sector of a row, or half of one where a CTA has many pairs.
+template <int LIST, int THREADS, int COLS>
+__global__ void __launch_bounds__(THREADS) mk_fork_rows_kernel(Pool p, const int32_t* parent, const int32_t* child, int n,
+                                                               const int32_t* lens_before) {
+    constexpr int DEEP = LIST * COLS / THREADS, AT_ONCE = THREADS / COLS;
+    static_assert(MAX_ROWS <= 65536, "two rows in a word");
+    __shared__ uint32_t pairs[LIST];
+    __shared__ int held[LIST];
+    __shared__ int most;
+    const int tid = threadIdx.x;
+    for (int i = tid; i < n; i += THREADS) pairs[i] = uint32_t(__ldg(parent + i)) << 16 | (uint32_t(__ldg(child + i)) & 0xffffu);
+    if (tid == 0) most = 0;
     wait_for_previous();
-    const int i = blockIdx.x, len = kept_len[i];
-    if (len >= 0) fork_row(p, __ldg(child + i), kept + int64_t(i) * p.max_pages, len, threadIdx.x, 256);
+    __syncthreads();
+    int longest = 0;
+    for (int i = tid; i < n; i += THREADS) {
+        const int len = lens_before[i];
+        held[i] = p.pages_of(len);
+        longest = max(longest, held[i]);  // stays 0 when the call is refused
+        if (blockIdx.x == 0 && len >= 0) p.lens[pairs[i] & 0xffffu] = len;
+    }
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (tid % 32 == 0 && longest > 0) atomicMax(&most, longest);
+    __syncthreads();
+    for (uint32_t c0 = blockIdx.x * COLS; c0 < uint32_t(most); c0 += gridDim.x * COLS) {
+        const uint32_t col = c0 + tid % COLS;
+        int v[DEEP];
+#pragma unroll
+        for (int k = 0; k < DEEP; ++k) {
+            const int i = k * AT_ONCE + tid / COLS;
+            if (i < n && col < uint32_t(held[i])) v[k] = p.table[int64_t(pairs[i] >> 16) * p.max_pages + col];
+        }
+        __syncthreads();
+#pragma unroll
+        for (int k = 0; k < DEEP; ++k) {
+            const int i = k * AT_ONCE + tid / COLS;
+            if (i < n && col < uint32_t(held[i])) p.table[int64_t(pairs[i] & 0xffffu) * p.max_pages + col] = v[k];
+        }
+    }
 }
-// All of it by one CTA, a warp per pair: for a few sequences one launch less on the host
-// (a fork and an extension of one pair 30 us there, 36 with the two above; 12 on the GPU).
+// All of it by one CTA, a warp per pair and 128 columns at a time: for a few sequences one
+// launch less on the host (32 pairs of 125 pages 5.4 us, 33 of them by the two above 6.1;
+// long rows want more CTAs, 32 of 4096 pages 69, 64 of 8192 20).
 constexpr int FORK_FEW = PLAN_THREADS / 32;
-__global__ void __launch_bounds__(PLAN_THREADS) mk_fork_few_kernel(Pool p, const int32_t* parent, const int32_t* child, int n,
-                                                                   int32_t* kept, int32_t* kept_len) {
+__global__ void __launch_bounds__(PLAN_THREADS) mk_fork_few_kernel(Pool p, const int32_t* parent, const int32_t* child, int n) {
     __shared__ uint32_t seen[MAX_ROWS / 32];
-    __shared__ int bad;
+    __shared__ int bad, most;
+    if (threadIdx.x == 0) most = 0;
     if (!fork_is_good(p, parent, child, n, seen, &bad)) return;
     const int i = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    if (i < n) fork_count(p, __ldg(parent + i), __ldg(child + i), kept + int64_t(i) * p.max_pages, kept_len + i, lane, 32);
-    __syncthreads();
-    if (i < n) fork_row(p, __ldg(child + i), kept + int64_t(i) * p.max_pages, kept_len[i], lane, 32);
+    int from = 0, to = 0, len = 0, np = 0, no = 0;
+    if (i < n) {
+        from = __ldg(parent + i);
+        to = __ldg(child + i);
+        len = max(p.lens[from], 0);
+        np = p.pages_of(len);
+        no = p.pages_of(p.lens[to]);
+        if (lane == 0) atomicMax(&most, max(np, no));
+    }
+    __syncthreads();  // every length has been read
+    if (i < n && lane == 0) p.lens[to] = len;
+    const int32_t* theirs = p.table + int64_t(from) * p.max_pages;
+    int32_t* own = p.table + int64_t(to) * p.max_pages;
+    constexpr int DEEP = 4;
+    for (int64_t c0 = 0; c0 < most; c0 += 32 * DEEP) {
+        int v[DEEP];
+#pragma unroll
+        for (int k = 0; k < DEEP; ++k) {
+            const int64_t j = c0 + k * 32 + lane;
+            if (j < np) count_page(p, v[k] = theirs[j], 1);
+            if (j < no) count_page(p, own[j], -1);
+        }
+        __syncthreads();  // every pair's entries of these columns have been read
+#pragma unroll
+        for (int k = 0; k < DEEP; ++k) {
+            const int64_t j = c0 + k * 32 + lane;
+            if (j < np) own[j] = v[k];
+        }
+    }
 }
 
 // ---- free
@@ -548,7 +601,7 @@ mk_status_t workspace_of(Workspace& cached, int dev, cudaStream_t st, void* work
         *out = static_cast<uint8_t*>(workspace);
         return MK_OK;
     }
-    const mk_status_t s = cached.get(WS_PAGES, dev, st, need, need);
+    const mk_status_t s = cached.get(WS_PAGES, dev, st, need, 0);
     *out = cached.data();
     return s;
 }
@@ -571,7 +624,7 @@ mk_status_t launched() { return cudaGetLastError() == cudaSuccess ? MK_OK : MK_E
 
 constexpr size_t HEAD_BYTES = 256;
 
-size_t fork_bytes(int max_pages, int n) { return ws_align(size_t(n) * 4) + ws_align(size_t(n) * size_t(max_pages) * 4); }
+size_t fork_bytes(int n) { return ws_align(size_t(n) * 4); }
 size_t extend_bytes(int num_pages, int n) { return HEAD_BYTES + 2 * ws_align(size_t(n) * 4) + ws_align(size_t(num_pages) * 4); }
 size_t compact_bytes(int num_pages) { return HEAD_BYTES + ws_align(1024 * 4) + 3 * ws_align(size_t(num_pages) * 4); }
 
@@ -582,7 +635,7 @@ using namespace mk;
 
 extern "C" size_t mk_pages_workspace_size(int max_pages, int num_pages, int n) {
     if (max_pages < 0 || num_pages < 0 || n < 0 || n > MAX_LIST) return 0;
-    return std::max({fork_bytes(max_pages, n), extend_bytes(num_pages, n), compact_bytes(num_pages)});
+    return std::max({fork_bytes(n), extend_bytes(num_pages, n), compact_bytes(num_pages)});
 }
 
 extern "C" mk_status_t mk_copy_pages(void* const* caches, const int64_t* page_strides, const int64_t* page_bytes, int n_caches,
@@ -615,17 +668,23 @@ extern "C" mk_status_t mk_fork_sequences(int32_t* block_table, int32_t* seq_lens
     if ((s = host_device(&dev, &sms, &err)) != MK_OK) return s;
     if (n == 0) return MK_OK;
     const cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const Pool p{block_table, seq_lens, refs, err, rows, max_pages, num_pages, page_size};
     Workspace cached;
     uint8_t* ws = nullptr;
-    if ((s = workspace_of(cached, dev, st, workspace, ws_bytes, fork_bytes(max_pages, n), &ws)) != MK_OK) return s;
-    int32_t* kept_len = reinterpret_cast<int32_t*>(ws);
-    int32_t* kept = reinterpret_cast<int32_t*>(ws + ws_align(size_t(n) * 4));
-    const Pool p{block_table, seq_lens, refs, err, rows, max_pages, num_pages, page_size};
+    if (workspace || n > FORK_FEW)
+        if ((s = workspace_of(cached, dev, st, workspace, ws_bytes, fork_bytes(n), &ws)) != MK_OK) return s;
     if (n <= FORK_FEW) {
-        mk_fork_few_kernel<<<1, PLAN_THREADS, 0, st>>>(p, parent, child, n, kept, kept_len);
+        mk_fork_few_kernel<<<1, PLAN_THREADS, 0, st>>>(p, parent, child, n);
     } else {
-        mk_fork_count_kernel<<<n, 256, 0, st>>>(p, parent, child, n, kept, kept_len);
-        launch_behind(mk_fork_rows_kernel, n, 256, st, p, child, kept, kept_len);
+        int32_t* lens_before = reinterpret_cast<int32_t*>(ws);
+        mk_fork_count_kernel<<<n, 256, 0, st>>>(p, parent, child, n, lens_before);
+        const auto rows_of = [&](auto kernel, int threads, int cols, int each) {  // `each` CTAs of an SM
+            const int grid = std::max(1, std::min(sms * each, (max_pages - 1) / cols + 1));
+            launch_behind(kernel, grid, threads, st, p, parent, child, n, lens_before);
+        };
+        if (n <= 256) rows_of(mk_fork_rows_kernel<256, 256, 8>, 256, 8, 8);
+        else if (n <= 1024) rows_of(mk_fork_rows_kernel<1024, 256, 8>, 256, 8, 4);
+        else rows_of(mk_fork_rows_kernel<MAX_LIST, PLAN_THREADS, 4>, PLAN_THREADS, 4, 1);
     }
     return launched();
 }
