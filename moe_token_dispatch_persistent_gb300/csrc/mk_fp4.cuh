@@ -22,8 +22,9 @@ constexpr int FP4_GROUP = 16;  // columns per scale
 enum CacheSite : int {
     SITE_SLOT_RANGE = 23,    // a slot outside the pool; info: the token
     SITE_SEQUENCE = 24,      // a sequence outside the table, or named twice; info: its place in the list
-    SITE_POOL_FULL = 25,     // too few free pages, or too few entries in a row of the table; info: those missing
+    SITE_POOL_FULL = 25,     // too few free pages, or too few entries in a row of the table; info: those missing, 2^31 - 1 at most
     SITE_PAGE_INDEX = 26,    // a page outside the pool; info: the page
+    SITE_TOKEN_COUNT = 27,   // a count of new tokens outside [0, most], or a length below 0; info: its place in the list
 };
 
 __device__ __forceinline__ void cache_error(DevError* e, uint32_t code, uint32_t site, uint32_t info) {

@@ -300,6 +300,18 @@ struct Extension {
     int32_t ok, moves;
 };
 
+// Reports what entry i of an extension's list is refused for.
+__device__ void extend_error(const Pool& p, const int32_t* seqs, const int32_t* count, int most, int i) {
+    const int s = __ldg(seqs + i), more = __ldg(count + i), len = p.lens[s];
+    if (more < 0 || more > most || len < 0) {
+        cache_error(p.err, ERR_FAULT, SITE_TOKEN_COUNT, uint32_t(i));
+        return;
+    }
+    const int64_t pages = (int64_t(len) + more + p.page_size - 1) / p.page_size;
+    if (pages > p.max_pages) cache_error(p.err, ERR_FAULT, SITE_POOL_FULL, uint32_t(pages - p.max_pages));
+    else cache_error(p.err, ERR_FAULT, SITE_PAGE_INDEX, uint32_t(p.table[int64_t(s) * p.max_pages + len / p.page_size]));
+}
+
 // Decides everything, by one CTA: which shared pages are copied (src, dst), which
 // pages each sequence gets, their lengths.  `fresh` has room for num_pages.
 __global__ void __launch_bounds__(PLAN_THREADS) mk_extend_plan_kernel(Pool p, const int32_t* seqs, const int32_t* count, int n, int most,
@@ -332,30 +344,40 @@ __global__ void __launch_bounds__(PLAN_THREADS) mk_extend_plan_kernel(Pool p, co
                 atomicAdd(&wanted, static_cast<unsigned long long>(p.pages_of(len + more) - p.pages_of(len)));
         }
         __syncthreads();
-        good = bad == INT_MAX && wanted <= static_cast<unsigned long long>(p.num_pages);
-        if (!good && tid == 0) cache_error(p.err, ERR_FAULT, SITE_POOL_FULL, uint32_t(bad));
+        good = bad == INT_MAX;
+        if (!good && tid == 0) extend_error(p, seqs, count, most, bad);
+    }
+    // Whether a sequence copies the page that it is in the middle of: if others hold it
+    // still when those before it in the list have left it (the last of them keeps it).
+    const auto copies_page = [&](int i) {
+        const int page = last[i];
+        if (page < 0) return false;
+        const int holders = p.refs[page];
+        if (holders <= 1) return false;
+        int before = 0;
+        for (int j = 0; j < i; ++j) before += last[j] == page;
+        return holders - before > 1;
+    };
+    if (good && wanted > static_cast<unsigned long long>(p.num_pages)) {
+        good = false;
+        for (int i = tid; i < n; i += PLAN_THREADS)
+            if (copies_page(i)) atomicAdd(&wanted, 1ull);
+        int mine = 0, free;
+        for (int at = tid; at < p.num_pages; at += PLAN_THREADS) mine += p.refs[at] == 0;
+        scan(mine, part, &free);
+        if (tid == 0) cache_error(p.err, ERR_FAULT, SITE_POOL_FULL, uint32_t(min(wanted - free, static_cast<unsigned long long>(INT_MAX))));
     }
     if (!good) {
         if (tid == 0) *head = Extension{0, 0};
         return;
     }
-    // A sequence copies the page that it is in the middle of if others hold it still
-    // when those before it in the list have left it: the last of them keeps it.
     int need = 0, moved = 0;
     for (int i0 = 0; i0 < n; i0 += PLAN_THREADS) {
         const int i = i0 + tid;
         int mine = 0;
         bool copies = false;
         if (i < n) {
-            const int page = last[i];
-            if (page >= 0) {
-                const int holders = p.refs[page];
-                if (holders > 1) {
-                    int before = 0;
-                    for (int j = 0; j < i; ++j) before += last[j] == page;
-                    copies = holders - before > 1;
-                }
-            }
+            copies = copies_page(i);
             const int s = __ldg(seqs + i), len = p.lens[s];
             mine = p.pages_of(len + __ldg(count + i)) - p.pages_of(len) + copies;
         }
