@@ -572,7 +572,9 @@ mk_status_t mk_compact_pages(const int32_t* block_table, const int32_t* seq_lens
                              void* const* caches, const int64_t* page_strides, const int64_t* page_bytes, int n_caches,
                              void* stream, void* workspace, size_t ws_bytes);
 
-/* Workspace bytes that each of these four needs at most (0 for invalid sizes). */
+/* Workspace bytes that mk_fork_sequences, mk_extend_sequences and (with n = 0)
+ * mk_compact_pages need at most, whatever max_pages is; the other two take none.
+ * 0 for invalid sizes. */
 size_t mk_pages_workspace_size(int max_pages, int num_pages, int n);
 
 /* Synchronise `stream`, then return and clear the device error word
