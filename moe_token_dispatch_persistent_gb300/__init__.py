@@ -1049,7 +1049,8 @@ _i64_arrays = {}  # C array types by length
 def _page_buffers(caches, dev, pages=None):
     """The three C arrays of tensors whose first dimension is the page and whose
     pages are dense, in whatever order of the other dimensions: their addresses,
-    their length, what holds them, and the number of pages."""
+    their length, what holds them and the tensors, and the number of pages."""
+    caches = tuple(caches)  # (once: it may be a generator)
     base, strides, sizes = [], [], []
     shape = stride = dtype = None
     for t in caches:
@@ -1082,7 +1083,7 @@ def _page_buffers(caches, dev, pages=None):
         kind = _i64_arrays[n] = ctypes.c_int64 * (3 * n)
     arrays = kind(*base, *strides, *sizes)
     at = ctypes.addressof(arrays)
-    return at, at + 8 * n, at + 16 * n, n, arrays, pages
+    return at, at + 8 * n, at + 16 * n, n, (arrays, *caches), pages
 
 
 def _i32_list(t, dev, n, what):
@@ -1119,12 +1120,12 @@ def copy_pages(caches, src, dst, stream=None, check=True):
     _on_device(dev)
     n = _i32_list(src, dev, None, "src")
     _i32_list(dst, dev, n, "dst")
-    base, strides, sizes, number, _held, pages = _page_buffers(caches, dev)
+    base, strides, sizes, number, held, pages = _page_buffers(caches, dev)
     other = None if stream is None else _other_stream(stream, dev)
     status = lib().mk_copy_pages(base, strides, sizes, number, pages or 0, src.data_ptr(), dst.data_ptr(), n,
                                  _raw_stream(dev) if stream is None else _stream(stream))
     if status or check or other is not None:
-        _finish(status, "mk_copy_pages", stream, other, check, (src, dst, *caches), ())
+        _finish(status, "mk_copy_pages", stream, other, check, (src, dst, *held), ())
 
 
 def fork_sequences(block_table, seq_lens, refs, parent, child, page_size, stream=None, workspace=None, ws_bytes=0, check=True):
@@ -1160,7 +1161,7 @@ def extend_sequences(block_table, seq_lens, refs, seqs, count, most, caches, pag
     dev, pool = _pool(block_table, seq_lens, refs, page_size)
     n = _i32_list(seqs, dev, None, "seqs")
     _i32_list(count, dev, n, "count")
-    base, strides, sizes, number, _held, _ = _page_buffers(caches, dev, refs.shape[0])
+    base, strides, sizes, number, held, _ = _page_buffers(caches, dev, refs.shape[0])
     other = None if stream is None else _other_stream(stream, dev)
     slots = (_empty if other is None else _empty_on(other))((n, most), (most, 1), _torch.int64, dev)
     status = lib().mk_extend_sequences(*pool, seqs.data_ptr(), count.data_ptr(), n, most, slots.data_ptr(), base, strides,
@@ -1168,7 +1169,7 @@ def extend_sequences(block_table, seq_lens, refs, seqs, count, most, caches, pag
                                        ws_bytes)
     if status or check or other is not None:
         _finish(status, "mk_extend_sequences", stream, other, check,
-                (block_table, seq_lens, refs, seqs, count, workspace, *caches), (slots,))
+                (block_table, seq_lens, refs, seqs, count, workspace, *held), (slots,))
     return slots
 
 
@@ -1178,7 +1179,7 @@ def compact_pages(block_table, seq_lens, refs, caches, page_size, table_out=None
     ``block_table`` and ``refs`` as they are then, in ``table_out`` and
     ``refs_out`` when given (which may be block_table and refs themselves)."""
     dev, pool = _pool(block_table, seq_lens, refs, page_size)
-    base, strides, sizes, number, _held, _ = _page_buffers(caches, dev, refs.shape[0])
+    base, strides, sizes, number, held, _ = _page_buffers(caches, dev, refs.shape[0])
     other = None if stream is None else _other_stream(stream, dev)
     empty = _empty if other is None else _empty_on(other)
     made = []
@@ -1195,5 +1196,5 @@ def compact_pages(block_table, seq_lens, refs, caches, page_size, table_out=None
                                     _raw_stream(dev) if stream is None else _stream(stream), _ptr(workspace), ws_bytes)
     if status or check or other is not None:
         _finish(status, "mk_compact_pages", stream, other, check,
-                (block_table, seq_lens, refs, table_out, refs_out, workspace, *caches), made)
+                (block_table, seq_lens, refs, table_out, refs_out, workspace, *held), made)
     return {"block_table": table_out, "refs": refs_out}
