@@ -1050,6 +1050,8 @@ def _page_buffers(caches, dev, pages=None):
     """The three C arrays of tensors whose first dimension is the page and whose
     pages are dense, in whatever order of the other dimensions: their addresses,
     their length, what holds them and the tensors, and the number of pages."""
+    if isinstance(caches, _torch.Tensor):
+        raise ValueError("caches are a list of tensors: one tensor's pages would be taken for caches")
     caches = tuple(caches)  # (once: it may be a generator)
     base, strides, sizes = [], [], []
     shape = stride = dtype = None
