@@ -48,6 +48,7 @@ namespace mk {
 namespace {
 
 constexpr int ROWS = 16;          // query heads per warp (rows of the product)
+
 // D columns a head, groups of R * 16 query heads.
 template <int D, int R>
 struct Geo {
@@ -80,11 +81,9 @@ struct Geo {
     static constexpr int SM_SCORES = SM_SMALL + 128;  // partial scores of warps that share a range, twice
     static constexpr int SMEM = SM_SCORES + (SPLIT > 1 ? 2 * WARPS * (KEYS / 8) * 512 : 0);
     static_assert(RANGES * PART * 4 <= SM_HEADS, "the last results lie where the rings were");
-    static constexpr int SLOT = 2 * GROUP + GROUP * D;  // floats of a partial result: m, l, O
+    static_assert(2 * GROUP + GROUP * D <= ATTN_SLOT_FLOATS, "a partial result (m, l, O) fits its slot");
     static_assert(SMEM + 2 * RANGES * 28 + 16 <= 232448, "shared memory of one CTA on sm_103");
 };
-
-static_assert(std::max(Geo<256, 1>::SLOT, Geo<128, 2>::SLOT) <= ATTN_SLOT_FLOATS, "a partial result fits its slot");
 
 struct AttnParams {
     const __nv_bfloat16* q;
