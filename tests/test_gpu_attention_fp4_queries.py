@@ -54,3 +54,14 @@ def test_largest_column_at_the_lower_end(exponent):
     c.q = q
     scale = 2.0 ** (-exponent - 1)
     c.check(c.run(scale=scale), scale)
+
+
+def test_a_key_whose_scale_is_nan():
+    c = Case([40, 40], 8, 2, 64, 16, seed=9)
+    good = c.run()
+    c.cache["k_scales"].view(torch.uint8)[int(c.table[0, 1]), 3, 1, 2] = 0x7f
+    o = c.run()
+    for n in ("out", "lse"):
+        assert torch.all(torch.isnan(o[n][0, 4:]))
+        o[n][0, 4:] = good[n][0, 4:]
+        assert torch.equal(o[n], good[n])
