@@ -487,7 +487,8 @@ mk_status_t mk_qk_norm_rope(const mk_qk_norm_rope_t* args, void* stream);
  *   k(j,c,:) = value * scale * k_factor[c],   v likewise with v_factor,
  * products and sums in fp32, except that the weights e^(s_j - m) enter the
  * product with v with 11 significant bits (those below 2^-24 of the largest
- * with fewer; below 2^-34 they count as 0 there).  Element (page, token, head)
+ * with fewer; below 2^-34 they count as 0 there), and q with its 8 relative to its head's
+ * largest column (those below 2^-28 of that with fewer, to 2^-39 of it).  Element (page, token, head)
  * of a cache's values begins at byte page*page_stride + token*token_stride +
  * head*head_stride, D/2 bytes in a row; of its scales at page*scale_page_stride
  * + ..., D/16 bytes.  k and v share strides.  A cache whose rows of one head lie
@@ -498,8 +499,9 @@ mk_status_t mk_qk_norm_rope(const mk_qk_norm_rope_t* args, void* stream);
  * Limits as above, but: q 16-byte aligned and q_stride a multiple of 8; values
  * 16-byte aligned with strides of multiples of 16 bytes; scales D/16-byte
  * aligned with strides of multiples of D/16; fewer than 2^31 tiles of 16 keys
- * and 8 query heads in all.  A scale that is NaN makes its columns NaN, an infinite or
- * NaN query its head's out and lse.  Errors and lengths as above.
+ * and 8 query heads in all; scale * k_factor[c] below 2^127.  A value's scale that is NaN
+ * makes its columns of out NaN, a key's scale and an infinite or NaN query their heads'
+ * out and lse.  Errors and lengths as above.
  * workspace: NULL (library cache) or mk_paged_attention_fp4_workspace_size()
  * bytes, 256-byte aligned, zero-filled before its first use and used by this
  * entry point only; one stream at a time. */

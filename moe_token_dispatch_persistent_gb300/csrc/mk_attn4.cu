@@ -18,16 +18,17 @@
 // significant bits and is exact in fp16; the queries keep their 8 there, moved by
 // a power of two per head; the weights e^(s - m) are rounded to fp16, 11 bits, an
 // eighth of the output's own rounding, and moved by 2^10 so that those above
-// 2^-24 of the largest keep all of them.
+// 2^-24 of the largest keep all of them (two parts of 11 bits, as exact as fp32,
+// cost 16 products and 24 more instructions a tile: 104 us became 117).
 //
 // Work is cut and joined as in mk_attn_split.cuh.  A tile is KEYS keys of one
 // (sequence, group of up to 8, 16 or 24 query heads of one key-value head); each warp
 // has a ring of tiles in shared memory, filled by its own asynchronous copies.
 //
-// Measured on GB300: four sequences of 131071 keys, 8 key-value heads of 128: 105 us,
-// 5.7 TB/s (524 instructions a tile of 32 keys, 2.3 a cycle and SM); 64 sequences of 0
-// to 16384 keys in pages of 24 (128 MB) 42 us, of which 4 until the first copies and 7
-// for the joins; one of 8191 keys 11.8 us.
+// Measured on GB300: four sequences of 131071 keys, 8 key-value heads of 128: 104 us,
+// 5.8 TB/s (524 instructions a tile of 32 keys, 2.3 a cycle and SM); 64 sequences of 0
+// to 16384 keys in pages of 24 (128 MB) 40 us, of which 4 until the first copies and 7
+// for the joins; one of 8191 keys 12.0 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -16,9 +16,9 @@
 // columns each, four whole pairs; a warp takes one token, or a part of its heads
 // when there are few tokens, so that a token's sines are computed once.  Traffic
 // bounds it, 4 bytes an element for 7 to 10 operations, but not by far: 16384
-// tokens of 32 + 2 * 8 heads of 128 into bf16 pages take 72 us (5.6 TB/s, 95
+// tokens of 32 + 2 * 8 heads of 128 into bf16 pages take 70 us (5.8 TB/s, 96
 // instructions for two rows; with partner columns in other lanes 184, 126 us),
-// 8192 of them into 4-bit pages 52 us; one token 3.3 us.
+// 8192 of them into 4-bit pages 51 us; one token 3.5 us.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
@@ -38,7 +38,7 @@ constexpr int ROPE_PAIRS = ROPE_MAX_D / 2;
 constexpr int ROPE_AXES = 4;
 constexpr int ROPE_WARPS = 8;
 constexpr int ROPE_AHEAD = 4;  // rows in flight per lane
-constexpr int ROPE_CTAS = 4;   // of an SM: 64 registers a thread
+constexpr int ROPE_CTAS = 4;   // of an SM: 64 registers a thread (some forms spill for it, up to 44 words)
 
 struct RopeParams {
     const __nv_bfloat16 *q, *k, *v;
